@@ -16,17 +16,18 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe2bit.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_DEVICE = 0, 1, 2, 3
-DT_F32, DT_BF16 = 0, 1
+DT_F32, DT_BF16, DT_E4M3_BLOCK, DT_E4M3_ROW = 0, 1, 2, 3
 FMT_IQ2X, FMT_Q2K, FMT_Q4K = 1, 2, 3
 PATH_AUTO, PATH_GENERIC, PATH_GEMV, PATH_GEMM = 0, 1, 2, 3
 PRECISION_EXACT, PRECISION_FAST = 0, 1
-ABI_VERSION = 3
+ABI_VERSION = 4
+NORM_MAX_HIDDEN = 32768
 
 EXPORTS = [
     "moe_abi_version", "moe_sync_debug", "moe_last_error", "moe_weight_bytes", "moe_prepare_weights",
     "moe_dequantize", "moe_route_workspace", "moe_route", "moe_expert_ffn_workspace", "moe_expert_ffn",
     "moe_expert_gate_up", "moe_expert_down", "moe_combine", "moe_combine_steer", "moe_probe_stream_read",
-    "moe_expert_ffn_noalloc", "moe_layer_workspace", "moe_layer",
+    "moe_expert_ffn_noalloc", "moe_layer_workspace", "moe_layer", "moe_add_rms_norm", "moe_combine_norm",
 ]
 
 
@@ -91,6 +92,11 @@ def _load():
     L.moe_layer.restype = ctypes.c_int
     L.moe_layer.argtypes = [ctypes.POINTER(LayerDesc), vp, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                             ctypes.c_float, vp, vp, sz, vp]
+    L.moe_add_rms_norm.restype = ctypes.c_int
+    L.moe_add_rms_norm.argtypes = [vp, i32, i32, i32, vp, vp, i32, vp, i32, ctypes.c_float, vp, i32, vp, vp]
+    L.moe_combine_norm.restype = ctypes.c_int
+    L.moe_combine_norm.argtypes = [vp, vp, vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, i32, vp, i32,
+                                   ctypes.c_float, vp, i32, vp, vp]
     L.moe_probe_stream_read.restype = ctypes.c_int
     L.moe_probe_stream_read.argtypes = [vp, sz, vp, i32, vp]
     if L.moe_abi_version() != ABI_VERSION:
@@ -312,6 +318,91 @@ def moe_layer(desc: LayerDesc, x, w_router, topk_idx, topk_w, expert_offsets, pe
                          _i32(topk_idx), _f32(topk_w), _f32(logits), _i32(expert_offsets), _i32(perm), _i32(active),
                          _f32(slot_out), _f32(shared_out), _f32(steer_v), float(steer_f), _f32(y), _ptr(ws),
                          ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def _addr(t, dev):
+    """Address of a contiguous tensor on GPU `dev` (None passes), as an int."""
+    if t is None:
+        return None
+    if dev < 0 or t.get_device() != dev:
+        if not t.is_cuda:
+            raise TypeError("expected a GPU tensor (the library takes device pointers)")
+        raise ValueError(f"tensors on devices {dev} and {t.get_device()}")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _stream_on(stream, dev):
+    """The given stream, or torch's current one on GPU `dev`, which has to be the current device (the library
+    launches there)."""
+    import torch
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on device {dev}, the current device is {torch.cuda.current_device()}")
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+
+
+def _norm_output(T, H, residual, residual_out, weight, y, y_scale):
+    """Shape and type checks of what the norm calls share; (res_dt, y_dt)."""
+    import torch
+    n = T * H
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual_out must be given iff residual is")
+    res_dt = DT_F32
+    if residual is not None:
+        res_dt = _dt(residual)
+        if residual_out.dtype != residual.dtype:
+            raise TypeError(f"residual_out: expected {residual.dtype}, got {residual_out.dtype}")
+        _need(residual, n, "residual")
+        _need(residual_out, n, "residual_out")
+    _need(weight, H, "weight")
+    _need(y, n, "y")
+    if y.dtype != torch.float8_e4m3fn:
+        if y_scale is not None:
+            raise ValueError("y_scale is given iff y is float8_e4m3fn")
+        return res_dt, _dt(y)
+    if y_scale is None:
+        raise ValueError("y_scale is given iff y is float8_e4m3fn")
+    if y_scale.dtype == torch.float32:
+        _need(y_scale, T, "y_scale")
+        return res_dt, DT_E4M3_ROW
+    if y_scale.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+        raise TypeError(f"y_scale: expected float32 (row scales), float8_e8m0fnu or uint8 (block scales), got "
+                        f"{y_scale.dtype}")
+    _need(y_scale, T * ((H + 31) // 32), "y_scale")
+    return res_dt, DT_E4M3_BLOCK
+
+
+def moe_add_rms_norm(x, residual, residual_out, weight, eps, y, y_scale=None, stream=None):
+    """residual_out = x + residual; y = rms_norm(residual_out) * weight.  y float32, bfloat16, or float8_e4m3fn with
+    y_scale float8_e8m0fnu / uint8 [T][ceil(H/32)] (block scales) or float32 [T] (row scales); residual and
+    residual_out may be None together, or the same tensor."""
+    T, H = _rows(x)
+    res_dt, y_dt = _norm_output(T, H, residual, residual_out, weight, y, y_scale)
+    x_dt, w_dt, dev = _dt(x), _dt(weight), x.get_device()
+    _check(lib.moe_add_rms_norm(_addr(x, dev), x_dt, T, H, _addr(residual, dev), _addr(residual_out, dev), res_dt,
+                                _addr(weight, dev), w_dt, eps, _addr(y, dev), y_dt, _addr(y_scale, dev),
+                                _stream_on(stream, dev)))
+
+
+def moe_combine_norm(slot_out, topk_w, shared_out, residual, residual_out, weight, eps, y, y_scale=None, steer_v=None,
+                     steer_f=0.0, stream=None):
+    """moe_add_rms_norm of the combine's result (steered when steer_v is given): slot_out [T*k][H], topk_w [T][k]."""
+    if slot_out.dim() != 2 or topk_w.dim() != 2 or slot_out.shape[0] != topk_w.numel():
+        raise ValueError(f"slot_out must be [T*k][H] and topk_w [T][k], got {tuple(slot_out.shape)} and "
+                         f"{tuple(topk_w.shape)}")
+    (T, k), H = topk_w.shape, slot_out.shape[1]
+    _need(shared_out, T * H, "shared_out")
+    _need(steer_v, H, "steer_v")
+    for t in (slot_out, topk_w, shared_out, steer_v):
+        if t is not None and _dt(t) != DT_F32:
+            raise TypeError(f"expected torch.float32, got {t.dtype}")
+    res_dt, y_dt = _norm_output(T, H, residual, residual_out, weight, y, y_scale)
+    w_dt, dev = _dt(weight), slot_out.get_device()
+    _check(lib.moe_combine_norm(_addr(slot_out, dev), _addr(topk_w, dev), _addr(shared_out, dev), T, k, H,
+                                _addr(steer_v, dev), float(steer_f), _addr(residual, dev), _addr(residual_out, dev),
+                                res_dt, _addr(weight, dev), w_dt, eps, _addr(y, dev), y_dt, _addr(y_scale, dev),
+                                _stream_on(stream, dev)))
 
 
 def moe_probe_stream_read(buf, nbytes, sink, n_blocks, stream=None):

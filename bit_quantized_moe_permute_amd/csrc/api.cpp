@@ -464,6 +464,109 @@ moe_status moe_layer(const moe_layer_desc *L, const void *x, int32_t x_dt, int32
     return from_hip(moe::launch_combine(slot_out, topk_w, shared_out, T, k, H, y, hs), fn, hs);
 }
 
+// ---------------------------------------------------------------------------
+// residual addition + RMS norm
+// ---------------------------------------------------------------------------
+static bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
+    const char *a = static_cast<const char *>(p), *b = static_cast<const char *>(q);
+    return a && b && a < b + qn && b < a + pn;
+}
+
+static size_t dt_bytes(int32_t dt) { return dt == MOE_DT_F32 ? 4 : dt == MOE_DT_BF16 ? 2 : 1; }
+
+// Host checks of what the two norm calls share; fills `a` apart from the source row.
+static moe_status norm_args(const char *fn, int32_t n_tokens, int32_t hidden, const void *residual,
+                            void *residual_out, int32_t res_dt, const void *weight, int32_t w_dt, float eps, void *y,
+                            int32_t y_dt, void *y_scale, moe::NormArgs &a) {
+    memset(&a, 0, sizeof a);
+    if (n_tokens < 1) return fail(MOE_ERR_INVALID_ARG, "%s: n_tokens < 1", fn);
+    if (hidden < 1) return fail(MOE_ERR_INVALID_ARG, "%s: hidden < 1", fn);
+    if (!weight || !y) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if ((residual == nullptr) != (residual_out == nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "%s: residual_out must be given iff residual is", fn);
+    if ((residual && res_dt != MOE_DT_F32 && res_dt != MOE_DT_BF16) || (w_dt != MOE_DT_F32 && w_dt != MOE_DT_BF16))
+        return fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+    if (y_dt < MOE_DT_F32 || y_dt > MOE_DT_E4M3_ROW) return fail(MOE_ERR_INVALID_ARG, "%s: unknown output dtype", fn);
+    const bool scaled = y_dt == MOE_DT_E4M3_BLOCK || y_dt == MOE_DT_E4M3_ROW;
+    if (scaled != (y_scale != nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "%s: y_scale must be given iff y is e4m3", fn);
+    if (!std::isfinite(eps) || eps < 0.f) return fail(MOE_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+    if ((residual && (!aligned(residual, dt_bytes(res_dt)) || !aligned(residual_out, dt_bytes(res_dt)))) ||
+        !aligned(weight, dt_bytes(w_dt)) || !aligned(y, dt_bytes(y_dt)) ||
+        (y_dt == MOE_DT_E4M3_ROW && !aligned(y_scale, 4)))
+        return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    const size_t n = (size_t)n_tokens * hidden, rb = residual ? n * dt_bytes(res_dt) : 0, yb = n * dt_bytes(y_dt);
+    const size_t sb = y_dt == MOE_DT_E4M3_ROW ? 4 * (size_t)n_tokens
+                                              : (size_t)n_tokens * (((size_t)hidden + 31) / 32);
+    const size_t wb = (size_t)hidden * dt_bytes(w_dt);
+    if (overlap(y, yb, residual, rb) || overlap(y, yb, residual_out, rb) || overlap(y, yb, weight, wb) ||
+        overlap(y, yb, y_scale, sb) || overlap(residual_out, rb, weight, wb) || overlap(residual_out, rb, y_scale, sb) ||
+        overlap(y_scale, sb, residual, rb) || overlap(y_scale, sb, weight, wb) ||
+        (residual != residual_out && overlap(residual_out, rb, residual, rb)))
+        return fail(MOE_ERR_INVALID_ARG, "%s: an output overlaps another buffer", fn);
+    if (hidden > MOE_NORM_MAX_HIDDEN)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: hidden > %d", fn, MOE_NORM_MAX_HIDDEN);
+    a.T = n_tokens; a.H = hidden;
+    a.residual = residual; a.residual_out = residual_out;
+    a.res_kind = !residual ? moe::RES_NONE : res_dt == MOE_DT_F32 ? moe::RES_F32 : moe::RES_BF16;
+    a.weight = weight; a.w_bf16 = w_dt == MOE_DT_BF16;
+    a.eps = eps;
+    a.y = y; a.y_scale = y_scale;
+    a.y_kind = y_dt == MOE_DT_F32 ? moe::NORM_F32 : y_dt == MOE_DT_BF16 ? moe::NORM_BF16
+             : y_dt == MOE_DT_E4M3_BLOCK ? moe::NORM_MX8 : moe::NORM_ROW8;
+    return MOE_OK;
+}
+
+// No output of a norm call may overlap its input `p` of `n` bytes.
+static bool norm_writes(const moe::NormArgs &a, const void *p, size_t n) {
+    const size_t e = (size_t)a.T * a.H;
+    const size_t rb = a.res_kind == moe::RES_NONE ? 0 : e * (a.res_kind == moe::RES_F32 ? 4 : 2);
+    const size_t yb = e * (a.y_kind == moe::NORM_F32 ? 4 : a.y_kind == moe::NORM_BF16 ? 2 : 1);
+    const size_t sb = a.y_kind == moe::NORM_ROW8 ? 4 * (size_t)a.T : (size_t)a.T * (((size_t)a.H + 31) / 32);
+    return overlap(p, n, a.residual_out, rb) || overlap(p, n, a.y, yb) || overlap(p, n, a.y_scale, sb);
+}
+
+moe_status moe_add_rms_norm(const void *x, int32_t x_dt, int32_t n_tokens, int32_t hidden, const void *residual,
+                            void *residual_out, int32_t res_dt, const void *weight, int32_t w_dt, float eps, void *y,
+                            int32_t y_dt, void *y_scale, void *stream) {
+    const char *fn = "moe_add_rms_norm";
+    if (!x) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (x_dt != MOE_DT_F32 && x_dt != MOE_DT_BF16) return fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+    if (!aligned(x, dt_bytes(x_dt))) return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    moe::NormArgs a;
+    moe_status st = norm_args(fn, n_tokens, hidden, residual, residual_out, res_dt, weight, w_dt, eps, y, y_dt,
+                              y_scale, a);
+    if (st != MOE_OK) return st;
+    if (norm_writes(a, x, (size_t)n_tokens * hidden * dt_bytes(x_dt)))
+        return fail(MOE_ERR_INVALID_ARG, "%s: an output overlaps x", fn);
+    a.x = x; a.x_bf16 = x_dt == MOE_DT_BF16;
+    return from_hip(moe::launch_norm(a, (hipStream_t)stream), fn, (hipStream_t)stream);
+}
+
+moe_status moe_combine_norm(const float *slot_out, const float *topk_w, const float *shared_out, int32_t n_tokens,
+                            int32_t top_k, int32_t hidden, const float *steer_v, float steer_f, const void *residual,
+                            void *residual_out, int32_t res_dt, const void *weight, int32_t w_dt, float eps, void *y,
+                            int32_t y_dt, void *y_scale, void *stream) {
+    const char *fn = "moe_combine_norm";
+    if (!slot_out || !topk_w) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (top_k < 1) return fail(MOE_ERR_INVALID_ARG, "%s: bad shape", fn);
+    if (!aligned(slot_out, 4) || !aligned(topk_w, 4) || (shared_out && !aligned(shared_out, 4)) ||
+        (steer_v && !aligned(steer_v, 4)))
+        return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    if (steer_v && !std::isfinite(steer_f)) return fail(MOE_ERR_INVALID_ARG, "%s: steering strength not finite", fn);
+    moe::NormArgs a;
+    moe_status st = norm_args(fn, n_tokens, hidden, residual, residual_out, res_dt, weight, w_dt, eps, y, y_dt,
+                              y_scale, a);
+    if (st != MOE_OK) return st;
+    const size_t row = (size_t)hidden * 4;
+    if (norm_writes(a, slot_out, (size_t)n_tokens * top_k * row) || norm_writes(a, topk_w, (size_t)n_tokens * top_k * 4) ||
+        (shared_out && norm_writes(a, shared_out, n_tokens * row)) || (steer_v && norm_writes(a, steer_v, row)))
+        return fail(MOE_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+    a.slot_out = slot_out; a.topk_w = topk_w; a.shared_out = shared_out; a.k = top_k;
+    a.steer_v = steer_v; a.steer_f = steer_f;
+    return from_hip(moe::launch_norm(a, (hipStream_t)stream), fn, (hipStream_t)stream);
+}
+
 moe_status moe_probe_stream_read(const void *buf, size_t bytes, uint32_t *sink, int32_t n_blocks, void *stream) {
     if (!buf || !sink) return fail(MOE_ERR_INVALID_ARG, "moe_probe_stream_read: null pointer");
     if (bytes < 16 || bytes % 16 || !aligned(buf, 16) || !aligned(sink, 4))

@@ -77,6 +77,29 @@ hipError_t launch_combine(const float *slot_out, const float *topk_w, const floa
 hipError_t launch_combine_steer(const float *slot_out, const float *topk_w, const float *shared_out, int T, int k,
                                 int H, const float *v, float F, float *y, hipStream_t st);
 
+// norm.hip: residual addition + RMS norm of x, or (slot_out set) of the combine's result
+enum { NORM_F32 = 0, NORM_BF16 = 1, NORM_MX8 = 2, NORM_ROW8 = 3 };
+enum { RES_NONE = 0, RES_F32 = 1, RES_BF16 = 2 };
+struct NormArgs {
+    int T, H;
+    const void *x;
+    int x_bf16;
+    const float *slot_out, *topk_w, *shared_out;   // instead of x; shared_out optional
+    int k;
+    const float *steer_v;                          // optional
+    float steer_f;
+    const void *residual;
+    void *residual_out;                            // may be `residual` itself
+    int res_kind;
+    const void *weight;
+    int w_bf16;
+    float eps;
+    void *y;
+    int y_kind;
+    void *y_scale;                                 // MX8: [T][ceil(H/32)] e8m0 bytes; ROW8: [T] fp32
+};
+hipError_t launch_norm(const NormArgs &a, hipStream_t st);
+
 // probe.hip: streaming-read ceiling (measurement only)
 hipError_t launch_stream_read(const void *buf, int64_t bytes, uint32_t *sink, int n_blocks, hipStream_t st);
 

@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 3
+#define MOE_ABI_VERSION 4
 
 typedef enum {
     MOE_OK = 0,
@@ -72,7 +72,16 @@ typedef enum {
     MOE_ERR_DEVICE = 3
 } moe_status;
 
-typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
+/*
+ * The two e4m3 types are outputs of the norm calls only: 8-bit values (OCP
+ * e4m3: 4 exponent bits, 3 mantissa bits, largest 448, no infinity) beside
+ * scales,
+ *   E4M3_BLOCK  one power-of-two scale per 32 consecutive columns of a row,
+ *               [rows][ceil(cols/32)] bytes holding e + 127: value = code * 2^e
+ *               (the block format the matrix cores read);
+ *   E4M3_ROW    one fp32 scale per row, [rows]: value = code * scale.
+ */
+typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_E4M3_BLOCK = 2, MOE_DT_E4M3_ROW = 3 } moe_dtype;
 
 typedef enum { MOE_FMT_IQ2X = 1, MOE_FMT_Q2K = 2, MOE_FMT_Q4K = 3 } moe_format;
 
@@ -359,6 +368,56 @@ moe_status moe_layer(const moe_layer_desc *L, const void *x, int32_t x_dt, int32
                      int32_t w_dt, const float *bias, int32_t *topk_idx, float *topk_w, float *logits,
                      int32_t *expert_offsets, int32_t *perm, int32_t *active, float *slot_out, float *shared_out,
                      const float *steer_v, float steer_f, float *y, void *ws, size_t ws_bytes, void *stream);
+
+/* Largest row length of the two norm calls below. */
+#define MOE_NORM_MAX_HIDDEN 32768
+
+/*
+ * Residual addition and root-mean-square norm around the layer: the layer reads
+ * the norm of a residual stream, and its output joins that stream.
+ *
+ *   v = x[t] + residual[t]            (fp32; x[t] alone without a residual)
+ *   residual_out[t] = v, rounded to its type, and v = that value from here on
+ *   n = v / sqrt(sum_c v[c]^2 / hidden + eps) * weight
+ *   y[t] = n, rounded to y_dt
+ *
+ *   x            [n_tokens][hidden], fp32 (moe_layer's y) or bf16;
+ *   residual     [n_tokens][hidden], fp32 or bf16 (res_dt), or NULL;
+ *   residual_out the same shape and type, given iff residual is; it may be
+ *                `residual` itself (updated in place);
+ *   weight       [hidden], fp32 or bf16;
+ *   y            [n_tokens][hidden] fp32, bf16 (what moe_route and
+ *                moe_expert_ffn read) or e4m3;
+ *   y_scale      given iff y is e4m3.  E4M3_BLOCK: the exponent e of a block is
+ *                the least with max |n| <= 448 * 2^e, clamped to [-127, 127]
+ *                (no value saturates; an all-zero block has e = -127).
+ *                E4M3_ROW: scale = max(max |n|, 448 * 2^-126) / 448.  Codes are
+ *                n over the scale, rounded to nearest even.
+ * No other two buffers may overlap.  Sums are fp32 in an order that depends on
+ * the shape alone, so a row's result does not depend on the other rows, and
+ * repeated calls give the same bits.  The sum of a row's squares must fit fp32.
+ * Every hidden up to MOE_NORM_MAX_HIDDEN is taken; hidden % 8 == 0 with 16-byte
+ * aligned pointers takes 16-byte loads.  Errors: MOE_ERR_INVALID_ARG (null,
+ * misaligned to its own type or overlapping buffer, bad shape or dtype, eps
+ * negative or not finite), MOE_ERR_UNSUPPORTED (hidden above the limit),
+ * MOE_ERR_DEVICE (launch failure).
+ */
+moe_status moe_add_rms_norm(const void *x, int32_t x_dt, int32_t n_tokens, int32_t hidden, const void *residual,
+                            void *residual_out, int32_t res_dt, const void *weight, int32_t w_dt, float eps, void *y,
+                            int32_t y_dt, void *y_scale, void *stream);
+
+/*
+ * The combine that closes the layer, the residual addition and the norm that
+ * opens the next block, in one launch: moe_add_rms_norm of
+ *   x[t][c] = sum_{j<k} topk_w[t][j] * slot_out[t*k+j][c] (+ shared_out[t][c])
+ * as in moe_combine, then steered as in moe_combine_steer when steer_v is not
+ * NULL.  The combined row stays in registers (it is not written).  Arguments
+ * and errors as in those three calls; the pointers must be 4-byte aligned.
+ */
+moe_status moe_combine_norm(const float *slot_out, const float *topk_w, const float *shared_out, int32_t n_tokens,
+                            int32_t top_k, int32_t hidden, const float *steer_v, float steer_f, const void *residual,
+                            void *residual_out, int32_t res_dt, const void *weight, int32_t w_dt, float eps, void *y,
+                            int32_t y_dt, void *y_scale, void *stream);
 
 /*
  * Measurement helper, not part of the layer: reads `bytes` bytes of `buf`
