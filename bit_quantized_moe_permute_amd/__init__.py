@@ -28,6 +28,7 @@ EXPORTS = [
     "moe_dequantize", "moe_route_workspace", "moe_route", "moe_expert_ffn_workspace", "moe_expert_ffn",
     "moe_expert_gate_up", "moe_expert_down", "moe_combine", "moe_combine_steer", "moe_probe_stream_read",
     "moe_expert_ffn_noalloc", "moe_layer_workspace", "moe_layer", "moe_add_rms_norm", "moe_combine_norm",
+    "moe_shared_ffn_workspace", "moe_shared_ffn",
 ]
 
 
@@ -48,6 +49,16 @@ class LayerDesc(ctypes.Structure):
         ("shared_gate", ctypes.c_void_p), ("shared_up", ctypes.c_void_p), ("shared_down", ctypes.c_void_p),
         ("path", ctypes.c_int32),
         ("precision", ctypes.c_int32),
+    ]
+
+
+class AdapterDesc(ctypes.Structure):
+    """moe_adapter_desc (include/moe2bit.h)."""
+    _fields_ = [
+        ("n_adapters", ctypes.c_int32), ("max_rank", ctypes.c_int32),
+        ("rank", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+        ("gate_a", ctypes.c_void_p), ("gate_b", ctypes.c_void_p), ("up_a", ctypes.c_void_p), ("up_b", ctypes.c_void_p),
+        ("down_a", ctypes.c_void_p), ("down_b", ctypes.c_void_p),
     ]
 
 
@@ -97,6 +108,11 @@ def _load():
     L.moe_combine_norm.restype = ctypes.c_int
     L.moe_combine_norm.argtypes = [vp, vp, vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, i32, vp, i32,
                                    ctypes.c_float, vp, i32, vp, vp]
+    L.moe_shared_ffn_workspace.restype = sz
+    L.moe_shared_ffn_workspace.argtypes = [ctypes.POINTER(LayerDesc), ctypes.POINTER(AdapterDesc), i32]
+    L.moe_shared_ffn.restype = ctypes.c_int
+    L.moe_shared_ffn.argtypes = [ctypes.POINTER(LayerDesc), ctypes.POINTER(AdapterDesc), vp, i32, i32, vp, vp, i32, vp,
+                                 sz, vp]
     L.moe_probe_stream_read.restype = ctypes.c_int
     L.moe_probe_stream_read.argtypes = [vp, sz, vp, i32, vp]
     if L.moe_abi_version() != ABI_VERSION:
@@ -405,6 +421,32 @@ def moe_combine_norm(slot_out, topk_w, shared_out, residual, residual_out, weigh
                                 _stream_on(stream, dev)))
 
 
+def moe_shared_ffn_workspace(desc: LayerDesc, n_tokens: int, adapters=None) -> int:
+    """adapters: an AdapterPool, or None."""
+    return lib.moe_shared_ffn_workspace(desc, None if adapters is None else adapters.desc, n_tokens)
+
+
+def moe_shared_ffn(desc: LayerDesc, x, out, ws, adapters=None, token_adapter=None, stream=None):
+    """The layer's shared expert on x [T][H] into out [T][H], token t through adapter token_adapter[t] of the
+    AdapterPool `adapters` (an index outside the pool: none)."""
+    T, H = _rows(x, desc.hidden)
+    _need(out, T * H, "out")
+    dev, pool = x.get_device(), None
+    if adapters is not None:
+        import torch
+        if (adapters.hidden, adapters.inter) != (H, desc.shared_inter):
+            raise ValueError(f"adapters are for hidden {adapters.hidden}, inter {adapters.inter}; the layer has "
+                             f"{H}, {desc.shared_inter}")
+        if adapters.device_index != dev and dev >= 0:
+            raise ValueError(f"tensors on devices {dev} and {adapters.device_index}")
+        if token_adapter is None or token_adapter.dtype != torch.int32:
+            raise TypeError("token_adapter must be an int32 tensor")
+        _need(token_adapter, T, "token_adapter")
+        pool = adapters.desc
+    _check(lib.moe_shared_ffn(desc, pool, _addr(x, dev), _dt(x), T, _addr(token_adapter, dev), _addr(out, dev), _dt(out),
+                              _addr(ws, dev), ws.numel() * ws.element_size(), _stream_on(stream, dev)))
+
+
 def moe_probe_stream_read(buf, nbytes, sink, n_blocks, stream=None):
     """Measurement helper: one streaming read of buf's first nbytes bytes (sink: n_blocks uint32 words)."""
     _need_bytes(buf, nbytes, "buf")
@@ -412,4 +454,4 @@ def moe_probe_stream_read(buf, nbytes, sink, n_blocks, stream=None):
     _check(lib.moe_probe_stream_read(_ptr(buf), nbytes, _ptr(sink), n_blocks, _stream(stream)))
 
 
-from .layer import DeviceLayer, LayerBuffers  # noqa: E402  (needs `lib` loaded)
+from .layer import AdapterPool, DeviceLayer, LayerBuffers  # noqa: E402  (needs `lib` loaded)

@@ -567,6 +567,76 @@ moe_status moe_combine_norm(const float *slot_out, const float *topk_w, const fl
     return from_hip(moe::launch_norm(a, (hipStream_t)stream), fn, (hipStream_t)stream);
 }
 
+// ---------------------------------------------------------------------------
+// shared expert with low-rank adapters
+// ---------------------------------------------------------------------------
+static moe_status check_shared(const char *fn, const moe_layer_desc *L, const moe_adapter_desc *A, int32_t n_tokens) {
+    if (!L) return fail(MOE_ERR_INVALID_ARG, "%s: null layer", fn);
+    if (n_tokens < 1) return fail(MOE_ERR_INVALID_ARG, "%s: n_tokens < 1", fn);
+    if (L->hidden < 8 || L->shared_inter < 8 || L->hidden % 8 || L->shared_inter % 8)
+        return fail(MOE_ERR_INVALID_ARG, "%s: hidden and shared_inter must be positive multiples of 8", fn);
+    if (!L->shared_gate || !L->shared_up || !L->shared_down)
+        return fail(MOE_ERR_INVALID_ARG, "%s: null shared expert weights", fn);
+    if (!aligned(L->shared_gate, 16) || !aligned(L->shared_up, 16) || !aligned(L->shared_down, 16))
+        return fail(MOE_ERR_INVALID_ARG, "%s: shared expert weights not 16-byte aligned", fn);
+    if (!A) return MOE_OK;
+    if (A->n_adapters < 1 || A->n_adapters > MOE_MAX_ADAPTERS)
+        return fail(MOE_ERR_INVALID_ARG, "%s: n_adapters outside [1, %d]", fn, MOE_MAX_ADAPTERS);
+    if (A->max_rank < 8 || A->max_rank > MOE_MAX_RANK || A->max_rank % 8)
+        return fail(MOE_ERR_INVALID_ARG, "%s: max_rank must be a multiple of 8 in [8, %d]", fn, MOE_MAX_RANK);
+    const void *ab[3][2] = {{A->gate_a, A->gate_b}, {A->up_a, A->up_b}, {A->down_a, A->down_b}};
+    for (const auto &p : ab) {
+        if ((p[0] == nullptr) != (p[1] == nullptr))
+            return fail(MOE_ERR_INVALID_ARG, "%s: both matrices of a projection's adapters, or neither", fn);
+        if (!aligned(p[0], 16) || !aligned(p[1], 16))
+            return fail(MOE_ERR_INVALID_ARG, "%s: adapter weights not 16-byte aligned", fn);
+    }
+    if (!aligned(A->rank, 4) || !aligned(A->scale, 4))
+        return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer (adapter ranks or scales)", fn);
+    return MOE_OK;
+}
+
+size_t moe_shared_ffn_workspace(const moe_layer_desc *L, const moe_adapter_desc *A, int32_t n_tokens) {
+    if (check_shared("moe_shared_ffn_workspace", L, A, n_tokens) != MOE_OK) return 0;
+    return moe::shared_workspace(n_tokens, L->hidden, L->shared_inter, A ? A->n_adapters : 0, A ? A->max_rank : 0);
+}
+
+moe_status moe_shared_ffn(const moe_layer_desc *L, const moe_adapter_desc *A, const void *x, int32_t x_dt,
+                          int32_t n_tokens, const int32_t *token_adapter, void *out, int32_t out_dt, void *ws,
+                          size_t ws_bytes, void *stream) {
+    const char *fn = "moe_shared_ffn";
+    moe_status st = check_shared(fn, L, A, n_tokens);
+    if (st != MOE_OK) return st;
+    if (!x || !out || !ws || (A && !token_adapter)) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if ((x_dt != MOE_DT_F32 && x_dt != MOE_DT_BF16) || (out_dt != MOE_DT_F32 && out_dt != MOE_DT_BF16))
+        return fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+    if (!aligned(x, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(token_adapter, 4))
+        return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer (x/out 16 B, ws 256 B)", fn);
+    const size_t need = moe_shared_ffn_workspace(L, A, n_tokens);
+    if (ws_bytes < need) return fail(MOE_ERR_INVALID_ARG, "%s: workspace too small (%zu < %zu)", fn, ws_bytes, need);
+    const size_t n = (size_t)n_tokens * L->hidden, xb = n * dt_bytes(x_dt), ob = n * dt_bytes(out_dt);
+    const size_t ib = A ? (size_t)n_tokens * 4 : 0;
+    if (overlap(out, ob, x, xb) || overlap(ws, need, x, xb) || overlap(ws, need, out, ob) ||
+        overlap(out, ob, token_adapter, ib) || overlap(ws, need, token_adapter, ib))
+        return fail(MOE_ERR_INVALID_ARG, "%s: out or ws overlaps another buffer", fn);
+    moe::SharedArgs a;
+    memset(&a, 0, sizeof a);
+    a.T = n_tokens; a.H = L->hidden; a.Is = L->shared_inter;
+    a.x = x; a.x_bf16 = x_dt == MOE_DT_BF16;
+    a.gate = static_cast<const uint16_t *>(L->shared_gate);
+    a.up = static_cast<const uint16_t *>(L->shared_up);
+    a.down = static_cast<const uint16_t *>(L->shared_down);
+    if (A) {
+        a.n = A->n_adapters; a.R = A->max_rank; a.rank = A->rank; a.scale = A->scale;
+        a.gate_a = static_cast<const uint16_t *>(A->gate_a); a.gate_b = static_cast<const uint16_t *>(A->gate_b);
+        a.up_a = static_cast<const uint16_t *>(A->up_a); a.up_b = static_cast<const uint16_t *>(A->up_b);
+        a.down_a = static_cast<const uint16_t *>(A->down_a); a.down_b = static_cast<const uint16_t *>(A->down_b);
+        a.token_adapter = token_adapter;
+    }
+    a.out = out; a.out_bf16 = out_dt == MOE_DT_BF16;
+    return from_hip(moe::launch_shared(a, ws, (hipStream_t)stream), fn, (hipStream_t)stream);
+}
+
 moe_status moe_probe_stream_read(const void *buf, size_t bytes, uint32_t *sink, int32_t n_blocks, void *stream) {
     if (!buf || !sink) return fail(MOE_ERR_INVALID_ARG, "moe_probe_stream_read: null pointer");
     if (bytes < 16 || bytes % 16 || !aligned(buf, 16) || !aligned(sink, 4))

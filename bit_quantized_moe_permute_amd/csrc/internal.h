@@ -100,6 +100,47 @@ struct NormArgs {
 };
 hipError_t launch_norm(const NormArgs &a, hipStream_t st);
 
+// ffn_shared.hip: the shared expert with low-rank adapters
+constexpr int MAX_ADAPTERS = 4096, MAX_RANK = 256;
+constexpr int FEW_TOKENS = 64;           // up to here the weight rows stream past all tokens at once
+constexpr int ITEM_TOKENS = 64;          // tokens of one adapter per work item of the down-rank products
+struct SharedArgs {
+    int T, H, Is;
+    const void *x;
+    int x_bf16;
+    const uint16_t *gate, *up, *down;
+    int n, R;                            // adapters (0: none), rows of A / columns of B per adapter
+    const int32_t *rank;                 // optional
+    const float *scale;                  // optional
+    const uint16_t *gate_a, *gate_b, *up_a, *up_b, *down_a, *down_b;   // a pair may be NULL
+    const int32_t *token_adapter;
+    void *out;
+    int out_bf16;
+    // filled by the launcher
+    int ks, sorted;
+    int32_t *perm, *plan_ad, *n_items;   // sorted position -> token, its adapter (-1: none)
+    int4 *items;                         // adapter, first sorted position, tokens
+};
+struct LowRank {
+    const uint16_t *x;                   // [P][T][K] bf16 planes
+    int K, np;
+    int gather;                          // rows of x are tokens (through perm), not sorted positions
+    const uint16_t *a[2];
+    float *s;                            // [ks][T][np][R]
+};
+struct Product {
+    const uint16_t *x;                   // [P][T][K] bf16 planes
+    int K, N, gather;
+    const uint16_t *w[2], *b[2];
+    const float *s;
+    uint16_t *h;                         // gate/up: [hp][T][N] bf16 planes, by sorted position
+    int hp;
+    void *out;                           // down: [T][N], by token
+    int out_bf16;
+};
+size_t shared_workspace(int T, int H, int Is, int n, int R);
+hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st);
+
 // probe.hip: streaming-read ceiling (measurement only)
 hipError_t launch_stream_read(const void *buf, int64_t bytes, uint32_t *sink, int n_blocks, hipStream_t st);
 

@@ -10,13 +10,53 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (FMT_IQ2X, PATH_AUTO, PRECISION_EXACT, LayerDesc, moe_combine, moe_combine_steer, moe_expert_ffn,
-               moe_expert_ffn_workspace, moe_layer, moe_layer_workspace, moe_prepare_weights, moe_route,
-               moe_route_workspace, moe_weight_bytes)
+from . import (FMT_IQ2X, PATH_AUTO, PRECISION_EXACT, AdapterDesc, LayerDesc, moe_add_rms_norm, moe_combine,
+               moe_combine_norm, moe_combine_steer, moe_expert_ffn, moe_expert_ffn_workspace, moe_layer,
+               moe_layer_workspace, moe_prepare_weights, moe_route, moe_route_workspace, moe_shared_ffn,
+               moe_shared_ffn_workspace, moe_weight_bytes)
 
 
 def _u8(a: np.ndarray, device) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(a).view(np.uint8).reshape(-1)).to(device)
+
+
+class AdapterPool:
+    """Low-rank adapters of a shared expert resident in device memory.
+
+    gate, up, down: (A, B) bf16 tensors, A [n][R][columns of W] and B [n][rows of W][R], or None for a projection
+    without adapters; adapter a adds scale[a] * B[a] A[a] to W.  rank: int32 [n] (ranks up to R; None: all R).
+    scale: fp32 [n] (None: all 1).  The pool keeps the tensors; their values may be changed in place (an adapter loaded
+    into a slot) between calls.
+    """
+
+    def __init__(self, hidden, inter, gate=None, up=None, down=None, rank=None, scale=None):
+        self.hidden, self.inter = hidden, inter
+        pairs = {"gate": (gate, inter, hidden), "up": (up, inter, hidden), "down": (down, hidden, inter)}
+        given = [p[0] for p in pairs.values() if p[0] is not None]
+        if not given:
+            raise ValueError("adapters for no projection")
+        n, R = given[0][0].shape[:2]
+        self.n, self.max_rank = n, R
+        self.device_index = given[0][0].get_device()
+        self.desc = AdapterDesc(n_adapters=n, max_rank=R)
+        self._keep = []
+        for name, (ab, rows, cols) in pairs.items():
+            if ab is not None:
+                self._hold(name + "_a", ab[0], (n, R, cols), torch.bfloat16)
+                self._hold(name + "_b", ab[1], (n, rows, R), torch.bfloat16)
+        if rank is not None:
+            self._hold("rank", rank, (n,), torch.int32)
+        if scale is not None:
+            self._hold("scale", scale, (n,), torch.float32)
+
+    def _hold(self, name, t, shape, dtype):
+        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape}, got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        if t.get_device() != self.device_index:
+            raise ValueError(f"{name}: adapters on devices {self.device_index} and {t.get_device()}")
+        self._keep.append(t)
+        setattr(self.desc, name, t.data_ptr())
 
 
 class DeviceLayer:
@@ -51,6 +91,14 @@ class DeviceLayer:
         self.path = path
         self.desc = self.make_desc(path)
         self.steer_v, self.steer_f = None, 0.0
+        self.adapters = None
+
+    def set_adapters(self, pool: AdapterPool | None):
+        """Low-rank adapters of this layer's shared expert, for forward() calls that name each token's; None: none."""
+        if pool is not None and (pool.hidden, pool.inter) != (self.H, self.Is):
+            raise ValueError(f"adapters are for hidden {pool.hidden}, inter {pool.inter}; the layer's shared expert has "
+                             f"{self.H}, {self.Is}")
+        self.adapters = pool
 
     def set_steering(self, v, F: float = 1.0):
         """Directional steering of this layer's FFN output, y -= F * v * dot(v, y): v is one fp32 value per hidden
@@ -84,6 +132,12 @@ class DeviceLayer:
             d.shared_gate, d.shared_up, d.shared_down = (s.data_ptr() for s in self.shared)
         d.path = path
         d.precision = precision
+        return d
+
+    def routed_desc(self, desc: LayerDesc | None = None) -> LayerDesc:
+        """The layer without its shared expert (which moe_shared_ffn computes then)."""
+        d = LayerDesc.from_buffer_copy(desc or self.desc)
+        d.shared_inter, d.shared_gate, d.shared_up, d.shared_down = 0, None, None, None
         return d
 
     def clone(self) -> "DeviceLayer":
@@ -122,6 +176,8 @@ class LayerBuffers:
     ws_ffn: torch.Tensor
     y: torch.Tensor
     ws: torch.Tensor            # one buffer: ws_route and ws_ffn are views into it (the layout moe_layer takes)
+    ws_shared: torch.Tensor | None = None       # moe_shared_ffn's, when the layer has adapters
+    xn: torch.Tensor | None = None              # the normed rows forward_block() hands to the layer
 
     @classmethod
     def allocate(cls, L: DeviceLayer, T: int, with_logits: bool = False) -> "LayerBuffers":
@@ -131,6 +187,7 @@ class LayerBuffers:
         ws_r = (moe_route_workspace(T, L.E, L.k) + 255) // 256 * 256
         ws_l = moe_layer_workspace(L.desc, T)
         ws = torch.empty(max(ws_l, ws_r + 256), dtype=torch.uint8, device=dev)
+        ws_s = moe_shared_ffn_workspace(L.desc, T, L.adapters) if L.adapters is not None else 0
         return cls(
             T=T,
             topk_idx=torch.empty(T, L.k, **i32), topk_w=torch.empty(T, L.k, **f32),
@@ -143,18 +200,50 @@ class LayerBuffers:
             ws_ffn=ws[ws_r:],
             y=torch.empty(T, L.H, **f32),
             ws=ws,
+            ws_shared=torch.empty(ws_s, dtype=torch.uint8, device=dev) if ws_s else None,
+            xn=torch.empty(T, L.H, dtype=torch.bfloat16, device=dev),
         )
 
 
-def forward(L: DeviceLayer, x: torch.Tensor, b: LayerBuffers, desc: LayerDesc | None = None, stream=None):
-    """route -> expert FFN -> combine (+ steering, when the layer has a direction) for x [T][H] (bf16 or fp32)
-    into b.y."""
-    T = x.shape[0]
-    assert T == b.T
+def _route_and_experts(L: DeviceLayer, x, b: LayerBuffers, desc, token_adapter, stream):
+    """moe_route and the experts: b.slot_out and b.shared_out.  With adapters and token_adapter the shared expert runs
+    as a call of its own."""
+    assert x.shape[0] == b.T
     moe_route(x, L.w_router, L.E, L.k, b.topk_idx, b.topk_w, b.offsets, b.perm, b.active, b.ws_route, bias=L.bias,
               logits=b.logits, stream=stream)
-    moe_expert_ffn(desc or L.desc, x, b.topk_idx, b.offsets, b.perm, b.active, b.slot_out, b.shared_out, b.ws_ffn,
+    if token_adapter is None:
+        moe_expert_ffn(desc or L.desc, x, b.topk_idx, b.offsets, b.perm, b.active, b.slot_out, b.shared_out, b.ws_ffn,
+                       stream=stream)
+        return
+    if L.adapters is None:
+        raise ValueError("token_adapter given, but the layer has no adapters (set_adapters)")
+    if b.ws_shared is None:
+        raise ValueError("these buffers were allocated before the layer had adapters")
+    moe_expert_ffn(L.routed_desc(desc), x, b.topk_idx, b.offsets, b.perm, b.active, b.slot_out, None, b.ws_ffn,
                    stream=stream)
+    moe_shared_ffn(L.desc, x, b.shared_out, b.ws_shared, L.adapters, token_adapter, stream=stream)
+
+
+def forward_block(L: DeviceLayer, x: torch.Tensor, residual: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor,
+                  eps: float, b: LayerBuffers, y: torch.Tensor, y_scale=None, token_adapter=None, stream=None):
+    """The layer between its two norms, on a residual stream that is updated in place:
+
+        residual += x;  xn = norm(residual) * w_in;  residual += layer(xn);  y = norm(residual) * w_out
+
+    x [T][H] fp32 or bf16 (the attention's output), y in any type of moe_add_rms_norm."""
+    moe_add_rms_norm(x, residual, residual, w_in, eps, b.xn, stream=stream)
+    _route_and_experts(L, b.xn, b, None, token_adapter, stream)
+    moe_combine_norm(b.slot_out, b.topk_w, b.shared_out, residual, residual, w_out, eps, y, y_scale,
+                     steer_v=L.steer_v, steer_f=L.steer_f, stream=stream)
+    return y
+
+
+def forward(L: DeviceLayer, x: torch.Tensor, b: LayerBuffers, desc: LayerDesc | None = None, stream=None,
+            token_adapter: torch.Tensor | None = None):
+    """route -> expert FFN -> combine (+ steering, when the layer has a direction) for x [T][H] (bf16 or fp32)
+    into b.y.  token_adapter (int32 [T]): each token's adapter of the shared expert (L.set_adapters)."""
+    T = x.shape[0]
+    _route_and_experts(L, x, b, desc, token_adapter, stream)
     if L.steer_v is None:
         moe_combine(b.slot_out, b.topk_w, b.shared_out, T, L.k, L.H, b.y, stream=stream)
     else:

@@ -420,6 +420,63 @@ moe_status moe_combine_norm(const float *slot_out, const float *topk_w, const fl
                             int32_t y_dt, void *y_scale, void *stream);
 
 /*
+ * Low-rank adapters of the shared expert's projections (host struct; read
+ * during the call only): a pool of n_adapters, one of which each token may use.
+ * Projection W of a token with adapter a acts as W + scale[a] * B[a] A[a].
+ *   max_rank (R): rows of each A[a] and columns of each B[a]; a multiple of 8,
+ *     8 <= R <= MOE_MAX_RANK.  n_adapters: 1 .. MOE_MAX_ADAPTERS.
+ *   rank: device int32 [n_adapters], or NULL (all R).  Adapter a has its first
+ *     rank[a] rows of A and columns of B (clamped to 0 .. R); what lies behind
+ *     them is not used, whatever it holds.
+ *   scale: device fp32 [n_adapters], or NULL (all 1).
+ *   gate_a, up_a [n][R][H], gate_b, up_b [n][Is][R], down_a [n][R][Is], down_b
+ *     [n][H][R]: bf16, device, 16-byte aligned; the two of a projection are
+ *     both given or both NULL (projection without adapters).
+ */
+#define MOE_MAX_ADAPTERS 4096
+#define MOE_MAX_RANK 256
+typedef struct {
+    int32_t n_adapters, max_rank;
+    const int32_t *rank;
+    const float *scale;
+    const void *gate_a, *gate_b, *up_a, *up_b, *down_a, *down_b;
+} moe_adapter_desc;
+
+/* Workspace bytes moe_shared_ffn needs for n_tokens tokens (any x and output
+ * type); 0 for arguments that call refuses.  A may be NULL. */
+size_t moe_shared_ffn_workspace(const moe_layer_desc *L, const moe_adapter_desc *A, int32_t n_tokens);
+
+/*
+ * The shared expert as a call of its own, with adapters of many requests in one
+ * batch:
+ *   out[t] = Wd' (silu(Wg' x[t]) * (Wu' x[t])),  W' = W + scale[a] B[a] A[a],
+ * a = token_adapter[t].  It takes the place of the shared half of
+ * moe_expert_ffn (called with a layer whose shared_inter is 0); `out` in fp32
+ * is the shared_out of moe_combine and moe_combine_norm.
+ *   L: hidden, shared_inter and the shared_* weights are read, nothing else.
+ *   A: adapters, or NULL (none; token_adapter is not read then).
+ *   x [n_tokens][H], bf16 or fp32.  fp32 activations are read as two bf16 parts
+ *     (16 significant bits).
+ *   token_adapter: device int32 [n_tokens]; a value outside 0 .. n_adapters - 1
+ *     (such as -1) means no adapter for that token.
+ *   out [n_tokens][H], fp32 or bf16.
+ *   ws: 256-byte aligned, at least moe_shared_ffn_workspace(L, A, n_tokens)
+ *     bytes; calls that may overlap in time need one each.
+ * Sums are fp32 in an order fixed by the shapes; the low-rank products A[a] x
+ * and, with an fp32 out, the SwiGLU result h are carried as two bf16 parts, h
+ * with a bf16 out as one.  A token's result has the same bits whatever other
+ * tokens and adapters the call holds (at the same n_tokens and n_adapters), and
+ * non-finite values in one adapter reach only the tokens that use it.
+ * hidden and shared_inter must be multiples of 8; x, out and the weights 16-byte
+ * aligned.  Errors: MOE_ERR_INVALID_ARG (null, misaligned or overlapping
+ * pointer, bad shape or dtype, workspace too small), MOE_ERR_DEVICE (launch
+ * failure).
+ */
+moe_status moe_shared_ffn(const moe_layer_desc *L, const moe_adapter_desc *A, const void *x, int32_t x_dt,
+                          int32_t n_tokens, const int32_t *token_adapter, void *out, int32_t out_dt, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/*
  * Measurement helper, not part of the layer: reads `bytes` bytes of `buf`
  * (device, 16-byte aligned, a multiple of 16) once with 16-byte lane loads
  * in n_blocks workgroups of 256 threads, and XORs each workgroup's fold of the
