@@ -21,7 +21,6 @@ using namespace moe;
 
 namespace {
 
-typedef const __attribute__((address_space(1))) void *gas_ptr;
 typedef __attribute__((address_space(3))) void *las_ptr;
 
 __device__ uint4 zero_chunk;             // 16 zero bytes that tiles read past the end of a row
@@ -330,24 +329,38 @@ __global__ __launch_bounds__(512) void k_few(SharedArgs a, Product g) {
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: a workgroup of four waves computes 128 weight rows (gate/up: 64 of each) x BT tokens; both operands
-// pass through LDS in 64-wide K stages, three of them, filled by direct-to-LDS loads two stages ahead.
+// Many tokens: a workgroup of four waves computes 128 weight rows (gate/up: 64 of each) x BT tokens, each wave 64 x BT/2
+// of them; both operands pass through LDS in 64-wide K stages, three of them, filled by direct-to-LDS loads.
 // LDS rows are 128 bytes; 16-byte chunk c of row r lies at position c ^ (r & 7), so eight rows' reads of one chunk
 // column touch all banks once.
+//
+// The loads are written as assembly: the compiler would otherwise wait for all of them before any LDS read.  They
+// have no register outputs; wait_stage() counts them (the kernel has no other vector memory access between the first
+// issue and the last stage) and orders the workgroup.
 // ---------------------------------------------------------------------------
 template <int N> __device__ __forceinline__ void wait_stage() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-constexpr int BW = 128, BK = 64;
+// 64 lanes' 16 bytes at their `src` -> 1 KiB of LDS at byte address `dst` (wave-uniform), in lane order.  The
+// destination goes through m0, which is put back: the compiler may count on its value.
+__device__ __forceinline__ void load_to_lds(const void *src, uint32_t dst) {
+    uint32_t m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off\n\t"
+                 "s_mov_b32 m0, %0"
+                 : "=&s"(m0) : "v"(src), "s"(dst) : "memory");
+}
+
+constexpr int BW = 128, BK = 64, STAGES = 3;
 
 template <bool GU, int P, int BT>
 __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles_w, int tiles_t) {
     constexpr int WT = 2;                                    // waves along the tokens, and along the weight rows
     constexpr int FW = BW / 2 / 32, FT = BT / WT / 32;       // 32 x 32 fragments per wave
     constexpr int ROWS = BW + BT, LOADS = ROWS / 8 / 4;      // direct-to-LDS loads (8 rows each) per wave and stage
-    __shared__ __attribute__((aligned(128))) uint4 tile[3][ROWS * 8];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i32 = lane & 31, hh = lane >> 5;
+    __shared__ __attribute__((aligned(1024))) uint4 tile[STAGES][ROWS * 8];
+    const int lane = threadIdx.x & 63, i32 = lane & 31, hh = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int K = g.K;
     // XCD-aware order: consecutive workgroups go to the eight XCDs in turn; each XCD takes a run of tiles with the
     // token tile fastest, so the workgroups that read the same weight rows share an L2
@@ -373,19 +386,26 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
         }
         src[i] += 8 * chunk;
     }
-    const int ksteps = (K + BK - 1) / BK, nsteps = ksteps * P;
+    const int nsteps = (K + BK - 1) / BK * P;
     const int64_t plane = (int64_t)a.T * K;
-    auto issue = [&](int s) {
-        const int p = s / ksteps, k0 = (s - p * ksteps) * BK;
-        const bool in = k0 + 8 * chunk < K;
-        uint4 *dst = tile[s % 3];
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int r8 = wave * LOADS + i;
-            const uint16_t *q = src[i] + k0 + (r8 * 8 >= BW ? p * plane : 0);
-            if (!in) q = reinterpret_cast<const uint16_t *>(&zero_chunk);
-            __builtin_amdgcn_global_load_lds((gas_ptr)q, (las_ptr)(dst + r8 * 64), 16, 0, 0);
-        }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(las_ptr)tile + wave * LOADS * 1024u;
+    const uint16_t *zeros = reinterpret_cast<const uint16_t *>(&zero_chunk);
+    asm("" : "+v"(zeros));                                   // kept in registers: a select below, not a branch
+    // Loads of the next stage to issue: its K offset and plane.  Past the end of the last row, and in stages behind the last,
+    // they read zeros, so that every stage has the same number of loads in flight.
+    int ik = 0, ip = 0;
+    bool in = 8 * chunk < K;
+    uint32_t idst = lds0;
+    auto issue = [&](int i) {                                // i: load of this wave (compile-time)
+        const uint16_t *q = src[i] + ik;
+        if (P > 1 && (wave * LOADS + i) * 8 >= BW) q += ip ? plane : 0;
+        load_to_lds(in ? q : zeros, idst + i * 1024u);
+    };
+    auto next_stage = [&]() {
+        ik += BK;
+        if (P > 1 && ip == 0 && ik >= K) { ik = 0; ip = 1; }
+        in = ik + 8 * chunk < K;
+        idst = idst == lds0 + (STAGES - 1) * ROWS * 128u ? lds0 : idst + ROWS * 128u;
     };
     f32x16_t acc[FW][FT];
 #pragma unroll
@@ -395,30 +415,56 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
     const int rw = (wave / WT) * FW * 32, rt = BW + (wave % WT) * FT * 32;
-    auto compute = [&](int s) {
-        const uint4 *t = tile[s % 3];
+    uint4 fw[2][FW], ft[2][FT];
+    auto read = [&](const uint4 *t, int kk, int b) {
+        const int c = (2 * kk + hh) ^ (i32 & 7);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            uint4 fw[FW], ft[FT];
-            const int c = (2 * kk + hh) ^ (i32 & 7);
+        for (int i = 0; i < FW; ++i) fw[b][i] = t[(rw + i * 32 + i32) * 8 + c];
 #pragma unroll
-            for (int i = 0; i < FW; ++i) fw[i] = t[(rw + i * 32 + i32) * 8 + c];
+        for (int j = 0; j < FT; ++j) ft[b][j] = t[(rt + j * 32 + i32) * 8 + c];
+    };
+    // the products of one 16-wide slice, with a quarter of a stage's loads issued among them
+    auto products = [&](int b, int quarter) {
+        constexpr int M = FW * FT;
 #pragma unroll
-            for (int j = 0; j < FT; ++j) ft[j] = t[(rt + j * 32 + i32) * 8 + c];
+        for (int m = 0; m < M; ++m) {
+            acc[m % FW][m / FW] = mfma32(fw[b][m % FW], ft[b][m / FW], acc[m % FW][m / FW]);
+            const int l0 = quarter * LOADS / 4, n = (quarter + 1) * LOADS / 4 - l0;
 #pragma unroll
-            for (int i = 0; i < FW; ++i)
-#pragma unroll
-                for (int j = 0; j < FT; ++j) acc[i][j] = mfma32(fw[i], ft[j], acc[i][j]);
+            for (int i = 0; i < LOADS; ++i)
+                if (i >= l0 + m * n / M && i < l0 + (m + 1) * n / M) issue(i);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
-    issue(0);
-    if (nsteps > 1) issue(1);
+    // Stages 0 and 1 and the first quarter of stage 2 are loaded ahead.  Fragments of the next slice are read while the
+    // matrix cores work on the present one.  Before a stage's last slice: wait for the next stage (the one after it stays
+    // in flight) and for the workgroup; from then on nobody reads the present stage's buffer, and it takes the loads of
+    // the stage three further on.
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) issue(i);
+    next_stage();
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) issue(i);
+    next_stage();
+#pragma unroll
+    for (int i = 0; i < LOADS / 4; ++i) issue(i);
+    wait_stage<LOADS + LOADS / 4>();
+    int rb = 0;
+    read(tile[0], 0, 0);
     for (int s = 0; s < nsteps; ++s) {
-        if (s + 1 < nsteps) wait_stage<LOADS>();
-        else wait_stage<0>();
-        if (s + 2 < nsteps) issue(s + 2);
-        compute(s);
+        const uint4 *t = tile[rb];
+#pragma unroll
+        for (int kk = 0; kk < 3; ++kk) {
+            read(t, kk + 1, (kk + 1) & 1);
+            products(kk & 1, kk + 1);
+        }
+        next_stage();
+        rb = rb == STAGES - 1 ? 0 : rb + 1;
+        wait_stage<LOADS>();
+        read(tile[rb], 0, 0);                                // behind the last stage: zeros, not used
+        products(1, 0);
     }
+    wait_stage<0>();
     // D: lane holds token i32 of a fragment, weight rows 8 * (v / 4) + 4 * hh + v % 4
     const int np = GU ? 2 : 1;
 #pragma unroll
@@ -511,15 +557,14 @@ hipError_t launch_product(const SharedArgs &a, const Product &g, hipStream_t st)
         return hipGetLastError();
     }
     const int rows = GU ? BW / 2 : BW, tw = (g.N + rows - 1) / rows;
-    const int tt128 = (T + 127) / 128;
     const dim3 blk(256);
-    if (tw * tt128 >= 256) {
-        const int total = tw * tt128;
-        hipLaunchKernelGGL((k_many<GU, P, 128>), dim3((unsigned)((total + 7) / 8 * 8)), blk, 0, st, a, g, tw, tt128);
-    } else {
-        const int tt = (T + 63) / 64, total = tw * tt;
-        hipLaunchKernelGGL((k_many<GU, P, 64>), dim3((unsigned)((total + 7) / 8 * 8)), blk, 0, st, a, g, tw, tt);
-    }
+    auto tiles = [&](int bt) { return tw * ((T + bt - 1) / bt); };
+    const int bt = tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
+    const dim3 grd((unsigned)((tiles(bt) + 7) / 8 * 8));
+    const int tt = (T + bt - 1) / bt;
+    if (bt == 256) hipLaunchKernelGGL((k_many<GU, P, 256>), grd, blk, 0, st, a, g, tw, tt);
+    else if (bt == 128) hipLaunchKernelGGL((k_many<GU, P, 128>), grd, blk, 0, st, a, g, tw, tt);
+    else hipLaunchKernelGGL((k_many<GU, P, 64>), grd, blk, 0, st, a, g, tw, tt);
     return hipGetLastError();
 }
 
