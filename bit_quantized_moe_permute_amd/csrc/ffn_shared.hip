@@ -6,8 +6,8 @@
 // matrix cores with fp32 sums.  Launches: [split] [plan] [down-rank] gate/up [down-rank] down --
 //
 //   split      fp32 activations as two bf16 planes hi + lo = bf16(x), bf16(x - hi): 16 significant bits
-//   plan       (many tokens) the tokens ordered by adapter, and work items of up to 64 tokens of one adapter
-//   down-rank  s[t][r] = A_a[r] . x[t] for each token's own adapter, fp32, summed over a few K splits by the reader
+//   plan       (many tokens) the tokens ordered by adapter, and work items of up to 16 tokens of one adapter
+//   down-rank  s[t][r] = c_a (A_a[r] . x[t]) for each token's own adapter, as two bf16 parts
 //   gate/up    weight rows x tokens; the adapters' B_a s in the epilogue; SwiGLU; h as one bf16 plane (bf16 result)
 //              or two (fp32 result, whose error then stays near 2^-17)
 //   down       the same product with Wd and h
@@ -60,22 +60,9 @@ __device__ __forceinline__ int adapter_at(const SharedArgs &a, int pos) {
     return (unsigned)id < (unsigned)a.n ? id : -1;
 }
 
-// Eight columns j8*8.. of the down-rank result of row `pos` (projection `proj` of `np`), scaled, as bf16 hi and lo.
-__device__ __forceinline__ void low_rank8(const SharedArgs &a, const float *s, int np, int pos, int proj, int j8,
-                                          float scale, int rank, uint4 &hi, uint4 &lo) {
-    float v[8] = {};
-    for (int k = 0; k < a.ks; ++k) {
-        const float4 *p = reinterpret_cast<const float4 *>(s + (((int64_t)k * a.T + pos) * np + proj) * a.R + 8 * j8);
-        const float4 x = p[0], y = p[1];
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 8 * j8 + i < rank ? v[i] * scale : 0.f;
-    hi = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = bf16_rest(v[i]);
-    lo = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+// Row `pos` of the low-rank results of projection `proj` of `np`: [hi, lo][R] bf16, scaled, zero from the adapter's rank on.
+__device__ __forceinline__ const uint16_t *low_rank_row(const SharedArgs &a, const uint16_t *s, int np, int pos, int proj) {
+    return s + ((int64_t)pos * np + proj) * 2 * a.R;
 }
 
 // ---------------------------------------------------------------------------
@@ -146,18 +133,19 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// down-rank: s[ks][pos][proj][r] = sum over this K split of A_a[r] . x[pos] for the NP projections that read x.
-// blockIdx.x = item (sorted: of the plan; else the blockIdx.x-th distinct adapter among at most 64 tokens),
-// blockIdx.y = K split; the four waves split K further and their sums meet in LDS.
+// down-rank: s[pos][proj][hi, lo][r] = scale_a (A_a[r] . x[pos]) for the np projections that read x.  One workgroup takes up
+// to 16 tokens of one adapter (blockIdx.x = item; without a plan the blockIdx.x-th distinct adapter among at most 64
+// tokens, and blockIdx.z its group of 16) and FR fragments of 16 of the np * R rows; its sixteen waves split K, and their
+// sums meet in LDS.
 // ---------------------------------------------------------------------------
-constexpr int LR_FRAGS = 8;              // 16-row fragments of [NP][R] per pass
+constexpr int LR_WAVES = 16;
 
-template <int P, bool SORTED>
-__global__ __launch_bounds__(256) void k_low_rank(SharedArgs a, LowRank L) {
-    __shared__ float red[4][LR_FRAGS * 256];
+template <int P, int FR, bool SORTED>
+__global__ __launch_bounds__(64 * LR_WAVES) void k_low_rank(SharedArgs a, LowRank L) {
+    __shared__ float red[LR_WAVES][FR * 256];
     __shared__ int rows[64], meta[2];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, q = lane >> 4;
-    int ad, cnt;
+    int ad, cnt, t0 = 0;
     if constexpr (SORTED) {
         if ((int)blockIdx.x >= *a.n_items) return;
         const int4 it = a.items[blockIdx.x];
@@ -166,13 +154,13 @@ __global__ __launch_bounds__(256) void k_low_rank(SharedArgs a, LowRank L) {
         if ((int)threadIdx.x < cnt) rows[threadIdx.x] = it.y + threadIdx.x;
         __syncthreads();
     } else {
+        t0 = 16 * blockIdx.z;
         if (wave == 0) {
             const int id = adapter_at(a, lane);
             unsigned long long left = __ballot(id >= 0);
             int found = -1, num = 0;
             for (int d = 0; left; ++d) {
-                const int first = __ffsll(left) - 1;
-                const int cur = __shfl(id, first, 64);
+                const int cur = __shfl(id, __ffsll(left) - 1, 64);
                 const unsigned long long same = __ballot(id == cur);
                 if (d == (int)blockIdx.x) {
                     found = cur;
@@ -187,74 +175,147 @@ __global__ __launch_bounds__(256) void k_low_rank(SharedArgs a, LowRank L) {
         __syncthreads();
         ad = meta[0];
         cnt = meta[1];
-        if (ad < 0) return;
+        if (ad < 0 || t0 >= cnt) return;
     }
-    const int K = L.K, R = a.R, nrows = L.np * R, rank = rank_of(a, ad);
-    const int steps = (K + 31) / 32, parts = a.ks * 4, part = blockIdx.y * 4 + wave;
-    const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
-    for (int t0 = 0; t0 < cnt; t0 += 16) {
-        const int pos = rows[min(t0 + i16, cnt - 1)];
-        const int64_t xrow = SORTED && L.gather ? a.perm[pos] : pos;
-        for (int f0 = 0; f0 * 16 < nrows; f0 += LR_FRAGS) {
-            f32x4_t acc[LR_FRAGS];
-            const uint16_t *arow[LR_FRAGS];
+    const int K = L.K, R = a.R, nrows = L.np * R, rank = rank_of(a, ad), f0 = blockIdx.y * FR;
+    const int steps = (K + 31) / 32;
+    const int s0 = steps * wave / LR_WAVES, s1 = steps * (wave + 1) / LR_WAVES;
+    const int pos = rows[min(t0 + i16, cnt - 1)];
+    const uint16_t *xrow = L.x + (int64_t)(SORTED && L.gather ? a.perm[pos] : pos) * K;
+    const int64_t plane = (int64_t)a.T * K;
+    f32x4_t acc[FR];
+    const uint16_t *arow[FR];
 #pragma unroll
-            for (int f = 0; f < LR_FRAGS; ++f) {
-                acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-                const int rr = (f0 + f) * 16 + i16, proj = rr / R, r = rr - proj * R;
-                arow[f] = rr < nrows && r < rank && L.a[proj] ? L.a[proj] + ((int64_t)ad * R + r) * K : nullptr;
-            }
-            for (int s = s0; s < s1; ++s) {
-                const int k = s * 32 + q * 8;
-                uint4 b[P];
+    for (int f = 0; f < FR; ++f) {
+        acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        const int rr = (f0 + f) * 16 + i16, proj = rr / R, r = rr - proj * R;
+        arow[f] = rr < nrows && r < rank && L.a[proj] ? L.a[proj] + ((int64_t)ad * R + r) * K : nullptr;
+    }
+    constexpr int U = 4;
+    for (int s = s0; s < s1; s += U) {
+        uint4 b[U][P], w[U][FR];
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    b[p] = k < K ? load16(L.x + ((int64_t)p * a.T + xrow) * K + k) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < U; ++j) {
+            const int k = (s + j) * 32 + q * 8;
+            const bool in = s + j < s1 && k < K;
 #pragma unroll
-                for (int f = 0; f < LR_FRAGS; ++f) {
-                    if ((f0 + f) * 16 >= nrows) break;
-                    const uint4 w = arow[f] && k < K ? load16(arow[f] + k) : make_uint4(0, 0, 0, 0);
+            for (int f = 0; f < FR; ++f) w[j][f] = in && arow[f] ? load16(arow[f] + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                    for (int p = 0; p < P; ++p) acc[f] = mfma16(w, b[p], acc[f]);
-                }
-            }
-#pragma unroll
-            for (int f = 0; f < LR_FRAGS; ++f)
-                *reinterpret_cast<f32x4_t *>(&red[wave][f * 256 + i16 * 16 + 4 * q]) = acc[f];   // [token][row]
-            __syncthreads();
-            for (int e = threadIdx.x; e < LR_FRAGS * 256; e += 256) {
-                const int f = e >> 8, tok = (e >> 4) & 15, rr = (f0 + f) * 16 + (e & 15);
-                if (t0 + tok < cnt && rr < nrows)
-                    L.s[((int64_t)blockIdx.y * a.T + rows[t0 + tok]) * nrows + rr] =
-                        (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
-            }
-            __syncthreads();
+            for (int p = 0; p < P; ++p) b[j][p] = in ? load16(xrow + p * plane + k) : make_uint4(0, 0, 0, 0);
         }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+            for (int f = 0; f < FR; ++f)
+#pragma unroll
+                for (int p = 0; p < P; ++p) acc[f] = mfma16(w[j][f], b[j][p], acc[f]);
+    }
+#pragma unroll
+    for (int f = 0; f < FR; ++f)
+        *reinterpret_cast<f32x4_t *>(&red[wave][f * 256 + i16 * 16 + 4 * q]) = acc[f];       // [token][row]
+    __syncthreads();
+    const float scale = a.scale ? a.scale[ad] : 1.f;
+    for (int e = threadIdx.x; e < FR * 256; e += 64 * LR_WAVES) {
+        const int f = e >> 8, tok = (e >> 4) & 15, rr = (f0 + f) * 16 + (e & 15);
+        if (t0 + tok >= cnt || rr >= nrows) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < LR_WAVES; ++w) v += red[w][e];
+        v *= scale;
+        const int proj = rr / R, r = rr - proj * R;
+        uint16_t *o = L.s + ((int64_t)rows[t0 + tok] * L.np + proj) * 2 * R + r;
+        o[0] = __builtin_bit_cast(uint16_t, (__bf16)v);
+        o[R] = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(v));
     }
 }
 
 // ---------------------------------------------------------------------------
 // Few tokens: one workgroup streams 16 weight rows (gate/up: 8 gate rows and the same 8 of up) once, straight into
-// the matrix instruction's operand registers; its eight waves split K and their sums meet in LDS.
+// the matrix instruction's operand registers; its sixteen waves split K, and the adapters' terms in units of 32 of an
+// adapter's rank values, whose first operands are loaded ahead of the weights.  All sums meet in LDS.
 // ---------------------------------------------------------------------------
-template <bool GU, int P, int TF>
-__global__ __launch_bounds__(512) void k_few(SharedArgs a, Product g) {
-    __shared__ float red[8][TF][16][17];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, q = lane >> 4;
+constexpr int FEW_WAVES = 16;
+
+template <bool GU, int P, int TF, bool AD>
+__global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g) {
+    constexpr int NW = FEW_WAVES;
+    __shared__ float red[NW][TF][16][17];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
     const int K = g.K, r0 = blockIdx.x * (GU ? 8 : 16);
     const int wr = GU ? r0 + (i16 & 7) : r0 + i16;
+    f32x4_t acc[TF];
+#pragma unroll
+    for (int f = 0; f < TF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    // Unit (adapter ad, cg) covers columns 32 cg .. 32 cg + 31 of [gate, up][R] and belongs to wave (ad * CG + cg) % 16, so
+    // a token's sum has the same order whatever else is in the batch.
+    constexpr int NB = TF == 4 ? 1 : 2;                              // units in flight
+    const int c8 = AD ? a.R / 8 : 1, chunks = GU ? 2 * c8 : c8, CG = (chunks + 3) / 4;
+    int id64 = -1, cg0 = 0, turn = 0, idf[TF];
+    bool first = false;                                              // the first token of its adapter
+    unsigned long long units = 0;
+    uint4 uw[NB], hi[NB][TF], lo[NB][TF];
+    int ad[NB];
+    auto load_units = [&]() {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            uw[b] = make_uint4(0, 0, 0, 0);
+            ad[b] = -1;
+#pragma unroll
+            for (int f = 0; f < TF; ++f) hi[b][f] = lo[b][f] = uw[b];
+            if (!units) continue;
+            const int l = __ffsll(units) - 1;
+            units &= units - 1;
+            ad[b] = __shfl(id64, l, 64);
+            const int c = 4 * (__shfl(cg0, l, 64) + NW * turn) + q, proj = c / c8, j8 = c - proj * c8;
+            if (c < chunks && g.b[proj]) {
+                if ((!GU || (i16 >> 3) == proj) && wr < g.N)
+                    uw[b] = keep_first(load16(g.b[proj] + ((int64_t)ad[b] * g.N + wr) * a.R + 8 * j8),
+                                       rank_of(a, ad[b]) - 8 * j8);
+#pragma unroll
+                for (int f = 0; f < TF; ++f)
+                    if (idf[f] == ad[b]) {
+                        const uint16_t *s = low_rank_row(a, g.s, GU ? 2 : 1, f * 16 + i16, proj) + 8 * j8;
+                        hi[b][f] = load16(s);
+                        lo[b][f] = load16(s + a.R);
+                    }
+            }
+        }
+    };
+    auto add_units = [&]() {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int f = 0; f < TF; ++f) {
+                f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+                d = mfma16(uw[b], hi[b][f], d);
+                d = mfma16(uw[b], lo[b][f], d);
+                if (ad[b] >= 0 && idf[f] == ad[b]) acc[f] += d;
+            }
+    };
+    if constexpr (AD) {
+        id64 = adapter_at(a, lane);
+        for (unsigned long long left = __ballot(id64 >= 0); left;) {
+            const int l = __ffsll(left) - 1, cur = __shfl(id64, l, 64);
+            first |= lane == l;
+            left &= ~__ballot(id64 == cur);
+        }
+#pragma unroll
+        for (int f = 0; f < TF; ++f) idf[f] = __shfl(id64, f * 16 + i16, 64);
+        cg0 = (wave - id64 * CG) & (NW - 1);
+        units = __ballot(first && cg0 < CG);
+        load_units();
+    }
+
     const uint16_t *wrow = (GU && i16 >= 8 ? g.w[1] : g.w[0]) + (int64_t)min(wr, g.N - 1) * K;
     const int steps = (K + 31) / 32;
-    const int s0 = steps * wave / 8, s1 = steps * (wave + 1) / 8;
-    f32x4_t acc[TF];
+    const int s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
     const uint16_t *xrow[TF];
 #pragma unroll
-    for (int f = 0; f < TF; ++f) {
-        acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        xrow[f] = g.x + (int64_t)min(f * 16 + i16, a.T - 1) * K;
-    }
+    for (int f = 0; f < TF; ++f) xrow[f] = g.x + (int64_t)min(f * 16 + i16, a.T - 1) * K;
     const int64_t plane = (int64_t)a.T * K;
-    constexpr int U = TF == 1 ? 8 : 4;
+    // U steps' weights are in flight at once; the activations (from the caches) XU steps at a time
+    constexpr int U = 8, XU = TF * P == 1 ? 8 : TF * P == 2 ? 4 : TF * P == 4 ? 2 : 1;
     for (int s = s0; s < s1; s += U) {
         uint4 w[U];
 #pragma unroll
@@ -263,42 +324,35 @@ __global__ __launch_bounds__(512) void k_few(SharedArgs a, Product g) {
             w[j] = s + j < s1 && k < K ? load16(wrow + k) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int k = (s + j) * 32 + q * 8;
-            const bool in = s + j < s1 && k < K;
+        for (int j0 = 0; j0 < U; j0 += XU) {
+            uint4 x[XU][TF][P];
 #pragma unroll
-            for (int f = 0; f < TF; ++f)
+            for (int j = 0; j < XU; ++j) {
+                const int k = (s + j0 + j) * 32 + q * 8;
+                const bool in = s + j0 + j < s1 && k < K;
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    acc[f] = mfma16(w[j], in ? load16(xrow[f] + p * plane + k) : make_uint4(0, 0, 0, 0), acc[f]);
+                for (int f = 0; f < TF; ++f)
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        x[j][f][p] = in ? load16(xrow[f] + p * plane + k) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < XU; ++j)
+#pragma unroll
+                for (int f = 0; f < TF; ++f)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) acc[f] = mfma16(w[j0 + j], x[j][f][p], acc[f]);
         }
     }
-    if (a.n) {
-        // adapter a is added by wave a % 8: a token's sum has the same order whatever else is in the batch
-        const int c8 = a.R / 8, chunks = GU ? 2 * c8 : c8;
-#pragma unroll
-        for (int f = 0; f < TF; ++f) {
-            const int pos = f * 16 + i16, id = adapter_at(a, pos);
-            unsigned long long left = __ballot(id >= 0 && (id & 7) == wave);
-            while (left) {
-                const int ad = __shfl(id, __ffsll(left) - 1, 64);
-                left &= ~__ballot(id == ad);
-                const float scale = a.scale ? a.scale[ad] : 1.f;
-                const int rank = rank_of(a, ad);
-                f32x4_t d = {0.f, 0.f, 0.f, 0.f};
-                for (int c0 = 0; c0 < chunks; c0 += 4) {
-                    const int c = c0 + q, proj = c / c8, j8 = c - proj * c8;
-                    uint4 w = make_uint4(0, 0, 0, 0), hi = w, lo = w;
-                    if (c < chunks && 8 * j8 < rank && g.b[proj]) {
-                        if ((!GU || (i16 >> 3) == proj) && wr < g.N)
-                            w = keep_first(load16(g.b[proj] + ((int64_t)ad * g.N + wr) * a.R + 8 * j8), rank - 8 * j8);
-                        if (id == ad) low_rank8(a, g.s, GU ? 2 : 1, pos, proj, j8, scale, rank, hi, lo);
-                    }
-                    d = mfma16(w, hi, d);
-                    d = mfma16(w, lo, d);
-                }
-                if (id == ad) acc[f] += d;
+    if constexpr (AD) {
+        add_units();
+        for (;;) {
+            while (units) {
+                load_units();
+                add_units();
             }
+            if (++turn * NW >= CG) break;
+            units = __ballot(first && cg0 + NW * turn < CG);
         }
     }
 #pragma unroll
@@ -307,17 +361,17 @@ __global__ __launch_bounds__(512) void k_few(SharedArgs a, Product g) {
         for (int v = 0; v < 4; ++v) red[wave][f][i16][4 * q + v] = acc[f][v];       // [token][row]
     __syncthreads();
     constexpr int NR = GU ? 8 : 16;
-    for (int e = threadIdx.x; e < TF * 16 * NR; e += 512) {
+    for (int e = threadIdx.x; e < TF * 16 * NR; e += 64 * NW) {
         const int r = e % NR, tok = e / NR, f = tok >> 4, c = tok & 15;
         if (tok >= a.T || r0 + r >= g.N) continue;
         float y = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) y += red[w][f][c][r];
+        for (int w = 0; w < NW; ++w) y += red[w][f][c][r];
         const int64_t o = (int64_t)tok * g.N + r0 + r;
         if constexpr (GU) {
             float up = 0.f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) up += red[w][f][c][r + 8];
+            for (int w = 0; w < NW; ++w) up += red[w][f][c][r + 8];
             const float h = silu_mul(y, up);
             g.h[o] = __builtin_bit_cast(uint16_t, (__bf16)h);
             if (g.hp == 2) g.h[(int64_t)a.T * g.N + o] = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(h));
@@ -466,50 +520,77 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
     }
     wait_stage<0>();
     // D: lane holds token i32 of a fragment, weight rows 8 * (v / 4) + 4 * hh + v % 4
-    const int np = GU ? 2 : 1;
+    if (a.n) {
+        // One adapter of 64 of this wave's tokens at a time, in accumulators of its own.  Rank values go 16 at a time, each
+        // once with the high and once with the low part of the token's low-rank result.
+        constexpr int NP = GU ? 2 : 1, JG = FT < 2 ? FT : 2;
+#pragma unroll
+        for (int jg = 0; jg < FT; jg += JG) {
+            int idj[JG];
+            unsigned long long left[JG];
+#pragma unroll
+            for (int j = 0; j < JG; ++j) {
+                idj[j] = adapter_at(a, t0 + (rt - BW) + (jg + j) * 32 + i32);
+                left[j] = __ballot(idj[j] >= 0);
+            }
+#pragma unroll
+            for (int j0 = 0; j0 < JG; ++j0)
+                while (left[j0]) {
+                    const int ad = __shfl(idj[j0], __ffsll(left[j0]) - 1, 64);
+#pragma unroll
+                    for (int j = 0; j < JG; ++j) left[j] &= ~__ballot(idj[j] == ad);
+                    const int rank = rank_of(a, ad);
+                    f32x16_t d[FW][JG];
+#pragma unroll
+                    for (int i = 0; i < FW; ++i)
+#pragma unroll
+                        for (int j = 0; j < JG; ++j)
+#pragma unroll
+                            for (int v = 0; v < 16; ++v) d[i][j][v] = 0.f;
+                    for (int c0 = 0; 8 * c0 < rank; c0 += 2) {
+                        const int j8 = c0 + hh;
+                        const bool in = 8 * j8 < rank;
+                        uint4 w[FW], u[JG][NP][2];
+#pragma unroll
+                        for (int i = 0; i < FW; ++i) {
+                            const int m = GU ? i & 1 : 0;
+                            const int wr = GU ? w0 + (rw >> 6) * 32 + i32 : w0 + rw + i * 32 + i32;
+                            w[i] = make_uint4(0, 0, 0, 0);
+                            if (in && wr < g.N && g.b[m]) w[i] = load16(g.b[m] + ((int64_t)ad * g.N + wr) * a.R + 8 * j8);
+                        }
+#pragma unroll
+                        for (int j = 0; j < JG; ++j)
+#pragma unroll
+                            for (int p = 0; p < NP; ++p) {
+                                u[j][p][0] = u[j][p][1] = make_uint4(0, 0, 0, 0);
+                                if (in && idj[j] == ad && g.b[p]) {
+                                    const int pos = t0 + (rt - BW) + (jg + j) * 32 + i32;
+                                    const uint16_t *s = low_rank_row(a, g.s, NP, pos, p) + 8 * j8;
+                                    u[j][p][0] = load16(s);
+                                    u[j][p][1] = load16(s + a.R);
+                                }
+                            }
+#pragma unroll
+                        for (int i = 0; i < FW; ++i) {
+                            if (rank - 8 * c0 < 16) w[i] = keep_first(w[i], rank - 8 * j8);
+#pragma unroll
+                            for (int j = 0; j < JG; ++j)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) d[i][j] = mfma32(w[i], u[j][GU ? i & 1 : 0][h], d[i][j]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < JG; ++j)
+                        if (idj[j] == ad) {
+#pragma unroll
+                            for (int i = 0; i < FW; ++i) acc[i][jg + j] += d[i][j];
+                        }
+                }
+        }
+    }
 #pragma unroll
     for (int j = 0; j < FT; ++j) {
         const int pos = t0 + (rt - BW) + j * 32 + i32;
-        if (a.n) {
-            const int id = adapter_at(a, pos);
-            unsigned long long left = __ballot(id >= 0);
-            while (left) {
-                const int ad = __shfl(id, __ffsll(left) - 1, 64);
-                left &= ~__ballot(id == ad);
-                const float scale = a.scale ? a.scale[ad] : 1.f;
-                const int rank = rank_of(a, ad);
-                f32x16_t d[FW];
-#pragma unroll
-                for (int i = 0; i < FW; ++i)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) d[i][v] = 0.f;
-                for (int c0 = 0; 8 * c0 < rank; c0 += 2) {
-                    const int j8 = c0 + hh;
-                    const bool in = 8 * j8 < rank;
-                    uint4 hi[2], lo[2];
-#pragma unroll
-                    for (int p = 0; p < np; ++p) {
-                        hi[p] = lo[p] = make_uint4(0, 0, 0, 0);
-                        if (in && id == ad && g.b[p])
-                            low_rank8(a, g.s, np, pos, p, j8, scale, rank, hi[p], lo[p]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < FW; ++i) {
-                        const int m = GU ? i & 1 : 0;
-                        const int wr = GU ? w0 + (rw >> 6) * 32 + i32 : w0 + rw + i * 32 + i32;
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (in && wr < g.N && g.b[m])
-                            w = keep_first(load16(g.b[m] + ((int64_t)ad * g.N + wr) * a.R + 8 * j8), rank - 8 * j8);
-                        d[i] = mfma32(w, hi[m], d[i]);
-                        d[i] = mfma32(w, lo[m], d[i]);
-                    }
-                }
-                if (id == ad) {
-#pragma unroll
-                    for (int i = 0; i < FW; ++i) acc[i][j] += d[i];
-                }
-            }
-        }
         if (pos >= a.T) continue;
         if constexpr (GU) {
             const int64_t row = (int64_t)pos * g.N;
@@ -546,16 +627,19 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
     }
 }
 
+template <bool GU, int P, bool AD>
+hipError_t launch_few(const SharedArgs &a, const Product &g, hipStream_t st) {
+    const dim3 grd((unsigned)((g.N + (GU ? 7 : 15)) / (GU ? 8 : 16))), blk(64 * FEW_WAVES);
+    if (a.T <= 16) hipLaunchKernelGGL((k_few<GU, P, 1, AD>), grd, blk, 0, st, a, g);
+    else if (a.T <= 32) hipLaunchKernelGGL((k_few<GU, P, 2, AD>), grd, blk, 0, st, a, g);
+    else hipLaunchKernelGGL((k_few<GU, P, 4, AD>), grd, blk, 0, st, a, g);
+    return hipGetLastError();
+}
+
 template <bool GU, int P>
 hipError_t launch_product(const SharedArgs &a, const Product &g, hipStream_t st) {
     const int T = a.T;
-    if (T <= FEW_TOKENS) {
-        const dim3 grd((unsigned)((g.N + (GU ? 7 : 15)) / (GU ? 8 : 16))), blk(512);
-        if (T <= 16) hipLaunchKernelGGL((k_few<GU, P, 1>), grd, blk, 0, st, a, g);
-        else if (T <= 32) hipLaunchKernelGGL((k_few<GU, P, 2>), grd, blk, 0, st, a, g);
-        else hipLaunchKernelGGL((k_few<GU, P, 4>), grd, blk, 0, st, a, g);
-        return hipGetLastError();
-    }
+    if (T <= FEW_TOKENS) return a.n ? launch_few<GU, P, true>(a, g, st) : launch_few<GU, P, false>(a, g, st);
     const int rows = GU ? BW / 2 : BW, tw = (g.N + rows - 1) / rows;
     const dim3 blk(256);
     auto tiles = [&](int bt) { return tw * ((T + bt - 1) / bt); };
@@ -570,13 +654,17 @@ hipError_t launch_product(const SharedArgs &a, const Product &g, hipStream_t st)
 
 template <int P>
 hipError_t launch_low_rank(const SharedArgs &a, const LowRank &L, hipStream_t st) {
-    const int nd = a.T < a.n ? a.T : a.n;
-    if (a.sorted) {
-        const dim3 grd((unsigned)(a.T / ITEM_TOKENS + nd), (unsigned)a.ks);
-        hipLaunchKernelGGL((k_low_rank<P, true>), grd, dim3(256), 0, st, a, L);
-    } else {
-        hipLaunchKernelGGL((k_low_rank<P, false>), dim3((unsigned)nd, (unsigned)a.ks), dim3(256), 0, st, a, L);
-    }
+    // few items: one fragment per workgroup, so that more CUs share the adapters' rows; else several, so that a token's row is
+    // read fewer times
+    const int nd = a.T < a.n ? a.T : a.n, frags = (L.np * a.R + 15) / 16;
+    constexpr int FR = P == 1 ? 4 : 2;
+    const dim3 blk(64 * LR_WAVES);
+    if (a.sorted)
+        hipLaunchKernelGGL((k_low_rank<P, FR, true>), dim3((unsigned)(a.T / ITEM_TOKENS + nd), (unsigned)((frags + FR - 1) / FR)),
+                           blk, 0, st, a, L);
+    else
+        hipLaunchKernelGGL((k_low_rank<P, 1, false>), dim3((unsigned)nd, (unsigned)frags, (unsigned)((a.T + 15) / 16)), blk,
+                           0, st, a, L);
     return hipGetLastError();
 }
 
@@ -586,7 +674,7 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 struct Layout {
     size_t x, perm, ad, items, n_items, s, h, total;
 };
-Layout layout(int T, int H, int Is, int n, int R, int ks, bool x_f32, int hp) {
+Layout layout(int T, int H, int Is, int n, int R, bool x_f32, int hp) {
     Layout l;
     size_t o = 0;
     auto take = [&](size_t b) { const size_t at = o; o += up256(b); return at; };
@@ -597,19 +685,10 @@ Layout layout(int T, int H, int Is, int n, int R, int ks, bool x_f32, int hp) {
     l.ad = take(sorted ? (size_t)T * 4 : 0);
     l.items = take(sorted ? ((size_t)T / ITEM_TOKENS + nd) * 16 : 0);
     l.n_items = take(sorted ? 4 : 0);
-    l.s = take(n > 0 ? (size_t)ks * T * 2 * R * 4 : 0);      // gate/up's, then down's
+    l.s = take(n > 0 ? (size_t)T * 2 * 2 * R * 2 : 0);      // gate/up's, then down's
     l.h = take((size_t)T * Is * 2 * hp);
     l.total = o;
     return l;
-}
-
-// K splits of the down-rank products: enough workgroups for the 256 CUs, at most 8 partial sums for the reader.
-int low_rank_splits(int T, int n) {
-    if (!n) return 0;
-    const int nd = T < n ? T : n, items = T > FEW_TOKENS ? T / ITEM_TOKENS + nd : nd;
-    int ks = 1;
-    while (ks < 8 && ks * items < 256) ks *= 2;
-    return ks;
 }
 
 }  // namespace
@@ -618,15 +697,14 @@ namespace moe {
 
 size_t shared_workspace(int T, int H, int Is, int n, int R) {
     // the largest over the activation and result types, so that one buffer serves every call of these sizes
-    return layout(T, H, Is, n, R, low_rank_splits(T, n), true, 2).total;
+    return layout(T, H, Is, n, R, true, 2).total;
 }
 
 hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     char *base = static_cast<char *>(ws);
     const int hp = a.out_bf16 ? 1 : 2;
-    a.ks = low_rank_splits(a.T, a.n);
     a.sorted = a.n > 0 && a.T > FEW_TOKENS;
-    const Layout l = layout(a.T, a.H, a.Is, a.n, a.R, a.ks, !a.x_bf16, hp);
+    const Layout l = layout(a.T, a.H, a.Is, a.n, a.R, !a.x_bf16, hp);
     const uint16_t *x = static_cast<const uint16_t *>(a.x);
     hipError_t e;
     if (!a.x_bf16) {
@@ -645,7 +723,7 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
         hipLaunchKernelGGL(k_plan, dim3(1), dim3(PLAN_THREADS), 0, st, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    float *s = reinterpret_cast<float *>(base + l.s);
+    uint16_t *s = reinterpret_cast<uint16_t *>(base + l.s);
     uint16_t *h = reinterpret_cast<uint16_t *>(base + l.h);
     LowRank lx = {x, a.H, 2, 1, {a.gate_a, a.up_a}, s}, lh = {h, a.Is, 1, 0, {a.down_a, nullptr}, s};
     Product gu = {}, dn = {};

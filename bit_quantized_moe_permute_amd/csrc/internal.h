@@ -103,7 +103,7 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t st);
 // ffn_shared.hip: the shared expert with low-rank adapters
 constexpr int MAX_ADAPTERS = 4096, MAX_RANK = 256;
 constexpr int FEW_TOKENS = 64;           // up to here the weight rows stream past all tokens at once
-constexpr int ITEM_TOKENS = 64;          // tokens of one adapter per work item of the down-rank products
+constexpr int ITEM_TOKENS = 16;          // tokens of one adapter per work item of the down-rank products
 struct SharedArgs {
     int T, H, Is;
     const void *x;
@@ -117,7 +117,7 @@ struct SharedArgs {
     void *out;
     int out_bf16;
     // filled by the launcher
-    int ks, sorted;
+    int sorted;
     int32_t *perm, *plan_ad, *n_items;   // sorted position -> token, its adapter (-1: none)
     int4 *items;                         // adapter, first sorted position, tokens
 };
@@ -126,13 +126,13 @@ struct LowRank {
     int K, np;
     int gather;                          // rows of x are tokens (through perm), not sorted positions
     const uint16_t *a[2];
-    float *s;                            // [ks][T][np][R]
+    uint16_t *s;                         // [T][np][hi, lo][R]
 };
 struct Product {
     const uint16_t *x;                   // [P][T][K] bf16 planes
     int K, N, gather;
     const uint16_t *w[2], *b[2];
-    const float *s;
+    const uint16_t *s;                   // [T][np][hi, lo][R]
     uint16_t *h;                         // gate/up: [hp][T][N] bf16 planes, by sorted position
     int hp;
     void *out;                           // down: [T][N], by token
