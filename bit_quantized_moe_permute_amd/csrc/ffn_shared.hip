@@ -7,7 +7,7 @@
 //
 //   split      fp32 activations as two bf16 planes hi + lo = bf16(x), bf16(x - hi): 16 significant bits
 //   plan       (many tokens) the tokens ordered by adapter, and work items of up to 16 tokens of one adapter
-//   down-rank  s[t][r] = c_a (A_a[r] . x[t]) for each token's own adapter, as two bf16 parts
+//   down-rank  s[t][r] = c_a (A_a[r] . x[t]) for each token's own adapter, in fp32 or (many tokens) as two bf16 parts
 //   gate/up    weight rows x tokens; the adapters' B_a s in the epilogue; SwiGLU; h as one bf16 plane (bf16 result)
 //              or two (fp32 result, whose error then stays near 2^-17)
 //   down       the same product with Wd and h
@@ -40,6 +40,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b});
 }
 __device__ __forceinline__ float bf16_rest(float a) { return a - (float)(__bf16)a; }
+
+// c + sum of eight products of bf16 values, fp32
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float c) {
+    c = dot2_bf16(__builtin_bit_cast(bf16x2_t, a.x), __builtin_bit_cast(bf16x2_t, b.x), c);
+    c = dot2_bf16(__builtin_bit_cast(bf16x2_t, a.y), __builtin_bit_cast(bf16x2_t, b.y), c);
+    c = dot2_bf16(__builtin_bit_cast(bf16x2_t, a.z), __builtin_bit_cast(bf16x2_t, b.z), c);
+    return dot2_bf16(__builtin_bit_cast(bf16x2_t, a.w), __builtin_bit_cast(bf16x2_t, b.w), c);
+}
 
 // The first `n` of eight bf16 values, the others zero.
 __device__ __forceinline__ uint4 keep_first(uint4 v, int n) {
@@ -85,14 +93,33 @@ __global__ __launch_bounds__(256) void k_split(const float *__restrict__ x, uint
 constexpr int PLAN_THREADS = 1024;
 
 __global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a) {
-    __shared__ int count[MAX_ADAPTERS + 1], wsum[2][PLAN_THREADS / 64];
+    __shared__ int count[MAX_ADAPTERS + 1], begin[MAX_ADAPTERS + 2], item0[MAX_ADAPTERS + 1], wsum[2][PLAN_THREADS / 64];
     const int n = a.n, tid = threadIdx.x;
     for (int i = tid; i <= n; i += PLAN_THREADS) count[i] = 0;
+    constexpr int HELD = 4;                                          // tokens per thread whose bin stays in a register
+    int bin[HELD];
+    auto bin_of = [&](int t) {
+        const int id = t < a.T ? a.token_adapter[t] : -1;
+        return (unsigned)id < (unsigned)n ? id : n;
+    };
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) bin[j] = bin_of(tid + j * PLAN_THREADS);
     __syncthreads();
-    for (int t = tid; t < a.T; t += PLAN_THREADS) {
-        const int id = a.token_adapter[t];
-        atomicAdd(&count[(unsigned)id < (unsigned)n ? id : n], 1);
-    }
+    // a wave whose tokens all have one bin (runs of one request) adds once
+    auto add = [&](int t, int b) -> int {
+        const unsigned long long in = __ballot(t < a.T);
+        if (in == 0) return 0;
+        const int b0 = __builtin_amdgcn_readfirstlane(b);
+        if (__ballot(t < a.T && b != b0) == 0) {
+            int base = 0;
+            if ((tid & 63) == 0) base = atomicAdd(&count[b0], __popcll(in));
+            return __builtin_amdgcn_readfirstlane(base) + (tid & 63);
+        }
+        return t < a.T ? atomicAdd(&count[b], 1) : 0;
+    };
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) add(tid + j * PLAN_THREADS, bin[j]);
+    for (int t = tid + HELD * PLAN_THREADS; t - tid < a.T; t += PLAN_THREADS) add(t, bin_of(t));
     __syncthreads();
     constexpr int PER = MAX_ADAPTERS / PLAN_THREADS + 1;             // consecutive bins per thread
     int c[PER], tok = 0, it = 0;
@@ -116,72 +143,86 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a) {
     for (int j = 0; j < PER; ++j) {
         const int b = tid * PER + j;
         if (b > n) break;
-        count[b] = btok;                                             // becomes the bin's cursor
-        if (b < n)
-            for (int s = 0; s < c[j]; s += ITEM_TOKENS)
-                a.items[bit++] = make_int4(b, btok + s, min(ITEM_TOKENS, c[j] - s), 0);
+        count[b] = begin[b] = btok;                                  // the bin's cursor, its first position, its first item
+        item0[b] = bit;
         btok += c[j];
+        if (b < n) bit += (c[j] + ITEM_TOKENS - 1) / ITEM_TOKENS;
+        if (b == n) begin[n + 1] = btok;
     }
     if (tid == PLAN_THREADS - 1) *a.n_items = bit;
     __syncthreads();
-    for (int t = tid; t < a.T; t += PLAN_THREADS) {
-        const int id = a.token_adapter[t], b = (unsigned)id < (unsigned)n ? id : n;
-        const int pos = atomicAdd(&count[b], 1);
+    auto place = [&](int t, int b) {
+        const int pos = add(t, b);
+        if (t >= a.T) return;
         a.perm[pos] = t;
         a.plan_ad[pos] = b < n ? b : -1;
-    }
+        const int i = pos - begin[b];                                // every ITEM_TOKENS-th position opens an item
+        if (b < n && i % ITEM_TOKENS == 0)
+            a.items[item0[b] + i / ITEM_TOKENS] = make_int4(b, pos, min(ITEM_TOKENS, begin[b + 1] - pos), 0);
+    };
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) place(tid + j * PLAN_THREADS, bin[j]);
+    for (int t = tid + HELD * PLAN_THREADS; t - tid < a.T; t += PLAN_THREADS) place(t, bin_of(t));
 }
 
 // ---------------------------------------------------------------------------
-// down-rank: s[pos][proj][hi, lo][r] = scale_a (A_a[r] . x[pos]) for the np projections that read x.  One workgroup takes up
-// to 16 tokens of one adapter (blockIdx.x = item; without a plan the blockIdx.x-th distinct adapter among at most 64
-// tokens, and blockIdx.z its group of 16) and FR fragments of 16 of the np * R rows; its sixteen waves split K, and their
-// sums meet in LDS.
+// Few tokens, down-rank: s[t][proj][r] = scale_a (A_a[r] . x[t]) in fp32, one wave per (token, row): no wait but that for the
+// token's adapter index and that for the row, and no exchange but the wave's own sum.
+// ---------------------------------------------------------------------------
+template <int P>
+__global__ __launch_bounds__(256) void k_low_rank_few(SharedArgs a, LowRank L) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nrows = L.np * a.R, id = blockIdx.x * 4 + wave;
+    if (id >= a.T * nrows) return;
+    const int t = id / nrows, rr = id - t * nrows, proj = rr / a.R, r = rr - proj * a.R;
+    const int ad = adapter_at(a, t);
+    if (ad < 0 || !L.a[proj]) return;                        // not read either
+    const uint16_t *A = L.a[proj] + ((int64_t)ad * a.R + r) * L.K, *x = L.x + (int64_t)t * L.K;
+    const int64_t plane = (int64_t)a.T * L.K;
+    constexpr int U = 8;
+    float acc[P] = {};
+    for (int k0 = 0; k0 < L.K; k0 += U * 512) {
+        uint4 w[U], v[P][U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int k = k0 + j * 512 + lane * 8;
+            w[j] = k < L.K ? load16(A + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int p = 0; p < P; ++p) v[p][j] = k < L.K ? load16(x + p * plane + k) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+            for (int p = 0; p < P; ++p) acc[p] = dot8(w[j], v[p][j], acc[p]);
+    }
+    float y = acc[0];
+    if constexpr (P == 2) y += acc[1];
+    y = wave_sum(y);
+    if (lane == 0)
+        L.s32[(int64_t)id] = r < rank_of(a, ad) ? y * (a.scale ? a.scale[ad] : 1.f) : 0.f;
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens, down-rank: s[pos][proj][hi, lo][r] = scale_a (A_a[r] . x[pos]) for the np projections that read x.  One
+// workgroup takes an item (up to 16 tokens of one adapter) and FR fragments of 16 of the np * R rows; its sixteen waves split
+// K, and their sums meet in LDS.
 // ---------------------------------------------------------------------------
 constexpr int LR_WAVES = 16;
 
-template <int P, int FR, bool SORTED>
+template <int P, int FR>
 __global__ __launch_bounds__(64 * LR_WAVES) void k_low_rank(SharedArgs a, LowRank L) {
     __shared__ float red[LR_WAVES][FR * 256];
-    __shared__ int rows[64], meta[2];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, q = lane >> 4;
-    int ad, cnt, t0 = 0;
-    if constexpr (SORTED) {
-        if ((int)blockIdx.x >= *a.n_items) return;
-        const int4 it = a.items[blockIdx.x];
-        ad = it.x;
-        cnt = it.z;
-        if ((int)threadIdx.x < cnt) rows[threadIdx.x] = it.y + threadIdx.x;
-        __syncthreads();
-    } else {
-        t0 = 16 * blockIdx.z;
-        if (wave == 0) {
-            const int id = adapter_at(a, lane);
-            unsigned long long left = __ballot(id >= 0);
-            int found = -1, num = 0;
-            for (int d = 0; left; ++d) {
-                const int cur = __shfl(id, __ffsll(left) - 1, 64);
-                const unsigned long long same = __ballot(id == cur);
-                if (d == (int)blockIdx.x) {
-                    found = cur;
-                    num = __popcll(same);
-                    if (id == cur) rows[__popcll(same & ((1ull << lane) - 1))] = lane;
-                    break;
-                }
-                left &= ~same;
-            }
-            if (lane == 0) { meta[0] = found; meta[1] = num; }
-        }
-        __syncthreads();
-        ad = meta[0];
-        cnt = meta[1];
-        if (ad < 0 || t0 >= cnt) return;
-    }
-    const int K = L.K, R = a.R, nrows = L.np * R, rank = rank_of(a, ad), f0 = blockIdx.y * FR;
+    // each XCD takes a run of items, and with it few adapters
+    const int per = (gridDim.x + 7) / 8, item = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+    if (item >= *a.n_items) return;
+    const int4 it = a.items[item];
+    const int ad = it.x, cnt = it.z;
+    const int K = L.K, R = a.R, nrows = L.np * R, f0 = blockIdx.y * FR;
     const int steps = (K + 31) / 32;
     const int s0 = steps * wave / LR_WAVES, s1 = steps * (wave + 1) / LR_WAVES;
-    const int pos = rows[min(t0 + i16, cnt - 1)];
-    const uint16_t *xrow = L.x + (int64_t)(SORTED && L.gather ? a.perm[pos] : pos) * K;
+    const int pos = it.y + min(i16, cnt - 1);
+    const uint16_t *xrow = L.x + (int64_t)(L.gather ? a.perm[pos] : pos) * K;
     const int64_t plane = (int64_t)a.T * K;
     f32x4_t acc[FR];
     const uint16_t *arow[FR];
@@ -189,9 +230,9 @@ __global__ __launch_bounds__(64 * LR_WAVES) void k_low_rank(SharedArgs a, LowRan
     for (int f = 0; f < FR; ++f) {
         acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         const int rr = (f0 + f) * 16 + i16, proj = rr / R, r = rr - proj * R;
-        arow[f] = rr < nrows && r < rank && L.a[proj] ? L.a[proj] + ((int64_t)ad * R + r) * K : nullptr;
+        arow[f] = rr < nrows && L.a[proj] ? L.a[proj] + ((int64_t)ad * R + r) * K : nullptr;
     }
-    constexpr int U = 4;
+    constexpr int U = P == 1 ? 8 : 4;
     for (int s = s0; s < s1; s += U) {
         uint4 b[U][P], w[U][FR];
 #pragma unroll
@@ -215,15 +256,16 @@ __global__ __launch_bounds__(64 * LR_WAVES) void k_low_rank(SharedArgs a, LowRan
         *reinterpret_cast<f32x4_t *>(&red[wave][f * 256 + i16 * 16 + 4 * q]) = acc[f];       // [token][row]
     __syncthreads();
     const float scale = a.scale ? a.scale[ad] : 1.f;
+    const int rank = rank_of(a, ad);                         // what lies behind it was read, and is dropped here
     for (int e = threadIdx.x; e < FR * 256; e += 64 * LR_WAVES) {
         const int f = e >> 8, tok = (e >> 4) & 15, rr = (f0 + f) * 16 + (e & 15);
-        if (t0 + tok >= cnt || rr >= nrows) continue;
+        if (tok >= cnt || rr >= nrows) continue;
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < LR_WAVES; ++w) v += red[w][e];
-        v *= scale;
         const int proj = rr / R, r = rr - proj * R;
-        uint16_t *o = L.s + ((int64_t)rows[t0 + tok] * L.np + proj) * 2 * R + r;
+        v = r < rank ? v * scale : 0.f;
+        uint16_t *o = L.s + ((int64_t)(it.y + tok) * L.np + proj) * 2 * R + r;
         o[0] = __builtin_bit_cast(uint16_t, (__bf16)v);
         o[R] = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(v));
     }
@@ -231,83 +273,28 @@ __global__ __launch_bounds__(64 * LR_WAVES) void k_low_rank(SharedArgs a, LowRan
 
 // ---------------------------------------------------------------------------
 // Few tokens: one workgroup streams 16 weight rows (gate/up: 8 gate rows and the same 8 of up) once, straight into
-// the matrix instruction's operand registers; its sixteen waves split K, and the adapters' terms in units of 32 of an
-// adapter's rank values, whose first operands are loaded ahead of the weights.  All sums meet in LDS.
+// the matrix instruction's operand registers; its sixteen waves split K, and their sums meet in LDS.  An adapter's term is
+// formed per token in fp32, wave w taking tokens w, w + 16, ..., lane (row, q) the rank values 8 q .. 8 q + 7 of each 32;
+// their loads go out between the weights' and the activations'.
 // ---------------------------------------------------------------------------
 constexpr int FEW_WAVES = 16;
 
 template <bool GU, int P, int TF, bool AD>
 __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g) {
     constexpr int NW = FEW_WAVES;
-    __shared__ float red[NW][TF][16][17];
+    __shared__ float red[NW][TF][16][17], low[TF * 16][17];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
     const int K = g.K, r0 = blockIdx.x * (GU ? 8 : 16);
-    const int wr = GU ? r0 + (i16 & 7) : r0 + i16;
+    const int wr = GU ? r0 + (i16 & 7) : r0 + i16, half = GU ? i16 >> 3 : 0;
     f32x4_t acc[TF];
 #pragma unroll
     for (int f = 0; f < TF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    // Unit (adapter ad, cg) covers columns 32 cg .. 32 cg + 31 of [gate, up][R] and belongs to wave (ad * CG + cg) % 16, so
-    // a token's sum has the same order whatever else is in the batch.
-    constexpr int NB = TF == 4 ? 1 : 2;                              // units in flight
-    const int c8 = AD ? a.R / 8 : 1, chunks = GU ? 2 * c8 : c8, CG = (chunks + 3) / 4;
-    int id64 = -1, cg0 = 0, turn = 0, idf[TF];
-    bool first = false;                                              // the first token of its adapter
-    unsigned long long units = 0;
-    uint4 uw[NB], hi[NB][TF], lo[NB][TF];
-    int ad[NB];
-    auto load_units = [&]() {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            uw[b] = make_uint4(0, 0, 0, 0);
-            ad[b] = -1;
-#pragma unroll
-            for (int f = 0; f < TF; ++f) hi[b][f] = lo[b][f] = uw[b];
-            if (!units) continue;
-            const int l = __ffsll(units) - 1;
-            units &= units - 1;
-            ad[b] = __shfl(id64, l, 64);
-            const int c = 4 * (__shfl(cg0, l, 64) + NW * turn) + q, proj = c / c8, j8 = c - proj * c8;
-            if (c < chunks && g.b[proj]) {
-                if ((!GU || (i16 >> 3) == proj) && wr < g.N)
-                    uw[b] = keep_first(load16(g.b[proj] + ((int64_t)ad[b] * g.N + wr) * a.R + 8 * j8),
-                                       rank_of(a, ad[b]) - 8 * j8);
-#pragma unroll
-                for (int f = 0; f < TF; ++f)
-                    if (idf[f] == ad[b]) {
-                        const uint16_t *s = low_rank_row(a, g.s, GU ? 2 : 1, f * 16 + i16, proj) + 8 * j8;
-                        hi[b][f] = load16(s);
-                        lo[b][f] = load16(s + a.R);
-                    }
-            }
-        }
-    };
-    auto add_units = [&]() {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int f = 0; f < TF; ++f) {
-                f32x4_t d = {0.f, 0.f, 0.f, 0.f};
-                d = mfma16(uw[b], hi[b][f], d);
-                d = mfma16(uw[b], lo[b][f], d);
-                if (ad[b] >= 0 && idf[f] == ad[b]) acc[f] += d;
-            }
-    };
+    int ad[TF];
     if constexpr (AD) {
-        id64 = adapter_at(a, lane);
-        for (unsigned long long left = __ballot(id64 >= 0); left;) {
-            const int l = __ffsll(left) - 1, cur = __shfl(id64, l, 64);
-            first |= lane == l;
-            left &= ~__ballot(id64 == cur);
-        }
 #pragma unroll
-        for (int f = 0; f < TF; ++f) idf[f] = __shfl(id64, f * 16 + i16, 64);
-        cg0 = (wave - id64 * CG) & (NW - 1);
-        units = __ballot(first && cg0 < CG);
-        load_units();
+        for (int f = 0; f < TF; ++f) ad[f] = adapter_at(a, f * 16 + wave);
     }
-
-    const uint16_t *wrow = (GU && i16 >= 8 ? g.w[1] : g.w[0]) + (int64_t)min(wr, g.N - 1) * K;
+    const uint16_t *wrow = (half ? g.w[1] : g.w[0]) + (int64_t)min(wr, g.N - 1) * K;
     const int steps = (K + 31) / 32;
     const int s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
     const uint16_t *xrow[TF];
@@ -316,13 +303,37 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
     const int64_t plane = (int64_t)a.T * K;
     // U steps' weights are in flight at once; the activations (from the caches) XU steps at a time
     constexpr int U = 8, XU = TF * P == 1 ? 8 : TF * P == 2 ? 4 : TF * P == 4 ? 2 : 1;
-    for (int s = s0; s < s1; s += U) {
-        uint4 w[U];
+    uint4 w[U];
+    auto load_weights = [&](int s) {
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const int k = (s + j) * 32 + q * 8;
             w[j] = s + j < s1 && k < K ? load16(wrow + k) : make_uint4(0, 0, 0, 0);
         }
+    };
+    load_weights(s0);
+    // this lane's part of an adapter's term for token f * 16 + wave, rank values 32 c + 8 q .. + 7
+    uint4 bw[TF];
+    float4 ss[TF][2];
+    auto load_low = [&](int c) {
+        const int r = 32 * c + 8 * q;
+#pragma unroll
+        for (int f = 0; f < TF; ++f) {
+            bw[f] = make_uint4(0, 0, 0, 0);
+            ss[f][0] = ss[f][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (ad[f] >= 0 && r < a.R && wr < g.N && g.b[half]) {
+                bw[f] = load16(g.b[half] + ((int64_t)ad[f] * g.N + wr) * a.R + r);
+                const float4 *p = reinterpret_cast<const float4 *>(
+                    g.s32 + ((int64_t)(f * 16 + wave) * (GU ? 2 : 1) + half) * a.R + r);
+                ss[f][0] = p[0];
+                ss[f][1] = p[1];
+            }
+        }
+    };
+    constexpr bool AHEAD = TF < 4;                           // with 64 tokens the registers do not hold both
+    if constexpr (AD && AHEAD) load_low(0);
+    for (int s = s0; s < s1; s += U) {
+        if (s != s0) load_weights(s);
 #pragma unroll
         for (int j0 = 0; j0 < U; j0 += XU) {
             uint4 x[XU][TF][P];
@@ -345,14 +356,28 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
         }
     }
     if constexpr (AD) {
-        add_units();
-        for (;;) {
-            while (units) {
-                load_units();
-                add_units();
+        float d[TF] = {};
+        for (int c = 0; 32 * c < a.R; ++c) {
+            if (c || !AHEAD) load_low(c);
+#pragma unroll
+            for (int f = 0; f < TF; ++f) {
+                const int rank = ad[f] < 0 ? 0 : rank_of(a, ad[f]) - (32 * c + 8 * q);       // of this lane's eight
+                const uint4 b = keep_first(bw[f], rank);
+                const uint32_t bb[4] = {b.x, b.y, b.z, b.w};
+                const float sv[8] = {ss[f][0].x, ss[f][0].y, ss[f][0].z, ss[f][0].w,
+                                     ss[f][1].x, ss[f][1].y, ss[f][1].z, ss[f][1].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    d[f] = __fmaf_rn(__uint_as_float(bb[i] << 16), sv[2 * i], d[f]);
+                    d[f] = __fmaf_rn(__uint_as_float(bb[i] & 0xFFFF0000u), sv[2 * i + 1], d[f]);
+                }
             }
-            if (++turn * NW >= CG) break;
-            units = __ballot(first && cg0 + NW * turn < CG);
+        }
+#pragma unroll
+        for (int f = 0; f < TF; ++f) {
+            d[f] += __shfl_xor(d[f], 16, 64);
+            d[f] += __shfl_xor(d[f], 32, 64);
+            if (q == 0) low[f * 16 + wave][i16] = d[f];
         }
     }
 #pragma unroll
@@ -364,12 +389,12 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
     for (int e = threadIdx.x; e < TF * 16 * NR; e += 64 * NW) {
         const int r = e % NR, tok = e / NR, f = tok >> 4, c = tok & 15;
         if (tok >= a.T || r0 + r >= g.N) continue;
-        float y = 0.f;
+        float y = AD ? low[tok][r] : 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) y += red[w][f][c][r];
         const int64_t o = (int64_t)tok * g.N + r0 + r;
         if constexpr (GU) {
-            float up = 0.f;
+            float up = AD ? low[tok][r + 8] : 0.f;
 #pragma unroll
             for (int w = 0; w < NW; ++w) up += red[w][f][c][r + 8];
             const float h = silu_mul(y, up);
@@ -385,8 +410,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
 // ---------------------------------------------------------------------------
 // Many tokens: a workgroup of four waves computes 128 weight rows (gate/up: 64 of each) x BT tokens, each wave 64 x BT/2
 // of them; both operands pass through LDS in 64-wide K stages, three of them, filled by direct-to-LDS loads.
-// LDS rows are 128 bytes; 16-byte chunk c of row r lies at position c ^ (r & 7), so eight rows' reads of one chunk
-// column touch all banks once.
+// LDS rows are 128 bytes, half of the 64 banks; 16-byte chunk c of row r lies at position c ^ (r / 2 % 8), so sixteen rows'
+// reads of one chunk column touch every bank once.
 //
 // The loads are written as assembly: the compiler would otherwise wait for all of them before any LDS read.  They
 // have no register outputs; wait_stage() counts them (the kernel has no other vector memory access between the first
@@ -426,7 +451,8 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
 
     // this lane's global rows: load i of this wave fills tile rows 8 * (wave * LOADS + i) .. + 7
     const uint16_t *src[LOADS];
-    const int chunk = (lane & 7) ^ (lane >> 3);
+    static_assert(LOADS % 2 == 0, "");                       // so that load i covers an odd group of eight rows iff i is odd
+    const int chunk0 = (lane & 7) ^ (lane >> 4), chunk1 = chunk0 ^ 4;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
         const int r = 8 * (wave * LOADS + i) + (lane >> 3);
@@ -438,7 +464,7 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
             const int pos = min(t0 + r - BW, a.T - 1);
             src[i] = g.x + (int64_t)(g.gather && a.sorted ? a.perm[pos] : pos) * K;
         }
-        src[i] += 8 * chunk;
+        src[i] += 8 * (i & 1 ? chunk1 : chunk0);
     }
     const int nsteps = (K + BK - 1) / BK * P;
     const int64_t plane = (int64_t)a.T * K;
@@ -448,17 +474,18 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
     // Loads of the next stage to issue: its K offset and plane.  Past the end of the last row, and in stages behind the last,
     // they read zeros, so that every stage has the same number of loads in flight.
     int ik = 0, ip = 0;
-    bool in = 8 * chunk < K;
+    bool in0 = 8 * chunk0 < K, in1 = 8 * chunk1 < K;
     uint32_t idst = lds0;
     auto issue = [&](int i) {                                // i: load of this wave (compile-time)
         const uint16_t *q = src[i] + ik;
         if (P > 1 && (wave * LOADS + i) * 8 >= BW) q += ip ? plane : 0;
-        load_to_lds(in ? q : zeros, idst + i * 1024u);
+        load_to_lds((i & 1 ? in1 : in0) ? q : zeros, idst + i * 1024u);
     };
     auto next_stage = [&]() {
         ik += BK;
         if (P > 1 && ip == 0 && ik >= K) { ik = 0; ip = 1; }
-        in = ik + 8 * chunk < K;
+        in0 = ik + 8 * chunk0 < K;
+        in1 = ik + 8 * chunk1 < K;
         idst = idst == lds0 + (STAGES - 1) * ROWS * 128u ? lds0 : idst + ROWS * 128u;
     };
     f32x16_t acc[FW][FT];
@@ -471,7 +498,7 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
     const int rw = (wave / WT) * FW * 32, rt = BW + (wave % WT) * FT * 32;
     uint4 fw[2][FW], ft[2][FT];
     auto read = [&](const uint4 *t, int kk, int b) {
-        const int c = (2 * kk + hh) ^ (i32 & 7);
+        const int c = (2 * kk + hh) ^ (i32 >> 1 & 7);
 #pragma unroll
         for (int i = 0; i < FW; ++i) fw[b][i] = t[(rw + i * 32 + i32) * 8 + c];
 #pragma unroll
@@ -654,17 +681,14 @@ hipError_t launch_product(const SharedArgs &a, const Product &g, hipStream_t st)
 
 template <int P>
 hipError_t launch_low_rank(const SharedArgs &a, const LowRank &L, hipStream_t st) {
-    // few items: one fragment per workgroup, so that more CUs share the adapters' rows; else several, so that a token's row is
-    // read fewer times
+    if (!a.sorted) {
+        hipLaunchKernelGGL((k_low_rank_few<P>), dim3((unsigned)((a.T * L.np * a.R + 3) / 4)), dim3(256), 0, st, a, L);
+        return hipGetLastError();
+    }
     const int nd = a.T < a.n ? a.T : a.n, frags = (L.np * a.R + 15) / 16;
-    constexpr int FR = P == 1 ? 4 : 2;
-    const dim3 blk(64 * LR_WAVES);
-    if (a.sorted)
-        hipLaunchKernelGGL((k_low_rank<P, FR, true>), dim3((unsigned)(a.T / ITEM_TOKENS + nd), (unsigned)((frags + FR - 1) / FR)),
-                           blk, 0, st, a, L);
-    else
-        hipLaunchKernelGGL((k_low_rank<P, 1, false>), dim3((unsigned)nd, (unsigned)frags, (unsigned)((a.T + 15) / 16)), blk,
-                           0, st, a, L);
+    constexpr int FR = 2;
+    const unsigned items = (unsigned)(a.T / ITEM_TOKENS + nd + 7) / 8 * 8;
+    hipLaunchKernelGGL((k_low_rank<P, FR>), dim3(items, (unsigned)((frags + FR - 1) / FR)), dim3(64 * LR_WAVES), 0, st, a, L);
     return hipGetLastError();
 }
 
@@ -725,12 +749,13 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     }
     uint16_t *s = reinterpret_cast<uint16_t *>(base + l.s);
     uint16_t *h = reinterpret_cast<uint16_t *>(base + l.h);
-    LowRank lx = {x, a.H, 2, 1, {a.gate_a, a.up_a}, s}, lh = {h, a.Is, 1, 0, {a.down_a, nullptr}, s};
+    float *s32 = reinterpret_cast<float *>(s);               // the same place, the same size
+    LowRank lx = {x, a.H, 2, 1, {a.gate_a, a.up_a}, s, s32}, lh = {h, a.Is, 1, 0, {a.down_a, nullptr}, s, s32};
     Product gu = {}, dn = {};
     gu.x = x; gu.K = a.H; gu.N = a.Is; gu.gather = 1;
-    gu.w[0] = a.gate; gu.w[1] = a.up; gu.b[0] = a.gate_b; gu.b[1] = a.up_b; gu.s = s; gu.h = h; gu.hp = hp;
+    gu.w[0] = a.gate; gu.w[1] = a.up; gu.b[0] = a.gate_b; gu.b[1] = a.up_b; gu.s = s; gu.s32 = s32; gu.h = h; gu.hp = hp;
     dn.x = h; dn.K = a.Is; dn.N = a.H; dn.gather = 0;
-    dn.w[0] = a.down; dn.b[0] = a.down_b; dn.s = s; dn.out = a.out; dn.out_bf16 = a.out_bf16;
+    dn.w[0] = a.down; dn.b[0] = a.down_b; dn.s = s; dn.s32 = s32; dn.out = a.out; dn.out_bf16 = a.out_bf16;
     SharedArgs ag = a, ad = a;                              // a half without adapters runs as if there were none
     if (!a.gate_a && !a.up_a) ag.n = 0;
     if (!a.down_a) ad.n = 0;

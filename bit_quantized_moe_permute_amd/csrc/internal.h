@@ -126,13 +126,15 @@ struct LowRank {
     int K, np;
     int gather;                          // rows of x are tokens (through perm), not sorted positions
     const uint16_t *a[2];
-    uint16_t *s;                         // [T][np][hi, lo][R]
+    uint16_t *s;                         // [T][np][hi, lo][R], many tokens
+    float *s32;                          // [T][np][R], few tokens
 };
 struct Product {
     const uint16_t *x;                   // [P][T][K] bf16 planes
     int K, N, gather;
     const uint16_t *w[2], *b[2];
-    const uint16_t *s;                   // [T][np][hi, lo][R]
+    const uint16_t *s;                   // [T][np][hi, lo][R], many tokens
+    const float *s32;                    // [T][np][R], few tokens
     uint16_t *h;                         // gate/up: [hp][T][N] bf16 planes, by sorted position
     int hp;
     void *out;                           // down: [T][N], by token
