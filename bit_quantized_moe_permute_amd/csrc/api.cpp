@@ -575,6 +575,10 @@ static moe_status check_shared(const char *fn, const moe_layer_desc *L, const mo
     if (n_tokens < 1) return fail(MOE_ERR_INVALID_ARG, "%s: n_tokens < 1", fn);
     if (L->hidden < 8 || L->shared_inter < 8 || L->hidden % 8 || L->shared_inter % 8)
         return fail(MOE_ERR_INVALID_ARG, "%s: hidden and shared_inter must be positive multiples of 8", fn);
+    if (L->hidden > MOE_SHARED_MAX_DIM || L->shared_inter > MOE_SHARED_MAX_DIM)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: hidden or shared_inter above %d", fn, MOE_SHARED_MAX_DIM);
+    if ((int64_t)n_tokens * (L->hidden > L->shared_inter ? L->hidden : L->shared_inter) >= (int64_t)1 << 30)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: n_tokens * hidden (or shared_inter) must be below 2^30; split the batch", fn);
     if (!L->shared_gate || !L->shared_up || !L->shared_down)
         return fail(MOE_ERR_INVALID_ARG, "%s: null shared expert weights", fn);
     if (!aligned(L->shared_gate, 16) || !aligned(L->shared_up, 16) || !aligned(L->shared_down, 16))

@@ -23,8 +23,6 @@ namespace {
 
 typedef __attribute__((address_space(3))) void *las_ptr;
 
-__device__ uint4 zero_chunk;             // 16 zero bytes that tiles read past the end of a row
-
 __device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                    0, 0, 0);
@@ -321,8 +319,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
         for (int f = 0; f < TF; ++f) {
             bw[f] = make_uint4(0, 0, 0, 0);
             ss[f][0] = ss[f][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (ad[f] >= 0 && r < a.R && wr < g.N && g.b[half]) {
-                bw[f] = load16(g.b[half] + ((int64_t)ad[f] * g.N + wr) * a.R + r);
+            if (ad[f] >= 0 && r < a.R && wr < g.N && (half ? g.b[1] : g.b[0])) {
+                bw[f] = load16((half ? g.b[1] : g.b[0]) + ((int64_t)ad[f] * g.N + wr) * a.R + r);
                 const float4 *p = reinterpret_cast<const float4 *>(
                     g.s32 + ((int64_t)(f * 16 + wave) * (GU ? 2 : 1) + half) * a.R + r);
                 ss[f][0] = p[0];
@@ -421,18 +419,22 @@ template <int N> __device__ __forceinline__ void wait_stage() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// 64 lanes' 16 bytes at their `src` -> 1 KiB of LDS at byte address `dst` (wave-uniform), in lane order.  The
-// destination goes through m0, which is put back: the compiler may count on its value.
-__device__ __forceinline__ void load_to_lds(const void *src, uint32_t dst) {
+// 64 lanes' 16 bytes at base + off -> 1 KiB of LDS at byte address `dst` (wave-uniform), in lane order.  The destination
+// goes through m0, which is put back: the compiler may count on its value.
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32 |
+           (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+}
+__device__ __forceinline__ void load_to_lds(uint64_t base, uint32_t off, uint32_t dst) {
     uint32_t m0;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off\n\t"
-                 "s_mov_b32 m0, %0"
-                 : "=&s"(m0) : "v"(src), "s"(dst) : "memory");
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0) : "v"(off), "s"(base), "s"(dst) : "memory");
 }
 
 constexpr int BW = 128, BK = 64, STAGES = 3;
 
-template <bool GU, int P, int BT>
+// TAIL: K is no multiple of 64, so a row's last step is not a whole one.
+template <bool GU, int P, int BT, bool TAIL>
 __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles_w, int tiles_t) {
     constexpr int WT = 2;                                    // waves along the tokens, and along the weight rows
     constexpr int FW = BW / 2 / 32, FT = BT / WT / 32;       // 32 x 32 fragments per wave
@@ -449,43 +451,46 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
     const int tw = id / tiles_t, tt = id - tw * tiles_t;
     const int w0 = tw * (GU ? BW / 2 : BW), t0 = tt * BT;
 
-    // this lane's global rows: load i of this wave fills tile rows 8 * (wave * LOADS + i) .. + 7
-    const uint16_t *src[LOADS];
-    static_assert(LOADS % 2 == 0, "");                       // so that load i covers an odd group of eight rows iff i is odd
+    // Load i of this wave fills rows 8 * (wave * LOADS + i) .. + 7 of the tile from one operand (`base`); `off`: byte offset of
+    // this lane's row and chunk from there (launch_shared() keeps them below 2^32).  Rows behind the last repeat it; their
+    // results are not stored.
+    static_assert(LOADS % 2 == 0 && BW / 8 % 2 == 0, "");    // load i covers an odd group of eight rows iff i is odd
     const int chunk0 = (lane & 7) ^ (lane >> 4), chunk1 = chunk0 ^ 4;
+    uint64_t base[LOADS];
+    uint32_t off[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-        const int r = 8 * (wave * LOADS + i) + (lane >> 3);
-        if (r < BW) {
+        const int r8 = 8 * (wave * LOADS + i), r = r8 + (lane >> 3), c = i & 1 ? chunk1 : chunk0;
+        const uint16_t *from = g.x;
+        int row;
+        if (r8 < BW) {
             // gate/up: rows come in 32-row groups gate, up, gate, up so that a wave holds both of the same rows
-            const int m = GU ? (r >> 5) & 1 : 0, wr = GU ? w0 + (r >> 6) * 32 + (r & 31) : w0 + r;
-            src[i] = g.w[m] + (int64_t)min(wr, g.N - 1) * K;
+            row = min(GU ? (r >> 6) * 32 + (r & 31) : r, g.N - 1 - w0);
+            from = (GU && (r8 >> 5 & 1) ? g.w[1] : g.w[0]) + (int64_t)w0 * K;
         } else {
             const int pos = min(t0 + r - BW, a.T - 1);
-            src[i] = g.x + (int64_t)(g.gather && a.sorted ? a.perm[pos] : pos) * K;
+            row = g.gather && a.sorted ? a.perm[pos] : pos;
         }
-        src[i] += 8 * (i & 1 ? chunk1 : chunk0);
+        base[i] = uniform64((uint64_t)(uintptr_t)from);
+        off[i] = 2u * ((uint32_t)row * (uint32_t)K + 8u * c);
     }
-    const int nsteps = (K + BK - 1) / BK * P;
-    const int64_t plane = (int64_t)a.T * K;
+    const int ksteps = (K + BK - 1) / BK, nsteps = ksteps * P;
+    const int tail = K % BK / 8;                             // chunks in a row's last step (TAIL)
     const uint32_t lds0 = (uint32_t)(uintptr_t)(las_ptr)tile + wave * LOADS * 1024u;
-    const uint16_t *zeros = reinterpret_cast<const uint16_t *>(&zero_chunk);
-    asm("" : "+v"(zeros));                                   // kept in registers: a select below, not a branch
-    // Loads of the next stage to issue: its K offset and plane.  Past the end of the last row, and in stages behind the last,
-    // they read zeros, so that every stage has the same number of loads in flight.
-    int ik = 0, ip = 0;
-    bool in0 = 8 * chunk0 < K, in1 = 8 * chunk1 < K;
-    uint32_t idst = lds0;
+    // Loads of the next stage to issue: its step, and the byte offsets of step and plane.  A chunk behind the row's end repeats the
+    // step's first one (its products are masked), and stages behind the last repeat that: every stage has the same
+    // number of loads in flight.
+    int istep = 0;
+    uint32_t iw = 0, ix = 0, idst = lds0;
+    const uint32_t back0 = TAIL && chunk0 >= tail ? 16u * chunk0 : 0u, back1 = TAIL && chunk1 >= tail ? 16u * chunk1 : 0u;
     auto issue = [&](int i) {                                // i: load of this wave (compile-time)
-        const uint16_t *q = src[i] + ik;
-        if (P > 1 && (wave * LOADS + i) * 8 >= BW) q += ip ? plane : 0;
-        load_to_lds((i & 1 ? in1 : in0) ? q : zeros, idst + i * 1024u);
+        uint32_t o = off[i] + ((wave * LOADS + i) * 8 < BW ? iw : ix);
+        if (TAIL && istep == ksteps - 1) o -= i & 1 ? back1 : back0;
+        load_to_lds(base[i], o, idst + i * 1024u);
     };
     auto next_stage = [&]() {
-        ik += BK;
-        if (P > 1 && ip == 0 && ik >= K) { ik = 0; ip = 1; }
-        in0 = ik + 8 * chunk0 < K;
-        in1 = ik + 8 * chunk1 < K;
+        if (istep + 1 < ksteps) { ++istep; iw += 2 * BK; ix += 2 * BK; }
+        else if (P > 1 && ix == iw) { istep = 0; iw = 0; ix = 2u * (uint32_t)a.T * (uint32_t)K; }
         idst = idst == lds0 + (STAGES - 1) * ROWS * 128u ? lds0 : idst + ROWS * 128u;
     };
     f32x16_t acc[FW][FT];
@@ -497,30 +502,31 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
     const int rw = (wave / WT) * FW * 32, rt = BW + (wave % WT) * FT * 32;
     uint4 fw[2][FW], ft[2][FT];
-    auto read = [&](const uint4 *t, int kk, int b) {
+    auto read_one = [&](const uint4 *t, int kk, int b, int n) {      // fragment n of the slice: weights first
         const int c = (2 * kk + hh) ^ (i32 >> 1 & 7);
-#pragma unroll
-        for (int i = 0; i < FW; ++i) fw[b][i] = t[(rw + i * 32 + i32) * 8 + c];
-#pragma unroll
-        for (int j = 0; j < FT; ++j) ft[b][j] = t[(rt + j * 32 + i32) * 8 + c];
+        if (n < FW) fw[b][n] = t[(rw + n * 32 + i32) * 8 + c];
+        else ft[b][n - FW] = t[(rt + (n - FW) * 32 + i32) * 8 + c];
     };
-    // the products of one 16-wide slice, with a quarter of a stage's loads issued among them
-    auto products = [&](int b, int quarter) {
-        constexpr int M = FW * FT;
+    // The products of one 16-wide slice (buffer b).  Between them go the reads of the next slice and a quarter of a stage's
+    // loads, so that the matrix cores have work while these are issued.
+    auto slice = [&](int b, const uint4 *nt, int nkk, int quarter) {
+        constexpr int M = FW * FT, NR = FW + FT;
+        const int l0 = quarter * LOADS / 4, nl = (quarter + 1) * LOADS / 4 - l0;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             acc[m % FW][m / FW] = mfma32(fw[b][m % FW], ft[b][m / FW], acc[m % FW][m / FW]);
-            const int l0 = quarter * LOADS / 4, n = (quarter + 1) * LOADS / 4 - l0;
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+                if (n >= m * 2 * NR / M && n < (m + 1) * 2 * NR / M) read_one(nt, nkk, b ^ 1, n);      // in the first half
 #pragma unroll
             for (int i = 0; i < LOADS; ++i)
-                if (i >= l0 + m * n / M && i < l0 + (m + 1) * n / M) issue(i);
+                if (i >= l0 + m * nl / M && i < l0 + (m + 1) * nl / M) issue(i);                     // towards the end
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // Stages 0 and 1 and the first quarter of stage 2 are loaded ahead.  Fragments of the next slice are read while the
-    // matrix cores work on the present one.  Before a stage's last slice: wait for the next stage (the one after it stays
-    // in flight) and for the workgroup; from then on nobody reads the present stage's buffer, and it takes the loads of
-    // the stage three further on.
+    // Stages 0 and 1 and the first quarter of stage 2 are loaded ahead.  Before a stage's last slice: wait for the next stage
+    // (the one after it stays in flight) and for the workgroup; from then on nobody reads the present stage's buffer, and
+    // it takes the loads of the stage three further on.
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) issue(i);
     next_stage();
@@ -530,20 +536,30 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
 #pragma unroll
     for (int i = 0; i < LOADS / 4; ++i) issue(i);
     wait_stage<LOADS + LOADS / 4>();
-    int rb = 0;
-    read(tile[0], 0, 0);
+    int rb = 0, step = 0;
+#pragma unroll
+    for (int n = 0; n < FW + FT; ++n) read_one(tile[0], 0, 0, n);
     for (int s = 0; s < nsteps; ++s) {
         const uint4 *t = tile[rb];
+        // weights behind the row's end count as zeros; the step's other chunks are masked alike
+        auto mask = [&](int kk, int b) {
+            if (TAIL && step == ksteps - 1) {
+#pragma unroll
+                for (int i = 0; i < FW; ++i)
+                    if (2 * kk + hh >= tail) fw[b][i] = make_uint4(0, 0, 0, 0);
+            }
+        };
 #pragma unroll
         for (int kk = 0; kk < 3; ++kk) {
-            read(t, kk + 1, (kk + 1) & 1);
-            products(kk & 1, kk + 1);
+            mask(kk, kk & 1);
+            slice(kk & 1, t, kk + 1, kk + 1);
         }
         next_stage();
         rb = rb == STAGES - 1 ? 0 : rb + 1;
         wait_stage<LOADS>();
-        read(tile[rb], 0, 0);                                // behind the last stage: zeros, not used
-        products(1, 0);
+        mask(3, 1);
+        slice(1, tile[rb], 0, 0);                            // behind the last stage: a read of old values, not used
+        step = step + 1 == ksteps ? 0 : step + 1;
     }
     wait_stage<0>();
     // D: lane holds token i32 of a fragment, weight rows 8 * (v / 4) + 4 * hh + v % 4
@@ -563,7 +579,7 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
 #pragma unroll
             for (int j0 = 0; j0 < JG; ++j0)
                 while (left[j0]) {
-                    const int ad = __shfl(idj[j0], __ffsll(left[j0]) - 1, 64);
+                    const int ad = __builtin_amdgcn_readlane(idj[j0], __ffsll(left[j0]) - 1);
 #pragma unroll
                     for (int j = 0; j < JG; ++j) left[j] &= ~__ballot(idj[j] == ad);
                     const int rank = rank_of(a, ad);
@@ -663,20 +679,24 @@ hipError_t launch_few(const SharedArgs &a, const Product &g, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <bool GU, int P, bool TAIL>
+hipError_t launch_many(const SharedArgs &a, const Product &g, int bt, int tw, int tt, hipStream_t st) {
+    const dim3 grd((unsigned)((tw * tt + 7) / 8 * 8)), blk(256);
+    if (bt == 256) hipLaunchKernelGGL((k_many<GU, P, 256, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+    else if (bt == 128) hipLaunchKernelGGL((k_many<GU, P, 128, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+    else hipLaunchKernelGGL((k_many<GU, P, 64, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+    return hipGetLastError();
+}
+
 template <bool GU, int P>
 hipError_t launch_product(const SharedArgs &a, const Product &g, hipStream_t st) {
     const int T = a.T;
     if (T <= FEW_TOKENS) return a.n ? launch_few<GU, P, true>(a, g, st) : launch_few<GU, P, false>(a, g, st);
     const int rows = GU ? BW / 2 : BW, tw = (g.N + rows - 1) / rows;
-    const dim3 blk(256);
     auto tiles = [&](int bt) { return tw * ((T + bt - 1) / bt); };
     const int bt = tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
-    const dim3 grd((unsigned)((tiles(bt) + 7) / 8 * 8));
     const int tt = (T + bt - 1) / bt;
-    if (bt == 256) hipLaunchKernelGGL((k_many<GU, P, 256>), grd, blk, 0, st, a, g, tw, tt);
-    else if (bt == 128) hipLaunchKernelGGL((k_many<GU, P, 128>), grd, blk, 0, st, a, g, tw, tt);
-    else hipLaunchKernelGGL((k_many<GU, P, 64>), grd, blk, 0, st, a, g, tw, tt);
-    return hipGetLastError();
+    return g.K % BK ? launch_many<GU, P, true>(a, g, bt, tw, tt, st) : launch_many<GU, P, false>(a, g, bt, tw, tt, st);
 }
 
 template <int P>

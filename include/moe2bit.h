@@ -433,6 +433,7 @@ moe_status moe_combine_norm(const float *slot_out, const float *topk_w, const fl
  *     [n][H][R]: bf16, device, 16-byte aligned; the two of a projection are
  *     both given or both NULL (projection without adapters).
  */
+#define MOE_SHARED_MAX_DIM (1 << 20)
 #define MOE_MAX_ADAPTERS 4096
 #define MOE_MAX_RANK 256
 typedef struct {
@@ -469,8 +470,9 @@ size_t moe_shared_ffn_workspace(const moe_layer_desc *L, const moe_adapter_desc 
  * non-finite values in one adapter reach only the tokens that use it.
  * hidden and shared_inter must be multiples of 8; x, out and the weights 16-byte
  * aligned.  Errors: MOE_ERR_INVALID_ARG (null, misaligned or overlapping
- * pointer, bad shape or dtype, workspace too small), MOE_ERR_DEVICE (launch
- * failure).
+ * pointer, bad shape or dtype, workspace too small), MOE_ERR_UNSUPPORTED (hidden
+ * or shared_inter above MOE_SHARED_MAX_DIM, or n_tokens times the larger of them
+ * 2^30 or more), MOE_ERR_DEVICE (launch failure).
  */
 moe_status moe_shared_ffn(const moe_layer_desc *L, const moe_adapter_desc *A, const void *x, int32_t x_dt,
                           int32_t n_tokens, const int32_t *token_adapter, void *out, int32_t out_dt, void *ws,
