@@ -6,7 +6,7 @@
 // matrix cores with fp32 sums.  Launches: [split] [plan] [down-rank] gate/up [down-rank] down --
 //
 //   split      fp32 activations as two bf16 planes hi + lo = bf16(x), bf16(x - hi): 16 significant bits
-//   plan       (many tokens) the tokens ordered by adapter, and work items of up to 16 tokens of one adapter
+//   plan       (many tokens) the tokens ordered by adapter, and work items of up to 64 tokens of one adapter
 //   down-rank  s[t][r] = c_a (A_a[r] . x[t]) for each token's own adapter, in fp32 or (many tokens) as two bf16 parts
 //   gate/up    weight rows x tokens; the adapters' B_a s in the epilogue; SwiGLU; h as one bf16 plane (bf16 result)
 //              or two (fp32 result, whose error then stays near 2^-17)
@@ -55,6 +55,27 @@ __device__ __forceinline__ uint4 keep_first(uint4 v, int n) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+template <int N> __device__ __forceinline__ void wait_stage() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 64 lanes' 16 bytes at base + off -> 1 KiB of LDS at byte address `dst` (wave-uniform), in lane order.  The destination
+// goes through m0, which is put back: the compiler may count on its value.
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32 |
+           (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+}
+__device__ __forceinline__ void load_to_lds(uint64_t base, uint32_t off, uint32_t dst) {
+    uint32_t m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0) : "v"(off), "s"(base), "s"(dst) : "memory");
+}
+
+// A value at a wave-uniform place, through the scalar cache: its wait is apart from that for the vector loads in flight.
+template <typename T> __device__ __forceinline__ T uniform_at(const T *p, int64_t i) {
+    return reinterpret_cast<const __attribute__((address_space(4))) T *>(reinterpret_cast<uintptr_t>(p))[i];
+}
+
 __device__ __forceinline__ int rank_of(const SharedArgs &a, int ad) {
     return a.rank ? min(max(a.rank[ad], 0), a.R) : a.R;
 }
@@ -84,7 +105,7 @@ __global__ __launch_bounds__(256) void k_split(const float *__restrict__ x, uint
 }
 
 // ---------------------------------------------------------------------------
-// plan: tokens ordered by adapter (those without one last), and items of up to ITEM_TOKENS tokens of one adapter.
+// plan (many tokens): tokens ordered by adapter (those without one last), and items of up to ITEM_TOKENS tokens of one adapter.
 // One workgroup.  Within an adapter the order is that of LDS atomics and may differ between calls: a row's place in
 // a tile changes no bit of its result.
 // ---------------------------------------------------------------------------
@@ -164,202 +185,214 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens, down-rank: s[t][proj][r] = scale_a (A_a[r] . x[t]) in fp32, one wave per (token, row): no wait but that for the
+// Few tokens: what a product reads of its activations.
+//
+// Packed activations [P][TF][steps][64 lanes][8]: the matrix instruction's operand of 16 tokens and 32 of K in lane order, so
+// that a wave reads 1 KiB in a row.  Lane l holds token l % 16 and k = 8 (l / 16) .. + 7; behind the end of K zeros.
+// Read from rows instead, the 64 lanes' 16-byte pieces would lie in 64 places, and a wave's load would take four times as
+// long (measured as the bound of the row-reading kernel at 24 tokens: 18.5 us against 10.6 for the gate/up product).
+//
+// Low-rank results s[t][proj][r] = scale_a (A_a[r] . x[t]) in fp32, one wave per (token, row): no wait but that for the
 // token's adapter index and that for the row, and no exchange but the wave's own sum.
 // ---------------------------------------------------------------------------
-template <int P>
-__global__ __launch_bounds__(256) void k_low_rank_few(SharedArgs a, LowRank L) {
+// TF: fragments of 16 tokens, rounded up to what the kernels are built for; those behind the last token hold anything.
+__host__ __device__ __forceinline__ int few_frags(int T) { return T <= 16 ? 1 : T <= 32 ? 2 : 4; }
+
+enum { ACT_BF16 = 0, ACT_PLANES = 1, ACT_F32 = 2 };          // x: one bf16 plane, two of them, fp32
+
+template <int SRC>
+__global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uint16_t *packed, int pack_blocks) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int nrows = L.np * a.R, id = blockIdx.x * 4 + wave;
+    const int K = L.K, steps = (K + 31) / 32;
+    if ((int)blockIdx.x < pack_blocks) {
+        const int i = blockIdx.x * 4 + wave, tf = (a.T + 15) / 16, f = i / steps, step = i - f * steps;
+        if (f >= tf) return;
+        const int t = f * 16 + (lane & 15), k = step * 32 + 8 * (lane >> 4);
+        uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+        if (t < a.T && k < K) {
+            if constexpr (SRC == ACT_F32) {
+                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(L.xv) + (int64_t)t * K + k);
+                const float4 u = p[0], v = p[1];
+                hi = make_uint4(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w), pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+                lo = make_uint4(pack_bf16(bf16_rest(u.x), bf16_rest(u.y)), pack_bf16(bf16_rest(u.z), bf16_rest(u.w)),
+                                pack_bf16(bf16_rest(v.x), bf16_rest(v.y)), pack_bf16(bf16_rest(v.z), bf16_rest(v.w)));
+            } else {
+                hi = load16(static_cast<const uint16_t *>(L.xv) + (int64_t)t * K + k);
+            }
+        }
+        uint4 *o = reinterpret_cast<uint4 *>(packed);
+        o[(int64_t)i * 64 + lane] = hi;
+        if constexpr (SRC == ACT_F32) o[((int64_t)few_frags(a.T) * steps + i) * 64 + lane] = lo;
+        return;
+    }
+    const int nrows = L.np * a.R, id = (blockIdx.x - pack_blocks) * 4 + wave;
     if (id >= a.T * nrows) return;
     const int t = id / nrows, rr = id - t * nrows, proj = rr / a.R, r = rr - proj * a.R;
     const int ad = adapter_at(a, t);
-    if (ad < 0 || !L.a[proj]) return;                        // not read either
-    const uint16_t *A = L.a[proj] + ((int64_t)ad * a.R + r) * L.K, *x = L.x + (int64_t)t * L.K;
-    const int64_t plane = (int64_t)a.T * L.K;
-    constexpr int U = 8;
-    float acc[P] = {};
-    for (int k0 = 0; k0 < L.K; k0 += U * 512) {
-        uint4 w[U], v[P][U];
+    const uint16_t *A = proj ? L.a[1] : L.a[0];
+    if (ad < 0 || !A) return;                                // not read either
+    A += ((int64_t)ad * a.R + r) * K;
+    const int64_t row = (int64_t)t * K, plane = (int64_t)a.T * K;
+    constexpr int U = SRC == ACT_F32 ? 4 : 8, P = SRC == ACT_PLANES ? 2 : 1;
+    float acc[2] = {0.f, 0.f};
+    for (int k0 = 0; k0 < K; k0 += U * 512) {
+        uint4 w[U], v[SRC == ACT_BF16 ? 1 : 2][U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const int k = k0 + j * 512 + lane * 8;
-            w[j] = k < L.K ? load16(A + k) : make_uint4(0, 0, 0, 0);
+            const bool in = k < K;
+            w[j] = in ? load16(A + k) : make_uint4(0, 0, 0, 0);
+            if constexpr (SRC == ACT_F32) {
+                const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const float *>(L.xv) + row + k);
+                v[0][j] = in ? x[0] : make_uint4(0, 0, 0, 0);
+                v[1][j] = in ? x[1] : make_uint4(0, 0, 0, 0);
+            } else {
 #pragma unroll
-            for (int p = 0; p < P; ++p) v[p][j] = k < L.K ? load16(x + p * plane + k) : make_uint4(0, 0, 0, 0);
+                for (int p = 0; p < P; ++p)
+                    v[p][j] = in ? load16(static_cast<const uint16_t *>(L.xv) + row + p * plane + k) : make_uint4(0, 0, 0, 0);
+            }
         }
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-#pragma unroll
-            for (int p = 0; p < P; ++p) acc[p] = dot8(w[j], v[p][j], acc[p]);
-    }
-    float y = acc[0];
-    if constexpr (P == 2) y += acc[1];
-    y = wave_sum(y);
-    if (lane == 0)
-        L.s32[(int64_t)id] = r < rank_of(a, ad) ? y * (a.scale ? a.scale[ad] : 1.f) : 0.f;
-}
-
-// ---------------------------------------------------------------------------
-// Many tokens, down-rank: s[pos][proj][hi, lo][r] = scale_a (A_a[r] . x[pos]) for the np projections that read x.  One
-// workgroup takes an item (up to 16 tokens of one adapter) and FR fragments of 16 of the np * R rows; its sixteen waves split
-// K, and their sums meet in LDS.
-// ---------------------------------------------------------------------------
-constexpr int LR_WAVES = 16;
-
-template <int P, int FR>
-__global__ __launch_bounds__(64 * LR_WAVES) void k_low_rank(SharedArgs a, LowRank L) {
-    __shared__ float red[LR_WAVES][FR * 256];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, q = lane >> 4;
-    // each XCD takes a run of items, and with it few adapters
-    const int per = (gridDim.x + 7) / 8, item = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-    if (item >= *a.n_items) return;
-    const int4 it = a.items[item];
-    const int ad = it.x, cnt = it.z;
-    const int K = L.K, R = a.R, nrows = L.np * R, f0 = blockIdx.y * FR;
-    const int steps = (K + 31) / 32;
-    const int s0 = steps * wave / LR_WAVES, s1 = steps * (wave + 1) / LR_WAVES;
-    const int pos = it.y + min(i16, cnt - 1);
-    const uint16_t *xrow = L.x + (int64_t)(L.gather ? a.perm[pos] : pos) * K;
-    const int64_t plane = (int64_t)a.T * K;
-    f32x4_t acc[FR];
-    const uint16_t *arow[FR];
-#pragma unroll
-    for (int f = 0; f < FR; ++f) {
-        acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        const int rr = (f0 + f) * 16 + i16, proj = rr / R, r = rr - proj * R;
-        arow[f] = rr < nrows && L.a[proj] ? L.a[proj] + ((int64_t)ad * R + r) * K : nullptr;
-    }
-    constexpr int U = P == 1 ? 8 : 4;
-    for (int s = s0; s < s1; s += U) {
-        uint4 b[U][P], w[U][FR];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const int k = (s + j) * 32 + q * 8;
-            const bool in = s + j < s1 && k < K;
+            if constexpr (SRC == ACT_F32) {
+                const uint32_t wv[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                const uint32_t xv[8] = {v[0][j].x, v[0][j].y, v[0][j].z, v[0][j].w, v[1][j].x, v[1][j].y, v[1][j].z, v[1][j].w};
 #pragma unroll
-            for (int f = 0; f < FR; ++f) w[j][f] = in && arow[f] ? load16(arow[f] + k) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 4; ++i) {
+                    acc[0] = __fmaf_rn(__uint_as_float(wv[i] << 16), __uint_as_float(xv[2 * i]), acc[0]);
+                    acc[1] = __fmaf_rn(__uint_as_float(wv[i] & 0xFFFF0000u), __uint_as_float(xv[2 * i + 1]), acc[1]);
+                }
+            } else {
 #pragma unroll
-            for (int p = 0; p < P; ++p) b[j][p] = in ? load16(xrow + p * plane + k) : make_uint4(0, 0, 0, 0);
+                for (int p = 0; p < P; ++p) acc[p] = dot8(w[j], v[p][j], acc[p]);
+            }
         }
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-#pragma unroll
-            for (int f = 0; f < FR; ++f)
-#pragma unroll
-                for (int p = 0; p < P; ++p) acc[f] = mfma16(w[j][f], b[j][p], acc[f]);
     }
-#pragma unroll
-    for (int f = 0; f < FR; ++f)
-        *reinterpret_cast<f32x4_t *>(&red[wave][f * 256 + i16 * 16 + 4 * q]) = acc[f];       // [token][row]
-    __syncthreads();
-    const float scale = a.scale ? a.scale[ad] : 1.f;
-    const int rank = rank_of(a, ad);                         // what lies behind it was read, and is dropped here
-    for (int e = threadIdx.x; e < FR * 256; e += 64 * LR_WAVES) {
-        const int f = e >> 8, tok = (e >> 4) & 15, rr = (f0 + f) * 16 + (e & 15);
-        if (tok >= cnt || rr >= nrows) continue;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < LR_WAVES; ++w) v += red[w][e];
-        const int proj = rr / R, r = rr - proj * R;
-        v = r < rank ? v * scale : 0.f;
-        uint16_t *o = L.s + ((int64_t)(it.y + tok) * L.np + proj) * 2 * R + r;
-        o[0] = __builtin_bit_cast(uint16_t, (__bf16)v);
-        o[R] = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(v));
-    }
+    const float y = wave_sum(acc[0] + acc[1]);
+    if (lane == 0) L.s32[(int64_t)id] = r < rank_of(a, ad) ? y * (a.scale ? a.scale[ad] : 1.f) : 0.f;
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: one workgroup streams 16 weight rows (gate/up: 8 gate rows and the same 8 of up) once, straight into
-// the matrix instruction's operand registers; its sixteen waves split K, and their sums meet in LDS.  An adapter's term is
-// formed per token in fp32, wave w taking tokens w, w + 16, ..., lane (row, q) the rank values 8 q .. 8 q + 7 of each 32;
-// their loads go out between the weights' and the activations'.
+// Few tokens, a product: one workgroup streams 16 weight rows (gate/up: 8 gate rows and the same 8 of up) once.  Its waves
+// split K: in each round of 2048 a wave takes 2048 / NW of every row, through LDS of its own that direct-to-LDS loads fill
+// with whole 256- or 512-byte pieces of rows (two rounds in flight: 128 KiB per workgroup).  Chunk c of row r lies at position
+// c ^ r, so that sixteen rows' reads of one chunk column touch every bank once.  The waves' sums meet in LDS.
+// An adapter's term is formed per token in fp32, wave w taking tokens w, w + NW, ...; its loads go out with the weights'.
+// Sixteen waves for few operands per step; eight, with twice the registers, where a step has four or more of them.
 // ---------------------------------------------------------------------------
-constexpr int FEW_WAVES = 16;
+constexpr int FEW_ROUND = 2048;
+constexpr int few_waves(int P, int TF) { return P * TF >= 4 ? 8 : 16; }
+
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 template <bool GU, int P, int TF, bool AD>
-__global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g) {
-    constexpr int NW = FEW_WAVES;
-    __shared__ float red[NW][TF][16][17], low[TF * 16][17];
+__global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Product g) {
+    constexpr int NW = few_waves(P, TF), SLICE = FEW_ROUND / NW;         // K of a wave per round
+    constexpr int LINE = SLICE / 8, LOADS = 16 * LINE / 64;              // chunks of a row's piece; loads of 64 chunks
+    constexpr int TW = TF * 16 / NW;                                     // tokens per wave (adapters' terms)
+    __shared__ __attribute__((aligned(1024))) uint4 ring[2][NW][16 * LINE];
+    __shared__ float low[TF * 16][17];
+    float (*red)[TF][16][17] = reinterpret_cast<float (*)[TF][16][17]>(ring);      // after the last product
+    static_assert(sizeof(float) * NW * TF * 16 * 17 <= sizeof(ring), "");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
     const int K = g.K, r0 = blockIdx.x * (GU ? 8 : 16);
-    const int wr = GU ? r0 + (i16 & 7) : r0 + i16, half = GU ? i16 >> 3 : 0;
-    f32x4_t acc[TF];
+    // load j fills 64 / LINE rows' pieces; a chunk behind the row's end repeats the piece's first (its products meet zero
+    // activations), rows behind the last repeat it (their sums are not stored)
+    const int rf = GU ? min(r0, g.N - 8) : r0;                           // gate/up: workgroups behind the last rows write zeros
+    uint64_t base[2];
+    base[0] = uniform64((uint64_t)(uintptr_t)(g.w[0] + (int64_t)rf * K));
+    base[1] = GU ? uniform64((uint64_t)(uintptr_t)(g.w[1] + (int64_t)rf * K)) : base[0];
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(las_ptr)ring + wave * (16u * LINE * 16u);
+    const int rounds = (K + FEW_ROUND - 1) / FEW_ROUND, steps = (K + 31) / 32;
+    auto issue = [&](int r, int b) {
+        const int k = r * FEW_ROUND + wave * SLICE;
+        if (k >= K) return;
 #pragma unroll
-    for (int f = 0; f < TF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    int ad[TF];
-    if constexpr (AD) {
-#pragma unroll
-        for (int f = 0; f < TF; ++f) ad[f] = adapter_at(a, f * 16 + wave);
-    }
-    const uint16_t *wrow = (half ? g.w[1] : g.w[0]) + (int64_t)min(wr, g.N - 1) * K;
-    const int steps = (K + 31) / 32;
-    const int s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
-    const uint16_t *xrow[TF];
-#pragma unroll
-    for (int f = 0; f < TF; ++f) xrow[f] = g.x + (int64_t)min(f * 16 + i16, a.T - 1) * K;
-    const int64_t plane = (int64_t)a.T * K;
-    // U steps' weights are in flight at once; the activations (from the caches) XU steps at a time
-    constexpr int U = 8, XU = TF * P == 1 ? 8 : TF * P == 2 ? 4 : TF * P == 4 ? 2 : 1;
-    uint4 w[U];
-    auto load_weights = [&](int s) {
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int k = (s + j) * 32 + q * 8;
-            w[j] = s + j < s1 && k < K ? load16(wrow + k) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < LOADS; ++j) {
+            const int row = j * (64 / LINE) + lane / LINE, c = lane % LINE ^ row;
+            uint32_t o = 2u * ((uint32_t)(GU ? row & 7 : min(row, g.N - 1 - r0)) * (uint32_t)K + (uint32_t)k);
+            if (k + 8 * c < K) o += 16u * c;
+            load_to_lds(base[GU && j >= LOADS / 2], o, lds0 + b * (uint32_t)(sizeof(ring) / 2) + j * 1024u);
         }
     };
-    load_weights(s0);
-    // this lane's part of an adapter's term for token f * 16 + wave, rank values 32 c + 8 q .. + 7
-    uint4 bw[TF];
-    float4 ss[TF][2];
+    // An adapter's term for token f * NW + wave: lane (row lr = lane / 4, lane % 4) takes rank values 8 (lane % 4) .. + 7 of each
+    // 32, so that four lanes in a row read 64 bytes of one row of B.
+    const int lr = lane >> 2, half = GU ? lr >> 3 : 0, wr = GU ? r0 + (lr & 7) : r0 + lr;
+    const uint16_t *const gb = half ? g.b[1] : g.b[0];
+    int ad[TW];
+    uint4 bw[TW];
+    float4 ss[TW][2];
     auto load_low = [&](int c) {
-        const int r = 32 * c + 8 * q;
+        const int r = 32 * c + 8 * (lane & 3);
 #pragma unroll
-        for (int f = 0; f < TF; ++f) {
+        for (int f = 0; f < TW; ++f) {
             bw[f] = make_uint4(0, 0, 0, 0);
             ss[f][0] = ss[f][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (ad[f] >= 0 && r < a.R && wr < g.N && (half ? g.b[1] : g.b[0])) {
-                bw[f] = load16((half ? g.b[1] : g.b[0]) + ((int64_t)ad[f] * g.N + wr) * a.R + r);
+            if (ad[f] >= 0 && r < a.R && wr < g.N && gb) {
+                bw[f] = load16(gb + ((int64_t)ad[f] * g.N + wr) * a.R + r);
                 const float4 *p = reinterpret_cast<const float4 *>(
-                    g.s32 + ((int64_t)(f * 16 + wave) * (GU ? 2 : 1) + half) * a.R + r);
+                    g.s32 + ((int64_t)(f * NW + wave) * (GU ? 2 : 1) + half) * a.R + r);
                 ss[f][0] = p[0];
                 ss[f][1] = p[1];
             }
         }
     };
-    constexpr bool AHEAD = TF < 4;                           // with 64 tokens the registers do not hold both
-    if constexpr (AD && AHEAD) load_low(0);
-    for (int s = s0; s < s1; s += U) {
-        if (s != s0) load_weights(s);
+    f32x4_t acc[TF];
 #pragma unroll
-        for (int j0 = 0; j0 < U; j0 += XU) {
-            uint4 x[XU][TF][P];
+    for (int f = 0; f < TF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const uint4 *const xp = reinterpret_cast<const uint4 *>(g.x);
+    const int64_t plane = (int64_t)TF * steps * 64;
+    constexpr int SPW = SLICE / 32;                                      // steps of a wave per round
+    constexpr int XB = TF * P <= 2 ? 2 * SPW : TF * P == 4 ? SPW : SPW / 2;      // steps whose activations are loaded together
+    for (int r = 0; r < rounds; r += 2) {
+        if (r) wait_reads();                                              // the slices of the rounds before are read
+        issue(r, 0);
+        if (r + 1 < rounds) issue(r + 1, 1);
+        if constexpr (AD) {
+            if (r == 0) {
 #pragma unroll
-            for (int j = 0; j < XU; ++j) {
-                const int k = (s + j0 + j) * 32 + q * 8;
-                const bool in = s + j0 + j < s1 && k < K;
-#pragma unroll
-                for (int f = 0; f < TF; ++f)
-#pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        x[j][f][p] = in ? load16(xrow[f] + p * plane + k) : make_uint4(0, 0, 0, 0);
+                for (int f = 0; f < TW; ++f) {
+                    const int t = f * NW + wave, id = t < a.T ? uniform_at(a.token_adapter, t) : -1;
+                    ad[f] = (unsigned)id < (unsigned)a.n ? id : -1;
+                }
+                load_low(0);
             }
+        }
+        const int s0 = r * (FEW_ROUND / 32) + wave * SPW;
+        auto step_of = [&](int i) { return s0 + i / SPW * (FEW_ROUND / 32) + i % SPW; };
 #pragma unroll
-            for (int j = 0; j < XU; ++j)
+        for (int ib = 0; ib < 2 * SPW; ib += XB) {
+            if (step_of(ib) >= steps) break;
+            uint4 x[XB][TF][P];
+#pragma unroll
+            for (int i = 0; i < XB; ++i)
 #pragma unroll
                 for (int f = 0; f < TF; ++f)
 #pragma unroll
-                    for (int p = 0; p < P; ++p) acc[f] = mfma16(w[j0 + j], x[j][f][p], acc[f]);
+                    for (int p = 0; p < P; ++p) {
+                        const int st = step_of(ib + i);
+                        x[i][f][p] = st < steps ? xp[p * plane + ((int64_t)f * steps + st) * 64 + lane] : make_uint4(0, 0, 0, 0);
+                    }
+            if (ib == 0) wait_loads();
+#pragma unroll
+            for (int i = 0; i < XB; ++i) {
+                if (step_of(ib + i) >= steps) break;
+                const uint4 w = ring[(ib + i) / SPW][wave][i16 * LINE + ((4 * ((ib + i) % SPW) + q) ^ i16)];
+#pragma unroll
+                for (int f = 0; f < TF; ++f)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) acc[f] = mfma16(w, x[i][f][p], acc[f]);
+            }
         }
     }
     if constexpr (AD) {
-        float d[TF] = {};
+        float d[TW] = {};
         for (int c = 0; 32 * c < a.R; ++c) {
-            if (c || !AHEAD) load_low(c);
+            if (c) load_low(c);
 #pragma unroll
-            for (int f = 0; f < TF; ++f) {
-                const int rank = ad[f] < 0 ? 0 : rank_of(a, ad[f]) - (32 * c + 8 * q);       // of this lane's eight
+            for (int f = 0; f < TW; ++f) {
+                const int rank = (ad[f] < 0 ? 0 : rank_of(a, ad[f])) - (32 * c + 8 * (lane & 3));     // of this lane's eight
                 const uint4 b = keep_first(bw[f], rank);
                 const uint32_t bb[4] = {b.x, b.y, b.z, b.w};
                 const float sv[8] = {ss[f][0].x, ss[f][0].y, ss[f][0].z, ss[f][0].w,
@@ -372,12 +405,14 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
             }
         }
 #pragma unroll
-        for (int f = 0; f < TF; ++f) {
-            d[f] += __shfl_xor(d[f], 16, 64);
-            d[f] += __shfl_xor(d[f], 32, 64);
-            if (q == 0) low[f * 16 + wave][i16] = d[f];
+        for (int f = 0; f < TW; ++f) {
+            d[f] += __shfl_xor(d[f], 1, 64);
+            d[f] += __shfl_xor(d[f], 2, 64);
+            if ((lane & 3) == 0) low[f * NW + wave][lr] = d[f];
         }
     }
+    wait_loads();                                            // a wave without steps has none; the ring is free after the barrier
+    __syncthreads();
 #pragma unroll
     for (int f = 0; f < TF; ++f)
 #pragma unroll
@@ -386,19 +421,27 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
     constexpr int NR = GU ? 8 : 16;
     for (int e = threadIdx.x; e < TF * 16 * NR; e += 64 * NW) {
         const int r = e % NR, tok = e / NR, f = tok >> 4, c = tok & 15;
-        if (tok >= a.T || r0 + r >= g.N) continue;
+        if (tok >= a.T) continue;
         float y = AD ? low[tok][r] : 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) y += red[w][f][c][r];
-        const int64_t o = (int64_t)tok * g.N + r0 + r;
         if constexpr (GU) {
             float up = AD ? low[tok][r + 8] : 0.f;
 #pragma unroll
             for (int w = 0; w < NW; ++w) up += red[w][f][c][r + 8];
-            const float h = silu_mul(y, up);
-            g.h[o] = __builtin_bit_cast(uint16_t, (__bf16)h);
-            if (g.hp == 2) g.h[(int64_t)a.T * g.N + o] = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(h));
+            const int i = r0 + r, hsteps = (g.N + 31) / 32;
+            const float h = r0 < g.N ? silu_mul(y, up) : 0.f;           // packed rows end in zeros
+            const uint16_t hi = __builtin_bit_cast(uint16_t, (__bf16)h), lo = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(h));
+            const int64_t o = (((int64_t)f * hsteps + i / 32) * 64 + (i % 32 / 8) * 16 + c) * 8 + i % 8;
+            g.h[o] = hi;
+            if (g.hp == 2) g.h[(int64_t)TF * hsteps * 512 + o] = lo;
+            if (g.hrow && r0 < g.N) {                                    // for the down-rank products
+                g.hrow[(int64_t)tok * g.N + i] = hi;
+                if (g.hp == 2) g.hrow[(int64_t)a.T * g.N + (int64_t)tok * g.N + i] = lo;
+            }
         } else {
+            if (r0 + r >= g.N) continue;
+            const int64_t o = (int64_t)tok * g.N + r0 + r;
             if (g.out_bf16) static_cast<__bf16 *>(g.out)[o] = (__bf16)y;
             else static_cast<float *>(g.out)[o] = y;
         }
@@ -415,27 +458,15 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
 // have no register outputs; wait_stage() counts them (the kernel has no other vector memory access between the first
 // issue and the last stage) and orders the workgroup.
 // ---------------------------------------------------------------------------
-template <int N> __device__ __forceinline__ void wait_stage() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-// 64 lanes' 16 bytes at base + off -> 1 KiB of LDS at byte address `dst` (wave-uniform), in lane order.  The destination
-// goes through m0, which is put back: the compiler may count on its value.
-__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
-    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32 |
-           (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
-}
-__device__ __forceinline__ void load_to_lds(uint64_t base, uint32_t off, uint32_t dst) {
-    uint32_t m0;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
-                 : "=&s"(m0) : "v"(off), "s"(base), "s"(dst) : "memory");
-}
-
 constexpr int BW = 128, BK = 64, STAGES = 3;
+enum { MODE_GATE_UP = 0, MODE_DOWN = 1, MODE_LOW_RANK = 2 };
 
+// Down-rank (MODE_LOW_RANK): a tile's tokens are an item of the plan, its weight rows those of that adapter's A matrices, and
+// blockIdx.y is a part of K; the sums of the parts are added by k_low_rank_sum.
 // TAIL: K is no multiple of 64, so a row's last step is not a whole one.
-template <bool GU, int P, int BT, bool TAIL>
+template <int MODE, int P, int BT, bool TAIL>
 __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles_w, int tiles_t) {
+    constexpr bool GU = MODE == MODE_GATE_UP, LOW = MODE == MODE_LOW_RANK;
     constexpr int WT = 2;                                    // waves along the tokens, and along the weight rows
     constexpr int FW = BW / 2 / 32, FT = BT / WT / 32;       // 32 x 32 fragments per wave
     constexpr int ROWS = BW + BT, LOADS = ROWS / 8 / 4;      // direct-to-LDS loads (8 rows each) per wave and stage
@@ -449,7 +480,15 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
     const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
     const int tw = id / tiles_t, tt = id - tw * tiles_t;
-    const int w0 = tw * (GU ? BW / 2 : BW), t0 = tt * BT;
+    const int w0 = tw * (GU ? BW / 2 : BW);
+    int t0 = tt * BT, last = a.T - 1, ad0 = 0;               // first and last row of the tile's tokens
+    if constexpr (LOW) {
+        if (tt >= *a.n_items) return;
+        const int4 it = a.items[tt];
+        ad0 = it.x;
+        t0 = it.y;
+        last = it.y + it.z - 1;
+    }
 
     // Load i of this wave fills rows 8 * (wave * LOADS + i) .. + 7 of the tile from one operand (`base`); `off`: byte offset of
     // this lane's row and chunk from there (launch_shared() keeps them below 2^32).  Rows behind the last repeat it; their
@@ -463,25 +502,36 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
         const int r8 = 8 * (wave * LOADS + i), r = r8 + (lane >> 3), c = i & 1 ? chunk1 : chunk0;
         const uint16_t *from = g.x;
         int row;
-        if (r8 < BW) {
+        if (LOW && r8 < BW) {
+            // the adapter's rows [projection][R], eight of them in one projection; in a projection without adapters any
+            // (its results are not read)
+            const int rr = min(w0 + r8, g.N - 8), proj = rr / a.R;
+            row = rr - proj * a.R + (lane >> 3);
+            from = (proj ? (g.w[1] ? g.w[1] : g.w[0]) : (g.w[0] ? g.w[0] : g.w[1])) + (int64_t)ad0 * a.R * K;
+        } else if (r8 < BW) {
             // gate/up: rows come in 32-row groups gate, up, gate, up so that a wave holds both of the same rows
             row = min(GU ? (r >> 6) * 32 + (r & 31) : r, g.N - 1 - w0);
             from = (GU && (r8 >> 5 & 1) ? g.w[1] : g.w[0]) + (int64_t)w0 * K;
         } else {
-            const int pos = min(t0 + r - BW, a.T - 1);
+            const int pos = min(t0 + r - BW, last);
             row = g.gather && a.sorted ? a.perm[pos] : pos;
         }
         base[i] = uniform64((uint64_t)(uintptr_t)from);
         off[i] = 2u * ((uint32_t)row * (uint32_t)K + 8u * c);
     }
-    const int ksteps = (K + BK - 1) / BK, nsteps = ksteps * P;
+    const int ksteps = (K + BK - 1) / BK;
+    // steps of this workgroup: all, or (down-rank) those of its part of K
+    const int sb = LOW ? ksteps * (int)blockIdx.y / (int)gridDim.y : 0;
+    const int se = LOW ? ksteps * ((int)blockIdx.y + 1) / (int)gridDim.y : ksteps;
+    const int nsteps = (se - sb) * P;
     const int tail = K % BK / 8;                             // chunks in a row's last step (TAIL)
     const uint32_t lds0 = (uint32_t)(uintptr_t)(las_ptr)tile + wave * LOADS * 1024u;
     // Loads of the next stage to issue: its step, and the byte offsets of step and plane.  A chunk behind the row's end repeats the
     // step's first one (its products are masked), and stages behind the last repeat that: every stage has the same
     // number of loads in flight.
-    int istep = 0;
-    uint32_t iw = 0, ix = 0, idst = lds0;
+    int istep = sb;
+    const uint32_t xplane = 2u * (uint32_t)a.T * (uint32_t)K;
+    uint32_t iw = 2 * BK * sb, ix = iw, idst = lds0;
     const uint32_t back0 = TAIL && chunk0 >= tail ? 16u * chunk0 : 0u, back1 = TAIL && chunk1 >= tail ? 16u * chunk1 : 0u;
     auto issue = [&](int i) {                                // i: load of this wave (compile-time)
         uint32_t o = off[i] + ((wave * LOADS + i) * 8 < BW ? iw : ix);
@@ -489,8 +539,8 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
         load_to_lds(base[i], o, idst + i * 1024u);
     };
     auto next_stage = [&]() {
-        if (istep + 1 < ksteps) { ++istep; iw += 2 * BK; ix += 2 * BK; }
-        else if (P > 1 && ix == iw) { istep = 0; iw = 0; ix = 2u * (uint32_t)a.T * (uint32_t)K; }
+        if (istep + 1 < se) { ++istep; iw += 2 * BK; ix += 2 * BK; }
+        else if (P > 1 && ix == iw) { istep = sb; iw = 2 * BK * sb; ix = iw + xplane; }
         idst = idst == lds0 + (STAGES - 1) * ROWS * 128u ? lds0 : idst + ROWS * 128u;
     };
     f32x16_t acc[FW][FT];
@@ -536,7 +586,7 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
 #pragma unroll
     for (int i = 0; i < LOADS / 4; ++i) issue(i);
     wait_stage<LOADS + LOADS / 4>();
-    int rb = 0, step = 0;
+    int rb = 0, step = sb;
 #pragma unroll
     for (int n = 0; n < FW + FT; ++n) read_one(tile[0], 0, 0, n);
     for (int s = 0; s < nsteps; ++s) {
@@ -559,11 +609,29 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
         wait_stage<LOADS>();
         mask(3, 1);
         slice(1, tile[rb], 0, 0);                            // behind the last stage: a read of old values, not used
-        step = step + 1 == ksteps ? 0 : step + 1;
+        step = step + 1 == se ? sb : step + 1;
     }
     wait_stage<0>();
     // D: lane holds token i32 of a fragment, weight rows 8 * (v / 4) + 4 * hh + v % 4
-    if (a.n) {
+    if constexpr (LOW) {
+        // fp32 sums of this part of K: [part][pos][projection][R]
+#pragma unroll
+        for (int j = 0; j < FT; ++j) {
+            const int pos = t0 + (rt - BW) + j * 32 + i32;
+            if (pos > last) continue;
+            float *o = g.part + ((int64_t)blockIdx.y * a.T + pos) * g.N;
+#pragma unroll
+            for (int i = 0; i < FW; ++i)
+#pragma unroll
+                for (int v4 = 0; v4 < 4; ++v4) {
+                    const int rr = w0 + rw + i * 32 + 8 * v4 + 4 * hh;
+                    const f32x16_t &y = acc[i][j];
+                    if (rr < g.N)
+                        *reinterpret_cast<float4 *>(o + rr) = make_float4(y[4 * v4], y[4 * v4 + 1], y[4 * v4 + 2], y[4 * v4 + 3]);
+                }
+        }
+        return;
+    } else if (a.n) {
         // One adapter of 64 of this wave's tokens at a time, in accumulators of its own.  Rank values go 16 at a time, each
         // once with the high and once with the low part of the token's low-rank result.
         constexpr int NP = GU ? 2 : 1, JG = FT < 2 ? FT : 2;
@@ -670,45 +738,111 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
     }
 }
 
+constexpr int MAX_PARTS = 8;
+
+// s[pos][proj][hi, lo][r] = scale_a * (sum of the parts of K, in order), as two bf16 parts; 0 from the adapter's rank on.
+__global__ __launch_bounds__(256) void k_low_rank_sum(SharedArgs a, const float *part, int parts, int np, uint16_t *s) {
+    const int per = np * a.R / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)a.T * per) return;
+    const int pos = (int)(i / per), rr = 4 * (int)(i - (int64_t)pos * per), proj = rr / a.R, r = rr - proj * a.R;
+    const int ad = a.plan_ad[pos];
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 x[MAX_PARTS];
+#pragma unroll
+    for (int k = 0; k < MAX_PARTS; ++k)
+        x[k] = k < parts ? *reinterpret_cast<const float4 *>(part + ((int64_t)k * a.T + pos) * np * a.R + rr) : v;
+#pragma unroll
+    for (int k = 0; k < MAX_PARTS; ++k) { v.x += x[k].x; v.y += x[k].y; v.z += x[k].z; v.w += x[k].w; }
+    if (ad < 0) return;                                      // of no adapter: neither written before nor read after
+    const float c = a.scale ? a.scale[ad] : 1.f;
+    const int rank = rank_of(a, ad) - r;
+    v.x = 0 < rank ? v.x * c : 0.f;
+    v.y = 1 < rank ? v.y * c : 0.f;
+    v.z = 2 < rank ? v.z * c : 0.f;
+    v.w = 3 < rank ? v.w * c : 0.f;
+    uint16_t *o = s + ((int64_t)pos * np + proj) * 2 * a.R + r;
+    *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    *reinterpret_cast<uint2 *>(o + a.R) =
+        make_uint2(pack_bf16(bf16_rest(v.x), bf16_rest(v.y)), pack_bf16(bf16_rest(v.z), bf16_rest(v.w)));
+}
+
 template <bool GU, int P, bool AD>
 hipError_t launch_few(const SharedArgs &a, const Product &g, hipStream_t st) {
-    const dim3 grd((unsigned)((g.N + (GU ? 7 : 15)) / (GU ? 8 : 16))), blk(64 * FEW_WAVES);
-    if (a.T <= 16) hipLaunchKernelGGL((k_few<GU, P, 1, AD>), grd, blk, 0, st, a, g);
-    else if (a.T <= 32) hipLaunchKernelGGL((k_few<GU, P, 2, AD>), grd, blk, 0, st, a, g);
+    // gate/up: whole steps of the packed h, whose last rows may be zeros
+    const int tf = few_frags(a.T);
+    const dim3 grd((unsigned)(GU ? (g.N + 31) / 32 * 4 : (g.N + 15) / 16)), blk((unsigned)(64 * few_waves(P, tf)));
+    if (tf == 1) hipLaunchKernelGGL((k_few<GU, P, 1, AD>), grd, blk, 0, st, a, g);
+    else if (tf == 2) hipLaunchKernelGGL((k_few<GU, P, 2, AD>), grd, blk, 0, st, a, g);
     else hipLaunchKernelGGL((k_few<GU, P, 4, AD>), grd, blk, 0, st, a, g);
     return hipGetLastError();
 }
 
-template <bool GU, int P, bool TAIL>
-hipError_t launch_many(const SharedArgs &a, const Product &g, int bt, int tw, int tt, hipStream_t st) {
-    const dim3 grd((unsigned)((tw * tt + 7) / 8 * 8)), blk(256);
-    if (bt == 256) hipLaunchKernelGGL((k_many<GU, P, 256, TAIL>), grd, blk, 0, st, a, g, tw, tt);
-    else if (bt == 128) hipLaunchKernelGGL((k_many<GU, P, 128, TAIL>), grd, blk, 0, st, a, g, tw, tt);
-    else hipLaunchKernelGGL((k_many<GU, P, 64, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+template <bool GU>
+hipError_t few(const SharedArgs &a, const Product &g, int planes, hipStream_t st) {
+    if (planes == 1) return a.n ? launch_few<GU, 1, true>(a, g, st) : launch_few<GU, 1, false>(a, g, st);
+    return a.n ? launch_few<GU, 2, true>(a, g, st) : launch_few<GU, 2, false>(a, g, st);
+}
+
+// Packs the activations (packed) and forms the low-rank results (a.n), one launch for both.
+hipError_t few_inputs(const SharedArgs &a, const LowRank &L, int src, uint16_t *packed, hipStream_t st) {
+    const int pack = packed ? ((a.T + 15) / 16 * ((L.K + 31) / 32) + 3) / 4 : 0;
+    const int low = a.n ? (a.T * L.np * a.R + 3) / 4 : 0;
+    if (!pack && !low) return hipSuccess;
+    const dim3 grd((unsigned)(pack + low)), blk(256);
+    if (src == ACT_BF16) hipLaunchKernelGGL((k_few_inputs<ACT_BF16>), grd, blk, 0, st, a, L, packed, pack);
+    else if (src == ACT_PLANES) hipLaunchKernelGGL((k_few_inputs<ACT_PLANES>), grd, blk, 0, st, a, L, packed, pack);
+    else hipLaunchKernelGGL((k_few_inputs<ACT_F32>), grd, blk, 0, st, a, L, packed, pack);
     return hipGetLastError();
 }
 
-template <bool GU, int P>
-hipError_t launch_product(const SharedArgs &a, const Product &g, hipStream_t st) {
-    const int T = a.T;
-    if (T <= FEW_TOKENS) return a.n ? launch_few<GU, P, true>(a, g, st) : launch_few<GU, P, false>(a, g, st);
-    const int rows = GU ? BW / 2 : BW, tw = (g.N + rows - 1) / rows;
-    auto tiles = [&](int bt) { return tw * ((T + bt - 1) / bt); };
-    const int bt = tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
-    const int tt = (T + bt - 1) / bt;
-    return g.K % BK ? launch_many<GU, P, true>(a, g, bt, tw, tt, st) : launch_many<GU, P, false>(a, g, bt, tw, tt, st);
+template <int MODE, int P, bool TAIL>
+hipError_t launch_many(const SharedArgs &a, const Product &g, int bt, int tw, int tt, int parts, hipStream_t st) {
+    const dim3 grd((unsigned)((tw * tt + 7) / 8 * 8), (unsigned)parts), blk(256);
+    if constexpr (MODE != MODE_LOW_RANK) {
+        if (bt == 256) hipLaunchKernelGGL((k_many<MODE, P, 256, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+        else if (bt == 128) hipLaunchKernelGGL((k_many<MODE, P, 128, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+    }
+    if (bt == 64) hipLaunchKernelGGL((k_many<MODE, P, 64, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+    return hipGetLastError();
 }
 
-template <int P>
-hipError_t launch_low_rank(const SharedArgs &a, const LowRank &L, hipStream_t st) {
-    if (!a.sorted) {
-        hipLaunchKernelGGL((k_low_rank_few<P>), dim3((unsigned)((a.T * L.np * a.R + 3) / 4)), dim3(256), 0, st, a, L);
-        return hipGetLastError();
-    }
-    const int nd = a.T < a.n ? a.T : a.n, frags = (L.np * a.R + 15) / 16;
-    constexpr int FR = 2;
-    const unsigned items = (unsigned)(a.T / ITEM_TOKENS + nd + 7) / 8 * 8;
-    hipLaunchKernelGGL((k_low_rank<P, FR>), dim3(items, (unsigned)((frags + FR - 1) / FR)), dim3(64 * LR_WAVES), 0, st, a, L);
+template <int MODE>
+hipError_t many_tiles(const SharedArgs &a, const Product &g, int planes, int bt, int tw, int tt, int parts, hipStream_t st) {
+    if (planes == 1)
+        return g.K % BK ? launch_many<MODE, 1, true>(a, g, bt, tw, tt, parts, st)
+                        : launch_many<MODE, 1, false>(a, g, bt, tw, tt, parts, st);
+    return g.K % BK ? launch_many<MODE, 2, true>(a, g, bt, tw, tt, parts, st)
+                    : launch_many<MODE, 2, false>(a, g, bt, tw, tt, parts, st);
+}
+
+template <int MODE>
+hipError_t many(const SharedArgs &a, const Product &g, int planes, hipStream_t st) {
+    const int rows = MODE == MODE_GATE_UP ? BW / 2 : BW, tw = (g.N + rows - 1) / rows;
+    auto tiles = [&](int bt) { return tw * ((a.T + bt - 1) / bt); };
+    const int bt = tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
+    return many_tiles<MODE>(a, g, planes, bt, tw, (a.T + bt - 1) / bt, 1, st);
+}
+
+int plan_items(int T, int n) { return T / ITEM_TOKENS + (T < n ? T : n); }     // at most
+
+// Parts of K of the down-rank products: enough workgroups for the 256 CUs, each with some steps.
+int low_rank_parts(int T, int n, int R, int np, int K) {
+    const int tiles = plan_items(T, n) * ((np * R + BW - 1) / BW), steps = (K + BK - 1) / BK;
+    int parts = 1;
+    while (parts < MAX_PARTS && parts * tiles < 256 && steps >= 8 * parts) parts *= 2;
+    return parts;
+}
+
+hipError_t many_low_rank(const SharedArgs &a, const LowRank &L, int planes, hipStream_t st) {
+    Product g = {};
+    g.x = static_cast<const uint16_t *>(L.xv); g.K = L.K; g.N = L.np * a.R; g.gather = L.gather;
+    g.w[0] = L.a[0]; g.w[1] = L.a[1]; g.part = L.part;
+    const int parts = low_rank_parts(a.T, a.n, a.R, L.np, L.K);
+    hipError_t e = many_tiles<MODE_LOW_RANK>(a, g, planes, 64, (g.N + BW - 1) / BW, plan_items(a.T, a.n), parts, st);
+    if (e != hipSuccess) return e;
+    const int64_t quads = (int64_t)a.T * g.N / 4;
+    hipLaunchKernelGGL(k_low_rank_sum, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, st, a, L.part, parts, L.np, L.s);
     return hipGetLastError();
 }
 
@@ -716,21 +850,32 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Workspace layout, from the shapes and types alone.
 struct Layout {
-    size_t x, perm, ad, items, n_items, s, h, total;
+    size_t x, perm, ad, items, n_items, s, part, h, hrow, total;
 };
 Layout layout(int T, int H, int Is, int n, int R, bool x_f32, int hp) {
-    Layout l;
+    Layout l = {};
     size_t o = 0;
-    auto take = [&](size_t b) { const size_t at = o; o += up256(b); return at; };
-    const bool sorted = n > 0 && T > FEW_TOKENS;
-    const size_t nd = (size_t)(T < n ? T : n);
-    l.x = take(x_f32 ? (size_t)T * H * 4 : 0);
-    l.perm = take(sorted ? (size_t)T * 4 : 0);
-    l.ad = take(sorted ? (size_t)T * 4 : 0);
-    l.items = take(sorted ? ((size_t)T / ITEM_TOKENS + nd) * 16 : 0);
-    l.n_items = take(sorted ? 4 : 0);
-    l.s = take(n > 0 ? (size_t)T * 2 * 2 * R * 2 : 0);      // gate/up's, then down's
-    l.h = take((size_t)T * Is * 2 * hp);
+    auto take = [&](size_t b) { const size_t at = o; o += (b + 255) / 256 * 256; return at; };
+    const bool small = T <= FEW_TOKENS;
+    const size_t tf = few_frags(T);
+    auto packed = [&](int K, int p) { return (size_t)p * tf * ((K + 31) / 32) * 1024; };
+    l.s = take(n > 0 ? (size_t)T * 2 * R * 4 : 0);           // gate/up's, then down's
+    if (small) {
+        l.x = take(packed(H, x_f32 ? 2 : 1));
+        l.h = take(packed(Is, hp));
+        l.hrow = take(n > 0 ? (size_t)T * Is * 2 * hp : 0);
+    } else {
+        l.x = take(x_f32 ? (size_t)T * H * 4 : 0);
+        l.h = take((size_t)T * Is * 2 * hp);
+        if (n > 0) {
+            l.perm = take((size_t)T * 4);
+            l.ad = take((size_t)T * 4);
+            l.items = take((size_t)plan_items(T, n) * 16);
+            l.n_items = take(4);
+            const size_t gu = (size_t)low_rank_parts(T, n, R, 2, H) * 2, dn = (size_t)low_rank_parts(T, n, R, 1, Is);
+            l.part = take((gu > dn ? gu : dn) * T * R * 4);
+        }
+    }
     l.total = o;
     return l;
 }
@@ -746,18 +891,37 @@ size_t shared_workspace(int T, int H, int Is, int n, int R) {
 
 hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     char *base = static_cast<char *>(ws);
-    const int hp = a.out_bf16 ? 1 : 2;
-    a.sorted = a.n > 0 && a.T > FEW_TOKENS;
+    const int hp = a.out_bf16 ? 1 : 2, xp = a.x_bf16 ? 1 : 2;
     const Layout l = layout(a.T, a.H, a.Is, a.n, a.R, !a.x_bf16, hp);
-    const uint16_t *x = static_cast<const uint16_t *>(a.x);
+    auto u16 = [&](size_t at) { return reinterpret_cast<uint16_t *>(base + at); };
+    uint16_t *s = u16(l.s), *h = u16(l.h);
+    float *s32 = reinterpret_cast<float *>(s), *part = reinterpret_cast<float *>(base + l.part);
+    const bool small = a.T <= FEW_TOKENS;
+    a.sorted = a.n > 0 && !small;
+    SharedArgs ag = a, ad = a;                              // a half without adapters runs as if there were none
+    if (!a.gate_a && !a.up_a) ag.n = 0;
+    if (!a.down_a) ad.n = 0;
+    LowRank lx = {a.x, a.H, 2, 1, {a.gate_a, a.up_a}, s, s32, part}, lh = {h, a.Is, 1, 0, {a.down_a, nullptr}, s, s32, part};
+    Product gu = {}, dn = {};
+    gu.x = static_cast<const uint16_t *>(a.x); gu.K = a.H; gu.N = a.Is; gu.gather = 1;
+    gu.w[0] = a.gate; gu.w[1] = a.up; gu.b[0] = a.gate_b; gu.b[1] = a.up_b; gu.s = s; gu.s32 = s32; gu.h = h; gu.hp = hp;
+    dn.x = h; dn.K = a.Is; dn.N = a.H; dn.gather = 0;
+    dn.w[0] = a.down; dn.b[0] = a.down_b; dn.s = s; dn.s32 = s32; dn.out = a.out; dn.out_bf16 = a.out_bf16;
     hipError_t e;
+    if (small) {
+        gu.x = u16(l.x);
+        if (ad.n) { gu.hrow = u16(l.hrow); lh.xv = gu.hrow; }
+        if ((e = few_inputs(ag, lx, a.x_bf16 ? ACT_BF16 : ACT_F32, u16(l.x), st)) != hipSuccess) return e;
+        if ((e = few<true>(ag, gu, xp, st)) != hipSuccess) return e;
+        if ((e = few_inputs(ad, lh, hp == 1 ? ACT_BF16 : ACT_PLANES, nullptr, st)) != hipSuccess) return e;
+        return few<false>(ad, dn, hp, st);
+    }
     if (!a.x_bf16) {
-        uint16_t *planes = reinterpret_cast<uint16_t *>(base + l.x);
         const int64_t n = (int64_t)a.T * a.H;
         hipLaunchKernelGGL(k_split, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st,
-                           static_cast<const float *>(a.x), planes, n);
+                           static_cast<const float *>(a.x), u16(l.x), n);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        x = planes;
+        lx.xv = gu.x = u16(l.x);
     }
     if (a.sorted) {
         a.perm = reinterpret_cast<int32_t *>(base + l.perm);
@@ -766,23 +930,15 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
         a.n_items = reinterpret_cast<int32_t *>(base + l.n_items);
         hipLaunchKernelGGL(k_plan, dim3(1), dim3(PLAN_THREADS), 0, st, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
+        const int ng = ag.n, nd = ad.n;
+        ag = ad = a;
+        ag.n = ng;
+        ad.n = nd;
     }
-    uint16_t *s = reinterpret_cast<uint16_t *>(base + l.s);
-    uint16_t *h = reinterpret_cast<uint16_t *>(base + l.h);
-    float *s32 = reinterpret_cast<float *>(s);               // the same place, the same size
-    LowRank lx = {x, a.H, 2, 1, {a.gate_a, a.up_a}, s, s32}, lh = {h, a.Is, 1, 0, {a.down_a, nullptr}, s, s32};
-    Product gu = {}, dn = {};
-    gu.x = x; gu.K = a.H; gu.N = a.Is; gu.gather = 1;
-    gu.w[0] = a.gate; gu.w[1] = a.up; gu.b[0] = a.gate_b; gu.b[1] = a.up_b; gu.s = s; gu.s32 = s32; gu.h = h; gu.hp = hp;
-    dn.x = h; dn.K = a.Is; dn.N = a.H; dn.gather = 0;
-    dn.w[0] = a.down; dn.b[0] = a.down_b; dn.s = s; dn.s32 = s32; dn.out = a.out; dn.out_bf16 = a.out_bf16;
-    SharedArgs ag = a, ad = a;                              // a half without adapters runs as if there were none
-    if (!a.gate_a && !a.up_a) ag.n = 0;
-    if (!a.down_a) ad.n = 0;
-    if (ag.n && (e = a.x_bf16 ? launch_low_rank<1>(ag, lx, st) : launch_low_rank<2>(ag, lx, st)) != hipSuccess) return e;
-    if ((e = a.x_bf16 ? launch_product<true, 1>(ag, gu, st) : launch_product<true, 2>(ag, gu, st)) != hipSuccess) return e;
-    if (ad.n && (e = hp == 1 ? launch_low_rank<1>(ad, lh, st) : launch_low_rank<2>(ad, lh, st)) != hipSuccess) return e;
-    return hp == 1 ? launch_product<false, 1>(ad, dn, st) : launch_product<false, 2>(ad, dn, st);
+    if (ag.n && (e = many_low_rank(ag, lx, xp, st)) != hipSuccess) return e;
+    if ((e = many<MODE_GATE_UP>(ag, gu, xp, st)) != hipSuccess) return e;
+    if (ad.n && (e = many_low_rank(ad, lh, hp, st)) != hipSuccess) return e;
+    return many<MODE_DOWN>(ad, dn, hp, st);
 }
 
 }  // namespace moe

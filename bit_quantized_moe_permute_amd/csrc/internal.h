@@ -103,7 +103,7 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t st);
 // ffn_shared.hip: the shared expert with low-rank adapters
 constexpr int MAX_ADAPTERS = 4096, MAX_RANK = 256;
 constexpr int FEW_TOKENS = 64;           // up to here the weight rows stream past all tokens at once
-constexpr int ITEM_TOKENS = 16;          // tokens of one adapter per work item of the down-rank products
+constexpr int ITEM_TOKENS = 64;          // tokens of one adapter per work item of the down-rank products
 struct SharedArgs {
     int T, H, Is;
     const void *x;
@@ -122,21 +122,24 @@ struct SharedArgs {
     int4 *items;                         // adapter, first sorted position, tokens
 };
 struct LowRank {
-    const uint16_t *x;                   // [P][T][K] bf16 planes
+    const void *xv;                      // [P][T][K] bf16 planes, or [T][K] fp32 (few tokens)
     int K, np;
     int gather;                          // rows of x are tokens (through perm), not sorted positions
     const uint16_t *a[2];
     uint16_t *s;                         // [T][np][hi, lo][R], many tokens
     float *s32;                          // [T][np][R], few tokens
+    float *part;                         // [parts][T][np][R], many tokens
 };
 struct Product {
-    const uint16_t *x;                   // [P][T][K] bf16 planes
+    const uint16_t *x;                   // [P][T][K] bf16 planes, or (few tokens) packed
     int K, N, gather;
     const uint16_t *w[2], *b[2];
     const uint16_t *s;                   // [T][np][hi, lo][R], many tokens
     const float *s32;                    // [T][np][R], few tokens
-    uint16_t *h;                         // gate/up: [hp][T][N] bf16 planes, by sorted position
+    uint16_t *h;                         // gate/up: [hp][T][N] bf16 planes by sorted position, or (few tokens) packed
+    uint16_t *hrow;                      // gate/up, few tokens: [hp][T][N] too, if set
     int hp;
+    float *part;                         // down-rank, many tokens
     void *out;                           // down: [T][N], by token
     int out_bf16;
 };
