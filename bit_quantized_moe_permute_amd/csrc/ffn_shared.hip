@@ -7,7 +7,7 @@
 //
 //   split      fp32 activations as two bf16 planes hi + lo = bf16(x), bf16(x - hi): 16 significant bits
 //   plan       (many tokens) the tokens ordered by adapter, and work items of up to 64 tokens of one adapter
-//   down-rank  s[t][r] = c_a (A_a[r] . x[t]) for each token's own adapter, in fp32 or (many tokens) as two bf16 parts
+//   down-rank  s[t][r] = c_a (A_a[r] . x[t]) for each token's own adapter, as two bf16 parts
 //   gate/up    weight rows x tokens; the adapters' B_a s in the epilogue; SwiGLU; h as one bf16 plane (bf16 result)
 //              or two (fp32 result, whose error then stays near 2^-17)
 //   down       the same product with Wd and h
@@ -77,7 +77,7 @@ template <typename T> __device__ __forceinline__ T uniform_at(const T *p, int64_
 }
 
 __device__ __forceinline__ int rank_of(const SharedArgs &a, int ad) {
-    return a.rank ? min(max(a.rank[ad], 0), a.R) : a.R;
+    return a.rank ? min(max(uniform_at(a.rank, ad), 0), a.R) : a.R;
 }
 
 // Adapter of row `pos` (sorted position with a plan, else token), -1 for none.
@@ -188,22 +188,26 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a) {
 // Few tokens: what a product reads of its activations.
 //
 // Packed activations [P][TF][steps][64 lanes][8]: the matrix instruction's operand of 16 tokens and 32 of K in lane order, so
-// that a wave reads 1 KiB in a row.  Lane l holds token l % 16 and k = 8 (l / 16) .. + 7; behind the end of K zeros.
+// that a wave reads 1 KiB in a row.  Lane l holds token l % 16 and k = 8 (l / 16) .. + 7; steps of 32 up to a multiple of 2048,
+// zeros behind the end of K.
 // Read from rows instead, the 64 lanes' 16-byte pieces would lie in 64 places, and a wave's load would take four times as
 // long (measured as the bound of the row-reading kernel at 24 tokens: 18.5 us against 10.6 for the gate/up product).
 //
-// Low-rank results s[t][proj][r] = scale_a (A_a[r] . x[t]) in fp32, one wave per (token, row): no wait but that for the
-// token's adapter index and that for the row, and no exchange but the wave's own sum.
+// Low-rank results s[t][proj][hi, lo][r] = scale_a (A_a[r] . x[t]) as two bf16 parts, one wave per (token, row): no wait but that
+// for the token's adapter index and that for the row, and no exchange but the wave's own sum.
 // ---------------------------------------------------------------------------
 // TF: fragments of 16 tokens, rounded up to what the kernels are built for; those behind the last token hold anything.
 __host__ __device__ __forceinline__ int few_frags(int T) { return T <= 16 ? 1 : T <= 32 ? 2 : 4; }
+
+constexpr int FEW_ROUND = 2048;
+__host__ __device__ __forceinline__ int few_steps(int K) { return (K + FEW_ROUND - 1) / FEW_ROUND * (FEW_ROUND / 32); }
 
 enum { ACT_BF16 = 0, ACT_PLANES = 1, ACT_F32 = 2 };          // x: one bf16 plane, two of them, fp32
 
 template <int SRC>
 __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uint16_t *packed, int pack_blocks) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int K = L.K, steps = (K + 31) / 32;
+    const int K = L.K, steps = few_steps(K);
     if ((int)blockIdx.x < pack_blocks) {
         const int i = blockIdx.x * 4 + wave, tf = (a.T + 15) / 16, f = i / steps, step = i - f * steps;
         if (f >= tf) return;
@@ -228,7 +232,7 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
     const int nrows = L.np * a.R, id = (blockIdx.x - pack_blocks) * 4 + wave;
     if (id >= a.T * nrows) return;
     const int t = id / nrows, rr = id - t * nrows, proj = rr / a.R, r = rr - proj * a.R;
-    const int ad = adapter_at(a, t);
+    const int token_ad = uniform_at(a.token_adapter, t), ad = (unsigned)token_ad < (unsigned)a.n ? token_ad : -1;
     const uint16_t *A = proj ? L.a[1] : L.a[0];
     if (ad < 0 || !A) return;                                // not read either
     A += ((int64_t)ad * a.R + r) * K;
@@ -268,8 +272,13 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
             }
         }
     }
-    const float y = wave_sum(acc[0] + acc[1]);
-    if (lane == 0) L.s32[(int64_t)id] = r < rank_of(a, ad) ? y * (a.scale ? a.scale[ad] : 1.f) : 0.f;
+    float y = wave_sum(acc[0] + acc[1]);
+    y = r < rank_of(a, ad) ? y * (a.scale ? uniform_at(a.scale, ad) : 1.f) : 0.f;
+    uint16_t *o = L.s + ((int64_t)t * L.np + proj) * 2 * a.R + r;
+    if (lane == 0) {
+        o[0] = __builtin_bit_cast(uint16_t, (__bf16)y);
+        o[a.R] = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(y));
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -280,7 +289,6 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
 // An adapter's term is formed per token in fp32, wave w taking tokens w, w + NW, ...; its loads go out with the weights'.
 // Sixteen waves for few operands per step; eight, with twice the registers, where a step has four or more of them.
 // ---------------------------------------------------------------------------
-constexpr int FEW_ROUND = 2048;
 constexpr int few_waves(int P, int TF) { return P * TF >= 4 ? 8 : 16; }
 
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
@@ -290,100 +298,113 @@ template <bool GU, int P, int TF, bool AD>
 __global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Product g) {
     constexpr int NW = few_waves(P, TF), SLICE = FEW_ROUND / NW;         // K of a wave per round
     constexpr int LINE = SLICE / 8, LOADS = 16 * LINE / 64;              // chunks of a row's piece; loads of 64 chunks
-    constexpr int TW = TF * 16 / NW;                                     // tokens per wave (adapters' terms)
+    constexpr int TW = TF * 16 / NW, NP = GU ? 2 : 1;                    // tokens per wave (adapters' terms)
     __shared__ __attribute__((aligned(1024))) uint4 ring[2][NW][16 * LINE];
-    __shared__ float low[TF * 16][17];
-    float (*red)[TF][16][17] = reinterpret_cast<float (*)[TF][16][17]>(ring);      // after the last product
-    static_assert(sizeof(float) * NW * TF * 16 * 17 <= sizeof(ring), "");
+    __shared__ float low[TF * 16][16];
+    f32x4_t (*red)[TF][64] = reinterpret_cast<f32x4_t (*)[TF][64]>(ring);         // after the last product
+    static_assert(sizeof(f32x4_t) * NW * TF * 64 <= sizeof(ring), "");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
-    const int K = g.K, r0 = blockIdx.x * (GU ? 8 : 16);
-    // load j fills 64 / LINE rows' pieces; a chunk behind the row's end repeats the piece's first (its products meet zero
-    // activations), rows behind the last repeat it (their sums are not stored)
-    const int rf = GU ? min(r0, g.N - 8) : r0;                           // gate/up: workgroups behind the last rows write zeros
-    uint64_t base[2];
-    base[0] = uniform64((uint64_t)(uintptr_t)(g.w[0] + (int64_t)rf * K));
-    base[1] = GU ? uniform64((uint64_t)(uintptr_t)(g.w[1] + (int64_t)rf * K)) : base[0];
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(las_ptr)ring + wave * (16u * LINE * 16u);
-    const int rounds = (K + FEW_ROUND - 1) / FEW_ROUND, steps = (K + 31) / 32;
-    auto issue = [&](int r, int b) {
+    const int K = g.K, r0 = blockIdx.x * (GU ? 8 : 16), hsteps = few_steps(g.N);
+    if (GU && r0 >= g.N) {                                               // packed rows end in zeros
+        for (int e = threadIdx.x; e < g.hp * TF * 16; e += 64 * NW) {
+            const int f = e >> 4, c = e & 15;                            // f: plane and fragment
+            reinterpret_cast<uint4 *>(g.h)[((int64_t)f * hsteps + r0 / 32) * 64 + r0 % 32 / 8 * 16 + c] = make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
+    // Load j fills 64 / LINE rows' pieces: lane's row j * 64 / LINE + lane / LINE, chunk c = lane % LINE ^ row.
+    constexpr int RPL = 64 / LINE;                                       // rows per load
+    const uint64_t w0 = uniform64((uint64_t)(uintptr_t)(g.w[0] + (int64_t)r0 * K));
+    const uint64_t w1 = GU ? uniform64((uint64_t)(uintptr_t)(g.w[1] + (int64_t)r0 * K)) : w0;
+    const int row0 = lane / LINE, c0 = (lane % LINE) ^ row0;
+    const uint32_t stride = 2u * (uint32_t)K, lds0 = (uint32_t)(uintptr_t)(las_ptr)ring + wave * (16u * LINE * 16u);
+    const int rows = GU ? 8 : min(16, g.N - r0);
+    auto issue = [&](int r, int b) __attribute__((always_inline)) {
         const int k = r * FEW_ROUND + wave * SLICE;
         if (k >= K) return;
+        const bool whole = k + SLICE <= K;
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
-            const int row = j * (64 / LINE) + lane / LINE, c = lane % LINE ^ row;
-            uint32_t o = 2u * ((uint32_t)(GU ? row & 7 : min(row, g.N - 1 - r0)) * (uint32_t)K + (uint32_t)k);
-            if (k + 8 * c < K) o += 16u * c;
-            load_to_lds(base[GU && j >= LOADS / 2], o, lds0 + b * (uint32_t)(sizeof(ring) / 2) + j * 1024u);
+            const int jr = GU ? j % (LOADS / 2) * RPL : j * RPL;         // first row of the load in its matrix
+            const int c = c0 ^ (j * RPL);
+            // rows behind the last repeat it (their sums are not stored)
+            uint32_t o = (uint32_t)(GU ? jr + row0 : min(jr + row0, rows - 1)) * stride + 2u * (uint32_t)k;
+            // a chunk behind the row's end repeats the piece's first (its products meet zero activations)
+            o += whole || k + 8 * c < K ? 16u * c : 0u;
+            load_to_lds(GU && j >= LOADS / 2 ? w1 : w0, o, lds0 + b * (uint32_t)(sizeof(ring) / 2) + j * 1024u);
         }
     };
     // An adapter's term for token f * NW + wave: lane (row lr = lane / 4, lane % 4) takes rank values 8 (lane % 4) .. + 7 of each
     // 32, so that four lanes in a row read 64 bytes of one row of B.
-    const int lr = lane >> 2, half = GU ? lr >> 3 : 0, wr = GU ? r0 + (lr & 7) : r0 + lr;
+    const int lr = lane >> 2, half = GU ? lr >> 3 : 0, wr = GU ? r0 + (lr & 7) : r0 + lr, r4 = 8 * (lane & 3);
     const uint16_t *const gb = half ? g.b[1] : g.b[0];
-    int ad[TW];
-    uint4 bw[TW];
-    float4 ss[TW][2];
-    auto load_low = [&](int c) {
-        const int r = 32 * c + 8 * (lane & 3);
+    const bool has = wr < g.N && gb;
+    int ad[TW], rank[TW];
+    uint4 bw[TW], hi[TW], lo[TW];
+    auto load_low = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int f = 0; f < TW; ++f) {
-            bw[f] = make_uint4(0, 0, 0, 0);
-            ss[f][0] = ss[f][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (ad[f] >= 0 && r < a.R && wr < g.N && gb) {
-                bw[f] = load16(gb + ((int64_t)ad[f] * g.N + wr) * a.R + r);
-                const float4 *p = reinterpret_cast<const float4 *>(
-                    g.s32 + ((int64_t)(f * NW + wave) * (GU ? 2 : 1) + half) * a.R + r);
-                ss[f][0] = p[0];
-                ss[f][1] = p[1];
+            bw[f] = hi[f] = lo[f] = make_uint4(0, 0, 0, 0);
+            if (ad[f] < 0 || 32 * c >= rank[f]) continue;                // uniform
+            if (has && 32 * c + r4 < rank[f]) {
+                bw[f] = load16(gb + ((int64_t)ad[f] * g.N + wr) * a.R + 32 * c + r4);
+                const uint16_t *p = g.s + ((int64_t)(f * NW + wave) * NP + half) * 2 * a.R + 32 * c + r4;
+                hi[f] = load16(p);
+                lo[f] = load16(p + a.R);
             }
         }
     };
     f32x4_t acc[TF];
 #pragma unroll
     for (int f = 0; f < TF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    const uint4 *const xp = reinterpret_cast<const uint4 *>(g.x);
-    const int64_t plane = (int64_t)TF * steps * 64;
     constexpr int SPW = SLICE / 32;                                      // steps of a wave per round
-    constexpr int XB = TF * P <= 2 ? 2 * SPW : TF * P == 4 ? SPW : SPW / 2;      // steps whose activations are loaded together
-    for (int r = 0; r < rounds; r += 2) {
-        if (r) wait_reads();                                              // the slices of the rounds before are read
-        issue(r, 0);
-        if (r + 1 < rounds) issue(r + 1, 1);
-        if constexpr (AD) {
-            if (r == 0) {
+    constexpr int XB = TF * P <= 2 ? SPW : TF * P == 4 ? SPW / 2 : SPW / 4;      // steps whose activations are loaded together
+    const int rounds = (K + FEW_ROUND - 1) / FEW_ROUND, steps = few_steps(K);
+    const uint4 *xw = reinterpret_cast<const uint4 *>(g.x) + wave * (SPW * 64) + lane;
+    uint4 x[XB][TF][P];
+    auto load_x = [&](int i0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int f = 0; f < TF; ++f)
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const uint4 *src = xw + (int64_t)(p * TF + f) * steps * 64 + i0 * 64;
+#pragma unroll
+                for (int i = 0; i < XB; ++i) x[i][f][p] = src[i * 64];
+            }
+    };
+    for (int r = 0; r < rounds; ++r, xw += FEW_ROUND / 32 * 64) {
+        const int b = r & 1;
+        if (r == 0) {
+            issue(0, 0);
+            if (rounds > 1) issue(1, 1);
+            if constexpr (AD) {
 #pragma unroll
                 for (int f = 0; f < TW; ++f) {
                     const int t = f * NW + wave, id = t < a.T ? uniform_at(a.token_adapter, t) : -1;
                     ad[f] = (unsigned)id < (unsigned)a.n ? id : -1;
+                    rank[f] = ad[f] < 0 ? 0 : rank_of(a, ad[f]);
                 }
                 load_low(0);
             }
         }
-        const int s0 = r * (FEW_ROUND / 32) + wave * SPW;
-        auto step_of = [&](int i) { return s0 + i / SPW * (FEW_ROUND / 32) + i % SPW; };
+        if (r * FEW_ROUND + wave * SLICE >= K) break;                    // no slice in this round or a later one
+        const uint4 *const slice = ring[b][wave] + i16 * LINE;
 #pragma unroll
-        for (int ib = 0; ib < 2 * SPW; ib += XB) {
-            if (step_of(ib) >= steps) break;
-            uint4 x[XB][TF][P];
-#pragma unroll
-            for (int i = 0; i < XB; ++i)
-#pragma unroll
-                for (int f = 0; f < TF; ++f)
-#pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const int st = step_of(ib + i);
-                        x[i][f][p] = st < steps ? xp[p * plane + ((int64_t)f * steps + st) * 64 + lane] : make_uint4(0, 0, 0, 0);
-                    }
-            if (ib == 0) wait_loads();
+        for (int i0 = 0; i0 < SPW; i0 += XB) {
+            load_x(i0);
+            if (i0 == 0) wait_loads();
 #pragma unroll
             for (int i = 0; i < XB; ++i) {
-                if (step_of(ib + i) >= steps) break;
-                const uint4 w = ring[(ib + i) / SPW][wave][i16 * LINE + ((4 * ((ib + i) % SPW) + q) ^ i16)];
+                const uint4 w = slice[(4 * (i0 + i) + q) ^ i16];
 #pragma unroll
                 for (int f = 0; f < TF; ++f)
 #pragma unroll
                     for (int p = 0; p < P; ++p) acc[f] = mfma16(w, x[i][f][p], acc[f]);
             }
+        }
+        if (r + 2 < rounds) {
+            wait_reads();                                                // the slice is read
+            issue(r + 2, b);
         }
     }
     if constexpr (AD) {
@@ -392,16 +413,9 @@ __global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Pro
             if (c) load_low(c);
 #pragma unroll
             for (int f = 0; f < TW; ++f) {
-                const int rank = (ad[f] < 0 ? 0 : rank_of(a, ad[f])) - (32 * c + 8 * (lane & 3));     // of this lane's eight
-                const uint4 b = keep_first(bw[f], rank);
-                const uint32_t bb[4] = {b.x, b.y, b.z, b.w};
-                const float sv[8] = {ss[f][0].x, ss[f][0].y, ss[f][0].z, ss[f][0].w,
-                                     ss[f][1].x, ss[f][1].y, ss[f][1].z, ss[f][1].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    d[f] = __fmaf_rn(__uint_as_float(bb[i] << 16), sv[2 * i], d[f]);
-                    d[f] = __fmaf_rn(__uint_as_float(bb[i] & 0xFFFF0000u), sv[2 * i + 1], d[f]);
-                }
+                if (32 * c >= rank[f]) continue;
+                const uint4 w = rank[f] - 32 * c >= 32 ? bw[f] : keep_first(bw[f], rank[f] - 32 * c - r4);
+                d[f] = dot8(w, lo[f], dot8(w, hi[f], d[f]));
             }
         }
 #pragma unroll
@@ -414,9 +428,7 @@ __global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Pro
     wait_loads();                                            // a wave without steps has none; the ring is free after the barrier
     __syncthreads();
 #pragma unroll
-    for (int f = 0; f < TF; ++f)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) red[wave][f][i16][4 * q + v] = acc[f][v];       // [token][row]
+    for (int f = 0; f < TF; ++f) red[wave][f][lane] = acc[f];            // lane: token i16, rows 4 q .. + 3
     __syncthreads();
     constexpr int NR = GU ? 8 : 16;
     for (int e = threadIdx.x; e < TF * 16 * NR; e += 64 * NW) {
@@ -424,20 +436,20 @@ __global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Pro
         if (tok >= a.T) continue;
         float y = AD ? low[tok][r] : 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) y += red[w][f][c][r];
+        for (int w = 0; w < NW; ++w) y += red[w][f][(r >> 2) * 16 + c][r & 3];
         if constexpr (GU) {
             float up = AD ? low[tok][r + 8] : 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) up += red[w][f][c][r + 8];
-            const int i = r0 + r, hsteps = (g.N + 31) / 32;
-            const float h = r0 < g.N ? silu_mul(y, up) : 0.f;           // packed rows end in zeros
-            const uint16_t hi = __builtin_bit_cast(uint16_t, (__bf16)h), lo = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(h));
+            for (int w = 0; w < NW; ++w) up += red[w][f][(r >> 2) * 16 + 32 + c][r & 3];
+            const int i = r0 + r;
+            const float h = silu_mul(y, up);
+            const uint16_t top = __builtin_bit_cast(uint16_t, (__bf16)h), rest = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(h));
             const int64_t o = (((int64_t)f * hsteps + i / 32) * 64 + (i % 32 / 8) * 16 + c) * 8 + i % 8;
-            g.h[o] = hi;
-            if (g.hp == 2) g.h[(int64_t)TF * hsteps * 512 + o] = lo;
-            if (g.hrow && r0 < g.N) {                                    // for the down-rank products
-                g.hrow[(int64_t)tok * g.N + i] = hi;
-                if (g.hp == 2) g.hrow[(int64_t)a.T * g.N + (int64_t)tok * g.N + i] = lo;
+            g.h[o] = top;
+            if (g.hp == 2) g.h[(int64_t)TF * hsteps * 512 + o] = rest;
+            if (g.hrow) {                                                // for the down-rank products
+                g.hrow[(int64_t)tok * g.N + i] = top;
+                if (g.hp == 2) g.hrow[(int64_t)a.T * g.N + (int64_t)tok * g.N + i] = rest;
             }
         } else {
             if (r0 + r >= g.N) continue;
@@ -771,7 +783,7 @@ template <bool GU, int P, bool AD>
 hipError_t launch_few(const SharedArgs &a, const Product &g, hipStream_t st) {
     // gate/up: whole steps of the packed h, whose last rows may be zeros
     const int tf = few_frags(a.T);
-    const dim3 grd((unsigned)(GU ? (g.N + 31) / 32 * 4 : (g.N + 15) / 16)), blk((unsigned)(64 * few_waves(P, tf)));
+    const dim3 grd((unsigned)(GU ? few_steps(g.N) * 4 : (g.N + 15) / 16)), blk((unsigned)(64 * few_waves(P, tf)));
     if (tf == 1) hipLaunchKernelGGL((k_few<GU, P, 1, AD>), grd, blk, 0, st, a, g);
     else if (tf == 2) hipLaunchKernelGGL((k_few<GU, P, 2, AD>), grd, blk, 0, st, a, g);
     else hipLaunchKernelGGL((k_few<GU, P, 4, AD>), grd, blk, 0, st, a, g);
@@ -786,7 +798,7 @@ hipError_t few(const SharedArgs &a, const Product &g, int planes, hipStream_t st
 
 // Packs the activations (packed) and forms the low-rank results (a.n), one launch for both.
 hipError_t few_inputs(const SharedArgs &a, const LowRank &L, int src, uint16_t *packed, hipStream_t st) {
-    const int pack = packed ? ((a.T + 15) / 16 * ((L.K + 31) / 32) + 3) / 4 : 0;
+    const int pack = packed ? ((a.T + 15) / 16 * few_steps(L.K) + 3) / 4 : 0;
     const int low = a.n ? (a.T * L.np * a.R + 3) / 4 : 0;
     if (!pack && !low) return hipSuccess;
     const dim3 grd((unsigned)(pack + low)), blk(256);
@@ -858,7 +870,7 @@ Layout layout(int T, int H, int Is, int n, int R, bool x_f32, int hp) {
     auto take = [&](size_t b) { const size_t at = o; o += (b + 255) / 256 * 256; return at; };
     const bool small = T <= FEW_TOKENS;
     const size_t tf = few_frags(T);
-    auto packed = [&](int K, int p) { return (size_t)p * tf * ((K + 31) / 32) * 1024; };
+    auto packed = [&](int K, int p) { return (size_t)p * tf * few_steps(K) * 1024; };
     l.s = take(n > 0 ? (size_t)T * 2 * R * 4 : 0);           // gate/up's, then down's
     if (small) {
         l.x = take(packed(H, x_f32 ? 2 : 1));
@@ -895,18 +907,18 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     const Layout l = layout(a.T, a.H, a.Is, a.n, a.R, !a.x_bf16, hp);
     auto u16 = [&](size_t at) { return reinterpret_cast<uint16_t *>(base + at); };
     uint16_t *s = u16(l.s), *h = u16(l.h);
-    float *s32 = reinterpret_cast<float *>(s), *part = reinterpret_cast<float *>(base + l.part);
+    float *part = reinterpret_cast<float *>(base + l.part);
     const bool small = a.T <= FEW_TOKENS;
     a.sorted = a.n > 0 && !small;
     SharedArgs ag = a, ad = a;                              // a half without adapters runs as if there were none
     if (!a.gate_a && !a.up_a) ag.n = 0;
     if (!a.down_a) ad.n = 0;
-    LowRank lx = {a.x, a.H, 2, 1, {a.gate_a, a.up_a}, s, s32, part}, lh = {h, a.Is, 1, 0, {a.down_a, nullptr}, s, s32, part};
+    LowRank lx = {a.x, a.H, 2, 1, {a.gate_a, a.up_a}, s, part}, lh = {h, a.Is, 1, 0, {a.down_a, nullptr}, s, part};
     Product gu = {}, dn = {};
     gu.x = static_cast<const uint16_t *>(a.x); gu.K = a.H; gu.N = a.Is; gu.gather = 1;
-    gu.w[0] = a.gate; gu.w[1] = a.up; gu.b[0] = a.gate_b; gu.b[1] = a.up_b; gu.s = s; gu.s32 = s32; gu.h = h; gu.hp = hp;
+    gu.w[0] = a.gate; gu.w[1] = a.up; gu.b[0] = a.gate_b; gu.b[1] = a.up_b; gu.s = s; gu.h = h; gu.hp = hp;
     dn.x = h; dn.K = a.Is; dn.N = a.H; dn.gather = 0;
-    dn.w[0] = a.down; dn.b[0] = a.down_b; dn.s = s; dn.s32 = s32; dn.out = a.out; dn.out_bf16 = a.out_bf16;
+    dn.w[0] = a.down; dn.b[0] = a.down_b; dn.s = s; dn.out = a.out; dn.out_bf16 = a.out_bf16;
     hipError_t e;
     if (small) {
         gu.x = u16(l.x);
