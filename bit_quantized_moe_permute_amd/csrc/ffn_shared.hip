@@ -3,9 +3,9 @@
 //   g = Wg x + c_a Bg_a (Ag_a x),  u likewise,  h = silu(g) * u,  out = Wd h + c_a Bd_a (Ad_a h)
 //
 // with a = token_adapter[t] (no adapter terms where it is outside 0 .. n_adapters - 1).  All products run on the bf16
-// matrix cores with fp32 sums.  Launches: [split] [plan] [down-rank] gate/up [down-rank] down --
+// matrix cores with fp32 sums; fp32 activations are read as two bf16 parts bf16(x), bf16(x - that): 16 significant bits.
+// Launches: [plan] [down-rank] gate/up [down-rank] down --
 //
-//   split      fp32 activations as two bf16 planes hi + lo = bf16(x), bf16(x - hi): 16 significant bits
 //   plan       (many tokens) the tokens ordered by adapter, and work items of up to 64 tokens of one adapter
 //   down-rank  s[t][r] = c_a (A_a[r] . x[t]) for each token's own adapter, as two bf16 parts
 //   gate/up    weight rows x tokens; the adapters' B_a s in the epilogue; SwiGLU; h as one bf16 plane (bf16 result)
@@ -93,25 +93,22 @@ __device__ __forceinline__ const uint16_t *low_rank_row(const SharedArgs &a, con
 }
 
 // ---------------------------------------------------------------------------
-// fp32 activations -> bf16 planes [2][T][H]
-// ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void k_split(const float *__restrict__ x, uint16_t *__restrict__ planes, int64_t n) {
-    const int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
-    if (i >= n) return;
-    const float4 v = *reinterpret_cast<const float4 *>(x + i);
-    *reinterpret_cast<uint2 *>(planes + i) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-    *reinterpret_cast<uint2 *>(planes + n + i) =
-        make_uint2(pack_bf16(bf16_rest(v.x), bf16_rest(v.y)), pack_bf16(bf16_rest(v.z), bf16_rest(v.w)));
-}
-
-// ---------------------------------------------------------------------------
 // plan (many tokens): tokens ordered by adapter (those without one last), and items of up to ITEM_TOKENS tokens of one adapter.
-// One workgroup.  Within an adapter the order is that of LDS atomics and may differ between calls: a row's place in
+// One workgroup; the launch's others bring fp32 activations into bf16 planes [2][T][H].  Within an adapter the order is that of LDS atomics and may differ between calls: a row's place in
 // a tile changes no bit of its result.
 // ---------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024;
 
-__global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a) {
+__global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a, uint16_t *planes, int plans) {
+    if ((int)blockIdx.x >= plans) {
+        const int64_t i = 4 * ((int64_t)(blockIdx.x - plans) * PLAN_THREADS + threadIdx.x), m = (int64_t)a.T * a.H;
+        if (i >= m) return;
+        const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.x) + i);
+        *reinterpret_cast<uint2 *>(planes + i) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        *reinterpret_cast<uint2 *>(planes + m + i) =
+            make_uint2(pack_bf16(bf16_rest(v.x), bf16_rest(v.y)), pack_bf16(bf16_rest(v.z), bf16_rest(v.w)));
+        return;
+    }
     __shared__ int count[MAX_ADAPTERS + 1], begin[MAX_ADAPTERS + 2], item0[MAX_ADAPTERS + 1], wsum[2][PLAN_THREADS / 64];
     const int n = a.n, tid = threadIdx.x;
     for (int i = tid; i <= n; i += PLAN_THREADS) count[i] = 0;
@@ -187,7 +184,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a) {
 // ---------------------------------------------------------------------------
 // Few tokens: what a product reads of its activations.
 //
-// Packed activations [P][TF][steps][64 lanes][8]: the matrix instruction's operand of 16 tokens and 32 of K in lane order, so
+// Tokens go in groups of up to 64.  Packed activations [group][P][TF][steps][64 lanes][8]: the matrix instruction's operand of 16 tokens and 32 of K in lane order, so
 // that a wave reads 1 KiB in a row.  Lane l holds token l % 16 and k = 8 (l / 16) .. + 7; steps of 32 up to a multiple of 2048,
 // zeros behind the end of K.
 // Read from rows instead, the 64 lanes' 16-byte pieces would lie in 64 places, and a wave's load would take four times as
@@ -199,6 +196,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a) {
 // TF: fragments of 16 tokens, rounded up to what the kernels are built for; those behind the last token hold anything.
 __host__ __device__ __forceinline__ int few_frags(int T) { return T <= 16 ? 1 : T <= 32 ? 2 : 4; }
 
+__host__ __device__ __forceinline__ int few_groups(int T) { return (T + FEW_TOKENS - 1) / FEW_TOKENS; }
 constexpr int FEW_ROUND = 2048;
 __host__ __device__ __forceinline__ int few_steps(int K) { return (K + FEW_ROUND - 1) / FEW_ROUND * (FEW_ROUND / 32); }
 
@@ -209,9 +207,11 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int K = L.K, steps = few_steps(K);
     if ((int)blockIdx.x < pack_blocks) {
-        const int i = blockIdx.x * 4 + wave, tf = (a.T + 15) / 16, f = i / steps, step = i - f * steps;
-        if (f >= tf) return;
-        const int t = f * 16 + (lane & 15), k = step * 32 + 8 * (lane >> 4);
+        constexpr int P = SRC == ACT_F32 ? 2 : 1;
+        const int i = blockIdx.x * 4 + wave, tf = few_frags(a.T), frag = i / steps, step = i - frag * steps;
+        const int grp = frag / tf, f = frag - grp * tf;
+        if (frag * 16 >= a.T) return;
+        const int t = frag * 16 + (lane & 15), k = step * 32 + 8 * (lane >> 4);
         uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
         if (t < a.T && k < K) {
             if constexpr (SRC == ACT_F32) {
@@ -224,9 +224,9 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
                 hi = load16(static_cast<const uint16_t *>(L.xv) + (int64_t)t * K + k);
             }
         }
-        uint4 *o = reinterpret_cast<uint4 *>(packed);
-        o[(int64_t)i * 64 + lane] = hi;
-        if constexpr (SRC == ACT_F32) o[((int64_t)few_frags(a.T) * steps + i) * 64 + lane] = lo;
+        uint4 *o = reinterpret_cast<uint4 *>(packed) + ((int64_t)(grp * P * tf + f) * steps + step) * 64 + lane;
+        o[0] = hi;
+        if constexpr (SRC == ACT_F32) o[(int64_t)tf * steps * 64] = lo;
         return;
     }
     const int nrows = L.np * a.R, id = (blockIdx.x - pack_blocks) * 4 + wave;
@@ -283,20 +283,19 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
 
 // ---------------------------------------------------------------------------
 // Few tokens, a product: one workgroup streams 16 weight rows (gate/up: 8 gate rows and the same 8 of up) once.  Its waves
-// split K: in each round of 2048 a wave takes 2048 / NW of every row, through LDS of its own that direct-to-LDS loads fill
-// with whole 256- or 512-byte pieces of rows (two rounds in flight: 128 KiB per workgroup).  Chunk c of row r lies at position
+// split K: in each round of 2048 a wave takes 256 of every row, through LDS of its own that direct-to-LDS loads fill with
+// 512-byte pieces of rows (two rounds in flight: 128 KiB per workgroup).  Chunk c of row r lies at position
 // c ^ r, so that sixteen rows' reads of one chunk column touch every bank once.  The waves' sums meet in LDS.
 // An adapter's term is formed per token in fp32, wave w taking tokens w, w + NW, ...; its loads go out with the weights'.
-// Sixteen waves for few operands per step; eight, with twice the registers, where a step has four or more of them.
 // ---------------------------------------------------------------------------
-constexpr int few_waves(int P, int TF) { return P * TF >= 4 ? 8 : 16; }
+constexpr int FEW_WAVES = 8;
 
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 template <bool GU, int P, int TF, bool AD>
-__global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Product g) {
-    constexpr int NW = few_waves(P, TF), SLICE = FEW_ROUND / NW;         // K of a wave per round
+__global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g) {
+    constexpr int NW = FEW_WAVES, SLICE = FEW_ROUND / NW;         // K of a wave per round
     constexpr int LINE = SLICE / 8, LOADS = 16 * LINE / 64;              // chunks of a row's piece; loads of 64 chunks
     constexpr int TW = TF * 16 / NW, NP = GU ? 2 : 1;                    // tokens per wave (adapters' terms)
     __shared__ __attribute__((aligned(1024))) uint4 ring[2][NW][16 * LINE];
@@ -305,10 +304,12 @@ __global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Pro
     static_assert(sizeof(f32x4_t) * NW * TF * 64 <= sizeof(ring), "");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
     const int K = g.K, r0 = blockIdx.x * (GU ? 8 : 16), hsteps = few_steps(g.N);
+    const int t0 = blockIdx.y * FEW_TOKENS;                              // this workgroup's tokens
+    uint16_t *const h = g.h + (int64_t)blockIdx.y * g.hp * TF * hsteps * 512;
     if (GU && r0 >= g.N) {                                               // packed rows end in zeros
         for (int e = threadIdx.x; e < g.hp * TF * 16; e += 64 * NW) {
             const int f = e >> 4, c = e & 15;                            // f: plane and fragment
-            reinterpret_cast<uint4 *>(g.h)[((int64_t)f * hsteps + r0 / 32) * 64 + r0 % 32 / 8 * 16 + c] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4 *>(h)[((int64_t)f * hsteps + r0 / 32) * 64 + r0 % 32 / 8 * 16 + c] = make_uint4(0, 0, 0, 0);
         }
         return;
     }
@@ -348,7 +349,7 @@ __global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Pro
             if (ad[f] < 0 || 32 * c >= rank[f]) continue;                // uniform
             if (has && 32 * c + r4 < rank[f]) {
                 bw[f] = load16(gb + ((int64_t)ad[f] * g.N + wr) * a.R + 32 * c + r4);
-                const uint16_t *p = g.s + ((int64_t)(f * NW + wave) * NP + half) * 2 * a.R + 32 * c + r4;
+                const uint16_t *p = g.s + ((int64_t)(t0 + f * NW + wave) * NP + half) * 2 * a.R + 32 * c + r4;
                 hi[f] = load16(p);
                 lo[f] = load16(p + a.R);
             }
@@ -360,7 +361,7 @@ __global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Pro
     constexpr int SPW = SLICE / 32;                                      // steps of a wave per round
     constexpr int XB = TF * P <= 2 ? SPW : TF * P == 4 ? SPW / 2 : SPW / 4;      // steps whose activations are loaded together
     const int rounds = (K + FEW_ROUND - 1) / FEW_ROUND, steps = few_steps(K);
-    const uint4 *xw = reinterpret_cast<const uint4 *>(g.x) + wave * (SPW * 64) + lane;
+    const uint4 *xw = reinterpret_cast<const uint4 *>(g.x) + (int64_t)blockIdx.y * P * TF * steps * 64 + wave * (SPW * 64) + lane;
     uint4 x[XB][TF][P];
     auto load_x = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
@@ -380,7 +381,7 @@ __global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Pro
             if constexpr (AD) {
 #pragma unroll
                 for (int f = 0; f < TW; ++f) {
-                    const int t = f * NW + wave, id = t < a.T ? uniform_at(a.token_adapter, t) : -1;
+                    const int t = t0 + f * NW + wave, id = t < a.T ? uniform_at(a.token_adapter, t) : -1;
                     ad[f] = (unsigned)id < (unsigned)a.n ? id : -1;
                     rank[f] = ad[f] < 0 ? 0 : rank_of(a, ad[f]);
                 }
@@ -433,7 +434,8 @@ __global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Pro
     constexpr int NR = GU ? 8 : 16;
     for (int e = threadIdx.x; e < TF * 16 * NR; e += 64 * NW) {
         const int r = e % NR, tok = e / NR, f = tok >> 4, c = tok & 15;
-        if (tok >= a.T) continue;
+        const int t = t0 + tok;
+        if (t >= a.T) continue;
         float y = AD ? low[tok][r] : 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) y += red[w][f][(r >> 2) * 16 + c][r & 3];
@@ -442,18 +444,18 @@ __global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Pro
 #pragma unroll
             for (int w = 0; w < NW; ++w) up += red[w][f][(r >> 2) * 16 + 32 + c][r & 3];
             const int i = r0 + r;
-            const float h = silu_mul(y, up);
-            const uint16_t top = __builtin_bit_cast(uint16_t, (__bf16)h), rest = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(h));
+            const float hv = silu_mul(y, up);
+            const uint16_t top = __builtin_bit_cast(uint16_t, (__bf16)hv), rest = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(hv));
             const int64_t o = (((int64_t)f * hsteps + i / 32) * 64 + (i % 32 / 8) * 16 + c) * 8 + i % 8;
-            g.h[o] = top;
-            if (g.hp == 2) g.h[(int64_t)TF * hsteps * 512 + o] = rest;
+            h[o] = top;
+            if (g.hp == 2) h[(int64_t)TF * hsteps * 512 + o] = rest;
             if (g.hrow) {                                                // for the down-rank products
-                g.hrow[(int64_t)tok * g.N + i] = top;
-                if (g.hp == 2) g.hrow[(int64_t)a.T * g.N + (int64_t)tok * g.N + i] = rest;
+                g.hrow[(int64_t)t * g.N + i] = top;
+                if (g.hp == 2) g.hrow[(int64_t)a.T * g.N + (int64_t)t * g.N + i] = rest;
             }
         } else {
             if (r0 + r >= g.N) continue;
-            const int64_t o = (int64_t)tok * g.N + r0 + r;
+            const int64_t o = (int64_t)t * g.N + r0 + r;
             if (g.out_bf16) static_cast<__bf16 *>(g.out)[o] = (__bf16)y;
             else static_cast<float *>(g.out)[o] = y;
         }
@@ -471,20 +473,24 @@ __global__ __launch_bounds__(64 * few_waves(P, TF)) void k_few(SharedArgs a, Pro
 // issue and the last stage) and orders the workgroup.
 // ---------------------------------------------------------------------------
 constexpr int BW = 128, BK = 64, STAGES = 3;
+constexpr int many_split(int BT) { return BT == 64 ? 2 : 1; }
 enum { MODE_GATE_UP = 0, MODE_DOWN = 1, MODE_LOW_RANK = 2 };
 
 // Down-rank (MODE_LOW_RANK): a tile's tokens are an item of the plan, its weight rows those of that adapter's A matrices, and
 // blockIdx.y is a part of K; the sums of the parts are added by k_low_rank_sum.
+// The small tiles have two groups of four waves, each working two of a stage's four 16-wide slices: with one wave per SIMD and
+// a few products per slice, the waits for LDS would stand open.
 // TAIL: K is no multiple of 64, so a row's last step is not a whole one.
 template <int MODE, int P, int BT, bool TAIL>
-__global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles_w, int tiles_t) {
+__global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Product g, int tiles_w, int tiles_t) {
     constexpr bool GU = MODE == MODE_GATE_UP, LOW = MODE == MODE_LOW_RANK;
     constexpr int WT = 2;                                    // waves along the tokens, and along the weight rows
     constexpr int FW = BW / 2 / 32, FT = BT / WT / 32;       // 32 x 32 fragments per wave
-    constexpr int ROWS = BW + BT, LOADS = ROWS / 8 / 4;      // direct-to-LDS loads (8 rows each) per wave and stage
+    constexpr int KSP = many_split(BT), NS = 4 / KSP;        // groups of four waves that share a stage's slices; slices of each
+    constexpr int ROWS = BW + BT, LOADS = ROWS / 8 / (4 * KSP);          // direct-to-LDS loads (8 rows each) per wave and stage
     __shared__ __attribute__((aligned(1024))) uint4 tile[STAGES][ROWS * 8];
     const int lane = threadIdx.x & 63, i32 = lane & 31, hh = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w4 = wave & 3, kk0 = (wave >> 2) * NS;
     const int K = g.K;
     // XCD-aware order: consecutive workgroups go to the eight XCDs in turn; each XCD takes a run of tiles with the
     // token tile fastest, so the workgroups that read the same weight rows share an L2
@@ -505,13 +511,12 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
     // Load i of this wave fills rows 8 * (wave * LOADS + i) .. + 7 of the tile from one operand (`base`); `off`: byte offset of
     // this lane's row and chunk from there (launch_shared() keeps them below 2^32).  Rows behind the last repeat it; their
     // results are not stored.
-    static_assert(LOADS % 2 == 0 && BW / 8 % 2 == 0, "");    // load i covers an odd group of eight rows iff i is odd
-    const int chunk0 = (lane & 7) ^ (lane >> 4), chunk1 = chunk0 ^ 4;
+    const int tail = K % BK / 8;                             // chunks in a row's last step (TAIL)
     uint64_t base[LOADS];
-    uint32_t off[LOADS];
+    uint32_t off[LOADS], back[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-        const int r8 = 8 * (wave * LOADS + i), r = r8 + (lane >> 3), c = i & 1 ? chunk1 : chunk0;
+        const int r8 = 8 * (wave * LOADS + i), r = r8 + (lane >> 3), c = (lane & 7) ^ (r >> 1 & 7);
         const uint16_t *from = g.x;
         int row;
         if (LOW && r8 < BW) {
@@ -530,13 +535,13 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
         }
         base[i] = uniform64((uint64_t)(uintptr_t)from);
         off[i] = 2u * ((uint32_t)row * (uint32_t)K + 8u * c);
+        back[i] = TAIL && c >= tail ? 16u * c : 0u;
     }
     const int ksteps = (K + BK - 1) / BK;
     // steps of this workgroup: all, or (down-rank) those of its part of K
     const int sb = LOW ? ksteps * (int)blockIdx.y / (int)gridDim.y : 0;
     const int se = LOW ? ksteps * ((int)blockIdx.y + 1) / (int)gridDim.y : ksteps;
     const int nsteps = (se - sb) * P;
-    const int tail = K % BK / 8;                             // chunks in a row's last step (TAIL)
     const uint32_t lds0 = (uint32_t)(uintptr_t)(las_ptr)tile + wave * LOADS * 1024u;
     // Loads of the next stage to issue: its step, and the byte offsets of step and plane.  A chunk behind the row's end repeats the
     // step's first one (its products are masked), and stages behind the last repeat that: every stage has the same
@@ -544,10 +549,9 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
     int istep = sb;
     const uint32_t xplane = 2u * (uint32_t)a.T * (uint32_t)K;
     uint32_t iw = 2 * BK * sb, ix = iw, idst = lds0;
-    const uint32_t back0 = TAIL && chunk0 >= tail ? 16u * chunk0 : 0u, back1 = TAIL && chunk1 >= tail ? 16u * chunk1 : 0u;
     auto issue = [&](int i) {                                // i: load of this wave (compile-time)
         uint32_t o = off[i] + ((wave * LOADS + i) * 8 < BW ? iw : ix);
-        if (TAIL && istep == ksteps - 1) o -= i & 1 ? back1 : back0;
+        if (TAIL && istep == ksteps - 1) o -= back[i];
         load_to_lds(base[i], o, idst + i * 1024u);
     };
     auto next_stage = [&]() {
@@ -562,18 +566,18 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
         for (int j = 0; j < FT; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    const int rw = (wave / WT) * FW * 32, rt = BW + (wave % WT) * FT * 32;
+    const int rw = (w4 / WT) * FW * 32, rt = BW + (w4 % WT) * FT * 32;
     uint4 fw[2][FW], ft[2][FT];
     auto read_one = [&](const uint4 *t, int kk, int b, int n) {      // fragment n of the slice: weights first
         const int c = (2 * kk + hh) ^ (i32 >> 1 & 7);
         if (n < FW) fw[b][n] = t[(rw + n * 32 + i32) * 8 + c];
         else ft[b][n - FW] = t[(rt + (n - FW) * 32 + i32) * 8 + c];
     };
-    // The products of one 16-wide slice (buffer b).  Between them go the reads of the next slice and a quarter of a stage's
-    // loads, so that the matrix cores have work while these are issued.
-    auto slice = [&](int b, const uint4 *nt, int nkk, int quarter) {
+    // The products of one 16-wide slice (buffer b).  Between them go the reads of the next slice and part `part` of NS of a
+    // stage's loads, so that the matrix cores have work while these are issued.
+    auto slice = [&](int b, const uint4 *nt, int nkk, int part) {
         constexpr int M = FW * FT, NR = FW + FT;
-        const int l0 = quarter * LOADS / 4, nl = (quarter + 1) * LOADS / 4 - l0;
+        const int l0 = part * LOADS / NS, nl = (part + 1) * LOADS / NS - l0;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             acc[m % FW][m / FW] = mfma32(fw[b][m % FW], ft[b][m / FW], acc[m % FW][m / FW]);
@@ -586,7 +590,7 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // Stages 0 and 1 and the first quarter of stage 2 are loaded ahead.  Before a stage's last slice: wait for the next stage
+    // Stages 0 and 1 and the first part of stage 2 are loaded ahead.  Before a stage's last slice: wait for the next stage
     // (the one after it stays in flight) and for the workgroup; from then on nobody reads the present stage's buffer, and
     // it takes the loads of the stage three further on.
 #pragma unroll
@@ -596,11 +600,11 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
     for (int i = 0; i < LOADS; ++i) issue(i);
     next_stage();
 #pragma unroll
-    for (int i = 0; i < LOADS / 4; ++i) issue(i);
-    wait_stage<LOADS + LOADS / 4>();
+    for (int i = 0; i < LOADS / NS; ++i) issue(i);
+    wait_stage<LOADS + LOADS / NS>();
     int rb = 0, step = sb;
 #pragma unroll
-    for (int n = 0; n < FW + FT; ++n) read_one(tile[0], 0, 0, n);
+    for (int n = 0; n < FW + FT; ++n) read_one(tile[0], kk0, 0, n);
     for (int s = 0; s < nsteps; ++s) {
         const uint4 *t = tile[rb];
         // weights behind the row's end count as zeros; the step's other chunks are masked alike
@@ -612,18 +616,38 @@ __global__ __launch_bounds__(256) void k_many(SharedArgs a, Product g, int tiles
             }
         };
 #pragma unroll
-        for (int kk = 0; kk < 3; ++kk) {
-            mask(kk, kk & 1);
-            slice(kk & 1, t, kk + 1, kk + 1);
+        for (int k = 0; k < NS - 1; ++k) {
+            mask(kk0 + k, k & 1);
+            slice(k & 1, t, kk0 + k + 1, k + 1);
         }
         next_stage();
         rb = rb == STAGES - 1 ? 0 : rb + 1;
         wait_stage<LOADS>();
-        mask(3, 1);
-        slice(1, tile[rb], 0, 0);                            // behind the last stage: a read of old values, not used
+        mask(kk0 + NS - 1, 1);
+        slice(1, tile[rb], kk0, 0);                          // behind the last stage: a read of old values, not used
         step = step + 1 == se ? sb : step + 1;
     }
     wait_stage<0>();
+    if constexpr (KSP == 2) {                                // the second group's sums join the first's, which goes on alone
+        f32x4_t *part = reinterpret_cast<f32x4_t *>(tile) + w4 * (FW * FT * 4 * 64) + lane;
+        static_assert(4 * FW * FT * 4 * 64 * sizeof(f32x4_t) <= sizeof(tile), "");
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < FW * FT * 4; ++i) {
+            f32x16_t &y = acc[i / 4 / FT][i / 4 % FT];
+            const int v = i % 4 * 4;
+            if (wave >= 4) part[i * 64] = f32x4_t{y[v], y[v + 1], y[v + 2], y[v + 3]};
+        }
+        __syncthreads();
+        if (wave >= 4) return;
+#pragma unroll
+        for (int i = 0; i < FW * FT * 4; ++i) {
+            f32x16_t &y = acc[i / 4 / FT][i / 4 % FT];
+            const int v = i % 4 * 4;
+            const f32x4_t x = part[i * 64];
+            y[v] += x.x; y[v + 1] += x.y; y[v + 2] += x.z; y[v + 3] += x.w;
+        }
+    }
     // D: lane holds token i32 of a fragment, weight rows 8 * (v / 4) + 4 * hh + v % 4
     if constexpr (LOW) {
         // fp32 sums of this part of K: [part][pos][projection][R]
@@ -783,7 +807,7 @@ template <bool GU, int P, bool AD>
 hipError_t launch_few(const SharedArgs &a, const Product &g, hipStream_t st) {
     // gate/up: whole steps of the packed h, whose last rows may be zeros
     const int tf = few_frags(a.T);
-    const dim3 grd((unsigned)(GU ? few_steps(g.N) * 4 : (g.N + 15) / 16)), blk((unsigned)(64 * few_waves(P, tf)));
+    const dim3 grd((unsigned)(GU ? few_steps(g.N) * 4 : (g.N + 15) / 16), (unsigned)few_groups(a.T)), blk(64 * FEW_WAVES);
     if (tf == 1) hipLaunchKernelGGL((k_few<GU, P, 1, AD>), grd, blk, 0, st, a, g);
     else if (tf == 2) hipLaunchKernelGGL((k_few<GU, P, 2, AD>), grd, blk, 0, st, a, g);
     else hipLaunchKernelGGL((k_few<GU, P, 4, AD>), grd, blk, 0, st, a, g);
@@ -810,7 +834,7 @@ hipError_t few_inputs(const SharedArgs &a, const LowRank &L, int src, uint16_t *
 
 template <int MODE, int P, bool TAIL>
 hipError_t launch_many(const SharedArgs &a, const Product &g, int bt, int tw, int tt, int parts, hipStream_t st) {
-    const dim3 grd((unsigned)((tw * tt + 7) / 8 * 8), (unsigned)parts), blk(256);
+    const dim3 grd((unsigned)((tw * tt + 7) / 8 * 8), (unsigned)parts), blk((unsigned)(256 * many_split(bt)));
     if constexpr (MODE != MODE_LOW_RANK) {
         if (bt == 256) hipLaunchKernelGGL((k_many<MODE, P, 256, TAIL>), grd, blk, 0, st, a, g, tw, tt);
         else if (bt == 128) hipLaunchKernelGGL((k_many<MODE, P, 128, TAIL>), grd, blk, 0, st, a, g, tw, tt);
@@ -860,6 +884,14 @@ hipError_t many_low_rank(const SharedArgs &a, const LowRank &L, int planes, hipS
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
+// Whether the weights stream past groups of up to 64 tokens (once from memory, then from the caches), or tiles of both operands
+// pass through LDS, which costs four more launches for the plan and the down-rank parts.  Measured, streamed against tiles,
+// fp32 out, hidden x inter: 100 tokens 1024 x 1024 27 and 50 us, 4096 x 2048 61 and 72; 200 tokens 2048 x 1024 46 and 53; 128 tokens
+// 4096 x 2048 (bf16 out) 56 and 63; 333 tokens 1000 x 520 58 and 61; 600 tokens 512 x 1024 63 and 41.
+bool few_path(int T, int H, int Is) {
+    return T <= FEW_TOKENS || (T <= 4 * FEW_TOKENS && (int64_t)few_groups(T) * H * Is <= 1 << 24);
+}
+
 // Workspace layout, from the shapes and types alone.
 struct Layout {
     size_t x, perm, ad, items, n_items, s, part, h, hrow, total;
@@ -868,8 +900,8 @@ Layout layout(int T, int H, int Is, int n, int R, bool x_f32, int hp) {
     Layout l = {};
     size_t o = 0;
     auto take = [&](size_t b) { const size_t at = o; o += (b + 255) / 256 * 256; return at; };
-    const bool small = T <= FEW_TOKENS;
-    const size_t tf = few_frags(T);
+    const bool small = few_path(T, H, Is);
+    const size_t tf = (size_t)few_groups(T) * few_frags(T);
     auto packed = [&](int K, int p) { return (size_t)p * tf * few_steps(K) * 1024; };
     l.s = take(n > 0 ? (size_t)T * 2 * R * 4 : 0);           // gate/up's, then down's
     if (small) {
@@ -908,7 +940,7 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     auto u16 = [&](size_t at) { return reinterpret_cast<uint16_t *>(base + at); };
     uint16_t *s = u16(l.s), *h = u16(l.h);
     float *part = reinterpret_cast<float *>(base + l.part);
-    const bool small = a.T <= FEW_TOKENS;
+    const bool small = few_path(a.T, a.H, a.Is);
     a.sorted = a.n > 0 && !small;
     SharedArgs ag = a, ad = a;                              // a half without adapters runs as if there were none
     if (!a.gate_a && !a.up_a) ag.n = 0;
@@ -928,20 +960,20 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
         if ((e = few_inputs(ad, lh, hp == 1 ? ACT_BF16 : ACT_PLANES, nullptr, st)) != hipSuccess) return e;
         return few<false>(ad, dn, hp, st);
     }
-    if (!a.x_bf16) {
-        const int64_t n = (int64_t)a.T * a.H;
-        hipLaunchKernelGGL(k_split, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st,
-                           static_cast<const float *>(a.x), u16(l.x), n);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        lx.xv = gu.x = u16(l.x);
-    }
+    if (!a.x_bf16) lx.xv = gu.x = u16(l.x);
     if (a.sorted) {
         a.perm = reinterpret_cast<int32_t *>(base + l.perm);
         a.plan_ad = reinterpret_cast<int32_t *>(base + l.ad);
         a.items = reinterpret_cast<int4 *>(base + l.items);
         a.n_items = reinterpret_cast<int32_t *>(base + l.n_items);
-        hipLaunchKernelGGL(k_plan, dim3(1), dim3(PLAN_THREADS), 0, st, a);
+    }
+    if (a.sorted || !a.x_bf16) {
+        const int64_t quads = a.x_bf16 ? 0 : (int64_t)a.T * a.H / 4;
+        hipLaunchKernelGGL(k_plan, dim3((unsigned)(a.sorted + (quads + PLAN_THREADS - 1) / PLAN_THREADS)), dim3(PLAN_THREADS),
+                           0, st, a, u16(l.x), a.sorted);
         if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (a.sorted) {
         const int ng = ag.n, nd = ad.n;
         ag = ad = a;
         ag.n = ng;

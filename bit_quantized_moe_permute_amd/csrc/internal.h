@@ -102,7 +102,7 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t st);
 
 // ffn_shared.hip: the shared expert with low-rank adapters
 constexpr int MAX_ADAPTERS = 4096, MAX_RANK = 256;
-constexpr int FEW_TOKENS = 64;           // up to here the weight rows stream past all tokens at once
+constexpr int FEW_TOKENS = 64;           // tokens that a streamed weight row meets at once
 constexpr int ITEM_TOKENS = 64;          // tokens of one adapter per work item of the down-rank products
 struct SharedArgs {
     int T, H, Is;
