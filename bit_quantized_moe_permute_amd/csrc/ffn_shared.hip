@@ -3,13 +3,14 @@
 //   g = Wg x + c_a Bg_a (Ag_a x),  u likewise,  h = silu(g) * u,  out = Wd h + c_a Bd_a (Ad_a h)
 //
 // with a = token_adapter[t] (no adapter terms where it is outside 0 .. n_adapters - 1).  All products run on the bf16
-// matrix cores with fp32 sums; fp32 activations are read as two bf16 parts bf16(x), bf16(x - that): 16 significant bits.
+// matrix cores with fp32 sums.  What is not bf16 by itself -- fp32 activations, the low-rank results, and h where the result is
+// fp32 -- is carried as three bf16 parts (24 bits) and multiplied part by part; h for a bf16 result as one bf16 value, whose
+// rounding (2^-9 on average) is of the size of the result's own.
 // Launches: [plan] [down-rank] gate/up [down-rank] down --
 //
 //   plan       (many tokens) the tokens ordered by adapter, and work items of up to 64 tokens of one adapter
-//   down-rank  s[t][r] = c_a (A_a[r] . x[t]) for each token's own adapter, as two bf16 parts
-//   gate/up    weight rows x tokens; the adapters' B_a s in the epilogue; SwiGLU; h as one bf16 plane (bf16 result)
-//              or two (fp32 result, whose error then stays near 2^-17)
+//   down-rank  s[t][r] = c_a (A_a[r] . x[t]) for each token's own adapter
+//   gate/up    weight rows x tokens; the adapters' B_a s in the epilogue; SwiGLU; h
 //   down       the same product with Wd and h
 //
 // An adapter's term is formed in accumulators of its own and added to the rows of its own tokens only, so nothing of
@@ -38,6 +39,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b});
 }
 __device__ __forceinline__ float bf16_rest(float a) { return a - (float)(__bf16)a; }
+
+// Part p of 3 of a value: three bf16 parts, each the rounded rest of those before, hold all 24 bits of an fp32 value.
+__device__ __forceinline__ float bf16_part(float v, int p) { return p == 0 ? v : p == 1 ? bf16_rest(v) : bf16_rest(bf16_rest(v)); }
+__device__ __forceinline__ uint4 pack_part(const float (&v)[8], int p) {
+    return make_uint4(pack_bf16(bf16_part(v[0], p), bf16_part(v[1], p)), pack_bf16(bf16_part(v[2], p), bf16_part(v[3], p)),
+                      pack_bf16(bf16_part(v[4], p), bf16_part(v[5], p)), pack_bf16(bf16_part(v[6], p), bf16_part(v[7], p)));
+}
+__device__ __forceinline__ uint2 pack_part(const float (&v)[4], int p) {
+    return make_uint2(pack_bf16(bf16_part(v[0], p), bf16_part(v[1], p)), pack_bf16(bf16_part(v[2], p), bf16_part(v[3], p)));
+}
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
 // c + sum of eight products of bf16 values, fp32
 __device__ __forceinline__ float dot8(uint4 a, uint4 b, float c) {
@@ -87,14 +99,14 @@ __device__ __forceinline__ int adapter_at(const SharedArgs &a, int pos) {
     return (unsigned)id < (unsigned)a.n ? id : -1;
 }
 
-// Row `pos` of the low-rank results of projection `proj` of `np`: [hi, lo][R] bf16, scaled, zero from the adapter's rank on.
+// Row `pos` of the low-rank results of projection `proj` of `np`: [3 parts][R] bf16, scaled, zero from the adapter's rank on.
 __device__ __forceinline__ const uint16_t *low_rank_row(const SharedArgs &a, const uint16_t *s, int np, int pos, int proj) {
-    return s + ((int64_t)pos * np + proj) * 2 * a.R;
+    return s + ((int64_t)pos * np + proj) * 3 * a.R;
 }
 
 // ---------------------------------------------------------------------------
 // plan (many tokens): tokens ordered by adapter (those without one last), and items of up to ITEM_TOKENS tokens of one adapter.
-// One workgroup; the launch's others bring fp32 activations into bf16 planes [2][T][H].  Within an adapter the order is that of LDS atomics and may differ between calls: a row's place in
+// One workgroup; the launch's others bring fp32 activations into three bf16 planes [3][T][H].  Within an adapter the order is that of LDS atomics and may differ between calls: a row's place in
 // a tile changes no bit of its result.
 // ---------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024;
@@ -103,10 +115,10 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a, uint16_t *p
     if ((int)blockIdx.x >= plans) {
         const int64_t i = 4 * ((int64_t)(blockIdx.x - plans) * PLAN_THREADS + threadIdx.x), m = (int64_t)a.T * a.H;
         if (i >= m) return;
-        const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.x) + i);
-        *reinterpret_cast<uint2 *>(planes + i) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-        *reinterpret_cast<uint2 *>(planes + m + i) =
-            make_uint2(pack_bf16(bf16_rest(v.x), bf16_rest(v.y)), pack_bf16(bf16_rest(v.z), bf16_rest(v.w)));
+        const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.x) + i);
+        const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2 *>(planes + p * m + i) = pack_part(v, p);
         return;
     }
     __shared__ int count[MAX_ADAPTERS + 1], begin[MAX_ADAPTERS + 2], item0[MAX_ADAPTERS + 1], wsum[2][PLAN_THREADS / 64];
@@ -190,8 +202,8 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a, uint16_t *p
 // Read from rows instead, the 64 lanes' 16-byte pieces would lie in 64 places, and a wave's load would take four times as
 // long (measured as the bound of the row-reading kernel at 24 tokens: 18.5 us against 10.6 for the gate/up product).
 //
-// Low-rank results s[t][proj][hi, lo][r] = scale_a (A_a[r] . x[t]) as two bf16 parts, one wave per (token, row): no wait but that
-// for the token's adapter index and that for the row, and no exchange but the wave's own sum.
+// Low-rank results s[t][proj][3 parts][r] = scale_a (A_a[r] . x[t]), one wave per (token, row): no wait but that for the token's
+// adapter index and that for the row, and no exchange but the wave's own sum.
 // ---------------------------------------------------------------------------
 // TF: fragments of 16 tokens, rounded up to what the kernels are built for; those behind the last token hold anything.
 __host__ __device__ __forceinline__ int few_frags(int T) { return T <= 16 ? 1 : T <= 32 ? 2 : 4; }
@@ -200,33 +212,33 @@ __host__ __device__ __forceinline__ int few_groups(int T) { return (T + FEW_TOKE
 constexpr int FEW_ROUND = 2048;
 __host__ __device__ __forceinline__ int few_steps(int K) { return (K + FEW_ROUND - 1) / FEW_ROUND * (FEW_ROUND / 32); }
 
-enum { ACT_BF16 = 0, ACT_PLANES = 1, ACT_F32 = 2 };          // x: one bf16 plane, two of them, fp32
+enum { ACT_BF16 = 0, ACT_PLANES = 1, ACT_F32 = 2 };          // x: one bf16 plane, three of them, fp32
 
 template <int SRC>
 __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uint16_t *packed, int pack_blocks) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int K = L.K, steps = few_steps(K);
     if ((int)blockIdx.x < pack_blocks) {
-        constexpr int P = SRC == ACT_F32 ? 2 : 1;
+        constexpr int P = SRC == ACT_F32 ? 3 : 1;
         const int i = blockIdx.x * 4 + wave, tf = few_frags(a.T), frag = i / steps, step = i - frag * steps;
         const int grp = frag / tf, f = frag - grp * tf;
         if (frag * 16 >= a.T) return;
         const int t = frag * 16 + (lane & 15), k = step * 32 + 8 * (lane >> 4);
-        uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-        if (t < a.T && k < K) {
-            if constexpr (SRC == ACT_F32) {
-                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(L.xv) + (int64_t)t * K + k);
-                const float4 u = p[0], v = p[1];
-                hi = make_uint4(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w), pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-                lo = make_uint4(pack_bf16(bf16_rest(u.x), bf16_rest(u.y)), pack_bf16(bf16_rest(u.z), bf16_rest(u.w)),
-                                pack_bf16(bf16_rest(v.x), bf16_rest(v.y)), pack_bf16(bf16_rest(v.z), bf16_rest(v.w)));
-            } else {
-                hi = load16(static_cast<const uint16_t *>(L.xv) + (int64_t)t * K + k);
-            }
-        }
         uint4 *o = reinterpret_cast<uint4 *>(packed) + ((int64_t)(grp * P * tf + f) * steps + step) * 64 + lane;
-        o[0] = hi;
-        if constexpr (SRC == ACT_F32) o[(int64_t)tf * steps * 64] = lo;
+        const bool in = t < a.T && k < K;
+        if constexpr (SRC == ACT_F32) {
+            float4 u = make_float4(0.f, 0.f, 0.f, 0.f), w = u;
+            if (in) {
+                const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(L.xv) + (int64_t)t * K + k);
+                u = src[0];
+                w = src[1];
+            }
+            const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int p = 0; p < P; ++p) o[(int64_t)p * tf * steps * 64] = pack_part(v, p);
+        } else {
+            o[0] = in ? load16(static_cast<const uint16_t *>(L.xv) + (int64_t)t * K + k) : make_uint4(0, 0, 0, 0);
+        }
         return;
     }
     const int nrows = L.np * a.R, id = (blockIdx.x - pack_blocks) * 4 + wave;
@@ -237,10 +249,10 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
     if (ad < 0 || !A) return;                                // not read either
     A += ((int64_t)ad * a.R + r) * K;
     const int64_t row = (int64_t)t * K, plane = (int64_t)a.T * K;
-    constexpr int U = SRC == ACT_F32 ? 4 : 8, P = SRC == ACT_PLANES ? 2 : 1;
-    float acc[2] = {0.f, 0.f};
+    constexpr int U = SRC == ACT_BF16 ? 8 : 4, P = SRC == ACT_PLANES ? 3 : 1, V = SRC == ACT_F32 ? 2 : P;
+    float acc[3] = {0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < K; k0 += U * 512) {
-        uint4 w[U], v[SRC == ACT_BF16 ? 1 : 2][U];
+        uint4 w[U], v[V][U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const int k = k0 + j * 512 + lane * 8;
@@ -272,13 +284,10 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
             }
         }
     }
-    float y = wave_sum(acc[0] + acc[1]);
+    float y = wave_sum(acc[0] + (acc[1] + acc[2]));
     y = r < rank_of(a, ad) ? y * (a.scale ? uniform_at(a.scale, ad) : 1.f) : 0.f;
-    uint16_t *o = L.s + ((int64_t)t * L.np + proj) * 2 * a.R + r;
-    if (lane == 0) {
-        o[0] = __builtin_bit_cast(uint16_t, (__bf16)y);
-        o[a.R] = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(y));
-    }
+    uint16_t *o = L.s + ((int64_t)t * L.np + proj) * 3 * a.R + r;
+    if (lane < 3) o[lane * a.R] = bf16_bits(bf16_part(y, lane));
 }
 
 // ---------------------------------------------------------------------------
@@ -340,18 +349,20 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
     const int lr = lane >> 2, half = GU ? lr >> 3 : 0, wr = GU ? r0 + (lr & 7) : r0 + lr, r4 = 8 * (lane & 3);
     const uint16_t *const gb = half ? g.b[1] : g.b[0];
     const bool has = wr < g.N && gb;
+    constexpr int FB = TF < 4 ? TW : 2;                                  // tokens at once (the registers of 64 tokens' first
+    constexpr bool AHEAD = FB == TW;                                     // loads would be too many)
     int ad[TW], rank[TW];
-    uint4 bw[TW], hi[TW], lo[TW];
-    auto load_low = [&](int c) __attribute__((always_inline)) {
+    uint4 bw[TW], sv[TW][3];
+    auto load_low = [&](int f0, int c) __attribute__((always_inline)) {
 #pragma unroll
-        for (int f = 0; f < TW; ++f) {
-            bw[f] = hi[f] = lo[f] = make_uint4(0, 0, 0, 0);
+        for (int f = f0; f < f0 + FB; ++f) {
+            bw[f] = sv[f][0] = sv[f][1] = sv[f][2] = make_uint4(0, 0, 0, 0);
             if (ad[f] < 0 || 32 * c >= rank[f]) continue;                // uniform
             if (has && 32 * c + r4 < rank[f]) {
                 bw[f] = load16(gb + ((int64_t)ad[f] * g.N + wr) * a.R + 32 * c + r4);
-                const uint16_t *p = g.s + ((int64_t)(t0 + f * NW + wave) * NP + half) * 2 * a.R + 32 * c + r4;
-                hi[f] = load16(p);
-                lo[f] = load16(p + a.R);
+                const uint16_t *p = low_rank_row(a, g.s, NP, t0 + f * NW + wave, half) + 32 * c + r4;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) sv[f][i] = load16(p + i * a.R);
             }
         }
     };
@@ -359,7 +370,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
 #pragma unroll
     for (int f = 0; f < TF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     constexpr int SPW = SLICE / 32;                                      // steps of a wave per round
-    constexpr int XB = TF * P <= 2 ? SPW : TF * P == 4 ? SPW / 2 : SPW / 4;      // steps whose activations are loaded together
+    constexpr int XB = TF * P <= 2 ? SPW : TF * P <= 4 ? SPW / 2 : TF * P == 6 ? SPW / 4 : SPW / 8;   // steps whose activations are
+                                                                         // loaded together
     const int rounds = (K + FEW_ROUND - 1) / FEW_ROUND, steps = few_steps(K);
     const uint4 *xw = reinterpret_cast<const uint4 *>(g.x) + (int64_t)blockIdx.y * P * TF * steps * 64 + wave * (SPW * 64) + lane;
     uint4 x[XB][TF][P];
@@ -385,7 +397,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
                     ad[f] = (unsigned)id < (unsigned)a.n ? id : -1;
                     rank[f] = ad[f] < 0 ? 0 : rank_of(a, ad[f]);
                 }
-                load_low(0);
+                if (AHEAD) load_low(0, 0);
             }
         }
         if (r * FEW_ROUND + wave * SLICE >= K) break;                    // no slice in this round or a later one
@@ -410,15 +422,17 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
     }
     if constexpr (AD) {
         float d[TW] = {};
-        for (int c = 0; 32 * c < a.R; ++c) {
-            if (c) load_low(c);
 #pragma unroll
-            for (int f = 0; f < TW; ++f) {
-                if (32 * c >= rank[f]) continue;
-                const uint4 w = rank[f] - 32 * c >= 32 ? bw[f] : keep_first(bw[f], rank[f] - 32 * c - r4);
-                d[f] = dot8(w, lo[f], dot8(w, hi[f], d[f]));
+        for (int f0 = 0; f0 < TW; f0 += FB)
+            for (int c = 0; 32 * c < a.R; ++c) {
+                if (c || !AHEAD) load_low(f0, c);
+#pragma unroll
+                for (int f = f0; f < f0 + FB; ++f) {
+                    if (32 * c >= rank[f]) continue;
+                    const uint4 w = rank[f] - 32 * c >= 32 ? bw[f] : keep_first(bw[f], rank[f] - 32 * c - r4);
+                    d[f] = dot8(w, sv[f][2], dot8(w, sv[f][1], dot8(w, sv[f][0], d[f])));
+                }
             }
-        }
 #pragma unroll
         for (int f = 0; f < TW; ++f) {
             d[f] += __shfl_xor(d[f], 1, 64);
@@ -445,13 +459,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
             for (int w = 0; w < NW; ++w) up += red[w][f][(r >> 2) * 16 + 32 + c][r & 3];
             const int i = r0 + r;
             const float hv = silu_mul(y, up);
-            const uint16_t top = __builtin_bit_cast(uint16_t, (__bf16)hv), rest = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(hv));
             const int64_t o = (((int64_t)f * hsteps + i / 32) * 64 + (i % 32 / 8) * 16 + c) * 8 + i % 8;
-            h[o] = top;
-            if (g.hp == 2) h[(int64_t)TF * hsteps * 512 + o] = rest;
-            if (g.hrow) {                                                // for the down-rank products
-                g.hrow[(int64_t)t * g.N + i] = top;
-                if (g.hp == 2) g.hrow[(int64_t)a.T * g.N + (int64_t)t * g.N + i] = rest;
+            for (int p = 0; p < g.hp; ++p) {
+                const uint16_t part = bf16_bits(bf16_part(hv, p));
+                h[p * ((int64_t)TF * hsteps * 512) + o] = part;
+                if (g.hrow) g.hrow[((int64_t)p * a.T + t) * g.N + i] = part;     // for the down-rank products
             }
         } else {
             if (r0 + r >= g.N) continue;
@@ -463,8 +475,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: a workgroup of four waves computes 128 weight rows (gate/up: 64 of each) x BT tokens, each wave 64 x BT/2
-// of them; both operands pass through LDS in 64-wide K stages, three of them, filled by direct-to-LDS loads.
+// Many tokens: a workgroup of four waves computes 128 weight rows (gate/up: 64 of each) x BT tokens (P planes of them, which meet
+// the same weights), each wave 64 x BT/2 of them; both operands pass through LDS in 64-wide K stages, three of them, filled by direct-to-LDS loads.
 // LDS rows are 128 bytes, half of the 64 banks; 16-byte chunk c of row r lies at position c ^ (r / 2 % 8), so sixteen rows'
 // reads of one chunk column touch every bank once.
 //
@@ -487,7 +499,7 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
     constexpr int WT = 2;                                    // waves along the tokens, and along the weight rows
     constexpr int FW = BW / 2 / 32, FT = BT / WT / 32;       // 32 x 32 fragments per wave
     constexpr int KSP = many_split(BT), NS = 4 / KSP;        // groups of four waves that share a stage's slices; slices of each
-    constexpr int ROWS = BW + BT, LOADS = ROWS / 8 / (4 * KSP);          // direct-to-LDS loads (8 rows each) per wave and stage
+    constexpr int ROWS = BW + P * BT, LOADS = ROWS / 8 / (4 * KSP);          // direct-to-LDS loads (8 rows each) per wave and stage
     __shared__ __attribute__((aligned(1024))) uint4 tile[STAGES][ROWS * 8];
     const int lane = threadIdx.x & 63, i32 = lane & 31, hh = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w4 = wave & 3, kk0 = (wave >> 2) * NS;
@@ -530,8 +542,9 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
             row = min(GU ? (r >> 6) * 32 + (r & 31) : r, g.N - 1 - w0);
             from = (GU && (r8 >> 5 & 1) ? g.w[1] : g.w[0]) + (int64_t)w0 * K;
         } else {
-            const int pos = min(t0 + r - BW, last);
+            const int p = (r8 - BW) / BT, pos = min(t0 + r - BW - p * BT, last);
             row = g.gather && a.sorted ? a.perm[pos] : pos;
+            from = g.x + (int64_t)p * a.T * K;
         }
         base[i] = uniform64((uint64_t)(uintptr_t)from);
         off[i] = 2u * ((uint32_t)row * (uint32_t)K + 8u * c);
@@ -541,22 +554,19 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
     // steps of this workgroup: all, or (down-rank) those of its part of K
     const int sb = LOW ? ksteps * (int)blockIdx.y / (int)gridDim.y : 0;
     const int se = LOW ? ksteps * ((int)blockIdx.y + 1) / (int)gridDim.y : ksteps;
-    const int nsteps = (se - sb) * P;
+    const int nsteps = se - sb;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(las_ptr)tile + wave * LOADS * 1024u;
-    // Loads of the next stage to issue: its step, and the byte offsets of step and plane.  A chunk behind the row's end repeats the
-    // step's first one (its products are masked), and stages behind the last repeat that: every stage has the same
+    // Loads of the next stage to issue: its step, and its byte offset in a row.  A chunk behind the row's end repeats the step's first one (its products are masked), and stages behind the last repeat that: every stage has the same
     // number of loads in flight.
     int istep = sb;
-    const uint32_t xplane = 2u * (uint32_t)a.T * (uint32_t)K;
-    uint32_t iw = 2 * BK * sb, ix = iw, idst = lds0;
+    uint32_t ioff = 2 * BK * sb, idst = lds0;
     auto issue = [&](int i) {                                // i: load of this wave (compile-time)
-        uint32_t o = off[i] + ((wave * LOADS + i) * 8 < BW ? iw : ix);
+        uint32_t o = off[i] + ioff;
         if (TAIL && istep == ksteps - 1) o -= back[i];
         load_to_lds(base[i], o, idst + i * 1024u);
     };
     auto next_stage = [&]() {
-        if (istep + 1 < se) { ++istep; iw += 2 * BK; ix += 2 * BK; }
-        else if (P > 1 && ix == iw) { istep = sb; iw = 2 * BK * sb; ix = iw + xplane; }
+        if (istep + 1 < se) { ++istep; ioff += 2 * BK; }
         idst = idst == lds0 + (STAGES - 1) * ROWS * 128u ? lds0 : idst + ROWS * 128u;
     };
     f32x16_t acc[FW][FT];
@@ -567,20 +577,20 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
     const int rw = (w4 / WT) * FW * 32, rt = BW + (w4 % WT) * FT * 32;
-    uint4 fw[2][FW], ft[2][FT];
+    uint4 fw[2][FW], ft[2][P * FT];
     auto read_one = [&](const uint4 *t, int kk, int b, int n) {      // fragment n of the slice: weights first
         const int c = (2 * kk + hh) ^ (i32 >> 1 & 7);
         if (n < FW) fw[b][n] = t[(rw + n * 32 + i32) * 8 + c];
-        else ft[b][n - FW] = t[(rt + (n - FW) * 32 + i32) * 8 + c];
+        else ft[b][n - FW] = t[(rt + (n - FW) / FT * BT + (n - FW) % FT * 32 + i32) * 8 + c];
     };
     // The products of one 16-wide slice (buffer b).  Between them go the reads of the next slice and part `part` of NS of a
     // stage's loads, so that the matrix cores have work while these are issued.
     auto slice = [&](int b, const uint4 *nt, int nkk, int part) {
-        constexpr int M = FW * FT, NR = FW + FT;
+        constexpr int M = P * FW * FT, NR = FW + P * FT;
         const int l0 = part * LOADS / NS, nl = (part + 1) * LOADS / NS - l0;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            acc[m % FW][m / FW] = mfma32(fw[b][m % FW], ft[b][m / FW], acc[m % FW][m / FW]);
+            acc[m % FW][m / FW % FT] = mfma32(fw[b][m % FW], ft[b][m / FW], acc[m % FW][m / FW % FT]);
 #pragma unroll
             for (int n = 0; n < NR; ++n)
                 if (n >= m * 2 * NR / M && n < (m + 1) * 2 * NR / M) read_one(nt, nkk, b ^ 1, n);      // in the first half
@@ -604,7 +614,7 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
     wait_stage<LOADS + LOADS / NS>();
     int rb = 0, step = sb;
 #pragma unroll
-    for (int n = 0; n < FW + FT; ++n) read_one(tile[0], kk0, 0, n);
+    for (int n = 0; n < FW + P * FT; ++n) read_one(tile[0], kk0, 0, n);
     for (int s = 0; s < nsteps; ++s) {
         const uint4 *t = tile[rb];
         // weights behind the row's end count as zeros; the step's other chunks are masked alike
@@ -625,7 +635,7 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
         wait_stage<LOADS>();
         mask(kk0 + NS - 1, 1);
         slice(1, tile[rb], kk0, 0);                          // behind the last stage: a read of old values, not used
-        step = step + 1 == se ? sb : step + 1;
+        ++step;
     }
     wait_stage<0>();
     if constexpr (KSP == 2) {                                // the second group's sums join the first's, which goes on alone
@@ -669,7 +679,7 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
         return;
     } else if (a.n) {
         // One adapter of 64 of this wave's tokens at a time, in accumulators of its own.  Rank values go 16 at a time, each
-        // once with the high and once with the low part of the token's low-rank result.
+        // once with each part of the token's low-rank result.
         constexpr int NP = GU ? 2 : 1, JG = FT < 2 ? FT : 2;
 #pragma unroll
         for (int jg = 0; jg < FT; jg += JG) {
@@ -697,7 +707,7 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
                     for (int c0 = 0; 8 * c0 < rank; c0 += 2) {
                         const int j8 = c0 + hh;
                         const bool in = 8 * j8 < rank;
-                        uint4 w[FW], u[JG][NP][2];
+                        uint4 w[FW], u[JG][NP][3];
 #pragma unroll
                         for (int i = 0; i < FW; ++i) {
                             const int m = GU ? i & 1 : 0;
@@ -709,12 +719,12 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
                         for (int j = 0; j < JG; ++j)
 #pragma unroll
                             for (int p = 0; p < NP; ++p) {
-                                u[j][p][0] = u[j][p][1] = make_uint4(0, 0, 0, 0);
+                                u[j][p][0] = u[j][p][1] = u[j][p][2] = make_uint4(0, 0, 0, 0);
                                 if (in && idj[j] == ad && g.b[p]) {
                                     const int pos = t0 + (rt - BW) + (jg + j) * 32 + i32;
                                     const uint16_t *s = low_rank_row(a, g.s, NP, pos, p) + 8 * j8;
-                                    u[j][p][0] = load16(s);
-                                    u[j][p][1] = load16(s + a.R);
+#pragma unroll
+                                    for (int h = 0; h < 3; ++h) u[j][p][h] = load16(s + h * a.R);
                                 }
                             }
 #pragma unroll
@@ -723,7 +733,7 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
 #pragma unroll
                             for (int j = 0; j < JG; ++j)
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) d[i][j] = mfma32(w[i], u[j][GU ? i & 1 : 0][h], d[i][j]);
+                                for (int h = 0; h < 3; ++h) d[i][j] = mfma32(w[i], u[j][GU ? i & 1 : 0][h], d[i][j]);
                         }
                     }
 #pragma unroll
@@ -748,11 +758,8 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
                 float h[4];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) h[v] = silu_mul(acc[0][j][4 * v4 + v], acc[1][j][4 * v4 + v]);
-                *reinterpret_cast<uint2 *>(g.h + row + wr) = make_uint2(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]));
-                if (g.hp == 2)
-                    *reinterpret_cast<uint2 *>(g.h + (int64_t)a.T * g.N + row + wr) =
-                        make_uint2(pack_bf16(bf16_rest(h[0]), bf16_rest(h[1])),
-                                   pack_bf16(bf16_rest(h[2]), bf16_rest(h[3])));
+                for (int p = 0; p < g.hp; ++p)
+                    *reinterpret_cast<uint2 *>(g.h + (int64_t)p * a.T * g.N + row + wr) = pack_part(h, p);
             }
         } else {
             const int64_t row = (int64_t)(a.sorted ? a.perm[pos] : pos) * g.N;
@@ -776,20 +783,21 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
 
 constexpr int MAX_PARTS = 8;
 
-// s[pos][proj][hi, lo][r] = scale_a * (sum of the parts of K, in order), as two bf16 parts; 0 from the adapter's rank on.
+// s[pos][proj][3 parts][r] = scale_a * (sum of the parts of K, in order); 0 from the adapter's rank on.
 __global__ __launch_bounds__(256) void k_low_rank_sum(SharedArgs a, const float *part, int parts, int np, uint16_t *s) {
     const int per = np * a.R / 4;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (int64_t)a.T * per) return;
     const int pos = (int)(i / per), rr = 4 * (int)(i - (int64_t)pos * per), proj = rr / a.R, r = rr - proj * a.R;
     const int ad = a.plan_ad[pos];
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float4 x[MAX_PARTS];
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f}, x[MAX_PARTS];
 #pragma unroll
-    for (int k = 0; k < MAX_PARTS; ++k)
-        x[k] = k < parts ? *reinterpret_cast<const float4 *>(part + ((int64_t)k * a.T + pos) * np * a.R + rr) : v;
+    for (int k = 0; k < MAX_PARTS; ++k) {
+        x[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if (k < parts) x[k] = *reinterpret_cast<const f32x4_t *>(part + ((int64_t)k * a.T + pos) * np * a.R + rr);
+    }
 #pragma unroll
-    for (int k = 0; k < MAX_PARTS; ++k) { v.x += x[k].x; v.y += x[k].y; v.z += x[k].z; v.w += x[k].w; }
+    for (int k = 0; k < MAX_PARTS; ++k) v += x[k];
     if (ad < 0) return;                                      // of no adapter: neither written before nor read after
     const float c = a.scale ? a.scale[ad] : 1.f;
     const int rank = rank_of(a, ad) - r;
@@ -797,10 +805,10 @@ __global__ __launch_bounds__(256) void k_low_rank_sum(SharedArgs a, const float 
     v.y = 1 < rank ? v.y * c : 0.f;
     v.z = 2 < rank ? v.z * c : 0.f;
     v.w = 3 < rank ? v.w * c : 0.f;
-    uint16_t *o = s + ((int64_t)pos * np + proj) * 2 * a.R + r;
-    *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-    *reinterpret_cast<uint2 *>(o + a.R) =
-        make_uint2(pack_bf16(bf16_rest(v.x), bf16_rest(v.y)), pack_bf16(bf16_rest(v.z), bf16_rest(v.w)));
+    const float y[4] = {v.x, v.y, v.z, v.w};
+    uint16_t *o = s + ((int64_t)pos * np + proj) * 3 * a.R + r;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2 *>(o + p * a.R) = pack_part(y, p);
 }
 
 template <bool GU, int P, bool AD>
@@ -817,7 +825,7 @@ hipError_t launch_few(const SharedArgs &a, const Product &g, hipStream_t st) {
 template <bool GU>
 hipError_t few(const SharedArgs &a, const Product &g, int planes, hipStream_t st) {
     if (planes == 1) return a.n ? launch_few<GU, 1, true>(a, g, st) : launch_few<GU, 1, false>(a, g, st);
-    return a.n ? launch_few<GU, 2, true>(a, g, st) : launch_few<GU, 2, false>(a, g, st);
+    return a.n ? launch_few<GU, 3, true>(a, g, st) : launch_few<GU, 3, false>(a, g, st);
 }
 
 // Packs the activations (packed) and forms the low-rank results (a.n), one launch for both.
@@ -835,7 +843,7 @@ hipError_t few_inputs(const SharedArgs &a, const LowRank &L, int src, uint16_t *
 template <int MODE, int P, bool TAIL>
 hipError_t launch_many(const SharedArgs &a, const Product &g, int bt, int tw, int tt, int parts, hipStream_t st) {
     const dim3 grd((unsigned)((tw * tt + 7) / 8 * 8), (unsigned)parts), blk((unsigned)(256 * many_split(bt)));
-    if constexpr (MODE != MODE_LOW_RANK) {
+    if constexpr (MODE != MODE_LOW_RANK && P == 1) {
         if (bt == 256) hipLaunchKernelGGL((k_many<MODE, P, 256, TAIL>), grd, blk, 0, st, a, g, tw, tt);
         else if (bt == 128) hipLaunchKernelGGL((k_many<MODE, P, 128, TAIL>), grd, blk, 0, st, a, g, tw, tt);
     }
@@ -848,15 +856,16 @@ hipError_t many_tiles(const SharedArgs &a, const Product &g, int planes, int bt,
     if (planes == 1)
         return g.K % BK ? launch_many<MODE, 1, true>(a, g, bt, tw, tt, parts, st)
                         : launch_many<MODE, 1, false>(a, g, bt, tw, tt, parts, st);
-    return g.K % BK ? launch_many<MODE, 2, true>(a, g, bt, tw, tt, parts, st)
-                    : launch_many<MODE, 2, false>(a, g, bt, tw, tt, parts, st);
+    return g.K % BK ? launch_many<MODE, 3, true>(a, g, bt, tw, tt, parts, st)
+                    : launch_many<MODE, 3, false>(a, g, bt, tw, tt, parts, st);
 }
 
 template <int MODE>
 hipError_t many(const SharedArgs &a, const Product &g, int planes, hipStream_t st) {
     const int rows = MODE == MODE_GATE_UP ? BW / 2 : BW, tw = (g.N + rows - 1) / rows;
     auto tiles = [&](int bt) { return tw * ((a.T + bt - 1) / bt); };
-    const int bt = tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
+    // three planes of 128 tokens would not fit three times into LDS
+    const int bt = planes > 1 ? 64 : tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
     return many_tiles<MODE>(a, g, planes, bt, tw, (a.T + bt - 1) / bt, 1, st);
 }
 
@@ -903,13 +912,13 @@ Layout layout(int T, int H, int Is, int n, int R, bool x_f32, int hp) {
     const bool small = few_path(T, H, Is);
     const size_t tf = (size_t)few_groups(T) * few_frags(T);
     auto packed = [&](int K, int p) { return (size_t)p * tf * few_steps(K) * 1024; };
-    l.s = take(n > 0 ? (size_t)T * 2 * R * 4 : 0);           // gate/up's, then down's
+    l.s = take(n > 0 ? (size_t)T * 2 * 3 * R * 2 : 0);       // gate/up's, then down's
     if (small) {
-        l.x = take(packed(H, x_f32 ? 2 : 1));
+        l.x = take(packed(H, x_f32 ? 3 : 1));
         l.h = take(packed(Is, hp));
         l.hrow = take(n > 0 ? (size_t)T * Is * 2 * hp : 0);
     } else {
-        l.x = take(x_f32 ? (size_t)T * H * 4 : 0);
+        l.x = take(x_f32 ? (size_t)T * H * 3 * 2 : 0);
         l.h = take((size_t)T * Is * 2 * hp);
         if (n > 0) {
             l.perm = take((size_t)T * 4);
@@ -930,12 +939,12 @@ namespace moe {
 
 size_t shared_workspace(int T, int H, int Is, int n, int R) {
     // the largest over the activation and result types, so that one buffer serves every call of these sizes
-    return layout(T, H, Is, n, R, true, 2).total;
+    return layout(T, H, Is, n, R, true, 3).total;
 }
 
 hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     char *base = static_cast<char *>(ws);
-    const int hp = a.out_bf16 ? 1 : 2, xp = a.x_bf16 ? 1 : 2;
+    const int hp = a.out_bf16 ? 1 : 3, xp = a.x_bf16 ? 1 : 3;
     const Layout l = layout(a.T, a.H, a.Is, a.n, a.R, !a.x_bf16, hp);
     auto u16 = [&](size_t at) { return reinterpret_cast<uint16_t *>(base + at); };
     uint16_t *s = u16(l.s), *h = u16(l.h);

@@ -126,14 +126,14 @@ struct LowRank {
     int K, np;
     int gather;                          // rows of x are tokens (through perm), not sorted positions
     const uint16_t *a[2];
-    uint16_t *s;                         // [T][np][hi, lo][R]
+    uint16_t *s;                         // [T][np][3 parts][R]
     float *part;                         // [parts][T][np][R], many tokens
 };
 struct Product {
     const uint16_t *x;                   // [P][T][K] bf16 planes, or (few tokens) packed
     int K, N, gather;
     const uint16_t *w[2], *b[2];
-    const uint16_t *s;                   // [T][np][hi, lo][R]
+    const uint16_t *s;                   // [T][np][3 parts][R]
     uint16_t *h;                         // gate/up: [hp][T][N] bf16 planes by sorted position, or (few tokens) packed
     uint16_t *hrow;                      // gate/up, few tokens: [hp][T][N] too, if set
     int hp;

@@ -456,16 +456,15 @@ size_t moe_shared_ffn_workspace(const moe_layer_desc *L, const moe_adapter_desc 
  * is the shared_out of moe_combine and moe_combine_norm.
  *   L: hidden, shared_inter and the shared_* weights are read, nothing else.
  *   A: adapters, or NULL (none; token_adapter is not read then).
- *   x [n_tokens][H], bf16 or fp32.  fp32 activations are read as two bf16 parts
- *     (16 significant bits).
+ *   x [n_tokens][H], bf16 or fp32.
  *   token_adapter: device int32 [n_tokens]; a value outside 0 .. n_adapters - 1
  *     (such as -1) means no adapter for that token.
  *   out [n_tokens][H], fp32 or bf16.
  *   ws: 256-byte aligned, at least moe_shared_ffn_workspace(L, A, n_tokens)
  *     bytes; calls that may overlap in time need one each.
- * Sums are fp32 in an order fixed by the shapes; the low-rank products A[a] x
- * and, with an fp32 out, the SwiGLU result h are carried as two bf16 parts, h
- * with a bf16 out as one.  A token's result has the same bits whatever other
+ * Sums are fp32 in an order fixed by the shapes; fp32 activations, the low-rank
+ * products A[a] x and, with an fp32 out, the SwiGLU result h are carried with
+ * all 24 bits (three bf16 parts), h with a bf16 out as one bf16 value.  A token's result has the same bits whatever other
  * tokens and adapters the call holds (at the same n_tokens and n_adapters), and
  * non-finite values in one adapter reach only the tokens that use it.
  * hidden and shared_inter must be multiples of 8; x, out and the weights 16-byte
