@@ -336,57 +336,72 @@ def moe_layer(desc: LayerDesc, x, w_router, topk_idx, topk_w, expert_offsets, pe
                          ws.numel() * ws.element_size(), _stream(stream)))
 
 
-def _addr(t, dev):
-    """Address of a contiguous tensor on GPU `dev` (None passes), as an int."""
-    if t is None:
-        return None
-    if dev < 0 or t.get_device() != dev:
-        if not t.is_cuda:
-            raise TypeError("expected a GPU tensor (the library takes device pointers)")
-        raise ValueError(f"tensors on devices {dev} and {t.get_device()}")
-    if not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
-    return t.data_ptr()
+def _addrs(dev, *tensors):
+    """Addresses (ints) of contiguous tensors on GPU `dev`; None passes."""
+    if dev < 0:
+        raise TypeError("expected a GPU tensor (the library takes device pointers)")
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev:
+            if not t.is_cuda:
+                raise TypeError("expected a GPU tensor (the library takes device pointers)")
+            raise ValueError(f"tensors on devices {dev} and {t.get_device()}")
+        if not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        out.append(t.data_ptr())
+    return out
 
 
 def _stream_on(stream, dev):
     """The given stream, or torch's current one on GPU `dev`, which has to be the current device (the library
     launches there)."""
-    import torch
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors on device {dev}, the current device is {torch.cuda.current_device()}")
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    now = torch._C._cuda_getDevice()
+    if dev != now:
+        raise ValueError(f"tensors on device {dev}, the current device is {now}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream
+
+
+def _type(t, what):
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+    return dt
 
 
 def _norm_output(T, H, residual, residual_out, weight, y, y_scale):
-    """Shape and type checks of what the norm calls share; (res_dt, y_dt)."""
-    import torch
+    """Shape and type checks of what the norm calls share; (res_dt, w_dt, y_dt)."""
     n = T * H
-    if (residual is None) != (residual_out is None):
-        raise ValueError("residual_out must be given iff residual is")
     res_dt = DT_F32
-    if residual is not None:
-        res_dt = _dt(residual)
+    if residual is not None and residual_out is not None:
+        res_dt = _type(residual, "residual")
         if residual_out.dtype != residual.dtype:
             raise TypeError(f"residual_out: expected {residual.dtype}, got {residual_out.dtype}")
-        _need(residual, n, "residual")
-        _need(residual_out, n, "residual_out")
-    _need(weight, H, "weight")
-    _need(y, n, "y")
-    if y.dtype != torch.float8_e4m3fn:
-        if y_scale is not None:
-            raise ValueError("y_scale is given iff y is float8_e4m3fn")
-        return res_dt, _dt(y)
+        if residual.numel() < n or residual_out.numel() < n:
+            _need(residual, n, "residual")
+            _need(residual_out, n, "residual_out")
+    elif residual is not None or residual_out is not None:
+        raise ValueError("residual_out must be given iff residual is")
+    if weight.numel() < H or y.numel() < n:
+        _need(weight, H, "weight")
+        _need(y, n, "y")
+    w_dt, y_dt = _type(weight, "weight"), _DTYPES.get(y.dtype)
     if y_scale is None:
+        if y.dtype == torch.float8_e4m3fn:
+            raise ValueError("y_scale is given iff y is float8_e4m3fn")
+        return res_dt, w_dt, _type(y, "y")
+    if y.dtype != torch.float8_e4m3fn:
         raise ValueError("y_scale is given iff y is float8_e4m3fn")
     if y_scale.dtype == torch.float32:
         _need(y_scale, T, "y_scale")
-        return res_dt, DT_E4M3_ROW
+        return res_dt, w_dt, DT_E4M3_ROW
     if y_scale.dtype not in (torch.float8_e8m0fnu, torch.uint8):
         raise TypeError(f"y_scale: expected float32 (row scales), float8_e8m0fnu or uint8 (block scales), got "
                         f"{y_scale.dtype}")
     _need(y_scale, T * ((H + 31) // 32), "y_scale")
-    return res_dt, DT_E4M3_BLOCK
+    return res_dt, w_dt, DT_E4M3_BLOCK
 
 
 def moe_add_rms_norm(x, residual, residual_out, weight, eps, y, y_scale=None, stream=None):
@@ -394,11 +409,12 @@ def moe_add_rms_norm(x, residual, residual_out, weight, eps, y, y_scale=None, st
     y_scale float8_e8m0fnu / uint8 [T][ceil(H/32)] (block scales) or float32 [T] (row scales); residual and
     residual_out may be None together, or the same tensor."""
     T, H = _rows(x)
-    res_dt, y_dt = _norm_output(T, H, residual, residual_out, weight, y, y_scale)
-    x_dt, w_dt, dev = _dt(x), _dt(weight), x.get_device()
-    _check(lib.moe_add_rms_norm(_addr(x, dev), x_dt, T, H, _addr(residual, dev), _addr(residual_out, dev), res_dt,
-                                _addr(weight, dev), w_dt, eps, _addr(y, dev), y_dt, _addr(y_scale, dev),
-                                _stream_on(stream, dev)))
+    res_dt, w_dt, y_dt = _norm_output(T, H, residual, residual_out, weight, y, y_scale)
+    x_dt, dev = _type(x, "x"), x.get_device()
+    px, pr, po, pw, py, ps = _addrs(dev, x, residual, residual_out, weight, y, y_scale)
+    st = lib.moe_add_rms_norm(px, x_dt, T, H, pr, po, res_dt, pw, w_dt, eps, py, y_dt, ps, _stream_on(stream, dev))
+    if st:
+        _check(st)
 
 
 def moe_combine_norm(slot_out, topk_w, shared_out, residual, residual_out, weight, eps, y, y_scale=None, steer_v=None,
@@ -411,14 +427,16 @@ def moe_combine_norm(slot_out, topk_w, shared_out, residual, residual_out, weigh
     _need(shared_out, T * H, "shared_out")
     _need(steer_v, H, "steer_v")
     for t in (slot_out, topk_w, shared_out, steer_v):
-        if t is not None and _dt(t) != DT_F32:
+        if t is not None and t.dtype != torch.float32:
             raise TypeError(f"expected torch.float32, got {t.dtype}")
-    res_dt, y_dt = _norm_output(T, H, residual, residual_out, weight, y, y_scale)
-    w_dt, dev = _dt(weight), slot_out.get_device()
-    _check(lib.moe_combine_norm(_addr(slot_out, dev), _addr(topk_w, dev), _addr(shared_out, dev), T, k, H,
-                                _addr(steer_v, dev), float(steer_f), _addr(residual, dev), _addr(residual_out, dev),
-                                res_dt, _addr(weight, dev), w_dt, eps, _addr(y, dev), y_dt, _addr(y_scale, dev),
-                                _stream_on(stream, dev)))
+    res_dt, w_dt, y_dt = _norm_output(T, H, residual, residual_out, weight, y, y_scale)
+    dev = slot_out.get_device()
+    pslot, ptw, psh, pv, pr, po, pw, py, ps = _addrs(dev, slot_out, topk_w, shared_out, steer_v, residual, residual_out,
+                                                     weight, y, y_scale)
+    st = lib.moe_combine_norm(pslot, ptw, psh, T, k, H, pv, steer_f, pr, po, res_dt, pw, w_dt, eps, py, y_dt, ps,
+                              _stream_on(stream, dev))
+    if st:
+        _check(st)
 
 
 def moe_shared_ffn_workspace(desc: LayerDesc, n_tokens: int, adapters=None) -> int:
@@ -430,10 +448,10 @@ def moe_shared_ffn(desc: LayerDesc, x, out, ws, adapters=None, token_adapter=Non
     """The layer's shared expert on x [T][H] into out [T][H], token t through adapter token_adapter[t] of the
     AdapterPool `adapters` (an index outside the pool: none)."""
     T, H = _rows(x, desc.hidden)
-    _need(out, T * H, "out")
+    if out.numel() < T * H:
+        _need(out, T * H, "out")
     dev, pool = x.get_device(), None
     if adapters is not None:
-        import torch
         if (adapters.hidden, adapters.inter) != (H, desc.shared_inter):
             raise ValueError(f"adapters are for hidden {adapters.hidden}, inter {adapters.inter}; the layer has "
                              f"{H}, {desc.shared_inter}")
@@ -443,8 +461,12 @@ def moe_shared_ffn(desc: LayerDesc, x, out, ws, adapters=None, token_adapter=Non
             raise TypeError("token_adapter must be an int32 tensor")
         _need(token_adapter, T, "token_adapter")
         pool = adapters.desc
-    _check(lib.moe_shared_ffn(desc, pool, _addr(x, dev), _dt(x), T, _addr(token_adapter, dev), _addr(out, dev), _dt(out),
-                              _addr(ws, dev), ws.numel() * ws.element_size(), _stream_on(stream, dev)))
+    x_dt, out_dt = _type(x, "x"), _type(out, "out")
+    px, pi, po, pws = _addrs(dev, x, token_adapter, out, ws)
+    st = lib.moe_shared_ffn(desc, pool, px, x_dt, T, pi, po, out_dt, pws, ws.numel() * ws.element_size(),
+                            _stream_on(stream, dev))
+    if st:
+        _check(st)
 
 
 def moe_probe_stream_read(buf, nbytes, sink, n_blocks, stream=None):
@@ -453,5 +475,9 @@ def moe_probe_stream_read(buf, nbytes, sink, n_blocks, stream=None):
     _need_bytes(sink, 4 * n_blocks, "sink")
     _check(lib.moe_probe_stream_read(_ptr(buf), nbytes, _ptr(sink), n_blocks, _stream(stream)))
 
+
+import torch  # noqa: E402  (after the library: it fails first where it is missing)
+
+_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
 
 from .layer import AdapterPool, DeviceLayer, LayerBuffers  # noqa: E402  (needs `lib` loaded)

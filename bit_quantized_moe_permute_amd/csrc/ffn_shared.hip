@@ -724,7 +724,8 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
                                     const int pos = t0 + (rt - BW) + (jg + j) * 32 + i32;
                                     const uint16_t *s = low_rank_row(a, g.s, NP, pos, p) + 8 * j8;
 #pragma unroll
-                                    for (int h = 0; h < 3; ++h) u[j][p][h] = load16(s + h * a.R);
+                                    for (int h = 0; h < 3; ++h)
+                                        if (h < a.sparts) u[j][p][h] = load16(s + h * a.R);
                                 }
                             }
 #pragma unroll
@@ -733,7 +734,8 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
 #pragma unroll
                             for (int j = 0; j < JG; ++j)
 #pragma unroll
-                                for (int h = 0; h < 3; ++h) d[i][j] = mfma32(w[i], u[j][GU ? i & 1 : 0][h], d[i][j]);
+                                for (int h = 0; h < 3; ++h)
+                                    if (h < a.sparts) d[i][j] = mfma32(w[i], u[j][GU ? i & 1 : 0][h], d[i][j]);
                         }
                     }
 #pragma unroll
@@ -950,6 +952,7 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     uint16_t *s = u16(l.s), *h = u16(l.h);
     float *part = reinterpret_cast<float *>(base + l.part);
     const bool small = few_path(a.T, a.H, a.Is);
+    a.sparts = a.out_bf16 ? 2 : 3;                          // 16 bits of the low-rank results are enough beside a bf16 result
     a.sorted = a.n > 0 && !small;
     SharedArgs ag = a, ad = a;                              // a half without adapters runs as if there were none
     if (!a.gate_a && !a.up_a) ag.n = 0;
