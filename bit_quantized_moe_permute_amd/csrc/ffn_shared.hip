@@ -302,13 +302,22 @@ constexpr int FEW_WAVES = 8;
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-template <bool GU, int P, int TF, bool AD>
+// AD: the adapters' low-rank results are read (AD_READ), or (AD_HERE, down, few values) formed by every workgroup from the rows of
+// h while its weights are on their way: that reads A out of the caches in every workgroup, where a launch between the two products
+// costs 4 us. fp32 result, launch against here: 16 values of 2048 (1 token, rank 16) 25.6 -> 24.0 us the whole call, of 4096
+// 40.2 -> 38.2, of 512 14.8 -> 13.6;
+// 32 values of 2048 24.9 -> 25.9, 8 of 8192 111.7 -> 112.8.
+enum { AD_NONE = 0, AD_READ = 1, AD_HERE = 2 };
+constexpr int HERE_VALUES = 16, HERE_TERMS = 1 << 16;        // tokens * max_rank, and times shared_inter, up to which AD_HERE is taken
+
+template <bool GU, int P, int TF, int AD>
 __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g) {
     constexpr int NW = FEW_WAVES, SLICE = FEW_ROUND / NW;         // K of a wave per round
     constexpr int LINE = SLICE / 8, LOADS = 16 * LINE / 64;              // chunks of a row's piece; loads of 64 chunks
     constexpr int TW = TF * 16 / NW, NP = GU ? 2 : 1;                    // tokens per wave (adapters' terms)
     __shared__ __attribute__((aligned(1024))) uint4 ring[2][NW][16 * LINE];
     __shared__ float low[TF * 16][16];
+    __shared__ float here[AD == AD_HERE ? HERE_VALUES : 1];
     f32x4_t (*red)[TF][64] = reinterpret_cast<f32x4_t (*)[TF][64]>(ring);         // after the last product
     static_assert(sizeof(f32x4_t) * NW * TF * 64 <= sizeof(ring), "");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
@@ -360,9 +369,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
             if (ad[f] < 0 || 32 * c >= rank[f]) continue;                // uniform
             if (has && 32 * c + r4 < rank[f]) {
                 bw[f] = load16(gb + ((int64_t)ad[f] * g.N + wr) * a.R + 32 * c + r4);
-                const uint16_t *p = low_rank_row(a, g.s, NP, t0 + f * NW + wave, half) + 32 * c + r4;
+                if constexpr (AD == AD_READ) {
+                    const uint16_t *p = low_rank_row(a, g.s, NP, t0 + f * NW + wave, half) + 32 * c + r4;
 #pragma unroll
-                for (int i = 0; i < 3; ++i) sv[f][i] = load16(p + i * a.R);
+                    for (int i = 0; i < 3; ++i) sv[f][i] = load16(p + i * a.R);
+                }
             }
         }
     };
@@ -385,19 +396,46 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
                 for (int i = 0; i < XB; ++i) x[i][f][p] = src[i * 64];
             }
     };
+    issue(0, 0);
+    if (rounds > 1) issue(1, 1);
+    if constexpr (AD == AD_HERE) {
+        // here[t][r] = scale (A[r] . h[t]), one wave per value
+        for (int e = wave; e < a.T * a.R; e += NW) {
+            const int t = e / a.R, r = e - t * a.R, id = uniform_at(a.token_adapter, t);
+            float y = 0.f;
+            if ((unsigned)id < (unsigned)a.n && r < rank_of(a, id)) {
+                const uint16_t *A = g.a + ((int64_t)id * a.R + r) * K, *hr = g.hrow + (int64_t)t * K;
+                for (int k0 = lane * 8; k0 < K; k0 += 4 * 512) {
+                    uint4 av[4], hv[4][P];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = k0 + i * 512 < K ? k0 + i * 512 : lane * 8;
+                        av[i] = load16(A + k);
+#pragma unroll
+                        for (int p = 0; p < P; ++p) hv[i][p] = load16(hr + (int64_t)p * a.T * K + k);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (k0 + i * 512 < K)
+#pragma unroll
+                            for (int p = 0; p < P; ++p) y = dot8(av[i], hv[i][p], y);
+                }
+                y = wave_sum(y) * (a.scale ? uniform_at(a.scale, id) : 1.f);
+            }
+            if (lane == 0) here[e] = y;
+        }
+    }
     for (int r = 0; r < rounds; ++r, xw += FEW_ROUND / 32 * 64) {
         const int b = r & 1;
         if (r == 0) {
-            issue(0, 0);
-            if (rounds > 1) issue(1, 1);
-            if constexpr (AD) {
+            if constexpr (AD != AD_NONE) {
 #pragma unroll
                 for (int f = 0; f < TW; ++f) {
                     const int t = t0 + f * NW + wave, id = t < a.T ? uniform_at(a.token_adapter, t) : -1;
                     ad[f] = (unsigned)id < (unsigned)a.n ? id : -1;
                     rank[f] = ad[f] < 0 ? 0 : rank_of(a, ad[f]);
                 }
-                if (AHEAD) load_low(0, 0);
+                if (AD == AD_READ && AHEAD) load_low(0, 0);
             }
         }
         if (r * FEW_ROUND + wave * SLICE >= K) break;                    // no slice in this round or a later one
@@ -420,17 +458,27 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
             issue(r + 2, b);
         }
     }
-    if constexpr (AD) {
+    if constexpr (AD == AD_HERE) __syncthreads();
+    if constexpr (AD != AD_NONE) {
         float d[TW] = {};
 #pragma unroll
         for (int f0 = 0; f0 < TW; f0 += FB)
             for (int c = 0; 32 * c < a.R; ++c) {
-                if (c || !AHEAD) load_low(f0, c);
+                if (AD == AD_HERE || c || !AHEAD) load_low(f0, c);
 #pragma unroll
                 for (int f = f0; f < f0 + FB; ++f) {
                     if (32 * c >= rank[f]) continue;
                     const uint4 w = rank[f] - 32 * c >= 32 ? bw[f] : keep_first(bw[f], rank[f] - 32 * c - r4);
-                    d[f] = dot8(w, sv[f][2], dot8(w, sv[f][1], dot8(w, sv[f][0], d[f])));
+                    if constexpr (AD == AD_HERE) {
+                        const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+                        const float *sv = here + (f * NW + wave) * a.R + 32 * c + r4;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (32 * c + r4 + i < rank[f])
+                                d[f] = __fmaf_rn(__uint_as_float(i & 1 ? wv[i / 2] & 0xFFFF0000u : wv[i / 2] << 16), sv[i], d[f]);
+                    } else {
+                        d[f] = dot8(w, sv[f][2], dot8(w, sv[f][1], dot8(w, sv[f][0], d[f])));
+                    }
                 }
             }
 #pragma unroll
@@ -450,11 +498,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
         const int r = e % NR, tok = e / NR, f = tok >> 4, c = tok & 15;
         const int t = t0 + tok;
         if (t >= a.T) continue;
-        float y = AD ? low[tok][r] : 0.f;
+        float y = AD != AD_NONE ? low[tok][r] : 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) y += red[w][f][(r >> 2) * 16 + c][r & 3];
         if constexpr (GU) {
-            float up = AD ? low[tok][r + 8] : 0.f;
+            float up = AD != AD_NONE ? low[tok][r + 8] : 0.f;
 #pragma unroll
             for (int w = 0; w < NW; ++w) up += red[w][f][(r >> 2) * 16 + 32 + c][r & 3];
             const int i = r0 + r;
@@ -813,21 +861,35 @@ __global__ __launch_bounds__(256) void k_low_rank_sum(SharedArgs a, const float 
     for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2 *>(o + p * a.R) = pack_part(y, p);
 }
 
-template <bool GU, int P, bool AD>
+template <bool GU, int P, int AD>
 hipError_t launch_few(const SharedArgs &a, const Product &g, hipStream_t st) {
-    // gate/up: whole steps of the packed h, whose last rows may be zeros
+    // gate/up: whole rounds of the packed h, whose last rows may be zeros
     const int tf = few_frags(a.T);
     const dim3 grd((unsigned)(GU ? few_steps(g.N) * 4 : (g.N + 15) / 16), (unsigned)few_groups(a.T)), blk(64 * FEW_WAVES);
     if (tf == 1) hipLaunchKernelGGL((k_few<GU, P, 1, AD>), grd, blk, 0, st, a, g);
-    else if (tf == 2) hipLaunchKernelGGL((k_few<GU, P, 2, AD>), grd, blk, 0, st, a, g);
-    else hipLaunchKernelGGL((k_few<GU, P, 4, AD>), grd, blk, 0, st, a, g);
+    if constexpr (AD != AD_HERE) {
+        if (tf == 2) hipLaunchKernelGGL((k_few<GU, P, 2, AD>), grd, blk, 0, st, a, g);
+        else if (tf == 4) hipLaunchKernelGGL((k_few<GU, P, 4, AD>), grd, blk, 0, st, a, g);
+    }
     return hipGetLastError();
+}
+
+bool low_rank_here(const SharedArgs &a) {
+    return a.T <= HERE_VALUES && a.T * a.R <= HERE_VALUES && a.T * a.R * a.Is <= HERE_TERMS;
+}
+
+template <bool GU, int P>
+hipError_t few_planes(const SharedArgs &a, const Product &g, hipStream_t st) {
+    if (!a.n) return launch_few<GU, P, AD_NONE>(a, g, st);
+    if constexpr (!GU) {
+        if (low_rank_here(a)) return launch_few<GU, P, AD_HERE>(a, g, st);
+    }
+    return launch_few<GU, P, AD_READ>(a, g, st);
 }
 
 template <bool GU>
 hipError_t few(const SharedArgs &a, const Product &g, int planes, hipStream_t st) {
-    if (planes == 1) return a.n ? launch_few<GU, 1, true>(a, g, st) : launch_few<GU, 1, false>(a, g, st);
-    return a.n ? launch_few<GU, 3, true>(a, g, st) : launch_few<GU, 3, false>(a, g, st);
+    return planes == 1 ? few_planes<GU, 1>(a, g, st) : few_planes<GU, 3>(a, g, st);
 }
 
 // Packs the activations (packed) and forms the low-rank results (a.n), one launch for both.
@@ -969,7 +1031,12 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
         if (ad.n) { gu.hrow = u16(l.hrow); lh.xv = gu.hrow; }
         if ((e = few_inputs(ag, lx, a.x_bf16 ? ACT_BF16 : ACT_F32, u16(l.x), st)) != hipSuccess) return e;
         if ((e = few<true>(ag, gu, xp, st)) != hipSuccess) return e;
-        if ((e = few_inputs(ad, lh, hp == 1 ? ACT_BF16 : ACT_PLANES, nullptr, st)) != hipSuccess) return e;
+        if (ad.n && low_rank_here(ad)) {
+            dn.a = a.down_a;
+            dn.hrow = gu.hrow;
+        } else if ((e = few_inputs(ad, lh, hp == 1 ? ACT_BF16 : ACT_PLANES, nullptr, st)) != hipSuccess) {
+            return e;
+        }
         return few<false>(ad, dn, hp, st);
     }
     if (!a.x_bf16) lx.xv = gu.x = u16(l.x);
