@@ -506,6 +506,8 @@ static moe_status norm_args(const char *fn, int32_t n_tokens, int32_t hidden, co
         return fail(MOE_ERR_INVALID_ARG, "%s: an output overlaps another buffer", fn);
     if (hidden > MOE_NORM_MAX_HIDDEN)
         return fail(MOE_ERR_UNSUPPORTED, "%s: hidden > %d", fn, MOE_NORM_MAX_HIDDEN);
+    if (n_tokens > MOE_MAX_TOKENS)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: n_tokens > %d; split the batch", fn, MOE_MAX_TOKENS);
     a.T = n_tokens; a.H = hidden;
     a.residual = residual; a.residual_out = residual_out;
     a.res_kind = !residual ? moe::RES_NONE : res_dt == MOE_DT_F32 ? moe::RES_F32 : moe::RES_BF16;
@@ -577,6 +579,8 @@ static moe_status check_shared(const char *fn, const moe_layer_desc *L, const mo
         return fail(MOE_ERR_INVALID_ARG, "%s: hidden and shared_inter must be positive multiples of 8", fn);
     if (L->hidden > MOE_SHARED_MAX_DIM || L->shared_inter > MOE_SHARED_MAX_DIM)
         return fail(MOE_ERR_UNSUPPORTED, "%s: hidden or shared_inter above %d", fn, MOE_SHARED_MAX_DIM);
+    if (n_tokens > MOE_MAX_TOKENS)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: n_tokens > %d; split the batch", fn, MOE_MAX_TOKENS);
     if ((int64_t)n_tokens * (L->hidden > L->shared_inter ? L->hidden : L->shared_inter) >= (int64_t)1 << 30)
         return fail(MOE_ERR_UNSUPPORTED, "%s: n_tokens * hidden (or shared_inter) must be below 2^30; split the batch", fn);
     if (!L->shared_gate || !L->shared_up || !L->shared_down)

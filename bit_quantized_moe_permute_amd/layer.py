@@ -39,6 +39,7 @@ class AdapterPool:
         self.n, self.max_rank = n, R
         self.device_index = given[0][0].get_device()
         self.desc = AdapterDesc(n_adapters=n, max_rank=R)
+        self._given = dict(gate=gate, up=up, down=down, rank=rank, scale=scale)
         self._keep = []
         for name, (ab, rows, cols) in pairs.items():
             if ab is not None:
@@ -57,6 +58,12 @@ class AdapterPool:
             raise ValueError(f"{name}: adapters on devices {self.device_index} and {t.get_device()}")
         self._keep.append(t)
         setattr(self.desc, name, t.data_ptr())
+
+    def clone(self) -> "AdapterPool":
+        """A second copy of every device tensor (distinct addresses, same values)."""
+        return AdapterPool(self.hidden, self.inter, **{
+            n: t if t is None else t.clone() if n in ("rank", "scale") else tuple(v.clone() for v in t)
+            for n, t in self._given.items()})
 
 
 class DeviceLayer:
@@ -150,6 +157,7 @@ class DeviceLayer:
         c.bias = None if self.bias is None else self.bias.clone()
         c.shared = None if self.shared is None else tuple(s.clone() for s in self.shared)
         c.steer_v = None if self.steer_v is None else self.steer_v.clone()
+        c.adapters = None if self.adapters is None else self.adapters.clone()
         c.desc = c.make_desc(self.path)
         return c
 

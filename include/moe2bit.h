@@ -369,8 +369,10 @@ moe_status moe_layer(const moe_layer_desc *L, const void *x, int32_t x_dt, int32
                      int32_t *expert_offsets, int32_t *perm, int32_t *active, float *slot_out, float *shared_out,
                      const float *steer_v, float steer_f, float *y, void *ws, size_t ws_bytes, void *stream);
 
-/* Largest row length of the two norm calls below. */
+/* Largest row length of the two norm calls below, and most tokens of a call to
+ * them and to moe_shared_ffn (a launch's threads are counted in 32 bits). */
 #define MOE_NORM_MAX_HIDDEN 32768
+#define MOE_MAX_TOKENS ((1 << 22) - 1)
 
 /*
  * Residual addition and root-mean-square norm around the layer: the layer reads
@@ -399,8 +401,8 @@ moe_status moe_layer(const moe_layer_desc *L, const void *x, int32_t x_dt, int32
  * Every hidden up to MOE_NORM_MAX_HIDDEN is taken; hidden % 8 == 0 with 16-byte
  * aligned pointers takes 16-byte loads.  Errors: MOE_ERR_INVALID_ARG (null,
  * misaligned to its own type or overlapping buffer, bad shape or dtype, eps
- * negative or not finite), MOE_ERR_UNSUPPORTED (hidden above the limit),
- * MOE_ERR_DEVICE (launch failure).
+ * negative or not finite), MOE_ERR_UNSUPPORTED (hidden or n_tokens above the
+ * limits), MOE_ERR_DEVICE (launch failure).
  */
 moe_status moe_add_rms_norm(const void *x, int32_t x_dt, int32_t n_tokens, int32_t hidden, const void *residual,
                             void *residual_out, int32_t res_dt, const void *weight, int32_t w_dt, float eps, void *y,
@@ -464,14 +466,18 @@ size_t moe_shared_ffn_workspace(const moe_layer_desc *L, const moe_adapter_desc 
  *     bytes; calls that may overlap in time need one each.
  * Sums are fp32 in an order fixed by the shapes; fp32 activations, the low-rank
  * products A[a] x and, with an fp32 out, the SwiGLU result h are carried with
- * all 24 bits (three bf16 parts), h with a bf16 out as one bf16 value.  A token's result has the same bits whatever other
- * tokens and adapters the call holds (at the same n_tokens and n_adapters), and
- * non-finite values in one adapter reach only the tokens that use it.
+ * all 24 bits (three bf16 parts; with a bf16 out the products of many tokens
+ * read two parts of the low-rank ones), h with a bf16 out as one bf16 value.
+ * Values that round to infinity in bf16 (3.396e38 and above) give NaN.
+ * A token's result has the same bits whatever other tokens and adapters the
+ * call holds (at the same n_tokens and n_adapters), and non-finite values in
+ * one adapter or token reach only the tokens that use it.
  * hidden and shared_inter must be multiples of 8; x, out and the weights 16-byte
  * aligned.  Errors: MOE_ERR_INVALID_ARG (null, misaligned or overlapping
  * pointer, bad shape or dtype, workspace too small), MOE_ERR_UNSUPPORTED (hidden
- * or shared_inter above MOE_SHARED_MAX_DIM, or n_tokens times the larger of them
- * 2^30 or more), MOE_ERR_DEVICE (launch failure).
+ * or shared_inter above MOE_SHARED_MAX_DIM, n_tokens above MOE_MAX_TOKENS, or
+ * n_tokens times the larger dimension 2^30 or more), MOE_ERR_DEVICE (launch
+ * failure).
  */
 moe_status moe_shared_ffn(const moe_layer_desc *L, const moe_adapter_desc *A, const void *x, int32_t x_dt,
                           int32_t n_tokens, const int32_t *token_adapter, void *out, int32_t out_dt, void *ws,

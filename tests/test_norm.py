@@ -376,6 +376,8 @@ def test_add_rms_norm_refuses_long_rows(calls):
     far = dict(x=1 << 30, res=2 << 30, out=3 << 30, w=4 << 30, y=5 << 30)
     st, msg = _add(calls, H=32769, **far)
     assert st == 2 and "32768" in msg
+    st, msg = _add(calls, T=1 << 22, H=8, **far)
+    assert st == 2 and "split the batch" in msg
 
 
 @needs_lib

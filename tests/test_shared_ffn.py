@@ -6,8 +6,8 @@ W' = Wd + c B A of the token's adapter: what is off in h passes through all of W
 2^-17 of its terms' root sum of squares; gate and up enter h with a factor of at most 1.1 each (the largest slope of silu),
 and the down product adds its own: sqrt(2 * 1.1^2 + 1) * 2^-17 < 2^-16.  bf16 out: a rounding to bf16 is off by at most 2^-8,
 uniform rounding errors have 1/sqrt(3) of that as their root mean square, and errors of independent terms add in squares:
-h and the result at
-2^-8 / sqrt(3) each: 0.82 * 2^-8.  Below 64 terms that averaging is no argument (one term may be most of the sum), and the
+h and the result at 2^-8 / sqrt(3)
+each: 0.82 * 2^-8.  Below 64 terms that averaging is no argument (one term may be most of the sum), and the
 bf16 bound is the one of the largest errors: with |e_i| <= 2^-8 and w_i the columns of Wd,
 |sum e_i h_i w_i| <= 2^-8 sum |h_i| |w_i| <= 2^-8 sqrt(I) sqrt(sum h_i^2 |w_i|^2), and 2^-8 of the result: 2^-8 (sqrt(I) + 1).
 With adapters of low rank an output can be all in one direction b, where the errors of h meet in one number,
@@ -159,7 +159,7 @@ def test_with_adapters(m, T, H, I, n, R, x_t, out_t):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("projections", [("gate",), ("up",), ("down",), ("gate", "down"), ("gate", "up")])
-@pytest.mark.parametrize("T", [5, 90])
+@pytest.mark.parametrize("T", [5, 90, 300])
 def test_some_projections(m, projections, T):
     note(f"adapters of {projections} T={T}")
     c = Case(T, 136, 88, 4, 16, seed=T, projections=projections, scales=False)
@@ -174,6 +174,30 @@ def test_larger_layers(m, T, H, I, n, R, out_t):
     note(f"T={T} H={H} I={I} n={n} R={R} out={out_t}")
     c = Case(T, H, I, n, R, seed=T)
     c.check(c.run(m, out_t))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I", [(2100, 264, 2056), (2100, 4104, 72), (1100, 264, 2056), (1100, 4104, 72), (2112, 320, 2048)])
+@pytest.mark.parametrize("n", [0, 3])
+def test_wide_tiles(m, T, H, I, n):
+    """Tiles of 128 and 256 tokens (bf16 activations; enough tiles for every compute unit), whole and with odd ends."""
+    note(f"wide tiles T={T} H={H} I={I} n={n}")
+    c = Case(T, H, I, n, 24, seed=T, ranks=[24, 5, 17])
+    c.check(c.run(m, BF16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,R", [(1, 8), (1, 16), (2, 8), (1, 24), (2, 16), (3, 8)])
+@pytest.mark.parametrize("I", [8, 264, 2056, 8200])
+@pytest.mark.parametrize("out_t", [F32, BF16])
+def test_few_values(m, T, R, I, out_t):
+    """Both sides of the limits up to which the down product forms the low-rank results of h itself."""
+    note(f"few values T={T} R={R} I={I} out={out_t}")
+    for ranks in ([R], [R - 3, 0, 1]):
+        c = Case(T, 72, I, 4, R, seed=T, ranks=ranks)
+        c.ids = torch.arange(T, dtype=torch.int32)
+        c.spoil()
+        c.check(c.run(m, out_t))
 
 
 @pytest.mark.gpu
@@ -192,7 +216,7 @@ def test_token_orders(m, T, mix):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [3, 70])
+@pytest.mark.parametrize("T", [3, 70, 300])
 def test_pools_beyond_32_bits(m, T):
     """The last adapter of a pool whose A matrices pass 2^31 elements."""
     note(f"large pool T={T}")
@@ -221,7 +245,7 @@ def test_pools_beyond_32_bits(m, T):
 # one request and the others
 # ----------------------------------------------------------------------------
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [7, 20, 64, 65, 200])
+@pytest.mark.parametrize("T", [7, 20, 64, 65, 200, 257, 700])
 def test_a_token_does_not_depend_on_the_others(m, T):
     """Same bits for a token whatever adapters the other tokens use, in whatever order, and with NaN adapters among
     theirs; the tokens with the NaN adapter alone become NaN."""
@@ -244,6 +268,31 @@ def test_a_token_does_not_depend_on_the_others(m, T):
     got = c.run(m)
     assert torch.isnan(got[0]).all()
     assert torch.equal(got[1:], clean[1:])
+
+
+@pytest.mark.gpu
+def test_a_token_of_two(m):
+    """The same where the down product forms the low-rank results itself."""
+    note("independence T=2")
+    c = Case(2, 264, 136, 3, 8, seed=2)
+    c.ids = torch.tensor([0, 1], dtype=torch.int32)
+    first = c.run(m)
+    c.a["down"][0], c.b["up"][0] = float("nan"), float("inf")
+    got = c.run(m)
+    assert torch.isnan(got[0]).all() and torch.equal(got[1], first[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 40, 200, 300])
+@pytest.mark.parametrize("x_t", [BF16, F32])
+def test_a_token_that_is_not_finite(m, T, x_t):
+    """A padded row that holds NaN or infinities reaches no other row."""
+    note(f"not finite T={T} x={x_t}")
+    c = Case(T, 264, 136, 3, 8, x_t=x_t, seed=T)
+    clean = c.run(m)
+    c.x[0, 3], c.x[0, 90] = float("inf"), float("nan")
+    got = c.run(m)
+    assert torch.isnan(got[0]).all() and torch.equal(got[1:], clean[1:])
 
 
 @pytest.mark.gpu
@@ -271,7 +320,7 @@ def test_without_adapters_matches_the_layer_call(m):
 # streams and graphs
 # ----------------------------------------------------------------------------
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [3, 130])
+@pytest.mark.parametrize("T", [1, 3, 130, 300])
 def test_graph_replays_match_eager_calls(m, T):
     """Captured once, replayed with other activations, other token indices and another adapter loaded into a slot."""
     note(f"graph T={T}")
@@ -303,9 +352,39 @@ def test_graph_replays_match_eager_calls(m, T):
 
 
 @pytest.mark.gpu
+def test_two_graphs_share_a_workspace(m):
+    """Two captured calls of other sizes with one workspace, replayed in turn on one stream, eager calls between."""
+    note("two graphs, one workspace")
+    c = [Case(T, 264, 136, 6, 16, seed=T) for T in (3, 300)]
+    want = [k.run(m) for k in c]
+    on = [k.on_gpu(m) for k in c]
+    xs, outs = [k.x.cuda() for k in c], [torch.empty(k.T, k.H, device="cuda") for k in c]
+    ws = torch.empty(max(m.moe_shared_ffn_workspace(o[1], k.T, o[2]) for k, o in zip(c, on)), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graphs, cap = [], torch.cuda.Stream()
+    for o, x, out in zip(on, xs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.stream(cap):
+            with torch.cuda.graph(graphs[-1], stream=cap):
+                m.moe_shared_ffn(o[1], x, out, ws, o[2], o[3])
+    for i in range(4):
+        for out in outs:
+            out.fill_(7.0)
+        ws.fill_(0xFF if i % 2 else 0)
+        graphs[i % 2].replay()
+        graphs[1 - i % 2].replay()
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert torch.equal(out.cpu(), w), i
+        m.moe_shared_ffn(on[0][1], xs[0], outs[0], ws, on[0][2], on[0][3])
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0].cpu(), want[0]), i
+
+
+@pytest.mark.gpu
 def test_two_streams_with_a_workspace_each(m):
     note("two streams")
-    c = [Case(T, 264, 136, 6, 16, seed=T) for T in (40, 170)]
+    c = [Case(T, 264, 136, 6, 16, seed=T) for T in (40, 170, 300)]
     want = [k.run(m) for k in c]
     sides = [torch.cuda.Stream() for _ in c]
     on = [k.on_gpu(m) for k in c]
@@ -417,11 +496,35 @@ def test_shared_ffn_refuses(bad, word):
 
 
 @needs_lib
+@pytest.mark.parametrize("bad,word", [
+    (dict(layer=dict(hidden=(1 << 20) + 8)), "above"), (dict(layer=dict(shared_inter=(1 << 20) + 8)), "above"),
+    (dict(layer=dict(hidden=8, shared_inter=8), T=1 << 22), "n_tokens >"), (dict(layer=dict(hidden=1 << 20), T=1 << 10), "split the batch"),
+    (dict(layer=dict(shared_inter=1 << 10), T=1 << 20), "split the batch"),
+])
+def test_shared_ffn_limits(bad, word):
+    st, msg, ws = call(**bad)
+    assert st == 2 and word in msg and ws == 0, (st, msg)
+
+
+@needs_lib
 def test_workspace_sizes():
     assert call(T=0)[2] == 0 and call(layer=dict(hidden=60))[2] == 0
     none, some = call(x=None)[2], call(pool={}, x=None)[2]
     assert 0 < none < some
     assert call(pool={}, T=100, x=None)[2] > some
+
+
+@needs_lib
+def test_pool_clone():
+    import bit_quantized_moe_permute_amd as m
+    c = Case(3, 64, 32, 2, 8, projections=("gate", "down"), ranks=[8, 3])
+    pool = m.AdapterPool(64, 32, rank=c.rank, scale=c.scale, **{p: (c.a[p], c.b[p]) for p in c.a})
+    other = pool.clone()
+    assert (other.hidden, other.inter, other.n, other.max_rank) == (64, 32, 2, 8) and other.desc.up_a is None
+    assert len(other._keep) == len(pool._keep) == 6
+    for s, t in zip(pool._keep, other._keep):
+        assert torch.equal(s, t) and s.data_ptr() != t.data_ptr()
+    assert other.desc.gate_a == other._keep[0].data_ptr() and other.desc.scale == other._keep[-1].data_ptr()
 
 
 @needs_lib
