@@ -532,8 +532,9 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
 // have no register outputs; wait_stage() counts them (the kernel has no other vector memory access between the first
 // issue and the last stage) and orders the workgroup.
 // ---------------------------------------------------------------------------
-constexpr int BW = 128, BK = 64, STAGES = 3;
+constexpr int BK = 64, STAGES = 3;
 constexpr int many_split(int BT) { return BT == 64 ? 2 : 1; }
+constexpr int many_threads(int BW, int BT) { return 64 * (BW / 64) * 2 * many_split(BT); }
 enum { MODE_GATE_UP = 0, MODE_DOWN = 1, MODE_LOW_RANK = 2 };
 
 // Down-rank (MODE_LOW_RANK): a tile's tokens are an item of the plan, its weight rows those of that adapter's A matrices, and
@@ -541,16 +542,17 @@ enum { MODE_GATE_UP = 0, MODE_DOWN = 1, MODE_LOW_RANK = 2 };
 // The small tiles have two groups of four waves, each working two of a stage's four 16-wide slices: with one wave per SIMD and
 // a few products per slice, the waits for LDS would stand open.
 // TAIL: K is no multiple of 64, so a row's last step is not a whole one.
-template <int MODE, int P, int BT, bool TAIL>
-__global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Product g, int tiles_w, int tiles_t) {
+template <int MODE, int P, int BW, int BT, bool TAIL>
+__global__ __launch_bounds__(many_threads(BW, BT)) void k_many(SharedArgs a, Product g, int tiles_w, int tiles_t) {
     constexpr bool GU = MODE == MODE_GATE_UP, LOW = MODE == MODE_LOW_RANK;
     constexpr int WT = 2;                                    // waves along the tokens, and along the weight rows
-    constexpr int FW = BW / 2 / 32, FT = BT / WT / 32;       // 32 x 32 fragments per wave
-    constexpr int KSP = many_split(BT), NS = 4 / KSP;        // groups of four waves that share a stage's slices; slices of each
-    constexpr int ROWS = BW + P * BT, LOADS = ROWS / 8 / (4 * KSP);          // direct-to-LDS loads (8 rows each) per wave and stage
+    constexpr int FW = 2, FT = BT / WT / 32;                 // 32 x 32 fragments per wave
+    constexpr int GW = BW / 64 * WT;                         // waves of a group, which computes the tile from
+    constexpr int KSP = many_split(BT), NS = 4 / KSP;        // NS of a stage's four slices; groups
+    constexpr int ROWS = BW + P * BT, LOADS = ROWS / 8 / (GW * KSP);         // direct-to-LDS loads (8 rows each) per wave and stage
     __shared__ __attribute__((aligned(1024))) uint4 tile[STAGES][ROWS * 8];
     const int lane = threadIdx.x & 63, i32 = lane & 31, hh = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w4 = wave & 3, kk0 = (wave >> 2) * NS;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w4 = wave % GW, kk0 = wave / GW * NS;
     const int K = g.K;
     // XCD-aware order: consecutive workgroups go to the eight XCDs in turn; each XCD takes a run of tiles with the
     // token tile fastest, so the workgroups that read the same weight rows share an L2
@@ -625,6 +627,9 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
     const int rw = (w4 / WT) * FW * 32, rt = BW + (w4 % WT) * FT * 32;
+    int idj[FT];                                             // adapters of this lane's tokens (loaded ahead of the stages)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) idj[j] = LOW ? -1 : adapter_at(a, t0 + (rt - BW) + j * 32 + i32);
     uint4 fw[2][FW], ft[2][P * FT];
     auto read_one = [&](const uint4 *t, int kk, int b, int n) {      // fragment n of the slice: weights first
         const int c = (2 * kk + hh) ^ (i32 >> 1 & 7);
@@ -659,45 +664,41 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
     next_stage();
 #pragma unroll
     for (int i = 0; i < LOADS / NS; ++i) issue(i);
+    // Weights behind the row's end count as zeros: in the last step's stage they are overwritten in LDS once it is there.
+    auto clear_tail = [&](int step, uint4 *t) {
+        if (!TAIL || step != ksteps - 1) return;
+        for (int e = threadIdx.x; e < BW * 8; e += 64 * GW * KSP)
+            if (((e & 7) ^ (e >> 4 & 7)) >= tail) t[e] = make_uint4(0, 0, 0, 0);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
     wait_stage<LOADS + LOADS / NS>();
+    clear_tail(sb, tile[0]);
     int rb = 0, step = sb;
 #pragma unroll
     for (int n = 0; n < FW + P * FT; ++n) read_one(tile[0], kk0, 0, n);
     for (int s = 0; s < nsteps; ++s) {
         const uint4 *t = tile[rb];
-        // weights behind the row's end count as zeros; the step's other chunks are masked alike
-        auto mask = [&](int kk, int b) {
-            if (TAIL && step == ksteps - 1) {
 #pragma unroll
-                for (int i = 0; i < FW; ++i)
-                    if (2 * kk + hh >= tail) fw[b][i] = make_uint4(0, 0, 0, 0);
-            }
-        };
-#pragma unroll
-        for (int k = 0; k < NS - 1; ++k) {
-            mask(kk0 + k, k & 1);
-            slice(k & 1, t, kk0 + k + 1, k + 1);
-        }
+        for (int k = 0; k < NS - 1; ++k) slice(k & 1, t, kk0 + k + 1, k + 1);
         next_stage();
         rb = rb == STAGES - 1 ? 0 : rb + 1;
         wait_stage<LOADS>();
-        mask(kk0 + NS - 1, 1);
+        clear_tail(++step, tile[rb]);
         slice(1, tile[rb], kk0, 0);                          // behind the last stage: a read of old values, not used
-        ++step;
     }
     wait_stage<0>();
     if constexpr (KSP == 2) {                                // the second group's sums join the first's, which goes on alone
         f32x4_t *part = reinterpret_cast<f32x4_t *>(tile) + w4 * (FW * FT * 4 * 64) + lane;
-        static_assert(4 * FW * FT * 4 * 64 * sizeof(f32x4_t) <= sizeof(tile), "");
+        static_assert(GW * FW * FT * 4 * 64 * sizeof(f32x4_t) <= sizeof(tile), "");
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < FW * FT * 4; ++i) {
             f32x16_t &y = acc[i / 4 / FT][i / 4 % FT];
             const int v = i % 4 * 4;
-            if (wave >= 4) part[i * 64] = f32x4_t{y[v], y[v + 1], y[v + 2], y[v + 3]};
+            if (wave >= GW) part[i * 64] = f32x4_t{y[v], y[v + 1], y[v + 2], y[v + 3]};
         }
         __syncthreads();
-        if (wave >= 4) return;
+        if (wave >= GW) return;
 #pragma unroll
         for (int i = 0; i < FW * FT * 4; ++i) {
             f32x16_t &y = acc[i / 4 / FT][i / 4 % FT];
@@ -726,73 +727,81 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
         }
         return;
     } else if (a.n) {
-        // One adapter of 64 of this wave's tokens at a time, in accumulators of its own.  Rank values go 16 at a time, each
-        // once with each part of the token's low-rank result.
-        constexpr int NP = GU ? 2 : 1, JG = FT < 2 ? FT : 2;
+        // Up to NA adapters of 64 of this wave's tokens at a time, whose loads go out together; rank values go 16 at a time, each
+        // once with each part of the tokens' low-rank results.  An adapter's products are formed for all of the tokens, in
+        // sums of their own, and added to those of its own tokens.
+        constexpr int NP = GU ? 2 : 1, JG = FT < 2 ? FT : 2, SP = !GU && P == 1 ? 2 : 3, NA = 4;
 #pragma unroll
         for (int jg = 0; jg < FT; jg += JG) {
-            int idj[JG];
             unsigned long long left[JG];
 #pragma unroll
-            for (int j = 0; j < JG; ++j) {
-                idj[j] = adapter_at(a, t0 + (rt - BW) + (jg + j) * 32 + i32);
-                left[j] = __ballot(idj[j] >= 0);
-            }
+            for (int j = 0; j < JG; ++j) left[j] = __ballot(idj[jg + j] >= 0);
+            while (left[0] | left[JG - 1]) {
+                int ad[NA], rank[NA], top = 0;
 #pragma unroll
-            for (int j0 = 0; j0 < JG; ++j0)
-                while (left[j0]) {
-                    const int ad = __builtin_amdgcn_readlane(idj[j0], __ffsll(left[j0]) - 1);
+                for (int q = 0; q < NA; ++q) {
+                    ad[q] = -1;
+                    rank[q] = 0;
+                    if (!(left[0] | left[JG - 1])) continue;
+                    ad[q] = left[0] ? __builtin_amdgcn_readlane(idj[jg], __ffsll(left[0]) - 1)
+                                    : __builtin_amdgcn_readlane(idj[jg + JG - 1], __ffsll(left[JG - 1]) - 1);
 #pragma unroll
-                    for (int j = 0; j < JG; ++j) left[j] &= ~__ballot(idj[j] == ad);
-                    const int rank = rank_of(a, ad);
-                    f32x16_t d[FW][JG];
+                    for (int j = 0; j < JG; ++j) left[j] &= ~__ballot(idj[jg + j] == ad[q]);
+                    rank[q] = rank_of(a, ad[q]);
+                }
+                int c0 = 0;
+                do {
+                    const int j8 = c0 + hh;
+                    const bool in = 8 * j8 < a.R;
+                    uint4 w[NA][FW], u[JG][NP][SP];
 #pragma unroll
-                    for (int i = 0; i < FW; ++i)
+                    for (int j = 0; j < JG; ++j)
 #pragma unroll
-                        for (int j = 0; j < JG; ++j)
+                        for (int p = 0; p < NP; ++p) {
 #pragma unroll
-                            for (int v = 0; v < 16; ++v) d[i][j][v] = 0.f;
-                    for (int c0 = 0; 8 * c0 < rank; c0 += 2) {
-                        const int j8 = c0 + hh;
-                        const bool in = 8 * j8 < rank;
-                        uint4 w[FW], u[JG][NP][3];
+                            for (int h = 0; h < SP; ++h) u[j][p][h] = make_uint4(0, 0, 0, 0);
+                            if (in && idj[jg + j] >= 0 && g.b[p]) {
+                                const uint16_t *s = low_rank_row(a, g.s, NP, t0 + (rt - BW) + (jg + j) * 32 + i32, p) + 8 * j8;
+#pragma unroll
+                                for (int h = 0; h < SP; ++h) u[j][p][h] = load16(s + h * a.R);
+                            }
+                        }
+#pragma unroll
+                    for (int q = 0; q < NA; ++q)
 #pragma unroll
                         for (int i = 0; i < FW; ++i) {
                             const int m = GU ? i & 1 : 0;
                             const int wr = GU ? w0 + (rw >> 6) * 32 + i32 : w0 + rw + i * 32 + i32;
-                            w[i] = make_uint4(0, 0, 0, 0);
-                            if (in && wr < g.N && g.b[m]) w[i] = load16(g.b[m] + ((int64_t)ad * g.N + wr) * a.R + 8 * j8);
+                            w[q][i] = make_uint4(0, 0, 0, 0);
+                            if (in && ad[q] >= 0 && wr < g.N && g.b[m])
+                                w[q][i] = load16(g.b[m] + ((int64_t)ad[q] * g.N + wr) * a.R + 8 * j8);
+                        }
+#pragma unroll
+                    for (int q = 0; q < NA; ++q) {
+                        if (8 * c0 >= rank[q]) continue;
+                        top = max(top, rank[q]);
+                        f32x16_t d[FW][JG];
+#pragma unroll
+                        for (int i = 0; i < FW; ++i) {
+                            const uint4 wq = keep_first(w[q][i], rank[q] - 8 * j8);
+#pragma unroll
+                            for (int j = 0; j < JG; ++j) {
+#pragma unroll
+                                for (int v = 0; v < 16; ++v) d[i][j][v] = 0.f;
+#pragma unroll
+                                for (int h = 0; h < SP; ++h) d[i][j] = mfma32(wq, u[j][GU ? i & 1 : 0][h], d[i][j]);
+                            }
                         }
 #pragma unroll
                         for (int j = 0; j < JG; ++j)
+                            if (idj[jg + j] == ad[q]) {
 #pragma unroll
-                            for (int p = 0; p < NP; ++p) {
-                                u[j][p][0] = u[j][p][1] = u[j][p][2] = make_uint4(0, 0, 0, 0);
-                                if (in && idj[j] == ad && g.b[p]) {
-                                    const int pos = t0 + (rt - BW) + (jg + j) * 32 + i32;
-                                    const uint16_t *s = low_rank_row(a, g.s, NP, pos, p) + 8 * j8;
-#pragma unroll
-                                    for (int h = 0; h < 3; ++h)
-                                        if (h < a.sparts) u[j][p][h] = load16(s + h * a.R);
-                                }
+                                for (int i = 0; i < FW; ++i) acc[i][jg + j] += d[i][j];
                             }
-#pragma unroll
-                        for (int i = 0; i < FW; ++i) {
-                            if (rank - 8 * c0 < 16) w[i] = keep_first(w[i], rank - 8 * j8);
-#pragma unroll
-                            for (int j = 0; j < JG; ++j)
-#pragma unroll
-                                for (int h = 0; h < 3; ++h)
-                                    if (h < a.sparts) d[i][j] = mfma32(w[i], u[j][GU ? i & 1 : 0][h], d[i][j]);
-                        }
                     }
-#pragma unroll
-                    for (int j = 0; j < JG; ++j)
-                        if (idj[j] == ad) {
-#pragma unroll
-                            for (int i = 0; i < FW; ++i) acc[i][jg + j] += d[i][j];
-                        }
-                }
+                    c0 += 2;
+                } while (8 * c0 < top);
+            }
         }
     }
 #pragma unroll
@@ -808,8 +817,12 @@ __global__ __launch_bounds__(256 * many_split(BT)) void k_many(SharedArgs a, Pro
                 float h[4];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) h[v] = silu_mul(acc[0][j][4 * v4 + v], acc[1][j][4 * v4 + v]);
-                for (int p = 0; p < g.hp; ++p)
-                    *reinterpret_cast<uint2 *>(g.h + (int64_t)p * a.T * g.N + row + wr) = pack_part(h, p);
+                *reinterpret_cast<uint2 *>(g.h + row + wr) = pack_part(h, 0);
+                if (g.hp > 1) {
+#pragma unroll
+                    for (int p = 1; p < 3; ++p)
+                        *reinterpret_cast<uint2 *>(g.h + (int64_t)p * a.T * g.N + row + wr) = pack_part(h, p);
+                }
             }
         } else {
             const int64_t row = (int64_t)(a.sorted ? a.perm[pos] : pos) * g.N;
@@ -905,39 +918,45 @@ hipError_t few_inputs(const SharedArgs &a, const LowRank &L, int src, uint16_t *
 }
 
 template <int MODE, int P, bool TAIL>
-hipError_t launch_many(const SharedArgs &a, const Product &g, int bt, int tw, int tt, int parts, hipStream_t st) {
-    const dim3 grd((unsigned)((tw * tt + 7) / 8 * 8), (unsigned)parts), blk((unsigned)(256 * many_split(bt)));
+hipError_t launch_many(const SharedArgs &a, const Product &g, int bw, int bt, int tw, int tt, int parts, hipStream_t st) {
+    const dim3 grd((unsigned)((tw * tt + 7) / 8 * 8), (unsigned)parts), blk((unsigned)many_threads(bw, bt));
     if constexpr (MODE != MODE_LOW_RANK && P == 1) {
-        if (bt == 256) hipLaunchKernelGGL((k_many<MODE, P, 256, TAIL>), grd, blk, 0, st, a, g, tw, tt);
-        else if (bt == 128) hipLaunchKernelGGL((k_many<MODE, P, 128, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+        if (bt == 256) hipLaunchKernelGGL((k_many<MODE, P, 128, 256, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+        else if (bt == 128) hipLaunchKernelGGL((k_many<MODE, P, 128, 128, TAIL>), grd, blk, 0, st, a, g, tw, tt);
     }
-    if (bt == 64) hipLaunchKernelGGL((k_many<MODE, P, 64, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+    if (bt == 64 && bw == 128) hipLaunchKernelGGL((k_many<MODE, P, 128, 64, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+    else if (bt == 64) hipLaunchKernelGGL((k_many<MODE, P, 64, 64, TAIL>), grd, blk, 0, st, a, g, tw, tt);
     return hipGetLastError();
 }
 
 template <int MODE>
-hipError_t many_tiles(const SharedArgs &a, const Product &g, int planes, int bt, int tw, int tt, int parts, hipStream_t st) {
+hipError_t many_tiles(const SharedArgs &a, const Product &g, int planes, int bw, int bt, int tt, int parts, hipStream_t st) {
+    const int rows = MODE == MODE_GATE_UP ? bw / 2 : bw, tw = (g.N + rows - 1) / rows;
     if (planes == 1)
-        return g.K % BK ? launch_many<MODE, 1, true>(a, g, bt, tw, tt, parts, st)
-                        : launch_many<MODE, 1, false>(a, g, bt, tw, tt, parts, st);
-    return g.K % BK ? launch_many<MODE, 3, true>(a, g, bt, tw, tt, parts, st)
-                    : launch_many<MODE, 3, false>(a, g, bt, tw, tt, parts, st);
+        return g.K % BK ? launch_many<MODE, 1, true>(a, g, bw, bt, tw, tt, parts, st)
+                        : launch_many<MODE, 1, false>(a, g, bw, bt, tw, tt, parts, st);
+    return g.K % BK ? launch_many<MODE, 3, true>(a, g, bw, bt, tw, tt, parts, st)
+                    : launch_many<MODE, 3, false>(a, g, bw, bt, tw, tt, parts, st);
 }
 
 template <int MODE>
 hipError_t many(const SharedArgs &a, const Product &g, int planes, hipStream_t st) {
-    const int rows = MODE == MODE_GATE_UP ? BW / 2 : BW, tw = (g.N + rows - 1) / rows;
+    const int rows = MODE == MODE_GATE_UP ? 64 : 128, tw = (g.N + rows - 1) / rows;
     auto tiles = [&](int bt) { return tw * ((a.T + bt - 1) / bt); };
     // three planes of 128 tokens would not fit three times into LDS
     const int bt = planes > 1 ? 64 : tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
-    return many_tiles<MODE>(a, g, planes, bt, tw, (a.T + bt - 1) / bt, 1, st);
+    // half tiles where whole ones are for half of the compute units at most (whole call, whole tiles against half ones: 333
+    // tokens 1000 x 520 61.2 and 58.0 us, 300 tokens 2048 x 512 51.4 and 48.5, 400 tokens 1024 x 1024 49.4 and 46.7)
+    const int bw = bt == 64 && tiles(64) <= 128 ? 64 : 128;
+    return many_tiles<MODE>(a, g, planes, bw, bt, (a.T + bt - 1) / bt, 1, st);
 }
 
 int plan_items(int T, int n) { return T / ITEM_TOKENS + (T < n ? T : n); }     // at most
 
 // Parts of K of the down-rank products: enough workgroups for the 256 CUs, each with some steps.
+int low_rank_rows(int N) { return N <= 64 ? 64 : 128; }
 int low_rank_parts(int T, int n, int R, int np, int K) {
-    const int tiles = plan_items(T, n) * ((np * R + BW - 1) / BW), steps = (K + BK - 1) / BK;
+    const int bw = low_rank_rows(np * R), tiles = plan_items(T, n) * ((np * R + bw - 1) / bw), steps = (K + BK - 1) / BK;
     int parts = 1;
     while (parts < MAX_PARTS && parts * tiles < 256 && steps >= 8 * parts) parts *= 2;
     return parts;
@@ -948,7 +967,7 @@ hipError_t many_low_rank(const SharedArgs &a, const LowRank &L, int planes, hipS
     g.x = static_cast<const uint16_t *>(L.xv); g.K = L.K; g.N = L.np * a.R; g.gather = L.gather;
     g.w[0] = L.a[0]; g.w[1] = L.a[1]; g.part = L.part;
     const int parts = low_rank_parts(a.T, a.n, a.R, L.np, L.K);
-    hipError_t e = many_tiles<MODE_LOW_RANK>(a, g, planes, 64, (g.N + BW - 1) / BW, plan_items(a.T, a.n), parts, st);
+    hipError_t e = many_tiles<MODE_LOW_RANK>(a, g, planes, low_rank_rows(g.N), 64, plan_items(a.T, a.n), parts, st);
     if (e != hipSuccess) return e;
     const int64_t quads = (int64_t)a.T * g.N / 4;
     hipLaunchKernelGGL(k_low_rank_sum, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, st, a, L.part, parts, L.np, L.s);
@@ -1014,7 +1033,6 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     uint16_t *s = u16(l.s), *h = u16(l.h);
     float *part = reinterpret_cast<float *>(base + l.part);
     const bool small = few_path(a.T, a.H, a.Is);
-    a.sparts = a.out_bf16 ? 2 : 3;                          // 16 bits of the low-rank results are enough beside a bf16 result
     a.sorted = a.n > 0 && !small;
     SharedArgs ag = a, ad = a;                              // a half without adapters runs as if there were none
     if (!a.gate_a && !a.up_a) ag.n = 0;

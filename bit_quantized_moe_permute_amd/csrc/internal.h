@@ -118,7 +118,6 @@ struct SharedArgs {
     int out_bf16;
     // filled by the launcher
     int sorted;
-    int sparts;                          // parts of the low-rank results that many-token products read
     int32_t *perm, *plan_ad, *n_items;   // sorted position -> token, its adapter (-1: none)
     int4 *items;                         // adapter, first sorted position, tokens
 };
