@@ -977,11 +977,16 @@ hipError_t many_low_rank(const SharedArgs &a, const LowRank &L, int planes, hipS
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Whether the weights stream past groups of up to 64 tokens (once from memory, then from the caches), or tiles of both operands
-// pass through LDS, which costs four more launches for the plan and the down-rank parts.  Measured, streamed against tiles,
-// fp32 out, hidden x inter: 100 tokens 1024 x 1024 27 and 50 us, 4096 x 2048 61 and 72; 200 tokens 2048 x 1024 46 and 53; 128 tokens
-// 4096 x 2048 (bf16 out) 56 and 63; 333 tokens 1000 x 520 58 and 61; 600 tokens 512 x 1024 63 and 41.
+// pass through LDS, which costs up to five more launches for the plan and the down-rank parts.  Streamed against tiles,
+// hidden x inter, 16 adapters of rank up to 16 in runs, fp32 out:
+//   2 groups: 100 tokens 1024 x 1024 30.5 and 47.1 us, 128 tokens 4096 x 2048 77.4 and 67.1 (bf16 out 65.1 and 63.0; an
+//     adapter of rank 64 for each of 100 tokens, bf16 out: 73.9 and 93.0);
+//   4 groups: 256 tokens 512 x 512 37.6 and 40.6, 1024 x 1024 (bf16 out) 37.5 and 40.7, 200 tokens 2048 x 1024 56.0 and 51.1,
+//     256 tokens 4096 x 512 73.8 and 54.5;
+//   6 groups: 333 tokens 1000 x 520 (fp32 x) 69.4 and 51.7.
 bool few_path(int T, int H, int Is) {
-    return T <= FEW_TOKENS || (T <= 4 * FEW_TOKENS && (int64_t)few_groups(T) * H * Is <= 1 << 24);
+    const int64_t reads = (int64_t)few_groups(T) * H * Is;
+    return T <= FEW_TOKENS || (T <= 2 * FEW_TOKENS && reads <= 1 << 24) || (T <= 4 * FEW_TOKENS && reads <= 1 << 22);
 }
 
 // Workspace layout, from the shapes and types alone.
