@@ -512,7 +512,7 @@ static moe_status norm_args(const char *fn, int32_t n_tokens, int32_t hidden, co
     a.residual = residual; a.residual_out = residual_out;
     a.res_kind = !residual ? moe::RES_NONE : res_dt == MOE_DT_F32 ? moe::RES_F32 : moe::RES_BF16;
     a.weight = weight; a.w_bf16 = w_dt == MOE_DT_BF16;
-    a.eps = eps;
+    a.eps = eps; a.inv_hidden = 1.0 / hidden;
     a.y = y; a.y_scale = y_scale;
     a.y_kind = y_dt == MOE_DT_F32 ? moe::NORM_F32 : y_dt == MOE_DT_BF16 ? moe::NORM_BF16
              : y_dt == MOE_DT_E4M3_BLOCK ? moe::NORM_MX8 : moe::NORM_ROW8;

@@ -94,6 +94,7 @@ struct NormArgs {
     const void *weight;
     int w_bf16;
     float eps;
+    double inv_hidden;
     void *y;
     int y_kind;
     void *y_scale;                                 // MX8: [T][ceil(H/32)] e8m0 bytes; ROW8: [T] fp32

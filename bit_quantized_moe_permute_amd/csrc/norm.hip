@@ -28,6 +28,48 @@ __device__ __forceinline__ float wg_sum(float d, float *part, int nw) {
     return tot;
 }
 
+// v + its value in the lane that CTRL names
+template <int CTRL> __device__ __forceinline__ double add_dpp_f64(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)b, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(b >> 32), (int)(b >> 32), CTRL, 0xF, 0xF, false);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_f64(double v, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), l) << 32 |
+                                      (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, l));
+}
+
+// 1 / sqrt(sum / H + eps) in two fp32 parts, from the threads' fp32 sums of squares.  The row's one factor moves all of its
+// columns the same way, and where y is e4m3 an error in it decides blocks' scales and values that lie next to a rounding's
+// border: so the sums meet in binary64, and the square root is taken there (the instruction's estimate and one Newton step).
+// It costs no time: 11709 x 4096 61.2 us with and without, one row 6.3.
+struct Factor { float hi, lo; };
+__device__ __forceinline__ Factor row_factor(const NormArgs &a, float ss, double *part, int nw) {
+    double d = add_dpp_f64<0xB1>((double)ss);               // quad swaps, then mirrors of 8 and 16 lanes
+    d = add_dpp_f64<0x4E>(d);
+    d = add_dpp_f64<0x141>(d);
+    d = add_dpp_f64<0x140>(d);
+    d = (lane_f64(d, 0) + lane_f64(d, 16)) + (lane_f64(d, 32) + lane_f64(d, 48));
+    if (nw > 1) {
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = d;
+        __syncthreads();
+        d = 0.0;
+        for (int i = 0; i < nw; ++i) d += part[i];
+    }
+    const double m = fma(d, a.inv_hidden, (double)a.eps), r0 = __builtin_amdgcn_rsq(m);
+    const double r = m == HUGE_VAL ? 0.0 : fma(0.5 * r0, fma(-m * r0, r0, 1.0), r0);
+    const float hi = (float)r;
+    return {hi, (float)(r - (double)hi)};
+}
+// v * factor * w, off by little more than its one rounding
+__device__ __forceinline__ float normed(float v, const Factor &r, float w) {
+    const float hi = v * r.hi;
+    const float lo = __fmaf_rn(v, r.lo, __fmaf_rn(v, r.hi, -hi));
+    return __fmaf_rn(hi, w, lo * w);
+}
+
 __device__ __forceinline__ float wg_max(float d, float *part, int nw) {
     d = wave_max_f32(d);
     if (nw == 1) return d;
@@ -51,6 +93,12 @@ __device__ __forceinline__ float exp2_neg(int e) {
     return __uint_as_float(e < 127 ? (uint32_t)(127 - e) << 23 : 0x400000u);
 }
 __device__ __forceinline__ float row_scale(float amax) { return fmaxf(amax, E4M3_MAX * 0x1p-126f) / E4M3_MAX; }
+
+// v / s, s > 0: the product with 1 / s and the remainder's share (an infinite s, of a row that holds one: the product alone)
+__device__ __forceinline__ float quotient(float v, float s, float inv) {
+    const float q = v * inv;
+    return s < HUGE_VALF ? __fmaf_rn(__fmaf_rn(-q, s, v), inv, q) : q;
+}
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b});
@@ -104,7 +152,8 @@ enum { SRC_F32 = 0, SRC_BF16 = 1, SRC_COMBINE = 2 };     // what the row comes f
 // groups of a 32-column block lie in four adjacent lanes.  Needs H % 8 == 0 and 16-byte aligned rows.
 template <int SRC, int RES, int C, int KC>
 __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
-    __shared__ float part[3][16];
+    __shared__ float part[2][16];
+    __shared__ double part64[16];
     const int64_t t = blockIdx.x, row = t * a.H;
     const int nt = blockDim.x, nw = nt >> 6, ng = a.H >> 3;
     float v[C][8];
@@ -167,7 +216,7 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) d = __fmaf_rn(sv[r][i], v[r][i], d);
             }
-            const float sf = -a.steer_f * wg_sum(d, part[2], nw);
+            const float sf = -a.steer_f * wg_sum(d, part[0], nw);
 #pragma unroll
             for (int r = 0; r < C; ++r) {
                 if (!on[r]) continue;
@@ -220,7 +269,7 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __fmaf_rn(v[r][i], v[r][i], ss);
     }
-    const float rinv = 1.0f / __fsqrt_rn(wg_sum(ss, part[0], nw) / (float)a.H + a.eps);
+    const Factor rinv = row_factor(a, ss, part64, nw);
     float amax = 0.f;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
@@ -231,7 +280,7 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[r][i] = on[r] ? v[r][i] * rinv * f[i] : 0.f;
+            v[r][i] = on[r] ? normed(v[r][i], rinv, f[i]) : 0.f;
             amax = fmaxf(amax, fabsf(v[r][i]));
         }
     }
@@ -239,7 +288,11 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
     if (a.y_kind == NORM_ROW8) {
         const float s = row_scale(wg_max(amax, part[1], nw));
         if (threadIdx.x == 0) static_cast<float *>(a.y_scale)[t] = s;
-        inv = 1.0f / s;
+        const float rs = 1.0f / s;
+#pragma unroll
+        for (int r = 0; r < C; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[r][i] = quotient(v[r][i], s, rs);
     }
 #pragma unroll
     for (int r = 0; r < C; ++r) {
@@ -278,9 +331,10 @@ __device__ __forceinline__ float load1(const void *p, int64_t i, bool bf16) {
 // Any row length up to EL * blockDim.x and any alignment: column c = threadIdx.x + i * blockDim.x, one element per
 // load, so a 32-column block lies in one half of a wave.  Columns behind the row's end load its last one and count as
 // zero: without branches around them all of a row's loads are in flight at once (515 x 2055 bf16: 16.4 us with branches).
-template <int EL>
-__global__ __launch_bounds__(1024) void k_norm_any(NormArgs a, int src) {
-    __shared__ float part[3][16];
+template <int EL, int MAX_THREADS>
+__global__ __launch_bounds__(MAX_THREADS) void k_norm_any(NormArgs a, int src) {
+    __shared__ float part[2][16];
+    __shared__ double part64[16];
     const int64_t t = blockIdx.x, row = t * a.H;
     const int nt = blockDim.x, nw = nt >> 6;
     float v[EL], res[EL], wt[EL];
@@ -321,7 +375,7 @@ __global__ __launch_bounds__(1024) void k_norm_any(NormArgs a, int src) {
         for (int i = 0; i < EL; ++i) sv[i] = a.steer_v[at[i]];
 #pragma unroll
         for (int i = 0; i < EL; ++i) d = (int)threadIdx.x + i * nt < a.H ? __fmaf_rn(sv[i], v[i], d) : d;
-        const float sf = -a.steer_f * wg_sum(d, part[2], nw);
+        const float sf = -a.steer_f * wg_sum(d, part[0], nw);
 #pragma unroll
         for (int i = 0; i < EL; ++i) v[i] = __fmaf_rn(sf, sv[i], v[i]);
     }
@@ -336,18 +390,20 @@ __global__ __launch_bounds__(1024) void k_norm_any(NormArgs a, int src) {
         if (c < a.H && a.res_kind == RES_F32) static_cast<float *>(a.residual_out)[row + c] = v[i];
         if (c < a.H && a.res_kind == RES_BF16) static_cast<__bf16 *>(a.residual_out)[row + c] = (__bf16)v[i];
     }
-    const float rinv = 1.0f / __fsqrt_rn(wg_sum(ss, part[0], nw) / (float)a.H + a.eps);
+    const Factor rinv = row_factor(a, ss, part64, nw);
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < EL; ++i) {
-        v[i] *= rinv * wt[i];
+        v[i] = normed(v[i], rinv, wt[i]);
         amax = fmaxf(amax, fabsf(v[i]));
     }
     float inv = 1.f;
     if (a.y_kind == NORM_ROW8) {
         const float s = row_scale(wg_max(amax, part[1], nw));
         if (threadIdx.x == 0) static_cast<float *>(a.y_scale)[t] = s;
-        inv = 1.0f / s;
+        const float rs = 1.0f / s;
+#pragma unroll
+        for (int i = 0; i < EL; ++i) v[i] = quotient(v[i], s, rs);
     }
 #pragma unroll
     for (int i = 0; i < EL; ++i) {
@@ -398,9 +454,11 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t st) {
     if (!vec) {
         const int nt = a.H <= 256 ? 64 : a.H <= 8192 ? 256 : 1024;
         const dim3 grd((unsigned)a.T), blk((unsigned)nt);
-        if (a.H <= 4 * nt) hipLaunchKernelGGL((k_norm_any<4>), grd, blk, 0, st, a, src);
-        else if (a.H <= 16 * nt) hipLaunchKernelGGL((k_norm_any<16>), grd, blk, 0, st, a, src);
-        else hipLaunchKernelGGL((k_norm_any<32>), grd, blk, 0, st, a, src);
+        if (a.H <= 4 * nt) hipLaunchKernelGGL((k_norm_any<4, 256>), grd, blk, 0, st, a, src);
+        else if (a.H <= 4096) hipLaunchKernelGGL((k_norm_any<16, 256>), grd, blk, 0, st, a, src);
+        else if (a.H <= 8192) hipLaunchKernelGGL((k_norm_any<32, 256>), grd, blk, 0, st, a, src);
+        else if (a.H <= 16384) hipLaunchKernelGGL((k_norm_any<16, 1024>), grd, blk, 0, st, a, src);
+        else hipLaunchKernelGGL((k_norm_any<32, 1024>), grd, blk, 0, st, a, src);
         return hipGetLastError();
     }
     const int ng = a.H / 8;

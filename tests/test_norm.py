@@ -143,6 +143,34 @@ def test_add_rms_norm(m, T, H, x_t, res_t, w_t, y_t):
 @pytest.mark.gpu
 @pytest.mark.parametrize("H", [512, 515])
 @pytest.mark.parametrize("y_t", ["f32", "bf16", "block", "row"])
+def test_rows_that_are_not_finite(m, H, y_t):
+    """A NaN makes its row NaN, an infinity (whose row's factor is 0) itself alone; the other rows keep their bits, and rows
+    behind the last one are not written."""
+    note(f"not finite H={H} y={y_t}")
+    x, w = draw(8, 5, H).cuda(), draw(9, H, std=0.1, mean=1.0).cuda()
+
+    def run():
+        y, ys = outputs(7, H, y_t)
+        before = y.clone()
+        m.moe_add_rms_norm(x, None, None, w, EPS, y[:5], None if ys is None else ys[:5])
+        torch.cuda.synchronize()
+        assert torch.equal(y[5:].view(torch.uint8), before[5:].view(torch.uint8))
+        assert ys is None or (ys[5:] == 255).all() or torch.isnan(ys[5:]).all()
+        return y[:5].cpu(), None if ys is None else ys[:5].cpu()
+
+    clean, clean_s = run()
+    x[1, 3], x[2, 7] = float("nan"), float("inf")
+    y, ys = run()
+    keep = [0, 3, 4]
+    assert torch.equal(y[keep].view(torch.uint8), clean[keep].view(torch.uint8))
+    assert ys is None or torch.equal(ys[keep], clean_s[keep])
+    assert torch.isnan(y[1].float()).all()
+    assert torch.isnan(y[2, 7].float()) and int((y[2].float() != 0).sum()) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [512, 515])
+@pytest.mark.parametrize("y_t", ["f32", "bf16", "block", "row"])
 def test_rows_of_unusual_values(m, H, y_t):
     """Zero rows, tiny rows (eps decides), large rows, one spike, blocks of zeros, negative weights."""
     note(f"unusual rows H={H} y={y_t}")
