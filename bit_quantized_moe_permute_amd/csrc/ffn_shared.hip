@@ -15,6 +15,14 @@
 //
 // An adapter's term is formed in accumulators of its own and added to the rows of its own tokens only, so nothing of
 // one request's adapter (not even a NaN) reaches another request.
+//
+// Bound: the weights' bytes for few tokens, the matrix cores and the tiles' way into LDS for many.  hidden 4096, inter 2048,
+// kernels alone, fp32 out below 2048 tokens (a copy reaches 4.97 TB/s on this chip, a 2048 x 4096 x 4096 library product 62 us):
+//   1 token, rank 16:     inputs 3.8 us, gate/up 11.1 (33.6 MB, 3.0 TB/s), down 10.8 (16.9 MB, 1.6 TB/s)
+//   24 requests, rank 64: inputs 6.7, gate/up 15.9, inputs 4.3, down 12.6 (together 96 MB in 39.4 us, 2.4 TB/s)
+//   512 tokens, rank 16:  plan 4.8, down-rank 6.3 + 6.0, gate/up 29 (0.6 PFLOP/s), down-rank 6.7 + 6.2, down 29 (three planes:
+//                         0.9 PFLOP/s)
+//   2048 tokens, rank 16, bf16 out: plan 5.8, down-rank 9.1 + 6.0, gate/up 70 (1.0 PFLOP/s), down-rank 6.6 + 6.0, down 45 (0.8)
 #include "common.h"
 #include "internal.h"
 
@@ -106,8 +114,9 @@ __device__ __forceinline__ const uint16_t *low_rank_row(const SharedArgs &a, con
 
 // ---------------------------------------------------------------------------
 // plan (many tokens): tokens ordered by adapter (those without one last), and items of up to ITEM_TOKENS tokens of one adapter.
-// One workgroup; the launch's others bring fp32 activations into three bf16 planes [3][T][H].  Within an adapter the order is that of LDS atomics and may differ between calls: a row's place in
-// a tile changes no bit of its result.
+// One workgroup; the launch's others bring fp32 activations into three bf16 planes [3][T][H].  Within an adapter the order is that
+// of LDS atomics and may differ between calls: a row's place in a tile changes no bit of its result.  Bound by its chain of
+// loads, LDS atomics and barriers: 4.8 us for 512 tokens, 5.8 for 2048, of which a launch alone is about 3.
 // ---------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024;
 
@@ -196,11 +205,11 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a, uint16_t *p
 // ---------------------------------------------------------------------------
 // Few tokens: what a product reads of its activations.
 //
-// Tokens go in groups of up to 64.  Packed activations [group][P][TF][steps][64 lanes][8]: the matrix instruction's operand of 16 tokens and 32 of K in lane order, so
-// that a wave reads 1 KiB in a row.  Lane l holds token l % 16 and k = 8 (l / 16) .. + 7; steps of 32 up to a multiple of 2048,
-// zeros behind the end of K.
+// Tokens go in groups of up to 64.  Packed activations [group][P][TF][steps][64 lanes][8]: the matrix instruction's operand of
+// 16 tokens and 32 of K in lane order, so that a wave reads 1 KiB in a row.  Lane l holds token l % 16 and k = 8 (l / 16) .. + 7;
+// steps of 32 up to a multiple of 2048, zeros behind the end of K.
 // Read from rows instead, the 64 lanes' 16-byte pieces would lie in 64 places, and a wave's load would take four times as
-// long (measured as the bound of the row-reading kernel at 24 tokens: 18.5 us against 10.6 for the gate/up product).
+// long (64 requests, 4096 x 2048: gate/up 43 us reading rows, 22 with packed operands; down 33 and 17).
 //
 // Low-rank results s[t][proj][3 parts][r] = scale_a (A_a[r] . x[t]), one wave per (token, row): no wait but that for the token's
 // adapter index and that for the row, and no exchange but the wave's own sum.
@@ -293,7 +302,8 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
 // ---------------------------------------------------------------------------
 // Few tokens, a product: one workgroup streams 16 weight rows (gate/up: 8 gate rows and the same 8 of up) once.  Its waves
 // split K: in each round of 2048 a wave takes 256 of every row, through LDS of its own that direct-to-LDS loads fill with
-// 512-byte pieces of rows (two rounds in flight: 128 KiB per workgroup).  Chunk c of row r lies at position
+// 512-byte pieces of rows (two rounds in flight: 128 KiB per workgroup, what a copy's rate times the memory's latency asks of
+// a compute unit; 16 rows, so that 4096 x 2048 makes 256 workgroups).  Chunk c of row r lies at position
 // c ^ r, so that sixteen rows' reads of one chunk column touch every bank once.  The waves' sums meet in LDS.
 // An adapter's term is formed per token in fp32, wave w taking tokens w, w + NW, ...; its loads go out with the weights'.
 // ---------------------------------------------------------------------------
@@ -304,11 +314,10 @@ __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0
 
 // AD: the adapters' low-rank results are read (AD_READ), or (AD_HERE, down, few values) formed by every workgroup from the rows of
 // h while its weights are on their way: that reads A out of the caches in every workgroup, where a launch between the two products
-// costs 4 us. fp32 result, launch against here: 16 values of 2048 (1 token, rank 16) 25.6 -> 24.0 us the whole call, of 4096
-// 40.2 -> 38.2, of 512 14.8 -> 13.6;
-// 32 values of 2048 24.9 -> 25.9, 8 of 8192 111.7 -> 112.8.
+// costs 4 us.  fp32 result, a launch against here, whole calls: 16 values of 2048 (1 token, rank 16) 25.6 and 24.0 us, of 4096
+// 40.2 and 38.2, of 512 14.8 and 13.6; 32 values of 2048 24.9 and 25.9, 8 of 8192 111.7 and 112.8.
 enum { AD_NONE = 0, AD_READ = 1, AD_HERE = 2 };
-constexpr int HERE_VALUES = 16, HERE_TERMS = 1 << 16;        // tokens * max_rank, and times shared_inter, up to which AD_HERE is taken
+constexpr int HERE_VALUES = 16, HERE_TERMS = 1 << 16;        // tokens * max_rank, and times shared_inter, at most for AD_HERE
 
 template <bool GU, int P, int TF, int AD>
 __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g) {
@@ -523,8 +532,10 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: a workgroup of four waves computes 128 weight rows (gate/up: 64 of each) x BT tokens (P planes of them, which meet
-// the same weights), each wave 64 x BT/2 of them; both operands pass through LDS in 64-wide K stages, three of them, filled by direct-to-LDS loads.
+// Many tokens: a workgroup computes BW weight rows (gate/up: half of each) x BT tokens (P planes of them, which meet the same
+// weights), each wave 64 x BT/2 of them; both operands pass through LDS in 64-wide K stages, three of them (more gave nothing:
+// 512 tokens the same with four or six), filled by direct-to-LDS loads.  The matrix cores are busy half of the time at 2048
+// tokens, with no LDS bank conflict; twice the waves with half the tokens each ran the same (161 and 162 us the whole call).
 // LDS rows are 128 bytes, half of the 64 banks; 16-byte chunk c of row r lies at position c ^ (r / 2 % 8), so sixteen rows'
 // reads of one chunk column touch every bank once.
 //
@@ -539,8 +550,8 @@ enum { MODE_GATE_UP = 0, MODE_DOWN = 1, MODE_LOW_RANK = 2 };
 
 // Down-rank (MODE_LOW_RANK): a tile's tokens are an item of the plan, its weight rows those of that adapter's A matrices, and
 // blockIdx.y is a part of K; the sums of the parts are added by k_low_rank_sum.
-// The small tiles have two groups of four waves, each working two of a stage's four 16-wide slices: with one wave per SIMD and
-// a few products per slice, the waits for LDS would stand open.
+// The tiles of 64 tokens have two groups of waves, each working two of a stage's four 16-wide slices: with one wave per SIMD
+// and a few products per slice, the waits for LDS would stand open.
 // TAIL: K is no multiple of 64, so a row's last step is not a whole one.
 template <int MODE, int P, int BW, int BT, bool TAIL>
 __global__ __launch_bounds__(many_threads(BW, BT)) void k_many(SharedArgs a, Product g, int tiles_w, int tiles_t) {
@@ -571,8 +582,8 @@ __global__ __launch_bounds__(many_threads(BW, BT)) void k_many(SharedArgs a, Pro
     }
 
     // Load i of this wave fills rows 8 * (wave * LOADS + i) .. + 7 of the tile from one operand (`base`); `off`: byte offset of
-    // this lane's row and chunk from there (launch_shared() keeps them below 2^32).  Rows behind the last repeat it; their
-    // results are not stored.
+    // this lane's row and chunk from there (n_tokens * K < 2^30 and the limits of K keep them below 2^32).
+    // Rows behind the last repeat it; their results are not stored.
     const int tail = K % BK / 8;                             // chunks in a row's last step (TAIL)
     uint64_t base[LOADS];
     uint32_t off[LOADS], back[LOADS];
@@ -606,8 +617,9 @@ __global__ __launch_bounds__(many_threads(BW, BT)) void k_many(SharedArgs a, Pro
     const int se = LOW ? ksteps * ((int)blockIdx.y + 1) / (int)gridDim.y : ksteps;
     const int nsteps = se - sb;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(las_ptr)tile + wave * LOADS * 1024u;
-    // Loads of the next stage to issue: its step, and its byte offset in a row.  A chunk behind the row's end repeats the step's first one (its products are masked), and stages behind the last repeat that: every stage has the same
-    // number of loads in flight.
+    // Loads of the next stage to issue: its step, and its byte offset in a row.  A chunk behind the row's end repeats the step's
+    // first one (its products meet zero weights), and stages behind the last repeat that: every stage has the same number of
+    // loads in flight.
     int istep = sb;
     uint32_t ioff = 2 * BK * sb, idst = lds0;
     auto issue = [&](int i) {                                // i: load of this wave (compile-time)
@@ -727,9 +739,10 @@ __global__ __launch_bounds__(many_threads(BW, BT)) void k_many(SharedArgs a, Pro
         }
         return;
     } else if (a.n) {
-        // Up to NA adapters of 64 of this wave's tokens at a time, whose loads go out together; rank values go 16 at a time, each
-        // once with each part of the tokens' low-rank results.  An adapter's products are formed for all of the tokens, in
-        // sums of their own, and added to those of its own tokens.
+        // Up to NA adapters of 64 of this wave's tokens at a time, whose loads go out together (gate/up of 2048 tokens
+        // 70 us; 77 with one adapter after the other and its rank before its loads; 68 without adapters); rank values go 16 at a time,
+        // each once with each part of the tokens' low-rank results (of which a bf16 out takes two: 16 bits).  An adapter's
+        // products are formed for all of the tokens, in sums of their own, and added to those of its own tokens.
         constexpr int NP = GU ? 2 : 1, JG = FT < 2 ? FT : 2, SP = !GU && P == 1 ? 2 : 3, NA = 4;
 #pragma unroll
         for (int jg = 0; jg < FT; jg += JG) {

@@ -8,7 +8,9 @@
 //
 // Bound: HBM traffic for many rows, one memory round trip and two barriers for few.  One workgroup holds one row in
 // registers, so every input is read once: all loads of a row (source, residual, weight) are issued before the first
-// reduction.
+// reduction.  A copy of 2 GiB moves 4.97 TB/s on this chip; 11709 x 4096 with block scales takes 61.0 us (337 MB, 5.5 TB/s),
+// 1469 x 4096 with row scales 14.8 (78 MB, 5.3 TB/s), 2048 combined rows of 8 x 4096 66.4 (344 MB, 5.2 TB/s); one row of 4096
+// takes 2.4 us, one combined row 3.2, which is what a launch with one round trip to memory takes.
 #include "common.h"
 #include "internal.h"
 
@@ -330,7 +332,8 @@ __device__ __forceinline__ float load1(const void *p, int64_t i, bool bf16) {
 
 // Any row length up to EL * blockDim.x and any alignment: column c = threadIdx.x + i * blockDim.x, one element per
 // load, so a 32-column block lies in one half of a wave.  Columns behind the row's end load its last one and count as
-// zero: without branches around them all of a row's loads are in flight at once (515 x 2055 bf16: 16.4 us with branches).
+// zero: without branches around them all of a row's loads are in flight at once (515 x 2055 bf16: 9.8 us, 16.4 with branches;
+// 8.5 MB in elements of 2 bytes per lane, bound by their number and two barriers).
 template <int EL, int MAX_THREADS>
 __global__ __launch_bounds__(MAX_THREADS) void k_norm_any(NormArgs a, int src) {
     __shared__ float part[2][16];
