@@ -3,9 +3,9 @@
 //   g = Wg x + c_a Bg_a (Ag_a x),  u likewise,  h = silu(g) * u,  out = Wd h + c_a Bd_a (Ad_a h)
 //
 // with a = token_adapter[t] (no adapter terms where it is outside 0 .. n_adapters - 1).  All products run on the bf16
-// matrix cores with fp32 sums.  What is not bf16 by itself -- fp32 activations, the low-rank results, and h where the result is
-// fp32 -- is carried as three bf16 parts (24 bits) and multiplied part by part; h for a bf16 result as one bf16 value, whose
-// rounding (2^-9 on average) is of the size of the result's own.
+// matrix cores with fp32 sums.  What is not bf16 by itself -- fp32 activations, the low-rank results, and h -- is carried as bf16
+// parts and multiplied part by part: three (24 bits) where the result is fp32, two (16 bits) where it is bf16, and then one of h
+// for many tokens.
 // Launches: [plan] [down-rank] gate/up [down-rank] down --
 //
 //   plan       (many tokens) the tokens ordered by adapter, and work items of up to 64 tokens of one adapter
@@ -114,20 +114,21 @@ __device__ __forceinline__ const uint16_t *low_rank_row(const SharedArgs &a, con
 
 // ---------------------------------------------------------------------------
 // plan (many tokens): tokens ordered by adapter (those without one last), and items of up to ITEM_TOKENS tokens of one adapter.
-// One workgroup; the launch's others bring fp32 activations into three bf16 planes [3][T][H].  Within an adapter the order is that
+// One workgroup; the launch's others bring fp32 activations into xp bf16 planes [xp][T][H].  Within an adapter the order is that
 // of LDS atomics and may differ between calls: a row's place in a tile changes no bit of its result.  Bound by its chain of
 // loads, LDS atomics and barriers: 4.8 us for 512 tokens, 5.8 for 2048, of which a launch alone is about 3.
 // ---------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024;
 
-__global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a, uint16_t *planes, int plans) {
+__global__ __launch_bounds__(PLAN_THREADS) void k_plan(SharedArgs a, uint16_t *planes, int xp, int plans) {
     if ((int)blockIdx.x >= plans) {
         const int64_t i = 4 * ((int64_t)(blockIdx.x - plans) * PLAN_THREADS + threadIdx.x), m = (int64_t)a.T * a.H;
         if (i >= m) return;
         const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.x) + i);
         const float v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2 *>(planes + p * m + i) = pack_part(v, p);
+        for (int p = 0; p < 3; ++p)
+            if (p < xp) *reinterpret_cast<uint2 *>(planes + p * m + i) = pack_part(v, p);
         return;
     }
     __shared__ int count[MAX_ADAPTERS + 1], begin[MAX_ADAPTERS + 2], item0[MAX_ADAPTERS + 1], wsum[2][PLAN_THREADS / 64];
@@ -221,14 +222,14 @@ __host__ __device__ __forceinline__ int few_groups(int T) { return (T + FEW_TOKE
 constexpr int FEW_ROUND = 2048;
 __host__ __device__ __forceinline__ int few_steps(int K) { return (K + FEW_ROUND - 1) / FEW_ROUND * (FEW_ROUND / 32); }
 
-enum { ACT_BF16 = 0, ACT_PLANES = 1, ACT_F32 = 2 };          // x: one bf16 plane, three of them, fp32
+enum { ACT_BF16 = 0, ACT_PLANES = 1, ACT_F32 = 2 };          // x: one bf16 plane, PL of them, fp32 (packed as PL)
 
-template <int SRC>
+template <int SRC, int PL>
 __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uint16_t *packed, int pack_blocks) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int K = L.K, steps = few_steps(K);
     if ((int)blockIdx.x < pack_blocks) {
-        constexpr int P = SRC == ACT_F32 ? 3 : 1;
+        constexpr int P = SRC == ACT_F32 ? PL : 1;
         const int i = blockIdx.x * 4 + wave, tf = few_frags(a.T), frag = i / steps, step = i - frag * steps;
         const int grp = frag / tf, f = frag - grp * tf;
         if (frag * 16 >= a.T) return;
@@ -258,7 +259,7 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
     if (ad < 0 || !A) return;                                // not read either
     A += ((int64_t)ad * a.R + r) * K;
     const int64_t row = (int64_t)t * K, plane = (int64_t)a.T * K;
-    constexpr int U = SRC == ACT_BF16 ? 8 : 4, P = SRC == ACT_PLANES ? 3 : 1, V = SRC == ACT_F32 ? 2 : P;
+    constexpr int U = SRC == ACT_BF16 ? 8 : 4, P = SRC == ACT_PLANES ? PL : 1, V = SRC == ACT_F32 ? 2 : P;
     float acc[3] = {0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < K; k0 += U * 512) {
         uint4 w[U], v[V][U];
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
 #pragma unroll
     for (int f = 0; f < TF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     constexpr int SPW = SLICE / 32;                                      // steps of a wave per round
-    constexpr int XB = TF * P <= 2 ? SPW : TF * P <= 4 ? SPW / 2 : TF * P == 6 ? SPW / 4 : SPW / 8;   // steps whose activations are
+    constexpr int XB = TF * P <= 2 ? SPW : TF * P <= 4 ? SPW / 2 : TF * P <= 8 ? SPW / 4 : SPW / 8;   // steps whose activations are
                                                                          // loaded together
     const int rounds = (K + FEW_ROUND - 1) / FEW_ROUND, steps = few_steps(K);
     const uint4 *xw = reinterpret_cast<const uint4 *>(g.x) + (int64_t)blockIdx.y * P * TF * steps * 64 + wave * (SPW * 64) + lane;
@@ -517,7 +518,9 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
             const int i = r0 + r;
             const float hv = silu_mul(y, up);
             const int64_t o = (((int64_t)f * hsteps + i / 32) * 64 + (i % 32 / 8) * 16 + c) * 8 + i % 8;
-            for (int p = 0; p < g.hp; ++p) {
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                if (p >= g.hp) break;
                 const uint16_t part = bf16_bits(bf16_part(hv, p));
                 h[p * ((int64_t)TF * hsteps * 512) + o] = part;
                 if (g.hrow) g.hrow[((int64_t)p * a.T + t) * g.N + i] = part;     // for the down-rank products
@@ -915,18 +918,23 @@ hipError_t few_planes(const SharedArgs &a, const Product &g, hipStream_t st) {
 
 template <bool GU>
 hipError_t few(const SharedArgs &a, const Product &g, int planes, hipStream_t st) {
-    return planes == 1 ? few_planes<GU, 1>(a, g, st) : few_planes<GU, 3>(a, g, st);
+    if constexpr (GU) {
+        if (planes == 1) return few_planes<GU, 1>(a, g, st);
+    }
+    return planes == 2 ? few_planes<GU, 2>(a, g, st) : few_planes<GU, 3>(a, g, st);
 }
 
 // Packs the activations (packed) and forms the low-rank results (a.n), one launch for both.
-hipError_t few_inputs(const SharedArgs &a, const LowRank &L, int src, uint16_t *packed, hipStream_t st) {
+hipError_t few_inputs(const SharedArgs &a, const LowRank &L, int src, int planes, uint16_t *packed, hipStream_t st) {
     const int pack = packed ? ((a.T + 15) / 16 * few_steps(L.K) + 3) / 4 : 0;
     const int low = a.n ? (a.T * L.np * a.R + 3) / 4 : 0;
     if (!pack && !low) return hipSuccess;
     const dim3 grd((unsigned)(pack + low)), blk(256);
-    if (src == ACT_BF16) hipLaunchKernelGGL((k_few_inputs<ACT_BF16>), grd, blk, 0, st, a, L, packed, pack);
-    else if (src == ACT_PLANES) hipLaunchKernelGGL((k_few_inputs<ACT_PLANES>), grd, blk, 0, st, a, L, packed, pack);
-    else hipLaunchKernelGGL((k_few_inputs<ACT_F32>), grd, blk, 0, st, a, L, packed, pack);
+    if (src == ACT_BF16) hipLaunchKernelGGL((k_few_inputs<ACT_BF16, 1>), grd, blk, 0, st, a, L, packed, pack);
+    else if (src == ACT_PLANES && planes == 2) hipLaunchKernelGGL((k_few_inputs<ACT_PLANES, 2>), grd, blk, 0, st, a, L, packed, pack);
+    else if (src == ACT_PLANES) hipLaunchKernelGGL((k_few_inputs<ACT_PLANES, 3>), grd, blk, 0, st, a, L, packed, pack);
+    else if (planes == 2) hipLaunchKernelGGL((k_few_inputs<ACT_F32, 2>), grd, blk, 0, st, a, L, packed, pack);
+    else hipLaunchKernelGGL((k_few_inputs<ACT_F32, 3>), grd, blk, 0, st, a, L, packed, pack);
     return hipGetLastError();
 }
 
@@ -935,7 +943,9 @@ hipError_t launch_many(const SharedArgs &a, const Product &g, int bw, int bt, in
     const dim3 grd((unsigned)((tw * tt + 7) / 8 * 8), (unsigned)parts), blk((unsigned)many_threads(bw, bt));
     if constexpr (MODE != MODE_LOW_RANK && P == 1) {
         if (bt == 256) hipLaunchKernelGGL((k_many<MODE, P, 128, 256, TAIL>), grd, blk, 0, st, a, g, tw, tt);
-        else if (bt == 128) hipLaunchKernelGGL((k_many<MODE, P, 128, 128, TAIL>), grd, blk, 0, st, a, g, tw, tt);
+    }
+    if constexpr (MODE != MODE_LOW_RANK && P < 3) {
+        if (bt == 128) hipLaunchKernelGGL((k_many<MODE, P, 128, 128, TAIL>), grd, blk, 0, st, a, g, tw, tt);
     }
     if (bt == 64 && bw == 128) hipLaunchKernelGGL((k_many<MODE, P, 128, 64, TAIL>), grd, blk, 0, st, a, g, tw, tt);
     else if (bt == 64) hipLaunchKernelGGL((k_many<MODE, P, 64, 64, TAIL>), grd, blk, 0, st, a, g, tw, tt);
@@ -948,6 +958,11 @@ hipError_t many_tiles(const SharedArgs &a, const Product &g, int planes, int bw,
     if (planes == 1)
         return g.K % BK ? launch_many<MODE, 1, true>(a, g, bw, bt, tw, tt, parts, st)
                         : launch_many<MODE, 1, false>(a, g, bw, bt, tw, tt, parts, st);
+    if constexpr (MODE != MODE_DOWN) {
+        if (planes == 2)
+            return g.K % BK ? launch_many<MODE, 2, true>(a, g, bw, bt, tw, tt, parts, st)
+                            : launch_many<MODE, 2, false>(a, g, bw, bt, tw, tt, parts, st);
+    }
     return g.K % BK ? launch_many<MODE, 3, true>(a, g, bw, bt, tw, tt, parts, st)
                     : launch_many<MODE, 3, false>(a, g, bw, bt, tw, tt, parts, st);
 }
@@ -956,8 +971,8 @@ template <int MODE>
 hipError_t many(const SharedArgs &a, const Product &g, int planes, hipStream_t st) {
     const int rows = MODE == MODE_GATE_UP ? 64 : 128, tw = (g.N + rows - 1) / rows;
     auto tiles = [&](int bt) { return tw * ((a.T + bt - 1) / bt); };
-    // three planes of 128 tokens would not fit three times into LDS
-    const int bt = planes > 1 ? 64 : tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
+    // two planes of 256 tokens or three of 128 would not fit three times into LDS
+    const int bt = planes < 2 && tiles(256) >= 256 ? 256 : planes < 3 && tiles(128) >= 256 ? 128 : 64;
     // half tiles where whole ones are for half of the compute units at most (whole call, whole tiles against half ones: 333
     // tokens 1000 x 520 61.2 and 58.0 us, 300 tokens 2048 x 512 51.4 and 48.5, 400 tokens 1024 x 1024 49.4 and 46.7)
     const int bw = bt == 64 && tiles(64) <= 128 ? 64 : 128;
@@ -1006,7 +1021,7 @@ bool few_path(int T, int H, int Is) {
 struct Layout {
     size_t x, perm, ad, items, n_items, s, part, h, hrow, total;
 };
-Layout layout(int T, int H, int Is, int n, int R, bool x_f32, int hp) {
+Layout layout(int T, int H, int Is, int n, int R, int xp, int hp) {
     Layout l = {};
     size_t o = 0;
     auto take = [&](size_t b) { const size_t at = o; o += (b + 255) / 256 * 256; return at; };
@@ -1015,11 +1030,11 @@ Layout layout(int T, int H, int Is, int n, int R, bool x_f32, int hp) {
     auto packed = [&](int K, int p) { return (size_t)p * tf * few_steps(K) * 1024; };
     l.s = take(n > 0 ? (size_t)T * 2 * 3 * R * 2 : 0);       // gate/up's, then down's
     if (small) {
-        l.x = take(packed(H, x_f32 ? 3 : 1));
+        l.x = take(packed(H, xp));
         l.h = take(packed(Is, hp));
         l.hrow = take(n > 0 ? (size_t)T * Is * 2 * hp : 0);
     } else {
-        l.x = take(x_f32 ? (size_t)T * H * 3 * 2 : 0);
+        l.x = take(xp > 1 ? (size_t)T * H * xp * 2 : 0);
         l.h = take((size_t)T * Is * 2 * hp);
         if (n > 0) {
             l.perm = take((size_t)T * 4);
@@ -1040,17 +1055,20 @@ namespace moe {
 
 size_t shared_workspace(int T, int H, int Is, int n, int R) {
     // the largest over the activation and result types, so that one buffer serves every call of these sizes
-    return layout(T, H, Is, n, R, true, 3).total;
+    return layout(T, H, Is, n, R, 3, 3).total;
 }
 
 hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     char *base = static_cast<char *>(ws);
-    const int hp = a.out_bf16 ? 1 : 3, xp = a.x_bf16 ? 1 : 3;
-    const Layout l = layout(a.T, a.H, a.Is, a.n, a.R, !a.x_bf16, hp);
+    // bf16 parts of x and h.  Beside a bf16 result 16 bits are enough; for many tokens h then has one part, whose rounding is as
+    // large as the result's own (together 1.4 times that), because a second one would double the down product: 45 us of 2048
+    // tokens' 143 at 4096 x 2048.  For few tokens it hides behind the weights.
+    const bool small = few_path(a.T, a.H, a.Is);
+    const int xp = a.x_bf16 ? 1 : a.out_bf16 ? 2 : 3, hp = !a.out_bf16 ? 3 : small ? 2 : 1;
+    const Layout l = layout(a.T, a.H, a.Is, a.n, a.R, xp, hp);
     auto u16 = [&](size_t at) { return reinterpret_cast<uint16_t *>(base + at); };
     uint16_t *s = u16(l.s), *h = u16(l.h);
     float *part = reinterpret_cast<float *>(base + l.part);
-    const bool small = few_path(a.T, a.H, a.Is);
     a.sorted = a.n > 0 && !small;
     SharedArgs ag = a, ad = a;                              // a half without adapters runs as if there were none
     if (!a.gate_a && !a.up_a) ag.n = 0;
@@ -1065,12 +1083,12 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     if (small) {
         gu.x = u16(l.x);
         if (ad.n) { gu.hrow = u16(l.hrow); lh.xv = gu.hrow; }
-        if ((e = few_inputs(ag, lx, a.x_bf16 ? ACT_BF16 : ACT_F32, u16(l.x), st)) != hipSuccess) return e;
+        if ((e = few_inputs(ag, lx, a.x_bf16 ? ACT_BF16 : ACT_F32, xp, u16(l.x), st)) != hipSuccess) return e;
         if ((e = few<true>(ag, gu, xp, st)) != hipSuccess) return e;
         if (ad.n && low_rank_here(ad)) {
             dn.a = a.down_a;
             dn.hrow = gu.hrow;
-        } else if ((e = few_inputs(ad, lh, hp == 1 ? ACT_BF16 : ACT_PLANES, nullptr, st)) != hipSuccess) {
+        } else if ((e = few_inputs(ad, lh, ACT_PLANES, hp, nullptr, st)) != hipSuccess) {
             return e;
         }
         return few<false>(ad, dn, hp, st);
@@ -1085,7 +1103,7 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     if (a.sorted || !a.x_bf16) {
         const int64_t quads = a.x_bf16 ? 0 : (int64_t)a.T * a.H / 4;
         hipLaunchKernelGGL(k_plan, dim3((unsigned)(a.sorted + (quads + PLAN_THREADS - 1) / PLAN_THREADS)), dim3(PLAN_THREADS),
-                           0, st, a, u16(l.x), a.sorted);
+                           0, st, a, u16(l.x), xp, a.sorted);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.sorted) {

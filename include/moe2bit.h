@@ -464,10 +464,10 @@ size_t moe_shared_ffn_workspace(const moe_layer_desc *L, const moe_adapter_desc 
  *   out [n_tokens][H], fp32 or bf16.
  *   ws: 256-byte aligned, at least moe_shared_ffn_workspace(L, A, n_tokens)
  *     bytes; calls that may overlap in time need one each.
- * Sums are fp32 in an order fixed by the shapes; fp32 activations, the low-rank
- * products A[a] x and, with an fp32 out, the SwiGLU result h are carried with
- * all 24 bits (three bf16 parts; with a bf16 out the products of many tokens
- * read two parts of the low-rank ones), h with a bf16 out as one bf16 value.
+ * Sums are fp32 in an order fixed by the shapes.  With an fp32 out, fp32
+ * activations, the low-rank products A[a] x and the SwiGLU result h are carried
+ * with all 24 bits (three bf16 parts); with a bf16 out, with 16 bits (two
+ * parts), and h of large calls (never of 64 tokens or fewer) as one bf16 value.
  * Values that round to infinity in bf16 (3.396e38 and above) give NaN.
  * A token's result has the same bits whatever other tokens and adapters the
  * call holds (at the same n_tokens and n_adapters), and non-finite values in

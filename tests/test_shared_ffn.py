@@ -134,7 +134,7 @@ class Case:
 @pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 33, 64, 65, 100, 130, 257])
 @pytest.mark.parametrize("H,I", [(8, 8), (40, 24), (64, 128), (136, 72), (520, 264)])
-@pytest.mark.parametrize("x_t,out_t", [(BF16, F32), (F32, F32), (BF16, BF16)])
+@pytest.mark.parametrize("x_t,out_t", [(BF16, F32), (F32, F32), (BF16, BF16), (F32, BF16)])
 def test_without_adapters(m, T, H, I, x_t, out_t):
     note(f"T={T} H={H} I={I} x={x_t} out={out_t}")
     c = Case(T, H, I, x_t=x_t, seed=T)
@@ -145,7 +145,7 @@ def test_without_adapters(m, T, H, I, x_t, out_t):
 @pytest.mark.parametrize("T", [1, 3, 16, 29, 64, 65, 131, 300])
 @pytest.mark.parametrize("H,I,n,R", [(8, 8, 1, 8), (72, 40, 3, 8), (264, 136, 7, 24), (512, 256, 40, 16), (128, 64, 2, 256),
                                      (64, 192, 300, 40)])
-@pytest.mark.parametrize("x_t,out_t", [(BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("x_t,out_t", [(BF16, F32), (F32, BF16), (F32, F32), (BF16, BF16)])
 def test_with_adapters(m, T, H, I, n, R, x_t, out_t):
     """Mixed ranks (none, one, odd, full, above the pool's), tokens without an adapter and with indices outside the pool,
     NaN in what no token uses."""
@@ -178,11 +178,11 @@ def test_larger_layers(m, T, H, I, n, R, out_t):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,H,I", [(2100, 264, 2056), (2100, 4104, 72), (1100, 264, 2056), (1100, 4104, 72), (2112, 320, 2048)])
-@pytest.mark.parametrize("n", [0, 3])
-def test_wide_tiles(m, T, H, I, n):
-    """Tiles of 128 and 256 tokens (bf16 activations; enough tiles for every compute unit), whole and with odd ends."""
-    note(f"wide tiles T={T} H={H} I={I} n={n}")
-    c = Case(T, H, I, n, 24, seed=T, ranks=[24, 5, 17])
+@pytest.mark.parametrize("n,x_t", [(0, BF16), (3, BF16), (3, F32)])
+def test_wide_tiles(m, T, H, I, n, x_t):
+    """Tiles of 128 and 256 tokens (where they are enough for every compute unit), whole and with odd ends."""
+    note(f"wide tiles T={T} H={H} I={I} n={n} x={x_t}")
+    c = Case(T, H, I, n, 24, x_t, seed=T, ranks=[24, 5, 17])
     c.check(c.run(m, BF16))
 
 
