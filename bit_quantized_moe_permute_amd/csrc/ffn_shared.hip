@@ -724,11 +724,29 @@ __global__ __launch_bounds__(many_threads(BW, BT)) void k_many(SharedArgs a, Pro
     }
     // D: lane holds token i32 of a fragment, weight rows 8 * (v / 4) + 4 * hh + v % 4
     if constexpr (LOW) {
-        // fp32 sums of this part of K: [part][pos][projection][R]
+        // the whole K: s, scaled and split; else fp32 sums of this part of K: [part][pos][projection][R]
+        const float scale = !g.part && a.scale ? uniform_at(a.scale, ad0) : 1.f;
+        const int rank = g.part ? 0 : rank_of(a, ad0);
 #pragma unroll
         for (int j = 0; j < FT; ++j) {
             const int pos = t0 + (rt - BW) + j * 32 + i32;
             if (pos > last) continue;
+            if (!g.part) {
+#pragma unroll
+                for (int i = 0; i < FW; ++i)
+#pragma unroll
+                    for (int v4 = 0; v4 < 4; ++v4) {
+                        const int rr = w0 + rw + i * 32 + 8 * v4 + 4 * hh, proj = rr / a.R, r = rr - proj * a.R;
+                        if (rr >= g.N) continue;
+                        float y[4];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) y[v] = r + v < rank ? acc[i][j][4 * v4 + v] * scale : 0.f;
+                        uint16_t *o = g.h + ((int64_t)pos * (g.N / a.R) + proj) * 3 * a.R + r;
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2 *>(o + p * a.R) = pack_part(y, p);
+                    }
+                continue;
+            }
             float *o = g.part + ((int64_t)blockIdx.y * a.T + pos) * g.N;
 #pragma unroll
             for (int i = 0; i < FW; ++i)
@@ -981,11 +999,14 @@ hipError_t many(const SharedArgs &a, const Product &g, int planes, hipStream_t s
 
 int plan_items(int T, int n) { return T / ITEM_TOKENS + (T < n ? T : n); }     // at most
 
-// Parts of K of the down-rank products: enough workgroups for the 256 CUs, each with some steps.
+// Parts of K of the down-rank products: one for short rows (no sum to launch; 400 tokens 1024 x 512 of rank 16, whole calls, two
+// launches each against one: 42.2 and 40.3 us; of three planes and 16 steps, 333 tokens 1000 x 520: 52.9 and 55.5), else enough
+// workgroups for the 256 CUs, each with some steps.  The workspace is for three planes, which have the most parts.
 int low_rank_rows(int N) { return N <= 64 ? 64 : 128; }
-int low_rank_parts(int T, int n, int R, int np, int K) {
+int low_rank_parts(int T, int n, int R, int np, int K, int planes) {
     const int bw = low_rank_rows(np * R), tiles = plan_items(T, n) * ((np * R + bw - 1) / bw), steps = (K + BK - 1) / BK;
     int parts = 1;
+    if (steps <= 16 && steps * planes <= 24) return 1;
     while (parts < MAX_PARTS && parts * tiles < 256 && steps >= 8 * parts) parts *= 2;
     return parts;
 }
@@ -993,10 +1014,11 @@ int low_rank_parts(int T, int n, int R, int np, int K) {
 hipError_t many_low_rank(const SharedArgs &a, const LowRank &L, int planes, hipStream_t st) {
     Product g = {};
     g.x = static_cast<const uint16_t *>(L.xv); g.K = L.K; g.N = L.np * a.R; g.gather = L.gather;
-    g.w[0] = L.a[0]; g.w[1] = L.a[1]; g.part = L.part;
-    const int parts = low_rank_parts(a.T, a.n, a.R, L.np, L.K);
+    g.w[0] = L.a[0]; g.w[1] = L.a[1]; g.h = L.s;
+    const int parts = low_rank_parts(a.T, a.n, a.R, L.np, L.K, planes);
+    if (parts > 1) g.part = L.part;
     hipError_t e = many_tiles<MODE_LOW_RANK>(a, g, planes, low_rank_rows(g.N), 64, plan_items(a.T, a.n), parts, st);
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || parts == 1) return e;
     const int64_t quads = (int64_t)a.T * g.N / 4;
     hipLaunchKernelGGL(k_low_rank_sum, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, st, a, L.part, parts, L.np, L.s);
     return hipGetLastError();
@@ -1041,7 +1063,7 @@ Layout layout(int T, int H, int Is, int n, int R, int xp, int hp) {
             l.ad = take((size_t)T * 4);
             l.items = take((size_t)plan_items(T, n) * 16);
             l.n_items = take(4);
-            const size_t gu = (size_t)low_rank_parts(T, n, R, 2, H) * 2, dn = (size_t)low_rank_parts(T, n, R, 1, Is);
+            const size_t gu = (size_t)low_rank_parts(T, n, R, 2, H, 3) * 2, dn = (size_t)low_rank_parts(T, n, R, 1, Is, 3);
             l.part = take((gu > dn ? gu : dn) * T * R * 4);
         }
     }
