@@ -216,6 +216,23 @@ def test_token_orders(m, T, mix):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 60, 300, 9000])
+def test_the_most_adapters(m, T):
+    """A pool of 4096, its last ones among those in use, on a stream that is named."""
+    note(f"4096 adapters T={T}")
+    c = Case(T, 24, 16, 4096, 8, seed=T)
+    c.ids[0], c.ids[-1] = 4095, 4096
+    keep, desc, pool, ids = c.on_gpu(m)
+    x, out = c.x.cuda(), torch.empty(T, c.H, device="cuda")
+    ws = torch.empty(m.moe_shared_ffn_workspace(desc, T, pool), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    m.moe_shared_ffn(desc, x, out, ws, pool, ids, stream=side.cuda_stream)
+    side.synchronize()
+    c.check(out.cpu())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [3, 70, 300])
 def test_pools_beyond_32_bits(m, T):
     """The last adapter of a pool whose A matrices pass 2^31 elements."""
