@@ -172,11 +172,12 @@ def _need_bytes(t, n: int, what: str):
 
 def _rows(x, hidden: int | None = None):
     """(T, H) of a [T][H] activation tensor."""
-    if x.dim() != 2:
-        raise ValueError(f"activations must be [tokens][hidden], got shape {tuple(x.shape)}")
-    if hidden is not None and x.shape[1] != hidden:
-        raise ValueError(f"activations have {x.shape[1]} columns, the layer has hidden {hidden}")
-    return x.shape[0], x.shape[1]
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"activations must be [tokens][hidden], got shape {tuple(shape)}")
+    if hidden is not None and shape[1] != hidden:
+        raise ValueError(f"activations have {shape[1]} columns, the layer has hidden {hidden}")
+    return shape
 
 
 def _dt(t) -> int:
@@ -371,37 +372,62 @@ def _type(t, what):
     return dt
 
 
-def _norm_output(T, H, residual, residual_out, weight, y, y_scale):
-    """Shape and type checks of what the norm calls share; (res_dt, w_dt, y_dt)."""
+def _norm_output(dev, T, H, residual, residual_out, weight, y, y_scale):
+    """Shape, type and device checks of what the norm calls share; their arguments from the residual on: addresses and types
+    of residual, weight and output.  (A one-row call is bound by these checks: each tensor is asked once for what is needed.)"""
     n = T * H
+    pr = po = ps = None
     res_dt = DT_F32
     if residual is not None and residual_out is not None:
-        res_dt = _type(residual, "residual")
-        if residual_out.dtype != residual.dtype:
-            raise TypeError(f"residual_out: expected {residual.dtype}, got {residual_out.dtype}")
-        if residual.numel() < n or residual_out.numel() < n:
+        res_t = residual.dtype
+        res_dt = _DTYPES.get(res_t)
+        if res_dt is None:
+            _type(residual, "residual")
+        if residual_out is not residual:
+            if residual_out.dtype != res_t:
+                raise TypeError(f"residual_out: expected {res_t}, got {residual_out.dtype}")
+            if residual_out.numel() < n:
+                _need(residual_out, n, "residual_out")
+            if not residual_out.is_contiguous() or residual_out.get_device() != dev:
+                _addrs(dev, residual_out)
+            po = residual_out.data_ptr()
+        if residual.numel() < n:
             _need(residual, n, "residual")
-            _need(residual_out, n, "residual_out")
+        if not residual.is_contiguous() or residual.get_device() != dev:
+            _addrs(dev, residual)
+        pr = residual.data_ptr()
+        if po is None:
+            po = pr
     elif residual is not None or residual_out is not None:
         raise ValueError("residual_out must be given iff residual is")
     if weight.numel() < H or y.numel() < n:
         _need(weight, H, "weight")
         _need(y, n, "y")
-    w_dt, y_dt = _type(weight, "weight"), _DTYPES.get(y.dtype)
+    y_t = y.dtype
+    w_dt, y_dt = _DTYPES.get(weight.dtype), _DTYPES.get(y_t)
+    if w_dt is None:
+        _type(weight, "weight")
     if y_scale is None:
-        if y.dtype == torch.float8_e4m3fn:
+        if y_t == torch.float8_e4m3fn:
             raise ValueError("y_scale is given iff y is float8_e4m3fn")
-        return res_dt, w_dt, _type(y, "y")
-    if y.dtype != torch.float8_e4m3fn:
+        if y_dt is None:
+            _type(y, "y")
+    elif y_t != torch.float8_e4m3fn:
         raise ValueError("y_scale is given iff y is float8_e4m3fn")
-    if y_scale.dtype == torch.float32:
+    elif y_scale.dtype == torch.float32:
         _need(y_scale, T, "y_scale")
-        return res_dt, w_dt, DT_E4M3_ROW
-    if y_scale.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+        y_dt = DT_E4M3_ROW
+    elif y_scale.dtype in (torch.float8_e8m0fnu, torch.uint8):
+        _need(y_scale, T * ((H + 31) // 32), "y_scale")
+        y_dt = DT_E4M3_BLOCK
+    else:
         raise TypeError(f"y_scale: expected float32 (row scales), float8_e8m0fnu or uint8 (block scales), got "
                         f"{y_scale.dtype}")
-    _need(y_scale, T * ((H + 31) // 32), "y_scale")
-    return res_dt, w_dt, DT_E4M3_BLOCK
+    if not (weight.is_contiguous() and y.is_contiguous() and weight.get_device() == dev and y.get_device() == dev):
+        _addrs(dev, weight, y)
+    if y_scale is not None:
+        ps, = _addrs(dev, y_scale)
+    return pr, po, res_dt, weight.data_ptr(), w_dt, y.data_ptr(), y_dt, ps
 
 
 def moe_add_rms_norm(x, residual, residual_out, weight, eps, y, y_scale=None, stream=None):
@@ -409,10 +435,12 @@ def moe_add_rms_norm(x, residual, residual_out, weight, eps, y, y_scale=None, st
     y_scale float8_e8m0fnu / uint8 [T][ceil(H/32)] (block scales) or float32 [T] (row scales); residual and
     residual_out may be None together, or the same tensor."""
     T, H = _rows(x)
-    res_dt, w_dt, y_dt = _norm_output(T, H, residual, residual_out, weight, y, y_scale)
-    x_dt, dev = _type(x, "x"), x.get_device()
-    px, pr, po, pw, py, ps = _addrs(dev, x, residual, residual_out, weight, y, y_scale)
-    st = lib.moe_add_rms_norm(px, x_dt, T, H, pr, po, res_dt, pw, w_dt, eps, py, y_dt, ps, _stream_on(stream, dev))
+    dev = x.get_device()
+    pr, po, res_dt, pw, w_dt, py, y_dt, ps = _norm_output(dev, T, H, residual, residual_out, weight, y, y_scale)
+    x_dt = _type(x, "x")
+    if dev < 0 or not x.is_contiguous():
+        _addrs(dev, x)
+    st = lib.moe_add_rms_norm(x.data_ptr(), x_dt, T, H, pr, po, res_dt, pw, w_dt, eps, py, y_dt, ps, _stream_on(stream, dev))
     if st:
         _check(st)
 
@@ -420,21 +448,32 @@ def moe_add_rms_norm(x, residual, residual_out, weight, eps, y, y_scale=None, st
 def moe_combine_norm(slot_out, topk_w, shared_out, residual, residual_out, weight, eps, y, y_scale=None, steer_v=None,
                      steer_f=0.0, stream=None):
     """moe_add_rms_norm of the combine's result (steered when steer_v is given): slot_out [T*k][H], topk_w [T][k]."""
-    if slot_out.dim() != 2 or topk_w.dim() != 2 or slot_out.shape[0] != topk_w.numel():
+    (T, k), H = _rows(topk_w), _rows(slot_out)[1]
+    if slot_out.numel() != T * k * H:
         raise ValueError(f"slot_out must be [T*k][H] and topk_w [T][k], got {tuple(slot_out.shape)} and "
                          f"{tuple(topk_w.shape)}")
-    (T, k), H = topk_w.shape, slot_out.shape[1]
-    _need(shared_out, T * H, "shared_out")
-    _need(steer_v, H, "steer_v")
-    for t in (slot_out, topk_w, shared_out, steer_v):
-        if t is not None and t.dtype != torch.float32:
-            raise TypeError(f"expected torch.float32, got {t.dtype}")
-    res_dt, w_dt, y_dt = _norm_output(T, H, residual, residual_out, weight, y, y_scale)
-    dev = slot_out.get_device()
-    pslot, ptw, psh, pv, pr, po, pw, py, ps = _addrs(dev, slot_out, topk_w, shared_out, steer_v, residual, residual_out,
-                                                     weight, y, y_scale)
-    st = lib.moe_combine_norm(pslot, ptw, psh, T, k, H, pv, steer_f, pr, po, res_dt, pw, w_dt, eps, py, y_dt, ps,
-                              _stream_on(stream, dev))
+    f32 = torch.float32
+    dev, psh, pv = slot_out.get_device(), None, None
+    if slot_out.dtype != f32 or topk_w.dtype != f32:
+        raise TypeError(f"slot_out and topk_w: expected torch.float32, got {slot_out.dtype} and {topk_w.dtype}")
+    if shared_out is not None:
+        if shared_out.dtype != f32:
+            raise TypeError(f"shared_out: expected torch.float32, got {shared_out.dtype}")
+        if shared_out.numel() < T * H:
+            _need(shared_out, T * H, "shared_out")
+        if not shared_out.is_contiguous() or shared_out.get_device() != dev:
+            _addrs(dev, shared_out)
+        psh = shared_out.data_ptr()
+    if steer_v is not None:
+        if steer_v.dtype != f32:
+            raise TypeError(f"steer_v: expected torch.float32, got {steer_v.dtype}")
+        _need(steer_v, H, "steer_v")
+        pv, = _addrs(dev, steer_v)
+    pr, po, res_dt, pw, w_dt, py, y_dt, ps = _norm_output(dev, T, H, residual, residual_out, weight, y, y_scale)
+    if dev < 0 or not (slot_out.is_contiguous() and topk_w.is_contiguous() and topk_w.get_device() == dev):
+        _addrs(dev, slot_out, topk_w)
+    st = lib.moe_combine_norm(slot_out.data_ptr(), topk_w.data_ptr(), psh, T, k, H, pv, steer_f, pr, po, res_dt, pw, w_dt, eps,
+                              py, y_dt, ps, _stream_on(stream, dev))
     if st:
         _check(st)
 
