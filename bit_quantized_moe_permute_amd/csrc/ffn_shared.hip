@@ -18,8 +18,8 @@
 //
 // Bound: the weights' bytes for few tokens, the matrix cores and the tiles' way into LDS for many.  hidden 4096, inter 2048,
 // kernels alone, fp32 out below 2048 tokens (a copy reaches 4.97 TB/s on this chip, a 2048 x 4096 x 4096 library product 62 us):
-//   1 token, rank 16:     inputs 3.8 us, gate/up 11.1 (33.6 MB, 3.0 TB/s), down 10.8 (16.9 MB, 1.6 TB/s)
-//   24 requests, rank 64: inputs 6.7, gate/up 15.9, inputs 4.3, down 12.6 (together 96 MB in 39.4 us, 2.4 TB/s)
+//   1 token, rank 16:     inputs 3.8 us, gate/up 11.1 (33.6 MB, 3.0 TB/s), down 9.5 (16.9 MB, 1.8 TB/s)
+//   24 requests, rank 64: inputs 6.9, gate/up 15.9, inputs 4.3, down 12.5 (together 100 MB in 37.5 us, 2.7 TB/s)
 //   512 tokens, rank 16:  plan 4.8, down-rank 6.3 + 6.0, gate/up 29 (0.6 PFLOP/s), down-rank 6.7 + 6.2, down 29 (three planes:
 //                         0.9 PFLOP/s)
 //   2048 tokens, rank 16, bf16 out: plan 5.8, down-rank 9.1 + 6.0, gate/up 70 (1.0 PFLOP/s), down-rank 6.6 + 6.0, down 45 (0.8)
@@ -65,6 +65,16 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float c) {
     c = dot2_bf16(__builtin_bit_cast(bf16x2_t, a.y), __builtin_bit_cast(bf16x2_t, b.y), c);
     c = dot2_bf16(__builtin_bit_cast(bf16x2_t, a.z), __builtin_bit_cast(bf16x2_t, b.z), c);
     return dot2_bf16(__builtin_bit_cast(bf16x2_t, a.w), __builtin_bit_cast(bf16x2_t, b.w), c);
+}
+
+// Eight products of bf16 and fp32 values into two sums
+__device__ __forceinline__ void dot8_f32(uint4 a, uint4 lo, uint4 hi, float (&c)[2]) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w}, x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        c[0] = __fmaf_rn(__uint_as_float(w[i] << 16), __uint_as_float(x[2 * i]), c[0]);
+        c[1] = __fmaf_rn(__uint_as_float(w[i] & 0xFFFF0000u), __uint_as_float(x[2 * i + 1]), c[1]);
+    }
 }
 
 // The first `n` of eight bf16 values, the others zero.
@@ -222,21 +232,19 @@ __host__ __device__ __forceinline__ int few_groups(int T) { return (T + FEW_TOKE
 constexpr int FEW_ROUND = 2048;
 __host__ __device__ __forceinline__ int few_steps(int K) { return (K + FEW_ROUND - 1) / FEW_ROUND * (FEW_ROUND / 32); }
 
-enum { ACT_BF16 = 0, ACT_PLANES = 1, ACT_F32 = 2 };          // x: one bf16 plane, PL of them, fp32 (packed as PL)
-
-template <int SRC, int PL>
+// PL: bf16 planes that fp32 activations are packed as; 1: they are bf16.
+template <bool F32, int PL>
 __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uint16_t *packed, int pack_blocks) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int K = L.K, steps = few_steps(K);
     if ((int)blockIdx.x < pack_blocks) {
-        constexpr int P = SRC == ACT_F32 ? PL : 1;
         const int i = blockIdx.x * 4 + wave, tf = few_frags(a.T), frag = i / steps, step = i - frag * steps;
         const int grp = frag / tf, f = frag - grp * tf;
         if (frag * 16 >= a.T) return;
         const int t = frag * 16 + (lane & 15), k = step * 32 + 8 * (lane >> 4);
-        uint4 *o = reinterpret_cast<uint4 *>(packed) + ((int64_t)(grp * P * tf + f) * steps + step) * 64 + lane;
+        uint4 *o = reinterpret_cast<uint4 *>(packed) + ((int64_t)(grp * PL * tf + f) * steps + step) * 64 + lane;
         const bool in = t < a.T && k < K;
-        if constexpr (SRC == ACT_F32) {
+        if constexpr (F32) {
             float4 u = make_float4(0.f, 0.f, 0.f, 0.f), w = u;
             if (in) {
                 const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(L.xv) + (int64_t)t * K + k);
@@ -245,7 +253,7 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
             }
             const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int p = 0; p < P; ++p) o[(int64_t)p * tf * steps * 64] = pack_part(v, p);
+            for (int p = 0; p < PL; ++p) o[(int64_t)p * tf * steps * 64] = pack_part(v, p);
         } else {
             o[0] = in ? load16(static_cast<const uint16_t *>(L.xv) + (int64_t)t * K + k) : make_uint4(0, 0, 0, 0);
         }
@@ -258,9 +266,9 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
     const uint16_t *A = proj ? L.a[1] : L.a[0];
     if (ad < 0 || !A) return;                                // not read either
     A += ((int64_t)ad * a.R + r) * K;
-    const int64_t row = (int64_t)t * K, plane = (int64_t)a.T * K;
-    constexpr int U = SRC == ACT_BF16 ? 8 : 4, P = SRC == ACT_PLANES ? PL : 1, V = SRC == ACT_F32 ? 2 : P;
-    float acc[3] = {0.f, 0.f, 0.f};
+    const int64_t row = (int64_t)t * K;
+    constexpr int U = F32 ? 4 : 8, V = F32 ? 2 : 1;
+    float acc[2] = {0.f, 0.f};
     for (int k0 = 0; k0 < K; k0 += U * 512) {
         uint4 w[U], v[V][U];
 #pragma unroll
@@ -268,33 +276,21 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
             const int k = k0 + j * 512 + lane * 8;
             const bool in = k < K;
             w[j] = in ? load16(A + k) : make_uint4(0, 0, 0, 0);
-            if constexpr (SRC == ACT_F32) {
+            if constexpr (F32) {
                 const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const float *>(L.xv) + row + k);
                 v[0][j] = in ? x[0] : make_uint4(0, 0, 0, 0);
                 v[1][j] = in ? x[1] : make_uint4(0, 0, 0, 0);
             } else {
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-                    v[p][j] = in ? load16(static_cast<const uint16_t *>(L.xv) + row + p * plane + k) : make_uint4(0, 0, 0, 0);
+                v[0][j] = in ? load16(static_cast<const uint16_t *>(L.xv) + row + k) : make_uint4(0, 0, 0, 0);
             }
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            if constexpr (SRC == ACT_F32) {
-                const uint32_t wv[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-                const uint32_t xv[8] = {v[0][j].x, v[0][j].y, v[0][j].z, v[0][j].w, v[1][j].x, v[1][j].y, v[1][j].z, v[1][j].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[0] = __fmaf_rn(__uint_as_float(wv[i] << 16), __uint_as_float(xv[2 * i]), acc[0]);
-                    acc[1] = __fmaf_rn(__uint_as_float(wv[i] & 0xFFFF0000u), __uint_as_float(xv[2 * i + 1]), acc[1]);
-                }
-            } else {
-#pragma unroll
-                for (int p = 0; p < P; ++p) acc[p] = dot8(w[j], v[p][j], acc[p]);
-            }
+            if constexpr (F32) dot8_f32(w[j], v[0][j], v[1][j], acc);
+            else acc[0] = dot8(w[j], v[0][j], acc[0]);
         }
     }
-    float y = wave_sum(acc[0] + (acc[1] + acc[2]));
+    float y = wave_sum(acc[0] + acc[1]);
     y = r < rank_of(a, ad) ? y * (a.scale ? uniform_at(a.scale, ad) : 1.f) : 0.f;
     uint16_t *o = L.s + ((int64_t)t * L.np + proj) * 3 * a.R + r;
     if (lane < 3) o[lane * a.R] = bf16_bits(bf16_part(y, lane));
@@ -315,10 +311,10 @@ __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0
 
 // AD: the adapters' low-rank results are read (AD_READ), or (AD_HERE, down, few values) formed by every workgroup from the rows of
 // h while its weights are on their way: that reads A out of the caches in every workgroup, where a launch between the two products
-// costs 4 us.  fp32 result, a launch against here, whole calls: 16 values of 2048 (1 token, rank 16) 25.6 and 24.0 us, of 4096
-// 40.2 and 38.2, of 512 14.8 and 13.6; 32 values of 2048 24.9 and 25.9, 8 of 8192 111.7 and 112.8.
+// costs 4 us.  fp32 result, a launch against here, whole calls: 16 values of 512 16.4 and 14.2 us, of 2048 (1 token, rank 16,
+// hidden 4096) 24.4 and 22.8, of 4096 38.6 and 37.2; 32 values of 512 16.3 and 15.0, of 2048 24.6 and 24.5; 8 of 8192 107.1 and 108.4.
 enum { AD_NONE = 0, AD_READ = 1, AD_HERE = 2 };
-constexpr int HERE_VALUES = 16, HERE_TERMS = 1 << 16;        // tokens * max_rank, and times shared_inter, at most for AD_HERE
+constexpr int HERE_VALUES = 32, HERE_TERMS = 1 << 16;        // for AD_HERE at most: tokens * max_rank, and times inter
 
 template <bool GU, int P, int TF, int AD>
 __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g) {
@@ -409,30 +405,39 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
     issue(0, 0);
     if (rounds > 1) issue(1, 1);
     if constexpr (AD == AD_HERE) {
-        // here[t][r] = scale (A[r] . h[t]), one wave per value
-        for (int e = wave; e < a.T * a.R; e += NW) {
+        // here[t][r] = scale (A[r] . h[t]), two rows of A (of one token: R is even) per wave at a time
+        for (int e = 2 * wave; e < a.T * a.R; e += 2 * NW) {
             const int t = e / a.R, r = e - t * a.R, id = uniform_at(a.token_adapter, t);
-            float y = 0.f;
-            if ((unsigned)id < (unsigned)a.n && r < rank_of(a, id)) {
-                const uint16_t *A = g.a + ((int64_t)id * a.R + r) * K, *hr = g.hrow + (int64_t)t * K;
+            const int rows_a = (unsigned)id < (unsigned)a.n ? rank_of(a, id) - r : 0;
+            float y[2][2] = {};
+            if (rows_a > 0) {
+                const uint16_t *A = g.a + ((int64_t)id * a.R + r) * K;
+                const float *hr = g.hrow + (int64_t)t * K;
                 for (int k0 = lane * 8; k0 < K; k0 += 4 * 512) {
-                    uint4 av[4], hv[4][P];
+                    uint4 av[4][2], hv[4][2];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int k = k0 + i * 512 < K ? k0 + i * 512 : lane * 8;
-                        av[i] = load16(A + k);
-#pragma unroll
-                        for (int p = 0; p < P; ++p) hv[i][p] = load16(hr + (int64_t)p * a.T * K + k);
+                        const uint4 *h4 = reinterpret_cast<const uint4 *>(hr + k);
+                        hv[i][0] = h4[0];
+                        hv[i][1] = h4[1];
+                        av[i][0] = load16(A + k);
+                        av[i][1] = load16(A + K + k);                    // behind the rank: of no use
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (k0 + i * 512 < K)
-#pragma unroll
-                            for (int p = 0; p < P; ++p) y = dot8(av[i], hv[i][p], y);
+                        if (k0 + i * 512 < K) {
+                            dot8_f32(av[i][0], hv[i][0], hv[i][1], y[0]);
+                            dot8_f32(av[i][1], hv[i][0], hv[i][1], y[1]);
+                        }
                 }
-                y = wave_sum(y) * (a.scale ? uniform_at(a.scale, id) : 1.f);
             }
-            if (lane == 0) here[e] = y;
+            const float scale = rows_a > 0 && a.scale ? uniform_at(a.scale, id) : 1.f;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const float sum = wave_sum(y[v][0] + y[v][1]) * scale;
+                if (lane == 0) here[e + v] = v < rows_a ? sum : 0.f;
+            }
         }
     }
     for (int r = 0; r < rounds; ++r, xw += FEW_ROUND / 32 * 64) {
@@ -523,8 +528,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
                 if (p >= g.hp) break;
                 const uint16_t part = bf16_bits(bf16_part(hv, p));
                 h[p * ((int64_t)TF * hsteps * 512) + o] = part;
-                if (g.hrow) g.hrow[((int64_t)p * a.T + t) * g.N + i] = part;     // for the down-rank products
             }
+            if (g.hrow) g.hrow[(int64_t)t * g.N + i] = hv;                       // for the down-rank products
         } else {
             if (r0 + r >= g.N) continue;
             const int64_t o = (int64_t)t * g.N + r0 + r;
@@ -943,16 +948,14 @@ hipError_t few(const SharedArgs &a, const Product &g, int planes, hipStream_t st
 }
 
 // Packs the activations (packed) and forms the low-rank results (a.n), one launch for both.
-hipError_t few_inputs(const SharedArgs &a, const LowRank &L, int src, int planes, uint16_t *packed, hipStream_t st) {
+hipError_t few_inputs(const SharedArgs &a, const LowRank &L, bool f32, int planes, uint16_t *packed, hipStream_t st) {
     const int pack = packed ? ((a.T + 15) / 16 * few_steps(L.K) + 3) / 4 : 0;
     const int low = a.n ? (a.T * L.np * a.R + 3) / 4 : 0;
     if (!pack && !low) return hipSuccess;
     const dim3 grd((unsigned)(pack + low)), blk(256);
-    if (src == ACT_BF16) hipLaunchKernelGGL((k_few_inputs<ACT_BF16, 1>), grd, blk, 0, st, a, L, packed, pack);
-    else if (src == ACT_PLANES && planes == 2) hipLaunchKernelGGL((k_few_inputs<ACT_PLANES, 2>), grd, blk, 0, st, a, L, packed, pack);
-    else if (src == ACT_PLANES) hipLaunchKernelGGL((k_few_inputs<ACT_PLANES, 3>), grd, blk, 0, st, a, L, packed, pack);
-    else if (planes == 2) hipLaunchKernelGGL((k_few_inputs<ACT_F32, 2>), grd, blk, 0, st, a, L, packed, pack);
-    else hipLaunchKernelGGL((k_few_inputs<ACT_F32, 3>), grd, blk, 0, st, a, L, packed, pack);
+    if (!f32) hipLaunchKernelGGL((k_few_inputs<false, 1>), grd, blk, 0, st, a, L, packed, pack);
+    else if (planes == 2) hipLaunchKernelGGL((k_few_inputs<true, 2>), grd, blk, 0, st, a, L, packed, pack);
+    else hipLaunchKernelGGL((k_few_inputs<true, 3>), grd, blk, 0, st, a, L, packed, pack);
     return hipGetLastError();
 }
 
@@ -1054,7 +1057,7 @@ Layout layout(int T, int H, int Is, int n, int R, int xp, int hp) {
     if (small) {
         l.x = take(packed(H, xp));
         l.h = take(packed(Is, hp));
-        l.hrow = take(n > 0 ? (size_t)T * Is * 2 * hp : 0);
+        l.hrow = take(n > 0 ? (size_t)T * Is * 4 : 0);
     } else {
         l.x = take(xp > 1 ? (size_t)T * H * xp * 2 : 0);
         l.h = take((size_t)T * Is * 2 * hp);
@@ -1104,13 +1107,13 @@ hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     hipError_t e;
     if (small) {
         gu.x = u16(l.x);
-        if (ad.n) { gu.hrow = u16(l.hrow); lh.xv = gu.hrow; }
-        if ((e = few_inputs(ag, lx, a.x_bf16 ? ACT_BF16 : ACT_F32, xp, u16(l.x), st)) != hipSuccess) return e;
+        if (ad.n) lh.xv = gu.hrow = reinterpret_cast<float *>(base + l.hrow);
+        if ((e = few_inputs(ag, lx, !a.x_bf16, xp, u16(l.x), st)) != hipSuccess) return e;
         if ((e = few<true>(ag, gu, xp, st)) != hipSuccess) return e;
         if (ad.n && low_rank_here(ad)) {
             dn.a = a.down_a;
             dn.hrow = gu.hrow;
-        } else if ((e = few_inputs(ad, lh, ACT_PLANES, hp, nullptr, st)) != hipSuccess) {
+        } else if ((e = few_inputs(ad, lh, true, hp, nullptr, st)) != hipSuccess) {
             return e;
         }
         return few<false>(ad, dn, hp, st);

@@ -136,7 +136,7 @@ struct Product {
     const uint16_t *w[2], *b[2];
     const uint16_t *s;                   // [T][np][3 parts][R]
     uint16_t *h;                         // gate/up: [hp][T][N] bf16 planes by sorted position, or (few tokens) packed
-    uint16_t *hrow;                      // few tokens: h as [hp][T][N] too, written by gate/up if set
+    float *hrow;                         // few tokens: h as fp32 [T][N] too, written by gate/up if set
     const uint16_t *a;                   // down, few values: the adapters' A, applied to hrow
     int hp;
     float *part;                         // down-rank, many tokens

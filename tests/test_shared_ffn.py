@@ -187,7 +187,7 @@ def test_wide_tiles(m, T, H, I, n, x_t):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,R", [(1, 8), (1, 16), (2, 8), (1, 24), (2, 16), (3, 8)])
+@pytest.mark.parametrize("T,R", [(1, 8), (1, 16), (2, 8), (1, 24), (2, 16), (3, 8), (1, 32), (4, 8), (5, 8), (1, 40)])
 @pytest.mark.parametrize("I", [8, 264, 2056, 8200])
 @pytest.mark.parametrize("out_t", [F32, BF16])
 def test_few_values(m, T, R, I, out_t):
