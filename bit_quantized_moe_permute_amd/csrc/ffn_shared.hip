@@ -312,7 +312,8 @@ __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0
 // AD: the adapters' low-rank results are read (AD_READ), or (AD_HERE, down, few values) formed by every workgroup from the rows of
 // h while its weights are on their way: that reads A out of the caches in every workgroup, where a launch between the two products
 // costs 4 us.  fp32 result, a launch against here, whole calls: 16 values of 512 16.4 and 14.2 us, of 2048 (1 token, rank 16,
-// hidden 4096) 24.4 and 22.8, of 4096 38.6 and 37.2; 32 values of 512 16.3 and 15.0, of 2048 24.6 and 24.5; 8 of 8192 107.1 and 108.4.
+// hidden 4096) 24.4 and 22.8, of 4096 38.6 and 37.2; 32 values of 512 16.3 and 15.0, of 2048 24.6 and 24.5; 8 of 8192 107.1
+// and 108.4.
 enum { AD_NONE = 0, AD_READ = 1, AD_HERE = 2 };
 constexpr int HERE_VALUES = 32, HERE_TERMS = 1 << 16;        // for AD_HERE at most: tokens * max_rank, and times inter
 
@@ -543,7 +544,9 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
 // Many tokens: a workgroup computes BW weight rows (gate/up: half of each) x BT tokens (P planes of them, which meet the same
 // weights), each wave 64 x BT/2 of them; both operands pass through LDS in 64-wide K stages, three of them (more gave nothing:
 // 512 tokens the same with four or six), filled by direct-to-LDS loads.  The matrix cores are busy half of the time at 2048
-// tokens, with no LDS bank conflict; twice the waves with half the tokens each ran the same (161 and 162 us the whole call).
+// tokens, with no LDS bank conflict: a 16-wide slice of 128 x 256 takes 256 cycles of matrix instructions, and LDS 288 for the
+// 24 KiB that its waves read and the 12 that arrive.  Waves of 128 x 128 would read a third less, but leave half of the compute
+// units without a tile there; twice the waves with half the tokens each ran the same (161 and 162 us the whole call).
 // LDS rows are 128 bytes, half of the 64 banks; 16-byte chunk c of row r lies at position c ^ (r / 2 % 8), so sixteen rows'
 // reads of one chunk column touch every bank once.
 //
@@ -766,7 +769,7 @@ __global__ __launch_bounds__(many_threads(BW, BT)) void k_many(SharedArgs a, Pro
         return;
     } else if (a.n) {
         // Up to NA adapters of 64 of this wave's tokens at a time, whose loads go out together (gate/up of 2048 tokens
-        // 70 us; 77 with one adapter after the other and its rank before its loads; 68 without adapters); rank values go 16 at a time,
+        // 70 us; 77 with one adapter after the other and its rank before its loads; 68 without adapters).  Rank values go 16 at a time,
         // each once with each part of the tokens' low-rank results (of which a bf16 out takes two: 16 bits).  An adapter's
         // products are formed for all of the tokens, in sums of their own, and added to those of its own tokens.
         constexpr int NP = GU ? 2 : 1, JG = FT < 2 ? FT : 2, SP = !GU && P == 1 ? 2 : 3, NA = 4;
