@@ -23,6 +23,8 @@
 //   512 tokens, rank 16:  plan 4.8, down-rank 6.3 + 6.0, gate/up 29 (0.6 PFLOP/s), down-rank 6.7 + 6.2, down 29 (three planes:
 //                         0.9 PFLOP/s)
 //   2048 tokens, rank 16, bf16 out: plan 5.8, down-rank 9.1 + 6.0, gate/up 70 (1.0 PFLOP/s), down-rank 6.6 + 6.0, down 45 (0.8)
+#include <algorithm>
+
 #include "common.h"
 #include "internal.h"
 
@@ -769,9 +771,9 @@ __global__ __launch_bounds__(many_threads(BW, BT)) void k_many(SharedArgs a, Pro
         return;
     } else if (a.n) {
         // Up to NA adapters of 64 of this wave's tokens at a time, whose loads go out together (gate/up of 2048 tokens
-        // 70 us; 77 with one adapter after the other and its rank before its loads; 68 without adapters).  Rank values go 16 at a time,
-        // each once with each part of the tokens' low-rank results (of which a bf16 out takes two: 16 bits).  An adapter's
-        // products are formed for all of the tokens, in sums of their own, and added to those of its own tokens.
+        // 70 us; 77 with one adapter after the other and its rank before its loads; 68 without adapters).  Rank values go 16
+        // at a time, each once with each part of the tokens' low-rank results (two of which, 16 bits, beside a bf16 result).
+        // An adapter's products are formed for all of the tokens, in sums of their own, and added to those of its own tokens.
         constexpr int NP = GU ? 2 : 1, JG = FT < 2 ? FT : 2, SP = !GU && P == 1 ? 2 : 3, NA = 4;
 #pragma unroll
         for (int jg = 0; jg < FT; jg += JG) {
@@ -1007,7 +1009,7 @@ int plan_items(int T, int n) { return T / ITEM_TOKENS + (T < n ? T : n); }     /
 
 // Parts of K of the down-rank products: one for short rows (no sum to launch; 400 tokens 1024 x 512 of rank 16, whole calls, two
 // launches each against one: 42.2 and 40.3 us; of three planes and 16 steps, 333 tokens 1000 x 520: 52.9 and 55.5), else enough
-// workgroups for the 256 CUs, each with some steps.  The workspace is for three planes, which have the most parts.
+// workgroups for the 256 CUs, each with some steps.
 int low_rank_rows(int N) { return N <= 64 ? 64 : 128; }
 int low_rank_parts(int T, int n, int R, int np, int K, int planes) {
     const int bw = low_rank_rows(np * R), tiles = plan_items(T, n) * ((np * R + bw - 1) / bw), steps = (K + BK - 1) / BK;
@@ -1069,8 +1071,10 @@ Layout layout(int T, int H, int Is, int n, int R, int xp, int hp) {
             l.ad = take((size_t)T * 4);
             l.items = take((size_t)plan_items(T, n) * 16);
             l.n_items = take(4);
-            const size_t gu = (size_t)low_rank_parts(T, n, R, 2, H, 3) * 2, dn = (size_t)low_rank_parts(T, n, R, 1, Is, 3);
-            l.part = take((gu > dn ? gu : dn) * T * R * 4);
+            // parts * T of the down-rank products of T or fewer tokens: MAX_PARTS parts at most, and more than one only where
+            // parts / 2 times T / 64 items are below 256 workgroups
+            const size_t some = std::min<size_t>((size_t)MAX_PARTS * T, 512 * 64 + MAX_PARTS * 64);
+            l.part = take(std::max<size_t>(T, some) * 2 * R * 4);
         }
     }
     l.total = o;
@@ -1082,8 +1086,12 @@ Layout layout(int T, int H, int Is, int n, int R, int xp, int hp) {
 namespace moe {
 
 size_t shared_workspace(int T, int H, int Is, int n, int R) {
-    // the largest over the activation and result types, so that one buffer serves every call of these sizes
-    return layout(T, H, Is, n, R, 3, 3).total;
+    // the largest over the activation and result types and over fewer tokens (whose streamed path pads its operands), so that
+    // one buffer serves every call of these sizes
+    size_t most = layout(T, H, Is, n, R, 3, 3).total;
+    for (int t = FEW_TOKENS; t <= 4 * FEW_TOKENS; t += FEW_TOKENS)
+        if (t < T && few_path(t, H, Is)) most = std::max(most, layout(t, H, Is, n, R, 3, 3).total);
+    return most;
 }
 
 hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {

@@ -445,8 +445,8 @@ typedef struct {
     const void *gate_a, *gate_b, *up_a, *up_b, *down_a, *down_b;
 } moe_adapter_desc;
 
-/* Workspace bytes moe_shared_ffn needs for n_tokens tokens (any x and output
- * type); 0 for arguments that call refuses.  A may be NULL. */
+/* Workspace bytes moe_shared_ffn needs for n_tokens or fewer tokens (any x and
+ * output type); 0 for arguments that call refuses.  A may be NULL. */
 size_t moe_shared_ffn_workspace(const moe_layer_desc *L, const moe_adapter_desc *A, int32_t n_tokens);
 
 /*

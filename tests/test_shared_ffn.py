@@ -529,6 +529,12 @@ def test_workspace_sizes():
     none, some = call(x=None)[2], call(pool={}, x=None)[2]
     assert 0 < none < some
     assert call(pool={}, T=100, x=None)[2] > some
+    # a buffer for many tokens serves fewer
+    for layer in (dict(hidden=8, shared_inter=8), dict(hidden=64, shared_inter=32), dict(hidden=1024, shared_inter=1024), dict(hidden=1024, shared_inter=1200),
+                  dict(hidden=4096, shared_inter=2048)):
+        for pool in (None, dict(n_adapters=1, max_rank=256), dict(n_adapters=300, max_rank=8), dict(n_adapters=16, max_rank=32)):
+            sizes = [call(layer=layer, pool=pool, T=T, x=None)[2] for T in [*range(1, 700), *range(700, 20000, 61)]]
+            assert all(a <= b for a, b in zip(sizes, sizes[1:])), (layer, pool)
 
 
 @needs_lib
