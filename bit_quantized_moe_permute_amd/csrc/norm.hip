@@ -20,11 +20,14 @@ namespace {
 
 constexpr float E4M3_MAX = 448.f;
 
+// The waves' exchanges through LDS; a barrier that does not wait for the residual's stores.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 __device__ __forceinline__ float wg_sum(float d, float *part, int nw) {
     d = wave_sum(d);
     if (nw == 1) return d;
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = d;
-    __syncthreads();
+    lds_barrier();
     float tot = 0.f;
     for (int i = 0; i < nw; ++i) tot += part[i];
     return tot;
@@ -56,7 +59,7 @@ __device__ __forceinline__ Factor row_factor(const NormArgs &a, float ss, double
     d = (lane_f64(d, 0) + lane_f64(d, 16)) + (lane_f64(d, 32) + lane_f64(d, 48));
     if (nw > 1) {
         if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = d;
-        __syncthreads();
+        lds_barrier();
         d = 0.0;
         for (int i = 0; i < nw; ++i) d += part[i];
     }
@@ -76,7 +79,7 @@ __device__ __forceinline__ float wg_max(float d, float *part, int nw) {
     d = wave_max_f32(d);
     if (nw == 1) return d;
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = d;
-    __syncthreads();
+    lds_barrier();
     float m = 0.f;
     for (int i = 0; i < nw; ++i) m = fmaxf(m, part[i]);
     return m;
@@ -114,14 +117,25 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // --- eight consecutive columns of one thread -------------------------------------------------------------------
 struct Raw8 { uint4 lo, hi; };          // bf16: lo alone
 
-template <bool BF16> __device__ __forceinline__ Raw8 load8(const void *p, int64_t i) {
+// 16 and 8 bytes at addresses that are aligned (AL) or whole elements only: one load or store either way
+struct __attribute__((packed)) Any16 { uint4 v; };
+struct __attribute__((packed)) Any8 { uint2 v; };
+template <bool AL> __device__ __forceinline__ uint4 get16(const void *p) {
+    if constexpr (AL) return *static_cast<const uint4 *>(p);
+    else return static_cast<const Any16 *>(p)->v;
+}
+template <bool AL> __device__ __forceinline__ void put16(void *p, uint4 v) {
+    if constexpr (AL) *static_cast<uint4 *>(p) = v;
+    else static_cast<Any16 *>(p)->v = v;
+}
+
+template <bool BF16, bool AL> __device__ __forceinline__ Raw8 load8(const void *p, int64_t i) {
     Raw8 r;
     if constexpr (BF16) {
-        r.lo = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+        r.lo = get16<AL>(static_cast<const uint16_t *>(p) + i);
     } else {
-        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
-        r.lo = q[0];
-        r.hi = q[1];
+        r.lo = get16<AL>(static_cast<const float *>(p) + i);
+        r.hi = get16<AL>(static_cast<const float *>(p) + i + 4);
     }
     return r;
 }
@@ -139,108 +153,147 @@ template <bool BF16> __device__ __forceinline__ void unpack8(const Raw8 &r, floa
         for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
     }
 }
-__device__ __forceinline__ void store8_f32(void *p, int64_t i, const float (&f)[8]) {
-    float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+// The first `n` of eight columns are stored: all of them, or (AL false, a row's last group) fewer.
+template <bool AL> __device__ __forceinline__ void store8_f32(void *p, int64_t i, const float (&f)[8], int n) {
+    float *q = static_cast<float *>(p) + i;
+    if (AL || n == 8) {
+        put16<AL>(q, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+        put16<AL>(q + 4, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n) q[e] = f[e];
 }
-__device__ __forceinline__ void store8_bf16(void *p, int64_t i, const float (&f)[8]) {
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
-        make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+template <bool AL> __device__ __forceinline__ void store8_bf16(void *p, int64_t i, const float (&f)[8], int n) {
+    uint16_t *q = static_cast<uint16_t *>(p) + i;
+    if (AL || n == 8) {
+        put16<AL>(q, make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])));
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n) q[e] = (uint16_t)(bf16_pair(f[e], 0.f) & 0xFFFFu);
+}
+template <bool AL> __device__ __forceinline__ void store8_e4m3(void *p, int64_t i, const float (&f)[8], float k, int n) {
+    uint8_t *q = static_cast<uint8_t *>(p) + i;
+    const uint2 v = make_uint2(e4m3x4(f[0] * k, f[1] * k, f[2] * k, f[3] * k), e4m3x4(f[4] * k, f[5] * k, f[6] * k, f[7] * k));
+    if constexpr (AL) {
+        *reinterpret_cast<uint2 *>(q) = v;
+    } else if (n == 8) {
+        reinterpret_cast<Any8 *>(q)->v = v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < n) q[e] = (uint8_t)((e < 4 ? v.x : v.y) >> (8 * (e & 3)));
+    }
+}
+// f[i] = f[i + s], 0 <= s <= 7, zeros from the end on
+__device__ __forceinline__ void shift8(float (&f)[8], int s) {
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = (s & o) == 0 ? f[i] : i + o < 8 ? f[i + o] : 0.f;
 }
 
 enum { SRC_F32 = 0, SRC_BF16 = 1, SRC_COMBINE = 2 };     // what the row comes from
 // One row per workgroup, C groups of eight columns per thread: group g = threadIdx.x + r * blockDim.x, so the four
-// groups of a 32-column block lie in four adjacent lanes.  Needs H % 8 == 0 and 16-byte aligned rows.
-template <int SRC, int RES, int C, int KC>
+// groups of a 32-column block lie in four adjacent lanes.  AL: H % 8 == 0 and 16-byte aligned rows.  Else a row's last group
+// loads its last eight columns (H >= 8) and moves its own to the front: the loads stay without branches.  515 x 2055 bf16
+// takes OTHER.
+template <int SRC, int RES, int C, int KC, bool AL>
 __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
     __shared__ float part[2][16];
     __shared__ double part64[16];
     const int64_t t = blockIdx.x, row = t * a.H;
-    const int nt = blockDim.x, nw = nt >> 6, ng = a.H >> 3;
+    const int nt = blockDim.x, nw = nt >> 6;
     float v[C][8];
     Raw8 res[C], wt[C];
     bool on[C];
+    int n[C];                                                // columns of the group
+    int64_t at[C];                                           // its first column as loaded
 #pragma unroll
-    for (int r = 0; r < C; ++r) on[r] = (int)threadIdx.x + r * nt < ng;
+    for (int r = 0; r < C; ++r) {
+        const int c = 8 * ((int)threadIdx.x + r * nt);
+        on[r] = c < a.H;
+        n[r] = AL ? 8 : min(8, a.H - c);
+        at[r] = AL ? c : min(c, a.H - 8);
+    }
+    auto own = [&](float (&f)[8], int r) __attribute__((always_inline)) {
+        if (!AL && __ballot(on[r] && n[r] < 8)) shift8(f, on[r] ? 8 - n[r] : 0);
+    };
     if constexpr (SRC == SRC_COMBINE) {
+        constexpr int KB = KC > 0 ? KC : 4;                  // rows whose loads go out together
         const int k = KC > 0 ? KC : a.k;
         const float *w = a.topk_w + t * k;
 #pragma unroll
         for (int r = 0; r < C; ++r) {
-            const int64_t c = 8 * ((int64_t)threadIdx.x + (int64_t)r * nt);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[r][i] = 0.f;
             if (!on[r]) continue;
-            if constexpr (RES != RES_NONE) res[r] = load8<RES == RES_BF16>(a.residual, row + c);
-            wt[r] = a.w_bf16 ? load8<true>(a.weight, c) : load8<false>(a.weight, c);
-            if constexpr (KC > 0) {
-                Raw8 o[KC], sh;
+            if constexpr (RES != RES_NONE) res[r] = load8<RES == RES_BF16, AL>(a.residual, row + at[r]);
+            wt[r] = a.w_bf16 ? load8<true, AL>(a.weight, at[r]) : load8<false, AL>(a.weight, at[r]);
+            Raw8 sh;
+            if (a.shared_out) sh = load8<false, AL>(a.shared_out, row + at[r]);
+            for (int j0 = 0; j0 < k; j0 += KB) {
+                Raw8 o[KB];
 #pragma unroll
-                for (int j = 0; j < KC; ++j) o[j] = load8<false>(a.slot_out, (t * KC + j) * a.H + c);
-                if (a.shared_out) sh = load8<false>(a.shared_out, row + c);
+                for (int j = 0; j < KB; ++j)
+                    o[j] = load8<false, AL>(a.slot_out, (t * k + (KC > 0 ? j : min(j0 + j, k - 1))) * a.H + at[r]);
 #pragma unroll
-                for (int j = 0; j < KC; ++j) {
+                for (int j = 0; j < KB; ++j) {
+                    if (KC == 0 && j0 + j >= k) break;
                     float f[8];
                     unpack8<false>(o[j], f);
-                    const float wj = w[j];
+                    const float wj = w[j0 + j];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[r][i] = __fmaf_rn(wj, f[i], v[r][i]);
                 }
-                if (a.shared_out) {
-                    float f[8];
-                    unpack8<false>(sh, f);
+            }
+            if (a.shared_out) {
+                float f[8];
+                unpack8<false>(sh, f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[r][i] += f[i];
-                }
-            } else {
-                for (int j = 0; j < k; ++j) {
-                    float f[8];
-                    unpack8<false>(load8<false>(a.slot_out, (t * k + j) * a.H + c), f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[r][i] = __fmaf_rn(w[j], f[i], v[r][i]);
-                }
-                if (a.shared_out) {
-                    float f[8];
-                    unpack8<false>(load8<false>(a.shared_out, row + c), f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[r][i] += f[i];
-                }
+                for (int i = 0; i < 8; ++i) v[r][i] += f[i];
             }
         }
+#pragma unroll
+        for (int r = 0; r < C; ++r) own(v[r], r);
         if (a.steer_v) {
             float d = 0.f;
             float sv[C][8];
 #pragma unroll
             for (int r = 0; r < C; ++r) {
-                if (!on[r]) continue;
-                unpack8<false>(load8<false>(a.steer_v, 8 * ((int64_t)threadIdx.x + (int64_t)r * nt)), sv[r]);
+                if (on[r]) {
+                    unpack8<false>(load8<false, AL>(a.steer_v, at[r]), sv[r]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sv[r][i] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < C; ++r) {
+                own(sv[r], r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) d = __fmaf_rn(sv[r][i], v[r][i], d);
             }
             const float sf = -a.steer_f * wg_sum(d, part[0], nw);
 #pragma unroll
-            for (int r = 0; r < C; ++r) {
-                if (!on[r]) continue;
+            for (int r = 0; r < C; ++r)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[r][i] = __fmaf_rn(sf, sv[r][i], v[r][i]);
-            }
         }
     } else {
         Raw8 x[C];
 #pragma unroll
         for (int r = 0; r < C; ++r) {
-            const int64_t c = 8 * ((int64_t)threadIdx.x + (int64_t)r * nt);
             if (!on[r]) continue;
-            x[r] = load8<SRC == SRC_BF16>(a.x, row + c);
-            if constexpr (RES != RES_NONE) res[r] = load8<RES == RES_BF16>(a.residual, row + c);
+            x[r] = load8<SRC == SRC_BF16, AL>(a.x, row + at[r]);
+            if constexpr (RES != RES_NONE) res[r] = load8<RES == RES_BF16, AL>(a.residual, row + at[r]);
         }
 #pragma unroll
-        for (int r = 0; r < C; ++r) {
-            if (!on[r]) continue;
-            const int64_t c = 8 * ((int64_t)threadIdx.x + (int64_t)r * nt);
-            wt[r] = a.w_bf16 ? load8<true>(a.weight, c) : load8<false>(a.weight, c);
-        }
+        for (int r = 0; r < C; ++r)
+            if (on[r]) wt[r] = a.w_bf16 ? load8<true, AL>(a.weight, at[r]) : load8<false, AL>(a.weight, at[r]);
 #pragma unroll
         for (int r = 0; r < C; ++r) {
             if (on[r]) {
@@ -249,6 +302,7 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[r][i] = 0.f;
             }
+            own(v[r], r);
         }
     }
     float ss = 0.f;
@@ -256,16 +310,17 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
     for (int r = 0; r < C; ++r) {
         const int64_t c = 8 * ((int64_t)threadIdx.x + (int64_t)r * nt);
         if constexpr (RES != RES_NONE) {
+            float f[8] = {};
+            if (on[r]) unpack8<RES == RES_BF16>(res[r], f);
+            own(f, r);
             if (on[r]) {
-                float f[8];
-                unpack8<RES == RES_BF16>(res[r], f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     v[r][i] += f[i];
                     if constexpr (RES == RES_BF16) v[r][i] = bf16_round(v[r][i]);   // the norm is of what is stored
                 }
-                if constexpr (RES == RES_BF16) store8_bf16(a.residual_out, row + c, v[r]);
-                else store8_f32(a.residual_out, row + c, v[r]);
+                if constexpr (RES == RES_BF16) store8_bf16<AL>(a.residual_out, row + c, v[r], n[r]);
+                else store8_f32<AL>(a.residual_out, row + c, v[r], n[r]);
             }
         }
 #pragma unroll
@@ -280,6 +335,7 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
             if (a.w_bf16) unpack8<true>(wt[r], f);
             else unpack8<false>(wt[r], f);
         }
+        own(f, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             v[r][i] = on[r] ? normed(v[r][i], rinv, f[i]) : 0.f;
@@ -301,9 +357,9 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
         const int g = (int)threadIdx.x + r * nt;
         const int64_t c = 8 * (int64_t)g;
         if (a.y_kind == NORM_BF16) {
-            if (on[r]) store8_bf16(a.y, row + c, v[r]);
+            if (on[r]) store8_bf16<AL>(a.y, row + c, v[r], n[r]);
         } else if (a.y_kind == NORM_F32) {
-            if (on[r]) store8_f32(a.y, row + c, v[r]);
+            if (on[r]) store8_f32<AL>(a.y, row + c, v[r], n[r]);
         } else {
             if (a.y_kind == NORM_MX8) {
                 float m = 0.f;
@@ -316,12 +372,7 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
                     static_cast<uint8_t *>(a.y_scale)[t * ((a.H + 31) / 32) + (g >> 2)] = (uint8_t)(e + 127);
                 inv = exp2_neg(e);
             }
-            if (on[r]) {
-                const float (&f)[8] = v[r];
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.y) + row + c) =
-                    make_uint2(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                               e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-            }
+            if (on[r]) store8_e4m3<AL>(a.y, row + c, v[r], inv, n[r]);
         }
     }
 }
@@ -330,117 +381,76 @@ __device__ __forceinline__ float load1(const void *p, int64_t i, bool bf16) {
     return bf16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(p)[i]) : static_cast<const float *>(p)[i];
 }
 
-// Any row length up to EL * blockDim.x and any alignment: column c = threadIdx.x + i * blockDim.x, one element per
-// load, so a 32-column block lies in one half of a wave.  Columns behind the row's end load its last one and count as
-// zero: without branches around them all of a row's loads are in flight at once (515 x 2055 bf16: 9.8 us, 16.4 with branches;
-// 8.5 MB in elements of 2 bytes per lane, bound by their number and two barriers).
-template <int EL, int MAX_THREADS>
-__global__ __launch_bounds__(MAX_THREADS) void k_norm_any(NormArgs a, int src) {
-    __shared__ float part[2][16];
-    __shared__ double part64[16];
+// Rows of fewer than eight columns: one wave per row, one column per lane.
+__global__ __launch_bounds__(64) void k_norm_short(NormArgs a, int src) {
     const int64_t t = blockIdx.x, row = t * a.H;
-    const int nt = blockDim.x, nw = nt >> 6;
-    float v[EL], res[EL], wt[EL];
-    int at[EL];
-#pragma unroll
-    for (int i = 0; i < EL; ++i) at[i] = min((int)threadIdx.x + i * nt, a.H - 1);
-    if (src == SRC_COMBINE) {
-#pragma unroll
-        for (int i = 0; i < EL; ++i) v[i] = 0.f;
-        for (int j = 0; j < a.k; ++j) {
-            const float *o = a.slot_out + (t * a.k + j) * a.H, w = a.topk_w[t * a.k + j];
-            float x[EL];
-#pragma unroll
-            for (int i = 0; i < EL; ++i) x[i] = o[at[i]];
-#pragma unroll
-            for (int i = 0; i < EL; ++i) v[i] = __fmaf_rn(w, x[i], v[i]);
+    const int c = threadIdx.x;
+    const bool on = c < a.H;
+    float v = 0.f, w = 0.f;
+    if (on) {
+        if (src == SRC_COMBINE) {
+            for (int j = 0; j < a.k; ++j) v = __fmaf_rn(a.topk_w[t * a.k + j], a.slot_out[(t * a.k + j) * a.H + c], v);
+            if (a.shared_out) v += a.shared_out[row + c];
+        } else {
+            v = load1(a.x, row + c, src == SRC_BF16);
         }
-        if (a.shared_out) {
-            float x[EL];
-#pragma unroll
-            for (int i = 0; i < EL; ++i) x[i] = a.shared_out[row + at[i]];
-#pragma unroll
-            for (int i = 0; i < EL; ++i) v[i] += x[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < EL; ++i) v[i] = load1(a.x, row + at[i], src == SRC_BF16);
+        w = load1(a.weight, c, a.w_bf16);
     }
-    if (a.res_kind != RES_NONE) {
-#pragma unroll
-        for (int i = 0; i < EL; ++i) res[i] = load1(a.residual, row + at[i], a.res_kind == RES_BF16);
-    }
-#pragma unroll
-    for (int i = 0; i < EL; ++i) wt[i] = load1(a.weight, at[i], a.w_bf16);
     if (src == SRC_COMBINE && a.steer_v) {
-        float d = 0.f, sv[EL];
-#pragma unroll
-        for (int i = 0; i < EL; ++i) sv[i] = a.steer_v[at[i]];
-#pragma unroll
-        for (int i = 0; i < EL; ++i) d = (int)threadIdx.x + i * nt < a.H ? __fmaf_rn(sv[i], v[i], d) : d;
-        const float sf = -a.steer_f * wg_sum(d, part[0], nw);
-#pragma unroll
-        for (int i = 0; i < EL; ++i) v[i] = __fmaf_rn(sf, sv[i], v[i]);
+        const float sv = on ? a.steer_v[c] : 0.f;
+        v = __fmaf_rn(-a.steer_f * wave_sum(sv * v), sv, v);
     }
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < EL; ++i) {
-        const int c = (int)threadIdx.x + i * nt;
-        if (a.res_kind != RES_NONE) v[i] += res[i];
-        if (a.res_kind == RES_BF16) v[i] = bf16_round(v[i]);
-        if (c >= a.H) v[i] = 0.f;
-        ss = __fmaf_rn(v[i], v[i], ss);
-        if (c < a.H && a.res_kind == RES_F32) static_cast<float *>(a.residual_out)[row + c] = v[i];
-        if (c < a.H && a.res_kind == RES_BF16) static_cast<__bf16 *>(a.residual_out)[row + c] = (__bf16)v[i];
+    if (on && a.res_kind != RES_NONE) {
+        v += load1(a.residual, row + c, a.res_kind == RES_BF16);
+        if (a.res_kind == RES_BF16) v = bf16_round(v);
+        if (a.res_kind == RES_BF16) static_cast<__bf16 *>(a.residual_out)[row + c] = (__bf16)v;
+        else static_cast<float *>(a.residual_out)[row + c] = v;
     }
-    const Factor rinv = row_factor(a, ss, part64, nw);
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < EL; ++i) {
-        v[i] = normed(v[i], rinv, wt[i]);
-        amax = fmaxf(amax, fabsf(v[i]));
-    }
-    float inv = 1.f;
+    const Factor rinv = row_factor(a, on ? v * v : 0.f, nullptr, 1);
+    v = on ? normed(v, rinv, w) : 0.f;
+    const float amax = wave_max_f32(fabsf(v));
     if (a.y_kind == NORM_ROW8) {
-        const float s = row_scale(wg_max(amax, part[1], nw));
-        if (threadIdx.x == 0) static_cast<float *>(a.y_scale)[t] = s;
-        const float rs = 1.0f / s;
-#pragma unroll
-        for (int i = 0; i < EL; ++i) v[i] = quotient(v[i], s, rs);
+        const float s = row_scale(amax);
+        if (c == 0) static_cast<float *>(a.y_scale)[t] = s;
+        v = quotient(v, s, 1.0f / s);
+    } else if (a.y_kind == NORM_MX8) {
+        const int e = mx_exponent(amax);
+        if (c == 0) static_cast<uint8_t *>(a.y_scale)[t] = (uint8_t)(e + 127);
+        v *= exp2_neg(e);
     }
-#pragma unroll
-    for (int i = 0; i < EL; ++i) {
-        const int c = (int)threadIdx.x + i * nt;
-        if (a.y_kind == NORM_MX8) {
-            float m = fabsf(v[i]);
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-            const int e = mx_exponent(m);
-            if (c < a.H && (c & 31) == 0)
-                static_cast<uint8_t *>(a.y_scale)[t * ((a.H + 31) / 32) + (c >> 5)] = (uint8_t)(e + 127);
-            inv = exp2_neg(e);
-        }
-        if (c >= a.H) continue;
-        if (a.y_kind == NORM_BF16) static_cast<__bf16 *>(a.y)[row + c] = (__bf16)v[i];
-        else if (a.y_kind == NORM_F32) static_cast<float *>(a.y)[row + c] = v[i];
-        else static_cast<uint8_t *>(a.y)[row + c] = (uint8_t)(e4m3x4(v[i] * inv, 0.f, 0.f, 0.f) & 0xFFu);
-    }
+    if (!on) return;
+    if (a.y_kind == NORM_BF16) static_cast<__bf16 *>(a.y)[row + c] = (__bf16)v;
+    else if (a.y_kind == NORM_F32) static_cast<float *>(a.y)[row + c] = v;
+    else static_cast<uint8_t *>(a.y)[row + c] = (uint8_t)(e4m3x4(v, 0.f, 0.f, 0.f) & 0xFFu);
 }
 
-template <int SRC, int RES, int KC>
+template <int SRC, int RES, int KC, bool AL>
 hipError_t launch_vec(const NormArgs &a, int c, int nt, hipStream_t st) {
     const dim3 grd((unsigned)a.T), blk((unsigned)nt);
-    if (c == 1) hipLaunchKernelGGL((k_norm_vec<SRC, RES, 1, KC>), grd, blk, 0, st, a);
-    else if (c == 2) hipLaunchKernelGGL((k_norm_vec<SRC, RES, 2, KC>), grd, blk, 0, st, a);
-    else hipLaunchKernelGGL((k_norm_vec<SRC, RES, 4, KC>), grd, blk, 0, st, a);
+    if (c == 1) hipLaunchKernelGGL((k_norm_vec<SRC, RES, 1, KC, AL>), grd, blk, 0, st, a);
+    else if (c == 2) hipLaunchKernelGGL((k_norm_vec<SRC, RES, 2, KC, AL>), grd, blk, 0, st, a);
+    else hipLaunchKernelGGL((k_norm_vec<SRC, RES, 4, KC, AL>), grd, blk, 0, st, a);
     return hipGetLastError();
 }
 
-template <int SRC, int KC>
+template <int SRC, int KC, bool AL>
 hipError_t launch_res(const NormArgs &a, int c, int nt, hipStream_t st) {
-    if (a.res_kind == RES_NONE) return launch_vec<SRC, RES_NONE, KC>(a, c, nt, st);
-    if (a.res_kind == RES_F32) return launch_vec<SRC, RES_F32, KC>(a, c, nt, st);
-    return launch_vec<SRC, RES_BF16, KC>(a, c, nt, st);
+    if (a.res_kind == RES_NONE) return launch_vec<SRC, RES_NONE, KC, AL>(a, c, nt, st);
+    if (a.res_kind == RES_F32) return launch_vec<SRC, RES_F32, KC, AL>(a, c, nt, st);
+    return launch_vec<SRC, RES_BF16, KC, AL>(a, c, nt, st);
+}
+
+template <bool AL>
+hipError_t launch_rows(const NormArgs &a, int src, hipStream_t st) {
+    const int ng = (a.H + 7) / 8;
+    const int c = ng <= 1024 ? 1 : ng <= 2048 ? 2 : 4;
+    const int nt = ((ng + c - 1) / c + 63) / 64 * 64;
+    if (src == SRC_F32) return launch_res<SRC_F32, 0, AL>(a, c, nt, st);
+    if (src == SRC_BF16) return launch_res<SRC_BF16, 0, AL>(a, c, nt, st);
+    if constexpr (AL) {
+        if (a.k == 8) return launch_res<SRC_COMBINE, 8, AL>(a, c, nt, st);
+    }
+    return launch_res<SRC_COMBINE, 0, AL>(a, c, nt, st);
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p % 16) == 0; }
@@ -454,23 +464,11 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t st) {
     const bool vec = a.H % 8 == 0 && aligned16(a.x) && aligned16(a.residual) && aligned16(a.residual_out) &&
                      aligned16(a.weight) && aligned16(a.y) && aligned16(a.slot_out) && aligned16(a.shared_out) &&
                      aligned16(a.steer_v);
-    if (!vec) {
-        const int nt = a.H <= 256 ? 64 : a.H <= 8192 ? 256 : 1024;
-        const dim3 grd((unsigned)a.T), blk((unsigned)nt);
-        if (a.H <= 4 * nt) hipLaunchKernelGGL((k_norm_any<4, 256>), grd, blk, 0, st, a, src);
-        else if (a.H <= 4096) hipLaunchKernelGGL((k_norm_any<16, 256>), grd, blk, 0, st, a, src);
-        else if (a.H <= 8192) hipLaunchKernelGGL((k_norm_any<32, 256>), grd, blk, 0, st, a, src);
-        else if (a.H <= 16384) hipLaunchKernelGGL((k_norm_any<16, 1024>), grd, blk, 0, st, a, src);
-        else hipLaunchKernelGGL((k_norm_any<32, 1024>), grd, blk, 0, st, a, src);
+    if (a.H < 8) {
+        hipLaunchKernelGGL(k_norm_short, dim3((unsigned)a.T), dim3(64), 0, st, a, src);
         return hipGetLastError();
     }
-    const int ng = a.H / 8;
-    const int c = ng <= 1024 ? 1 : ng <= 2048 ? 2 : 4;
-    const int nt = ((ng + c - 1) / c + 63) / 64 * 64;
-    if (src == SRC_F32) return launch_res<SRC_F32, 0>(a, c, nt, st);
-    if (src == SRC_BF16) return launch_res<SRC_BF16, 0>(a, c, nt, st);
-    if (a.k == 8) return launch_res<SRC_COMBINE, 8>(a, c, nt, st);
-    return launch_res<SRC_COMBINE, 0>(a, c, nt, st);
+    return vec ? launch_rows<true>(a, src, st) : launch_rows<false>(a, src, st);
 }
 
 }  // namespace moe
