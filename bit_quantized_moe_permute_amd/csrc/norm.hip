@@ -4,13 +4,16 @@
 //   n = v / sqrt(sum v^2 / H + eps) * weight,  y = round(n)
 //
 // y is bf16, fp32, or e4m3: with one power-of-two scale per 32 columns (the block format that the scaled matrix
-// instructions of gfx950 read) or one fp32 scale per row.  All sums are fp32, in an order fixed per launch shape.
+// instructions of gfx950 read) or one fp32 scale per row.  All sums are in an order fixed per launch shape: a row's
+// squares in fp32 per thread and binary64 between them, combined rows in binary64.
 //
 // Bound: HBM traffic for many rows, one memory round trip and two barriers for few.  One workgroup holds one row in
 // registers, so every input is read once: all loads of a row (source, residual, weight) are issued before the first
 // reduction.  A copy of 2 GiB moves 4.97 TB/s on this chip; 11709 x 4096 with block scales takes 61.0 us (337 MB, 5.5 TB/s),
 // 1469 x 4096 with row scales 14.8 (78 MB, 5.3 TB/s), 2048 combined rows of 8 x 4096 66.4 (344 MB, 5.2 TB/s); one row of 4096
 // takes 2.4 us, one combined row 3.2, which is what a launch with one round trip to memory takes.
+#include <type_traits>
+
 #include "common.h"
 #include "internal.h"
 
@@ -18,27 +21,15 @@ using namespace moe;
 
 namespace {
 
-constexpr float E4M3_MAX = 448.f;
-
 // The waves' exchanges through LDS; a barrier that does not wait for the residual's stores.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-__device__ __forceinline__ float wg_sum(float d, float *part, int nw) {
-    d = wave_sum(d);
-    if (nw == 1) return d;
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = d;
-    lds_barrier();
-    float tot = 0.f;
-    for (int i = 0; i < nw; ++i) tot += part[i];
-    return tot;
-}
-
-// v + its value in the lane that CTRL names
-template <int CTRL> __device__ __forceinline__ double add_dpp_f64(double v) {
+// v of the lane that CTRL names
+template <int CTRL> __device__ __forceinline__ double dpp_f64(double v) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)b, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
     const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(b >> 32), (int)(b >> 32), CTRL, 0xF, 0xF, false);
-    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 __device__ __forceinline__ double lane_f64(double v, int l) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
@@ -46,43 +37,41 @@ __device__ __forceinline__ double lane_f64(double v, int l) {
                                       (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, l));
 }
 
+// Sum, or largest value that is no NaN (of values >= 0), over the workgroup
+template <bool MAX> __device__ __forceinline__ double join(double x, double y) { return MAX ? fmax(x, y) : x + y; }
+template <bool MAX> __device__ __forceinline__ double wg_join(double d, double *part, int nw) {
+    d = join<MAX>(d, dpp_f64<0xB1>(d));                     // quad swaps, then mirrors of 8 and 16 lanes
+    d = join<MAX>(d, dpp_f64<0x4E>(d));
+    d = join<MAX>(d, dpp_f64<0x141>(d));
+    d = join<MAX>(d, dpp_f64<0x140>(d));
+    d = join<MAX>(join<MAX>(lane_f64(d, 0), lane_f64(d, 16)), join<MAX>(lane_f64(d, 32), lane_f64(d, 48)));
+    if (nw == 1) return d;
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = d;
+    lds_barrier();
+    d = 0.0;
+    for (int i = 0; i < nw; ++i) d = join<MAX>(d, part[i]);
+    return d;
+}
+__device__ __forceinline__ double wg_sum(double d, double *part, int nw) { return wg_join<false>(d, part, nw); }
+
 // 1 / sqrt(sum / H + eps) in two fp32 parts, from the threads' fp32 sums of squares.  The row's one factor moves all of its
 // columns the same way, and where y is e4m3 an error in it decides blocks' scales and values that lie next to a rounding's
 // border: so the sums meet in binary64, and the square root is taken there (the instruction's estimate and one Newton step).
-// It costs no time: 11709 x 4096 61.2 us with and without, one row 6.3.
-struct Factor { float hi, lo; };
+// It costs no time: 11709 x 4096 61.2 us with and without, one row 6.3.  Combined rows in binary64 neither (2048 x 8 x 4096
+// 66.2 and 66.3 us), a row's scale and the quotients by it little (1469 x 4096 14.7 and 15.1).  8-bit outputs are the exact
+// ones' (of 25 random calls none had a differing code, where fp32 sums had up to 226).
+struct Factor { float hi, lo; double r; };
 __device__ __forceinline__ Factor row_factor(const NormArgs &a, float ss, double *part, int nw) {
-    double d = add_dpp_f64<0xB1>((double)ss);               // quad swaps, then mirrors of 8 and 16 lanes
-    d = add_dpp_f64<0x4E>(d);
-    d = add_dpp_f64<0x141>(d);
-    d = add_dpp_f64<0x140>(d);
-    d = (lane_f64(d, 0) + lane_f64(d, 16)) + (lane_f64(d, 32) + lane_f64(d, 48));
-    if (nw > 1) {
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = d;
-        lds_barrier();
-        d = 0.0;
-        for (int i = 0; i < nw; ++i) d += part[i];
-    }
-    const double m = fma(d, a.inv_hidden, (double)a.eps), r0 = __builtin_amdgcn_rsq(m);
+    const double m = fma(wg_sum((double)ss, part, nw), a.inv_hidden, (double)a.eps), r0 = __builtin_amdgcn_rsq(m);
     const double r = m == HUGE_VAL ? 0.0 : fma(0.5 * r0, fma(-m * r0, r0, 1.0), r0);
     const float hi = (float)r;
-    return {hi, (float)(r - (double)hi)};
+    return {hi, (float)(r - (double)hi), r};
 }
 // v * factor * w, off by little more than its one rounding
 __device__ __forceinline__ float normed(float v, const Factor &r, float w) {
     const float hi = v * r.hi;
     const float lo = __fmaf_rn(v, r.lo, __fmaf_rn(v, r.hi, -hi));
     return __fmaf_rn(hi, w, lo * w);
-}
-
-__device__ __forceinline__ float wg_max(float d, float *part, int nw) {
-    d = wave_max_f32(d);
-    if (nw == 1) return d;
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = d;
-    lds_barrier();
-    float m = 0.f;
-    for (int i = 0; i < nw; ++i) m = fmaxf(m, part[i]);
-    return m;
 }
 
 // Power-of-two block scale: the least e with amax <= 448 * 2^e (448 = 1.75 * 2^8), clamped to [-127, 127].  With
@@ -97,13 +86,8 @@ __device__ __forceinline__ int mx_exponent(float amax) {
 __device__ __forceinline__ float exp2_neg(int e) {
     return __uint_as_float(e < 127 ? (uint32_t)(127 - e) << 23 : 0x400000u);
 }
-__device__ __forceinline__ float row_scale(float amax) { return fmaxf(amax, E4M3_MAX * 0x1p-126f) / E4M3_MAX; }
-
-// v / s, s > 0: the product with 1 / s and the remainder's share (an infinite s, of a row that holds one: the product alone)
-__device__ __forceinline__ float quotient(float v, float s, float inv) {
-    const float q = v * inv;
-    return s < HUGE_VALF ? __fmaf_rn(__fmaf_rn(-q, s, v), inv, q) : q;
-}
+// A row's scale from its largest |n|.  Rows with one are normed, scaled and only then rounded: n / s in binary64.
+__device__ __forceinline__ double row_scale(double amax) { return fmax(amax, 448 * 0x1p-126) / 448; }
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b});
@@ -189,24 +173,33 @@ template <bool AL> __device__ __forceinline__ void store8_e4m3(void *p, int64_t 
     }
 }
 // f[i] = f[i + s], 0 <= s <= 7, zeros from the end on
-__device__ __forceinline__ void shift8(float (&f)[8], int s) {
+template <typename V> __device__ __forceinline__ void shift8(V (&f)[8], int s) {
 #pragma unroll
     for (int o = 4; o >= 1; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = (s & o) == 0 ? f[i] : i + o < 8 ? f[i + o] : 0.f;
+        for (int i = 0; i < 8; ++i) f[i] = (s & o) == 0 ? f[i] : i + o < 8 ? f[i + o] : V(0);
 }
+
+// v = x + residual is an fp32 value, whatever it is rounded to next (the compiler would round binary64 to bf16 at once)
+__device__ __forceinline__ float to_f32(double v) {
+    float f = (float)v;
+    asm("" : "+v"(f));
+    return f;
+}
+__device__ __forceinline__ float to_f32(float v) { return v; }
 
 enum { SRC_F32 = 0, SRC_BF16 = 1, SRC_COMBINE = 2 };     // what the row comes from
 // One row per workgroup, C groups of eight columns per thread: group g = threadIdx.x + r * blockDim.x, so the four
 // groups of a 32-column block lie in four adjacent lanes.  AL: H % 8 == 0 and 16-byte aligned rows.  Else a row's last group
-// loads its last eight columns (H >= 8) and moves its own to the front: the loads stay without branches.  515 x 2055 bf16
-// takes OTHER.
+// loads its last eight columns (H >= 8) and moves its own to the front, and addresses are aligned to elements only: one load
+// for eight columns all the same.  515 x 2055 bf16, whole call: 5.3 us, with one column per lane and load 9.9.
 template <int SRC, int RES, int C, int KC, bool AL>
 __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
-    __shared__ float part[2][16];
-    __shared__ double part64[16];
+    __shared__ double part64[3][16];
     const int64_t t = blockIdx.x, row = t * a.H;
     const int nt = blockDim.x, nw = nt >> 6;
+    // combined rows are summed in binary64 and rounded once, with the residual
+    typename std::conditional<SRC == SRC_COMBINE, double, float>::type s[C][8];
     float v[C][8];
     Raw8 res[C], wt[C];
     bool on[C];
@@ -219,7 +212,7 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
         n[r] = AL ? 8 : min(8, a.H - c);
         at[r] = AL ? c : min(c, a.H - 8);
     }
-    auto own = [&](float (&f)[8], int r) __attribute__((always_inline)) {
+    auto own = [&](auto &f, int r) __attribute__((always_inline)) {
         if (!AL && __ballot(on[r] && n[r] < 8)) shift8(f, on[r] ? 8 - n[r] : 0);
     };
     if constexpr (SRC == SRC_COMBINE) {
@@ -229,7 +222,7 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
 #pragma unroll
         for (int r = 0; r < C; ++r) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[r][i] = 0.f;
+            for (int i = 0; i < 8; ++i) s[r][i] = 0.0;
             if (!on[r]) continue;
             if constexpr (RES != RES_NONE) res[r] = load8<RES == RES_BF16, AL>(a.residual, row + at[r]);
             wt[r] = a.w_bf16 ? load8<true, AL>(a.weight, at[r]) : load8<false, AL>(a.weight, at[r]);
@@ -245,22 +238,22 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
                     if (KC == 0 && j0 + j >= k) break;
                     float f[8];
                     unpack8<false>(o[j], f);
-                    const float wj = w[j0 + j];
+                    const double wj = (double)w[j0 + j];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[r][i] = __fmaf_rn(wj, f[i], v[r][i]);
+                    for (int i = 0; i < 8; ++i) s[r][i] = fma(wj, (double)f[i], s[r][i]);
                 }
             }
             if (a.shared_out) {
                 float f[8];
                 unpack8<false>(sh, f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[r][i] += f[i];
+                for (int i = 0; i < 8; ++i) s[r][i] += (double)f[i];
             }
         }
 #pragma unroll
-        for (int r = 0; r < C; ++r) own(v[r], r);
+        for (int r = 0; r < C; ++r) own(s[r], r);
         if (a.steer_v) {
-            float d = 0.f;
+            double d = 0.0;
             float sv[C][8];
 #pragma unroll
             for (int r = 0; r < C; ++r) {
@@ -275,13 +268,13 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
             for (int r = 0; r < C; ++r) {
                 own(sv[r], r);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d = __fmaf_rn(sv[r][i], v[r][i], d);
+                for (int i = 0; i < 8; ++i) d = fma((double)sv[r][i], s[r][i], d);
             }
-            const float sf = -a.steer_f * wg_sum(d, part[0], nw);
+            const double sf = -(double)a.steer_f * wg_sum(d, part64[1], nw);
 #pragma unroll
             for (int r = 0; r < C; ++r)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[r][i] = __fmaf_rn(sf, sv[r][i], v[r][i]);
+                for (int i = 0; i < 8; ++i) s[r][i] = fma(sf, (double)sv[r][i], s[r][i]);
         }
     } else {
         Raw8 x[C];
@@ -297,18 +290,20 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
 #pragma unroll
         for (int r = 0; r < C; ++r) {
             if (on[r]) {
-                unpack8<SRC == SRC_BF16>(x[r], v[r]);
+                unpack8<SRC == SRC_BF16>(x[r], s[r]);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[r][i] = 0.f;
+                for (int i = 0; i < 8; ++i) s[r][i] = 0.f;
             }
-            own(v[r], r);
+            own(s[r], r);
         }
     }
     float ss = 0.f;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
         const int64_t c = 8 * ((int64_t)threadIdx.x + (int64_t)r * nt);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[r][i] = (float)s[r][i];
         if constexpr (RES != RES_NONE) {
             float f[8] = {};
             if (on[r]) unpack8<RES == RES_BF16>(res[r], f);
@@ -316,7 +311,7 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
             if (on[r]) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    v[r][i] += f[i];
+                    v[r][i] = to_f32(s[r][i] + f[i]);
                     if constexpr (RES == RES_BF16) v[r][i] = bf16_round(v[r][i]);   // the norm is of what is stored
                 }
                 if constexpr (RES == RES_BF16) store8_bf16<AL>(a.residual_out, row + c, v[r], n[r]);
@@ -326,31 +321,43 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __fmaf_rn(v[r][i], v[r][i], ss);
     }
-    const Factor rinv = row_factor(a, ss, part64, nw);
-    float amax = 0.f;
+    const Factor rinv = row_factor(a, ss, part64[0], nw);
+    auto weights = [&](float (&f)[8], int r) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 0; r < C; ++r) {
-        float f[8] = {};
+        for (int i = 0; i < 8; ++i) f[i] = 0.f;
         if (on[r]) {
             if (a.w_bf16) unpack8<true>(wt[r], f);
             else unpack8<false>(wt[r], f);
         }
         own(f, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[r][i] = on[r] ? normed(v[r][i], rinv, f[i]) : 0.f;
-            amax = fmaxf(amax, fabsf(v[r][i]));
-        }
-    }
+    };
     float inv = 1.f;
     if (a.y_kind == NORM_ROW8) {
-        const float s = row_scale(wg_max(amax, part[1], nw));
-        if (threadIdx.x == 0) static_cast<float *>(a.y_scale)[t] = s;
-        const float rs = 1.0f / s;
+        double amax = 0.0;
 #pragma unroll
-        for (int r = 0; r < C; ++r)
+        for (int r = 0; r < C; ++r) {
+            float f[8];
+            weights(f, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[r][i] = quotient(v[r][i], s, rs);
+            for (int i = 0; i < 8; ++i) amax = fmax(amax, on[r] ? fabs((double)v[r][i] * rinv.r * (double)f[i]) : 0.0);
+        }
+        const double s = row_scale(wg_join<true>(amax, part64[2], nw)), k = rinv.r / s;
+        if (threadIdx.x == 0) static_cast<float *>(a.y_scale)[t] = (float)s;
+#pragma unroll
+        for (int r = 0; r < C; ++r) {
+            float f[8];
+            weights(f, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[r][i] = on[r] ? (float)((double)v[r][i] * k * (double)f[i]) : 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < C; ++r) {
+            float f[8];
+            weights(f, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[r][i] = on[r] ? normed(v[r][i], rinv, f[i]) : 0.f;
+        }
     }
 #pragma unroll
     for (int r = 0; r < C; ++r) {
@@ -386,35 +393,37 @@ __global__ __launch_bounds__(64) void k_norm_short(NormArgs a, int src) {
     const int64_t t = blockIdx.x, row = t * a.H;
     const int c = threadIdx.x;
     const bool on = c < a.H;
-    float v = 0.f, w = 0.f;
+    float w = 0.f;
+    double s = 0.0;
     if (on) {
         if (src == SRC_COMBINE) {
-            for (int j = 0; j < a.k; ++j) v = __fmaf_rn(a.topk_w[t * a.k + j], a.slot_out[(t * a.k + j) * a.H + c], v);
-            if (a.shared_out) v += a.shared_out[row + c];
+            for (int j = 0; j < a.k; ++j) s = fma((double)a.topk_w[t * a.k + j], (double)a.slot_out[(t * a.k + j) * a.H + c], s);
+            if (a.shared_out) s += (double)a.shared_out[row + c];
         } else {
-            v = load1(a.x, row + c, src == SRC_BF16);
+            s = (double)load1(a.x, row + c, src == SRC_BF16);
         }
         w = load1(a.weight, c, a.w_bf16);
     }
     if (src == SRC_COMBINE && a.steer_v) {
-        const float sv = on ? a.steer_v[c] : 0.f;
-        v = __fmaf_rn(-a.steer_f * wave_sum(sv * v), sv, v);
+        const double sv = on ? (double)a.steer_v[c] : 0.0;
+        s = fma(-(double)a.steer_f * wg_sum(sv * s, nullptr, 1), sv, s);
     }
+    float v = (float)s;
     if (on && a.res_kind != RES_NONE) {
-        v += load1(a.residual, row + c, a.res_kind == RES_BF16);
+        v = to_f32(s + (double)load1(a.residual, row + c, a.res_kind == RES_BF16));
         if (a.res_kind == RES_BF16) v = bf16_round(v);
         if (a.res_kind == RES_BF16) static_cast<__bf16 *>(a.residual_out)[row + c] = (__bf16)v;
         else static_cast<float *>(a.residual_out)[row + c] = v;
     }
     const Factor rinv = row_factor(a, on ? v * v : 0.f, nullptr, 1);
+    const double n = on ? (double)v * rinv.r * (double)w : 0.0;
     v = on ? normed(v, rinv, w) : 0.f;
-    const float amax = wave_max_f32(fabsf(v));
     if (a.y_kind == NORM_ROW8) {
-        const float s = row_scale(amax);
-        if (c == 0) static_cast<float *>(a.y_scale)[t] = s;
-        v = quotient(v, s, 1.0f / s);
+        const double scale = row_scale(wg_join<true>(fabs(n), nullptr, 1));
+        if (c == 0) static_cast<float *>(a.y_scale)[t] = (float)scale;
+        v = (float)(n / scale);
     } else if (a.y_kind == NORM_MX8) {
-        const int e = mx_exponent(amax);
+        const int e = mx_exponent(wave_max_f32(fabsf(v)));
         if (c == 0) static_cast<uint8_t *>(a.y_scale)[t] = (uint8_t)(e + 127);
         v *= exp2_neg(e);
     }

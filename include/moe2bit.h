@@ -413,7 +413,8 @@ moe_status moe_add_rms_norm(const void *x, int32_t x_dt, int32_t n_tokens, int32
  * opens the next block, in one launch: moe_add_rms_norm of
  *   x[t][c] = sum_{j<k} topk_w[t][j] * slot_out[t*k+j][c] (+ shared_out[t][c])
  * as in moe_combine, then steered as in moe_combine_steer when steer_v is not
- * NULL.  The combined row stays in registers (it is not written).  Arguments
+ * NULL.  The combined row stays in registers (it is not written), in binary64:
+ * x + residual is rounded once, where moe_combine rounds each addition.  Arguments
  * and errors as in those three calls; the pointers must be 4-byte aligned.
  */
 moe_status moe_combine_norm(const float *slot_out, const float *topk_w, const float *shared_out, int32_t n_tokens,

@@ -257,7 +257,7 @@ def test_combine_norm(m, T, k, H, shared, steer, res_t, y_t):
     r_out = None if res is None else torch.full_like(rd, float("nan"))
     y, ys = outputs(T, H, y_t)
     m.moe_combine_norm(od, twd, shd, rd, r_out, wd, EPS, y, ys, steer_v=svd, steer_f=0.75)
-    # the separate calls: the same fused multiply-adds, so the plain combine's residual is equal bit for bit
+    # the separate calls
     yc = torch.empty(T, H, device="cuda")
     if steer:
         m.moe_combine_steer(od, twd, shd, T, k, H, svd, 0.75, yc)
@@ -277,8 +277,9 @@ def test_combine_norm(m, T, k, H, shared, steer, res_t, y_t):
         v = v + f64(res)
         err = err + 2.0**-24 * np.abs(v) + (2.0**-8 * np.abs(v) if res_t is BF16 else 0)
         assert (np.abs(f64(r_out) - v) <= err * (1 + 1e-6)).all()
-        if not steer:
-            assert torch.equal(r_out, (yc + rd.float()).to(res_t))
+        if not steer:                                     # one rounding of the whole sum, two in bf16 (fp32 between)
+            half = 2.0**-24 if res_t is F32 else 2.0**-8 + 2.0**-24
+            assert (np.abs(f64(r_out) - v) <= half * (1 + 1e-6) * np.abs(v)).all()
         v = f64(r_out)
         err = 0 * err
     n = norm64(v, w)
