@@ -333,22 +333,22 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
     };
     float inv = 1.f;
     if (a.y_kind == NORM_ROW8) {
-        double amax = 0.0;
+        double amax = 0.0;                                   // of v * weight, which binary64 holds exactly
 #pragma unroll
         for (int r = 0; r < C; ++r) {
             float f[8];
             weights(f, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmax(amax, on[r] ? fabs((double)v[r][i] * rinv.r * (double)f[i]) : 0.0);
+            for (int i = 0; i < 8; ++i) amax = fmax(amax, on[r] ? fabs((double)v[r][i] * (double)f[i]) : 0.0);
         }
-        const double s = row_scale(wg_join<true>(amax, part64[2], nw)), k = rinv.r / s;
+        const double s = row_scale(wg_join<true>(amax, part64[2], nw) * rinv.r), k = rinv.r / s;
         if (threadIdx.x == 0) static_cast<float *>(a.y_scale)[t] = (float)s;
 #pragma unroll
         for (int r = 0; r < C; ++r) {
             float f[8];
             weights(f, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[r][i] = on[r] ? (float)((double)v[r][i] * k * (double)f[i]) : 0.f;
+            for (int i = 0; i < 8; ++i) v[r][i] = on[r] ? (float)((double)v[r][i] * (double)f[i] * k) : 0.f;
         }
     } else {
 #pragma unroll

@@ -395,11 +395,11 @@ moe_status moe_layer(const moe_layer_desc *L, const void *x, int32_t x_dt, int32
  *                (no value saturates; an all-zero block has e = -127).
  *                E4M3_ROW: scale = max(max |n|, 448 * 2^-126) / 448.  Codes are
  *                n over the scale, rounded to nearest even.
- * No other two buffers may overlap.  Sums are fp32 in an order that depends on
- * the shape alone, so a row's result does not depend on the other rows, and
+ * No other two buffers may overlap.  Sums run in an order that depends on the
+ * shape alone (squares in fp32 per thread, binary64 between the threads), so a row's result does not depend on the other rows, and
  * repeated calls give the same bits.  The sum of a row's squares must fit fp32.
- * Every hidden up to MOE_NORM_MAX_HIDDEN is taken; hidden % 8 == 0 with 16-byte
- * aligned pointers takes 16-byte loads.  Errors: MOE_ERR_INVALID_ARG (null,
+ * Every hidden up to MOE_NORM_MAX_HIDDEN is taken, with pointers aligned to
+ * their elements.  Errors: MOE_ERR_INVALID_ARG (null,
  * misaligned to its own type or overlapping buffer, bad shape or dtype, eps
  * negative or not finite), MOE_ERR_UNSUPPORTED (hidden or n_tokens above the
  * limits), MOE_ERR_DEVICE (launch failure).
