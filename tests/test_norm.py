@@ -241,7 +241,8 @@ def test_many_short_rows(m):
 # ----------------------------------------------------------------------------
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,k,H", [(1, 8, 4096), (3, 8, 512), (5, 4, 1024), (2, 1, 72), (4, 3, 100), (2, 8, 1001), (1, 16, 8192),
-                                   (2, 2, 16384), (1, 2, 32768), (1, 1, 1)])
+                                   (2, 2, 16384), (1, 2, 32768), (1, 1, 1), (3, 4, 7), (2, 6, 9), (3, 5, 63), (2, 8, 9001),
+                                   (1, 3, 32767)])
 @pytest.mark.parametrize("shared,steer,res_t,y_t", [(True, False, BF16, "bf16"), (False, False, F32, "f32"),
                                                     (True, True, F32, "block"), (False, True, None, "row")])
 def test_combine_norm(m, T, k, H, shared, steer, res_t, y_t):
