@@ -4,8 +4,7 @@
 //
 // with a = token_adapter[t] (no adapter terms where it is outside 0 .. n_adapters - 1).  All products run on the bf16
 // matrix cores with fp32 sums.  What is not bf16 by itself -- fp32 activations, the low-rank results, and h -- is carried as bf16
-// parts and multiplied part by part: three (24 bits) where the result is fp32, two (16 bits) where it is bf16, and then one of h
-// for many tokens.
+// parts and multiplied part by part: three (24 bits) where the result is fp32, two (16 bits) where it is bf16.
 // Launches: [plan] [down-rank] gate/up [down-rank] down --
 //
 //   plan       (many tokens) the tokens ordered by adapter, and work items of up to 64 tokens of one adapter
@@ -774,7 +773,7 @@ __global__ __launch_bounds__(many_threads(BW, BT)) void k_many(SharedArgs a, Pro
         // 70 us; 77 with one adapter after the other and its rank before its loads; 68 without adapters).  Rank values go 16
         // at a time, each once with each part of the tokens' low-rank results (two of which, 16 bits, beside a bf16 result).
         // An adapter's products are formed for all of the tokens, in sums of their own, and added to those of its own tokens.
-        constexpr int NP = GU ? 2 : 1, JG = FT < 2 ? FT : 2, SP = !GU && P == 1 ? 2 : 3, NA = 4;
+        constexpr int NP = GU ? 2 : 1, JG = FT < 2 ? FT : 2, SP = !GU && P < 3 ? 2 : 3, NA = 4;
 #pragma unroll
         for (int jg = 0; jg < FT; jg += JG) {
             unsigned long long left[JG];
@@ -861,12 +860,9 @@ __global__ __launch_bounds__(many_threads(BW, BT)) void k_many(SharedArgs a, Pro
                 float h[4];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) h[v] = silu_mul(acc[0][j][4 * v4 + v], acc[1][j][4 * v4 + v]);
-                *reinterpret_cast<uint2 *>(g.h + row + wr) = pack_part(h, 0);
-                if (g.hp > 1) {
 #pragma unroll
-                    for (int p = 1; p < 3; ++p)
-                        *reinterpret_cast<uint2 *>(g.h + (int64_t)p * a.T * g.N + row + wr) = pack_part(h, p);
-                }
+                for (int p = 0; p < 3; ++p)
+                    if (p < g.hp) *reinterpret_cast<uint2 *>(g.h + (int64_t)p * a.T * g.N + row + wr) = pack_part(h, p);
             }
         } else {
             const int64_t row = (int64_t)(a.sorted ? a.perm[pos] : pos) * g.N;
@@ -981,14 +977,14 @@ hipError_t launch_many(const SharedArgs &a, const Product &g, int bw, int bt, in
 template <int MODE>
 hipError_t many_tiles(const SharedArgs &a, const Product &g, int planes, int bw, int bt, int tt, int parts, hipStream_t st) {
     const int rows = MODE == MODE_GATE_UP ? bw / 2 : bw, tw = (g.N + rows - 1) / rows;
-    if (planes == 1)
-        return g.K % BK ? launch_many<MODE, 1, true>(a, g, bw, bt, tw, tt, parts, st)
-                        : launch_many<MODE, 1, false>(a, g, bw, bt, tw, tt, parts, st);
     if constexpr (MODE != MODE_DOWN) {
-        if (planes == 2)
-            return g.K % BK ? launch_many<MODE, 2, true>(a, g, bw, bt, tw, tt, parts, st)
-                            : launch_many<MODE, 2, false>(a, g, bw, bt, tw, tt, parts, st);
+        if (planes == 1)
+            return g.K % BK ? launch_many<MODE, 1, true>(a, g, bw, bt, tw, tt, parts, st)
+                            : launch_many<MODE, 1, false>(a, g, bw, bt, tw, tt, parts, st);
     }
+    if (planes == 2)
+        return g.K % BK ? launch_many<MODE, 2, true>(a, g, bw, bt, tw, tt, parts, st)
+                        : launch_many<MODE, 2, false>(a, g, bw, bt, tw, tt, parts, st);
     return g.K % BK ? launch_many<MODE, 3, true>(a, g, bw, bt, tw, tt, parts, st)
                     : launch_many<MODE, 3, false>(a, g, bw, bt, tw, tt, parts, st);
 }
@@ -1096,11 +1092,11 @@ size_t shared_workspace(int T, int H, int Is, int n, int R) {
 
 hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     char *base = static_cast<char *>(ws);
-    // bf16 parts of x and h.  Beside a bf16 result 16 bits are enough; for many tokens h then has one part, whose rounding is as
-    // large as the result's own (together 1.4 times that), because a second one would double the down product: 45 us of 2048
-    // tokens' 143 at 4096 x 2048.  For few tokens it hides behind the weights.
+    // bf16 parts of x and h.  Beside a bf16 result 16 bits are enough: what they leave is 2^-8 of its own rounding.  One part of h
+    // would not be, though it halves the down product: its rounding is as large as the result's (2048 tokens of 4096 x 2048, error
+    // against binary64 2.35e-3 with one part, 1.66e-3 with two, which is that of one rounding).
     const bool small = few_path(a.T, a.H, a.Is);
-    const int xp = a.x_bf16 ? 1 : a.out_bf16 ? 2 : 3, hp = !a.out_bf16 ? 3 : small ? 2 : 1;
+    const int xp = a.x_bf16 ? 1 : a.out_bf16 ? 2 : 3, hp = a.out_bf16 ? 2 : 3;
     const Layout l = layout(a.T, a.H, a.Is, a.n, a.R, xp, hp);
     auto u16 = [&](size_t at) { return reinterpret_cast<uint16_t *>(base + at); };
     uint16_t *s = u16(l.s), *h = u16(l.h);

@@ -468,7 +468,7 @@ size_t moe_shared_ffn_workspace(const moe_layer_desc *L, const moe_adapter_desc 
  * Sums are fp32 in an order fixed by the shapes.  With an fp32 out, fp32
  * activations, the low-rank products A[a] x and the SwiGLU result h are carried
  * with all 24 bits (three bf16 parts); with a bf16 out, with 16 bits (two
- * parts), and h of large calls (never of 64 tokens or fewer) as one bf16 value.
+ * parts).
  * Values that round to infinity in bf16 (3.396e38 and above) give NaN.
  * A token's result has the same bits whatever other tokens and adapters the
  * call holds (at the same n_tokens and n_adapters), and non-finite values in
