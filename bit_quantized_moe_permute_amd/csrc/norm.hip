@@ -4,8 +4,7 @@
 //   n = v / sqrt(sum v^2 / H + eps) * weight,  y = round(n)
 //
 // y is bf16, fp32, or e4m3: with one power-of-two scale per 32 columns (the block format that the scaled matrix
-// instructions of gfx950 read) or one fp32 scale per row.  All sums are in an order fixed per launch shape: a row's
-// squares in fp32 per thread and binary64 between them, combined rows in binary64.
+// instructions of gfx950 read) or one fp32 scale per row.  All sums are in binary64, in an order fixed per launch shape.
 //
 // Bound: HBM traffic for many rows, one memory round trip and two barriers for few.  One workgroup holds one row in
 // registers, so every input is read once: all loads of a row (source, residual, weight) are issued before the first
@@ -54,20 +53,25 @@ template <bool MAX> __device__ __forceinline__ double wg_join(double d, double *
 }
 __device__ __forceinline__ double wg_sum(double d, double *part, int nw) { return wg_join<false>(d, part, nw); }
 
-// 1 / sqrt(sum / H + eps) in two fp32 parts, from the threads' fp32 sums of squares.  The row's one factor moves all of its
+// 1 / sqrt(sum / H + eps) in two fp32 parts, from the threads' binary64 sums of squares.  The row's one factor moves all of its
 // columns the same way, and where y is e4m3 an error in it decides blocks' scales and values that lie next to a rounding's
-// border: so the sums meet in binary64, and the square root is taken there (the instruction's estimate and one Newton step).
-// It costs no time: 11709 x 4096 61.2 us with and without, one row 6.3.  Combined rows in binary64 neither (2048 x 8 x 4096
-// 66.2 and 66.3 us), a row's scale and the quotients by it little (1469 x 4096 14.7 and 15.1).  8-bit outputs are the exact
-// ones' (of 25 random calls none had a differing code, where fp32 sums had up to 226).
-struct Factor { float hi, lo; double r; };
-__device__ __forceinline__ Factor row_factor(const NormArgs &a, float ss, double *part, int nw) {
-    const double m = fma(wg_sum((double)ss, part, nw), a.inv_hidden, (double)a.eps), r0 = __builtin_amdgcn_rsq(m);
+// border; and fp32 holds the squares of half of its own exponents only.  The square root is taken in binary64 too (the
+// instruction's estimate and one Newton step).  Whole calls with fp32 squares per thread and with binary64 ones: 11709 x 4096 60.6 and
+// 61.1 us, 1469 x 4096 15.0 and 15.1, one row the same.  Combined rows in binary64 cost nothing (2048 x 8 x 4096 66.2 and 66.3
+// us), a row's scale and the quotients by it little (1469 x 4096 14.7 and 15.1).  What is left is n's one rounding to fp32.
+struct Factor { float hi, lo; double r; int exp; };
+__device__ __forceinline__ Factor row_factor(const NormArgs &a, double ss, double *part, int nw) {
+    const double m = fma(wg_sum(ss, part, nw), a.inv_hidden, (double)a.eps), r0 = __builtin_amdgcn_rsq(m);
     const double r = m == HUGE_VAL ? 0.0 : fma(0.5 * r0, fma(-m * r0, r0, 1.0), r0);
-    const float hi = (float)r;
-    return {hi, (float)(r - (double)hi), r};
+    // Beside values near the ends of fp32 the factor is beyond it, or its low part is: then the values are multiplied by 2^exp
+    // first, exactly, and the factor is near 1
+    const bool far = r > 0x1p60 ? r < HUGE_VAL : r < 0x1p-60 && r > 0.0;
+    const int e = __builtin_amdgcn_readfirstlane(far ? ilogb(r) : 0);        // the same for the whole row
+    const double q = ldexp(r, -e);
+    const float hi = (float)q;
+    return {hi, (float)(q - (double)hi), r, e};
 }
-// v * factor * w, off by little more than its one rounding
+// v * factor * w, off by little more than its one rounding; v has been brought to the factor's 2^-exp
 __device__ __forceinline__ float normed(float v, const Factor &r, float w) {
     const float hi = v * r.hi;
     const float lo = __fmaf_rn(v, r.lo, __fmaf_rn(v, r.hi, -hi));
@@ -298,7 +302,7 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
             own(s[r], r);
         }
     }
-    float ss = 0.f;
+    double ss = 0.0;                                         // a square of fp32 is exact in binary64, however small or large
 #pragma unroll
     for (int r = 0; r < C; ++r) {
         const int64_t c = 8 * ((int64_t)threadIdx.x + (int64_t)r * nt);
@@ -319,7 +323,10 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = __fmaf_rn(v[r][i], v[r][i], ss);
+        for (int i = 0; i < 8; ++i) {
+            ss = fma((double)v[r][i], (double)v[r][i], ss);
+            asm("" : "+v"(v[r][i]));                         // from here on v is fp32 again: its binary64 form is not kept
+        }
     }
     const Factor rinv = row_factor(a, ss, part64[0], nw);
     auto weights = [&](float (&f)[8], int r) __attribute__((always_inline)) {
@@ -351,6 +358,12 @@ __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
             for (int i = 0; i < 8; ++i) v[r][i] = on[r] ? (float)((double)v[r][i] * (double)f[i] * k) : 0.f;
         }
     } else {
+        if (rinv.exp) {
+#pragma unroll
+            for (int r = 0; r < C; ++r)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[r][i] = ldexpf(v[r][i], rinv.exp);
+        }
 #pragma unroll
         for (int r = 0; r < C; ++r) {
             float f[8];
@@ -415,9 +428,9 @@ __global__ __launch_bounds__(64) void k_norm_short(NormArgs a, int src) {
         if (a.res_kind == RES_BF16) static_cast<__bf16 *>(a.residual_out)[row + c] = (__bf16)v;
         else static_cast<float *>(a.residual_out)[row + c] = v;
     }
-    const Factor rinv = row_factor(a, on ? v * v : 0.f, nullptr, 1);
+    const Factor rinv = row_factor(a, on ? (double)v * (double)v : 0.0, nullptr, 1);
     const double n = on ? (double)v * rinv.r * (double)w : 0.0;
-    v = on ? normed(v, rinv, w) : 0.f;
+    v = on ? normed(ldexpf(v, rinv.exp), rinv, w) : 0.f;
     if (a.y_kind == NORM_ROW8) {
         const double scale = row_scale(wg_join<true>(fabs(n), nullptr, 1));
         if (c == 0) static_cast<float *>(a.y_scale)[t] = (float)scale;

@@ -394,15 +394,16 @@ moe_status moe_layer(const moe_layer_desc *L, const void *x, int32_t x_dt, int32
  *                the least with max |n| <= 448 * 2^e, clamped to [-127, 127]
  *                (no value saturates; an all-zero block has e = -127).
  *                E4M3_ROW: scale = max(max |n|, 448 * 2^-126) / 448.  Codes are
- *                n over the scale, rounded to nearest even.
- * No other two buffers may overlap.  Sums run in an order that depends on the
- * shape alone (squares in fp32 per thread, binary64 between the threads), so a row's result does not depend on the other rows, and
- * repeated calls give the same bits.  The sum of a row's squares must fit fp32.
- * Every hidden up to MOE_NORM_MAX_HIDDEN is taken, with pointers aligned to
- * their elements.  Errors: MOE_ERR_INVALID_ARG (null,
- * misaligned to its own type or overlapping buffer, bad shape or dtype, eps
- * negative or not finite), MOE_ERR_UNSUPPORTED (hidden or n_tokens above the
- * limits), MOE_ERR_DEVICE (launch failure).
+ *                n over the scale, in fp32, rounded to nearest even.
+ * No other two buffers may overlap.  Sums are in binary64, in an order that
+ * depends on the shape alone, so a row's result does not depend on the other
+ * rows, and repeated calls give the same bits.  Rows of any finite values are
+ * taken, however small or large their squares (with eps = 0 an all-zero row is
+ * 0 / 0, NaN).  Every hidden up to MOE_NORM_MAX_HIDDEN is taken, with pointers
+ * aligned to their elements.  Errors: MOE_ERR_INVALID_ARG (null, misaligned to
+ * its own type or overlapping buffer, bad shape or dtype, eps negative or not
+ * finite), MOE_ERR_UNSUPPORTED (hidden or n_tokens above the limits),
+ * MOE_ERR_DEVICE (launch failure).
  */
 moe_status moe_add_rms_norm(const void *x, int32_t x_dt, int32_t n_tokens, int32_t hidden, const void *residual,
                             void *residual_out, int32_t res_dt, const void *weight, int32_t w_dt, float eps, void *y,
