@@ -13,7 +13,7 @@ import torch
 from . import (FMT_IQ2X, PATH_AUTO, PRECISION_EXACT, AdapterDesc, LayerDesc, moe_add_rms_norm, moe_combine,
                moe_combine_norm, moe_combine_steer, moe_expert_ffn, moe_expert_ffn_workspace, moe_layer,
                moe_layer_workspace, moe_prepare_weights, moe_route, moe_route_workspace, moe_shared_ffn,
-               moe_shared_ffn_workspace, moe_weight_bytes)
+               moe_shared_ffn_workspace, moe_weight_bytes, _norm_output)
 
 
 def _u8(a: np.ndarray, device) -> torch.Tensor:
@@ -213,20 +213,30 @@ class LayerBuffers:
         )
 
 
+def _check_adapters(L: DeviceLayer, b: LayerBuffers, token_adapter):
+    if token_adapter is None:
+        return
+    if L.adapters is None:
+        raise ValueError("token_adapter given, but the layer has no adapters (set_adapters)")
+    if token_adapter.dtype != torch.int32:
+        raise TypeError("token_adapter must be an int32 tensor")
+    if token_adapter.numel() < b.T:
+        raise ValueError(f"token_adapter: {token_adapter.numel()} elements, the call needs {b.T}")
+    if b.ws_shared is None:
+        raise ValueError("these buffers were allocated before the layer had adapters")
+    if b.ws_shared.numel() < moe_shared_ffn_workspace(L.desc, b.T, L.adapters):
+        raise ValueError("these buffers were allocated before the layer had these adapters")
+
+
 def _route_and_experts(L: DeviceLayer, x, b: LayerBuffers, desc, token_adapter, stream):
     """moe_route and the experts: b.slot_out and b.shared_out.  With adapters and token_adapter the shared expert runs
     as a call of its own."""
-    assert x.shape[0] == b.T
     moe_route(x, L.w_router, L.E, L.k, b.topk_idx, b.topk_w, b.offsets, b.perm, b.active, b.ws_route, bias=L.bias,
               logits=b.logits, stream=stream)
     if token_adapter is None:
         moe_expert_ffn(desc or L.desc, x, b.topk_idx, b.offsets, b.perm, b.active, b.slot_out, b.shared_out, b.ws_ffn,
                        stream=stream)
         return
-    if L.adapters is None:
-        raise ValueError("token_adapter given, but the layer has no adapters (set_adapters)")
-    if b.ws_shared is None:
-        raise ValueError("these buffers were allocated before the layer had adapters")
     moe_expert_ffn(L.routed_desc(desc), x, b.topk_idx, b.offsets, b.perm, b.active, b.slot_out, None, b.ws_ffn,
                    stream=stream)
     moe_shared_ffn(L.desc, x, b.shared_out, b.ws_shared, L.adapters, token_adapter, stream=stream)
@@ -238,7 +248,12 @@ def forward_block(L: DeviceLayer, x: torch.Tensor, residual: torch.Tensor, w_in:
 
         residual += x;  xn = norm(residual) * w_in;  residual += layer(xn);  y = norm(residual) * w_out
 
-    x [T][H] fp32 or bf16 (the attention's output), y in any type of moe_add_rms_norm."""
+    x [T][H] fp32 or bf16 (the attention's output) with the T of the buffers b, y in any type of moe_add_rms_norm.  A call
+    that is refused for its shapes, types or adapters leaves the residual as it was."""
+    if tuple(x.shape) != (b.T, L.H):
+        raise ValueError(f"x has shape {tuple(x.shape)}, the buffers and the layer take {(b.T, L.H)}")
+    _check_adapters(L, b, token_adapter)
+    _norm_output(x.get_device(), b.T, L.H, residual, residual, w_out, y, y_scale)
     moe_add_rms_norm(x, residual, residual, w_in, eps, b.xn, stream=stream)
     _route_and_experts(L, b.xn, b, None, token_adapter, stream)
     moe_combine_norm(b.slot_out, b.topk_w, b.shared_out, residual, residual, w_out, eps, y, y_scale,
@@ -251,6 +266,8 @@ def forward(L: DeviceLayer, x: torch.Tensor, b: LayerBuffers, desc: LayerDesc | 
     """route -> expert FFN -> combine (+ steering, when the layer has a direction) for x [T][H] (bf16 or fp32)
     into b.y.  token_adapter (int32 [T]): each token's adapter of the shared expert (L.set_adapters)."""
     T = x.shape[0]
+    assert T == b.T
+    _check_adapters(L, b, token_adapter)
     _route_and_experts(L, x, b, desc, token_adapter, stream)
     if L.steer_v is None:
         moe_combine(b.slot_out, b.topk_w, b.shared_out, T, L.k, L.H, b.y, stream=stream)
