@@ -10,6 +10,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "../../include/moe2bit.h"
 #include "internal.h"
@@ -627,6 +628,17 @@ moe_status moe_shared_ffn(const moe_layer_desc *L, const moe_adapter_desc *A, co
     if (overlap(out, ob, x, xb) || overlap(ws, need, x, xb) || overlap(ws, need, out, ob) ||
         overlap(out, ob, token_adapter, ib) || overlap(ws, need, token_adapter, ib))
         return fail(MOE_ERR_INVALID_ARG, "%s: out or ws overlaps another buffer", fn);
+    const size_t H = (size_t)L->hidden, Is = (size_t)L->shared_inter, wb = 2 * H * Is;
+    const size_t an = A ? 2 * (size_t)A->n_adapters * A->max_rank : 0, sb = A ? 4 * (size_t)A->n_adapters : 0;
+    const std::pair<const void *, size_t> weights[] = {
+        {L->shared_gate, wb}, {L->shared_up, wb}, {L->shared_down, wb},
+        {A ? A->gate_a : nullptr, an * H}, {A ? A->gate_b : nullptr, an * Is},
+        {A ? A->up_a : nullptr, an * H}, {A ? A->up_b : nullptr, an * Is},
+        {A ? A->down_a : nullptr, an * Is}, {A ? A->down_b : nullptr, an * H},
+        {A ? A->rank : nullptr, sb}, {A ? A->scale : nullptr, sb}};
+    for (const auto &w : weights)
+        if (overlap(out, ob, w.first, w.second) || overlap(ws, need, w.first, w.second))
+            return fail(MOE_ERR_INVALID_ARG, "%s: out or ws overlaps the layer's or the adapters' weights", fn);
     moe::SharedArgs a;
     memset(&a, 0, sizeof a);
     a.T = n_tokens; a.H = L->hidden; a.Is = L->shared_inter;

@@ -475,8 +475,9 @@ size_t moe_shared_ffn_workspace(const moe_layer_desc *L, const moe_adapter_desc 
  * call holds (at the same n_tokens and n_adapters), and non-finite values in
  * one adapter or token reach only the tokens that use it.
  * hidden and shared_inter must be multiples of 8; x, out and the weights 16-byte
- * aligned.  Errors: MOE_ERR_INVALID_ARG (null, misaligned or overlapping
- * pointer, bad shape or dtype, workspace too small), MOE_ERR_UNSUPPORTED (hidden
+ * aligned; out and ws must not overlap each other or anything that is read.
+ * Errors: MOE_ERR_INVALID_ARG (null, misaligned or overlapping pointer, bad
+ * shape or dtype, workspace too small), MOE_ERR_UNSUPPORTED (hidden
  * or shared_inter above MOE_SHARED_MAX_DIM, n_tokens above MOE_MAX_TOKENS, or
  * n_tokens times the larger dimension 2^30 or more), MOE_ERR_DEVICE (launch
  * failure).
