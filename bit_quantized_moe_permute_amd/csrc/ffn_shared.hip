@@ -1067,10 +1067,9 @@ Layout layout(int T, int H, int Is, int n, int R, int xp, int hp) {
             l.ad = take((size_t)T * 4);
             l.items = take((size_t)plan_items(T, n) * 16);
             l.n_items = take(4);
-            // parts * T of the down-rank products of T or fewer tokens: MAX_PARTS parts at most, and more than one only where
-            // parts / 2 times T / 64 items are below 256 workgroups
-            const size_t some = std::min<size_t>((size_t)MAX_PARTS * T, 512 * 64 + MAX_PARTS * 64);
-            l.part = take(std::max<size_t>(T, some) * 2 * R * 4);
+            // parts * T of the down-rank products of T or fewer tokens: MAX_PARTS parts at most, and more than one (a single part
+            // writes its results at once) only where parts / 2 times more than T / ITEM_TOKENS items are below 256 workgroups
+            l.part = take(std::min<size_t>((size_t)MAX_PARTS * T, 2 * 256 * ITEM_TOKENS) * 2 * R * 4);
         }
     }
     l.total = o;
