@@ -185,7 +185,7 @@ class LayerBuffers:
     y: torch.Tensor
     ws: torch.Tensor            # one buffer: ws_route and ws_ffn are views into it (the layout moe_layer takes)
     ws_shared: torch.Tensor | None = None       # moe_shared_ffn's, when the layer has adapters
-    xn: torch.Tensor | None = None              # the normed rows forward_block() hands to the layer
+    xn: torch.Tensor | None = None              # the normed rows forward_block() hands to the layer, from its first call on
 
     @classmethod
     def allocate(cls, L: DeviceLayer, T: int, with_logits: bool = False) -> "LayerBuffers":
@@ -209,8 +209,18 @@ class LayerBuffers:
             y=torch.empty(T, L.H, **f32),
             ws=ws,
             ws_shared=torch.empty(ws_s, dtype=torch.uint8, device=dev) if ws_s else None,
-            xn=torch.empty(T, L.H, dtype=torch.bfloat16, device=dev),
         )
+
+    def block_rows(self, L: DeviceLayer, stream=None) -> torch.Tensor:
+        """xn, allocated on the stream that writes it first (the memory may have been in use there before)."""
+        if self.xn is None:
+            shape = dict(size=(self.T, L.H), dtype=torch.bfloat16, device=L.device)
+            if stream is None:
+                self.xn = torch.empty(**shape)
+            else:
+                with torch.cuda.stream(torch.cuda.ExternalStream(stream)):
+                    self.xn = torch.empty(**shape)
+        return self.xn
 
 
 def _check_adapters(L: DeviceLayer, b: LayerBuffers, token_adapter):
@@ -254,8 +264,9 @@ def forward_block(L: DeviceLayer, x: torch.Tensor, residual: torch.Tensor, w_in:
         raise ValueError(f"x has shape {tuple(x.shape)}, the buffers and the layer take {(b.T, L.H)}")
     _check_adapters(L, b, token_adapter)
     _norm_output(x.get_device(), b.T, L.H, residual, residual, w_out, y, y_scale)
-    moe_add_rms_norm(x, residual, residual, w_in, eps, b.xn, stream=stream)
-    _route_and_experts(L, b.xn, b, None, token_adapter, stream)
+    xn = b.block_rows(L, stream)
+    moe_add_rms_norm(x, residual, residual, w_in, eps, xn, stream=stream)
+    _route_and_experts(L, xn, b, None, token_adapter, stream)
     moe_combine_norm(b.slot_out, b.topk_w, b.shared_out, residual, residual, w_out, eps, y, y_scale,
                      steer_v=L.steer_v, steer_f=L.steer_f, stream=stream)
     return y

@@ -17,7 +17,8 @@ def refused_call(**change):
     from bit_quantized_moe_permute_amd.layer import forward_block
     T, H = 4, 64
     L = SimpleNamespace(H=H, Is=32, adapters=None, steer_v=None, steer_f=0.0, desc=None)
-    b = SimpleNamespace(T=T, xn=torch.empty(T, H, dtype=BF16), ws_shared=None)
+    rows = torch.empty(T, H, dtype=BF16)
+    b = SimpleNamespace(T=T, xn=rows, ws_shared=None, block_rows=lambda *_: rows)
     a = dict(x=torch.zeros(T, H), residual=torch.zeros(T, H), w_in=torch.ones(H), w_out=torch.ones(H), y=torch.zeros(T, H),
              y_scale=None, token_adapter=None)
     a.update(change)
@@ -81,3 +82,51 @@ def test_a_refused_block_leaves_the_residual(m):  # noqa: F811
     refused(ValueError, ids=ids[:4], b=b2)
     DL.set_adapters(Case(T, H, DL.Is, 40, 256, seed=1).on_gpu(m)[2])
     refused(ValueError, ids=ids, b=b2)                    # buffers for smaller adapters
+
+
+@pytest.mark.gpu
+def test_rows_are_allocated_for_blocks_alone(m):  # noqa: F811
+    """Buffers take no memory for forward_block's rows before its first call, on torch's stream, a named one and under capture."""
+    from bit_quantized_moe_permute_amd.layer import LayerBuffers, forward, forward_block
+    note("rows of a block")
+    T = 6
+    DL, _, _ = layer(m, T)
+    H, w = DL.H, torch.ones(DL.H, device="cuda")
+    x, r, y = torch.randn(T, H, device="cuda"), torch.randn(T, H, device="cuda"), torch.empty(T, H, device="cuda")
+    want_r, want = r.clone(), torch.empty_like(y)
+    b = LayerBuffers.allocate(DL, T)
+    forward(DL, x.to(BF16), b)
+    assert b.xn is None
+    forward_block(DL, x, want_r, w, w, 1e-6, b, want)
+    rows = b.xn
+    forward_block(DL, x, r.clone(), w, w, 1e-6, b, y)
+    torch.cuda.synchronize()
+    assert b.xn is rows and rows.shape == (T, H) and torch.equal(y, want)
+    side = torch.cuda.Stream()
+    for stream in (side.cuda_stream, torch.cuda.default_stream().cuda_stream):
+        b, r2 = LayerBuffers.allocate(DL, T), r.clone()
+        y.fill_(0)
+        torch.cuda.synchronize()
+        forward_block(DL, x, r2, w, w, 1e-6, b, y, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(r2, want_r)
+    b, r2 = LayerBuffers.allocate(DL, T), r.clone()
+    torch.cuda.synchronize()
+    g, cap = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(cap):
+        with torch.cuda.graph(g, stream=cap):
+            forward_block(DL, x, r2, w, w, 1e-6, b, y)
+    for _ in range(3):
+        r2.copy_(r)
+        y.fill_(0)
+        junk = torch.full((64, H), float("nan"), device="cuda")
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(r2, want_r)
+        del junk
+    xn = b.xn.clone()
+    del g
+    r3 = r.clone()
+    forward_block(DL, x, r3, w, w, 1e-6, b, y.fill_(0))      # the rows outlive the graph
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(b.xn, xn)
