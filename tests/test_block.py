@@ -5,6 +5,8 @@ import numpy as np
 import pytest
 import torch
 
+from test_norm import f64, outputs
+from test_norm_precision import HALF, check, exact_norm
 from test_shared_ffn import BF16, F32, LIB, Case, m, needs_lib, note  # noqa: F401
 
 
@@ -130,3 +132,80 @@ def test_rows_are_allocated_for_blocks_alone(m):  # noqa: F811
     forward_block(DL, x, r3, w, w, 1e-6, b, y.fill_(0))      # the rows outlive the graph
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(b.xn, xn)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 7, 90])
+@pytest.mark.parametrize("res_t,w_t,y_t", [(BF16, BF16, "bf16"), (BF16, F32, "block"), (F32, BF16, "row"), (BF16, BF16, "f32")])
+@pytest.mark.parametrize("adapters", [False, True])
+def test_block_types(m, T, res_t, w_t, y_t, adapters):  # noqa: F811
+    """A bf16 residual stream and outputs of every type, against the oracle and binary64: the first norm and the last one
+    within their roundings of what is stored, the layer between them within its 1e-3 per token, the residual's rounding added."""
+    import oracle
+    from bit_quantized_moe_permute_amd.layer import LayerBuffers, forward_block
+    note(f"block T={T} residual={res_t} weights={w_t} y={y_t} adapters={adapters}")
+    DL, L, c = layer(m, T)
+    sp, H = L.spec, DL.H
+    ids = None
+    if adapters:
+        _, _, pool, ids = c.on_gpu(m)
+        DL.set_adapters(pool)
+    else:
+        c.n = 0
+    rng = np.random.default_rng(6)
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).to(BF16)
+    res = torch.from_numpy(2 * rng.standard_normal((T, H)).astype(np.float32)).to(res_t)
+    w_in, w_out = (torch.from_numpy((1 + 0.1 * rng.standard_normal(H)).astype(np.float32)).to(w_t) for _ in range(2))
+    b = LayerBuffers.allocate(DL, T)
+    r = res.cuda()
+    y, ys = outputs(T, H, y_t)
+    forward_block(DL, x.cuda(), r, w_in.cuda(), w_out.cuda(), 1e-6, b, y, ys, token_adapter=ids)
+    torch.cuda.synchronize()
+    r1 = f64((x.float() + res.float()).to(res_t))
+    check(b.xn, None, exact_norm(r1, w_in, 1e-6))
+    xn = b.xn.cpu()
+    ref = oracle.layer(xn.view(torch.int16).numpy().view(np.uint16), L.w_router, sp.top_k, sp.n_experts, sp.inter, sp.gate_up_fmt,
+                       L.gate, L.up, sp.down_fmt, L.down, L.codebook, shared=L.shared)
+    c.x = xn
+    out = ref["y"] - ref["shared_out"] + c.reference()[0].numpy()
+    r2 = r1 + out
+    norm = lambda v: np.linalg.norm(v, axis=1)  # noqa: E731
+    half = HALF if res_t is F32 else 2.0**-8 + HALF
+    assert (norm(f64(r) - r2) <= 1.01e-3 * norm(out) + half * norm(r2)).all()
+    check(y, ys, exact_norm(f64(r), w_out, 1e-6))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 7, 300])
+def test_block_replays(m, T):  # noqa: F811
+    """A captured block with adapters on a bf16 residual stream, replayed on changed rows and adapters, eager blocks between."""
+    from bit_quantized_moe_permute_amd.layer import LayerBuffers, forward_block
+    note(f"block graph T={T}")
+    DL, _, c = layer(m, T)
+    H = DL.H
+    _, _, pool, ids = c.on_gpu(m)
+    DL.set_adapters(pool)
+    w = torch.ones(H, device="cuda")
+    x, r = torch.randn(T, H, device="cuda").to(BF16), torch.zeros(T, H, dtype=BF16, device="cuda")
+    (y, ys), (want, want_s) = outputs(T, H, "block"), outputs(T, H, "block")
+    b, b2 = LayerBuffers.allocate(DL, T), LayerBuffers.allocate(DL, T)
+    forward_block(DL, x, r, w, w, 1e-6, b, y, ys, token_adapter=ids)
+    torch.cuda.synchronize()
+    g, cap = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    cap.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(cap):
+        with torch.cuda.graph(g, stream=cap):
+            forward_block(DL, x, r, w, w, 1e-6, b, y, ys, token_adapter=ids)
+    for i in range(4):
+        gen = torch.Generator().manual_seed(90 + i)
+        x.copy_(torch.randn(T, H, generator=gen))
+        r.copy_(torch.randn(T, H, generator=gen))
+        ids.copy_(torch.randint(-1, 6, (T,), generator=gen))
+        r2 = r.clone()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        forward_block(DL, x, r2, w, w, 1e-6, b2, want, want_s, token_adapter=ids)
+        torch.cuda.synchronize()
+        assert torch.equal(r, r2) and torch.equal(ys, want_s), i
+        assert torch.equal(y.view(torch.uint8), want.view(torch.uint8)), i
