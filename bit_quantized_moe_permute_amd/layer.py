@@ -249,7 +249,7 @@ def _route_and_experts(L: DeviceLayer, x, b: LayerBuffers, desc, token_adapter, 
         return
     moe_expert_ffn(L.routed_desc(desc), x, b.topk_idx, b.offsets, b.perm, b.active, b.slot_out, None, b.ws_ffn,
                    stream=stream)
-    moe_shared_ffn(L.desc, x, b.shared_out, b.ws_shared, L.adapters, token_adapter, stream=stream)
+    moe_shared_ffn(desc or L.desc, x, b.shared_out, b.ws_shared, L.adapters, token_adapter, stream=stream)
 
 
 def forward_block(L: DeviceLayer, x: torch.Tensor, residual: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor,

@@ -209,3 +209,25 @@ def test_block_replays(m, T):  # noqa: F811
         torch.cuda.synchronize()
         assert torch.equal(r, r2) and torch.equal(ys, want_s), i
         assert torch.equal(y.view(torch.uint8), want.view(torch.uint8)), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 70])
+def test_forward_takes_the_description_it_is_given(m, T):  # noqa: F811
+    """Another description's shared weights (here gate and up exchanged) are those that tokens with adapters use too: without
+    an adapter among the tokens the layer is the same as without token_adapter, within both calls' errors."""
+    from bit_quantized_moe_permute_amd.layer import LayerBuffers, forward
+    note(f"description T={T}")
+    DL, _, c = layer(m, T)
+    DL.set_adapters(c.on_gpu(m)[2])
+    x = c.x.cuda()
+    none = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    b = LayerBuffers.allocate(DL, T)
+    other = DL.make_desc()
+    other.shared_gate, other.shared_up = other.shared_up, other.shared_gate
+    for desc in (None, DL.make_desc(), other):
+        want = forward(DL, x, b, desc).clone()
+        got = forward(DL, x, b, desc, token_adapter=none)
+        torch.cuda.synchronize()
+        err = torch.linalg.vector_norm(got - want, dim=1) / torch.linalg.vector_norm(want, dim=1)
+        assert float(err.max()) <= 2.0**-15, float(err.max())
