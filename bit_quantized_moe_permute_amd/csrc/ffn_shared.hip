@@ -16,12 +16,14 @@
 // one request's adapter (not even a NaN) reaches another request.
 //
 // Bound: the weights' bytes for few tokens, the matrix cores and the tiles' way into LDS for many.  hidden 4096, inter 2048,
-// kernels alone, fp32 out below 2048 tokens (a copy reaches 4.97 TB/s on this chip, a 2048 x 4096 x 4096 library product 62 us):
-//   1 token, rank 16:     inputs 3.8 us, gate/up 11.1 (33.6 MB, 3.0 TB/s), down 9.5 (16.9 MB, 1.8 TB/s)
-//   24 requests, rank 64: inputs 6.9, gate/up 15.9, inputs 4.3, down 12.5 (together 100 MB in 37.5 us, 2.7 TB/s)
-//   512 tokens, rank 16:  plan 4.8, down-rank 6.3 + 6.0, gate/up 29 (0.6 PFLOP/s), down-rank 6.7 + 6.2, down 29 (three planes:
-//                         0.9 PFLOP/s)
-//   2048 tokens, rank 16, bf16 out: plan 5.8, down-rank 9.1 + 6.0, gate/up 70 (1.0 PFLOP/s), down-rank 6.6 + 6.0, down 45 (0.8)
+// kernels alone, medians (a copy reaches 4.85 to 4.97 TB/s on this chip, a 2048 x 4096 x 4096 library product takes 62 us):
+//   1 token, rank 16:     inputs 3.8 us, gate/up 10.6 (33.6 MB, 3.2 TB/s), down 9.3 (16.9 MB, 1.8 TB/s)
+//   24 requests, rank 64: inputs 7.3, gate/up 15.2, inputs 4.8, down 11.8 (together 100 MB in 39.1 us, 2.6 TB/s)
+//   512 tokens, rank 16, fp32 out: plan 4.8, down-rank 6.6 + 6.0, gate/up 29 to 38 from run to run (0.45 to 0.6 PFLOP/s),
+//                         down-rank 6.8 + 6.2, down 29 (three planes: 0.9 PFLOP/s)
+//   2048 tokens, rank 32, bf16 out: plan 6.2, down-rank 11 + 6.6, gate/up 81 to 87 (0.8 PFLOP/s), down-rank 9.4 + 6.4, down 81
+//                         to 87 (two planes: 0.8)
+//   the same, fp32 out:   down-rank 13 + 6.1, down 135 (three planes: 0.8), the others as before
 #include <algorithm>
 
 #include "common.h"
@@ -298,23 +300,25 @@ __global__ __launch_bounds__(256) void k_few_inputs(SharedArgs a, LowRank L, uin
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens, a product: one workgroup streams 16 weight rows (gate/up: 8 gate rows and the same 8 of up) once.  Its waves
-// split K: in each round of 2048 a wave takes 256 of every row, through LDS of its own that direct-to-LDS loads fill with
-// 512-byte pieces of rows (two rounds in flight: 128 KiB per workgroup, what a copy's rate times the memory's latency asks of
-// a compute unit; 16 rows, so that 4096 x 2048 makes 256 workgroups).  Chunk c of row r lies at position
-// c ^ r, so that sixteen rows' reads of one chunk column touch every bank once.  The waves' sums meet in LDS.
-// An adapter's term is formed per token in fp32, wave w taking tokens w, w + NW, ...; its loads go out with the weights'.
+// Few tokens, a product: one workgroup streams 16 weight rows (gate/up: 8 gate rows and the same 8 of up) once. Its waves split
+// K: in each round of 2048 a wave takes 256 of every row, through LDS of its own that direct-to-LDS loads fill with 512-byte
+// pieces of rows. The first two rounds are issued together (128 KiB per workgroup, what a copy's rate times the memory's
+// latency asks of a compute unit; 16 rows, so that 4096 x 2048 makes 256 workgroups). From then on the second buffer hides
+// little: a round's activations are loaded behind the next round's weights, and one wait stands for both. Chunk c of row r lies
+// at position c ^ r, so that sixteen rows' reads of one chunk column touch every bank once. The waves' sums meet in LDS. An
+// adapter's term is formed per token in fp32, wave w taking tokens w, w + NW, ...; its loads go out with the weights'.
 // ---------------------------------------------------------------------------
 constexpr int FEW_WAVES = 8;
 
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// AD: the adapters' low-rank results are read (AD_READ), or (AD_HERE, down, few values) formed by every workgroup from the rows of
-// h while its weights are on their way: that reads A out of the caches in every workgroup, where a launch between the two products
-// costs 4 us.  fp32 result, a launch against here, whole calls: 16 values of 512 16.4 and 14.2 us, of 2048 (1 token, rank 16,
-// hidden 4096) 24.4 and 22.8, of 4096 38.6 and 37.2; 32 values of 512 16.3 and 15.0, of 2048 24.6 and 24.5; 8 of 8192 107.1
-// and 108.4.
+// AD: the adapters' low-rank results are read (AD_READ), or (AD_HERE, down, few values) formed by every workgroup from the rows
+// of h. Their loads go out behind those of the first two rounds of weights and come back behind them, so that their products
+// follow the stream rather than run beside it. That reads A out of the caches in every workgroup, where a launch between the
+// two products costs 4 us. fp32 result, a launch against here, whole calls: 16 values of 512 16.4 and 14.2 us, of 2048 (1
+// token, rank 16, hidden 4096) 24.4 and 22.8, of 4096 38.6 and 37.2; 32 values of 512 16.3 and 15.0, of 2048 24.6 and 24.5; 8
+// of 8192 107.1 and 108.4.
 enum { AD_NONE = 0, AD_READ = 1, AD_HERE = 2 };
 constexpr int HERE_VALUES = 32, HERE_TERMS = 1 << 16;        // for AD_HERE at most: tokens * max_rank, and times inter
 
@@ -544,16 +548,18 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few(SharedArgs a, Product g)
 // ---------------------------------------------------------------------------
 // Many tokens: a workgroup computes BW weight rows (gate/up: half of each) x BT tokens (P planes of them, which meet the same
 // weights), each wave 64 x BT/2 of them; both operands pass through LDS in 64-wide K stages, three of them (more gave nothing:
-// 512 tokens the same with four or six), filled by direct-to-LDS loads.  The matrix cores are busy half of the time at 2048
-// tokens, with no LDS bank conflict: a 16-wide slice of 128 x 256 takes 256 cycles of matrix instructions, and LDS 288 for the
-// 24 KiB that its waves read and the 12 that arrive.  Waves of 128 x 128 would read a third less, but leave half of the compute
-// units without a tile there; twice the waves with half the tokens each ran the same (161 and 162 us the whole call).
+// 512 tokens the same with four or six), filled by direct-to-LDS loads. The matrix cores are busy half of the time at 2048
+// tokens, with no LDS bank conflict: a 16-wide slice of 128 x 256 (or of 128 x 128 in two planes) takes 256 cycles of matrix
+// instructions, and LDS 288 for the 24 KiB that its waves read and the 12 that arrive. Waves of 128 x 128 would read a third
+// less, but leave half of the compute units without a tile there; twice the waves with half the tokens each ran the same (161
+// and 162 us the whole call).
 // LDS rows are 128 bytes, half of the 64 banks; 16-byte chunk c of row r lies at position c ^ (r / 2 % 8), so sixteen rows'
 // reads of one chunk column touch every bank once.
 //
 // The loads are written as assembly: the compiler would otherwise wait for all of them before any LDS read.  They
-// have no register outputs; wait_stage() counts them (the kernel has no other vector memory access between the first
-// issue and the last stage) and orders the workgroup.
+// have no register outputs; wait_stage() counts them and orders the workgroup.  The kernel has no other vector memory access
+// between the first issue and the last stage but for two registers that gate/up's tile of 128 x 256 spills (12 bytes of scratch);
+// one more in flight would only make the counted wait a stricter one.
 // ---------------------------------------------------------------------------
 constexpr int BK = 64, STAGES = 3;
 constexpr int many_split(int BT) { return BT == 64 ? 2 : 1; }
@@ -769,10 +775,11 @@ __global__ __launch_bounds__(many_threads(BW, BT)) void k_many(SharedArgs a, Pro
         }
         return;
     } else if (a.n) {
-        // Up to NA adapters of 64 of this wave's tokens at a time, whose loads go out together (gate/up of 2048 tokens
-        // 70 us; 77 with one adapter after the other and its rank before its loads; 68 without adapters).  Rank values go 16
-        // at a time, each once with each part of the tokens' low-rank results (two of which, 16 bits, beside a bf16 result).
-        // An adapter's products are formed for all of the tokens, in sums of their own, and added to those of its own tokens.
+        // Up to NA adapters of 64 of this wave's tokens at a time, whose loads go out together (gate/up of 2048 tokens, rank
+        // 16, side by side: 70 us, 77 with one adapter after the other and its rank before its loads; without adapters it is 3
+        // us less than with them, 5 to 7 less at rank 32). Rank values go 16 at a time, each once with each part of the tokens'
+        // low-rank results (two of which, 16 bits, beside a bf16 result). An adapter's products are formed for all of the
+        // tokens, in sums of their own, and added to those of its own tokens.
         constexpr int NP = GU ? 2 : 1, JG = FT < 2 ? FT : 2, SP = !GU && P < 3 ? 2 : 3, NA = 4;
 #pragma unroll
         for (int jg = 0; jg < FT; jg += JG) {
@@ -1033,9 +1040,9 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 // Whether the weights stream past groups of up to 64 tokens (once from memory, then from the caches), or tiles of both operands
 // pass through LDS, which costs up to five more launches for the plan and the down-rank parts.  Streamed against tiles,
 // hidden x inter, 16 adapters of rank up to 16 in runs, fp32 out:
-//   2 groups: 100 tokens 1024 x 1024 30.5 and 47.1 us, 128 tokens 4096 x 2048 77.4 and 67.1 (bf16 out 65.1 and 63.0; an
-//     adapter of rank 64 for each of 100 tokens, bf16 out: 73.9 and 93.0);
-//   4 groups: 256 tokens 512 x 512 37.6 and 40.6, 1024 x 1024 (bf16 out) 37.5 and 40.7, 200 tokens 2048 x 1024 56.0 and 51.1,
+//   2 groups: 100 tokens 1024 x 1024 30.3 and 47.8 us, 128 tokens 4096 x 2048 75 and 68 (bf16 out 68 and 65; an adapter of
+//     rank 64 for each of 100 tokens, bf16 out: 103 and 211);
+//   4 groups: 256 tokens 512 x 512 33.2 and 37.4, 1024 x 1024 (bf16 out) 38.8 and 43.8, 200 tokens 2048 x 1024 56.0 and 51.1,
 //     256 tokens 4096 x 512 73.8 and 54.5;
 //   6 groups: 333 tokens 1000 x 520 (fp32 x) 69.4 and 51.7.
 bool few_path(int T, int H, int Is) {
@@ -1091,9 +1098,9 @@ size_t shared_workspace(int T, int H, int Is, int n, int R) {
 
 hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st) {
     char *base = static_cast<char *>(ws);
-    // bf16 parts of x and h.  Beside a bf16 result 16 bits are enough: what they leave is 2^-8 of its own rounding.  One part of h
-    // would not be, though it halves the down product: its rounding is as large as the result's (2048 tokens of 4096 x 2048, error
-    // against binary64 2.35e-3 with one part, 1.66e-3 with two, which is that of one rounding).
+    // bf16 parts of x and h.  Beside a bf16 result 16 bits are enough: what they leave is 2^-8 of its own rounding.  One part
+    // of h would not be, though it halves the down product: its rounding is as large as the result's (2048 tokens of 4096 x
+    // 2048, error against binary64 2.35e-3 with one part, 1.66e-3 with two, which is that of one rounding).
     const bool small = few_path(a.T, a.H, a.Is);
     const int xp = a.x_bf16 ? 1 : a.out_bf16 ? 2 : 3, hp = a.out_bf16 ? 2 : 3;
     const Layout l = layout(a.T, a.H, a.Is, a.n, a.R, xp, hp);

@@ -8,9 +8,11 @@
 //
 // Bound: HBM traffic for many rows, one memory round trip and two barriers for few.  One workgroup holds one row in
 // registers, so every input is read once: all loads of a row (source, residual, weight) are issued before the first
-// reduction.  A copy of 2 GiB moves 4.97 TB/s on this chip; 11709 x 4096 with block scales takes 61.0 us (337 MB, 5.5 TB/s),
-// 1469 x 4096 with row scales 14.8 (78 MB, 5.3 TB/s), 2048 combined rows of 8 x 4096 66.4 (344 MB, 5.2 TB/s); one row of 4096
-// takes 2.4 us, one combined row 3.2, which is what a launch with one round trip to memory takes.
+// reduction.  A copy of 2 GiB moves 4.85 to 4.97 TB/s on this chip; 11709 x 4096 with block scales takes 61.5 us (337 MB, 5.5
+// TB/s), 1469 x 4096 with row scales 15.6 (78 MB, 5.0 TB/s), 2048 combined rows of 8 x 4096 66.4 (344 MB, 5.2 TB/s); one row of
+// 4096 takes 2.4 us, one combined row 3.4, which is what a launch with one round trip to memory takes (kernels alone, medians).
+// Short rows leave most of a workgroup's lanes without columns (whole calls: 16384 x 128 bf16 8.3 us, 2.0 TB/s), and rows of
+// more than 16384 columns spill registers (512 x 32768 bf16 38 us, 3.5 TB/s; 512 x 16384 16.1, 4.2).
 #include <type_traits>
 
 #include "common.h"
@@ -53,12 +55,13 @@ template <bool MAX> __device__ __forceinline__ double wg_join(double d, double *
 }
 __device__ __forceinline__ double wg_sum(double d, double *part, int nw) { return wg_join<false>(d, part, nw); }
 
-// 1 / sqrt(sum / H + eps) in two fp32 parts, from the threads' binary64 sums of squares.  The row's one factor moves all of its
+// 1 / sqrt(sum / H + eps) in two fp32 parts, from the threads' binary64 sums of squares. The row's one factor moves all of its
 // columns the same way, and where y is e4m3 an error in it decides blocks' scales and values that lie next to a rounding's
-// border; and fp32 holds the squares of half of its own exponents only.  The square root is taken in binary64 too (the
-// instruction's estimate and one Newton step).  Whole calls with fp32 squares per thread and with binary64 ones: 11709 x 4096 60.6 and
-// 61.1 us, 1469 x 4096 15.0 and 15.1, one row the same.  Combined rows in binary64 cost nothing (2048 x 8 x 4096 66.2 and 66.3
-// us), a row's scale and the quotients by it little (1469 x 4096 14.7 and 15.1).  What is left is n's one rounding to fp32.
+// border; and fp32 holds the squares of half of its own exponents only. The square root is taken in binary64 too (the
+// instruction's estimate and one Newton step). Whole calls with fp32 squares per thread and with binary64 ones: 11709 x 4096
+// 60.6 and 61.1 us, 1469 x 4096 15.0 and 15.1, one row the same. Combined rows in binary64 cost nothing (2048 x 8 x 4096 66.2
+// and 66.3 us), a row's scale and the quotients by it little (1469 x 4096 14.7 and 15.1). What is left is n's one rounding to
+// fp32.
 struct Factor { float hi, lo; double r; int exp; };
 __device__ __forceinline__ Factor row_factor(const NormArgs &a, double ss, double *part, int nw) {
     const double m = fma(wg_sum(ss, part, nw), a.inv_hidden, (double)a.eps), r0 = __builtin_amdgcn_rsq(m);
@@ -196,7 +199,7 @@ enum { SRC_F32 = 0, SRC_BF16 = 1, SRC_COMBINE = 2 };     // what the row comes f
 // One row per workgroup, C groups of eight columns per thread: group g = threadIdx.x + r * blockDim.x, so the four
 // groups of a 32-column block lie in four adjacent lanes.  AL: H % 8 == 0 and 16-byte aligned rows.  Else a row's last group
 // loads its last eight columns (H >= 8) and moves its own to the front, and addresses are aligned to elements only: one load
-// for eight columns all the same.  515 x 2055 bf16, whole call: 5.3 us, with one column per lane and load 9.9.
+// for eight columns all the same.  515 x 2055 bf16, whole call: 5.4 us, with one column per lane and load 9.9.
 template <int SRC, int RES, int C, int KC, bool AL>
 __global__ __launch_bounds__(1024) void k_norm_vec(NormArgs a) {
     __shared__ double part64[3][16];
