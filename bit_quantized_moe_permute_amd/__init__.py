@@ -16,11 +16,12 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe2bit.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_DEVICE = 0, 1, 2, 3
-DT_F32, DT_BF16, DT_E4M3_BLOCK, DT_E4M3_ROW = 0, 1, 2, 3
+DT_F32, DT_BF16, DT_E4M3_BLOCK, DT_E4M3_ROW, DT_F16 = 0, 1, 2, 3, 4
 FMT_IQ2X, FMT_Q2K, FMT_Q4K = 1, 2, 3
 PATH_AUTO, PATH_GENERIC, PATH_GEMV, PATH_GEMM = 0, 1, 2, 3
 PRECISION_EXACT, PRECISION_FAST = 0, 1
-ABI_VERSION = 4
+ACT_NONE, ACT_SWIGLU = 0, 1
+ABI_VERSION = 5
 NORM_MAX_HIDDEN = 32768
 
 EXPORTS = [
@@ -28,7 +29,8 @@ EXPORTS = [
     "moe_dequantize", "moe_route_workspace", "moe_route", "moe_expert_ffn_workspace", "moe_expert_ffn",
     "moe_expert_gate_up", "moe_expert_down", "moe_combine", "moe_combine_steer", "moe_probe_stream_read",
     "moe_expert_ffn_noalloc", "moe_layer_workspace", "moe_layer", "moe_add_rms_norm", "moe_combine_norm",
-    "moe_shared_ffn_workspace", "moe_shared_ffn",
+    "moe_shared_ffn_workspace", "moe_shared_ffn", "moe_grouped_linear", "moe_grouped_dgrad", "moe_grouped_wgrad",
+    "moe_q4_linear",
 ]
 
 
@@ -59,6 +61,22 @@ class AdapterDesc(ctypes.Structure):
         ("rank", ctypes.c_void_p), ("scale", ctypes.c_void_p),
         ("gate_a", ctypes.c_void_p), ("gate_b", ctypes.c_void_p), ("up_a", ctypes.c_void_p), ("up_b", ctypes.c_void_p),
         ("down_a", ctypes.c_void_p), ("down_b", ctypes.c_void_p),
+    ]
+
+
+class GroupDesc(ctypes.Structure):
+    """moe_group_desc (include/moe2bit.h)."""
+    _fields_ = [
+        ("n_groups", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("offsets", ctypes.c_void_p),
+        ("in_index", ctypes.c_void_p), ("in_div", ctypes.c_int32), ("out_index", ctypes.c_void_p),
+    ]
+
+
+class Q4Desc(ctypes.Structure):
+    """moe_q4_desc (include/moe2bit.h)."""
+    _fields_ = [
+        ("n_mats", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("group", ctypes.c_int32),
+        ("scale_dt", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
     ]
 
 
@@ -113,6 +131,15 @@ def _load():
     L.moe_shared_ffn.restype = ctypes.c_int
     L.moe_shared_ffn.argtypes = [ctypes.POINTER(LayerDesc), ctypes.POINTER(AdapterDesc), vp, i32, i32, vp, vp, i32, vp,
                                  sz, vp]
+    gd = ctypes.POINTER(GroupDesc)
+    L.moe_grouped_linear.restype = ctypes.c_int
+    L.moe_grouped_linear.argtypes = [gd, vp, i32, vp, i32, i32, i32, vp, i32, i32, vp]
+    L.moe_grouped_dgrad.restype = ctypes.c_int
+    L.moe_grouped_dgrad.argtypes = [gd, vp, i32, vp, i32, i32, vp, i32, i32, vp]
+    L.moe_grouped_wgrad.restype = ctypes.c_int
+    L.moe_grouped_wgrad.argtypes = [gd, vp, i32, vp, i32, i32, i32, i32, vp, i32, vp]
+    L.moe_q4_linear.restype = ctypes.c_int
+    L.moe_q4_linear.argtypes = [gd, ctypes.POINTER(Q4Desc), vp, i32, i32, vp, i32, i32, vp]
     L.moe_probe_stream_read.restype = ctypes.c_int
     L.moe_probe_stream_read.argtypes = [vp, sz, vp, i32, vp]
     if L.moe_abi_version() != ABI_VERSION:
@@ -508,6 +535,109 @@ def moe_shared_ffn(desc: LayerDesc, x, out, ws, adapters=None, token_adapter=Non
         _check(st)
 
 
+def _bf16_rows(t, what, cols):
+    """Rows of a [rows][cols] bf16 tensor."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols:
+        raise ValueError(f"{what} must be [rows][{cols}], got shape {tuple(shape)}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what}: expected torch.bfloat16, got {t.dtype}")
+    return shape[0]
+
+
+def _out_rows(t, what, cols):
+    """Rows and type of a [rows][cols] output."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols:
+        raise ValueError(f"{what} must be [rows][{cols}], got shape {tuple(shape)}")
+    return shape[0], _type(t, what)
+
+
+def _stack(groups, w):
+    """(n_out, n_in) of a bf16 [groups][n_out][n_in] stack."""
+    shape = w.shape
+    if len(shape) != 3 or shape[0] != groups.n:
+        raise ValueError(f"weights must be [{groups.n}][n_out][n_in], got shape {tuple(shape)}")
+    if w.dtype != torch.bfloat16:
+        raise TypeError(f"weights: expected torch.bfloat16, got {w.dtype}")
+    return shape[1], shape[2]
+
+
+def _group_dev(groups, dev):
+    if groups.device_index is not None and groups.device_index != dev and dev >= 0:
+        raise ValueError(f"tensors on devices {dev} and {groups.device_index}")
+
+
+def moe_grouped_linear(groups, x, w, out, act=ACT_NONE, stream=None):
+    """out[o] = W_g x[r] for the rows of every group of `groups` (a RowGroups); x [rows][n_in] bf16, w
+    [groups][n_out][n_in] bf16, out [rows][n_out] float32 or bfloat16.  ACT_SWIGLU: w [groups][2 n_out][n_in], gate rows
+    then up rows, out = silu(gate) * up."""
+    N, K = _stack(groups, w)
+    if act == ACT_SWIGLU:
+        if N % 2:
+            raise ValueError(f"weights of a SwiGLU must have an even number of rows, got {N}")
+        N //= 2
+    x_rows = _bf16_rows(x, "x", K)
+    out_rows, out_dt = _out_rows(out, "out", N)
+    dev = x.get_device()
+    _group_dev(groups, dev)
+    px, pw, po = _addrs(dev, x, w, out)
+    st = lib.moe_grouped_linear(groups.desc, px, x_rows, pw, N, K, act, po, out_dt, out_rows, _stream_on(stream, dev))
+    if st:
+        _check(st)
+
+
+def moe_grouped_dgrad(groups, dy, w, dx, stream=None):
+    """The gradient of moe_grouped_linear (without activation) with respect to its input: dx[in_index[i], or i] =
+    W_g^T dy[o]; dy [rows][n_out] bf16, dx [rows][n_in] float32 or bfloat16."""
+    N, K = _stack(groups, w)
+    dy_rows = _bf16_rows(dy, "dy", N)
+    dx_rows, dx_dt = _out_rows(dx, "dx", K)
+    dev = dy.get_device()
+    _group_dev(groups, dev)
+    py, pw, po = _addrs(dev, dy, w, dx)
+    st = lib.moe_grouped_dgrad(groups.desc, py, dy_rows, pw, N, K, po, dx_dt, dx_rows, _stream_on(stream, dev))
+    if st:
+        _check(st)
+
+
+def moe_grouped_wgrad(groups, x, dy, dw, accumulate=False, stream=None):
+    """The gradient of moe_grouped_linear (without activation) with respect to its weights: dw[g] (+)= the sum of
+    dy[o] x[r]^T over the rows of group g; x [rows][n_in] and dy [rows][n_out] bf16, dw [groups][n_out][n_in] float32 or
+    bfloat16."""
+    shape = dw.shape
+    if len(shape) != 3 or shape[0] != groups.n:
+        raise ValueError(f"dw must be [{groups.n}][n_out][n_in], got shape {tuple(shape)}")
+    N, K = shape[1], shape[2]
+    x_rows, dy_rows, dw_dt = _bf16_rows(x, "x", K), _bf16_rows(dy, "dy", N), _type(dw, "dw")
+    dev = x.get_device()
+    _group_dev(groups, dev)
+    px, py, po = _addrs(dev, x, dy, dw)
+    st = lib.moe_grouped_wgrad(groups.desc, px, x_rows, py, dy_rows, N, K, bool(accumulate), po, dw_dt,
+                               _stream_on(stream, dev))
+    if st:
+        _check(st)
+
+
+def moe_q4_linear(groups, weights, x, out, act=ACT_NONE, stream=None):
+    """moe_grouped_linear with 4-bit weights (a Q4Weights with a matrix for every group of `groups`)."""
+    N = weights.rows
+    if act == ACT_SWIGLU:
+        if N % 2:
+            raise ValueError(f"weights of a SwiGLU must have an even number of rows, got {N}")
+        N //= 2
+    x_rows = _bf16_rows(x, "x", weights.cols)
+    out_rows, out_dt = _out_rows(out, "out", N)
+    dev = x.get_device()
+    _group_dev(groups, dev)
+    if weights.device_index != dev and dev >= 0:
+        raise ValueError(f"tensors on devices {dev} and {weights.device_index}")
+    px, po = _addrs(dev, x, out)
+    st = lib.moe_q4_linear(groups.desc, weights.desc, px, x_rows, act, po, out_dt, out_rows, _stream_on(stream, dev))
+    if st:
+        _check(st)
+
+
 def moe_probe_stream_read(buf, nbytes, sink, n_blocks, stream=None):
     """Measurement helper: one streaming read of buf's first nbytes bytes (sink: n_blocks uint32 words)."""
     _need_bytes(buf, nbytes, "buf")
@@ -519,4 +649,4 @@ import torch  # noqa: E402  (after the library: it fails first where it is missi
 
 _DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
 
-from .layer import AdapterPool, DeviceLayer, LayerBuffers  # noqa: E402  (needs `lib` loaded)
+from .layer import AdapterPool, DeviceLayer, LayerBuffers, Q4Weights, RowGroups  # noqa: E402  (needs `lib` loaded)

@@ -9,6 +9,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <utility>
 
@@ -655,6 +656,137 @@ moe_status moe_shared_ffn(const moe_layer_desc *L, const moe_adapter_desc *A, co
     }
     a.out = out; a.out_bf16 = out_dt == MOE_DT_BF16;
     return from_hip(moe::launch_shared(a, ws, (hipStream_t)stream), fn, (hipStream_t)stream);
+}
+
+// ---------------------------------------------------------------------------
+// products over rows grouped by expert
+// ---------------------------------------------------------------------------
+struct Buffer {
+    const void *p;
+    size_t bytes;
+};
+
+static moe_status check_groups(const char *fn, const moe_group_desc *g, moe::Groups &o) {
+    if (!g) return fail(MOE_ERR_INVALID_ARG, "%s: null group description", fn);
+    if (g->n_groups < 1 || g->n_groups > MOE_MAX_GROUPS)
+        return fail(MOE_ERR_INVALID_ARG, "%s: n_groups outside [1, %d]", fn, MOE_MAX_GROUPS);
+    if (g->n_rows < 1) return fail(MOE_ERR_INVALID_ARG, "%s: n_rows < 1", fn);
+    if (g->n_rows > MOE_MAX_ROWS) return fail(MOE_ERR_UNSUPPORTED, "%s: n_rows > %d; split the batch", fn, MOE_MAX_ROWS);
+    if (!g->offsets && g->n_groups != 1)
+        return fail(MOE_ERR_INVALID_ARG, "%s: offsets may be null for one group only", fn);
+    if (g->in_div < 1) return fail(MOE_ERR_INVALID_ARG, "%s: in_div < 1", fn);
+    if (!aligned(g->offsets, 4) || !aligned(g->in_index, 4) || !aligned(g->out_index, 4))
+        return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer (offsets or indices)", fn);
+    o.n = g->n_groups; o.rows = g->n_rows; o.offsets = g->offsets;
+    o.in_index = g->in_index; o.in_div = g->in_div; o.out_index = g->out_index;
+    return MOE_OK;
+}
+
+// The output of a grouped product against what it reads.
+static moe_status check_output(const char *fn, const moe::Groups &g, Buffer out, std::initializer_list<Buffer> read) {
+    for (const Buffer &r : read)
+        if (overlap(out.p, out.bytes, r.p, r.bytes)) return fail(MOE_ERR_INVALID_ARG, "%s: the output overlaps an input", fn);
+    const size_t n = (size_t)g.rows * 4;
+    if (overlap(out.p, out.bytes, g.offsets, ((size_t)g.n + 1) * 4) || overlap(out.p, out.bytes, g.in_index, n) ||
+        overlap(out.p, out.bytes, g.out_index, n))
+        return fail(MOE_ERR_INVALID_ARG, "%s: the output overlaps the offsets or an index", fn);
+    return MOE_OK;
+}
+
+static moe_status check_dims(const char *fn, int32_t n_out, int32_t n_in) {
+    if (n_out < 8 || n_in < 8 || n_out % 8 || n_in % 8)
+        return fail(MOE_ERR_INVALID_ARG, "%s: n_out and n_in must be positive multiples of 8", fn);
+    if (n_out > MOE_GROUPED_MAX_DIM || n_in > MOE_GROUPED_MAX_DIM)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: n_out or n_in above %d", fn, MOE_GROUPED_MAX_DIM);
+    return MOE_OK;
+}
+
+static moe_status grouped_call(const char *fn, int op, const moe_group_desc *g, const void *a, int32_t a_rows,
+                               const void *b, int32_t b_rows, int32_t n_out, int32_t n_in, int32_t act,
+                               int32_t accumulate, void *out, int32_t out_dt, int32_t out_rows, void *stream) {
+    moe::GroupedArgs p;
+    memset(&p, 0, sizeof p);
+    moe_status st = check_groups(fn, g, p.g);
+    if (st != MOE_OK || (st = check_dims(fn, n_out, n_in)) != MOE_OK) return st;
+    const bool wgrad = op == moe::GROUPED_WGRAD;
+    if (!a || !b || !out) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16))
+        return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer (16 B)", fn);
+    if (a_rows < 1 || (wgrad && b_rows < 1) || (!wgrad && out_rows < 1))
+        return fail(MOE_ERR_INVALID_ARG, "%s: a buffer without rows", fn);
+    if (out_dt != MOE_DT_F32 && out_dt != MOE_DT_BF16) return fail(MOE_ERR_INVALID_ARG, "%s: unknown output dtype", fn);
+    if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return fail(MOE_ERR_INVALID_ARG, "%s: unknown activation", fn);
+    const size_t weights = (size_t)g->n_groups * n_out * n_in * (act == MOE_ACT_SWIGLU ? 2 : 1);
+    const size_t in_cols = op == moe::GROUPED_DGRAD ? n_out : n_in, out_cols = op == moe::GROUPED_DGRAD ? n_in : n_out;
+    const Buffer o{out, (wgrad ? weights : (size_t)out_rows * out_cols) * dt_bytes(out_dt)};
+    st = check_output(fn, p.g, o, {{a, (size_t)a_rows * in_cols * 2}, {b, (wgrad ? (size_t)b_rows * n_out : weights) * 2}});
+    if (st != MOE_OK) return st;
+    p.a = static_cast<const uint16_t *>(a); p.a_rows = a_rows;
+    p.b = static_cast<const uint16_t *>(b); p.b_rows = b_rows;
+    p.n_out = n_out; p.n_in = n_in;
+    p.swiglu = act == MOE_ACT_SWIGLU; p.accumulate = accumulate != 0;
+    p.out = out; p.out_bf16 = out_dt == MOE_DT_BF16; p.out_rows = out_rows;
+    const hipError_t e = moe::launch_grouped(op, p, (hipStream_t)stream);
+    if (e == hipErrorInvalidConfiguration) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles; split the batch", fn);
+    return from_hip(e, fn, (hipStream_t)stream);
+}
+
+moe_status moe_grouped_linear(const moe_group_desc *g, const void *x, int32_t x_rows, const void *w, int32_t n_out,
+                              int32_t n_in, int32_t act, void *out, int32_t out_dt, int32_t out_rows, void *stream) {
+    return grouped_call("moe_grouped_linear", moe::GROUPED_FWD, g, x, x_rows, w, 0, n_out, n_in, act, 0, out, out_dt,
+                        out_rows, stream);
+}
+
+moe_status moe_grouped_dgrad(const moe_group_desc *g, const void *dy, int32_t dy_rows, const void *w, int32_t n_out,
+                             int32_t n_in, void *dx, int32_t dx_dt, int32_t dx_rows, void *stream) {
+    return grouped_call("moe_grouped_dgrad", moe::GROUPED_DGRAD, g, dy, dy_rows, w, 0, n_out, n_in, MOE_ACT_NONE, 0, dx,
+                        dx_dt, dx_rows, stream);
+}
+
+moe_status moe_grouped_wgrad(const moe_group_desc *g, const void *x, int32_t x_rows, const void *dy, int32_t dy_rows,
+                             int32_t n_out, int32_t n_in, int32_t accumulate, void *dw, int32_t dw_dt, void *stream) {
+    return grouped_call("moe_grouped_wgrad", moe::GROUPED_WGRAD, g, x, x_rows, dy, dy_rows, n_out, n_in, MOE_ACT_NONE,
+                        accumulate, dw, dw_dt, 0, stream);
+}
+
+moe_status moe_q4_linear(const moe_group_desc *g, const moe_q4_desc *w, const void *x, int32_t x_rows, int32_t act,
+                         void *out, int32_t out_dt, int32_t out_rows, void *stream) {
+    const char *fn = "moe_q4_linear";
+    moe::Q4Args p;
+    memset(&p, 0, sizeof p);
+    moe_status st = check_groups(fn, g, p.g);
+    if (st != MOE_OK) return st;
+    if (!w || !x || !out || !w->codes || !w->scale) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (w->n_mats != g->n_groups) return fail(MOE_ERR_INVALID_ARG, "%s: %d matrices for %d groups", fn, w->n_mats, g->n_groups);
+    if (w->group != 32 && w->group != 64 && w->group != 128)
+        return fail(MOE_ERR_INVALID_ARG, "%s: group must be 32, 64 or 128", fn);
+    if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return fail(MOE_ERR_INVALID_ARG, "%s: unknown activation", fn);
+    if (w->rows < 1 || w->cols < 1 || w->cols % w->group || (act == MOE_ACT_SWIGLU && w->rows % 2))
+        return fail(MOE_ERR_INVALID_ARG, "%s: cols must be a positive multiple of group, rows positive (SwiGLU: even)", fn);
+    if (w->rows > MOE_GROUPED_MAX_DIM || w->cols > MOE_GROUPED_MAX_DIM)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: rows or cols above %d", fn, MOE_GROUPED_MAX_DIM);
+    if ((w->scale_dt != MOE_DT_F32 && w->scale_dt != MOE_DT_BF16 && w->scale_dt != MOE_DT_F16) ||
+        (out_dt != MOE_DT_F32 && out_dt != MOE_DT_BF16))
+        return fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+    const size_t sb = w->scale_dt == MOE_DT_F32 ? 4 : 2;
+    if (!aligned(x, 16) || !aligned(out, 16) || !aligned(w->codes, 16) || !aligned(w->scale, sb))
+        return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer (x, out and codes 16 B)", fn);
+    if (x_rows < 1 || out_rows < 1) return fail(MOE_ERR_INVALID_ARG, "%s: a buffer without rows", fn);
+    p.N = act == MOE_ACT_SWIGLU ? w->rows / 2 : w->rows;
+    p.K = w->cols; p.group = w->group;
+    const size_t values = (size_t)w->n_mats * w->rows * w->cols, groups = values / w->group;
+    st = check_output(fn, p.g, {out, (size_t)out_rows * p.N * dt_bytes(out_dt)},
+                      {{x, (size_t)x_rows * p.K * 2}, {w->codes, values / 2}, {w->scale, groups * sb}, {w->zero, groups}});
+    if (st != MOE_OK) return st;
+    p.x = static_cast<const uint16_t *>(x); p.x_rows = x_rows;
+    p.codes = static_cast<const uint8_t *>(w->codes);
+    p.scale = w->scale; p.zero = w->zero;
+    p.scale_kind = w->scale_dt == MOE_DT_F32 ? moe::Q4_F32 : w->scale_dt == MOE_DT_BF16 ? moe::Q4_BF16 : moe::Q4_F16;
+    p.swiglu = act == MOE_ACT_SWIGLU;
+    p.out = out; p.out_bf16 = out_dt == MOE_DT_BF16; p.out_rows = out_rows;
+    const hipError_t e = moe::launch_q4(p, (hipStream_t)stream);
+    if (e == hipErrorInvalidConfiguration) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles; split the batch", fn);
+    return from_hip(e, fn, (hipStream_t)stream);
 }
 
 moe_status moe_probe_stream_read(const void *buf, size_t bytes, uint32_t *sink, int32_t n_blocks, void *stream) {

@@ -146,6 +146,43 @@ struct Product {
 size_t shared_workspace(int T, int H, int Is, int n, int R);
 hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st);
 
+// grouped.hip, q4.hip: products over rows grouped by expert
+struct Groups {
+    int n, rows;                         // groups, positions
+    const int32_t *offsets;              // NULL: one group of all rows
+    const int32_t *in_index;             // optional
+    int in_div;
+    const int32_t *out_index;            // optional
+};
+struct GroupedArgs {
+    Groups g;
+    const uint16_t *a;                   // rows that the positions read: x, or dy for the input's gradient
+    int a_rows;
+    const uint16_t *b;                   // the weights, or dy for theirs
+    int b_rows;                          // (rows of that dy)
+    int n_out, n_in;                     // the weights' rows and columns as they are stored, without SwiGLU's doubling
+    int swiglu, accumulate;
+    void *out;
+    int out_bf16, out_rows;
+};
+enum { GROUPED_FWD = 0, GROUPED_DGRAD = 1, GROUPED_WGRAD = 2 };
+hipError_t launch_grouped(int op, const GroupedArgs &a, hipStream_t st);
+enum { Q4_F32 = 0, Q4_BF16 = 1, Q4_F16 = 2 };
+struct Q4Args {
+    Groups g;
+    const uint16_t *x;
+    int x_rows;
+    int N, K, group;                     // rows (SwiGLU: of one half), columns
+    const uint8_t *codes;
+    const void *scale;
+    int scale_kind;
+    const uint8_t *zero;                 // optional
+    int swiglu;
+    void *out;
+    int out_bf16, out_rows;
+};
+hipError_t launch_q4(const Q4Args &a, hipStream_t st);
+
 // probe.hip: streaming-read ceiling (measurement only)
 hipError_t launch_stream_read(const void *buf, int64_t bytes, uint32_t *sink, int n_blocks, hipStream_t st);
 

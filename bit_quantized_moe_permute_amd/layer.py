@@ -10,7 +10,8 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from . import (FMT_IQ2X, PATH_AUTO, PRECISION_EXACT, AdapterDesc, LayerDesc, moe_add_rms_norm, moe_combine,
+from . import (DT_BF16, DT_F16, DT_F32, FMT_IQ2X, PATH_AUTO, PRECISION_EXACT, AdapterDesc, GroupDesc, LayerDesc, Q4Desc,
+               moe_add_rms_norm, moe_combine,
                moe_combine_norm, moe_combine_steer, moe_expert_ffn, moe_expert_ffn_workspace, moe_layer,
                moe_layer_workspace, moe_prepare_weights, moe_route, moe_route_workspace, moe_shared_ffn,
                moe_shared_ffn_workspace, moe_weight_bytes, _norm_output)
@@ -64,6 +65,81 @@ class AdapterPool:
         return AdapterPool(self.hidden, self.inter, **{
             n: t if t is None else t.clone() if n in ("rank", "scale") else tuple(v.clone() for v in t)
             for n, t in self._given.items()})
+
+
+def _device_tensor(name, t, shape, dtypes):
+    """Checks a tensor that is kept by address."""
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a GPU tensor (the library takes device pointers)")
+    if (shape is not None and tuple(t.shape) != shape) or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of {' or '.join(str(d) for d in dtypes)}"
+                         f"{'' if shape is None else f' and shape {shape}'}, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+class RowGroups:
+    """Rows grouped by expert for moe_grouped_linear and its gradients and moe_q4_linear: group g has the positions
+    offsets[g] .. offsets[g + 1] - 1 of n_rows; position i reads row in_index[i] // in_div of the input and writes row
+    out_index[i] of the output (without an index: row i).
+
+    offsets: int32 [n + 1] (moe_route's expert_offsets), None: one group of n_rows.  in_index, out_index: int32 [n_rows]
+    or None (moe_route's perm, with in_div = top_k where the input's rows are tokens).  The tensors are kept; their values
+    may be changed in place between calls (a new routing in the same buffers).
+    """
+
+    def __init__(self, n_rows, offsets=None, in_index=None, in_div=1, out_index=None):
+        i32 = (torch.int32,)
+        self.device_index = None
+        self._keep = []
+        for name, t in (("offsets", offsets), ("in_index", in_index), ("out_index", out_index)):
+            if t is None:
+                continue
+            _device_tensor(name, t, None, i32)
+            if name != "offsets" and t.numel() < n_rows:
+                raise ValueError(f"{name}: {t.numel()} elements, {n_rows} rows need as many")
+            if self.device_index not in (None, t.get_device()):
+                raise ValueError(f"{name}: tensors on devices {self.device_index} and {t.get_device()}")
+            self.device_index = t.get_device()
+            self._keep.append(t)
+        if offsets is not None and offsets.numel() < 2:
+            raise ValueError("offsets must have an element more than there are groups")
+        self.n, self.n_rows = 1 if offsets is None else offsets.numel() - 1, n_rows
+        self.desc = GroupDesc(n_groups=self.n, n_rows=n_rows, in_div=in_div,
+                              **{k: None if t is None else t.data_ptr()
+                                 for k, t in (("offsets", offsets), ("in_index", in_index), ("out_index", out_index))})
+
+
+class Q4Weights:
+    """4-bit weights with group scales resident in device memory, W[m][n][k] = (code - zero) * scale of k's group.
+
+    codes: uint8 [n][rows][cols / 2], column k in byte k / 2, even columns in the low four bits.  scale: fp16, bf16 or fp32
+    [n][rows][cols / group], group 32, 64 or 128.  zero: uint8 like scale, values 0 .. 15, or None: 8.  A single matrix may
+    come without its leading dimension.  The tensors are kept.
+    """
+
+    _SCALES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+
+    def __init__(self, codes, scale, zero=None):
+        codes, scale, zero = (t[None] if t is not None and t.dim() == 2 else t for t in (codes, scale, zero))
+        if codes.dim() != 3 or scale.dim() != 3:
+            raise ValueError(f"codes must be [n][rows][cols / 2], scale [n][rows][cols / group], got {tuple(codes.shape)} "
+                             f"and {tuple(scale.shape)}")
+        self.n, self.rows, self.cols = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+        groups = scale.shape[2]
+        if groups < 1 or self.cols % groups or self.cols // groups not in (32, 64, 128):
+            raise ValueError(f"{self.cols} columns in {groups} groups: a group must have 32, 64 or 128 columns")
+        self.group = self.cols // groups
+        shape = (self.n, self.rows, groups)
+        _device_tensor("codes", codes, None, (torch.uint8,))
+        _device_tensor("scale", scale, shape, tuple(self._SCALES))
+        self._keep = [codes, scale]
+        if zero is not None:
+            self._keep.append(_device_tensor("zero", zero, shape, (torch.uint8,)))
+        self.device_index = codes.get_device()
+        if any(t.get_device() != self.device_index for t in self._keep):
+            raise ValueError(f"codes, scale and zero on different devices: {[t.get_device() for t in self._keep]}")
+        self.desc = Q4Desc(n_mats=self.n, rows=self.rows, cols=self.cols, group=self.group, scale_dt=self._SCALES[scale.dtype],
+                           codes=codes.data_ptr(), scale=scale.data_ptr(), zero=None if zero is None else zero.data_ptr())
 
 
 class DeviceLayer:

@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 4
+#define MOE_ABI_VERSION 5
 
 typedef enum {
     MOE_OK = 0,
@@ -80,8 +80,9 @@ typedef enum {
  *               [rows][ceil(cols/32)] bytes holding e + 127: value = code * 2^e
  *               (the block format the matrix cores read);
  *   E4M3_ROW    one fp32 scale per row, [rows]: value = code * scale.
+ * F16 is a type of the group scales of 4-bit weights (moe_q4_desc) only.
  */
-typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_E4M3_BLOCK = 2, MOE_DT_E4M3_ROW = 3 } moe_dtype;
+typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_E4M3_BLOCK = 2, MOE_DT_E4M3_ROW = 3, MOE_DT_F16 = 4 } moe_dtype;
 
 typedef enum { MOE_FMT_IQ2X = 1, MOE_FMT_Q2K = 2, MOE_FMT_Q4K = 3 } moe_format;
 
@@ -485,6 +486,121 @@ size_t moe_shared_ffn_workspace(const moe_layer_desc *L, const moe_adapter_desc 
 moe_status moe_shared_ffn(const moe_layer_desc *L, const moe_adapter_desc *A, const void *x, int32_t x_dt,
                           int32_t n_tokens, const int32_t *token_adapter, void *out, int32_t out_dt, void *ws,
                           size_t ws_bytes, void *stream);
+
+/*
+ * Rows grouped by expert (host struct; read during the call only), for the
+ * products below: which rows of their inputs and outputs belong to which of
+ * n_groups matrices.  Positions i = offsets[g] .. offsets[g+1] - 1 are group
+ * g's; position i
+ *   has its input's row at  in_index[i] / in_div  (in_index NULL: at i), and
+ *   its output's row at     out_index[i]          (out_index NULL: at i).
+ * With moe_route's expert_offsets and perm, where perm lists slots t*k + j:
+ * in_index = perm, in_div = k reads the rows of the tokens; without indices
+ * rows are in perm's order; out_index = perm puts them into slot order.
+ *   n_groups: 1 .. MOE_MAX_GROUPS.  n_rows: 1 .. MOE_MAX_ROWS, the positions
+ *   that offsets may name (offsets below 0 or above n_rows are clamped).
+ *   offsets: device int32 [n_groups + 1], or NULL: one group of all n_rows
+ *     (n_groups must be 1).
+ *   in_index, out_index: device int32 [n_rows], or NULL.
+ *   in_div: >= 1.
+ * A position whose input row is outside the input counts as a row of zeros, and
+ * nothing is written for one whose output row is outside the output.  Rows of
+ * the output that no position names stay as they were.  Two positions with the
+ * same output row leave either's result there.  Offsets that overlap or
+ * decrease name groups whose results are undefined (nothing outside the
+ * buffers is touched).
+ */
+#define MOE_MAX_GROUPS 4096
+#define MOE_MAX_ROWS (1 << 24)
+#define MOE_GROUPED_MAX_DIM (1 << 20)
+typedef struct {
+    int32_t n_groups, n_rows;
+    const int32_t *offsets;
+    const int32_t *in_index;
+    int32_t in_div;
+    const int32_t *out_index;
+} moe_group_desc;
+
+/* What stands behind a product: nothing, or SwiGLU of its two halves. */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_act;
+
+/*
+ * Products with unquantized experts, the rows of each with its own matrix:
+ *   out[o] = W_g x[r]                                   (MOE_ACT_NONE)
+ *   out[o] = silu(G_g x[r]) * (U_g x[r]), W_g = [G; U]  (MOE_ACT_SWIGLU)
+ * for every position of group g, r and o its input and output row.
+ *   x [x_rows][n_in] bf16; w [n_groups][n_out][n_in] bf16 (SwiGLU: n_out rows
+ *   of G, then n_out of U, in each group); out [out_rows][n_out], fp32 or bf16.
+ * Sums are fp32; a bf16 out is rounded once.  A row's result does not depend on
+ * the other rows' values (a NaN or infinity stays in its own row), and repeated
+ * calls give the same bits.
+ * n_in and n_out must be multiples of 8, buffers 16-byte aligned; out must not
+ * overlap anything that is read.  Errors: MOE_ERR_INVALID_ARG (null, misaligned
+ * or overlapping pointer, bad shape, type or group description),
+ * MOE_ERR_UNSUPPORTED (n_in or n_out above MOE_GROUPED_MAX_DIM, n_rows above
+ * MOE_MAX_ROWS, or a product of so many tiles that a launch cannot count them),
+ * MOE_ERR_DEVICE (launch failure).
+ */
+moe_status moe_grouped_linear(const moe_group_desc *g, const void *x, int32_t x_rows, const void *w, int32_t n_out,
+                              int32_t n_in, int32_t act, void *out, int32_t out_dt, int32_t out_rows, void *stream);
+
+/*
+ * Gradient of moe_grouped_linear (MOE_ACT_NONE) with respect to its input, with
+ * the same group description: for every position of group g,
+ *   dx[in_index[i], or i] = W_g^T dy[o].
+ *   dy [dy_rows][n_out] bf16; w as above; dx [dx_rows][n_in], fp32 or bf16.
+ * in_div is not applied: where several positions read one row of x, dx holds
+ * the gradient of each (in slot order with in_index = perm), and that row's
+ * gradient is their sum (moe_combine with weights of 1).  Numerics and errors
+ * as above.
+ */
+moe_status moe_grouped_dgrad(const moe_group_desc *g, const void *dy, int32_t dy_rows, const void *w, int32_t n_out,
+                             int32_t n_in, void *dx, int32_t dx_dt, int32_t dx_rows, void *stream);
+
+/*
+ * Gradient of moe_grouped_linear (MOE_ACT_NONE) with respect to its weights,
+ * with the same group description:
+ *   dw[g] = sum over the positions of g of dy[o] x[r]^T   (+ dw[g], accumulate)
+ *   x [x_rows][n_in] and dy [dy_rows][n_out] bf16; dw [n_groups][n_out][n_in],
+ *   fp32 or bf16.  Groups without rows get zeros (with accumulate: stay).
+ * Sums are fp32 in an order that depends on shapes and offsets alone.  Errors
+ * as above.
+ */
+moe_status moe_grouped_wgrad(const moe_group_desc *g, const void *x, int32_t x_rows, const void *dy, int32_t dy_rows,
+                             int32_t n_out, int32_t n_in, int32_t accumulate, void *dw, int32_t dw_dt, void *stream);
+
+/*
+ * 4-bit weights with group scales (host struct; read during the call only):
+ *   W[m][n][k] = (code - zero[m][n][k / group]) * scale[m][n][k / group]
+ *   n_mats matrices of [rows][cols]; group: 32, 64 or 128; cols a multiple of
+ *   group, at most MOE_GROUPED_MAX_DIM like rows.
+ *   codes: [n_mats][rows][cols / 2] bytes, column k in byte k / 2, even columns
+ *     in the low four bits; 16-byte aligned.
+ *   scale: [n_mats][rows][cols / group], fp16, bf16 or fp32 (scale_dt), aligned
+ *     to its elements.
+ *   zero: [n_mats][rows][cols / group] bytes of 0 .. 15 (the high four bits are
+ *     not read), or NULL: 8 everywhere.
+ * This is the form of 4-bit checkpoints of dense projections and of experts that
+ * have no super-blocks; nothing is repacked.
+ */
+typedef struct {
+    int32_t n_mats, rows, cols, group;
+    int32_t scale_dt;
+    const void *codes, *scale;
+    const uint8_t *zero;
+} moe_q4_desc;
+
+/*
+ * moe_grouped_linear with 4-bit weights: w->n_mats must be the number of groups;
+ * x [x_rows][cols] bf16; out [out_rows][rows] (SwiGLU: [out_rows][rows / 2], rows
+ * even), fp32 or bf16.  With one matrix and offsets NULL it is a dense
+ * projection.  Codes less zero points are exact in the products, sums are fp32,
+ * a group's sum takes its scale in fp32, and a bf16 out is rounded once.  A
+ * group's weights are read once for each 64 of its rows.
+ * Errors as above (codes, x and out 16-byte aligned).
+ */
+moe_status moe_q4_linear(const moe_group_desc *g, const moe_q4_desc *w, const void *x, int32_t x_rows, int32_t act,
+                         void *out, int32_t out_dt, int32_t out_rows, void *stream);
 
 /*
  * Measurement helper, not part of the layer: reads `bytes` bytes of `buf`
