@@ -679,6 +679,12 @@ static moe_status check_groups(const char *fn, const moe_group_desc *g, moe::Gro
         return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer (offsets or indices)", fn);
     o.n = g->n_groups; o.rows = g->n_rows; o.offsets = g->offsets;
     o.in_index = g->in_index; o.in_div = g->in_div; o.out_index = g->out_index;
+    // with 2^(s-1) < d <= 2^s and m = ceil(2^(31+s) / d), m d - 2^(31+s) < d <= 2^s, so i m / 2^(31+s) is off i / d by less
+    // than i / 2^31 / d < 1 / d: its integer part is that of i / d
+    int shift = 0;
+    while (((int64_t)1 << shift) < g->in_div) ++shift;
+    o.div_mul = (uint32_t)((((uint64_t)1 << (31 + shift)) + g->in_div - 1) / g->in_div);
+    o.div_shift = shift ? shift - 1 : 0;
     return MOE_OK;
 }
 

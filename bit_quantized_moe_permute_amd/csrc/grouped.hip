@@ -56,56 +56,272 @@ __device__ __forceinline__ void store(void *out, int bf16, int64_t i, float v) {
     else static_cast<float *>(out)[i] = v;
 }
 
-template <int OP, bool SWIGLU> __global__ __launch_bounds__(256) void k_rows(GroupedArgs a) {
-    Tile t;
-    if (!find_tile(a.g, TILE, blockIdx.x, t)) return;
-    const int K = OP == GROUPED_FWD ? a.n_in : a.n_out, N = OP == GROUPED_FWD ? a.n_out : a.n_in, n0 = blockIdx.y * TILE;
-    const uint16_t *w = a.b + (int64_t)t.group * a.n_out * a.n_in * (SWIGLU ? 2 : 1);
-    auto load_a = [&](int r, int k) {
-        const int p = t.begin + r;
-        if (p >= t.end) return 0.f;
-        const int row = OP == GROUPED_FWD ? in_row(a.g, p, a.a_rows) : out_row(a.g, p, a.a_rows);
-        return row < 0 ? 0.f : at(a.a, (int64_t)row * K + k);
-    };
-    float acc[2][4][4] = {};
-    for (int h = 0; h < (SWIGLU ? 2 : 1); ++h)
-        products(K, load_a, [&](int c, int k) {
-            if (n0 + c >= N) return 0.f;
-            return OP == GROUPED_FWD ? at(w, ((int64_t)h * N + n0 + c) * K + k) : at(w, (int64_t)k * N + n0 + c);
-        }, acc[h]);
-    const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
-    for (int i = 0; i < 4; ++i) {
-        const int p = t.begin + tr * 4 + i;
-        if (p >= t.end) continue;
-        const int row = OP == GROUPED_FWD ? out_row(a.g, p, a.out_rows) : in_slot(a.g, p, a.out_rows);
-        if (row < 0) continue;
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + tc * 4 + j;
-            if (n < N) store(a.out, a.out_bf16, (int64_t)row * N + n, SWIGLU ? swiglu(acc[0][i][j], acc[1][i][j]) : acc[0][i][j]);
-        }
-    }
+typedef __attribute__((address_space(3))) void *las_ptr;
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t *las_s16x4;
+typedef const __attribute__((address_space(3))) u32x4_t *las_u32x4;
+
+__device__ const uint4 zeros[1] = {};
+
+__device__ __forceinline__ f32x16_t mfma32(uint4 a, uint4 b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
 }
 
-__global__ __launch_bounds__(256) void k_weights(GroupedArgs a) {
-    const int g = blockIdx.x, n0 = blockIdx.z * TILE, k0 = blockIdx.y * TILE, b = group_edge(a.g, g), e = group_edge(a.g, g + 1);
-    float acc[4][4] = {};
-    products(max(e - b, 0), [&](int n, int p) {
-        const int row = out_row(a.g, b + p, a.b_rows);
-        return row < 0 || n0 + n >= a.n_out ? 0.f : at(a.b, (int64_t)row * a.n_out + n0 + n);
-    }, [&](int k, int p) {
-        const int row = in_row(a.g, b + p, a.a_rows);
-        return row < 0 || k0 + k >= a.n_in ? 0.f : at(a.a, (int64_t)row * a.n_in + k0 + k);
-    }, acc);
-    const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + tr * 4 + i, k = k0 + tc * 4 + j;
-            if (n >= a.n_out || k >= a.n_in) continue;
-            const int64_t o = ((int64_t)g * a.n_out + n) * a.n_in + k;
-            float v = acc[i][j];
-            if (a.accumulate) v += a.out_bf16 ? at(static_cast<const uint16_t *>(a.out), o) : static_cast<const float *>(a.out)[o];
-            store(a.out, a.out_bf16, o, v);
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b});
+}
+
+// Everything in LDS is read, up to N of this wave's loads are still under way, and the workgroup is here.
+template <int N> __device__ __forceinline__ void wait_stage() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 16 bytes at each lane's address -> 1 KiB of LDS at byte address `dst` (wave-uniform), in lane order. The destination goes
+// through m0, which is put back: the compiler may count on its value.
+__device__ __forceinline__ void load_to_lds(uint64_t from, uint32_t dst) {
+    uint32_t m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0) : "v"(from), "s"(dst) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// A workgroup computes a tile of TP x TQ results, WP x WQ waves of FP x FQ fragments of 32 x 32. P is the side whose results lie
+// one behind the other in memory (the weights' rows; for the gradients the columns of W and x), Q the rows of the output.
+//
+//              P                        Q                        summed over
+//   forward    rows of W    [n][k]      rows of x    [r][k]      k
+//   dgrad      columns of W [n][k]      rows of dy   [o][n]      n
+//   wgrad      columns of x [r][k]      columns of dy [o][n]     positions
+//
+// Both pass through LDS in steps of 32 of the sum, NST of them in a ring that direct-to-LDS loads fill. An operand whose rows run
+// along the sum ("rows") keeps 64 bytes per row there: 16-byte chunk c of row r lies at c ^ (r / 4 % 4), so that sixteen rows'
+// reads of a chunk column touch every bank once. One whose rows run across it ("columns") is read with the transposing LDS
+// loads, four steps of the sum x 16 columns by 16 lanes: piece u of 16 columns of row r lies at u ^ swizzle(r).
+// What is outside (rows behind the group, steps behind the sum, rows that an index puts outside) is read from a block of zeros.
+//
+// The loads are written as assembly: the compiler would otherwise wait for all of them before any LDS read. They have no
+// register outputs; wait_stage() counts them and orders the workgroup. Nothing else of the loop loads through the vector memory
+// pipe.
+// ---------------------------------------------------------------------------
+constexpr int BK = 32;
+
+__device__ __forceinline__ uint32_t swizzle(int r) { return ((r & 1) * 2) ^ ((r >> 1 & 1) * 5); }
+
+template <int OP, int FP, int FQ, int WP, int WQ, int NST, bool SWIGLU>
+__global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(GroupedArgs a, int tiles_p, int tiles_q) {
+    constexpr bool COLS_P = OP != GROUPED_FWD, COLS_Q = OP == GROUPED_WGRAD;
+    constexpr int NW = WP * WQ, TP = 32 * FP * WP, TQ = 32 * FQ * WQ;
+    constexpr int LP = TP / 16 / NW, LQ = TQ / 16 / NW, LOADS = LP + LQ;             // loads of 1 KiB per wave and stage
+    constexpr uint32_t STAGE = (TP + TQ) * 64;
+    static_assert(LP * NW * 16 == TP && LQ * NW * 16 == TQ && (!COLS_P || TP >= 128) && (!COLS_Q || TQ >= 128), "");
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[NST * STAGE];
+    const int lane = threadIdx.x & 63, i32 = lane & 31, hh = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wp = wave / WQ, wq = wave % WQ;
+    const int P = OP == GROUPED_FWD ? a.n_out : a.n_in;                               // results per row of the output
+    // XCD-aware order: consecutive workgroups go to the eight XCDs in turn; each takes a run of tiles, in blocks of four tiles
+    // along Q whose workgroups read the same rows on the other side
+    int tp, group, begin, end, q0, last_q;
+    if constexpr (OP == GROUPED_WGRAD) {
+        const int total = tiles_p * tiles_q * a.g.n, per = (total + 7) / 8, id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+        if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
+        group = id / (tiles_p * tiles_q);
+        const int t = id - group * tiles_p * tiles_q;
+        tp = t / tiles_q;
+        q0 = (t - tp * tiles_q) * TQ;
+        last_q = a.n_out;
+        begin = group_edge(a.g, group);
+        end = group_edge(a.g, group + 1);
+    } else {
+        const Tiles all = scan_tiles(a.g, TQ);
+        const int total = all.total * tiles_p, per = (total + 7) / 8;
+        const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+        if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
+        const int block = id / (4 * tiles_p), in = id - block * 4 * tiles_p, height = min(4, all.total - 4 * block);
+        tp = in / height;
+        const Tile t = tile_at(a.g, all, TQ, 4 * block + in - tp * height);
+        group = t.group;
+        q0 = t.begin;
+        last_q = t.end;
+        begin = end = 0;
+    }
+    const int K = OP == GROUPED_FWD ? a.n_in : OP == GROUPED_DGRAD ? a.n_out : max(end - begin, 0);
+    const int p0 = tp * (SWIGLU ? TP / 2 : TP), ns = (K + BK - 1) / BK;
+    const uint64_t zero = (uint64_t)(uintptr_t)zeros;
+    const uint64_t weights = (uint64_t)(uintptr_t)a.b + (uint64_t)group * a.n_out * a.n_in * (SWIGLU ? 4 : 2);
+
+    // Load i of this wave, P's first: from[i] is this lane's 16 bytes in the next stage to load; inside says whether they are
+    // any of the operand's, left is how far the sum goes from there.
+    constexpr int RP = 512 / TP, RQ = 512 / TQ;              // columns: rows per load
+    const int chunk = (lane & 3) ^ (lane >> 4 & 3);          // rows: this lane's 8 of a step
+    uint64_t from[LOADS];
+    int left[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const bool is_p = i < LP;
+        const int l = is_p ? wave * LP + i : wave * LQ + i - LP;
+        if (is_p ? !COLS_P : !COLS_Q) {
+            const int r = 16 * l + (lane >> 2);
+            int row;
+            if (is_p) {
+                const int n = SWIGLU ? (r >> 6) * 32 + (r & 31) : r;
+                row = p0 + n < P ? (SWIGLU && (r >> 5 & 1) ? P : 0) + p0 + n : -1;
+            } else {
+                const int p = q0 + r;
+                row = p >= last_q ? -1 : OP == GROUPED_FWD ? in_row(a.g, p, a.a_rows) : out_row(a.g, p, a.a_rows);
+            }
+            from[i] = (is_p ? weights : (uint64_t)(uintptr_t)a.a) + 2 * ((uint64_t)(uint32_t)max(row, 0) * (uint32_t)K + 8 * chunk);
+            left[i] = row < 0 ? 0 : K - 8 * chunk;
+        } else {
+            const int rows = is_p ? RP : RQ, per_row = 64 / rows, r = l * rows + lane / per_row, s = lane % per_row;
+            const int c = ((int)((s >> 1) ^ swizzle(r)) << 1 | (s & 1)) * 8 + (is_p ? p0 : q0);      // first of 8 columns
+            const int cols = is_p ? P : a.n_out;
+            left[i] = c < cols ? K - r : 0;
+            from[i] = 2 * (uint64_t)c + (OP == GROUPED_DGRAD ? weights + 2 * (uint64_t)r * (uint32_t)cols
+                                                              : (uint64_t)(uintptr_t)(is_p ? a.a : a.b));
         }
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(las_ptr)ring;
+    int step = 0;                                            // the sum's position of the stage to load next
+    uint32_t idst = lds0;
+    auto issue = [&](int i) {                                // i: load of this wave (compile-time)
+        const bool is_p = i < LP;
+        uint64_t at = from[i];
+        bool in = step < left[i];
+        if constexpr (OP == GROUPED_WGRAD) {
+            // the rows of this load's positions, through the scalar cache: no wait for the loads under way
+            const int rows = is_p ? RP : RQ, l = is_p ? wave * LP + i : wave * LQ + i - LP, top = a.g.rows - 1;
+            int row = -1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j >= rows) continue;
+                const int p = min(begin + step + l * rows + j, top), limit = is_p ? a.a_rows : a.b_rows;
+                const int32_t *index = is_p ? a.g.in_index : a.g.out_index;
+                int r = p;
+                if (index) r = reinterpret_cast<const __attribute__((address_space(4))) int32_t *>(reinterpret_cast<uintptr_t>(index))[p];
+                if (is_p && index && r >= 0 && a.g.in_div > 1) r = (int)(__umulhi((uint32_t)r, a.g.div_mul) >> a.g.div_shift);
+                if ((unsigned)r >= (unsigned)limit) r = -1;
+                row = lane / (64 / rows) == j ? r : row;
+            }
+            in = in && row >= 0;
+            at += 2 * (uint64_t)(uint32_t)row * (uint32_t)(is_p ? P : a.n_out);
+        }
+        const int l = is_p ? wave * LP + i : TP / 16 + wave * LQ + i - LP;
+        load_to_lds(in ? at : zero, idst + l * 1024u);
+        if constexpr (OP == GROUPED_FWD) from[i] += 2 * BK;
+        else if constexpr (OP == GROUPED_DGRAD) from[i] += is_p ? 2 * BK * (uint64_t)(uint32_t)P : 2 * BK;
+    };
+    auto next_stage = [&]() {
+        step += BK;
+        idst = idst == lds0 + (NST - 1) * STAGE ? lds0 : idst + STAGE;
+    };
+    f32x16_t acc[FP][FQ];
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+#pragma unroll
+        for (int j = 0; j < FQ; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+    // Fragment n of a 16-wide slice: lane l has its row (column) l % 32 and 8 (l / 32) .. + 7 of the sum.
+    const int tr = 8 * hh + (lane >> 2 & 3);                 // columns: row of this lane's four values of the first read
+    uint4 fp[2][FP], fq[2][FQ];
+    auto read_one = [&](uint32_t stage, int kk, int b, int n) {
+        const bool is_p = n < FP;
+        const int f = is_p ? wp * FP + n : wq * FQ + n - FP;
+        const uint32_t base = stage + (is_p ? 0 : TP * 64);
+        uint4 v;
+        if (is_p ? !COLS_P : !COLS_Q) {
+            const uint32_t c = (uint32_t)((2 * kk + hh) ^ (i32 >> 2 & 3));
+            v = __builtin_bit_cast(uint4, *(las_u32x4)(uintptr_t)(base + (f * 32 + i32) * 64 + c * 16));
+        } else {
+            const uint32_t pitch = 2 * (is_p ? TP : TQ), u = (uint32_t)(2 * f + (lane >> 4 & 1)) ^ swizzle(lane >> 2);
+            const uint32_t at = base + (16 * kk + tr) * pitch + u * 32 + 8 * (lane & 3);
+            const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((las_s16x4)(uintptr_t)at);
+            const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((las_s16x4)(uintptr_t)(at + 4 * pitch));
+            const uint2 l2 = __builtin_bit_cast(uint2, lo), h2 = __builtin_bit_cast(uint2, hi);
+            v = make_uint4(l2.x, l2.y, h2.x, h2.y);
+        }
+        if (is_p) fp[b][n] = v;
+        else fq[b][n - FP] = v;
+    };
+    // The products of one slice (buffer b). Between them go the reads of the next slice and part `part` of 2 of a stage's loads,
+    // so that the matrix cores have work while these are issued.
+    auto slice = [&](int b, uint32_t next, int nkk, int part) {
+        constexpr int M = FP * FQ, NR = FP + FQ;
+        const int l0 = part * LOADS / 2, nl = (part + 1) * LOADS / 2 - l0;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            acc[m / FQ][m % FQ] = mfma32(fp[b][m / FQ], fq[b][m % FQ], acc[m / FQ][m % FQ]);
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+                if (n >= m * 2 * NR / M && n < (m + 1) * 2 * NR / M) read_one(next, nkk, b ^ 1, n);      // in the first half
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                if (i >= l0 + m * nl / M && i < l0 + (m + 1) * nl / M) issue(i);                        // towards the end
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // All but one and a half of the ring's stages are loaded ahead. Before a stage's second slice: wait for the next stage (those
+    // after it stay under way) and for the workgroup; from then on nobody reads the present stage, and it takes the loads of
+    // the stage NST further on.
+    if (ns > 0) {
+#pragma unroll
+        for (int s = 0; s < NST - 1; ++s) {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) issue(i);
+            next_stage();
+        }
+#pragma unroll
+        for (int i = 0; i < LOADS / 2; ++i) issue(i);
+        wait_stage<(NST - 2) * LOADS + LOADS / 2>();
+        uint32_t here = lds0;
+#pragma unroll
+        for (int n = 0; n < FP + FQ; ++n) read_one(here, 0, 0, n);
+        for (int s = 0; s < ns; ++s) {
+            slice(0, here, 1, 1);
+            next_stage();
+            here = here == lds0 + (NST - 1) * STAGE ? lds0 : here + STAGE;
+            wait_stage<(NST - 2) * LOADS>();
+            slice(1, here, 0, 0);                            // behind the last stage: a read of zeros, not used
+        }
+        wait_stage<0>();
+    }
+    // Lane l has column l % 32 of a fragment of results, P's rows 8 (v / 4) + 4 (l / 32) + v % 4.
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+        const int q = q0 + (wq * FQ + j) * 32 + i32;
+        int64_t row = -1;
+        if (q < last_q)
+            row = OP == GROUPED_FWD ? out_row(a.g, q, a.out_rows) : OP == GROUPED_DGRAD ? in_slot(a.g, q, a.out_rows)
+                                                                                      : (int64_t)group * a.n_out + q;
+        if (row < 0) continue;
+#pragma unroll
+        for (int i = 0; i < FP; i += SWIGLU ? 2 : 1)
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4) {
+                const int n = p0 + (SWIGLU ? (wp * FP + i) / 2 : wp * FP + i) * 32 + 8 * v4 + 4 * hh;
+                if (n >= P) continue;
+                f32x4_t y;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    y[v] = SWIGLU ? swiglu(acc[i][j][4 * v4 + v], acc[i + (SWIGLU ? 1 : 0)][j][4 * v4 + v]) : acc[i][j][4 * v4 + v];
+                const int64_t o = row * P + n;
+                uint2 *half = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + o);
+                f32x4_t *full = reinterpret_cast<f32x4_t *>(static_cast<float *>(a.out) + o);
+                if (OP == GROUPED_WGRAD && a.accumulate) {
+                    if (a.out_bf16) {
+                        const uint2 w = *half;
+                        y += f32x4_t{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                                     __uint_as_float(w.y & 0xFFFF0000u)};
+                    } else {
+                        y += *full;
+                    }
+                }
+                if (a.out_bf16) *half = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+                else *full = y;
+            }
+    }
 }
 
 template <bool SWIGLU> __global__ __launch_bounds__(256) void k_q4(Q4Args a) {
@@ -140,14 +356,31 @@ bool fits(int64_t x, int64_t y, int64_t z, int threads) {
 
 namespace moe {
 
-hipError_t launch_grouped(int op, const GroupedArgs &a, hipStream_t st) {
-    const int64_t tn = (a.n_out + TILE - 1) / TILE, tk = (a.n_in + TILE - 1) / TILE, tr = most_tiles(a.g, TILE);
-    if (!fits(tr, tn, tk, 256)) return hipErrorInvalidConfiguration;
-    if (op == GROUPED_WGRAD) hipLaunchKernelGGL(k_weights, dim3(a.g.n, tk, tn), dim3(256), 0, st, a);
-    else if (op == GROUPED_DGRAD) hipLaunchKernelGGL((k_rows<GROUPED_DGRAD, false>), dim3(tr, tk), dim3(256), 0, st, a);
-    else if (a.swiglu) hipLaunchKernelGGL((k_rows<GROUPED_FWD, true>), dim3(tr, tn), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_rows<GROUPED_FWD, false>), dim3(tr, tn), dim3(256), 0, st, a);
+template <int OP, int FP, int FQ, int WP, int WQ, int NST, bool SWIGLU>
+static hipError_t launch_tile(const GroupedArgs &a, hipStream_t st) {
+    constexpr int TP = 32 * FP * WP / (SWIGLU ? 2 : 1), TQ = 32 * FQ * WQ, threads = 64 * WP * WQ;
+    const int64_t tp = ((OP == GROUPED_FWD ? a.n_out : a.n_in) + TP - 1) / TP;
+    const int64_t tq = OP == GROUPED_WGRAD ? (a.n_out + TQ - 1) / TQ : most_tiles(a.g, TQ);
+    const int64_t blocks = (tp * tq * (OP == GROUPED_WGRAD ? a.g.n : 1) + 7) / 8 * 8;
+    if (!fits(blocks, 1, 1, threads)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((k_tile<OP, FP, FQ, WP, WQ, NST, SWIGLU>), dim3((unsigned)blocks), dim3(threads), 0, st, a, (int)tp, (int)tq);
     return hipGetLastError();
+}
+
+template <int OP, bool SWIGLU> static hipError_t launch_op(const GroupedArgs &a, hipStream_t st) {
+    if constexpr (OP == GROUPED_WGRAD) return launch_tile<OP, 4, 2, 2, 2, 3, false>(a, st);
+    else {
+        const int rows = (a.g.rows + a.g.n - 1) / a.g.n;
+        if (rows >= 192) return launch_tile<OP, 4, 4, 2, 2, 5, SWIGLU>(a, st);
+        if (rows >= 48) return launch_tile<OP, 4, 2, 2, 2, 3, SWIGLU>(a, st);
+        return launch_tile<OP, 2, 1, 2, 2, 4, SWIGLU>(a, st);
+    }
+}
+
+hipError_t launch_grouped(int op, const GroupedArgs &a, hipStream_t st) {
+    if (op == GROUPED_WGRAD) return launch_op<GROUPED_WGRAD, false>(a, st);
+    if (op == GROUPED_DGRAD) return launch_op<GROUPED_DGRAD, false>(a, st);
+    return a.swiglu ? launch_op<GROUPED_FWD, true>(a, st) : launch_op<GROUPED_FWD, false>(a, st);
 }
 
 hipError_t launch_q4(const Q4Args &a, hipStream_t st) {

@@ -16,7 +16,7 @@ __device__ __forceinline__ int in_row(const Groups &g, int p, int n_rows) {
     int r = p;
     if (g.in_index) {
         r = g.in_index[p];
-        if (r >= 0 && g.in_div > 1) r = (int)((uint32_t)r / (uint32_t)g.in_div);
+        if (r >= 0 && g.in_div > 1) r = (int)(__umulhi((uint32_t)r, g.div_mul) >> g.div_shift);
     }
     return (unsigned)r < (unsigned)n_rows ? r : -1;
 }
@@ -36,34 +36,41 @@ struct Tile {
     int group, begin, end;
 };
 
-// Tile number `item` when every group is cut into tiles of up to `height` positions, groups in order; false behind the last.
-// Every wave of a workgroup finds it for itself: a lane sums the tiles of a run of groups, a scan over the lanes finds the
-// lane whose run holds the item.
-__device__ __forceinline__ bool find_tile(const Groups &g, int height, int item, Tile &t) {
-    if (!g.offsets) {
-        t.group = 0;
-        t.begin = item * height;
-        t.end = min(t.begin + height, g.rows);
-        return t.begin < g.rows;
-    }
-    const int lane = threadIdx.x & 63, per = (g.n + 63) / 64, g0 = min(lane * per, g.n), g1 = min(g0 + per, g.n);
-    int sum = 0, b = group_edge(g, g0);
-    for (int i = g0; i < g1; ++i) {
+// The groups cut into tiles of up to `height` positions, in order. Every wave finds tiles for itself: a lane has the tiles of a
+// run of groups, and a scan over the lanes tells whose run holds a tile.
+struct Tiles {
+    int g0, g1, sum, upto, total;        // this lane's groups, their tiles, those up to their end; all tiles
+};
+__device__ __forceinline__ int tiles_of(int b, int e, int height) { return e > b ? (e - b + height - 1) / height : 0; }
+
+__device__ __forceinline__ Tiles scan_tiles(const Groups &g, int height) {
+    Tiles t;
+    const int lane = threadIdx.x & 63, per = (g.n + 63) / 64;
+    t.g0 = min(lane * per, g.n);
+    t.g1 = min(t.g0 + per, g.n);
+    t.sum = 0;
+    int b = group_edge(g, t.g0);
+    for (int i = t.g0; i < t.g1; ++i) {
         const int e = group_edge(g, i + 1);
-        if (e > b) sum += (e - b + height - 1) / height;
+        t.sum += tiles_of(b, e, height);
         b = e;
     }
-    int upto = sum;
+    t.upto = t.sum;
     for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(upto, o, 64);
-        if (lane >= o) upto += v;
+        const int v = __shfl_up(t.upto, o, 64);
+        if (lane >= o) t.upto += v;
     }
-    const unsigned long long here = __ballot(item >= upto - sum && item < upto);
-    if (!here) return false;
-    int left = item - (upto - sum), found[3] = {0, 0, 0};
-    b = group_edge(g, g0);
-    for (int i = g0; i < g1; ++i) {
-        const int e = group_edge(g, i + 1), n = e > b ? (e - b + height - 1) / height : 0;
+    t.total = __builtin_amdgcn_readlane(t.upto, 63);
+    return t;
+}
+
+// Tile `item`, 0 <= item < total.
+__device__ __forceinline__ Tile tile_at(const Groups &g, const Tiles &t, int height, int item) {
+    int left = item - (t.upto - t.sum), found[3] = {0, 0, 0};
+    const int who = __ffsll(__ballot(left >= 0 && left < t.sum)) - 1;
+    int b = group_edge(g, t.g0);
+    for (int i = t.g0; i < t.g1; ++i) {
+        const int e = group_edge(g, i + 1), n = tiles_of(b, e, height);
         if (left >= 0 && left < n) {
             found[0] = i;
             found[1] = b + left * height;
@@ -72,14 +79,19 @@ __device__ __forceinline__ bool find_tile(const Groups &g, int height, int item,
         left -= n;
         b = e;
     }
-    const int who = __ffsll(here) - 1;
-    t.group = __builtin_amdgcn_readlane(found[0], who);
-    t.begin = __builtin_amdgcn_readlane(found[1], who);
-    t.end = __builtin_amdgcn_readlane(found[2], who);
+    return Tile{__builtin_amdgcn_readlane(found[0], who), __builtin_amdgcn_readlane(found[1], who),
+                __builtin_amdgcn_readlane(found[2], who)};
+}
+
+// Tile number `item`; false behind the last.
+__device__ __forceinline__ bool find_tile(const Groups &g, int height, int item, Tile &t) {
+    const Tiles all = scan_tiles(g, height);
+    if (item >= all.total) return false;
+    t = tile_at(g, all, height, item);
     return true;
 }
 
-// Tiles that find_tile can have at most: whole ones, and one more for each group with rows.
+// Tiles that there can be at most: whole ones, and one more for each group with rows.
 inline int64_t most_tiles(const Groups &g, int height) {
     return g.offsets ? (int64_t)g.rows / height + (g.n < g.rows ? g.n : g.rows) : ((int64_t)g.rows + height - 1) / height;
 }

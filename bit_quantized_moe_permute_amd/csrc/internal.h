@@ -152,6 +152,7 @@ struct Groups {
     const int32_t *offsets;              // NULL: one group of all rows
     const int32_t *in_index;             // optional
     int in_div;
+    uint32_t div_mul, div_shift;         // i / in_div = umulhi(i, div_mul) >> div_shift, 0 <= i < 2^31, in_div > 1
     const int32_t *out_index;            // optional
 };
 struct GroupedArgs {
