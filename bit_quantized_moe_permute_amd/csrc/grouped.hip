@@ -1,60 +1,13 @@
-// Products over rows grouped by expert (moe_grouped_linear, moe_grouped_dgrad, moe_grouped_wgrad, moe_q4_linear):
+// Products over rows grouped by expert (moe_grouped_linear, moe_grouped_dgrad, moe_grouped_wgrad):
 //
 //   forward           out[o][n] = sum_k x[r][k] W_g[n][k]
 //   input's gradient  dx[i][k]  = sum_n dy[o][n] W_g[n][k]
 //   weights' gradient dW_g[n][k] = sum over the positions of g of dy[o][n] x[r][k]
-//
-// One workgroup computes 64 x 64 results from fp32 tiles in LDS, 16 steps of the sum at a time.
 #include "groups.h"
 
 using namespace moe;
 
 namespace {
-
-constexpr int TILE = 64, STEP = 16;
-
-__device__ __forceinline__ float at(const uint16_t *p, int64_t i) { return bf16_bits_to_f32(p[i]); }
-
-
-__device__ __forceinline__ float q4_scale(const Q4Args &a, int64_t i) {
-    if (a.scale_kind == Q4_F32) return static_cast<const float *>(a.scale)[i];
-    const uint16_t v = static_cast<const uint16_t *>(a.scale)[i];
-    return a.scale_kind == Q4_BF16 ? bf16_bits_to_f32(v) : f16_bits_to_f32(v);
-}
-
-// Weight row n, column k of matrix m.
-__device__ __forceinline__ float q4_at(const Q4Args &a, int64_t row, int k) {
-    const int64_t s = row * (a.K / a.group) + k / a.group;
-    const int q = a.codes[row * (a.K / 2) + k / 2] >> (k & 1 ? 4 : 0) & 15, z = a.zero ? a.zero[s] & 15 : 8;
-    return (float)(q - z) * q4_scale(a, s);
-}
-
-// R x C tile of products of load_a(row, k) and load_b(col, k), k < K; accumulates into acc[4][4].
-template <typename A, typename B>
-__device__ __forceinline__ void products(int K, A load_a, B load_b, float (&acc)[4][4]) {
-    __shared__ float as[STEP][TILE], bs[STEP][TILE];
-    const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
-    for (int k0 = 0; k0 < K; k0 += STEP) {
-        for (int e = threadIdx.x; e < STEP * TILE; e += 256) {
-            const int r = e / STEP, k = e % STEP;
-            as[k][r] = k0 + k < K ? load_a(r, k0 + k) : 0.f;
-            bs[k][r] = k0 + k < K ? load_b(r, k0 + k) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < STEP; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __fmaf_rn(as[k][tr * 4 + i], bs[k][tc * 4 + j], acc[i][j]);
-        __syncthreads();
-    }
-}
-
-__device__ __forceinline__ void store(void *out, int bf16, int64_t i, float v) {
-    if (bf16) static_cast<__bf16 *>(out)[i] = (__bf16)v;
-    else static_cast<float *>(out)[i] = v;
-}
 
 typedef __attribute__((address_space(3))) void *las_ptr;
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -324,34 +277,6 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
     }
 }
 
-template <bool SWIGLU> __global__ __launch_bounds__(256) void k_q4(Q4Args a) {
-    Tile t;
-    if (!find_tile(a.g, TILE, blockIdx.x, t)) return;
-    const int n0 = blockIdx.y * TILE;
-    const int64_t w = (int64_t)t.group * a.N * (SWIGLU ? 2 : 1);
-    auto load_a = [&](int r, int k) {
-        const int p = t.begin + r, row = p < t.end ? in_row(a.g, p, a.x_rows) : -1;
-        return row < 0 ? 0.f : at(a.x, (int64_t)row * a.K + k);
-    };
-    float acc[2][4][4] = {};
-    for (int h = 0; h < (SWIGLU ? 2 : 1); ++h)
-        products(a.K, load_a, [&](int c, int k) { return n0 + c < a.N ? q4_at(a, w + (int64_t)h * a.N + n0 + c, k) : 0.f; }, acc[h]);
-    const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
-    for (int i = 0; i < 4; ++i) {
-        const int p = t.begin + tr * 4 + i, row = p < t.end ? out_row(a.g, p, a.out_rows) : -1;
-        if (row < 0) continue;
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + tc * 4 + j;
-            if (n < a.N) store(a.out, a.out_bf16, (int64_t)row * a.N + n, SWIGLU ? swiglu(acc[0][i][j], acc[1][i][j]) : acc[0][i][j]);
-        }
-    }
-}
-
-// A grid whose threads and blocks a launch can count (2^32 threads, 2^16 blocks along y and z).
-bool fits(int64_t x, int64_t y, int64_t z, int threads) {
-    return x * threads < ((int64_t)1 << 32) && y < 65536 && z < 65536;
-}
-
 }  // namespace
 
 namespace moe {
@@ -362,7 +287,7 @@ static hipError_t launch_tile(const GroupedArgs &a, hipStream_t st) {
     const int64_t tp = ((OP == GROUPED_FWD ? a.n_out : a.n_in) + TP - 1) / TP;
     const int64_t tq = OP == GROUPED_WGRAD ? (a.n_out + TQ - 1) / TQ : most_tiles(a.g, TQ);
     const int64_t blocks = (tp * tq * (OP == GROUPED_WGRAD ? a.g.n : 1) + 7) / 8 * 8;
-    if (!fits(blocks, 1, 1, threads)) return hipErrorInvalidConfiguration;
+    if (!grid_fits(blocks, threads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((k_tile<OP, FP, FQ, WP, WQ, NST, SWIGLU>), dim3((unsigned)blocks), dim3(threads), 0, st, a, (int)tp, (int)tq);
     return hipGetLastError();
 }
@@ -381,14 +306,6 @@ hipError_t launch_grouped(int op, const GroupedArgs &a, hipStream_t st) {
     if (op == GROUPED_WGRAD) return launch_op<GROUPED_WGRAD, false>(a, st);
     if (op == GROUPED_DGRAD) return launch_op<GROUPED_DGRAD, false>(a, st);
     return a.swiglu ? launch_op<GROUPED_FWD, true>(a, st) : launch_op<GROUPED_FWD, false>(a, st);
-}
-
-hipError_t launch_q4(const Q4Args &a, hipStream_t st) {
-    const int64_t tr = most_tiles(a.g, TILE), tn = (a.N + TILE - 1) / TILE;
-    if (!fits(tr, tn, 1, 256)) return hipErrorInvalidConfiguration;
-    if (a.swiglu) hipLaunchKernelGGL(k_q4<true>, dim3(tr, tn), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL(k_q4<false>, dim3(tr, tn), dim3(256), 0, st, a);
-    return hipGetLastError();
 }
 
 }  // namespace moe

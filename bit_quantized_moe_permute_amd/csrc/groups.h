@@ -96,6 +96,9 @@ inline int64_t most_tiles(const Groups &g, int height) {
     return g.offsets ? (int64_t)g.rows / height + (g.n < g.rows ? g.n : g.rows) : ((int64_t)g.rows + height - 1) / height;
 }
 
+// Whether a launch can count its threads (in 32 bits).
+inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
+
 __device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
 
 }  // namespace moe
