@@ -319,6 +319,27 @@ def test_q4(m, shape, group, zero, scale, swiglu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("swiglu", [False, True], ids=["plain", "swiglu"])
+@pytest.mark.parametrize("group,zero,scale", [(32, True, torch.float16), (64, False, F32), (128, True, BF16)],
+                         ids=lambda v: str(v).replace("torch.", ""))
+@pytest.mark.parametrize("shape", [(1, 0, 1, 128, 32780), (9, 0, 1, 1408, 32801), (16, 0, 1, 256, 33000), (23, 0, 1, 384, 32770),
+                                   (33, 0, 1, 640, 32780), (70, 0, 1, 256, 32790), (40, 4, 40, 256, 890), (150, 4, 30, 128, 1300),
+                                   (300, 2, 20, 896, 1666)], ids=lambda s: "x".join(map(str, s)))
+def test_q4_many_weights(m, shape, group, zero, scale, swiglu):
+    """Matrices of many rows or many of them, with one to many rows of x to a group."""
+    c = Case(*shape, seed=10, swiglu=swiglu)
+    run_q4(m, c, Q4(c, group, zero, scale), F32, f"q4 {shape} group {group} zero={zero} {scale} swiglu={swiglu}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group,K", [(32, 96), (64, 192), (32, 1056)])
+@pytest.mark.parametrize("T", [2, 20, 70])
+def test_q4_many_weights_in_odd_rows(m, T, K, group):
+    c = Case(T, 0, 1, K, 32780, seed=10)
+    run_q4(m, c, Q4(c, group, True, torch.float16), BF16, f"q4 {T}x{K} group {group}")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("group,K", [(32, 32), (32, 96), (32, 1056), (64, 64), (64, 320)])
 @pytest.mark.parametrize("T", [1, 3, 20, 70])
 def test_q4_short_and_odd_rows(m, T, K, group):
