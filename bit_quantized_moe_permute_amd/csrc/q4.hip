@@ -56,41 +56,65 @@ __device__ __forceinline__ uint4 reorder(uint4 v) {
                       __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u));
 }
 
-// Scales (of type KIND) and zero points of one row's groups in a chunk, as they are loaded. TAIL: K is no multiple of a chunk;
-// groups behind the row's end repeat its last one (their products are zero).
-template <int G, int KIND, bool TAIL> struct Params {
+// 16 rows of a matrix, one to each lane l % 16: the first one's address is the same for all lanes, the others' distance from it a
+// 32-bit number, so that loads need no address arithmetic in vector registers.
+template <int G, int KIND> struct Rows {
+    static constexpr int SB = KIND == Q4_F32 ? 4 : 2;
+    const uint8_t *codes, *zero;
+    const char *scale;
+    uint32_t row, lane_codes;                                // this lane's row behind the first; its 16 bytes of a chunk
+
+    // first: row of the stack, n: this lane's row behind it
+    __device__ __forceinline__ void set(const Q4Args &a, int64_t first, int n) {
+        codes = a.codes + first * (a.K / 2);
+        scale = static_cast<const char *>(a.scale) + first * (a.K / G) * SB;
+        zero = a.zero ? a.zero + first * (a.K / G) : nullptr;
+        row = n;
+        lane_codes = n * (uint32_t)(a.K / 2) + 16 * (threadIdx.x >> 4 & 3);
+    }
+};
+
+// A chunk of 16 rows: codes, and the scales and zero points of its groups, as they are loaded.
+template <int G, int KIND> struct Chunk {
     static constexpr int SB = KIND == Q4_F32 ? 4 : 2, NG = CHUNK / G, WORDS = (NG * SB + 3) / 4;
+    u32x4_t codes;
     uint32_t scale[WORDS], zero;
 
-    // i: the chunk's first group (index into scale and zero); left: groups from there to the row's end
-    __device__ __forceinline__ void load(const Q4Args &a, int64_t i, int left) {
-        const char *from = static_cast<const char *>(a.scale) + i * SB;
+    // c: number of the chunk. Where the row ends inside it, what lies behind repeats its last codes and groups (their x is zero).
+    __device__ __forceinline__ void load_codes(const Q4Args &a, const Rows<G, KIND> &r, int c) {
+        uint32_t at = r.lane_codes;
+        if (NG > 1 && a.K / G - c * NG < NG) at -= max(16 * (int)(threadIdx.x >> 4 & 3) - (a.K / 2 - c * (CHUNK / 2) - 16), 0);
+        codes = *reinterpret_cast<const u32x4_t *>(r.codes + (int64_t)c * (CHUNK / 2) + at);
+    }
+    __device__ __forceinline__ void load(const Q4Args &a, const Rows<G, KIND> &r, int c) {
+        load_codes(a, r, c);
+        const int groups = a.K / G, left = groups - c * NG;
+        const char *s = r.scale + (int64_t)c * NG * SB;
+        const uint8_t *z = r.zero + (int64_t)c * NG;
+        const uint32_t g = r.row * (uint32_t)groups;
         zero = 0x08080808u;
-        if constexpr (!TAIL) {                               // at once, from an address aligned to elements
-            if constexpr (NG * SB == 2) {
-                scale[0] = *reinterpret_cast<const uint16_t *>(from);
-            } else {
-                __builtin_memcpy(scale, __builtin_assume_aligned(from, SB), NG * SB);
-            }
-            if (a.zero) {
-                if constexpr (NG == 4) __builtin_memcpy(&zero, a.zero + i, 4);
+        if (NG == 1 || left >= NG) {                         // at once, from addresses aligned to elements
+            if constexpr (NG * SB == 2) scale[0] = *reinterpret_cast<const uint16_t *>(s + g * SB);
+            else __builtin_memcpy(scale, __builtin_assume_aligned(s + g * SB, SB), NG * SB);
+            if (r.zero) {
+                if constexpr (NG == 4) __builtin_memcpy(&zero, z + g, 4);
                 else if constexpr (NG == 2) {
-                    uint16_t z;
-                    __builtin_memcpy(&z, a.zero + i, 2);
-                    zero = z;
-                } else zero = a.zero[i];
+                    uint16_t v;
+                    __builtin_memcpy(&v, z + g, 2);
+                    zero = v;
+                } else zero = z[g];
             }
         } else {
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
-                const int at = min(j, left - 1);
-                if constexpr (SB == 4) scale[j] = reinterpret_cast<const uint32_t *>(from)[at];
-                else scale[j / 2] = (j & 1 ? scale[j / 2] : 0u) | (uint32_t)reinterpret_cast<const uint16_t *>(from)[at] << (16 * (j & 1));
+                const uint32_t i = g + min(j, left - 1);
+                if constexpr (SB == 4) scale[j] = *reinterpret_cast<const uint32_t *>(s + i * SB);
+                else scale[j / 2] = (j & 1 ? scale[j / 2] : 0u) | (uint32_t)*reinterpret_cast<const uint16_t *>(s + i * SB) << (16 * (j & 1));
             }
-            if (a.zero) {
+            if (r.zero) {
                 zero = 0;
 #pragma unroll
-                for (int j = 0; j < NG; ++j) zero |= (uint32_t)a.zero[i + min(j, left - 1)] << (8 * j);
+                for (int j = 0; j < NG; ++j) zero |= (uint32_t)z[g + min(j, left - 1)] << (8 * j);
             }
         }
     }
@@ -100,9 +124,56 @@ template <int G, int KIND, bool TAIL> struct Params {
         return KIND == Q4_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h & 0xFFFFu);
     }
     // -(16 + zero point) as a pair of bf16
-    __device__ __forceinline__ uint32_t offset_of(int j) const {
-        const uint32_t z = (zero >> (8 * j) & 15u) << 3;
-        return 0xC180C180u | z | z << 16;
+    __device__ __forceinline__ uint32_t offset_of(int j) const { return (zero >> (8 * j) & 15u) * 0x80008u + 0xC180C180u; }
+};
+
+// Scales and zero points of 32 groups of 16 rows: lane l has 8 (l / 16) .. + 7 of row l % 16. Read chunk by chunk, a few bytes of
+// sixteen rows at a time, they would come out of the caches as whole lines again and again, since the codes that stream past them
+// push them out of the L1.
+template <int G, int KIND> struct Block {
+    using C = Chunk<G, KIND>;
+    static constexpr int SB = C::SB, NG = C::NG, GROUPS = 32, CHUNKS = GROUPS / NG;
+    uint32_t scale[2 * SB], zero[2];
+
+    // number b of a row's blocks; what lies behind the row's end is not used
+    __device__ __forceinline__ void load(const Q4Args &a, const Rows<G, KIND> &r, int64_t first, int64_t total, int b) {
+        const uint32_t at = r.row * (uint32_t)(a.K / G) + 8 * (threadIdx.x >> 4 & 3);
+        const char *s = r.scale + (int64_t)b * GROUPS * SB;
+        const uint8_t *z = r.zero + (int64_t)b * GROUPS;
+        zero[0] = zero[1] = 0x08080808u;
+        const int64_t left = total - first - (int64_t)b * GROUPS - at;       // groups from here to the end of the stack
+        if (__ballot(left < 8) == 0) {
+            __builtin_memcpy(scale, __builtin_assume_aligned(s + at * SB, SB), 8 * SB);
+            if (r.zero) __builtin_memcpy(zero, z + at, 8);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool in = j < left;
+            if constexpr (SB == 4) scale[j] = in ? reinterpret_cast<const uint32_t *>(s)[at + j] : 0u;
+            else scale[j / 2] = (j & 1 ? scale[j / 2] : 0u) | (in ? (uint32_t)reinterpret_cast<const uint16_t *>(s)[at + j] : 0u) << (16 * (j & 1));
+            if (r.zero && in) zero[j / 4] = (zero[j / 4] & ~(0xFFu << 8 * (j & 3))) | (uint32_t)z[at + j] << (8 * (j & 3));
+        }
+    }
+    // Those of chunk c to all lanes of its rows, u = c % 8 (compile-time).
+    __device__ __forceinline__ void to_chunk(C &to, const Q4Args &a, int u, int c) const {
+        const int from = 4 * ((c * NG % GROUPS / 8) * 16 + (threadIdx.x & 15));
+        auto word = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v); };
+        constexpr int W = C::WORDS;
+        if constexpr (NG * SB == 2) to.scale[0] = word(scale[u % 8 / 2]) >> (16 * (u & 1));
+        else
+#pragma unroll
+            for (int j = 0; j < W; ++j) to.scale[j] = word(scale[u * W % (2 * SB) + j]);
+        to.zero = a.zero ? word(zero[u * NG / 4 % 2]) >> (8 * (u * NG % 4)) : 0x08080808u;
+        const int left = a.K / G - c * NG;
+        if (NG > 1 && left < NG) {                           // nothing of the next row
+#pragma unroll
+            for (int j = 1; j < NG; ++j) {
+                if (j < left) continue;
+                if constexpr (SB == 4) to.scale[j] = 0;
+                else to.scale[j / 2] &= j & 1 ? 0xFFFFu : 0u;
+            }
+        }
     }
 };
 
@@ -111,18 +182,18 @@ __device__ __forceinline__ uint4 splat(uint32_t v) { return make_uint4(v, v, v, 
 // One chunk's products of R blocks of 16 weight rows with NB blocks of 16 rows of x into acc; x(t, s) is block t's operand of
 // columns 32 s .. + 31. (No branch may stand between a matrix instruction and the reading of its result: the compiler then loses
 // the wait between the two on one of the ways.)
-template <int R, int NB, typename P, typename X>
-__device__ __forceinline__ void chunk_products(const Unpack &unpack, const u32x4_t (&codes)[R], const P (&p)[R], X x, f32x4_t (&acc)[R][NB]) {
-    constexpr int STEPS = 4 / P::NG;                         // instructions per group
+template <int R, int NB, typename C, typename X>
+__device__ __forceinline__ void chunk_products(const Unpack &unpack, const C (&p)[R], X x, f32x4_t (&acc)[R][NB]) {
+    constexpr int STEPS = 4 / C::NG;                         // instructions per group
     uint32_t w[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) w[r][s] = codes[r][s];
+        for (int s = 0; s < 4; ++s) w[r][s] = p[r].codes[s];
         exchange(w[r]);
     }
 #pragma unroll
-    for (int j = 0; j < P::NG; ++j) {
+    for (int j = 0; j < C::NG; ++j) {
         f32x4_t d[R][NB];
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
@@ -182,7 +253,7 @@ __device__ __forceinline__ bool place(const Q4Args &a, int height, int rows, int
 // ---------------------------------------------------------------------------
 constexpr int FEW_WAVES = 8, FEW_AHEAD = 2;
 
-template <int R, int G, int KIND, bool TAIL, bool SWIGLU>
+template <int R, int G, int KIND, bool SWIGLU>
 __global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few(Q4Args a, int tiles_n) {
     static_assert(!SWIGLU || R == 2, "");
     constexpr int ROWS = SWIGLU ? 16 : 16 * R;               // results per position
@@ -191,44 +262,34 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few(Q4Args a, int tiles_n
     Tile t;
     int n0;
     if (!place(a, 16, ROWS, tiles_n, t, n0)) return;
-    const int xr = t.begin + i16 < t.end ? in_row(a.g, t.begin + i16, a.x_rows) : -1, x_end = xr < 0 ? 0 : a.K;
+    const int xr = t.begin + i16 < t.end ? in_row(a.g, t.begin + i16, a.x_rows) : -1, x_end = xr < 0 ? 0 : a.K - 8 * q;
     const uint16_t *x = a.x + (int64_t)max(xr, 0) * a.K + 8 * q;
-    const uint8_t *codes[R];
-    int64_t params[R];
-    const int groups = a.K / G;
+    Rows<G, KIND> rows[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int64_t row = (int64_t)t.group * a.N * (SWIGLU ? 2 : 1) +
-                            (SWIGLU ? (int64_t)r * a.N + min(n0 + i16, a.N - 1) : min(n0 + 16 * r + i16, a.N - 1));
-        codes[r] = a.codes + row * (a.K / 2);
-        params[r] = row * groups;
+        const int first = SWIGLU ? n0 : min(n0 + 16 * r, a.N - 1);
+        rows[r].set(a, ((int64_t)t.group * (SWIGLU ? 2 : 1) + (SWIGLU ? r : 0)) * a.N + first, min(first + i16, a.N - 1) - first);
     }
+    const int chunks = (a.K + CHUNK - 1) / CHUNK;
     const Unpack unpack;
     f32x4_t acc[R][1];
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[r][0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int c0 = wave * CHUNK; c0 < a.K; c0 += FEW_AHEAD * FEW_WAVES * CHUNK) {
-        u32x4_t w[FEW_AHEAD][R];
-        Params<G, KIND, TAIL> p[FEW_AHEAD][R];
+    for (int c0 = wave; c0 < chunks; c0 += FEW_AHEAD * FEW_WAVES) {
+        Chunk<G, KIND> p[FEW_AHEAD][R];
         uint4 v[FEW_AHEAD][4];
 #pragma unroll
         for (int u = 0; u < FEW_AHEAD; ++u) {
-            // a chunk behind the end reads the first one again, and its x is zeros
-            const int c = c0 + u * FEW_WAVES * CHUNK, at = c < a.K ? c : 0, end = c < a.K ? x_end : 0;
+            const int c = min(c0 + u * FEW_WAVES, chunks - 1);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int col = TAIL ? min(at + 32 * q, a.K - 32) : at + 32 * q;
-                w[u][r] = *reinterpret_cast<const u32x4_t *>(codes[r] + col / 2);
-                p[u][r].load(a, params[r] + at / G, groups - at / G);
-            }
+            for (int r = 0; r < R; ++r) p[u][r].load(a, rows[r], c);
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                v[u][s] = load_or_zeros(x + at + 32 * s, TAIL ? at + 32 * s + 8 * q < end : end > 0);
+            for (int s = 0; s < 4; ++s) v[u][s] = load_or_zeros(x + c * CHUNK + 32 * s, c * CHUNK + 32 * s < x_end);
         }
 #pragma unroll
         for (int u = 0; u < FEW_AHEAD; ++u) {
-            if (c0 + u * FEW_WAVES * CHUNK >= a.K) break;
-            chunk_products<R, 1>(unpack, w[u], p[u], [&](int, int s) { return reorder(v[u][s]); }, acc);
+            if (c0 + u * FEW_WAVES >= chunks) break;
+            chunk_products<R, 1>(unpack, p[u], [&](int, int s) { return reorder(v[u][s]); }, acc);
         }
     }
 #pragma unroll
@@ -253,19 +314,20 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few(Q4Args a, int tiles_n
 
 // ---------------------------------------------------------------------------
 // Many: a wave has two blocks of 16 weight rows (SwiGLU: 16 of gate and the same of up) along all of K, a workgroup four waves,
-// and up to 64 positions of a group, in one, two or four blocks of 16. Codes and parameters go straight to registers, AHEAD chunks ahead; the x of a chunk
-// passes through LDS, put into the order of unpack() on its way, 16-byte piece i of row r at i ^ r: sixteen rows' reads of one
-// piece column touch every bank once.
+// and up to 16 MAXB positions of a group, in one, two or four blocks of 16. Codes go straight to registers, AHEAD chunks ahead,
+// scales and zero points a block of 32 groups ahead; the x of a chunk passes through LDS, put into the order of unpack() on its
+// way, 16-byte piece i of row r at i ^ r: sixteen rows' reads of one piece column touch every bank once.
 // ---------------------------------------------------------------------------
-constexpr int MANY_WAVES = 4, MANY_ROWS = 32 * MANY_WAVES, MANY_BLOCKS = 4;
+constexpr int MANY_WAVES = 4, MANY_ROWS = 32 * MANY_WAVES;
 
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <int NB, int G, int KIND, bool TAIL, bool SWIGLU>
-__device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uint4 (*tile)[16 * MANY_BLOCKS][16]) {
-    constexpr int AHEAD = NB == 4 ? 2 : 4;                   // chunks of weights under way
+template <int NB, int G, int KIND, bool SWIGLU>
+__device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uint4 *lds) {
+    constexpr int AHEAD = NB == 4 ? 2 : 4;                   // chunks of codes under way
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
-    const int groups = a.K / G, chunks = (a.K + CHUNK - 1) / CHUNK;
+    uint4 (*tile)[16 * NB][16] = reinterpret_cast<uint4 (*)[16 * NB][16]>(lds);
+    const int chunks = (a.K + CHUNK - 1) / CHUNK;
     // this thread's part of x: rows threadIdx.x / 16 + 16 b, piece threadIdx.x % 16 of a chunk
     const int xi = threadIdx.x & 15, xr = threadIdx.x >> 4;
     const uint16_t *x[NB];
@@ -276,27 +338,23 @@ __device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uin
         x[b] = a.x + (int64_t)max(row, 0) * a.K + 8 * xi;
         x_end[b] = row < 0 ? 0 : a.K - 8 * xi;
     }
-    const uint8_t *codes[2];
-    int64_t params[2];
+    Rows<G, KIND> rows[2];
+    int64_t first_group[2];
+    const int64_t groups = (int64_t)a.g.n * a.N * (SWIGLU ? 2 : 1) * (a.K / G);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const int n = n0 + wave * (SWIGLU ? 16 : 32) + (SWIGLU ? 0 : 16 * r) + i16;
-        const int64_t row = ((int64_t)t.group * (SWIGLU ? 2 : 1) + (SWIGLU ? r : 0)) * a.N + min(n, a.N - 1);
-        codes[r] = a.codes + row * (a.K / 2);
-        params[r] = row * groups;
+        const int first = min(n0 + wave * (SWIGLU ? 16 : 32) + (SWIGLU ? 0 : 16 * r), a.N - 1);
+        const int64_t row = ((int64_t)t.group * (SWIGLU ? 2 : 1) + (SWIGLU ? r : 0)) * a.N + first;
+        rows[r].set(a, row, min(first + i16, a.N - 1) - first);
+        first_group[r] = row * (a.K / G);
     }
     const Unpack unpack;
-    u32x4_t w[AHEAD][2];
-    Params<G, KIND, TAIL> p[AHEAD][2];
+    Chunk<G, KIND> p[AHEAD][2];
+    Block<G, KIND> now[2], next[2];
     uint4 v[2][NB];
-    auto load_weights = [&](int u, int c) {                  // chunk c (behind the last: that one) into place u
-        const int at = min(c, chunks - 1) * CHUNK;
+    auto load_codes = [&](int u, int c) {                    // of chunk c, behind the last one that again
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int col = TAIL ? min(at + 32 * q, a.K - 32) : at + 32 * q;
-            w[u][r] = *reinterpret_cast<const u32x4_t *>(codes[r] + col / 2);
-            p[u][r].load(a, params[r] + at / G, groups - at / G);
-        }
+        for (int r = 0; r < 2; ++r) p[u][r].load_codes(a, rows[r], min(c, chunks - 1));
     };
     auto load_x = [&](int u, int c) {
 #pragma unroll
@@ -311,22 +369,33 @@ __device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uin
     for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int b = 0; b < NB; ++b) acc[r][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) next[r].load(a, rows[r], first_group[r], groups, 0);
     load_x(0, 0);
     load_x(1, 1);
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) load_weights(u, u);
+    for (int u = 0; u < AHEAD; ++u) load_codes(u, u);
     put_x(0);
     load_x(0, 2);
-    for (int c0 = 0; c0 < chunks; c0 += AHEAD) {
+    for (int c0 = 0; c0 < chunks; c0 += 8) {
+        if (c0 % Block<G, KIND>::CHUNKS == 0) {
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
+            for (int r = 0; r < 2; ++r) {
+                now[r] = next[r];
+                next[r].load(a, rows[r], first_group[r], groups, c0 / Block<G, KIND>::CHUNKS + 1);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
             const int c = c0 + u;
             if (c >= chunks) break;
             lds_barrier();                                   // this chunk's x is there, and nobody reads the one before it
             put_x((u + 1) & 1);
             load_x((u + 1) & 1, c + 3);
-            chunk_products<2, NB>(unpack, w[u], p[u], [&](int b, int s) { return tile[u & 1][16 * b + i16][(4 * s + q) ^ i16]; }, acc);
-            load_weights(u, c + AHEAD);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) now[r].to_chunk(p[u % AHEAD][r], a, u, c);
+            chunk_products<2, NB>(unpack, p[u % AHEAD], [&](int b, int s) { return tile[u & 1][16 * b + i16][(4 * s + q) ^ i16]; }, acc);
+            load_codes(u % AHEAD, c + AHEAD);
         }
     }
     // lane l's four values are positions 4 (l / 16) .. + 3 of weight row l % 16
@@ -344,54 +413,51 @@ __device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uin
         }
 }
 
-template <int G, int KIND, bool TAIL, bool SWIGLU>
-__global__ __launch_bounds__(64 * MANY_WAVES, 2) void k_many(Q4Args a, int tiles_n) {
-    __shared__ __attribute__((aligned(16))) uint4 tile[2][16 * MANY_BLOCKS][16];
+template <int MAXB, int G, int KIND, bool SWIGLU>
+__global__ __launch_bounds__(64 * MANY_WAVES, MAXB == 1 ? 3 : 2) void k_many(Q4Args a, int tiles_n) {
+    __shared__ __attribute__((aligned(16))) uint4 lds[2 * 16 * MAXB * 16];
     Tile t;
     int n0;
-    if (!place(a, 16 * MANY_BLOCKS, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS, tiles_n, t, n0)) return;
+    if (!place(a, 16 * MAXB, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS, tiles_n, t, n0)) return;
     const int blocks = (t.end - t.begin + 15) / 16;
-    if (blocks <= 1) many<1, G, KIND, TAIL, SWIGLU>(a, t, n0, tile);
-    else if (blocks == 2) many<2, G, KIND, TAIL, SWIGLU>(a, t, n0, tile);
-    else many<4, G, KIND, TAIL, SWIGLU>(a, t, n0, tile);
+    if (MAXB == 1 || blocks <= 1) many<1, G, KIND, SWIGLU>(a, t, n0, lds);
+    else if (MAXB == 2 || blocks == 2) many<MAXB == 1 ? 1 : 2, G, KIND, SWIGLU>(a, t, n0, lds);
+    else many<MAXB, G, KIND, SWIGLU>(a, t, n0, lds);
 }
 
 int64_t tiles(int N, int rows) { return (N + rows - 1) / rows; }
 
-template <int G, int KIND, bool TAIL, bool SWIGLU> hipError_t launch_many(const Q4Args &a, hipStream_t st) {
-    const int64_t tn = tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS), blocks = (most_tiles(a.g, 16 * MANY_BLOCKS) * tn + 7) / 8 * 8;
-    if (!grid_fits(blocks, 64 * MANY_WAVES)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_many<G, KIND, TAIL, SWIGLU>), dim3((unsigned)blocks), dim3(64 * MANY_WAVES), 0, st, a, (int)tn);
+template <int MAXB, int G, int KIND, bool SWIGLU> hipError_t launch_many(const Q4Args &a, hipStream_t st) {
+    constexpr int threads = 64 * MANY_WAVES;
+    const int64_t tn = tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS), blocks = (most_tiles(a.g, 16 * MAXB) * tn + 7) / 8 * 8;
+    if (!grid_fits(blocks, threads)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((k_many<MAXB, G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(threads), 0, st, a, (int)tn);
     return hipGetLastError();
 }
 
-template <int R, int G, int KIND, bool TAIL, bool SWIGLU> hipError_t launch_few(const Q4Args &a, hipStream_t st) {
+template <int R, int G, int KIND, bool SWIGLU> hipError_t launch_few(const Q4Args &a, hipStream_t st) {
     const int64_t tn = tiles(a.N, SWIGLU ? 16 : 16 * R), blocks = (most_tiles(a.g, 16) * tn + 7) / 8 * 8;
     if (!grid_fits(blocks, 64 * FEW_WAVES)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_few<R, G, KIND, TAIL, SWIGLU>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0, st, a, (int)tn);
+    hipLaunchKernelGGL((k_few<R, G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0, st, a, (int)tn);
     return hipGetLastError();
 }
 
-template <int G, int KIND, bool TAIL, bool SWIGLU> hipError_t launch_kind(const Q4Args &a, hipStream_t st) {
-    const int64_t used = a.g.n < a.g.rows ? a.g.n : a.g.rows;        // groups that can have rows
-    if (tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS) * used >= MANY_FROM) return launch_many<G, KIND, TAIL, SWIGLU>(a, st);
-    return launch_few<SWIGLU ? 2 : 1, G, KIND, TAIL, SWIGLU>(a, st);
+template <int G, int KIND, bool SWIGLU> hipError_t launch_kind(const Q4Args &a, hipStream_t st) {
+    // groups that can have rows, and rows of one of them
+    const int64_t used = a.g.n < a.g.rows ? a.g.n : a.g.rows, mean = (a.g.rows + used - 1) / used, most = (mean + 63) / 64 * used;
+    if (tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS) * most < MANY_FROM) return launch_few<SWIGLU ? 2 : 1, G, KIND, SWIGLU>(a, st);
+    if (mean <= (used > 1 ? 8 : 16)) return launch_many<1, G, KIND, SWIGLU>(a, st);
+    if (mean <= 32 && used == 1) return launch_many<2, G, KIND, SWIGLU>(a, st);
+    return launch_many<4, G, KIND, SWIGLU>(a, st);
 }
 
-template <int G, int KIND, bool TAIL> hipError_t launch_act(const Q4Args &a, hipStream_t st) {
-    return a.swiglu ? launch_kind<G, KIND, TAIL, true>(a, st) : launch_kind<G, KIND, TAIL, false>(a, st);
-}
-
-template <int G, int KIND> hipError_t launch_tail(const Q4Args &a, hipStream_t st) {
-    if constexpr (G < CHUNK) {
-        if (a.K % CHUNK) return launch_act<G, KIND, true>(a, st);
-    }
-    return launch_act<G, KIND, false>(a, st);
+template <int G, int KIND> hipError_t launch_act(const Q4Args &a, hipStream_t st) {
+    return a.swiglu ? launch_kind<G, KIND, true>(a, st) : launch_kind<G, KIND, false>(a, st);
 }
 
 template <int G> hipError_t launch_group(const Q4Args &a, hipStream_t st) {
-    return a.scale_kind == Q4_F32 ? launch_tail<G, Q4_F32>(a, st) : a.scale_kind == Q4_BF16 ? launch_tail<G, Q4_BF16>(a, st)
-                                                                                            : launch_tail<G, Q4_F16>(a, st);
+    return a.scale_kind == Q4_F32 ? launch_act<G, Q4_F32>(a, st) : a.scale_kind == Q4_BF16 ? launch_act<G, Q4_BF16>(a, st)
+                                                                                           : launch_act<G, Q4_F16>(a, st);
 }
 
 }  // namespace
