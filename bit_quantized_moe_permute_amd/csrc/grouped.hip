@@ -47,9 +47,9 @@ __device__ __forceinline__ void load_to_lds(uint64_t from, uint32_t dst) {
 //   dgrad      columns of W [n][k]      rows of dy   [o][n]      n
 //   wgrad      columns of x [r][k]      columns of dy [o][n]     positions
 //
-// Both pass through LDS in steps of 32 of the sum, NST of them in a ring that direct-to-LDS loads fill. An operand whose rows run
-// along the sum ("rows") keeps 64 bytes per row there: 16-byte chunk c of row r lies at c ^ (r / 4 % 4), so that sixteen rows'
-// reads of a chunk column touch every bank once. One whose rows run across it ("columns") is read with the transposing LDS
+// Both pass through LDS in steps of BK = 64 or 32 of the sum, NST of them in a ring that direct-to-LDS loads fill. An operand
+// whose rows run along the sum ("rows") keeps 2 BK bytes per row there: 16-byte chunk c of row r lies at c ^ (r / 2 % 8) (BK 32: c
+// ^ (r / 4 % 4)), so that sixteen rows' reads of a chunk column touch every bank once. One whose rows run across it ("columns") is read with the transposing LDS
 // loads, four steps of the sum x 16 columns by 16 lanes: piece u of 16 columns of row r lies at u ^ swizzle(r).
 // What is outside (rows behind the group, steps behind the sum, rows that an index puts outside) is read from a block of zeros.
 //
@@ -57,17 +57,15 @@ __device__ __forceinline__ void load_to_lds(uint64_t from, uint32_t dst) {
 // register outputs; wait_stage() counts them and orders the workgroup. Nothing else of the loop loads through the vector memory
 // pipe.
 // ---------------------------------------------------------------------------
-constexpr int BK = 32;
-
 __device__ __forceinline__ uint32_t swizzle(int r) { return ((r & 1) * 2) ^ ((r >> 1 & 1) * 5); }
 
-template <int OP, int FP, int FQ, int WP, int WQ, int NST, bool SWIGLU>
+template <int OP, int FP, int FQ, int WP, int WQ, int BK, int NST, bool SWIGLU>
 __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(GroupedArgs a, int tiles_p, int tiles_q) {
     constexpr bool COLS_P = OP != GROUPED_FWD, COLS_Q = OP == GROUPED_WGRAD;
     constexpr int NW = WP * WQ, TP = 32 * FP * WP, TQ = 32 * FQ * WQ;
-    constexpr int LP = TP / 16 / NW, LQ = TQ / 16 / NW, LOADS = LP + LQ;             // loads of 1 KiB per wave and stage
-    constexpr uint32_t STAGE = (TP + TQ) * 64;
-    static_assert(LP * NW * 16 == TP && LQ * NW * 16 == TQ && (!COLS_P || TP >= 128) && (!COLS_Q || TQ >= 128), "");
+    constexpr int RK = 512 / BK, LP = TP / RK / NW, LQ = TQ / RK / NW, LOADS = LP + LQ;      // rows per KiB; loads of 1 KiB per wave and stage
+    constexpr uint32_t STAGE = (TP + TQ) * 2 * BK;
+    static_assert(LP * NW * RK == TP && LQ * NW * RK == TQ && (!COLS_P || TP >= 128) && (!COLS_Q || TQ >= 128), "");
     __shared__ __attribute__((aligned(1024))) uint8_t ring[NST * STAGE];
     const int lane = threadIdx.x & 63, i32 = lane & 31, hh = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wp = wave / WQ, wq = wave % WQ;
@@ -106,7 +104,8 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
     // Load i of this wave, P's first: from[i] is this lane's 16 bytes in the next stage to load; inside says whether they are
     // any of the operand's, left is how far the sum goes from there.
     constexpr int RP = 512 / TP, RQ = 512 / TQ;              // columns: rows per load
-    const int chunk = (lane & 3) ^ (lane >> 4 & 3);          // rows: this lane's 8 of a step
+    constexpr int CK = BK / 8;                               // rows: chunks of a row in a step
+    auto place = [](int r, int c) { return BK == 64 ? c ^ (r >> 1 & 7) : c ^ (r >> 2 & 3); };
     uint64_t from[LOADS];
     int left[LOADS];
 #pragma unroll
@@ -114,7 +113,7 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
         const bool is_p = i < LP;
         const int l = is_p ? wave * LP + i : wave * LQ + i - LP;
         if (is_p ? !COLS_P : !COLS_Q) {
-            const int r = 16 * l + (lane >> 2);
+            const int r = RK * l + lane / CK, chunk = place(r, lane % CK);           // this lane's 8 of a step
             int row;
             if (is_p) {
                 const int n = SWIGLU ? (r >> 6) * 32 + (r & 31) : r;
@@ -159,7 +158,7 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
             in = in && row >= 0;
             at += 2 * (uint64_t)(uint32_t)row * (uint32_t)(is_p ? P : a.n_out);
         }
-        const int l = is_p ? wave * LP + i : TP / 16 + wave * LQ + i - LP;
+        const int l = is_p ? wave * LP + i : TP / RK + wave * LQ + i - LP;
         load_to_lds(in ? at : zero, idst + l * 1024u);
         if constexpr (OP == GROUPED_FWD) from[i] += 2 * BK;
         else if constexpr (OP == GROUPED_DGRAD) from[i] += is_p ? 2 * BK * (uint64_t)(uint32_t)P : 2 * BK;
@@ -182,11 +181,11 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
     auto read_one = [&](uint32_t stage, int kk, int b, int n) {
         const bool is_p = n < FP;
         const int f = is_p ? wp * FP + n : wq * FQ + n - FP;
-        const uint32_t base = stage + (is_p ? 0 : TP * 64);
+        const uint32_t base = stage + (is_p ? 0 : TP * 2 * BK);
         uint4 v;
         if (is_p ? !COLS_P : !COLS_Q) {
-            const uint32_t c = (uint32_t)((2 * kk + hh) ^ (i32 >> 2 & 3));
-            v = __builtin_bit_cast(uint4, *(las_u32x4)(uintptr_t)(base + (f * 32 + i32) * 64 + c * 16));
+            const uint32_t c = (uint32_t)place(i32, 2 * kk + hh);
+            v = __builtin_bit_cast(uint4, *(las_u32x4)(uintptr_t)(base + (f * 32 + i32) * 2 * BK + c * 16));
         } else {
             const uint32_t pitch = 2 * (is_p ? TP : TQ), u = (uint32_t)(2 * f + (lane >> 4 & 1)) ^ swizzle(lane >> 2);
             const uint32_t at = base + (16 * kk + tr) * pitch + u * 32 + 8 * (lane & 3);
@@ -198,11 +197,11 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
         if (is_p) fp[b][n] = v;
         else fq[b][n - FP] = v;
     };
-    // The products of one slice (buffer b). Between them go the reads of the next slice and part `part` of 2 of a stage's loads,
-    // so that the matrix cores have work while these are issued.
+    // The products of one slice (buffer b). Between them go the reads of the next slice and part `part` of 2 of a stage's loads
+    // (-1: none), so that the matrix cores have work while these are issued.
     auto slice = [&](int b, uint32_t next, int nkk, int part) {
         constexpr int M = FP * FQ, NR = FP + FQ;
-        const int l0 = part * LOADS / 2, nl = (part + 1) * LOADS / 2 - l0;
+        const int l0 = part * LOADS / 2, nl = part < 0 ? 0 : (part + 1) * LOADS / 2 - l0;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             acc[m / FQ][m % FQ] = mfma32(fp[b][m / FQ], fq[b][m % FQ], acc[m / FQ][m % FQ]);
@@ -215,10 +214,11 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // All but one and a half of the ring's stages are loaded ahead. Before a stage's second slice: wait for the next stage (those
+    // All but one and a half of the ring's stages are loaded ahead. Before a stage's last slice: wait for the next stage (those
     // after it stay under way) and for the workgroup; from then on nobody reads the present stage, and it takes the loads of
-    // the stage NST further on.
+    // the stage NST further on, in this slice and the next.
     if (ns > 0) {
+        constexpr int NS = BK / 16;                          // slices of a stage
 #pragma unroll
         for (int s = 0; s < NST - 1; ++s) {
 #pragma unroll
@@ -232,7 +232,8 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
 #pragma unroll
         for (int n = 0; n < FP + FQ; ++n) read_one(here, 0, 0, n);
         for (int s = 0; s < ns; ++s) {
-            slice(0, here, 1, 1);
+#pragma unroll
+            for (int k = 0; k < NS - 1; ++k) slice(k & 1, here, k + 1, k == 0 ? 1 : -1);
             next_stage();
             here = here == lds0 + (NST - 1) * STAGE ? lds0 : here + STAGE;
             wait_stage<(NST - 2) * LOADS>();
@@ -281,24 +282,25 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
 
 namespace moe {
 
-template <int OP, int FP, int FQ, int WP, int WQ, int NST, bool SWIGLU>
+template <int OP, int FP, int FQ, int WP, int WQ, int BK, int NST, bool SWIGLU>
 static hipError_t launch_tile(const GroupedArgs &a, hipStream_t st) {
     constexpr int TP = 32 * FP * WP / (SWIGLU ? 2 : 1), TQ = 32 * FQ * WQ, threads = 64 * WP * WQ;
     const int64_t tp = ((OP == GROUPED_FWD ? a.n_out : a.n_in) + TP - 1) / TP;
     const int64_t tq = OP == GROUPED_WGRAD ? (a.n_out + TQ - 1) / TQ : most_tiles(a.g, TQ);
     const int64_t blocks = (tp * tq * (OP == GROUPED_WGRAD ? a.g.n : 1) + 7) / 8 * 8;
     if (!grid_fits(blocks, threads)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_tile<OP, FP, FQ, WP, WQ, NST, SWIGLU>), dim3((unsigned)blocks), dim3(threads), 0, st, a, (int)tp, (int)tq);
+    hipLaunchKernelGGL((k_tile<OP, FP, FQ, WP, WQ, BK, NST, SWIGLU>), dim3((unsigned)blocks), dim3(threads), 0, st, a, (int)tp, (int)tq);
     return hipGetLastError();
 }
 
+constexpr int BIGK = 64, BIGS = 2;
 template <int OP, bool SWIGLU> static hipError_t launch_op(const GroupedArgs &a, hipStream_t st) {
-    if constexpr (OP == GROUPED_WGRAD) return launch_tile<OP, 4, 2, 2, 2, 3, false>(a, st);
+    if constexpr (OP == GROUPED_WGRAD) return launch_tile<OP, 4, 2, 2, 2, 32, 3, false>(a, st);
     else {
         const int rows = (a.g.rows + a.g.n - 1) / a.g.n;
-        if (rows >= 192) return launch_tile<OP, 4, 4, 2, 2, 5, SWIGLU>(a, st);
-        if (rows >= 48) return launch_tile<OP, 4, 2, 2, 2, 3, SWIGLU>(a, st);
-        return launch_tile<OP, 2, 1, 2, 2, 4, SWIGLU>(a, st);
+        if (rows >= 192) return launch_tile<OP, 4, 4, 2, 2, BIGK, BIGS, SWIGLU>(a, st);
+        if (rows >= 48) return launch_tile<OP, 4, 2, 2, 2, 32, 3, SWIGLU>(a, st);
+        return launch_tile<OP, 2, 1, 2, 2, 32, 4, SWIGLU>(a, st);
     }
 }
 

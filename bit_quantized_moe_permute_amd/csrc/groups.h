@@ -99,6 +99,14 @@ inline int64_t most_tiles(const Groups &g, int height) {
 // Whether a launch can count its threads (in 32 bits).
 inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
 
-__device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
+// silu(gate) * up. exp(-gate) as a power of two whose exponent keeps what its rounding lost; the quotient through the hardware's
+// reciprocal: some 2 units of the last place, in 11 instructions (library exp and division take 40: for 256 x 256 results of a
+// tile a tenth of its whole time).
+__device__ __forceinline__ float swiglu(float gate, float up) {
+    constexpr float L = 1.44269502f, L_REST = 1.92596299e-8f, LN2 = 0.693147181f;    // log2(e) in two parts
+    const float t = -gate * L, rest = __fmaf_rn(-gate, L_REST, __fmaf_rn(-gate, L, -t));
+    const float e = __builtin_amdgcn_exp2f(fminf(t, 126.f));
+    return gate * __builtin_amdgcn_rcpf(1.f + __fmaf_rn(e, rest * LN2, e)) * up;
+}
 
 }  // namespace moe
