@@ -3,6 +3,8 @@
 //   forward           out[o][n] = sum_k x[r][k] W_g[n][k]
 //   input's gradient  dx[i][k]  = sum_n dy[o][n] W_g[n][k]
 //   weights' gradient dW_g[n][k] = sum over the positions of g of dy[o][n] x[r][k]
+#include <type_traits>
+
 #include "groups.h"
 
 using namespace moe;
@@ -241,40 +243,68 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
         }
         wait_stage<0>();
     }
-    // Lane l has column l % 32 of a fragment of results, P's rows 8 (v / 4) + 4 (l / 32) + v % 4.
+    // Lane l has row l % 32 of a fragment of results, columns 8 (v / 4) + 4 (l / 32) + v % 4. Stored from there, every row would get
+    // 16 or 8 bytes at a time (16384 x 4096 results: 50 us); through LDS, where the ring was, 32 rows of a wave go out as runs of
+    // whole lines. 16-byte chunk c of row r lies at c ^ r.
+    constexpr int FO = SWIGLU ? FP / 2 : FP, COLS = 32 * FO;
+    static_assert(NW * 32 * COLS * 4 <= NST * STAGE, "");
+    uint8_t *rows = ring + wave * (32 * COLS * 4);
+    const int n0 = p0 + wp * COLS;
 #pragma unroll
     for (int j = 0; j < FQ; ++j) {
         const int q = q0 + (wq * FQ + j) * 32 + i32;
-        int64_t row = -1;
-        if (q < last_q)
-            row = OP == GROUPED_FWD ? out_row(a.g, q, a.out_rows) : OP == GROUPED_DGRAD ? in_slot(a.g, q, a.out_rows)
-                                                                                      : (int64_t)group * a.n_out + q;
-        if (row < 0) continue;
+        int row = -1;
+        if (q < last_q) row = OP == GROUPED_FWD ? out_row(a.g, q, a.out_rows) : OP == GROUPED_DGRAD ? in_slot(a.g, q, a.out_rows) : q;
+        if (__ballot(row >= 0) == 0) continue;
+        auto results = [&](auto bf16) {
+            constexpr int SIZE = decltype(bf16)::value ? 2 : 4, CHUNKS = COLS * SIZE / 16, ROWS = 64 / CHUNKS, PER = 16 / SIZE;
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < FP; i += SWIGLU ? 2 : 1)
+            for (int i = 0; i < FO; ++i)
 #pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4) {
-                const int n = p0 + (SWIGLU ? (wp * FP + i) / 2 : wp * FP + i) * 32 + 8 * v4 + 4 * hh;
-                if (n >= P) continue;
-                f32x4_t y;
+                for (int v4 = 0; v4 < 4; ++v4) {
+                    f32x4_t y;
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    y[v] = SWIGLU ? swiglu(acc[i][j][4 * v4 + v], acc[i + (SWIGLU ? 1 : 0)][j][4 * v4 + v]) : acc[i][j][4 * v4 + v];
-                const int64_t o = row * P + n;
-                uint2 *half = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + o);
-                f32x4_t *full = reinterpret_cast<f32x4_t *>(static_cast<float *>(a.out) + o);
-                if (OP == GROUPED_WGRAD && a.accumulate) {
-                    if (a.out_bf16) {
-                        const uint2 w = *half;
-                        y += f32x4_t{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                                     __uint_as_float(w.y & 0xFFFF0000u)};
-                    } else {
-                        y += *full;
-                    }
+                    for (int v = 0; v < 4; ++v)
+                        y[v] = SWIGLU ? swiglu(acc[SWIGLU ? 2 * i : i][j][4 * v4 + v], acc[SWIGLU ? 2 * i + 1 : i][j][4 * v4 + v])
+                                      : acc[i][j][4 * v4 + v];
+                    const int c = (i * 32 + 8 * v4 + 4 * hh) / PER;
+                    uint8_t *to = rows + i32 * (COLS * SIZE) + (c ^ (i32 & (CHUNKS - 1))) * 16;
+                    if constexpr (SIZE == 4) *reinterpret_cast<f32x4_t *>(to) = y;
+                    else *reinterpret_cast<uint2 *>(to + 8 * hh) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
                 }
-                if (a.out_bf16) *half = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-                else *full = y;
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+            const int c = lane % CHUNKS, n = n0 + c * PER;
+#pragma unroll
+            for (int k = 0; k < 32 / ROWS; ++k) {
+                const int r = k * ROWS + lane / CHUNKS, to = __shfl(row, r, 64);
+                u32x4_t y = *reinterpret_cast<const u32x4_t *>(rows + r * (COLS * SIZE) + (c ^ (r & (CHUNKS - 1))) * 16);
+                if (to < 0 || n >= P) continue;
+                const int64_t at = ((OP == GROUPED_WGRAD ? (int64_t)group * a.n_out : 0) + to) * P + n;
+                if constexpr (SIZE == 2) {
+                    *reinterpret_cast<u32x4_t *>(static_cast<uint16_t *>(a.out) + at) = y;
+                } else {
+                    f32x4_t v = __builtin_bit_cast(f32x4_t, y);
+                    uint2 *half = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at);
+                    f32x4_t *full = reinterpret_cast<f32x4_t *>(static_cast<float *>(a.out) + at);
+                    if (OP == GROUPED_WGRAD && a.accumulate) {
+                        if (a.out_bf16) {
+                            const uint2 w = *half;
+                            v += f32x4_t{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                                         __uint_as_float(w.y & 0xFFFF0000u)};
+                            *half = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                            continue;
+                        }
+                        v += *full;
+                    }
+                    *full = v;
+                }
             }
+            asm volatile("" ::: "memory");
+        };
+        if (a.out_bf16 && !(OP == GROUPED_WGRAD && a.accumulate)) results(std::true_type{});
+        else results(std::false_type{});
     }
 }
 
@@ -293,12 +323,11 @@ static hipError_t launch_tile(const GroupedArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-constexpr int BIGK = 64, BIGS = 2;
 template <int OP, bool SWIGLU> static hipError_t launch_op(const GroupedArgs &a, hipStream_t st) {
     if constexpr (OP == GROUPED_WGRAD) return launch_tile<OP, 4, 2, 2, 2, 32, 3, false>(a, st);
     else {
         const int rows = (a.g.rows + a.g.n - 1) / a.g.n;
-        if (rows >= 192) return launch_tile<OP, 4, 4, 2, 2, BIGK, BIGS, SWIGLU>(a, st);
+        if (rows >= 192) return launch_tile<OP, 4, 2, 2, 4, 64, 2, SWIGLU>(a, st);
         if (rows >= 48) return launch_tile<OP, 4, 2, 2, 2, 32, 3, SWIGLU>(a, st);
         return launch_tile<OP, 2, 1, 2, 2, 32, 4, SWIGLU>(a, st);
     }
