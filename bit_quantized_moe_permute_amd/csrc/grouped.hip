@@ -69,8 +69,15 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
     constexpr uint32_t STAGE = (TP + TQ) * 2 * BK;
     static_assert(LP * NW * RK == TP && LQ * NW * RK == TQ && (!COLS_P || TP >= 128) && (!COLS_Q || TQ >= 128), "");
     __shared__ __attribute__((aligned(1024))) uint8_t ring[NST * STAGE];
+    // Weights' gradient: the rows of x and dy of the next WINDOW positions (-1: none, or behind the group).
+    constexpr int WINDOW = OP == GROUPED_WGRAD ? 2048 : 1;
+    __shared__ int table[OP == GROUPED_WGRAD ? 2 : 1][WINDOW];
     const int lane = threadIdx.x & 63, i32 = lane & 31, hh = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wp = wave / WQ, wq = wave % WQ;
+    // Of the two waves that share a SIMD (w and w + 4 of eight), one has the first rows of the output and one the last: where a
+    // tile is not full, the waves without rows leave the others the matrix cores.
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w4 = wave & 3, back = wave >> 2;
+    const int wp = NW < 8 ? wave / WQ : WQ == 4 ? w4 & 1 : WQ == 2 ? (w4 >> 1) + 2 * back : wave / WQ;
+    const int wq = NW < 8 ? wave % WQ : WQ == 4 ? (back ? 3 - (w4 >> 1) : w4 >> 1) : WQ == 2 ? (w4 + back) & 1 : wave % WQ;
     const int P = OP == GROUPED_FWD ? a.n_out : a.n_in;                               // results per row of the output
     // XCD-aware order: consecutive workgroups go to the eight XCDs in turn; each takes a run of tiles, in blocks of four tiles
     // along Q whose workgroups read the same rows on the other side
@@ -138,27 +145,32 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
     const uint32_t lds0 = (uint32_t)(uintptr_t)(las_ptr)ring;
     int step = 0;                                            // the sum's position of the stage to load next
     uint32_t idst = lds0;
-    auto issue = [&](int i) {                                // i: load of this wave (compile-time)
+    // Rows of positions first .. + count - 1 of the sum into the table.
+    auto fill = [&](int first, int count) __attribute__((always_inline)) {
+        if constexpr (OP == GROUPED_WGRAD) {
+            for (int e = threadIdx.x; e < count; e += 64 * NW) {
+                const int p = begin + first + e;
+                const bool in = first + e < K;
+                table[0][(first + e) % WINDOW] = in ? in_row(a.g, p, a.a_rows) : -1;
+                table[1][(first + e) % WINDOW] = in ? out_row(a.g, p, a.b_rows) : -1;
+            }
+        }
+    };
+    int next_row[OP == GROUPED_WGRAD ? LOADS : 1];
+    auto look_up = [&](int i) __attribute__((always_inline)) {                              // the row that load i will read, ahead of its issue
+        if constexpr (OP == GROUPED_WGRAD) {
+            const bool is_p = i < LP;
+            const int rows = is_p ? RP : RQ, l = is_p ? wave * LP + i : wave * LQ + i - LP;
+            next_row[i] = table[is_p ? 0 : 1][(step + l * rows + lane / (64 / rows)) % WINDOW];
+        }
+    };
+    auto issue = [&](int i) __attribute__((always_inline)) {                                // i: load of this wave (compile-time)
         const bool is_p = i < LP;
         uint64_t at = from[i];
         bool in = step < left[i];
         if constexpr (OP == GROUPED_WGRAD) {
-            // the rows of this load's positions, through the scalar cache: no wait for the loads under way
-            const int rows = is_p ? RP : RQ, l = is_p ? wave * LP + i : wave * LQ + i - LP, top = a.g.rows - 1;
-            int row = -1;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j >= rows) continue;
-                const int p = min(begin + step + l * rows + j, top), limit = is_p ? a.a_rows : a.b_rows;
-                const int32_t *index = is_p ? a.g.in_index : a.g.out_index;
-                int r = p;
-                if (index) r = reinterpret_cast<const __attribute__((address_space(4))) int32_t *>(reinterpret_cast<uintptr_t>(index))[p];
-                if (is_p && index && r >= 0 && a.g.in_div > 1) r = (int)(__umulhi((uint32_t)r, a.g.div_mul) >> a.g.div_shift);
-                if ((unsigned)r >= (unsigned)limit) r = -1;
-                row = lane / (64 / rows) == j ? r : row;
-            }
-            in = in && row >= 0;
-            at += 2 * (uint64_t)(uint32_t)row * (uint32_t)(is_p ? P : a.n_out);
+            in = in && next_row[i] >= 0;
+            at += 2 * (uint64_t)(uint32_t)next_row[i] * (uint32_t)(is_p ? P : a.n_out);
         }
         const int l = is_p ? wave * LP + i : TP / RK + wave * LQ + i - LP;
         load_to_lds(in ? at : zero, idst + l * 1024u);
@@ -180,7 +192,7 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
     // Fragment n of a 16-wide slice: lane l has its row (column) l % 32 and 8 (l / 32) .. + 7 of the sum.
     const int tr = 8 * hh + (lane >> 2 & 3);                 // columns: row of this lane's four values of the first read
     uint4 fp[2][FP], fq[2][FQ];
-    auto read_one = [&](uint32_t stage, int kk, int b, int n) {
+    auto read_one = [&](uint32_t stage, int kk, int b, int n) __attribute__((always_inline)) {
         const bool is_p = n < FP;
         const int f = is_p ? wp * FP + n : wq * FQ + n - FP;
         const uint32_t base = stage + (is_p ? 0 : TP * 2 * BK);
@@ -200,16 +212,22 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
         else fq[b][n - FP] = v;
     };
     // The products of one slice (buffer b). Between them go the reads of the next slice and part `part` of 2 of a stage's loads
-    // (-1: none), so that the matrix cores have work while these are issued.
-    auto slice = [&](int b, uint32_t next, int nkk, int part) {
+    // (-1: none), so that the matrix cores have work while these are issued. A wave without results only loads.
+    const bool works = p0 + wp * 32 * FP / (SWIGLU ? 2 : 1) < P && q0 + wq * 32 * FQ < last_q;
+    auto slice = [&](auto working, int b, uint32_t next, int nkk, int part) __attribute__((always_inline)) {
         constexpr int M = FP * FQ, NR = FP + FQ;
         const int l0 = part * LOADS / 2, nl = part < 0 ? 0 : (part + 1) * LOADS / 2 - l0;
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-            acc[m / FQ][m % FQ] = mfma32(fp[b][m / FQ], fq[b][m % FQ], acc[m / FQ][m % FQ]);
+        for (int i = 0; i < LOADS; ++i)
+            if (i >= l0 && i < l0 + nl) look_up(i);
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
-                if (n >= m * 2 * NR / M && n < (m + 1) * 2 * NR / M) read_one(next, nkk, b ^ 1, n);      // in the first half
+        for (int m = 0; m < M; ++m) {
+            if constexpr (decltype(working)::value) {
+                acc[m / FQ][m % FQ] = mfma32(fp[b][m / FQ], fq[b][m % FQ], acc[m / FQ][m % FQ]);
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                    if (n >= m * 2 * NR / M && n < (m + 1) * 2 * NR / M) read_one(next, nkk, b ^ 1, n);  // in the first half
+            }
 #pragma unroll
             for (int i = 0; i < LOADS; ++i)
                 if (i >= l0 + m * nl / M && i < l0 + (m + 1) * nl / M) issue(i);                        // towards the end
@@ -219,30 +237,54 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
     // All but one and a half of the ring's stages are loaded ahead. Before a stage's last slice: wait for the next stage (those
     // after it stay under way) and for the workgroup; from then on nobody reads the present stage, and it takes the loads of
     // the stage NST further on, in this slice and the next.
-    if (ns > 0) {
-        constexpr int NS = BK / 16;                          // slices of a stage
-#pragma unroll
-        for (int s = 0; s < NST - 1; ++s) {
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) issue(i);
-            next_stage();
-        }
-#pragma unroll
-        for (int i = 0; i < LOADS / 2; ++i) issue(i);
-        wait_stage<(NST - 2) * LOADS + LOADS / 2>();
+    constexpr int NS = BK / 16;                              // slices of a stage
+    auto loop = [&](auto working) __attribute__((always_inline)) {
         uint32_t here = lds0;
+        if constexpr (decltype(working)::value) {
 #pragma unroll
-        for (int n = 0; n < FP + FQ; ++n) read_one(here, 0, 0, n);
+            for (int n = 0; n < FP + FQ; ++n) read_one(here, 0, 0, n);
+        }
         for (int s = 0; s < ns; ++s) {
 #pragma unroll
-            for (int k = 0; k < NS - 1; ++k) slice(k & 1, here, k + 1, k == 0 ? 1 : -1);
+            for (int k = 0; k < NS - 1; ++k) slice(working, k & 1, here, k + 1, k == 0 ? 1 : -1);
             next_stage();
             here = here == lds0 + (NST - 1) * STAGE ? lds0 : here + STAGE;
             wait_stage<(NST - 2) * LOADS>();
-            slice(1, here, 0, 0);                            // behind the last stage: a read of zeros, not used
+            // everybody has looked up the rows up to `step`: half of the table takes the ones behind the other half
+            if constexpr (OP == GROUPED_WGRAD) {
+                if (step % (WINDOW / 2) == 0 && step + WINDOW / 2 < K) {
+                    fill(step + WINDOW / 2, WINDOW / 2);
+                    __syncthreads();
+                }
+            }
+            slice(working, 1, here, 0, 0);                   // behind the last stage: a read of zeros, not used
         }
+    };
+    if (ns > 0) {
+        if constexpr (OP == GROUPED_WGRAD) {
+            fill(0, WINDOW);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int s = 0; s < NST - 1; ++s) {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                look_up(i);
+                issue(i);
+            }
+            next_stage();
+        }
+#pragma unroll
+        for (int i = 0; i < LOADS / 2; ++i) {
+            look_up(i);
+            issue(i);
+        }
+        wait_stage<(NST - 2) * LOADS + LOADS / 2>();
+        if (works) loop(std::true_type{});
+        else loop(std::false_type{});
         wait_stage<0>();
     }
+    if (!works) return;
     // Lane l has row l % 32 of a fragment of results, columns 8 (v / 4) + 4 (l / 32) + v % 4. Stored from there, every row would get
     // 16 or 8 bytes at a time (16384 x 4096 results: 50 us); through LDS, where the ring was, 32 rows of a wave go out as runs of
     // whole lines. 16-byte chunk c of row r lies at c ^ r.
@@ -256,7 +298,7 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
         int row = -1;
         if (q < last_q) row = OP == GROUPED_FWD ? out_row(a.g, q, a.out_rows) : OP == GROUPED_DGRAD ? in_slot(a.g, q, a.out_rows) : q;
         if (__ballot(row >= 0) == 0) continue;
-        auto results = [&](auto bf16) {
+        auto results = [&](auto bf16) __attribute__((always_inline)) {
             constexpr int SIZE = decltype(bf16)::value ? 2 : 4, CHUNKS = COLS * SIZE / 16, ROWS = 64 / CHUNKS, PER = 16 / SIZE;
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -323,13 +365,20 @@ static hipError_t launch_tile(const GroupedArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Tiles, P x Q. With 256 compute units, whole calls in us at (rows of x per expert) x experts, weights, measured side by side:
 template <int OP, bool SWIGLU> static hipError_t launch_op(const GroupedArgs &a, hipStream_t st) {
-    if constexpr (OP == GROUPED_WGRAD) return launch_tile<OP, 4, 2, 2, 2, 32, 3, false>(a, st);
-    else {
-        const int rows = (a.g.rows + a.g.n - 1) / a.g.n;
-        if (rows >= 192) return launch_tile<OP, 4, 2, 2, 4, 64, 2, SWIGLU>(a, st);
-        if (rows >= 48) return launch_tile<OP, 4, 2, 2, 2, 32, 3, SWIGLU>(a, st);
-        return launch_tile<OP, 2, 1, 2, 2, 32, 4, SWIGLU>(a, st);
+    if constexpr (OP == GROUPED_WGRAD) {
+        const int64_t tiles = (int64_t)((a.n_out + 255) / 256) * ((a.n_in + 255) / 256) * a.g.n;
+        if (tiles >= 256) return launch_tile<OP, 4, 2, 2, 4, 64, 2, false>(a, st);
+        return launch_tile<OP, 2, 1, 2, 4, 64, 3, false>(a, st);
+    } else {
+        const int64_t used = a.g.n < a.g.rows ? a.g.n : a.g.rows, mean = (a.g.rows + used - 1) / used;
+        const int64_t tp = (SWIGLU ? 2 * a.n_out : OP == GROUPED_FWD ? a.n_out : a.n_in) / 256 + 1;
+        const int64_t t128 = (mean + 127) / 128 * used * tp, t256 = (mean + 255) / 256 * used * tp;
+        if (mean >= 192 && t256 >= 512) return launch_tile<OP, 4, 2, 2, 4, 64, 2, SWIGLU>(a, st);
+        if (mean >= 192 && t128 >= 192) return launch_tile<OP, 2, 2, 4, 2, 64, 3, SWIGLU>(a, st);
+        if (mean >= 48 && t128 >= 256) return launch_tile<OP, 4, 2, 2, 2, 32, 3, SWIGLU>(a, st);
+        return launch_tile<OP, 2, 1, 2, 2, 64, 3, SWIGLU>(a, st);
     }
 }
 

@@ -352,15 +352,15 @@ __device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uin
     Chunk<G, KIND> p[AHEAD][2];
     Block<G, KIND> now[2], next[2];
     uint4 v[2][NB];
-    auto load_codes = [&](int u, int c) {                    // of chunk c, behind the last one that again
+    auto load_codes = [&](int u, int c) __attribute__((always_inline)) {                    // of chunk c, behind the last one that again
 #pragma unroll
         for (int r = 0; r < 2; ++r) p[u][r].load_codes(a, rows[r], min(c, chunks - 1));
     };
-    auto load_x = [&](int u, int c) {
+    auto load_x = [&](int u, int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) v[u][b] = load_or_zeros(x[b] + c * CHUNK, c * CHUNK < x_end[b]);
     };
-    auto put_x = [&](int u) {
+    auto put_x = [&](int u) __attribute__((always_inline)) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) tile[u][16 * b + xr][xi ^ xr] = reorder(v[u][b]);
     };

@@ -257,6 +257,27 @@ def test_wgrad(m, shape):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(2600, 2, 2, 264, 520), (5000, 1, 1, 64, 72), (4097, 0, 1, 136, 72), (2300, 2, 17, 1032, 1000)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_wgrad_of_many_rows(m, shape):
+    """More rows to a group than the kernel keeps indices of at once."""
+    run_wgrad(m, Case(*shape, seed=5, dst="slots"), F32, f"wgrad {shape}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(700, 4, 12, 520, 1288), (512, 8, 32, 264, 2056), (1300, 0, 1, 328, 5000), (2200, 3, 5, 136, 4104)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_large_products(m, shape):
+    """The largest tiles: enough rows and weights that they fill the chip, with ragged ends on every side."""
+    tail = 3 if shape[1] else 0                                     # (without offsets every position is of the one group)
+    c = Case(*shape, seed=6, dst="slots", tail=tail)
+    run_forward(m, c, BF16, f"linear {shape}")
+    run_dgrad(m, Case(*shape[:3], shape[4], shape[3], seed=6, src="sorted", tail=tail), F32, f"dgrad {shape}")
+    c.swiglu, c.w = True, torch.cat([c.w, c.w.flip(1)], dim=1)
+    run_forward(m, c, F32, f"linear {shape} swiglu")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("layout", LAYOUTS, ids=lambda d: "-".join(map(str, d.values())))
 def test_wgrad_layouts(m, layout):
     c = Case(77, 3, 12, 200, 136, seed=6, **layout)
