@@ -16,8 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe2bit.so")
 SOURCES = ["api.cpp", "prep.hip", "route.hip", "ffn_generic.hip", "ffn_gemv.hip", "ffn_gemm.hip", "combine.hip", "norm.hip",
-           "ffn_shared.hip", "grouped.hip", "q4.hip",
-           "probe.hip"]
+           "ffn_shared.hip", "grouped.hip", "q4_32.hip", "q4_64.hip", "q4_128.hip", "probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -262,7 +262,7 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
     };
     if (ns > 0) {
         if constexpr (OP == GROUPED_WGRAD) {
-            fill(0, WINDOW);
+            fill(0, min(K, WINDOW));
             __syncthreads();
         }
 #pragma unroll

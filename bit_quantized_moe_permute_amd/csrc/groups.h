@@ -37,23 +37,39 @@ struct Tile {
 };
 
 // The groups cut into tiles of up to `height` positions, in order. Every wave finds tiles for itself: a lane has the tiles of a
-// run of groups, and a scan over the lanes tells whose run holds a tile.
+// run of groups, and a scan over the lanes tells whose run holds a tile. Up to 256 groups the edges of a lane's four are loaded
+// at once and kept.
 struct Tiles {
     int g0, g1, sum, upto, total;        // this lane's groups, their tiles, those up to their end; all tiles
+    int edge[5];
 };
+constexpr int EDGES = 4;
 __device__ __forceinline__ int tiles_of(int b, int e, int height) { return e > b ? (e - b + height - 1) / height : 0; }
 
 __device__ __forceinline__ Tiles scan_tiles(const Groups &g, int height) {
     Tiles t;
-    const int lane = threadIdx.x & 63, per = (g.n + 63) / 64;
-    t.g0 = min(lane * per, g.n);
-    t.g1 = min(t.g0 + per, g.n);
+    if (!g.offsets) {
+        t.total = (g.rows + height - 1) / height;
+        return t;
+    }
+    const int lane = threadIdx.x & 63;
     t.sum = 0;
-    int b = group_edge(g, t.g0);
-    for (int i = t.g0; i < t.g1; ++i) {
-        const int e = group_edge(g, i + 1);
-        t.sum += tiles_of(b, e, height);
-        b = e;
+    if (g.n <= 64 * EDGES) {
+        t.g0 = lane * EDGES;
+#pragma unroll
+        for (int i = 0; i <= EDGES; ++i) t.edge[i] = group_edge(g, min(t.g0 + i, g.n));
+#pragma unroll
+        for (int i = 0; i < EDGES; ++i) t.sum += tiles_of(t.edge[i], t.edge[i + 1], height);
+    } else {
+        const int per = (g.n + 63) / 64;
+        t.g0 = min(lane * per, g.n);
+        t.g1 = min(t.g0 + per, g.n);
+        int b = group_edge(g, t.g0);
+        for (int i = t.g0; i < t.g1; ++i) {
+            const int e = group_edge(g, i + 1);
+            t.sum += tiles_of(b, e, height);
+            b = e;
+        }
     }
     t.upto = t.sum;
     for (int o = 1; o < 64; o <<= 1) {
@@ -66,29 +82,31 @@ __device__ __forceinline__ Tiles scan_tiles(const Groups &g, int height) {
 
 // Tile `item`, 0 <= item < total.
 __device__ __forceinline__ Tile tile_at(const Groups &g, const Tiles &t, int height, int item) {
+    if (!g.offsets) return Tile{0, item * height, min((item + 1) * height, g.rows)};
     int left = item - (t.upto - t.sum), found[3] = {0, 0, 0};
     const int who = __ffsll(__ballot(left >= 0 && left < t.sum)) - 1;
-    int b = group_edge(g, t.g0);
-    for (int i = t.g0; i < t.g1; ++i) {
-        const int e = group_edge(g, i + 1), n = tiles_of(b, e, height);
+    auto look = [&](int i, int b, int e) {
+        const int n = tiles_of(b, e, height);
         if (left >= 0 && left < n) {
             found[0] = i;
             found[1] = b + left * height;
             found[2] = min(found[1] + height, e);
         }
         left -= n;
-        b = e;
+    };
+    if (g.n <= 64 * EDGES) {
+#pragma unroll
+        for (int i = 0; i < EDGES; ++i) look(t.g0 + i, t.edge[i], t.edge[i + 1]);
+    } else {
+        int b = group_edge(g, t.g0);
+        for (int i = t.g0; i < t.g1; ++i) {
+            const int e = group_edge(g, i + 1);
+            look(i, b, e);
+            b = e;
+        }
     }
     return Tile{__builtin_amdgcn_readlane(found[0], who), __builtin_amdgcn_readlane(found[1], who),
                 __builtin_amdgcn_readlane(found[2], who)};
-}
-
-// Tile number `item`; false behind the last.
-__device__ __forceinline__ bool find_tile(const Groups &g, int height, int item, Tile &t) {
-    const Tiles all = scan_tiles(g, height);
-    if (item >= all.total) return false;
-    t = tile_at(g, all, height, item);
-    return true;
 }
 
 // Tiles that there can be at most: whole ones, and one more for each group with rows.

@@ -146,7 +146,7 @@ struct Product {
 size_t shared_workspace(int T, int H, int Is, int n, int R);
 hipError_t launch_shared(SharedArgs a, void *ws, hipStream_t st);
 
-// grouped.hip, q4.hip: products over rows grouped by expert
+// grouped.hip, q4_*.hip: products over rows grouped by expert
 struct Groups {
     int n, rows;                         // groups, positions
     const int32_t *offsets;              // NULL: one group of all rows
@@ -182,7 +182,12 @@ struct Q4Args {
     void *out;
     int out_bf16, out_rows;
 };
-hipError_t launch_q4(const Q4Args &a, hipStream_t st);
+hipError_t launch_q4_32(const Q4Args &a, hipStream_t st);
+hipError_t launch_q4_64(const Q4Args &a, hipStream_t st);
+hipError_t launch_q4_128(const Q4Args &a, hipStream_t st);
+inline hipError_t launch_q4(const Q4Args &a, hipStream_t st) {
+    return a.group == 32 ? launch_q4_32(a, st) : a.group == 64 ? launch_q4_64(a, st) : launch_q4_128(a, st);
+}
 
 // probe.hip: streaming-read ceiling (measurement only)
 hipError_t launch_stream_read(const void *buf, int64_t bytes, uint32_t *sink, int n_blocks, hipStream_t st);

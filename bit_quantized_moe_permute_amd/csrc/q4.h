@@ -2,7 +2,7 @@
 //
 //   out[o][n] = sum over groups j of scale[n][j] * sum over k in j of (code[n][k] - zero[n][j]) x[r][k]
 //
-// on the bf16 matrix cores. A code c becomes the bf16 number 16 + c by two bit operations (c goes into the mantissa behind the
+// on the bf16 matrix cores. (Each group length has a source of its own that instantiates what is here.) A code c becomes the bf16 number 16 + c by two bit operations (c goes into the mantissa behind the
 // exponent of 16), and a product of x with -(16 + zero), also exact in bf16, opens each group's sum:
 //
 //   sum (16 + c) x + sum -(16 + zero) x = sum (c - zero) x
@@ -12,13 +12,14 @@
 // The matrix instruction takes 16 weight rows, 16 rows of x and 32 columns: lane l has weight row (x row) l % 16 and columns
 // 8 (l / 16) .. + 7. Codes are loaded 16 bytes (32 columns) to a lane, four lanes to a row; a 4 x 4 exchange of dwords among these
 // four gives each instruction 32 consecutive columns, so that any group of 32 or more is whole.
+#pragma once
 #include "groups.h"
 
 using namespace moe;
 
 namespace {
 
-constexpr int MANY_FROM = 256;
+constexpr int MANY_FROM = 256, HALVES_BELOW = 512;
 constexpr int CHUNK = 128;                                   // columns of a row that four lanes load at once
 
 __device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
@@ -322,39 +323,47 @@ constexpr int MANY_WAVES = 4, MANY_ROWS = 32 * MANY_WAVES;
 
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <int NB, int G, int KIND, bool SWIGLU>
+template <int NB, int KS, int G, int KIND, bool SWIGLU>
 __device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uint4 *lds) {
     constexpr int AHEAD = NB == 4 ? 2 : 4;                   // chunks of codes under way
+    using B = Block<G, KIND>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
-    uint4 (*tile)[16 * NB][16] = reinterpret_cast<uint4 (*)[16 * NB][16]>(lds);
-    const int chunks = (a.K + CHUNK - 1) / CHUNK;
-    // this thread's part of x: rows threadIdx.x / 16 + 16 b, piece threadIdx.x % 16 of a chunk
-    const int xi = threadIdx.x & 15, xr = threadIdx.x >> 4;
+    const int w4 = wave % MANY_WAVES, part = wave / MANY_WAVES;
+    uint4 (*tile)[16 * NB][16] = reinterpret_cast<uint4 (*)[16 * NB][16]>(lds + part * (2 * 16 * NB * 16));
+    // the chunks of this group of waves: from c_begin on, `rounds` for every group, as far as there are any
+    const int chunks = (a.K + CHUNK - 1) / CHUNK, rounds = KS == 1 ? chunks : (chunks + 8 * KS - 1) / (8 * KS) * 8;
+    const int c_begin = part * rounds, c_end = min(c_begin + rounds, chunks);
+    // this thread's part of x: rows thread / 16 + 16 b, piece thread % 16 of a chunk, of the 256 threads of its group
+    const int xi = threadIdx.x & 15, xr = threadIdx.x >> 4 & 15;
     const uint16_t *x[NB];
     int x_end[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const int p = t.begin + 16 * b + xr, row = p < t.end ? in_row(a.g, p, a.x_rows) : -1;
         x[b] = a.x + (int64_t)max(row, 0) * a.K + 8 * xi;
-        x_end[b] = row < 0 ? 0 : a.K - 8 * xi;
+        x_end[b] = row < 0 ? 0 : min(a.K, c_end * CHUNK) - 8 * xi;
     }
     Rows<G, KIND> rows[2];
     int64_t first_group[2];
     const int64_t groups = (int64_t)a.g.n * a.N * (SWIGLU ? 2 : 1) * (a.K / G);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const int first = min(n0 + wave * (SWIGLU ? 16 : 32) + (SWIGLU ? 0 : 16 * r), a.N - 1);
+        const int first = min(n0 + w4 * (SWIGLU ? 16 : 32) + (SWIGLU ? 0 : 16 * r), a.N - 1);
         const int64_t row = ((int64_t)t.group * (SWIGLU ? 2 : 1) + (SWIGLU ? r : 0)) * a.N + first;
         rows[r].set(a, row, min(first + i16, a.N - 1) - first);
         first_group[r] = row * (a.K / G);
     }
     const Unpack unpack;
     Chunk<G, KIND> p[AHEAD][2];
-    Block<G, KIND> now[2], next[2];
+    B now[2], next[2];
     uint4 v[2][NB];
-    auto load_codes = [&](int u, int c) __attribute__((always_inline)) {                    // of chunk c, behind the last one that again
+    auto load_codes = [&](int u, int c) __attribute__((always_inline)) {     // of chunk c, behind the last one that again
 #pragma unroll
         for (int r = 0; r < 2; ++r) p[u][r].load_codes(a, rows[r], min(c, chunks - 1));
+    };
+    auto load_block = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) next[r].load(a, rows[r], first_group[r], groups, b);
     };
     auto load_x = [&](int u, int c) __attribute__((always_inline)) {
 #pragma unroll
@@ -369,34 +378,50 @@ __device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uin
     for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int b = 0; b < NB; ++b) acc[r][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    load_x(0, c_begin);
+    load_x(1, c_begin + 1);
+    load_block(c_begin / B::CHUNKS);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) next[r].load(a, rows[r], first_group[r], groups, 0);
-    load_x(0, 0);
-    load_x(1, 1);
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) load_codes(u, u);
+    for (int u = 0; u < AHEAD; ++u) load_codes(u, c_begin + u);
     put_x(0);
-    load_x(0, 2);
-    for (int c0 = 0; c0 < chunks; c0 += 8) {
-        if (c0 % Block<G, KIND>::CHUNKS == 0) {
+    load_x(0, c_begin + 2);
+    for (int c0 = c_begin; c0 < c_begin + rounds; c0 += 8) {
+        if (c0 == c_begin || c0 % B::CHUNKS == 0) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                now[r] = next[r];
-                next[r].load(a, rows[r], first_group[r], groups, c0 / Block<G, KIND>::CHUNKS + 1);
-            }
+            for (int r = 0; r < 2; ++r) now[r] = next[r];
+            load_block(c0 / B::CHUNKS + 1);
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const int c = c0 + u;
-            if (c >= chunks) break;
+            if (KS == 1 && c >= chunks) break;
             lds_barrier();                                   // this chunk's x is there, and nobody reads the one before it
             put_x((u + 1) & 1);
             load_x((u + 1) & 1, c + 3);
+            if (KS == 1 || c < chunks) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) now[r].to_chunk(p[u % AHEAD][r], a, u, c);
-            chunk_products<2, NB>(unpack, p[u % AHEAD], [&](int b, int s) { return tile[u & 1][16 * b + i16][(4 * s + q) ^ i16]; }, acc);
+                for (int r = 0; r < 2; ++r) now[r].to_chunk(p[u % AHEAD][r], a, u, c);
+                chunk_products<2, NB>(unpack, p[u % AHEAD], [&](int b, int s) { return tile[u & 1][16 * b + i16][(4 * s + q) ^ i16]; }, acc);
+            }
             load_codes(u % AHEAD, c + AHEAD);
         }
+    }
+    if constexpr (KS > 1) {                                  // the groups' sums join the first's, which goes on alone
+        static_assert(KS == 2, "");
+        f32x4_t *sums = reinterpret_cast<f32x4_t *>(lds);
+        __syncthreads();
+        if (part) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) sums[((r * NB + b) * MANY_WAVES + w4) * 64 + lane] = acc[r][b];
+        }
+        __syncthreads();
+        if (part) return;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) acc[r][b] += sums[((r * NB + b) * MANY_WAVES + w4) * 64 + lane];
     }
     // lane l's four values are positions 4 (l / 16) .. + 3 of weight row l % 16
 #pragma unroll
@@ -407,31 +432,31 @@ __device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uin
             if (row < 0) continue;
 #pragma unroll
             for (int r = 0; r < (SWIGLU ? 1 : 2); ++r) {
-                const int n = n0 + wave * (SWIGLU ? 16 : 32) + 16 * r + i16;
+                const int n = n0 + w4 * (SWIGLU ? 16 : 32) + 16 * r + i16;
                 if (n < a.N) store(a, (int64_t)row * a.N + n, SWIGLU ? swiglu(acc[0][b][j], acc[1][b][j]) : acc[r][b][j]);
             }
         }
 }
 
-template <int MAXB, int G, int KIND, bool SWIGLU>
-__global__ __launch_bounds__(64 * MANY_WAVES, MAXB == 1 ? 3 : 2) void k_many(Q4Args a, int tiles_n) {
-    __shared__ __attribute__((aligned(16))) uint4 lds[2 * 16 * MAXB * 16];
+template <int MAXB, int KS, int G, int KIND, bool SWIGLU>
+__global__ __launch_bounds__(64 * MANY_WAVES * KS, MAXB == 1 && KS == 1 ? 3 : 2) void k_many(Q4Args a, int tiles_n) {
+    __shared__ __attribute__((aligned(16))) uint4 lds[KS * 2 * 16 * MAXB * 16];
     Tile t;
     int n0;
     if (!place(a, 16 * MAXB, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS, tiles_n, t, n0)) return;
     const int blocks = (t.end - t.begin + 15) / 16;
-    if (MAXB == 1 || blocks <= 1) many<1, G, KIND, SWIGLU>(a, t, n0, lds);
-    else if (MAXB == 2 || blocks == 2) many<MAXB == 1 ? 1 : 2, G, KIND, SWIGLU>(a, t, n0, lds);
-    else many<MAXB, G, KIND, SWIGLU>(a, t, n0, lds);
+    if (MAXB == 1 || blocks <= 1) many<1, KS, G, KIND, SWIGLU>(a, t, n0, lds);
+    else if (blocks == 2) many<MAXB == 1 ? 1 : 2, KS, G, KIND, SWIGLU>(a, t, n0, lds);
+    else many<MAXB, KS, G, KIND, SWIGLU>(a, t, n0, lds);
 }
 
 int64_t tiles(int N, int rows) { return (N + rows - 1) / rows; }
 
-template <int MAXB, int G, int KIND, bool SWIGLU> hipError_t launch_many(const Q4Args &a, hipStream_t st) {
-    constexpr int threads = 64 * MANY_WAVES;
+template <int MAXB, int KS, int G, int KIND, bool SWIGLU> hipError_t launch_many(const Q4Args &a, hipStream_t st) {
+    constexpr int threads = 64 * MANY_WAVES * KS;
     const int64_t tn = tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS), blocks = (most_tiles(a.g, 16 * MAXB) * tn + 7) / 8 * 8;
     if (!grid_fits(blocks, threads)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_many<MAXB, G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(threads), 0, st, a, (int)tn);
+    hipLaunchKernelGGL((k_many<MAXB, KS, G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(threads), 0, st, a, (int)tn);
     return hipGetLastError();
 }
 
@@ -445,27 +470,23 @@ template <int R, int G, int KIND, bool SWIGLU> hipError_t launch_few(const Q4Arg
 template <int G, int KIND, bool SWIGLU> hipError_t launch_kind(const Q4Args &a, hipStream_t st) {
     // groups that can have rows, and rows of one of them
     const int64_t used = a.g.n < a.g.rows ? a.g.n : a.g.rows, mean = (a.g.rows + used - 1) / used, most = (mean + 63) / 64 * used;
-    if (tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS) * most < MANY_FROM) return launch_few<SWIGLU ? 2 : 1, G, KIND, SWIGLU>(a, st);
-    if (mean <= (used > 1 ? 8 : 16)) return launch_many<1, G, KIND, SWIGLU>(a, st);
-    if (mean <= 32 && used == 1) return launch_many<2, G, KIND, SWIGLU>(a, st);
-    return launch_many<4, G, KIND, SWIGLU>(a, st);
+    const int64_t many = tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS) * most;
+    if (many < MANY_FROM) return launch_few<SWIGLU ? 2 : 1, G, KIND, SWIGLU>(a, st);
+    if (mean <= (used > 1 ? 8 : 16)) return many < HALVES_BELOW ? launch_many<1, 2, G, KIND, SWIGLU>(a, st) : launch_many<1, 1, G, KIND, SWIGLU>(a, st);
+    return many < HALVES_BELOW ? launch_many<4, 2, G, KIND, SWIGLU>(a, st) : launch_many<4, 1, G, KIND, SWIGLU>(a, st);
 }
 
 template <int G, int KIND> hipError_t launch_act(const Q4Args &a, hipStream_t st) {
     return a.swiglu ? launch_kind<G, KIND, true>(a, st) : launch_kind<G, KIND, false>(a, st);
 }
 
-template <int G> hipError_t launch_group(const Q4Args &a, hipStream_t st) {
-    return a.scale_kind == Q4_F32 ? launch_act<G, Q4_F32>(a, st) : a.scale_kind == Q4_BF16 ? launch_act<G, Q4_BF16>(a, st)
-                                                                                           : launch_act<G, Q4_F16>(a, st);
-}
-
 }  // namespace
 
 namespace moe {
 
-hipError_t launch_q4(const Q4Args &a, hipStream_t st) {
-    return a.group == 32 ? launch_group<32>(a, st) : a.group == 64 ? launch_group<64>(a, st) : launch_group<128>(a, st);
+template <int G> hipError_t launch_q4_group(const Q4Args &a, hipStream_t st) {
+    return a.scale_kind == Q4_F32 ? launch_act<G, Q4_F32>(a, st) : a.scale_kind == Q4_BF16 ? launch_act<G, Q4_BF16>(a, st)
+                                                                                           : launch_act<G, Q4_F16>(a, st);
 }
 
 }  // namespace moe
