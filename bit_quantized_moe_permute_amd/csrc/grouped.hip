@@ -16,8 +16,6 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t *las_s16x4;
 typedef const __attribute__((address_space(3))) u32x4_t *las_u32x4;
 
-__device__ const uint4 zeros[1] = {};
-
 __device__ __forceinline__ f32x16_t mfma32(uint4 a, uint4 b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                    0, 0, 0);
@@ -350,6 +348,69 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows to an expert and few tiles of weights: a workgroup has 16 weight rows (SwiGLU: 16 of gate and the same of up) and up to
+// 16 positions of a group, the matrix instruction's 16 x 16 results; its waves take pieces of 128 columns in turn, FEW_AHEAD of
+// them loaded at once, and their sums meet in LDS. Lane l has weight row (x row) l % 16 and columns 8 (l / 16) .. + 7 of each 32.
+// ---------------------------------------------------------------------------
+constexpr int FEW_WAVES = 8, FEW_AHEAD = 2, FEW_COLS = 128, FEW_BELOW = 128;
+
+template <bool SWIGLU> __global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few_rows(GroupedArgs a, int tiles_n) {
+    constexpr int R = SWIGLU ? 2 : 1;
+    __shared__ __attribute__((aligned(16))) f32x4_t part[FEW_WAVES][R][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
+    const int N = a.n_out, K = a.n_in;
+    Tile t;
+    int n0;
+    if (!place(a.g, 16, 16, tiles_n, t, n0)) return;
+    const int xr = t.begin + i16 < t.end ? in_row(a.g, t.begin + i16, a.a_rows) : -1, x_end = xr < 0 ? 0 : K - 8 * q;
+    const uint16_t *x = a.a + (int64_t)max(xr, 0) * K + 8 * q;
+    const uint16_t *w[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[r] = a.b + (((int64_t)t.group * R + r) * N + min(n0 + i16, N - 1)) * K + 8 * q;
+    f32x4_t acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int k0 = wave * FEW_COLS; k0 < K; k0 += FEW_AHEAD * FEW_WAVES * FEW_COLS) {
+        uint4 v[FEW_AHEAD][4], u[FEW_AHEAD][R][4];
+#pragma unroll
+        for (int i = 0; i < FEW_AHEAD; ++i)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int k = k0 + i * FEW_WAVES * FEW_COLS + 32 * s;
+#pragma unroll
+                for (int r = 0; r < R; ++r) u[i][r][s] = load_or_zeros(w[r] + k, k + 8 * q < K);
+                v[i][s] = load_or_zeros(x + k, k < x_end);
+            }
+#pragma unroll
+        for (int i = 0; i < FEW_AHEAD; ++i)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int r = 0; r < R; ++r) acc[r] = mfma16(v[i][s], u[i][r][s], acc[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) part[wave][r][lane] = acc[r];
+    __syncthreads();
+    // lane l's four values are positions 4 (l / 16) .. + 3 of weight row l % 16
+    const float *sums = reinterpret_cast<const float *>(part);
+    const int e = threadIdx.x, n = e & 15, pos = e >> 4;
+    if (pos >= 16 || t.begin + pos >= t.end || n0 + n >= N) return;
+    const int row = out_row(a.g, t.begin + pos, a.out_rows);
+    if (row < 0) return;
+    float y[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        y[r] = 0.f;
+#pragma unroll
+        for (int j = 0; j < FEW_WAVES; ++j) y[r] += sums[((j * R + r) * 64 + n + 16 * (pos >> 2)) * 4 + (pos & 3)];
+    }
+    const float z = SWIGLU ? swiglu(y[0], y[R - 1]) : y[0];
+    const int64_t o = (int64_t)row * N + n0 + n;
+    if (a.out_bf16) static_cast<__bf16 *>(a.out)[o] = (__bf16)z;
+    else static_cast<float *>(a.out)[o] = z;
+}
+
 }  // namespace
 
 namespace moe {
@@ -365,7 +426,25 @@ static hipError_t launch_tile(const GroupedArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Tiles, P x Q. With 256 compute units, whole calls in us at (rows of x per expert) x experts, weights, measured side by side:
+template <bool SWIGLU> static hipError_t launch_few_rows(const GroupedArgs &a, hipStream_t st) {
+    const int64_t tn = (a.n_out + 15) / 16, blocks = (most_tiles(a.g, 16) * tn + 7) / 8 * 8;
+    if (!grid_fits(blocks, 64 * FEW_WAVES)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((k_few_rows<SWIGLU>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0, st, a, (int)tn);
+    return hipGetLastError();
+}
+
+// The kernel of a call, by the rows of one expert (`mean`; `used` experts can have rows) and by the tiles there are for the chip's 256
+// compute units. Whole calls in us, the one taken first, weights of 4096 x 4096 to an expert where nothing else is said:
+//   few rows: 16 weight rows per workgroup while tiles of 128 would leave half of the units idle: 1 token 7.5 against 26, 1024 x
+//     1024 and 4 tokens of 4 among 64 experts 9.7 and 10.4; at 128 tiles 16 tokens of 2 among 16 experts 12.6 (tiles) and 18.7
+//   128 x 64: 16384 slots of 64 rows 1910 (256 x 128 of 4 waves: 1737), 512 tokens 28 (128 x 128: 30, 256 x 128: 46 to 55), 300 x 4
+//     rows of 16 experts 11 (13, 14 to 24); three steps of 64 in the ring (six: 11 to 12, four of 32: 13)
+//   256 x 128, 4 waves, two workgroups to a unit: from 48 rows an expert, where the weights' stream counts: 64 rows of 256 experts
+//     1737 (8 waves, one workgroup: 1782; 128 x 64: 1910)
+//   256 x 128, 8 waves: from 192 rows, while 256 x 256 has less than two rounds: 2048 tokens 67 (4 waves 75, 256 x 256 80)
+//   256 x 256, 8 waves: 11709 tokens of 8 among 32 experts 2826 (4 waves of 128 x 128: 2956, 256 x 128: 3406 to 3606)
+// Weights' gradient: 256 x 256 (2048 tokens of 8 among 32 experts 1031; 256 x 128, two workgroups to a unit, 1065, 128 x 128 1305),
+// and 128 x 128 where that makes less than 256 tiles (8192 rows of one 1024 x 1024 matrix 79 against 329).
 template <int OP, bool SWIGLU> static hipError_t launch_op(const GroupedArgs &a, hipStream_t st) {
     if constexpr (OP == GROUPED_WGRAD) {
         const int64_t tiles = (int64_t)((a.n_out + 255) / 256) * ((a.n_in + 255) / 256) * a.g.n;
@@ -378,6 +457,9 @@ template <int OP, bool SWIGLU> static hipError_t launch_op(const GroupedArgs &a,
         if (mean >= 192 && t256 >= 512) return launch_tile<OP, 4, 2, 2, 4, 64, 2, SWIGLU>(a, st);
         if (mean >= 192 && t128 >= 192) return launch_tile<OP, 2, 2, 4, 2, 64, 3, SWIGLU>(a, st);
         if (mean >= 48 && t128 >= 256) return launch_tile<OP, 4, 2, 2, 2, 32, 3, SWIGLU>(a, st);
+        if constexpr (OP == GROUPED_FWD) {
+            if (mean <= 16 && used * (((SWIGLU ? 2 * a.n_out : a.n_out) + 127) / 128) < FEW_BELOW) return launch_few_rows<SWIGLU>(a, st);
+        }
         return launch_tile<OP, 2, 1, 2, 2, 64, 3, SWIGLU>(a, st);
     }
 }

@@ -114,6 +114,33 @@ inline int64_t most_tiles(const Groups &g, int height) {
     return g.offsets ? (int64_t)g.rows / height + (g.n < g.rows ? g.n : g.rows) : ((int64_t)g.rows + height - 1) / height;
 }
 
+// A workgroup's place: positions of a group, and rows of its matrix from n0 on. XCD-aware order: consecutive workgroups go to
+// the eight XCDs in turn; each takes a run of tiles, in blocks of four tiles of positions that read the same weights.
+__device__ __forceinline__ bool place(const Groups &g, int height, int rows, int tiles_n, Tile &t, int &n0) {
+    const Tiles all = scan_tiles(g, height);
+    const int total = all.total * tiles_n, per = (total + 7) / 8;
+    const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || id >= total) return false;
+    const int block = id / (4 * tiles_n), in = id - block * 4 * tiles_n, tiles = min(4, all.total - 4 * block), tn = in / tiles;
+    n0 = tn * rows;
+    t = tile_at(g, all, height, 4 * block + in - tn * tiles);
+    return true;
+}
+
+static __device__ const u32x4_t zeros[1] = {};
+
+// 16 bytes at p, or of zeros.
+typedef const __attribute__((address_space(1))) u32x4_t *global_u32x4;
+__device__ __forceinline__ uint4 load_or_zeros(const uint16_t *p, bool in) {
+    const uintptr_t at = in ? reinterpret_cast<uintptr_t>(p) : reinterpret_cast<uintptr_t>(zeros);
+    return __builtin_bit_cast(uint4, *reinterpret_cast<global_u32x4>(at));
+}
+
+__device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+}
+
 // Whether a launch can count its threads (in 32 bits).
 inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
 

@@ -22,11 +22,6 @@ namespace {
 constexpr int MANY_FROM = 256, HALVES_BELOW = 512;
 constexpr int CHUNK = 128;                                   // columns of a row that four lanes load at once
 
-__device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
-                                                   0, 0, 0);
-}
-
 // Dword j of lane group q (lanes 16 q .. + 15) to dword q of lane group j.
 __device__ __forceinline__ void exchange(uint32_t (&w)[4]) {
     const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false), b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
@@ -221,31 +216,9 @@ __device__ __forceinline__ void chunk_products(const Unpack &unpack, const C (&p
     }
 }
 
-__device__ const u32x4_t zeros[1] = {};
-
-// 16 bytes at p, or of zeros.
-typedef const __attribute__((address_space(1))) u32x4_t *global_u32x4;
-__device__ __forceinline__ uint4 load_or_zeros(const uint16_t *p, bool in) {
-    const uintptr_t at = in ? reinterpret_cast<uintptr_t>(p) : reinterpret_cast<uintptr_t>(zeros);
-    return __builtin_bit_cast(uint4, *reinterpret_cast<global_u32x4>(at));
-}
-
 __device__ __forceinline__ void store(const Q4Args &a, int64_t i, float v) {
     if (a.out_bf16) static_cast<__bf16 *>(a.out)[i] = (__bf16)v;
     else static_cast<float *>(a.out)[i] = v;
-}
-
-// A workgroup's place: positions of a group, and rows of its matrix from n0 on. XCD-aware order: consecutive workgroups go to
-// the eight XCDs in turn; each takes a run of tiles, in blocks of four tiles of positions that read the same weights.
-__device__ __forceinline__ bool place(const Q4Args &a, int height, int rows, int tiles_n, Tile &t, int &n0) {
-    const Tiles all = scan_tiles(a.g, height);
-    const int total = all.total * tiles_n, per = (total + 7) / 8;
-    const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= per || id >= total) return false;
-    const int block = id / (4 * tiles_n), in = id - block * 4 * tiles_n, tiles = min(4, all.total - 4 * block), tn = in / tiles;
-    n0 = tn * rows;
-    t = tile_at(a.g, all, height, 4 * block + in - tn * tiles);
-    return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -262,7 +235,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few(Q4Args a, int tiles_n
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
     Tile t;
     int n0;
-    if (!place(a, 16, ROWS, tiles_n, t, n0)) return;
+    if (!place(a.g, 16, ROWS, tiles_n, t, n0)) return;
     const int xr = t.begin + i16 < t.end ? in_row(a.g, t.begin + i16, a.x_rows) : -1, x_end = xr < 0 ? 0 : a.K - 8 * q;
     const uint16_t *x = a.x + (int64_t)max(xr, 0) * a.K + 8 * q;
     Rows<G, KIND> rows[R];
@@ -443,7 +416,7 @@ __global__ __launch_bounds__(64 * MANY_WAVES * KS, MAXB == 1 && KS == 1 ? 3 : 2)
     __shared__ __attribute__((aligned(16))) uint4 lds[KS * 2 * 16 * MAXB * 16];
     Tile t;
     int n0;
-    if (!place(a, 16 * MAXB, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS, tiles_n, t, n0)) return;
+    if (!place(a.g, 16 * MAXB, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS, tiles_n, t, n0)) return;
     const int blocks = (t.end - t.begin + 15) / 16;
     if (MAXB == 1 || blocks <= 1) many<1, KS, G, KIND, SWIGLU>(a, t, n0, lds);
     else if (blocks == 2) many<MAXB == 1 ? 1 : 2, KS, G, KIND, SWIGLU>(a, t, n0, lds);
