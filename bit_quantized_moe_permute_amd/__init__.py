@@ -535,22 +535,25 @@ def moe_shared_ffn(desc: LayerDesc, x, out, ws, adapters=None, token_adapter=Non
         _check(st)
 
 
+_I32_MAX = 2**31 - 1
+
+
 def _bf16_rows(t, what, cols):
-    """Rows of a [rows][cols] bf16 tensor."""
+    """Rows of a [rows][cols] bf16 tensor (those that an int32 can name)."""
     shape = t.shape
     if len(shape) != 2 or shape[1] != cols:
         raise ValueError(f"{what} must be [rows][{cols}], got shape {tuple(shape)}")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{what}: expected torch.bfloat16, got {t.dtype}")
-    return shape[0]
+    return min(shape[0], _I32_MAX)
 
 
 def _out_rows(t, what, cols):
-    """Rows and type of a [rows][cols] output."""
+    """Rows (those that an int32 can name) and type of a [rows][cols] output."""
     shape = t.shape
     if len(shape) != 2 or shape[1] != cols:
         raise ValueError(f"{what} must be [rows][{cols}], got shape {tuple(shape)}")
-    return shape[0], _type(t, what)
+    return min(shape[0], _I32_MAX), _type(t, what)
 
 
 def _stack(groups, w):

@@ -91,7 +91,7 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
         begin = group_edge(a.g, group);
         end = group_edge(a.g, group + 1);
     } else {
-        const Tiles all = scan_tiles(a.g, TQ);
+        const Tiles all = scan_tiles(a.g, TQ, tiles_q);
         const int total = all.total * tiles_p, per = (total + 7) / 8;
         const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
         if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
@@ -148,9 +148,9 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
         if constexpr (OP == GROUPED_WGRAD) {
             for (int e = threadIdx.x; e < count; e += 64 * NW) {
                 const int p = begin + first + e;
-                const bool in = first + e < K;
-                table[0][(first + e) % WINDOW] = in ? in_row(a.g, p, a.a_rows) : -1;
-                table[1][(first + e) % WINDOW] = in ? out_row(a.g, p, a.b_rows) : -1;
+                const int x = first + e < K ? in_row(a.g, p, a.a_rows) : -1, dy = first + e < K ? out_row(a.g, p, a.b_rows) : -1;
+                table[0][(first + e) % WINDOW] = dy < 0 ? -1 : x;        // without either the other may hold anything, NaN too
+                table[1][(first + e) % WINDOW] = x < 0 ? -1 : dy;
             }
         }
     };
@@ -355,14 +355,14 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
 // ---------------------------------------------------------------------------
 constexpr int FEW_WAVES = 8, FEW_AHEAD = 2, FEW_COLS = 128, FEW_BELOW = 128;
 
-template <bool SWIGLU> __global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few_rows(GroupedArgs a, int tiles_n) {
+template <bool SWIGLU> __global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few_rows(GroupedArgs a, int most, int tiles_n) {
     constexpr int R = SWIGLU ? 2 : 1;
     __shared__ __attribute__((aligned(16))) f32x4_t part[FEW_WAVES][R][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
     const int N = a.n_out, K = a.n_in;
     Tile t;
     int n0;
-    if (!place(a.g, 16, 16, tiles_n, t, n0)) return;
+    if (!place(a.g, 16, 16, most, tiles_n, t, n0)) return;
     const int xr = t.begin + i16 < t.end ? in_row(a.g, t.begin + i16, a.a_rows) : -1, x_end = xr < 0 ? 0 : K - 8 * q;
     const uint16_t *x = a.a + (int64_t)max(xr, 0) * K + 8 * q;
     const uint16_t *w[R];
@@ -427,9 +427,9 @@ static hipError_t launch_tile(const GroupedArgs &a, hipStream_t st) {
 }
 
 template <bool SWIGLU> static hipError_t launch_few_rows(const GroupedArgs &a, hipStream_t st) {
-    const int64_t tn = (a.n_out + 15) / 16, blocks = (most_tiles(a.g, 16) * tn + 7) / 8 * 8;
+    const int64_t tn = (a.n_out + 15) / 16, most = most_tiles(a.g, 16), blocks = (most * tn + 7) / 8 * 8;
     if (!grid_fits(blocks, 64 * FEW_WAVES)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_few_rows<SWIGLU>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0, st, a, (int)tn);
+    hipLaunchKernelGGL((k_few_rows<SWIGLU>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0, st, a, (int)most, (int)tn);
     return hipGetLastError();
 }
 

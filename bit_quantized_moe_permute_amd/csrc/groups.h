@@ -40,13 +40,14 @@ struct Tile {
 // run of groups, and a scan over the lanes tells whose run holds a tile. Up to 256 groups the edges of a lane's four are loaded
 // at once and kept.
 struct Tiles {
-    int g0, g1, sum, upto, total;        // this lane's groups, their tiles, those up to their end; all tiles
+    int g0, g1, sum, upto, total;        // this lane's groups, their tiles, those up to their end; all tiles, at most `most`
     int edge[5];
 };
 constexpr int EDGES = 4;
 __device__ __forceinline__ int tiles_of(int b, int e, int height) { return e > b ? (e - b + height - 1) / height : 0; }
 
-__device__ __forceinline__ Tiles scan_tiles(const Groups &g, int height) {
+// most: what most_tiles() says. Offsets that overlap can name more; those behind it are left out.
+__device__ __forceinline__ Tiles scan_tiles(const Groups &g, int height, int most) {
     Tiles t;
     if (!g.offsets) {
         t.total = (g.rows + height - 1) / height;
@@ -76,7 +77,7 @@ __device__ __forceinline__ Tiles scan_tiles(const Groups &g, int height) {
         const int v = __shfl_up(t.upto, o, 64);
         if (lane >= o) t.upto += v;
     }
-    t.total = __builtin_amdgcn_readlane(t.upto, 63);
+    t.total = (int)min((uint32_t)__builtin_amdgcn_readlane(t.upto, 63), (uint32_t)most);
     return t;
 }
 
@@ -116,8 +117,8 @@ inline int64_t most_tiles(const Groups &g, int height) {
 
 // A workgroup's place: positions of a group, and rows of its matrix from n0 on. XCD-aware order: consecutive workgroups go to
 // the eight XCDs in turn; each takes a run of tiles, in blocks of four tiles of positions that read the same weights.
-__device__ __forceinline__ bool place(const Groups &g, int height, int rows, int tiles_n, Tile &t, int &n0) {
-    const Tiles all = scan_tiles(g, height);
+__device__ __forceinline__ bool place(const Groups &g, int height, int rows, int most, int tiles_n, Tile &t, int &n0) {
+    const Tiles all = scan_tiles(g, height, most);
     const int total = all.total * tiles_n, per = (total + 7) / 8;
     const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= per || id >= total) return false;
@@ -144,14 +145,15 @@ __device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
 // Whether a launch can count its threads (in 32 bits).
 inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
 
-// silu(gate) * up. exp(-gate) as a power of two whose exponent keeps what its rounding lost; the quotient through the hardware's
-// reciprocal: some 2 units of the last place, in 11 instructions (library exp and division take 40: for 256 x 256 results of a
-// tile a tenth of its whole time).
+// silu(gate) * up. exp(-gate) as a power of two, times 1 + what the rounding of its exponent lost; the quotient through the
+// hardware's reciprocal: some 2 units of the last place, in 11 instructions (library exp and division take 40: for 256 x 256 results
+// of a tile a tenth of its whole time). The correction is below 1e-5 where the quotient matters; its bounds keep a gate of 2e7 and
+// more, or an infinite one, from making it anything else.
 __device__ __forceinline__ float swiglu(float gate, float up) {
     constexpr float L = 1.44269502f, L_REST = 1.92596299e-8f, LN2 = 0.693147181f;    // log2(e) in two parts
     const float t = -gate * L, rest = __fmaf_rn(-gate, L_REST, __fmaf_rn(-gate, L, -t));
-    const float e = __builtin_amdgcn_exp2f(fminf(t, 126.f));
-    return gate * __builtin_amdgcn_rcpf(1.f + __fmaf_rn(e, rest * LN2, e)) * up;
+    const float c = __builtin_amdgcn_fmed3f(__fmaf_rn(rest, LN2, 1.f), 0.99f, 1.01f);
+    return gate * __builtin_amdgcn_rcpf(__fmaf_rn(__builtin_amdgcn_exp2f(t), c, 1.f)) * up;
 }
 
 }  // namespace moe

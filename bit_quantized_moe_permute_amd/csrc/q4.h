@@ -228,14 +228,14 @@ __device__ __forceinline__ void store(const Q4Args &a, int64_t i, float v) {
 constexpr int FEW_WAVES = 8, FEW_AHEAD = 2;
 
 template <int R, int G, int KIND, bool SWIGLU>
-__global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few(Q4Args a, int tiles_n) {
+__global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few(Q4Args a, int most, int tiles_n) {
     static_assert(!SWIGLU || R == 2, "");
     constexpr int ROWS = SWIGLU ? 16 : 16 * R;               // results per position
     __shared__ __attribute__((aligned(16))) f32x4_t part[FEW_WAVES][R][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
     Tile t;
     int n0;
-    if (!place(a.g, 16, ROWS, tiles_n, t, n0)) return;
+    if (!place(a.g, 16, ROWS, most, tiles_n, t, n0)) return;
     const int xr = t.begin + i16 < t.end ? in_row(a.g, t.begin + i16, a.x_rows) : -1, x_end = xr < 0 ? 0 : a.K - 8 * q;
     const uint16_t *x = a.x + (int64_t)max(xr, 0) * a.K + 8 * q;
     Rows<G, KIND> rows[R];
@@ -412,11 +412,11 @@ __device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uin
 }
 
 template <int MAXB, int KS, int G, int KIND, bool SWIGLU>
-__global__ __launch_bounds__(64 * MANY_WAVES * KS, MAXB == 1 && KS == 1 ? 3 : 2) void k_many(Q4Args a, int tiles_n) {
+__global__ __launch_bounds__(64 * MANY_WAVES * KS, MAXB == 1 && KS == 1 ? 3 : 2) void k_many(Q4Args a, int most, int tiles_n) {
     __shared__ __attribute__((aligned(16))) uint4 lds[KS * 2 * 16 * MAXB * 16];
     Tile t;
     int n0;
-    if (!place(a.g, 16 * MAXB, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS, tiles_n, t, n0)) return;
+    if (!place(a.g, 16 * MAXB, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS, most, tiles_n, t, n0)) return;
     const int blocks = (t.end - t.begin + 15) / 16;
     if (MAXB == 1 || blocks <= 1) many<1, KS, G, KIND, SWIGLU>(a, t, n0, lds);
     else if (blocks == 2) many<MAXB == 1 ? 1 : 2, KS, G, KIND, SWIGLU>(a, t, n0, lds);
@@ -427,16 +427,16 @@ int64_t tiles(int N, int rows) { return (N + rows - 1) / rows; }
 
 template <int MAXB, int KS, int G, int KIND, bool SWIGLU> hipError_t launch_many(const Q4Args &a, hipStream_t st) {
     constexpr int threads = 64 * MANY_WAVES * KS;
-    const int64_t tn = tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS), blocks = (most_tiles(a.g, 16 * MAXB) * tn + 7) / 8 * 8;
+    const int64_t tn = tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS), most = most_tiles(a.g, 16 * MAXB), blocks = (most * tn + 7) / 8 * 8;
     if (!grid_fits(blocks, threads)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_many<MAXB, KS, G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(threads), 0, st, a, (int)tn);
+    hipLaunchKernelGGL((k_many<MAXB, KS, G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(threads), 0, st, a, (int)most, (int)tn);
     return hipGetLastError();
 }
 
 template <int R, int G, int KIND, bool SWIGLU> hipError_t launch_few(const Q4Args &a, hipStream_t st) {
-    const int64_t tn = tiles(a.N, SWIGLU ? 16 : 16 * R), blocks = (most_tiles(a.g, 16) * tn + 7) / 8 * 8;
+    const int64_t tn = tiles(a.N, SWIGLU ? 16 : 16 * R), most = most_tiles(a.g, 16), blocks = (most * tn + 7) / 8 * 8;
     if (!grid_fits(blocks, 64 * FEW_WAVES)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_few<R, G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0, st, a, (int)tn);
+    hipLaunchKernelGGL((k_few<R, G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0, st, a, (int)most, (int)tn);
     return hipGetLastError();
 }
 

@@ -89,6 +89,9 @@ class RowGroups:
 
     def __init__(self, n_rows, offsets=None, in_index=None, in_div=1, out_index=None):
         i32 = (torch.int32,)
+        for name, v in (("n_rows", n_rows), ("in_div", in_div)):
+            if not 1 <= v < 2**31:
+                raise ValueError(f"{name} must be 1 or more, and an int32, got {v}")
         self.device_index = None
         self._keep = []
         for name, t in (("offsets", offsets), ("in_index", in_index), ("out_index", out_index)):

@@ -563,6 +563,8 @@ moe_status moe_grouped_dgrad(const moe_group_desc *g, const void *dy, int32_t dy
  *   dw[g] = sum over the positions of g of dy[o] x[r]^T   (+ dw[g], accumulate)
  *   x [x_rows][n_in] and dy [dy_rows][n_out] bf16; dw [n_groups][n_out][n_in],
  *   fp32 or bf16.  Groups without rows get zeros (with accumulate: stay).
+ * A position whose row of x or of dy is outside its buffer is left out, whatever
+ * the other one holds.
  * Sums are fp32 in an order that depends on shapes and offsets alone.  Errors
  * as above.
  */
@@ -595,8 +597,9 @@ typedef struct {
  * x [x_rows][cols] bf16; out [out_rows][rows] (SwiGLU: [out_rows][rows / 2], rows
  * even), fp32 or bf16.  With one matrix and offsets NULL it is a dense
  * projection.  Codes less zero points are exact in the products, sums are fp32,
- * a group's sum takes its scale in fp32, and a bf16 out is rounded once.  A
- * group's weights are read once for each 64 of its rows.
+ * a group's sum takes its scale in fp32, and a bf16 out is rounded once.  (Sums
+ * hold up to 31 times |x|: x of 2^120 and above can overflow where the result
+ * would not.)  A group's weights are read once for each 16 or 64 of its rows.
  * Errors as above (codes, x and out 16-byte aligned).
  */
 moe_status moe_q4_linear(const moe_group_desc *g, const moe_q4_desc *w, const void *x, int32_t x_rows, int32_t act,

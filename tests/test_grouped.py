@@ -500,6 +500,92 @@ def test_non_finite_values_stay_in_their_rows_and_groups(m, T, k, E):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,E", [(6, 4), (1500, 2)])
+def test_wgrad_leaves_out_positions_without_either_row(m, T, E):
+    """A position without a row of x, or of dy, adds nothing: not even where the other row is not finite."""
+    c = Case(T, 2, E, 136, 72, dst="slots", seed=20)
+    c.in_index, c.out_index = c.perm.clone(), c.perm.clone()
+    c.x = c.x.repeat_interleave(2, 0)                               # a row of its own for every slot
+    no_x, no_dy = (next(b + i for e, b in enumerate(c.begin[:-1]) if c.counts[e] > 1) for i in (0, 1))
+    c.dy[int(c.perm[no_x])], c.x[int(c.perm[no_dy])] = float("nan"), float("inf")
+    c.in_index[no_x], c.out_index[no_dy] = -1, -1
+    groups = m.RowGroups(c.rows, offsets=c.offsets.cuda(), in_index=c.in_index.cuda(), out_index=c.out_index.cuda())
+    for dtype in (F32, BF16):
+        dw = torch.full((c.E, c.N, c.K), 7.0, dtype=dtype, device="cuda")
+        note(f"wgrad without either row {T} {dtype}")
+        m.moe_grouped_wgrad(groups, c.x.cuda(), c.dy.cuda(), dw)
+        torch.cuda.synchronize()
+        for e in range(c.E):
+            p = [i for i in c.positions(e) if i not in (no_x, no_dy)]
+            x, dy = (v[[int(c.perm[i]) for i in p]].double() for v in (c.x, c.dy))
+            want, tol = dy.T @ x, (len(p) + 1) * 2.0**-23 * (dy.abs().T @ x.abs())
+            if dtype == BF16:
+                tol = tol + 2.0**-8 * want.abs()
+            assert ((dw[e].cpu().double() - want).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+def test_many_overlapping_groups_touch_nothing_outside(m):
+    """4096 groups, every second one of all rows: far more tiles than a launch is made for."""
+    R, E, N, K = 300, 4096, 8, 32
+    offsets = torch.tensor([0, R] * (E // 2) + [0], dtype=torch.int32, device="cuda")
+    groups = m.RowGroups(R, offsets=offsets)
+    x = torch.ones(R, K, dtype=BF16, device="cuda")
+    w = torch.ones(E, N, K, dtype=BF16, device="cuda")
+    q = m.Q4Weights(torch.full((E, N, K // 2), 0x99, dtype=torch.uint8, device="cuda"), torch.ones(E, N, 1, device="cuda"))
+    for name, call in (("linear", lambda out: m.moe_grouped_linear(groups, x, w, out)),
+                       ("q4", lambda out: m.moe_q4_linear(groups, q, x, out))):
+        whole, out = guarded(R, N, F32, 7.0)
+        note(f"overlapping groups {name}")
+        call(out)
+        torch.cuda.synchronize()
+        assert (whole[R:] == 7.0).all() and ((out == 7.0) | (out == float(K))).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("kind", ["bf16", "q4"])
+def test_swiglu_of_large_and_infinite_gates(m, T, kind):
+    """Gates of either sign from 2^-100 to 2^100 and (bf16 weights) past the largest float: no overflow on the way reaches the
+    result. x[0] is the gate and x[1] the other half."""
+    g = torch.Generator().manual_seed(21)
+    K, N = 64, 16
+    x = torch.zeros(T, K, dtype=BF16)
+    out = torch.zeros(T, N, device="cuda")
+    w = torch.zeros(1, 2 * N, K)
+    scale = torch.exp2(torch.linspace(-100, 100, N).round())
+    scale[4:8] = torch.tensor([64.0, 90.0, 2.0**24, 2.0**26])       # where silu leaves the floats, and 2e7 and more
+    w[0, :N, 0], w[0, N:, 1] = scale, 1.0
+    x[:, 0] = torch.randn(T, generator=g).to(BF16)
+    x[::2, 0] = -x[::2, 0].abs()
+    x[:, 1] = torch.randn(T, generator=g).to(BF16)
+    groups = m.RowGroups(T)
+    note(f"large gates {T} {kind}")
+    if kind == "bf16":
+        w[0, N - 1, 0] = 3e38                                       # with an x of 4 the sum overflows
+        w = w.to(BF16)
+        if T > 1:
+            x[1, 0] = 4.0
+        m.moe_grouped_linear(groups, x.cuda(), w.cuda(), out, m.ACT_SWIGLU)
+    else:
+        w = w.to(BF16)
+        codes = torch.full((1, 2 * N, K), 8, dtype=torch.uint8)
+        codes[0, :N, 0] = codes[0, N:, 1] = 9
+        s = torch.ones(1, 2 * N, K // 32)
+        s[0, :N, 0] = w[0, :N, 0].float()
+        m.moe_q4_linear(groups, m.Q4Weights((codes[..., ::2] | codes[..., 1::2] << 4).contiguous().cuda(), s.cuda()), x.cuda(), out,
+                        m.ACT_SWIGLU)
+    torch.cuda.synchronize()
+    gate = (x[:, :1].double() * w[0, :N, 0].double()).float().double()      # one product of each sum is not zero
+    want = gate * torch.sigmoid(gate) * x[:, 1:2].double()
+    got = out.cpu().double()
+    finite = want.abs() < 3e38
+    assert ((got - want).abs()[finite] <= (2.0**-20 * want.abs() + 1e-35)[finite]).all()
+    large = want.abs() >= 3e38                                       # a gate of -inf: -inf * 0
+    assert torch.equal(got[large].sign(), want[large].sign()) and (got[large].abs() > 2.9e38).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [2, 50])
 def test_q4_non_finite_values_stay_in_their_rows(m, T):
     c = Case(T, 0, 1, 256, 40, seed=16)
@@ -803,6 +889,15 @@ def test_q4_weights_are_checked(host):
     call(1, "overlaps", o=S)
     call(1, "overlaps", o=Z)
     call(1, "overlaps", o=A)
+
+
+@pytest.mark.parametrize("value", [0, -1, 2**31, 2**32 + 4])
+def test_row_counts_are_int32(host, value):
+    """A number that an int32 does not hold is refused, not cut."""
+    with pytest.raises(ValueError, match="n_rows"):
+        host.RowGroups(value)
+    with pytest.raises(ValueError, match="in_div"):
+        host.RowGroups(4, in_div=value)
 
 
 def test_binding_checks(host):
