@@ -285,7 +285,9 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
     if (!works) return;
     // Lane l has row l % 32 of a fragment of results, columns 8 (v / 4) + 4 (l / 32) + v % 4. Stored from there, every row would get
     // 16 or 8 bytes at a time (16384 x 4096 results: 50 us); through LDS, where the ring was, 32 rows of a wave go out as runs of
-    // whole lines. 16-byte chunk c of row r lies at c ^ r.
+    // whole lines. 16-byte chunk c of row r lies at c ^ r. The weights' gradient is the largest thing that passes here and nothing of
+    // the call reads it again: it leaves around the L2, which keeps x and dy (512 MiB matrices of 32 experts: 1028 -> 939 us; the
+    // other outputs gain nothing from that, and what follows reads them).
     constexpr int FO = SWIGLU ? FP / 2 : FP, COLS = 32 * FO;
     static_assert(NW * 32 * COLS * 4 <= NST * STAGE, "");
     uint8_t *rows = ring + wave * (32 * COLS * 4);
@@ -323,7 +325,9 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
                 if (to < 0 || n >= P) continue;
                 const int64_t at = ((OP == GROUPED_WGRAD ? (int64_t)group * a.n_out : 0) + to) * P + n;
                 if constexpr (SIZE == 2) {
-                    *reinterpret_cast<u32x4_t *>(static_cast<uint16_t *>(a.out) + at) = y;
+                    u32x4_t *half = reinterpret_cast<u32x4_t *>(static_cast<uint16_t *>(a.out) + at);
+                    if (OP == GROUPED_WGRAD) __builtin_nontemporal_store(y, half);
+                    else *half = y;
                 } else {
                     f32x4_t v = __builtin_bit_cast(f32x4_t, y);
                     uint2 *half = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at);
@@ -338,7 +342,8 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
                         }
                         v += *full;
                     }
-                    *full = v;
+                    if (OP == GROUPED_WGRAD) __builtin_nontemporal_store(v, full);
+                    else *full = v;
                 }
             }
             asm volatile("" ::: "memory");
