@@ -3,6 +3,12 @@
 //   forward           out[o][n] = sum_k x[r][k] W_g[n][k]
 //   input's gradient  dx[i][k]  = sum_n dy[o][n] W_g[n][k]
 //   weights' gradient dW_g[n][k] = sum over the positions of g of dy[o][n] x[r][k]
+//
+// All on the bf16 matrix cores, with fp32 sums from the first to the last product; a bf16 output is rounded once, where it is
+// stored. Few rows to an expert: every weight is read once, and that is the time (one token of 8 among 256 experts, 256 MiB of
+// weights: 49 us, 5.4 TB/s; 2048 tokens of the same, all weights, 8.6 GB: 1742 us, 5.0 TB/s). Many rows: the products are (11709
+// tokens of 8 among 32 experts: 2822 us, 1114 TFLOP/s, where a library product of 8192 x 8192 x 8192 makes 1346). A large copy
+// moves 5.15 TB/s.
 #include <type_traits>
 
 #include "groups.h"
@@ -49,13 +55,22 @@ __device__ __forceinline__ void load_to_lds(uint64_t from, uint32_t dst) {
 //
 // Both pass through LDS in steps of BK = 64 or 32 of the sum, NST of them in a ring that direct-to-LDS loads fill. An operand
 // whose rows run along the sum ("rows") keeps 2 BK bytes per row there: 16-byte chunk c of row r lies at c ^ (r / 2 % 8) (BK 32: c
-// ^ (r / 4 % 4)), so that sixteen rows' reads of a chunk column touch every bank once. One whose rows run across it ("columns") is read with the transposing LDS
-// loads, four steps of the sum x 16 columns by 16 lanes: piece u of 16 columns of row r lies at u ^ swizzle(r).
+// ^ (r / 4 % 4)), so that sixteen rows' reads of a chunk column touch every bank once. One whose rows run across it ("columns") is
+// read with the transposing LDS loads, four steps of the sum x 16 columns by 16 lanes: piece u of 16 columns of row r lies at u ^
+// swizzle(r).
 // What is outside (rows behind the group, steps behind the sum, rows that an index puts outside) is read from a block of zeros.
 //
 // The loads are written as assembly: the compiler would otherwise wait for all of them before any LDS read. They have no
 // register outputs; wait_stage() counts them and orders the workgroup. Nothing else of the loop loads through the vector memory
 // pipe.
+//
+// What bounds it, forward: at 256 x 256 the loop runs like the library's, and ragged last tiles and the first loads of a tile are
+// the rest; LDS gives two fragments of 32 x 32 x 16 in the time of two such products, so a wave has 4 x 2 of them. Input's gradient
+// (2048 tokens of 8 among 32 experts of 4096 x 2048): 345 us, 790 TFLOP/s; 640 tiles are 2.5 rounds of the 256 units and take three.
+// Weights' gradient (32 experts of 4096 x 4096, 512 rows each): 939 us; a tile has eight steps only, and its first loads (offsets,
+// indices, rows, one behind the other) and its 256 KiB of results are not hidden behind another tile's products, since its ring and
+// its sums fill the unit (without the stores 765 us, without the loop 512). Workgroups that go on to a second tile by themselves
+// took longer.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t swizzle(int r) { return ((r & 1) * 2) ^ ((r >> 1 & 1) * 5); }
 
@@ -148,7 +163,8 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
         if constexpr (OP == GROUPED_WGRAD) {
             for (int e = threadIdx.x; e < count; e += 64 * NW) {
                 const int p = begin + first + e;
-                const int x = first + e < K ? in_row(a.g, p, a.a_rows) : -1, dy = first + e < K ? out_row(a.g, p, a.b_rows) : -1;
+                const int x = first + e < K ? in_row(a.g, p, a.a_rows) : -1;
+                const int dy = first + e < K ? out_row(a.g, p, a.b_rows) : -1;
                 table[0][(first + e) % WINDOW] = dy < 0 ? -1 : x;        // without either the other may hold anything, NaN too
                 table[1][(first + e) % WINDOW] = x < 0 ? -1 : dy;
             }
@@ -357,6 +373,8 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
 // Few rows to an expert and few tiles of weights: a workgroup has 16 weight rows (SwiGLU: 16 of gate and the same of up) and up to
 // 16 positions of a group, the matrix instruction's 16 x 16 results; its waves take pieces of 128 columns in turn, FEW_AHEAD of
 // them loaded at once, and their sums meet in LDS. Lane l has weight row (x row) l % 16 and columns 8 (l / 16) .. + 7 of each 32.
+// The weights' stream bounds it where there is one (4096 x 8192, one token: 12.0 us, 5.6 TB/s), the launch and the dependent loads
+// of offsets, index, rows and weights where there is little (16 experts of 1024 x 1024, one token: 5.5 us).
 // ---------------------------------------------------------------------------
 constexpr int FEW_WAVES = 8, FEW_AHEAD = 2, FEW_COLS = 128, FEW_BELOW = 128;
 
@@ -440,16 +458,19 @@ template <bool SWIGLU> static hipError_t launch_few_rows(const GroupedArgs &a, h
 
 // The kernel of a call, by the rows of one expert (`mean`; `used` experts can have rows) and by the tiles there are for the chip's 256
 // compute units. Whole calls in us, the one taken first, weights of 4096 x 4096 to an expert where nothing else is said:
-//   few rows: 16 weight rows per workgroup while tiles of 128 would leave half of the units idle: 1 token 7.5 against 26, 1024 x
-//     1024 and 4 tokens of 4 among 64 experts 9.7 and 10.4; at 128 tiles 16 tokens of 2 among 16 experts 12.6 (tiles) and 18.7
+//   few rows: 16 weight rows per workgroup while tiles of 128 would leave half of the units idle (FEW_BELOW): 1 token 7.5 (tiles:
+//     26), 16 tokens 9.6 (26), 8192 rows of weights 12.1 (26), 1024 x 1024 and one token of 4 among 64 experts 5.5 (9.7). From 128
+//     tiles on it depends: 16384 rows of weights, 1 token 37 (few: 31), 16 tokens of 2 among 16 experts of 1024 x 1024 12.6 (18.7);
+//     more rows read the weights more often: 16 tokens of 4 among 64 experts 19 (26), 264 tiles of 4096 x 4096 49 (63)
 //   128 x 64: 16384 slots of 64 rows 1910 (256 x 128 of 4 waves: 1737), 512 tokens 28 (128 x 128: 30, 256 x 128: 46 to 55), 300 x 4
 //     rows of 16 experts 11 (13, 14 to 24); three steps of 64 in the ring (six: 11 to 12, four of 32: 13)
 //   256 x 128, 4 waves, two workgroups to a unit: from 48 rows an expert, where the weights' stream counts: 64 rows of 256 experts
 //     1737 (8 waves, one workgroup: 1782; 128 x 64: 1910)
 //   256 x 128, 8 waves: from 192 rows, while 256 x 256 has less than two rounds: 2048 tokens 67 (4 waves 75, 256 x 256 80)
 //   256 x 256, 8 waves: 11709 tokens of 8 among 32 experts 2826 (4 waves of 128 x 128: 2956, 256 x 128: 3406 to 3606)
-// Weights' gradient: 256 x 256 (2048 tokens of 8 among 32 experts 1031; 256 x 128, two workgroups to a unit, 1065, 128 x 128 1305),
-// and 128 x 128 where that makes less than 256 tiles (8192 rows of one 1024 x 1024 matrix 79 against 329).
+// Weights' gradient: 256 x 256 (2048 tokens of 8 among 32 experts 939; 256 x 128, two workgroups to a unit, 961; 8192 rows of one
+// matrix 240 and 279), and 128 x 128 where that makes less than 256 tiles (8192 rows of one 1024 x 1024 matrix 80, 256 x 256 329;
+// there the 64 workgroups' LDS reads bound it: a ring of four steps takes as long).
 template <int OP, bool SWIGLU> static hipError_t launch_op(const GroupedArgs &a, hipStream_t st) {
     if constexpr (OP == GROUPED_WGRAD) {
         const int64_t tiles = (int64_t)((a.n_out + 255) / 256) * ((a.n_in + 255) / 256) * a.g.n;

@@ -2,12 +2,20 @@
 //
 //   out[o][n] = sum over groups j of scale[n][j] * sum over k in j of (code[n][k] - zero[n][j]) x[r][k]
 //
-// on the bf16 matrix cores. (Each group length has a source of its own that instantiates what is here.) A code c becomes the bf16 number 16 + c by two bit operations (c goes into the mantissa behind the
-// exponent of 16), and a product of x with -(16 + zero), also exact in bf16, opens each group's sum:
+// on the bf16 matrix cores. (Each group length has a source of its own that instantiates what is here.) A code c becomes the bf16
+// number 16 + c by two bit operations (c goes into the mantissa behind the exponent of 16), and a product of x with -(16 + zero),
+// also exact in bf16, opens each group's sum:
 //
 //   sum (16 + c) x + sum -(16 + zero) x = sum (c - zero) x
 //
-// so that no weight is rounded; the group's sum takes its scale in fp32.
+// so that no weight is rounded; the group's sum takes its scale in fp32, and sums over groups are fp32. (Taking the zero point from
+// the code would cost two conversions to each pair of codes; the product with the offset is one matrix instruction to 16 rows x 32
+// columns, on units that have time.)
+//
+// What bounds it: one to a few rows, the codes' stream and the latency before it (1 token, 4096 x 4096: 5.2 us; 3 tokens of 8 among
+// 256 experts, 207 MB: 47 us, 4.4 TB/s); from 16 rows on, the vector instructions that unpack (512 tokens of 8 among 256 experts of
+// 4096 x 2048, groups of 32: 401 to 419 us where codes and rows alone take 272: 180 vector instructions, a third of them unpacking,
+// to 16 products; three waves to a SIMD instead of two took it there from 475).
 //
 // The matrix instruction takes 16 weight rows, 16 rows of x and 32 columns: lane l has weight row (x row) l % 16 and columns
 // 8 (l / 16) .. + 7. Codes are loaded 16 bytes (32 columns) to a lane, four lanes to a row; a 4 x 4 exchange of dwords among these
@@ -19,7 +27,6 @@ using namespace moe;
 
 namespace {
 
-constexpr int MANY_FROM = 256, HALVES_BELOW = 512;
 constexpr int CHUNK = 128;                                   // columns of a row that four lanes load at once
 
 // Dword j of lane group q (lanes 16 q .. + 15) to dword q of lane group j.
@@ -223,7 +230,8 @@ __device__ __forceinline__ void store(const Q4Args &a, int64_t i, float v) {
 
 // ---------------------------------------------------------------------------
 // Few weights in all: a workgroup has 16 R weight rows (SwiGLU: 16 of gate and the same of up) and up to 16 positions of a group;
-// its waves take the row's chunks in turn, FEW_AHEAD of them loaded at once, and their sums meet in LDS.
+// its waves take the row's chunks in turn, FEW_AHEAD of them loaded at once, and their sums meet in LDS. 1 token, 4096 x 4096:
+// 5.2 us, of which a launch is 2; 4096 x 8192 8.1.
 // ---------------------------------------------------------------------------
 constexpr int FEW_WAVES = 8, FEW_AHEAD = 2;
 
@@ -288,17 +296,19 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few(Q4Args a, int most, i
 
 // ---------------------------------------------------------------------------
 // Many: a wave has two blocks of 16 weight rows (SwiGLU: 16 of gate and the same of up) along all of K, a workgroup four waves,
-// and up to 16 MAXB positions of a group, in one, two or four blocks of 16. Codes go straight to registers, AHEAD chunks ahead,
+// and up to 16 MAXB positions of a group, in one, two or four blocks of 16 (NB). Codes go straight to registers, AHEAD chunks ahead,
 // scales and zero points a block of 32 groups ahead; the x of a chunk passes through LDS, put into the order of unpack() on its
-// way, 16-byte piece i of row r at i ^ r: sixteen rows' reads of one piece column touch every bank once.
+// way, 16-byte piece i of row r at i ^ r: sixteen rows' reads of one piece column touch every bank once. With KS = 2 a workgroup has
+// eight waves, four for each half of K. Tiles of 64 have registers for two waves to a SIMD, the smaller ones for three (two chunks
+// ahead instead of four for it where there are two blocks; not with the scales of a block in fp32 and two blocks: 30 to 44 registers
+// short). All products of four groups before their scales: no gain.
 // ---------------------------------------------------------------------------
 constexpr int MANY_WAVES = 4, MANY_ROWS = 32 * MANY_WAVES;
 
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <int NB, int KS, int G, int KIND, bool SWIGLU>
+template <int NB, int AHEAD, int KS, int G, int KIND, bool SWIGLU>
 __device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uint4 *lds) {
-    constexpr int AHEAD = NB == 4 ? 2 : 4;                   // chunks of codes under way
     using B = Block<G, KIND>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
     const int w4 = wave % MANY_WAVES, part = wave / MANY_WAVES;
@@ -412,15 +422,15 @@ __device__ __forceinline__ void many(const Q4Args &a, const Tile &t, int n0, uin
 }
 
 template <int MAXB, int KS, int G, int KIND, bool SWIGLU>
-__global__ __launch_bounds__(64 * MANY_WAVES * KS, MAXB == 1 && KS == 1 ? 3 : 2) void k_many(Q4Args a, int most, int tiles_n) {
+__global__ __launch_bounds__(64 * MANY_WAVES * KS, KS == 1 && (MAXB == 1 || (MAXB == 2 && KIND != Q4_F32)) ? 3 : 2) void k_many(Q4Args a, int most, int tiles_n) {
     __shared__ __attribute__((aligned(16))) uint4 lds[KS * 2 * 16 * MAXB * 16];
     Tile t;
     int n0;
     if (!place(a.g, 16 * MAXB, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS, most, tiles_n, t, n0)) return;
     const int blocks = (t.end - t.begin + 15) / 16;
-    if (MAXB == 1 || blocks <= 1) many<1, KS, G, KIND, SWIGLU>(a, t, n0, lds);
-    else if (blocks == 2) many<MAXB == 1 ? 1 : 2, KS, G, KIND, SWIGLU>(a, t, n0, lds);
-    else many<MAXB, KS, G, KIND, SWIGLU>(a, t, n0, lds);
+    if (MAXB == 1 || blocks <= 1) many<1, 4, KS, G, KIND, SWIGLU>(a, t, n0, lds);
+    else if (MAXB == 2 || blocks == 2) many<MAXB == 1 ? 1 : 2, MAXB == 2 ? 2 : 4, KS, G, KIND, SWIGLU>(a, t, n0, lds);
+    else many<MAXB, MAXB == 4 ? 2 : 4, KS, G, KIND, SWIGLU>(a, t, n0, lds);
 }
 
 int64_t tiles(int N, int rows) { return (N + rows - 1) / rows; }
@@ -440,12 +450,25 @@ template <int R, int G, int KIND, bool SWIGLU> hipError_t launch_few(const Q4Arg
     return hipGetLastError();
 }
 
+// The kernel of a call, by the workgroups that k_many would have for the chip's 256 units. Whole calls in us, weights of 4096
+// columns:
+//   k_few below MANY_FROM, k_many from there: 1 token, 8192 rows of weights 8.1 (k_many: 18.3), 16384 rows 13.7 (18.3), 24576 rows
+//     19.0 (18.4; k_many has 192 workgroups); 64 tokens, 2048 rows 12.7 (35.9), 8192 rows 44 (36); 24 tokens, 8192 rows 23.3 (24.7)
+//   halves of K below HALVES_BELOW (less than two workgroups to a unit): 32768 rows, 1 token 18.6 (one: 23.5), 64 tokens 37.5 (40.7);
+//     above: 3 tokens of 8 among 256 experts (736 workgroups) 47.5 (halves: 58.7), 2048 tokens, 4096 rows 117 (136)
+//   tiles of 16 or 32 positions leave three waves to a SIMD registers, tiles of 64 two, but they read a group's weights once (the
+//     others' second reading comes out of caches). By the mean of 256 experts of 4096 x 2048, a token's 8 spread unevenly, tiles of
+//     16, 32, 64: mean 4 260, 268, 309; 8 327, 319, 398; 16 453, 401, 475; 31 693, 566, 614; 62 1177, 903, 863. One group has just
+//     its rows: 16 of 65536 rows of weights 38.6 (64: 38.9), 17 44.3 (16: 57.5, 32: 46.1).
+constexpr int MANY_FROM = 256, HALVES_BELOW = 512;
+
 template <int G, int KIND, bool SWIGLU> hipError_t launch_kind(const Q4Args &a, hipStream_t st) {
     // groups that can have rows, and rows of one of them
     const int64_t used = a.g.n < a.g.rows ? a.g.n : a.g.rows, mean = (a.g.rows + used - 1) / used, most = (mean + 63) / 64 * used;
     const int64_t many = tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS) * most;
     if (many < MANY_FROM) return launch_few<SWIGLU ? 2 : 1, G, KIND, SWIGLU>(a, st);
-    if (mean <= (used > 1 ? 8 : 16)) return many < HALVES_BELOW ? launch_many<1, 2, G, KIND, SWIGLU>(a, st) : launch_many<1, 1, G, KIND, SWIGLU>(a, st);
+    if (mean < (used > 1 ? 8 : 17)) return many < HALVES_BELOW ? launch_many<1, 2, G, KIND, SWIGLU>(a, st) : launch_many<1, 1, G, KIND, SWIGLU>(a, st);
+    if (used > 1 && mean <= 32 && many >= HALVES_BELOW) return launch_many<2, 1, G, KIND, SWIGLU>(a, st);
     return many < HALVES_BELOW ? launch_many<4, 2, G, KIND, SWIGLU>(a, st) : launch_many<4, 1, G, KIND, SWIGLU>(a, st);
 }
 

@@ -345,7 +345,7 @@ def test_q4(m, shape, group, zero, scale, swiglu):
                          ids=lambda v: str(v).replace("torch.", ""))
 @pytest.mark.parametrize("shape", [(1, 0, 1, 128, 32780), (9, 0, 1, 1408, 32801), (16, 0, 1, 256, 33000), (23, 0, 1, 384, 32770),
                                    (33, 0, 1, 640, 32780), (70, 0, 1, 256, 32790), (40, 4, 40, 256, 890), (150, 4, 30, 128, 1300),
-                                   (300, 2, 20, 896, 1666)], ids=lambda s: "x".join(map(str, s)))
+                                   (300, 2, 20, 896, 1666), (320, 2, 64, 128, 1100), (600, 2, 40, 1152, 1700)], ids=lambda s: "x".join(map(str, s)))
 def test_q4_many_weights(m, shape, group, zero, scale, swiglu):
     """Matrices of many rows or many of them, with one to many rows of x to a group."""
     c = Case(*shape, seed=10, swiglu=swiglu)
