@@ -69,8 +69,8 @@ __device__ __forceinline__ void load_to_lds(uint64_t from, uint32_t dst) {
 // (2048 tokens of 8 among 32 experts of 4096 x 2048): 345 us, 790 TFLOP/s; 640 tiles are 2.5 rounds of the 256 units and take three.
 // Weights' gradient (32 experts of 4096 x 4096, 512 rows each): 939 us; a tile has eight steps only, and its first loads (offsets,
 // indices, rows, one behind the other) and its 256 KiB of results are not hidden behind another tile's products, since its ring and
-// its sums fill the unit (without the stores 765 us, without the loop 512). Workgroups that go on to a second tile by themselves
-// took longer.
+// its sums fill the unit (with stores through the L2 1028 us, without the stores 765, without the loop 512). Workgroups that go on
+// to a second tile by themselves took longer.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t swizzle(int r) { return ((r & 1) * 2) ^ ((r >> 1 & 1) * 5); }
 

@@ -231,7 +231,7 @@ __device__ __forceinline__ void store(const Q4Args &a, int64_t i, float v) {
 // ---------------------------------------------------------------------------
 // Few weights in all: a workgroup has 16 R weight rows (SwiGLU: 16 of gate and the same of up) and up to 16 positions of a group;
 // its waves take the row's chunks in turn, FEW_AHEAD of them loaded at once, and their sums meet in LDS. 1 token, 4096 x 4096:
-// 5.2 us, of which a launch is 2; 4096 x 8192 8.1.
+// 5.2 us, the launch and two rounds of dependent loads; 4096 x 8192 8.1.
 // ---------------------------------------------------------------------------
 constexpr int FEW_WAVES = 8, FEW_AHEAD = 2;
 
