@@ -586,6 +586,45 @@ def test_swiglu_of_large_and_infinite_gates(m, T, kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 40])
+def test_rows_and_results_behind_4_gib(m, T):
+    """Rows of x, of the output and of dy and weights whose byte offsets pass 32 bits, against the same rows in small buffers."""
+    far, wide, K, N = 2**17 + 7, 2**14 + 64, 128, 136               # far x wide: 4.3 GB of bf16
+    g = torch.Generator(device="cuda").manual_seed(22)
+    normal = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF16)
+    big, near = torch.empty(far, wide, dtype=BF16, device="cuda"), normal(T, wide)
+    rows = far - 1 - 2 * torch.arange(T, device="cuda")
+    big[rows] = near
+    index, one = rows.to(torch.int32), lambda **kw: m.RowGroups(T, **kw)
+    w, wt = normal(1, N, wide), normal(1, wide, K)
+    q = m.Q4Weights(torch.randint(0, 256, (1, N, wide // 2), generator=g, device="cuda", dtype=torch.uint8),
+                    torch.rand(1, N, wide // 32, generator=g, device="cuda"))
+    note(f"behind 4 GiB {T}: inputs")
+    for cols, side, call in ((N, "in_index", lambda G, x, out: m.moe_grouped_linear(G, x, w, out)),
+                             (N, "in_index", lambda G, x, out: m.moe_q4_linear(G, q, x, out)),
+                             (K, "out_index", lambda G, x, out: m.moe_grouped_dgrad(G, x, wt, out))):
+        got, want = (torch.zeros(T, cols, device="cuda") for _ in range(2))
+        call(one(**{side: index}), big, got)
+        call(one(), near, want)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and want.abs().max() > 0
+    dw, dw0 = (torch.zeros(1, K, wide, device="cuda") for _ in range(2))
+    dy = normal(T, K)
+    m.moe_grouped_wgrad(one(in_index=index), big, dy, dw)
+    m.moe_grouped_wgrad(one(), near, dy, dw0)
+    torch.cuda.synchronize()
+    assert torch.equal(dw, dw0) and dw.abs().max() > 0
+    note(f"behind 4 GiB {T}: results")
+    x, out = normal(T, K), torch.zeros(T, wide, dtype=BF16, device="cuda")
+    big.zero_()
+    m.moe_grouped_linear(one(out_index=index), x, wt, big)
+    m.moe_grouped_linear(one(), x, wt, out)
+    torch.cuda.synchronize()
+    assert torch.equal(big[rows], out) and out.abs().max() > 0
+    assert not big[rows - 1].any() and not big[:100].any()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [2, 50])
 def test_q4_non_finite_values_stay_in_their_rows(m, T):
     c = Case(T, 0, 1, 256, 40, seed=16)
