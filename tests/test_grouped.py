@@ -156,7 +156,8 @@ def run_forward(m, c, out_t, what):
 
 # T, k, E, K, N: single rows, odd rows, tiles' edges, K and N that are no multiples of a tile, empty groups, many groups
 SHAPES = [
-    (1, 1, 1, 8, 8), (1, 0, 1, 1048, 72), (16, 0, 1, 136, 1000), (1, 2, 4, 64, 64), (1, 8, 256, 512, 136), (3, 2, 5, 72, 40), (5, 4, 16, 264, 520), (16, 1, 3, 128, 256),
+    (1, 1, 1, 8, 8), (1, 0, 1, 1048, 72), (4, 0, 1, 136, 16520), (16, 0, 1, 136, 1000), (1, 2, 4, 64, 64), (1, 8, 256, 512, 136),
+    (3, 2, 5, 72, 40), (5, 4, 16, 264, 520), (16, 1, 3, 128, 256),
     (17, 2, 4, 1000, 264), (33, 4, 8, 192, 128), (64, 1, 1, 256, 128), (65, 2, 3, 64, 192), (130, 4, 16, 520, 1000),
     (257, 2, 2, 128, 272), (300, 1, 300, 64, 64), (600, 2, 3, 320, 384), (1100, 1, 2, 1032, 520), (129, 0, 1, 512, 256),
 ]
