@@ -599,7 +599,7 @@ typedef struct {
  * projection.  Codes less zero points are exact in the products, sums are fp32,
  * a group's sum takes its scale in fp32, and a bf16 out is rounded once.  (Sums
  * hold up to 31 times |x|: x of 2^120 and above can overflow where the result
- * would not.)  A group's weights are read once for each 16 or 64 of its rows.
+ * would not.)  A group's weights are read once for each 16 to 64 of its rows.
  * Errors as above (codes, x and out 16-byte aligned).
  */
 moe_status moe_q4_linear(const moe_group_desc *g, const moe_q4_desc *w, const void *x, int32_t x_rows, int32_t act,
