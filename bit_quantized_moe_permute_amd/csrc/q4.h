@@ -183,8 +183,9 @@ template <int G, int KIND> struct Block {
 __device__ __forceinline__ uint4 splat(uint32_t v) { return make_uint4(v, v, v, v); }
 
 // One chunk's products of R blocks of 16 weight rows with NB blocks of 16 rows of x into acc; x(t, s) is block t's operand of
-// columns 32 s .. + 31. (No branch may stand between a matrix instruction and the reading of its result: the compiler then loses
-// the wait between the two on one of the ways.)
+// columns 32 s .. + 31. (No branch stands between a matrix instruction and the reading of its result: behind a branch around a load
+// the compiler has been seen to leave the shorter way too short a wait. Kernels that read their sums behind a loop have a branch
+// there; tests/test_matrix_waits.py walks every way of the built code.)
 template <int R, int NB, typename C, typename X>
 __device__ __forceinline__ void chunk_products(const Unpack &unpack, const C (&p)[R], X x, f32x4_t (&acc)[R][NB]) {
     constexpr int STEPS = 4 / C::NG;                         // instructions per group
