@@ -108,16 +108,18 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // --- eight consecutive columns of one thread -------------------------------------------------------------------
 struct Raw8 { uint4 lo, hi; };          // bf16: lo alone
 
-// 16 and 8 bytes at addresses that are aligned (AL) or whole elements only: one load or store either way
-struct __attribute__((packed)) Any16 { uint4 v; };
-struct __attribute__((packed)) Any8 { uint2 v; };
+// 16 and 8 bytes at addresses that are aligned (AL) or whole elements only: one load or store either way. (Vector types of the
+// compiler's own: a class like uint4 keeps its alignment in a packed struct.)
+struct __attribute__((packed)) Any16 { u32x4_t v; };
+struct __attribute__((packed)) Any8 { u32x2_t v; };
+static_assert(alignof(Any16) == 1 && alignof(Any8) == 1, "");
 template <bool AL> __device__ __forceinline__ uint4 get16(const void *p) {
     if constexpr (AL) return *static_cast<const uint4 *>(p);
-    else return static_cast<const Any16 *>(p)->v;
+    else return __builtin_bit_cast(uint4, static_cast<const Any16 *>(p)->v);
 }
 template <bool AL> __device__ __forceinline__ void put16(void *p, uint4 v) {
     if constexpr (AL) *static_cast<uint4 *>(p) = v;
-    else static_cast<Any16 *>(p)->v = v;
+    else static_cast<Any16 *>(p)->v = __builtin_bit_cast(u32x4_t, v);
 }
 
 template <bool BF16, bool AL> __device__ __forceinline__ Raw8 load8(const void *p, int64_t i) {
@@ -172,7 +174,7 @@ template <bool AL> __device__ __forceinline__ void store8_e4m3(void *p, int64_t 
     if constexpr (AL) {
         *reinterpret_cast<uint2 *>(q) = v;
     } else if (n == 8) {
-        reinterpret_cast<Any8 *>(q)->v = v;
+        reinterpret_cast<Any8 *>(q)->v = __builtin_bit_cast(u32x2_t, v);
     } else {
 #pragma unroll
         for (int e = 0; e < 7; ++e)
