@@ -21,6 +21,8 @@ SOURCES = ["api.cpp", "prep.hip", "route.hip", "ffn_generic.hip", "ffn_gemv.hip"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
+    # a host function that runs off its end goes on in other code; a packed struct that is not packed promises an alignment
+    "-Werror=return-type", "-Werror=packed-non-pod",
     # no packed-fp32 code generation (v_pk_*_f32)
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
@@ -32,10 +34,14 @@ def _compile(src: str) -> str:
     if src.endswith(".cpp"):
         cmd[1:1] = ["-x", "hip"]
     r = subprocess.run(cmd, capture_output=True, text=True)
+    # (the host side does not know the target feature, and says how often it said so)
     errs = "\n".join(l for l in r.stderr.splitlines()
-                     if "packed-fp32-ops" not in l and "unknown target feature" not in l)
+                     if "packed-fp32-ops" not in l and "unknown target feature" not in l
+                     and not l.endswith(("warning generated when compiling for host.", "warnings generated when compiling for host.")))
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{errs}")
+    if errs.strip():
+        print(f"{src}:\n{errs}", file=sys.stderr, flush=True)
     return obj
 
 
