@@ -105,6 +105,7 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
         last_q = a.n_out;
         begin = group_edge(a.g, group);
         end = group_edge(a.g, group + 1);
+        if (a.accumulate && end <= begin) return;            // stays as it is (-0 + 0 would be 0), and need not be read
     } else {
         const Tiles all = scan_tiles(a.g, TQ, tiles_q);
         const int total = all.total * tiles_p, per = (total + 7) / 8;
