@@ -146,14 +146,18 @@ __device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
 inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
 
 // silu(gate) * up. exp(-gate) as a power of two, times 1 + what the rounding of its exponent lost; the quotient through the
-// hardware's reciprocal: some 2 units of the last place, in 11 instructions (library exp and division take 40: for 256 x 256 results
+// hardware's reciprocal: some 2 units of the last place, in 16 instructions (library exp and division take 40: for 256 x 256 results
 // of a tile a tenth of its whole time). The correction is below 1e-5 where the quotient matters; its bounds keep a gate of 2e7 and
-// more, or an infinite one, from making it anything else.
+// more, or an infinite one, from making it anything else. Where exp(-gate) passes 2^64, 1 + exp(-gate) is exp(-gate), and what is
+// above goes to the other factor as a power of two: the sum would overflow from a gate of -88.7 on and its reciprocal leave the
+// normal floats at -87.3, while the product may be any float (from -131 on that factor is below 2^-126, and is 0).
 __device__ __forceinline__ float swiglu(float gate, float up) {
+#pragma clang fp contract(off)                               // 64 - t is of the rounded t, whose rest is in c
     constexpr float L = 1.44269502f, L_REST = 1.92596299e-8f, LN2 = 0.693147181f;    // log2(e) in two parts
     const float t = -gate * L, rest = __fmaf_rn(-gate, L_REST, __fmaf_rn(-gate, L, -t));
     const float c = __builtin_amdgcn_fmed3f(__fmaf_rn(rest, LN2, 1.f), 0.99f, 1.01f);
-    return gate * __builtin_amdgcn_rcpf(__fmaf_rn(__builtin_amdgcn_exp2f(t), c, 1.f)) * up;
+    const float s = __builtin_amdgcn_exp2f(fminf(64.f - t, 0.f));
+    return gate * __builtin_amdgcn_rcpf(__fmaf_rn(__builtin_amdgcn_exp2f(fminf(t, 64.f)), c, 1.f)) * (up * s);
 }
 
 }  // namespace moe

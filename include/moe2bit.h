@@ -531,7 +531,8 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_act;
  * for every position of group g, r and o its input and output row.
  *   x [x_rows][n_in] bf16; w [n_groups][n_out][n_in] bf16 (SwiGLU: n_out rows
  *   of G, then n_out of U, in each group); out [out_rows][n_out], fp32 or bf16.
- * Sums are fp32; a bf16 out is rounded once.  A row's result does not depend on
+ * Sums are fp32; a bf16 out is rounded once.  silu is right to some 2^-22 of its
+ * value down to gates of -131, and 0 below.  A row's result does not depend on
  * the other rows' values (a NaN or infinity stays in its own row), and repeated
  * calls give the same bits.
  * n_in and n_out must be multiples of 8, buffers 16-byte aligned; out must not

@@ -46,3 +46,44 @@ def test_accumulate_leaves_groups_without_rows_as_they_were(m, dtype, E, K, N):
 def test_accumulate(m, shape, dtype):
     """On the tiles of 256 x 256 (289 of one matrix, 600 of small ones) and of 128 x 128."""
     run_wgrad(m, Case(*shape, seed=53, dst="slots" if shape[1] else "sorted"), dtype, f"accumulate {shape}", accumulate=True)
+
+
+# ----------------------------------------------------------------------------
+# SwiGLU
+# ----------------------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 4, 40])
+@pytest.mark.parametrize("kind", ["bf16", "q4"])
+def test_swiglu_of_far_negative_gates(m, T, kind):
+    """silu(g) u for gates whose exp(-g) leaves the floats while the value does not: silu(-90) = -7e-38, times a u of 1e30.
+    Exponential, reciprocal and products are off by some 2^-22 (2^-20 taken) down to g = -131, where exp2's own result would be
+    below 2^-126 after 2^64 has been taken out; from there the value may be lost, and is at most |g| exp(g) |u|.  Products below
+    2^-126 are rounded to steps of 2^-149."""
+    step = 2.0**-3 if kind == "q4" else 0.5
+    gates = torch.cat([-80.0 - step * torch.arange(200), -105.0 - torch.arange(40)]).to(BF16 if kind == "bf16" else F32).float()
+    ups = torch.tensor([1.0, -2.0**60, 2.0**110, -2.0**-80, 2.0**127])
+    gates, ups = (t.reshape(-1) for t in torch.broadcast_tensors(gates[:, None], ups))
+    K, N = 64, gates.numel()
+    x = torch.zeros(T, K, dtype=BF16)
+    x[:, :2] = 1.0                                                  # x[0] makes the gate, x[1] the other half
+    out = torch.empty(T, N, device="cuda")
+    groups = m.RowGroups(T)
+    note(f"far negative gates {T} {kind}")
+    if kind == "bf16":
+        w = torch.zeros(1, 2 * N, K)
+        w[0, :N, 0], w[0, N:, 1] = gates, ups
+        m.moe_grouped_linear(groups, x.cuda(), w.to(BF16).cuda(), out, m.ACT_SWIGLU)
+    else:
+        codes = torch.full((1, 2 * N, K), 8, dtype=torch.uint8)
+        codes[0, :N, 0] = codes[0, N:, 1] = 9
+        s = torch.ones(1, 2 * N, K // 32)
+        s[0, :N, 0], s[0, N:, 0] = gates, ups
+        m.moe_q4_linear(groups, m.Q4Weights((codes[..., ::2] | codes[..., 1::2] << 4).contiguous().cuda(), s.cuda()), x.cuda(), out,
+                        m.ACT_SWIGLU)
+    torch.cuda.synchronize()
+    g, u = gates.double(), ups.double()
+    want = g * torch.sigmoid(g) * u
+    tol = torch.where(g >= -131, 2.0**-20 * want.abs() + 2.0**-149, want.abs() + 2.0**-149)
+    got = out.cpu().double()
+    bad = ~((got - want).abs() <= tol)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, gates {g[bad.any(0)][:8].tolist()}, others {u[bad.any(0)][:8].tolist()}"
