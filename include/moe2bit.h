@@ -532,7 +532,7 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_act;
  *   x [x_rows][n_in] bf16; w [n_groups][n_out][n_in] bf16 (SwiGLU: n_out rows
  *   of G, then n_out of U, in each group); out [out_rows][n_out], fp32 or bf16.
  * Sums are fp32; a bf16 out is rounded once.  silu is right to some 2^-22 of its
- * value down to gates of -131, and 0 below.  A row's result does not depend on
+ * value down to gates of -131, and may be 0 below.  A row's result does not depend on
  * the other rows' values (a NaN or infinity stays in its own row), and repeated
  * calls give the same bits.
  * n_in and n_out must be multiples of 8, buffers 16-byte aligned; out must not
@@ -598,9 +598,11 @@ typedef struct {
  * x [x_rows][cols] bf16; out [out_rows][rows] (SwiGLU: [out_rows][rows / 2], rows
  * even), fp32 or bf16.  With one matrix and offsets NULL it is a dense
  * projection.  Codes less zero points are exact in the products, sums are fp32,
- * a group's sum takes its scale in fp32, and a bf16 out is rounded once.  (Sums
- * hold up to 31 times |x|: x of 2^120 and above can overflow where the result
- * would not.)  A group's weights are read once for each 16 to 64 of its rows.
+ * a group's sum takes its scale in fp32, and a bf16 out is rounded once.  (A
+ * group's sum holds the products of its codes and zero points plus 16, up to
+ * 2432 times |x| on the way: x of 2^116 and above can overflow where the result
+ * would not, and an infinite x makes its row's results NaN.)  A group's weights
+ * are read once for each 16 to 64 of its rows.
  * Errors as above (codes, x and out 16-byte aligned).
  */
 moe_status moe_q4_linear(const moe_group_desc *g, const moe_q4_desc *w, const void *x, int32_t x_rows, int32_t act,

@@ -6,7 +6,7 @@ import os
 import pytest
 import torch
 
-from test_grouped import BF16, F32, LIB, Case, note, run_wgrad
+from test_grouped import BF16, F32, LIB, Q4, Case, note, run_wgrad
 
 
 @pytest.fixture(scope="module")
@@ -87,3 +87,50 @@ def test_swiglu_of_far_negative_gates(m, T, kind):
     got = out.cpu().double()
     bad = ~((got - want).abs() <= tol)
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, gates {g[bad.any(0)][:8].tolist()}, others {u[bad.any(0)][:8].tolist()}"
+
+
+# ----------------------------------------------------------------------------
+# 4-bit weights: the ends of the range of x
+# ----------------------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("group,zero", [(32, 15), (64, 15), (128, 15), (128, 0)])
+@pytest.mark.parametrize("T,N", [(1, 40), (50, 40), (50, 32800)])
+def test_q4_of_x_just_below_2_to_116(m, T, N, group, zero):
+    """Every x the largest bf16 below 2^116 and of one sign, codes and zero points that add up: an offset product of 32 columns and
+    the 3 x 32 columns before it come to at most 2432 |x| < 2^128.  2 K additions, each off by 2^-24 of a partial sum of at most
+    2432 |x|, K / group groups to a result."""
+    K, code = 256, 15 - zero
+    x = torch.full((T, K), 1.9921875 * 2.0**115, dtype=BF16)
+    x[1::2] *= -1
+    scale = 2.0**-12
+    q = m.Q4Weights(torch.full((1, N, K // 2), code * 17, dtype=torch.uint8, device="cuda"),
+                    torch.full((1, N, K // group), scale, device="cuda"),
+                    torch.full((1, N, K // group), zero, dtype=torch.uint8, device="cuda"))
+    out = torch.empty(T, N, device="cuda")
+    note(f"q4 of large x {T} {N} {group} {zero}")
+    m.moe_q4_linear(m.RowGroups(T), q, x.cuda(), out)
+    torch.cuda.synchronize()
+    want = (code - zero) * scale * x.double().sum(1, keepdim=True)
+    tol = 2 * K * 2.0**-24 * 2432 * x[0, 0].double().abs() * scale
+    assert ((out.cpu().double() - want).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("T,N", [(3, 40), (50, 32800)])
+def test_q4_of_an_x_that_is_not_finite(m, T, N, value):
+    """Its row is NaN throughout: (16 + code) x and -(16 + zero) x are infinities of both signs.  Other rows do not see it."""
+    c = Case(T, 0, 1, 192, N, seed=54)
+    q = Q4(c, 32, True, F32).on_gpu(m)
+    got = []
+    for v in (0.5, value):
+        c.x[1, 100] = v
+        for act in (m.ACT_NONE, m.ACT_SWIGLU):
+            out = torch.empty(T, N // (1 + act), device="cuda")
+            note(f"q4 of {v}")
+            m.moe_q4_linear(c.groups(m), q, c.x.cuda(), out, act)
+            torch.cuda.synchronize()
+            got.append(out.cpu())
+    rest = [t for t in range(T) if t != 1]
+    for clean, spoiled in zip(got[:2], got[2:]):
+        assert torch.equal(clean[rest], spoiled[rest]) and clean.isfinite().all() and spoiled[1].isnan().all()
