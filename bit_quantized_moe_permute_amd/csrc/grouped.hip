@@ -89,8 +89,9 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
     // Of the two waves that share a SIMD (w and w + 4 of eight), one has the first rows of the output and one the last: where a
     // tile is not full, the waves without rows leave the others the matrix cores.
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w4 = wave & 3, back = wave >> 2;
-    const int wp = NW < 8 ? wave / WQ : WQ == 4 ? w4 & 1 : WQ == 2 ? (w4 >> 1) + 2 * back : wave / WQ;
-    const int wq = NW < 8 ? wave % WQ : WQ == 4 ? (back ? 3 - (w4 >> 1) : w4 >> 1) : WQ == 2 ? (w4 + back) & 1 : wave % WQ;
+    static_assert(NW == 4 || (NW == 8 && (WQ == 2 || WQ == 4)), "");
+    const int wp = NW == 4 ? wave / WQ : WQ == 4 ? w4 & 1 : (w4 >> 1) + 2 * back;
+    const int wq = NW == 4 ? wave % WQ : WQ == 4 ? (back ? 3 - (w4 >> 1) : w4 >> 1) : (w4 + back) & 1;
     const int P = OP == GROUPED_FWD ? a.n_out : a.n_in;                               // results per row of the output
     // XCD-aware order: consecutive workgroups go to the eight XCDs in turn; each takes a run of tiles, in blocks of four tiles
     // along Q whose workgroups read the same rows on the other side

@@ -230,29 +230,25 @@ __device__ __forceinline__ void store(const Q4Args &a, int64_t i, float v) {
 }
 
 // ---------------------------------------------------------------------------
-// Few weights in all: a workgroup has 16 R weight rows (SwiGLU: 16 of gate and the same of up) and up to 16 positions of a group;
+// Few weights in all: a workgroup has 16 weight rows (SwiGLU: 16 of gate and the same of up) and up to 16 positions of a group;
 // its waves take the row's chunks in turn, FEW_AHEAD of them loaded at once, and their sums meet in LDS. 1 token, 4096 x 4096:
 // 5.2 us, the launch and two rounds of dependent loads; 4096 x 8192 8.1.
 // ---------------------------------------------------------------------------
 constexpr int FEW_WAVES = 8, FEW_AHEAD = 2;
 
-template <int R, int G, int KIND, bool SWIGLU>
+template <int G, int KIND, bool SWIGLU>
 __global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few(Q4Args a, int most, int tiles_n) {
-    static_assert(!SWIGLU || R == 2, "");
-    constexpr int ROWS = SWIGLU ? 16 : 16 * R;               // results per position
+    constexpr int R = SWIGLU ? 2 : 1;
     __shared__ __attribute__((aligned(16))) f32x4_t part[FEW_WAVES][R][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i16 = lane & 15, q = lane >> 4;
     Tile t;
     int n0;
-    if (!place(a.g, 16, ROWS, most, tiles_n, t, n0)) return;
+    if (!place(a.g, 16, 16, most, tiles_n, t, n0)) return;
     const int xr = t.begin + i16 < t.end ? in_row(a.g, t.begin + i16, a.x_rows) : -1, x_end = xr < 0 ? 0 : a.K - 8 * q;
     const uint16_t *x = a.x + (int64_t)max(xr, 0) * a.K + 8 * q;
     Rows<G, KIND> rows[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int first = SWIGLU ? n0 : min(n0 + 16 * r, a.N - 1);
-        rows[r].set(a, ((int64_t)t.group * (SWIGLU ? 2 : 1) + (SWIGLU ? r : 0)) * a.N + first, min(first + i16, a.N - 1) - first);
-    }
+    for (int r = 0; r < R; ++r) rows[r].set(a, ((int64_t)t.group * R + r) * a.N + n0, min(n0 + i16, a.N - 1) - n0);
     const int chunks = (a.K + CHUNK - 1) / CHUNK;
     const Unpack unpack;
     f32x4_t acc[R][1];
@@ -280,19 +276,18 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 4) void k_few(Q4Args a, int most, i
     __syncthreads();
     // lane l's four values are positions 4 (l / 16) .. + 3 of weight row l % 16
     const float *sums = reinterpret_cast<const float *>(part);
-    for (int e = threadIdx.x; e < 16 * ROWS; e += 64 * FEW_WAVES) {
-        const int n = e % ROWS, pos = e / ROWS;
-        if (t.begin + pos >= t.end || n0 + n >= a.N) continue;
-        const int row = out_row(a.g, t.begin + pos, a.out_rows);
-        if (row < 0) continue;
-        auto sum = [&](int r) {
-            float y = 0.f;
+    const int e = threadIdx.x, n = e & 15, pos = e >> 4;
+    if (pos >= 16 || t.begin + pos >= t.end || n0 + n >= a.N) return;
+    const int row = out_row(a.g, t.begin + pos, a.out_rows);
+    if (row < 0) return;
+    float y[R];
 #pragma unroll
-            for (int w = 0; w < FEW_WAVES; ++w) y += sums[((w * R + r) * 64 + (n & 15) + 16 * (pos >> 2)) * 4 + (pos & 3)];
-            return y;
-        };
-        store(a, (int64_t)row * a.N + n0 + n, SWIGLU ? swiglu(sum(0), sum(R - 1)) : sum(n >> 4));
+    for (int r = 0; r < R; ++r) {
+        y[r] = 0.f;
+#pragma unroll
+        for (int w = 0; w < FEW_WAVES; ++w) y[r] += sums[((w * R + r) * 64 + n + 16 * (pos >> 2)) * 4 + (pos & 3)];
     }
+    store(a, (int64_t)row * a.N + n0 + n, SWIGLU ? swiglu(y[0], y[R - 1]) : y[0]);
 }
 
 // ---------------------------------------------------------------------------
@@ -429,9 +424,10 @@ __global__ __launch_bounds__(64 * MANY_WAVES * KS, KS == 1 && (MAXB == 1 || (MAX
     int n0;
     if (!place(a.g, 16 * MAXB, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS, most, tiles_n, t, n0)) return;
     const int blocks = (t.end - t.begin + 15) / 16;
-    if (MAXB == 1 || blocks <= 1) many<1, 4, KS, G, KIND, SWIGLU>(a, t, n0, lds);
-    else if (MAXB == 2 || blocks == 2) many<MAXB == 1 ? 1 : 2, MAXB == 2 ? 2 : 4, KS, G, KIND, SWIGLU>(a, t, n0, lds);
-    else many<MAXB, MAXB == 4 ? 2 : 4, KS, G, KIND, SWIGLU>(a, t, n0, lds);
+    if constexpr (MAXB == 1) many<1, 4, KS, G, KIND, SWIGLU>(a, t, n0, lds);
+    else if (blocks <= 1) many<1, 4, KS, G, KIND, SWIGLU>(a, t, n0, lds);
+    else if (MAXB == 2 || blocks == 2) many<2, MAXB == 2 ? 2 : 4, KS, G, KIND, SWIGLU>(a, t, n0, lds);
+    else if constexpr (MAXB == 4) many<4, 2, KS, G, KIND, SWIGLU>(a, t, n0, lds);
 }
 
 int64_t tiles(int N, int rows) { return (N + rows - 1) / rows; }
@@ -444,10 +440,10 @@ template <int MAXB, int KS, int G, int KIND, bool SWIGLU> hipError_t launch_many
     return hipGetLastError();
 }
 
-template <int R, int G, int KIND, bool SWIGLU> hipError_t launch_few(const Q4Args &a, hipStream_t st) {
-    const int64_t tn = tiles(a.N, SWIGLU ? 16 : 16 * R), most = most_tiles(a.g, 16), blocks = (most * tn + 7) / 8 * 8;
+template <int G, int KIND, bool SWIGLU> hipError_t launch_few(const Q4Args &a, hipStream_t st) {
+    const int64_t tn = tiles(a.N, 16), most = most_tiles(a.g, 16), blocks = (most * tn + 7) / 8 * 8;
     if (!grid_fits(blocks, 64 * FEW_WAVES)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_few<R, G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0, st, a, (int)most, (int)tn);
+    hipLaunchKernelGGL((k_few<G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0, st, a, (int)most, (int)tn);
     return hipGetLastError();
 }
 
@@ -467,7 +463,7 @@ template <int G, int KIND, bool SWIGLU> hipError_t launch_kind(const Q4Args &a, 
     // groups that can have rows, and rows of one of them
     const int64_t used = a.g.n < a.g.rows ? a.g.n : a.g.rows, mean = (a.g.rows + used - 1) / used, most = (mean + 63) / 64 * used;
     const int64_t many = tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS) * most;
-    if (many < MANY_FROM) return launch_few<SWIGLU ? 2 : 1, G, KIND, SWIGLU>(a, st);
+    if (many < MANY_FROM) return launch_few<G, KIND, SWIGLU>(a, st);
     if (mean < (used > 1 ? 8 : 17)) return many < HALVES_BELOW ? launch_many<1, 2, G, KIND, SWIGLU>(a, st) : launch_many<1, 1, G, KIND, SWIGLU>(a, st);
     if (used > 1 && mean <= 32 && many >= HALVES_BELOW) return launch_many<2, 1, G, KIND, SWIGLU>(a, st);
     return many < HALVES_BELOW ? launch_many<4, 2, G, KIND, SWIGLU>(a, st) : launch_many<4, 1, G, KIND, SWIGLU>(a, st);
