@@ -1,0 +1,68 @@
+// Which kernel a call of the grouped products takes, by its counts and sizes alone. Host code without HIP: the test compiles it
+// by itself.
+#pragma once
+#include <cstdint>
+
+namespace moe {
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The positions of a call: groups that can have any, and their mean.
+struct Load {
+    int64_t used, rows, mean;
+    Load(int n_groups, int n_rows) : used(n_groups < n_rows ? n_groups : n_rows), rows(n_rows), mean(ceil_div(n_rows, used)) {}
+    // Tiles of up to `height` positions to expect: those of one group; of several, which share the positions unevenly, half a tile
+    // to each above whole ones, and one to each at least.
+    int64_t tiles(int height) const {
+        if (used == 1) return ceil_div(rows, height);
+        const int64_t t = rows / height + used / 2;
+        return t > used ? t : used;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// moe_q4_linear (q4.h): k_few with 16 weight rows to a workgroup, or k_many with 128 (SwiGLU: 64 of each half) and tiles of 16, 32
+// or 64 positions, along all of K or in two halves of it. Calls in us (weights of 4096 columns, one matrix, where nothing else is
+// said), the kernel taken first:
+//
+//   k_few while k_many's workgroups of 16 positions (w16) would be few: its time grows with w16, faster with more rows to a tile,
+//     where the other's stands still up to 256. Up to 160 with 4 rows at most: 1 row of 20480 rows of weights (160) 16.6 (halves of
+//     16: 18.4), of 24576 (192) 18.4 (few: 19.0), 4 of 20480 19.1 (19.2). Up to 128 with 8: 8 of 16384 (128) 18.4 (19.0), of 24576
+//     (192) 19.2 (26.2). Up to 96 with more: 16 of 12288 (96) 18.4 (19.3), 24 of 6144 (96) 18.3 (19.1), 16 of 16384 (128) 19.2
+//     (23.5), 64 of 8192 (256) 19.3 (44.3), 256 of 2048 (256) 19.8 (44.3); 16384 columns: 32 of 4096 (64) 44.5 (58), 64 (128) 58
+//     (86). Up to 128 where K is too short for halves: 1280 columns 64 of 4096 (128) 8.8 (10.3), 1024 columns 64 of 4096 9.2 (9.2),
+//     128 (256) 9.4 (16.4)
+//   tiles of 16 while these fit one round of the chip's 256 units, in two halves of K from 16 chunks of 128 columns on: 64 of 8192
+//     19.3 (whole: 21.8), 2048 columns 64 of 4096 12.3 (12.9); below them the second half has little or nothing: 1024 columns 128
+//     of 4096 whole 9.4 (halves: 11.1), 16384 rows of weights and 24 9.3 (11.0)
+//   beyond, up to 512 workgroups of tiles of 64 (w64):
+//     tiles of 64 in halves where the groups have 32 rows at most and one round holds them: 24 of 24576 24.9 (16: 29.5, 32: 30.6),
+//       24 of 32768 25.5 (16: 29.9)
+//     tiles of 16 up to two rounds: 128 of 8192 29.7 (32: 30.2, halves of 64: 36.5), 48 of 16384 29.5 (30.2, 35.6)
+//     tiles of 64 in halves in one round: 1024 of 2048 37.7 (32: 42.4, 16: 53.4), 64 of 24576 37.1 (41.8, 40.5)
+//     else tiles of 32: 128 of 24576 58.6 (64: 63.2, in halves 71.3, 16: 75.2), 512 tokens of 2 among 8 experts of 2048 rows 56.3
+//       (64.4, 73.6, 64.1); 1024 columns 128 of 16384 16.3 (17.4, 19.2, 20.2)
+//   from 512 on by the mean of the groups, along all of K (halves: 3 tokens of 8 among 256 experts, 768 workgroups, 58.7 against
+//     47.5). Tiles of 16 or 32 leave three waves to a SIMD registers, tiles of 64 two, but they read a group's weights once (the
+//     others' second reading comes out of caches). 256 experts of 4096 x 2048, a token's 8 spread unevenly, tiles of 16, 32, 64: mean
+//     4 260, 268, 309; 8 327, 319, 398; 16 453, 401, 475; 31 693, 566, 614; 62 1177, 903, 863. One group has just its rows: 16 of
+//     65536 rows of weights 38.6 (64: 38.9), 17 44.3 (16: 57.5, 32: 46.1).
+// ---------------------------------------------------------------------------
+enum Q4Kernel { Q4_FEW, Q4_16_HALVES, Q4_16, Q4_32, Q4_64_HALVES, Q4_64 };
+
+inline Q4Kernel q4_choice(bool swiglu, int n_groups, int n_rows, int N, int K) {
+    const Load l(n_groups, n_rows);
+    const int64_t tiles_n = ceil_div(N, swiglu ? 64 : 128), w16 = l.tiles(16) * tiles_n, w64 = l.tiles(64) * tiles_n;
+    const bool one = l.used == 1, halves = K >= 16 * 128;
+    if (w16 <= (l.mean <= 4 ? 160 : l.mean <= 8 || !halves ? 128 : 96)) return Q4_FEW;
+    if (w16 <= 256) return halves ? Q4_16_HALVES : Q4_16;
+    if (w64 < 512) {
+        if (halves && w64 <= 256 && (one ? l.mean : 2 * l.mean) <= 32) return Q4_64_HALVES;
+        if (w16 <= 512) return Q4_16;
+        return halves && w64 <= 256 ? Q4_64_HALVES : Q4_32;
+    }
+    if (l.mean < (one ? 17 : 8)) return Q4_16;
+    return !one && l.mean <= 32 ? Q4_32 : Q4_64;
+}
+
+}  // namespace moe

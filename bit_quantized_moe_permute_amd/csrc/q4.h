@@ -21,6 +21,7 @@
 // 8 (l / 16) .. + 7. Codes are loaded 16 bytes (32 columns) to a lane, four lanes to a row; a 4 x 4 exchange of dwords among these
 // four gives each instruction 32 consecutive columns, so that any group of 32 or more is whole.
 #pragma once
+#include "choice.h"
 #include "groups.h"
 
 using namespace moe;
@@ -430,43 +431,31 @@ __global__ __launch_bounds__(64 * MANY_WAVES * KS, KS == 1 && (MAXB == 1 || (MAX
     else if constexpr (MAXB == 4) many<4, 2, KS, G, KIND, SWIGLU>(a, t, n0, lds);
 }
 
-int64_t tiles(int N, int rows) { return (N + rows - 1) / rows; }
-
 template <int MAXB, int KS, int G, int KIND, bool SWIGLU> hipError_t launch_many(const Q4Args &a, hipStream_t st) {
     constexpr int threads = 64 * MANY_WAVES * KS;
-    const int64_t tn = tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS), most = most_tiles(a.g, 16 * MAXB), blocks = (most * tn + 7) / 8 * 8;
+    const int64_t tn = ceil_div(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS), most = most_tiles(a.g, 16 * MAXB), blocks = (most * tn + 7) / 8 * 8;
     if (!grid_fits(blocks, threads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((k_many<MAXB, KS, G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(threads), 0, st, a, (int)most, (int)tn);
     return hipGetLastError();
 }
 
 template <int G, int KIND, bool SWIGLU> hipError_t launch_few(const Q4Args &a, hipStream_t st) {
-    const int64_t tn = tiles(a.N, 16), most = most_tiles(a.g, 16), blocks = (most * tn + 7) / 8 * 8;
+    const int64_t tn = ceil_div(a.N, 16), most = most_tiles(a.g, 16), blocks = (most * tn + 7) / 8 * 8;
     if (!grid_fits(blocks, 64 * FEW_WAVES)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((k_few<G, KIND, SWIGLU>), dim3((unsigned)blocks), dim3(64 * FEW_WAVES), 0, st, a, (int)most, (int)tn);
     return hipGetLastError();
 }
 
-// The kernel of a call, by the workgroups that k_many would have for the chip's 256 units. Whole calls in us, weights of 4096
-// columns:
-//   k_few below MANY_FROM, k_many from there: 1 token, 8192 rows of weights 8.1 (k_many: 18.3), 16384 rows 13.7 (18.3), 24576 rows
-//     19.0 (18.4; k_many has 192 workgroups); 64 tokens, 2048 rows 12.7 (35.9), 8192 rows 44 (36); 24 tokens, 8192 rows 23.3 (24.7)
-//   halves of K below HALVES_BELOW (less than two workgroups to a unit): 32768 rows, 1 token 18.6 (one: 23.5), 64 tokens 37.5 (40.7);
-//     above: 3 tokens of 8 among 256 experts (736 workgroups) 47.5 (halves: 58.7), 2048 tokens, 4096 rows 117 (136)
-//   tiles of 16 or 32 positions leave three waves to a SIMD registers, tiles of 64 two, but they read a group's weights once (the
-//     others' second reading comes out of caches). By the mean of 256 experts of 4096 x 2048, a token's 8 spread unevenly, tiles of
-//     16, 32, 64: mean 4 260, 268, 309; 8 327, 319, 398; 16 453, 401, 475; 31 693, 566, 614; 62 1177, 903, 863. One group has just
-//     its rows: 16 of 65536 rows of weights 38.6 (64: 38.9), 17 44.3 (16: 57.5, 32: 46.1).
-constexpr int MANY_FROM = 256, HALVES_BELOW = 512;
-
 template <int G, int KIND, bool SWIGLU> hipError_t launch_kind(const Q4Args &a, hipStream_t st) {
-    // groups that can have rows, and rows of one of them
-    const int64_t used = a.g.n < a.g.rows ? a.g.n : a.g.rows, mean = (a.g.rows + used - 1) / used, most = (mean + 63) / 64 * used;
-    const int64_t many = tiles(a.N, SWIGLU ? MANY_ROWS / 2 : MANY_ROWS) * most;
-    if (many < MANY_FROM) return launch_few<G, KIND, SWIGLU>(a, st);
-    if (mean < (used > 1 ? 8 : 17)) return many < HALVES_BELOW ? launch_many<1, 2, G, KIND, SWIGLU>(a, st) : launch_many<1, 1, G, KIND, SWIGLU>(a, st);
-    if (used > 1 && mean <= 32 && many >= HALVES_BELOW) return launch_many<2, 1, G, KIND, SWIGLU>(a, st);
-    return many < HALVES_BELOW ? launch_many<4, 2, G, KIND, SWIGLU>(a, st) : launch_many<4, 1, G, KIND, SWIGLU>(a, st);
+    switch (q4_choice(SWIGLU, a.g.n, a.g.rows, a.N, a.K)) {
+        case Q4_FEW: return launch_few<G, KIND, SWIGLU>(a, st);
+        case Q4_16_HALVES: return launch_many<1, 2, G, KIND, SWIGLU>(a, st);
+        case Q4_16: return launch_many<1, 1, G, KIND, SWIGLU>(a, st);
+        case Q4_32: return launch_many<2, 1, G, KIND, SWIGLU>(a, st);
+        case Q4_64_HALVES: return launch_many<4, 2, G, KIND, SWIGLU>(a, st);
+        case Q4_64: break;
+    }
+    return launch_many<4, 1, G, KIND, SWIGLU>(a, st);
 }
 
 template <int G, int KIND> hipError_t launch_act(const Q4Args &a, hipStream_t st) {

@@ -1,0 +1,16 @@
+// Prints the kernel that a call takes, for lines of: operation, SwiGLU, groups, rows, n_out, n_in.
+#include <cstdio>
+#include <cstring>
+
+#include "choice.h"
+
+int main() {
+    static const char *const q4[] = {"few", "16 halves", "16", "32", "64 halves", "64"};
+    char op[16];
+    int swiglu, groups, rows, n_out, n_in;
+    while (scanf("%15s %d %d %d %d %d", op, &swiglu, &groups, &rows, &n_out, &n_in) == 6) {
+        if (!strcmp(op, "q4")) puts(q4[moe::q4_choice(swiglu, groups, rows, n_out, n_in)]);
+        else return 1;
+    }
+    return 0;
+}

@@ -1,12 +1,10 @@
 """The grouped products where a call's sizes choose another kernel, and the values at the edges of their numerics.
 
 Tolerances are those of test_grouped.py (its docstring derives them)."""
-import os
-
 import pytest
 import torch
 
-from test_grouped import BF16, F32, LIB, Q4, Case, note, run_wgrad
+from test_grouped import BF16, F32, Q4, U, Case, compare, guarded, note, run_q4, run_wgrad, swiglu
 
 
 @pytest.fixture(scope="module")
@@ -134,3 +132,53 @@ def test_q4_of_an_x_that_is_not_finite(m, T, N, value):
     rest = [t for t in range(T) if t != 1]
     for clean, spoiled in zip(got[:2], got[2:]):
         assert torch.equal(clean[rest], spoiled[rest]) and clean.isfinite().all() and spoiled[1].isnan().all()
+
+
+# ----------------------------------------------------------------------------
+# 4-bit weights: every kernel (test_grouped_choice.py holds the shapes to their kernels)
+# ----------------------------------------------------------------------------
+# kernel -> rows, weight rows: ends of rows and tiles inside the last block
+Q4_ROWS = {"few": (37, 150), "16 halves": (157, 1290), "16": (410, 1290), "32": (2090, 1290), "64 halves": (890, 1290), "64": (3005, 1290)}
+# columns, group, scales, zero points: rows that end inside a chunk of 128, a second and third block of 32 groups (from 1024 columns
+# with groups of 32, 2048 with 64, 4096 with 128), in one and in two halves
+Q4_COLUMNS = [(96, 32, F32, False), (1056, 32, F32, False), (2144, 32, torch.float16, True), (2240, 64, F32, False),
+              (4288, 64, torch.float16, True), (4480, 128, F32, True), (8448, 128, BF16, False)]
+Q4_EXPERTS = [("16", (6, 4, 24, 192, 2730)), ("16", (3, 8, 30, 160, 2820)), ("64 halves", (64, 2, 8, 2112, 2720)), ("32", (280, 2, 8, 256, 2720))]
+
+
+def q4_paths():
+    return [(kernel, T, N, K) for kernel, (T, N) in Q4_ROWS.items() for K, *_ in Q4_COLUMNS if "halves" not in kernel or K >= 2048]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [False, True], ids=["plain", "swiglu"])
+@pytest.mark.parametrize("kernel,T,N,K", q4_paths())
+def test_q4_paths(m, kernel, T, N, K, act):
+    _, group, scale_t, with_zero = next(c for c in Q4_COLUMNS if c[0] == K)
+    g = torch.Generator(device="cuda").manual_seed(55)
+    what = f"q4 {kernel} {T} rows, {N} x {K}, groups of {group}, {scale_t}, zero points {with_zero}, swiglu {act}"
+    codes = torch.randint(0, 256, (1, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scale = ((0.5 + torch.rand(1, N, K // group, generator=g, device="cuda")) * K**-0.5 / 8).to(scale_t)
+    zero = torch.randint(0, 16, (1, N, K // group), generator=g, device="cuda", dtype=torch.uint8) if with_zero else None
+    x = torch.randn(T, K, generator=g, device="cuda").to(BF16)
+    fill = 5.5
+    whole, out = guarded(T, N // (1 + act), F32, fill)
+    note(what)
+    m.moe_q4_linear(m.RowGroups(T), m.Q4Weights(codes, scale, zero), x, out, m.ACT_SWIGLU if act else m.ACT_NONE)
+    torch.cuda.synchronize()
+    q = torch.stack([codes[0] & 15, codes[0] >> 4], dim=2).view(N, K).double()
+    per = lambda t: t.double().repeat_interleave(group, dim=1)
+    w = (q - (8.0 if zero is None else per(zero[0]))) * per(scale[0])
+    y, t = x.double() @ w.T, 4 * (2 * K)**0.5 * U * torch.sqrt(x.double().square() @ (31 * per(scale[0])).square().T)
+    if act:
+        y, t = swiglu(y, t)
+    more = y.new_zeros(3, y.shape[1])
+    compare(whole, torch.cat([y, more]).cpu(), torch.cat([t, more]).cpu(), list(range(T)), fill, what)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel,shape", Q4_EXPERTS, ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else v)
+def test_q4_paths_of_experts(m, kernel, shape):
+    """Down projections of few and more tokens: no activation, in slot order."""
+    c = Case(*shape, seed=56, dst="slots")
+    run_q4(m, c, Q4(c, 32, True, torch.float16), F32, f"q4 {kernel} {shape}")
