@@ -65,4 +65,25 @@ inline Q4Kernel q4_choice(bool swiglu, int n_groups, int n_rows, int N, int K) {
     return !one && l.mean <= 32 ? Q4_32 : Q4_64;
 }
 
+// ---------------------------------------------------------------------------
+// moe_grouped_linear and moe_grouped_dgrad (grouped.hip). Calls in us, the kernel taken first, one matrix of 4096 x 4096 or weights of
+// 4096 columns where nothing else is said.
+//
+//   k_few_rows (16 weight rows to a workgroup, forward only) while its workgroups are few: its time grows with them, where the tiles'
+//     stands still until these fill the chip.
+//     Below 2048 workgroups for up to 4 rows of one matrix, which are read from the caches all along: 1 row, 16384 rows of weights
+//       (1024) 31.5 (tiles: 37), 24576 (1536) 37 (44), 4 rows of 16384 33 (37)
+//     Below 1024 for up to 16 rows: 1 row 7.6 (26), 16 rows 9.7 (26), 12288 rows of weights (768) 19 (32), 16 of these 27 (32), 1024 x
+//       1024 and one token of 4 among 64 experts 4.4 (9.6). There tiles: 16 rows of 16384 (1024) 38 (few: 41), 16 tokens of 2 among 16
+//       experts of 1024 x 1024 10.3 (11.7)
+//     Up to 768 for more: 24 rows (512) 16.5 (26.4), 48 (768) 23.4 (27.1), 64 (1024) 27.1 (few: 30.3), 1024 rows of weights and 192 (768)
+//       23.3 (27.1), 256 (1024) 27.1 (30.2), 1024 columns 32 rows (512) 6.6 (9.0), 64 (1024) 9.3 (11.1), 16384 columns 32 (512) 66
+//       (116), 64 (1024) 123 (121)
+// ---------------------------------------------------------------------------
+inline bool few_rows_choice(bool swiglu, int n_groups, int n_rows, int n_out) {
+    const Load l(n_groups, n_rows);
+    const int64_t workgroups = l.tiles(16) * ceil_div(n_out, 16) * (swiglu ? 2 : 1);         // (in SwiGLU's each has twice the weights)
+    return workgroups < (l.used == 1 && l.mean <= 4 ? 2048 : l.mean <= 16 ? 1024 : 769);
+}
+
 }  // namespace moe

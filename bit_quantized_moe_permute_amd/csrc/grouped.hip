@@ -11,6 +11,7 @@
 // moves 5.15 TB/s.
 #include <type_traits>
 
+#include "choice.h"
 #include "groups.h"
 
 using namespace moe;
@@ -460,11 +461,7 @@ template <bool SWIGLU> static hipError_t launch_few_rows(const GroupedArgs &a, h
 
 // The kernel of a call, by the rows of one expert (`mean`; `used` experts can have rows) and by the tiles there are for the chip's 256
 // compute units. Whole calls in us, the one taken first, weights of 4096 x 4096 to an expert where nothing else is said:
-//   few rows: 16 weight rows per workgroup while tiles of 128 would leave half of the units idle: 1 token 7.5 (tiles: 26), 16 tokens
-//     9.6 (26), 12288 rows of weights 19 (32), 16 tokens of these 27 (32), 1024 x 1024 and one token of 4 among 64 experts 5.5 (9.7).
-//     From 128 tiles on up to 4 rows of one group only, which are read from the caches all along: 1 token, 16384 rows of weights 31.5
-//     (37), 24576 37 (44), 4 tokens 41 (46). There tiles: 16 tokens, 16384 rows of weights 38 (few: 41), 16 tokens of 2 among 16
-//     experts of 1024 x 1024 12.6 (18.7), one token's 8 of 256 experts of 4096 x 4096 49 (63)
+//   few rows: the rule and its figures stand at few_rows_choice()
 //   128 x 64: 16384 slots of 64 rows 1910 (256 x 128 of 4 waves: 1737), 512 tokens 28 (128 x 128: 30, 256 x 128: 46 to 55), 300 x 4
 //     rows of 16 experts 11 (13, 14 to 24); three steps of 64 in the ring (six: 11 to 12, four of 32: 13)
 //   256 x 128, 4 waves, two workgroups to a unit: from 48 rows an expert, where the weights' stream counts: 64 rows of 256 experts
@@ -486,10 +483,8 @@ template <int OP, bool SWIGLU> static hipError_t launch_op(const GroupedArgs &a,
         if (mean >= 192 && t256 >= 512) return launch_tile<OP, 4, 2, 2, 4, 64, 2, SWIGLU>(a, st);
         if (mean >= 192 && t128 >= 192) return launch_tile<OP, 2, 2, 4, 2, 64, 3, SWIGLU>(a, st);
         if (mean >= 48 && t128 >= 256) return launch_tile<OP, 4, 2, 2, 2, 32, 3, SWIGLU>(a, st);
-        if constexpr (OP == GROUPED_FWD) {
-            const int64_t tiles = used * (((SWIGLU ? 2 * a.n_out : a.n_out) + 127) / 128);
-            if (mean <= 16 && tiles < (used == 1 && mean <= 4 ? 256 : 128)) return launch_few_rows<SWIGLU>(a, st);
-        }
+        if constexpr (OP == GROUPED_FWD)
+            if (few_rows_choice(SWIGLU, a.g.n, a.g.rows, a.n_out)) return launch_few_rows<SWIGLU>(a, st);
         return launch_tile<OP, 2, 1, 2, 2, 64, 3, SWIGLU>(a, st);
     }
 }

@@ -10,6 +10,7 @@ int main() {
     int swiglu, groups, rows, n_out, n_in;
     while (scanf("%15s %d %d %d %d %d", op, &swiglu, &groups, &rows, &n_out, &n_in) == 6) {
         if (!strcmp(op, "q4")) puts(q4[moe::q4_choice(swiglu, groups, rows, n_out, n_in)]);
+        else if (!strcmp(op, "linear")) puts(moe::few_rows_choice(swiglu, groups, rows, n_out) ? "few rows" : "tiles");
         else return 1;
     }
     return 0;

@@ -58,6 +58,22 @@ def test_q4(choose):
     check(choose, [("q4", *c) for c in Q4])
 
 
+# SwiGLU, groups, rows, weight rows (of one half), columns -> kernel
+FEW_ROWS = [
+    (0, 1, 1, 4096, 4096, "few rows"), (0, 1, 4, 32752, 4096, "few rows"), (0, 1, 4, 32768, 4096, "tiles"),
+    (0, 1, 5, 16384, 4096, "tiles"), (0, 1, 16, 12288, 4096, "few rows"), (0, 1, 16, 16384, 4096, "tiles"),
+    (0, 1, 17, 4096, 4096, "few rows"), (0, 1, 48, 4096, 4096, "few rows"), (0, 1, 49, 4096, 4096, "tiles"),
+    (0, 1, 192, 1024, 4096, "few rows"), (0, 1, 193, 1024, 4096, "tiles"), (0, 1, 32, 8192, 4096, "tiles"),
+    (0, 64, 4, 1024, 1024, "few rows"), (0, 16, 32, 1024, 1024, "tiles"), (1, 256, 8, 2048, 4096, "tiles"),
+    (1, 8, 2, 2048, 4096, "few rows"), (1, 1, 4, 16384, 4096, "tiles"), (1, 1, 4, 16368, 4096, "few rows"),
+    (0, 16, 1200, 520, 1000, "tiles"), (1, 16, 80, 264, 520, "few rows"),
+]
+
+
+def test_few_rows(choose):
+    check(choose, [("linear", *c) for c in FEW_ROWS])
+
+
 def test_the_gpu_tests_reach_their_kernels(choose):
     check(choose, [("q4", swiglu, 1, T, N // (1 + swiglu), K, kernel) for kernel, T, N, K in paths.q4_paths() for swiglu in (0, 1)])
     check(choose, [("q4", 0, E, T * max(k, 1), N, K, kernel) for kernel, (T, k, E, K, N) in paths.Q4_EXPERTS])

@@ -4,7 +4,7 @@ Tolerances are those of test_grouped.py (its docstring derives them)."""
 import pytest
 import torch
 
-from test_grouped import BF16, F32, Q4, U, Case, compare, guarded, note, run_q4, run_wgrad, swiglu
+from test_grouped import BF16, F32, LAYOUTS, Q4, U, Case, compare, guarded, note, run_forward, run_q4, run_wgrad, swiglu
 
 
 @pytest.fixture(scope="module")
@@ -182,3 +182,17 @@ def test_q4_paths_of_experts(m, kernel, shape):
     """Down projections of few and more tokens: no activation, in slot order."""
     c = Case(*shape, seed=56, dst="slots")
     run_q4(m, c, Q4(c, 32, True, torch.float16), F32, f"q4 {kernel} {shape}")
+
+
+# ----------------------------------------------------------------------------
+# bf16 weights: every kernel
+# ----------------------------------------------------------------------------
+# what test_grouped.LAYOUTS are, on shapes whose groups have more than 16 rows and few weight rows, and more of these
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS, ids=lambda d: "-".join(map(str, d.values())))
+@pytest.mark.parametrize("shape", [(140, 3, 9, 328, 136), (140, 3, 9, 328, 616), (33, 2, 3, 1096, 200)], ids=lambda s: "x".join(map(str, s)))
+def test_linear_layouts_of_more_rows(m, shape, layout):
+    c = Case(*shape, seed=57, **layout)
+    run_forward(m, c, F32, f"linear {shape} {layout}")
+    c.swiglu, c.w = True, torch.cat([c.w, c.w.flip(1)], dim=1)
+    run_forward(m, c, BF16, f"linear {shape} {layout} swiglu")
