@@ -79,11 +79,45 @@ inline Q4Kernel q4_choice(bool swiglu, int n_groups, int n_rows, int N, int K) {
 //     Up to 768 for more: 24 rows (512) 16.5 (26.4), 48 (768) 23.4 (27.1), 64 (1024) 27.1 (few: 30.3), 1024 rows of weights and 192 (768)
 //       23.3 (27.1), 256 (1024) 27.1 (30.2), 1024 columns 32 rows (512) 6.6 (9.0), 64 (1024) 9.3 (11.1), 16384 columns 32 (512) 66
 //       (116), 64 (1024) 123 (121)
+//
+//   The tiles, by their numbers t128 of 256 x 128 and t256 of 256 x 256 results (SwiGLU: of both halves) against 256 units; one
+//   workgroup of 8 waves fills a unit. What is left of several groups' positions counts as half a tile each.
+//     256 x 128 or 256 x 256 of 8 waves, from 128 rows a group and 160 tiles of 256 x 128 on, where the rounds of 256 workgroups are
+//       fewer, one of 256 x 128 counted as 0.61 of one of 256 x 256 (63 us; 111 for one, 96 each of two, sums of 4096): forward, one matrix of 4096 x
+//       4096, 2048 rows (1 round, 1) 63 (256 x 256: 80), 2560 (2, 1) 87 (256 x 128: 109), 4096 (2, 1) 111 (125), 6144 (3, 2) 190 (192),
+//       8192 (4, 2) 224 (255); input's gradient the same to 3%. 2048 tokens of 8 among 32 experts, input's gradient of 4096 -> 2048
+//       (9, 5) 321 (342), of 2048 -> 4096 (5, 3) 348 (334), 1024 tokens of that (3, 2) 206 (228). 4096 tokens of 4
+//       among 16 experts of 520 x 1000 (2, 1) 32 (37). Less than 160: 1024 rows (128) 43.7 with 128 x 64 (256 x 128: 46); from there:
+//       1280 (160) 50 (69).
+//     Several groups of 128 to 255 rows have most in one tile of 256: 512 tokens of 8 among 32 experts, input's gradient, 4096 ->
+//       2048 139 (256 x 128: 144), 2048 -> 4096 116 (146), 768 of these 157 (170) and 132 (145), forward 144 (153; SwiGLU 280 and 272),
+//       4096 tokens of 8 among 256 experts with SwiGLU 1939 (2307; 256 x 128 of 4 waves 2554)
+//     256 x 128 of 4 waves, two workgroups to a unit, from 256 tiles on, forward from 48 rows a group: 2048 tokens of 8 among 256
+//       experts with SwiGLU 1737 (8 waves 1782, 128 x 64 1910), 1024 of these (32 rows) 1737 with 128 x 64 (256 x 128 1810). The input's
+//       gradient from 1 row on if its sum is long: one token's row in each of 32 experts, 4096 -> 2048 99 (128 x 64: 130), 4 tokens of 8
+//       among 256, 2048 -> 4096, 91 (100), 128 of 8 among 32 103 (135), 256 experts 797 (838); sums of 512: 16 tokens of 4 among 64
+//       experts of 512 x 1024 10.7 (256 x 128: 12.2), 256 of these 13.8 (14.7)
+//     128 x 64 else: 300 x 4 rows of 16 experts 11 (128 x 128 13, 256 x 128 14 to 24)
 // ---------------------------------------------------------------------------
 inline bool few_rows_choice(bool swiglu, int n_groups, int n_rows, int n_out) {
     const Load l(n_groups, n_rows);
     const int64_t workgroups = l.tiles(16) * ceil_div(n_out, 16) * (swiglu ? 2 : 1);         // (in SwiGLU's each has twice the weights)
     return workgroups < (l.used == 1 && l.mean <= 4 ? 2048 : l.mean <= 16 ? 1024 : 769);
+}
+
+enum GroupedKernel { TILE_128_64, TILE_256_128_4, TILE_256_128_8, TILE_256_256, FEW_ROWS };
+
+// dgrad: the input's gradient
+inline GroupedKernel grouped_choice(bool dgrad, bool swiglu, int n_groups, int n_rows, int n_out, int n_in) {
+    const Load l(n_groups, n_rows);
+    const int64_t tiles_p = ceil_div(dgrad ? n_in : swiglu ? 2 * n_out : n_out, 256);
+    const int64_t t128 = l.tiles(128) * tiles_p, t256 = l.tiles(256) * tiles_p;
+    if (l.mean >= 128 && t128 >= 160) {
+        if (l.used > 1 && l.mean < 256) return TILE_256_256;
+        return 61 * ceil_div(t128, 256) < 100 * ceil_div(t256, 256) ? TILE_256_128_8 : TILE_256_256;
+    }
+    if (t128 >= 256 && (l.mean >= 48 || (dgrad && n_out >= 1024))) return TILE_256_128_4;
+    return !dgrad && few_rows_choice(swiglu, n_groups, n_rows, n_out) ? FEW_ROWS : TILE_128_64;
 }
 
 }  // namespace moe

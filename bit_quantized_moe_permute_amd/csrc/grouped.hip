@@ -459,32 +459,28 @@ template <bool SWIGLU> static hipError_t launch_few_rows(const GroupedArgs &a, h
     return hipGetLastError();
 }
 
-// The kernel of a call, by the rows of one expert (`mean`; `used` experts can have rows) and by the tiles there are for the chip's 256
-// compute units. Whole calls in us, the one taken first, weights of 4096 x 4096 to an expert where nothing else is said:
-//   few rows: the rule and its figures stand at few_rows_choice()
-//   128 x 64: 16384 slots of 64 rows 1910 (256 x 128 of 4 waves: 1737), 512 tokens 28 (128 x 128: 30, 256 x 128: 46 to 55), 300 x 4
-//     rows of 16 experts 11 (13, 14 to 24); three steps of 64 in the ring (six: 11 to 12, four of 32: 13)
-//   256 x 128, 4 waves, two workgroups to a unit: from 48 rows an expert, where the weights' stream counts: 64 rows of 256 experts
-//     1737 (8 waves, one workgroup: 1782; 128 x 64: 1910)
-//   256 x 128, 8 waves: from 192 rows, while 256 x 256 has less than two rounds: 2048 tokens 67 (4 waves 75, 256 x 256 80)
-//   256 x 256, 8 waves: 11709 tokens of 8 among 32 experts 2826 (4 waves of 128 x 128: 2956, 256 x 128: 3406 to 3606)
+// The rule between the kernels of the forward product and the input's gradient stands at grouped_choice(). Other tiles: 16384 slots of
+// 64 rows, weights of 4096 x 4096, 1737 with 256 x 128 of 4 waves (128 x 64: 1910); 512 tokens of one matrix 28 with 128 x 64 (128 x
+// 128: 30, 256 x 128: 46 to 55), its ring of three steps of 64 (300 x 4 rows 11; six 11 to 12, four of 32 13); 11709 tokens of 8 among
+// 32 experts 2826 with 256 x 256 (4 waves of 128 x 128: 2956, 256 x 128: 3406 to 3606).
 // Weights' gradient: 256 x 256 (2048 tokens of 8 among 32 experts 939; 256 x 128, two workgroups to a unit, 961; 8192 rows of one
 // matrix 240 and 279), and 128 x 128 where that makes less than 256 tiles (8192 rows of one 1024 x 1024 matrix 80, 256 x 256 329;
 // there the 64 workgroups' LDS reads bound it: a ring of four steps takes as long).
 template <int OP, bool SWIGLU> static hipError_t launch_op(const GroupedArgs &a, hipStream_t st) {
     if constexpr (OP == GROUPED_WGRAD) {
-        const int64_t tiles = (int64_t)((a.n_out + 255) / 256) * ((a.n_in + 255) / 256) * a.g.n;
+        const int64_t tiles = ceil_div(a.n_out, 256) * ceil_div(a.n_in, 256) * a.g.n;
         if (tiles >= 256) return launch_tile<OP, 4, 2, 2, 4, 64, 2, false>(a, st);
         return launch_tile<OP, 2, 1, 2, 4, 64, 3, false>(a, st);
     } else {
-        const int64_t used = a.g.n < a.g.rows ? a.g.n : a.g.rows, mean = (a.g.rows + used - 1) / used;
-        const int64_t tp = (SWIGLU ? 2 * a.n_out : OP == GROUPED_FWD ? a.n_out : a.n_in) / 256 + 1;
-        const int64_t t128 = (mean + 127) / 128 * used * tp, t256 = (mean + 255) / 256 * used * tp;
-        if (mean >= 192 && t256 >= 512) return launch_tile<OP, 4, 2, 2, 4, 64, 2, SWIGLU>(a, st);
-        if (mean >= 192 && t128 >= 192) return launch_tile<OP, 2, 2, 4, 2, 64, 3, SWIGLU>(a, st);
-        if (mean >= 48 && t128 >= 256) return launch_tile<OP, 4, 2, 2, 2, 32, 3, SWIGLU>(a, st);
-        if constexpr (OP == GROUPED_FWD)
-            if (few_rows_choice(SWIGLU, a.g.n, a.g.rows, a.n_out)) return launch_few_rows<SWIGLU>(a, st);
+        switch (grouped_choice(OP == GROUPED_DGRAD, SWIGLU, a.g.n, a.g.rows, a.n_out, a.n_in)) {
+            case TILE_256_256: return launch_tile<OP, 4, 2, 2, 4, 64, 2, SWIGLU>(a, st);
+            case TILE_256_128_8: return launch_tile<OP, 2, 2, 4, 2, 64, 3, SWIGLU>(a, st);
+            case TILE_256_128_4: return launch_tile<OP, 4, 2, 2, 2, 32, 3, SWIGLU>(a, st);
+            case FEW_ROWS:
+                if constexpr (OP == GROUPED_FWD) return launch_few_rows<SWIGLU>(a, st);
+                break;
+            case TILE_128_64: break;
+        }
         return launch_tile<OP, 2, 1, 2, 2, 64, 3, SWIGLU>(a, st);
     }
 }

@@ -60,13 +60,13 @@ def test_q4(choose):
 
 # SwiGLU, groups, rows, weight rows (of one half), columns -> kernel
 FEW_ROWS = [
-    (0, 1, 1, 4096, 4096, "few rows"), (0, 1, 4, 32752, 4096, "few rows"), (0, 1, 4, 32768, 4096, "tiles"),
-    (0, 1, 5, 16384, 4096, "tiles"), (0, 1, 16, 12288, 4096, "few rows"), (0, 1, 16, 16384, 4096, "tiles"),
-    (0, 1, 17, 4096, 4096, "few rows"), (0, 1, 48, 4096, 4096, "few rows"), (0, 1, 49, 4096, 4096, "tiles"),
-    (0, 1, 192, 1024, 4096, "few rows"), (0, 1, 193, 1024, 4096, "tiles"), (0, 1, 32, 8192, 4096, "tiles"),
-    (0, 64, 4, 1024, 1024, "few rows"), (0, 16, 32, 1024, 1024, "tiles"), (1, 256, 8, 2048, 4096, "tiles"),
-    (1, 8, 2, 2048, 4096, "few rows"), (1, 1, 4, 16384, 4096, "tiles"), (1, 1, 4, 16368, 4096, "few rows"),
-    (0, 16, 1200, 520, 1000, "tiles"), (1, 16, 80, 264, 520, "few rows"),
+    (0, 1, 1, 4096, 4096, "few rows"), (0, 1, 4, 32752, 4096, "few rows"), (0, 1, 4, 32768, 4096, "128x64"),
+    (0, 1, 5, 16384, 4096, "128x64"), (0, 1, 16, 12288, 4096, "few rows"), (0, 1, 16, 16384, 4096, "128x64"),
+    (0, 1, 17, 4096, 4096, "few rows"), (0, 1, 48, 4096, 4096, "few rows"), (0, 1, 49, 4096, 4096, "128x64"),
+    (0, 1, 192, 1024, 4096, "few rows"), (0, 1, 193, 1024, 4096, "128x64"), (0, 1, 32, 8192, 4096, "128x64"),
+    (0, 64, 4, 1024, 1024, "few rows"), (0, 16, 32, 1024, 1024, "128x64"), (1, 256, 8, 2048, 4096, "128x64"),
+    (1, 8, 2, 2048, 4096, "few rows"), (1, 1, 4, 16384, 4096, "128x64"), (1, 1, 4, 16368, 4096, "few rows"),
+    (0, 16, 1200, 520, 1000, "128x64"), (1, 16, 80, 264, 520, "few rows"),
 ]
 
 
@@ -74,6 +74,38 @@ def test_few_rows(choose):
     check(choose, [("linear", *c) for c in FEW_ROWS])
 
 
+# SwiGLU, groups, rows, weight rows (of one half), columns -> kernel of the forward product
+TILES = [
+    (0, 1, 1024, 4096, 4096, "128x64"), (0, 1, 1152, 4096, 4096, "128x64"), (0, 1, 1153, 4096, 4096, "256x128 of 8"),
+    (0, 1, 2048, 4096, 4096, "256x128 of 8"), (0, 1, 2049, 4096, 4096, "256x256"), (0, 1, 4096, 4096, 4096, "256x256"),
+    (0, 1, 6144, 4096, 4096, "256x128 of 8"), (0, 1, 8192, 4096, 4096, "256x256"), (1, 1, 2048, 2048, 4096, "256x128 of 8"),
+    (0, 1, 127, 65536, 4096, "256x128 of 4"), (0, 1, 128, 65536, 4096, "256x128 of 8"), (0, 32, 4096, 2048, 4096, "256x256"),
+    (0, 32, 4064, 2048, 4096, "256x128 of 4"), (0, 32, 8128, 4096, 2048, "256x256"), (0, 32, 8192, 2048, 4096, "256x128 of 8"),
+    (1, 256, 16384, 2048, 4096, "256x128 of 4"), (1, 256, 32768, 2048, 4096, "256x256"), (1, 256, 8192, 2048, 4096, "128x64"),
+    (1, 32, 93672, 2048, 4096, "256x256"), (0, 16, 1200, 520, 1000, "128x64"), (0, 16, 8192, 520, 1000, "256x128 of 8"),
+    (0, 16, 16384, 520, 1000, "256x256"),
+]
+# groups, rows, n_out, n_in -> kernel of the input's gradient
+DGRAD = [
+    (1, 1, 4096, 4096, "128x64"), (1, 1024, 4096, 4096, "128x64"), (1, 2048, 4096, 4096, "256x128 of 8"), (1, 4096, 4096, 4096, "256x256"),
+    (256, 8, 2048, 4096, "128x64"), (256, 16, 2048, 4096, "256x128 of 4"), (256, 32, 4096, 2048, "256x128 of 4"),
+    (64, 64, 512, 1024, "128x64"), (64, 64, 1024, 1024, "256x128 of 4"), (64, 1024, 512, 1024, "128x64"),
+    (32, 1024, 2048, 4096, "256x128 of 4"), (32, 4064, 4096, 2048, "256x128 of 4"), (32, 4096, 4096, 2048, "256x256"),
+    (32, 8192, 4096, 2048, "256x128 of 8"), (32, 8192, 2048, 4096, "256x256"), (32, 16384, 2048, 4096, "256x256"),
+    (16, 524, 520, 1000, "128x64"), (16, 4096, 520, 1000, "256x128 of 8"),
+]
+
+
+def test_tiles(choose):
+    check(choose, [("linear", *c) for c in TILES])
+    check(choose, [("dgrad", 0, *c) for c in DGRAD])
+
+
 def test_the_gpu_tests_reach_their_kernels(choose):
     check(choose, [("q4", swiglu, 1, T, N // (1 + swiglu), K, kernel) for kernel, T, N, K in paths.q4_paths() for swiglu in (0, 1)])
+    for kernel, forward, (T, k, E, K, P) in paths.BF16_SHAPES:
+        rows = T * max(k, 1)
+        if forward:
+            check(choose, [("linear", 0, E, rows, P, K, kernel), ("linear", 1, E, rows, P // 2, K, kernel)])
+        check(choose, [("dgrad", 0, E, rows, K, P, kernel)])
     check(choose, [("q4", 0, E, T * max(k, 1), N, K, kernel) for kernel, (T, k, E, K, N) in paths.Q4_EXPERTS])

@@ -4,7 +4,7 @@ Tolerances are those of test_grouped.py (its docstring derives them)."""
 import pytest
 import torch
 
-from test_grouped import BF16, F32, LAYOUTS, Q4, U, Case, compare, guarded, note, run_forward, run_q4, run_wgrad, swiglu
+from test_grouped import BF16, F32, LAYOUTS, Q4, U, Case, compare, guarded, note, run_dgrad, run_forward, run_q4, run_wgrad, swiglu
 
 
 @pytest.fixture(scope="module")
@@ -196,3 +196,41 @@ def test_linear_layouts_of_more_rows(m, shape, layout):
     run_forward(m, c, F32, f"linear {shape} {layout}")
     c.swiglu, c.w = True, torch.cat([c.w, c.w.flip(1)], dim=1)
     run_forward(m, c, BF16, f"linear {shape} {layout} swiglu")
+
+
+# kernel, forward too (else the input's gradient alone), (T, k, E, terms of a sum, results of a row): 4 to 17 steps of a ring of two or
+# three, ragged ends on every side
+BF16_SHAPES = [
+    ("128x64", True, (130, 4, 16, 520, 1008)), ("256x128 of 4", True, (300, 4, 16, 200, 4000)), ("256x128 of 4", False, (10, 4, 20, 1032, 3336)),
+    ("256x128 of 8", True, (1300, 0, 1, 328, 4112)), ("256x128 of 8", True, (450, 2, 3, 520, 5008)),
+    ("256x256", True, (2570, 0, 1, 328, 4112)), ("256x256", True, (420, 3, 5, 1032, 3600)),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel,forward,shape", BF16_SHAPES, ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else str(v))
+def test_bf16_paths(m, kernel, forward, shape):
+    T, k, E, K, P = shape
+    tail = 5 if k else 0
+    if forward:
+        c = Case(T, k, E, K, P, seed=58, dst="slots", tail=tail)
+        run_forward(m, c, F32, f"linear {kernel} {shape}")
+        run_forward(m, c, BF16, f"linear {kernel} {shape}")
+        c = Case(T, k, E, K, P // 2, seed=59, src="sorted", tail=tail, swiglu=True)
+        run_forward(m, c, F32, f"linear {kernel} {shape} swiglu")
+        run_forward(m, c, BF16, f"linear {kernel} {shape} swiglu")
+    c = Case(T, k, E, P, K, seed=60, dst="slots", tail=tail)
+    run_dgrad(m, c, F32, f"dgrad {kernel} {shape}")
+    run_dgrad(m, c, BF16, f"dgrad {kernel} {shape}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(4500, 0, 1, 4104, 4112), (3100, 2, 5, 2056, 2312)], ids=lambda s: "x".join(map(str, s)))
+def test_wgrad_of_many_rows_in_large_tiles(m, shape):
+    """256 tiles of 256 x 256 and more (289; 450 in five matrices), and more rows to a group than the kernel keeps indices of at once:
+    its table is filled again while a ring of two steps runs."""
+    T, k, E, K, N = shape
+    c = Case(*shape, seed=61, dst="slots" if k else "sorted", some=2 if k else None)
+    assert max(c.counts) > 2 * 1024 and E * -(-K // 256) * -(-N // 256) >= 256
+    run_wgrad(m, c, F32, f"wgrad {shape}")
+    run_wgrad(m, c, BF16, f"wgrad {shape} accumulate", accumulate=True)
