@@ -120,4 +120,14 @@ inline GroupedKernel grouped_choice(bool dgrad, bool swiglu, int n_groups, int n
     return !dgrad && few_rows_choice(swiglu, n_groups, n_rows, n_out) ? FEW_ROWS : TILE_128_64;
 }
 
+// ---------------------------------------------------------------------------
+// moe_grouped_wgrad: tiles of 256 x 256 of 8 waves from half of the chip's units on, 128 x 128 of 8 waves where these would be fewer.
+// Calls in us, fp32 results, by the number of 256 x 256: 64, one matrix of 2048 x 2048, 512 rows 11.1 (256 x 256: 20.2), 8192 92 (179);
+// 128, 2048 x 4096, 64 rows 10.8 (11.7), 512 20.7 (21.7), 2048 54.3 (54.1), 8192 195 (191); 160, 4096 x 2560, 64 rows 12.7 (128 x 128:
+// 14.5), 8192 189 (258); 196, 3584 x 3584, 512 rows 25 (35), 8192 218 (336); 256, 4096 x 4096, 8192 rows 248 (395); 192, 12 experts of
+// 1024 x 1024, 64 rows of 2 14.1 (16.5), 8192 43.5 (57.4); 300 x 2, 300 experts of 264 x 136 24.5 to 31.7 either way. (Of 32 experts of
+// 4096 x 4096, 2048 tokens of 8, 256 x 256 939, 256 x 128 two workgroups to a unit 961; 8192 rows of one matrix 240 and 279.)
+// ---------------------------------------------------------------------------
+inline bool wgrad_256(int n_groups, int n_out, int n_in) { return ceil_div(n_out, 256) * ceil_div(n_in, 256) * n_groups > 128; }
+
 }  // namespace moe

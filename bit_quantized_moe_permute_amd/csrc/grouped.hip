@@ -459,17 +459,14 @@ template <bool SWIGLU> static hipError_t launch_few_rows(const GroupedArgs &a, h
     return hipGetLastError();
 }
 
-// The rule between the kernels of the forward product and the input's gradient stands at grouped_choice(). Other tiles: 16384 slots of
-// 64 rows, weights of 4096 x 4096, 1737 with 256 x 128 of 4 waves (128 x 64: 1910); 512 tokens of one matrix 28 with 128 x 64 (128 x
-// 128: 30, 256 x 128: 46 to 55), its ring of three steps of 64 (300 x 4 rows 11; six 11 to 12, four of 32 13); 11709 tokens of 8 among
-// 32 experts 2826 with 256 x 256 (4 waves of 128 x 128: 2956, 256 x 128: 3406 to 3606).
-// Weights' gradient: 256 x 256 (2048 tokens of 8 among 32 experts 939; 256 x 128, two workgroups to a unit, 961; 8192 rows of one
-// matrix 240 and 279), and 128 x 128 where that makes less than 256 tiles (8192 rows of one 1024 x 1024 matrix 80, 256 x 256 329;
-// there the 64 workgroups' LDS reads bound it: a ring of four steps takes as long).
+// The rules between the kernels stand at grouped_choice() and wgrad_256(). Other tiles: 16384 slots of 64 rows, weights of 4096 x 4096,
+// 1737 us with 256 x 128 of 4 waves (128 x 64: 1910); 512 tokens of one matrix 28 with 128 x 64 (128 x 128: 30, 256 x 128: 46 to 55),
+// its ring of three steps of 64 (300 x 4 rows 11; six 11 to 12, four of 32 13); 11709 tokens of 8 among 32 experts 2826 with 256 x
+// 256 (4 waves of 128 x 128: 2956, 256 x 128: 3406 to 3606). Weights' gradient of few tiles (8192 rows of one 1024 x 1024 matrix: 64
+// workgroups, 80 us): their LDS reads bound it, a ring of four steps takes as long.
 template <int OP, bool SWIGLU> static hipError_t launch_op(const GroupedArgs &a, hipStream_t st) {
     if constexpr (OP == GROUPED_WGRAD) {
-        const int64_t tiles = ceil_div(a.n_out, 256) * ceil_div(a.n_in, 256) * a.g.n;
-        if (tiles >= 256) return launch_tile<OP, 4, 2, 2, 4, 64, 2, false>(a, st);
+        if (wgrad_256(a.g.n, a.n_out, a.n_in)) return launch_tile<OP, 4, 2, 2, 4, 64, 2, false>(a, st);
         return launch_tile<OP, 2, 1, 2, 4, 64, 3, false>(a, st);
     } else {
         switch (grouped_choice(OP == GROUPED_DGRAD, SWIGLU, a.g.n, a.g.rows, a.n_out, a.n_in)) {

@@ -13,6 +13,7 @@ int main() {
         if (!strcmp(op, "q4")) puts(q4[moe::q4_choice(swiglu, groups, rows, n_out, n_in)]);
         else if (!strcmp(op, "linear")) puts(bf16[moe::grouped_choice(false, swiglu, groups, rows, n_out, n_in)]);
         else if (!strcmp(op, "dgrad")) puts(bf16[moe::grouped_choice(true, false, groups, rows, n_out, n_in)]);
+        else if (!strcmp(op, "wgrad")) puts(moe::wgrad_256(groups, n_out, n_in) ? "256x256" : "128x128");
         else return 1;
     }
     return 0;

@@ -96,6 +96,17 @@ DGRAD = [
 ]
 
 
+# groups, rows, n_out, n_in -> kernel of the weights' gradient
+WGRAD = [
+    (1, 8192, 2048, 2048, "128x128"), (1, 64, 4096, 2048, "128x128"), (1, 64, 4104, 2048, "256x256"), (1, 8192, 2560, 4096, "256x256"),
+    (8, 128, 1024, 1024, "128x128"), (9, 128, 1024, 1024, "256x256"), (32, 154, 512, 1000, "256x256"), (4096, 8, 8, 8, "256x256"),
+]
+
+
+def test_weights_gradient(choose):
+    check(choose, [("wgrad", 0, *c) for c in WGRAD])
+
+
 def test_tiles(choose):
     check(choose, [("linear", *c) for c in TILES])
     check(choose, [("dgrad", 0, *c) for c in DGRAD])
@@ -108,4 +119,5 @@ def test_the_gpu_tests_reach_their_kernels(choose):
         if forward:
             check(choose, [("linear", 0, E, rows, P, K, kernel), ("linear", 1, E, rows, P // 2, K, kernel)])
         check(choose, [("dgrad", 0, E, rows, K, P, kernel)])
+    check(choose, [("wgrad", 0, E, T * max(k, 1), N, K, "256x256") for T, k, E, K, N in paths.WGRAD_256])
     check(choose, [("q4", 0, E, T * max(k, 1), N, K, kernel) for kernel, (T, k, E, K, N) in paths.Q4_EXPERTS])
