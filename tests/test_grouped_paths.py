@@ -236,3 +236,128 @@ def test_wgrad_in_large_tiles(m, shape):
     c = Case(*shape, seed=61, dst="slots" if k else "sorted", some=2 if k else None)
     run_wgrad(m, c, F32, f"wgrad {shape}")
     run_wgrad(m, c, BF16, f"wgrad {shape} accumulate", accumulate=True)
+
+
+# ----------------------------------------------------------------------------
+# stacks of weights, gradients and results behind 4 GiB
+# ----------------------------------------------------------------------------
+def near(got, want, tol, what):
+    """Like compare(), on the GPU."""
+    if got.dtype == BF16:
+        tol = tol + 2.0**-8 * want.abs()
+    worst = float(((got.double() - want).abs() / tol.clamp_min(1e-300)).nan_to_num(nan=1e9).max())
+    note(f"{what}: worst {worst:.3f} of the tolerance")
+    assert worst <= 1, what
+
+
+def product(x, w, sizes=None, terms=1):
+    """x w^T in binary64 and its tolerance (sizes: what it is taken over, default w)."""
+    x, w = x.double(), w.double()
+    s = w if sizes is None else sizes
+    return x @ w.T, 4 * (x.shape[1] * terms)**0.5 * U * torch.sqrt(x.square() @ s.square().T)
+
+
+def rows_of(E, T, last):
+    """Offsets of E groups: `last` of T positions in the last group, the others in group E - 2."""
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E - 1], off[E] = T - last, T
+    return off, ((E - 2, 0, T - last), (E - 1, T - last, T))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,N,K,T", [(4096, 512, 1032, 3), (4096, 512, 1032, 40), (35, 8192, 8192, 40), (35, 8192, 8192, 4300)])
+def test_weights_behind_4_gib(m, E, N, K, T):
+    """Forward, with SwiGLU, and the input's gradient, of the last two of a stack of matrices that passes 2^32 bytes before them."""
+    assert (E - 2) * N * K * 2 > 2**32
+    g = torch.Generator(device="cuda").manual_seed(62)
+    w = torch.empty(E, N, K, dtype=BF16, device="cuda")
+    for e in (E - 2, E - 1):
+        w[e] = (torch.randn(N, K, generator=g, device="cuda") * K**-0.5).to(BF16)
+    x, dy = (torch.randn(T, n, generator=g, device="cuda").to(BF16) for n in (K, N))
+    off, groups = rows_of(E, T, (T + 1) // 2)
+    G = m.RowGroups(T, offsets=off)
+    y, s, dx = (torch.full((T, n), 7.0, device="cuda") for n in (N, N // 2, K))
+    note(f"weights behind 4 GiB {E} {N} {K} {T}")
+    m.moe_grouped_linear(G, x, w, y)
+    m.moe_grouped_linear(G, x, w, s, m.ACT_SWIGLU)
+    m.moe_grouped_dgrad(G, dy, w, dx)
+    torch.cuda.synchronize()
+    for e, a, b in groups:
+        want, tol = product(x[a:b], w[e])
+        near(y[a:b], want, tol, f"linear {e}")
+        near(s[a:b], *swiglu(want, tol), f"swiglu {e}")
+        near(dx[a:b], *product(dy[a:b], w[e].T), f"dgrad {e}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,N,K,T", [(4096, 256, 8320, 3), (35, 16384, 16384, 2), (35, 16384, 16384, 4), (35, 16384, 16384, 500),
+                                     (35, 16384, 16384, 3000)])
+def test_codes_behind_4_gib(m, E, N, K, T):
+    """4-bit codes likewise, up to the last scale and zero point of the stack; k_few, k_many in halves, in tiles of 16, 32 and 64."""
+    assert (E - 2) * N * K // 2 > 2**32
+    g = torch.Generator(device="cuda").manual_seed(63)
+    codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device="cuda")
+    scale = torch.empty(E, N, K // 64, dtype=torch.float16, device="cuda")
+    zero = torch.empty(E, N, K // 64, dtype=torch.uint8, device="cuda")
+    for e in (E - 2, E - 1):
+        codes[e] = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+        scale[e] = (0.5 + torch.rand(N, K // 64, generator=g, device="cuda")) * K**-0.5 / 8
+        zero[e] = torch.randint(0, 16, (N, K // 64), generator=g, device="cuda", dtype=torch.uint8)
+    x = torch.randn(T, K, generator=g, device="cuda").to(BF16)
+    off, groups = rows_of(E, T, (T + 1) // 2)
+    G, q = m.RowGroups(T, offsets=off), m.Q4Weights(codes, scale, zero)
+    y, s = torch.full((T, N), 7.0, device="cuda"), torch.full((T, N // 2), 7.0, device="cuda")
+    note(f"codes behind 4 GiB {E} {N} {K} {T}")
+    m.moe_q4_linear(G, q, x, y)
+    m.moe_q4_linear(G, q, x, s, m.ACT_SWIGLU)
+    torch.cuda.synchronize()
+    per = lambda t: t.double().repeat_interleave(64, dim=1)
+    for e, a, b in groups:
+        w = (torch.stack([codes[e] & 15, codes[e] >> 4], dim=2).view(N, K).double() - per(zero[e])).mul_(per(scale[e]))
+        want, tol = product(x[a:b], w, 31 * per(scale[e]), terms=2)
+        near(y[a:b], want, tol, f"q4 {e}")
+        near(s[a:b], *swiglu(want, tol), f"q4 swiglu {e}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,E,N,K", [(F32, 35, 8192, 4104), (BF16, 35, 8192, 8200), (F32, 4096, 512, 520)])
+def test_weights_gradients_behind_4_gib(m, dtype, E, N, K):
+    T = 70
+    assert (E - 2) * N * K * (4 if dtype == F32 else 2) > 2**32
+    g = torch.Generator(device="cuda").manual_seed(64)
+    x, dy = (torch.randn(T, n, generator=g, device="cuda").to(BF16) for n in (K, N))
+    off, groups = rows_of(E, T, (T + 1) // 2)
+    G = m.RowGroups(T, offsets=off)
+    dw = torch.full((E, N, K), 7.0, dtype=dtype, device="cuda")
+    note(f"weights' gradients behind 4 GiB {dtype} {E}")
+    m.moe_grouped_wgrad(G, x, dy, dw)
+    torch.cuda.synchronize()
+    assert not any(bool(dw[e].any()) for e in range(E - 2))
+    for e, a, b in groups:
+        near(dw[e], *product(dy[a:b].T, x[a:b].T), f"wgrad {e}")
+    for e, a, b in groups:
+        dw[e] = 1.0
+    m.moe_grouped_wgrad(G, x, dy, dw, accumulate=True)
+    torch.cuda.synchronize()
+    for e, a, b in groups:
+        want, tol = product(dy[a:b].T, x[a:b].T)
+        near(dw[e], want + 1, tol + 2 * U * (want + 1).abs(), f"wgrad accumulate {e}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_q4_results_behind_4_gib(m, T):
+    far, N, K = 2**17 + 7, 2**14 + 64, 128
+    g = torch.Generator(device="cuda").manual_seed(65)
+    out = torch.zeros(far, N, dtype=BF16, device="cuda")
+    rows = far - 1 - 2 * torch.arange(T, device="cuda")
+    codes = torch.randint(0, 256, (1, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scale = (0.5 + torch.rand(1, N, K // 32, generator=g, device="cuda")) / 90
+    x = torch.randn(T, K, generator=g, device="cuda").to(BF16)
+    note(f"q4 results behind 4 GiB {T}")
+    m.moe_q4_linear(m.RowGroups(T, out_index=rows.to(torch.int32)), m.Q4Weights(codes, scale), x, out)
+    torch.cuda.synchronize()
+    per = scale[0].double().repeat_interleave(32, dim=1)
+    w = (torch.stack([codes[0] & 15, codes[0] >> 4], dim=2).view(N, K).double() - 8) * per
+    near(out[rows], *product(x, w, 31 * per, terms=2), "q4 results")
+    assert not out[rows - 1].any() and not out[:100].any()
