@@ -447,7 +447,7 @@ template <int G, int KIND, bool SWIGLU> hipError_t launch_few(const Q4Args &a, h
 }
 
 template <int G, int KIND, bool SWIGLU> hipError_t launch_kind(const Q4Args &a, hipStream_t st) {
-    switch (q4_choice(SWIGLU, a.g.n, a.g.rows, a.N, a.K)) {
+    switch (q4_choice(SWIGLU, a.g.n, a.g.rows, a.N, a.K, G)) {
         case Q4_FEW: return launch_few<G, KIND, SWIGLU>(a, st);
         case Q4_16_HALVES: return launch_many<1, 2, G, KIND, SWIGLU>(a, st);
         case Q4_16: return launch_many<1, 1, G, KIND, SWIGLU>(a, st);

@@ -138,16 +138,18 @@ def test_q4_of_an_x_that_is_not_finite(m, T, N, value):
 # 4-bit weights: every kernel (test_grouped_choice.py holds the shapes to their kernels)
 # ----------------------------------------------------------------------------
 # kernel -> rows, weight rows: ends of rows and tiles inside the last block
-Q4_ROWS = {"few": (37, 150), "16 halves": (157, 1290), "16": (410, 1290), "32": (2090, 1290), "64 halves": (890, 1290), "64": (3005, 1290)}
+Q4_ROWS = {"few": (37, 150), "16 halves": (330, 1290), "16": (497, 1290), "32": (2090, 1290), "64 halves": (890, 1290), "64": (3005, 1290)}
 # columns, group, scales, zero points: rows that end inside a chunk of 128, a second and third block of 32 groups (from 1024 columns
 # with groups of 32, 2048 with 64, 4096 with 128), in one and in two halves
-Q4_COLUMNS = [(96, 32, F32, False), (1056, 32, F32, False), (2144, 32, torch.float16, True), (2240, 64, F32, False),
-              (4288, 64, torch.float16, True), (4480, 128, F32, True), (8448, 128, BF16, False)]
+Q4_COLUMNS = [(96, 32, F32, False), (1056, 32, F32, False), (2144, 32, torch.float16, True), (2240, 64, F32, False), (3616, 32, BF16, True),
+              (3904, 64, F32, True), (4288, 64, torch.float16, True), (4480, 128, F32, True), (7936, 128, torch.float16, False), (8448, 128, BF16, False)]
+Q4_HALVES = (3616, 3904, 7936, 8448)                                # where two halves of K make k_many faster
 Q4_EXPERTS = [("16", (6, 4, 24, 192, 2730)), ("16", (3, 8, 30, 160, 2820)), ("64 halves", (64, 2, 8, 2112, 2720)), ("32", (280, 2, 8, 256, 2720))]
 
 
 def q4_paths():
-    return [(kernel, T, N, K) for kernel, (T, N) in Q4_ROWS.items() for K, *_ in Q4_COLUMNS if "halves" not in kernel or K >= 2048]
+    return [(kernel, T, N, K) for kernel, (T, N) in Q4_ROWS.items() for K, *_ in Q4_COLUMNS
+            if "halves" not in kernel or K in Q4_HALVES or (K > 2048 and kernel == "64 halves")]
 
 
 @pytest.mark.gpu
@@ -203,7 +205,7 @@ def test_linear_layouts_of_more_rows(m, shape, layout):
 BF16_SHAPES = [
     ("128x64", True, (130, 4, 16, 520, 1008)), ("256x128 of 4", True, (300, 4, 16, 200, 4000)), ("256x128 of 4", False, (10, 4, 20, 1032, 3336)),
     ("256x128 of 8", True, (1300, 0, 1, 328, 4112)), ("256x128 of 8", True, (450, 2, 3, 520, 5008)),
-    ("256x256", True, (2570, 0, 1, 328, 4112)), ("256x256", True, (420, 3, 5, 1032, 3600)),
+    ("256x128 of 8", True, (420, 3, 5, 1032, 3600)), ("256x256", True, (2570, 0, 1, 328, 4112)), ("256x256", True, (420, 3, 5, 520, 7008)),
 ]
 
 
