@@ -7,7 +7,7 @@
 // All on the bf16 matrix cores, with fp32 sums from the first to the last product; a bf16 output is rounded once, where it is
 // stored. Few rows to an expert: every weight is read once, and that is the time (one token of 8 among 256 experts, 256 MiB of
 // weights: 49 us, 5.4 TB/s; 2048 tokens of the same, all weights, 8.6 GB: 1742 us, 5.0 TB/s). Many rows: the products are (11709
-// tokens of 8 among 32 experts: 2822 us, 1114 TFLOP/s, where a library product of 8192 x 8192 x 8192 makes 1346). A large copy
+// tokens of 8 among 32 experts: 2880 us, 1091 TFLOP/s, where a library product of 8192 x 8192 x 8192 makes 1346). A large copy
 // moves 5.15 TB/s.
 #include <type_traits>
 
