@@ -7,7 +7,7 @@
 // All on the bf16 matrix cores, with fp32 sums from the first to the last product; a bf16 output is rounded once, where it is
 // stored. Few rows to an expert: every weight is read once, and that is the time (one token of 8 among 256 experts, 256 MiB of
 // weights: 49 us, 5.4 TB/s; 2048 tokens of the same, all weights, 8.6 GB: 1742 us, 5.0 TB/s). Many rows: the products are (11709
-// tokens of 8 among 32 experts: 2880 us, 1091 TFLOP/s, where a library product of 8192 x 8192 x 8192 makes 1346). A large copy
+// tokens of 8 among 32 experts: 2811 us, 1119 TFLOP/s, where a library product of 8192 x 8192 x 8192 makes 1346). A large copy
 // moves 5.15 TB/s.
 #include <type_traits>
 
@@ -324,14 +324,22 @@ __global__ __launch_bounds__(64 * WP * WQ, FP * FQ <= 8 ? 2 : 1) void k_tile(Gro
             for (int i = 0; i < FO; ++i)
 #pragma unroll
                 for (int v4 = 0; v4 < 4; ++v4) {
-                    f32x4_t y;
+                    float y[4];
+                    if constexpr (SWIGLU) {
+                        float g[4], u[4];
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        y[v] = SWIGLU ? swiglu(acc[SWIGLU ? 2 * i : i][j][4 * v4 + v], acc[SWIGLU ? 2 * i + 1 : i][j][4 * v4 + v])
-                                      : acc[i][j][4 * v4 + v];
+                        for (int v = 0; v < 4; ++v) {
+                            g[v] = acc[2 * i][j][4 * v4 + v];
+                            u[v] = acc[2 * i + 1][j][4 * v4 + v];
+                        }
+                        swiglu(g, u, y);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) y[v] = acc[i][j][4 * v4 + v];
+                    }
                     const int c = (i * 32 + 8 * v4 + 4 * hh) / PER;
                     uint8_t *to = rows + i32 * (COLS * SIZE) + (c ^ (i32 & (CHUNKS - 1))) * 16;
-                    if constexpr (SIZE == 4) *reinterpret_cast<f32x4_t *>(to) = y;
+                    if constexpr (SIZE == 4) *reinterpret_cast<f32x4_t *>(to) = f32x4_t{y[0], y[1], y[2], y[3]};
                     else *reinterpret_cast<uint2 *>(to + 8 * hh) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
                 }
             asm volatile("" ::: "memory");

@@ -145,19 +145,40 @@ __device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
 // Whether a launch can count its threads (in 32 bits).
 inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
 
-// silu(gate) * up. exp(-gate) as a power of two, times 1 + what the rounding of its exponent lost; the quotient through the
-// hardware's reciprocal: some 2 units of the last place, in 16 instructions (library exp and division take 40: for 256 x 256 results
+// silu(gate) * up of N values. exp(-gate) as a power of two, times 1 + what the rounding of its exponent lost; the quotient through the
+// hardware's reciprocal: some 2 units of the last place, in 12 instructions (library exp and division take 40: for 256 x 256 results
 // of a tile a tenth of its whole time). The correction is below 1e-5 where the quotient matters; its bounds keep a gate of 2e7 and
 // more, or an infinite one, from making it anything else. Where exp(-gate) passes 2^64, 1 + exp(-gate) is exp(-gate), and what is
 // above goes to the other factor as a power of two: the sum would overflow from a gate of -88.7 on and its reciprocal leave the
-// normal floats at -87.3, while the product may be any float (from -131 on that factor is below 2^-126, and is 0).
-__device__ __forceinline__ float swiglu(float gate, float up) {
+// normal floats at -87.3, while the product may be any float (from -131 on that factor is below 2^-126, and is 0). A wave goes that way
+// only if one of N values of its lanes needs it, the others' bits are the same on either (always: 11709 tokens of 8 among 32 experts 2811
+// -> 2830 us, 5374 of 2 among 8 with sums of 368 39.5 -> 41.1).
+template <int N> __device__ __forceinline__ void swiglu(const float (&gate)[N], const float (&up)[N], float (&y)[N]) {
 #pragma clang fp contract(off)                               // 64 - t is of the rounded t, whose rest is in c
     constexpr float L = 1.44269502f, L_REST = 1.92596299e-8f, LN2 = 0.693147181f;    // log2(e) in two parts
-    const float t = -gate * L, rest = __fmaf_rn(-gate, L_REST, __fmaf_rn(-gate, L, -t));
-    const float c = __builtin_amdgcn_fmed3f(__fmaf_rn(rest, LN2, 1.f), 0.99f, 1.01f);
-    const float s = __builtin_amdgcn_exp2f(fminf(64.f - t, 0.f));
-    return gate * __builtin_amdgcn_rcpf(__fmaf_rn(__builtin_amdgcn_exp2f(fminf(t, 64.f)), c, 1.f)) * (up * s);
+    float t[N], c[N], most = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        t[i] = -gate[i] * L;
+        c[i] = __builtin_amdgcn_fmed3f(__fmaf_rn(__fmaf_rn(-gate[i], L_REST, __fmaf_rn(-gate[i], L, -t[i])), LN2, 1.f), 0.99f, 1.01f);
+        most = fmaxf(most, t[i]);
+    }
+    if (__any(most > 64.f)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float s = __builtin_amdgcn_exp2f(fminf(64.f - t[i], 0.f));
+            y[i] = gate[i] * __builtin_amdgcn_rcpf(__fmaf_rn(__builtin_amdgcn_exp2f(fminf(t[i], 64.f)), c[i], 1.f)) * (up[i] * s);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = gate[i] * __builtin_amdgcn_rcpf(__fmaf_rn(__builtin_amdgcn_exp2f(t[i]), c[i], 1.f)) * up[i];
+    }
+}
+__device__ __forceinline__ float swiglu(float gate, float up) {
+    const float g[1] = {gate}, u[1] = {up};
+    float y[1];
+    swiglu<1>(g, u, y);
+    return y[0];
 }
 
 }  // namespace moe

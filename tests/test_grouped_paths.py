@@ -87,6 +87,26 @@ def test_swiglu_of_far_negative_gates(m, T, kind):
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, gates {g[bad.any(0)][:8].tolist()}, others {u[bad.any(0)][:8].tolist()}"
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(6, 2, 4, 136, 72), (120, 2, 3, 136, 72), (1300, 0, 1, 136, 2056)], ids=lambda s: "x".join(map(str, s)))
+def test_swiglu_of_a_far_negative_gate_leaves_other_rows_alone(m, shape):
+    """One row's gates of -90 and below take the wave another way: the other rows' bits do not change."""
+    T, k, E, K, N = shape
+    c = Case(*shape, seed=66, swiglu=True)
+    c.w[:, :N, 0] = 1.0                                             # x[0] moves every gate
+    for far in (-100.0, -1000.0, float("-inf")):
+        got = []
+        for v in (0.5, far):
+            c.x[T // 2, 0] = v
+            out = torch.empty(c.rows, N, device="cuda")
+            note(f"far row {shape} {v}")
+            m.moe_grouped_linear(c.groups(m), c.x.cuda(), c.w.cuda(), out, m.ACT_SWIGLU)
+            torch.cuda.synchronize()
+            got.append(out.cpu())
+        rest = [p for p in range(c.rows) if c.r(p) != T // 2]
+        assert len(rest) < c.rows and torch.equal(got[0][rest], got[1][rest])
+
+
 # ----------------------------------------------------------------------------
 # 4-bit weights: the ends of the range of x
 # ----------------------------------------------------------------------------
